@@ -1,0 +1,360 @@
+"""Softmax cross attention and the learned relative position bias
+(C ABI in include/lisa_attention.h), on CUDA tensors.
+
+Argument marshalling only, as in ``lisa``: torch supplies device memory and
+streams, every step runs in the library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from .lisa import LISA_BF16, LISA_F32, LISA_OK, LisaError, load
+
+LISA_BUCKETS_EXACT = 0
+LISA_BUCKETS_LOG = 1
+LISA_MAX_OFFSETS = 16384
+
+ATTENTION_EXPORTED = ("lisa_relative_bias", "lisa_relative_bias_backward_workspace_bytes",
+                      "lisa_relative_bias_backward", "lisa_cross_attention_workspace_bytes",
+                      "lisa_cross_attention", "lisa_cross_attention_backward_workspace_bytes",
+                      "lisa_cross_attention_backward")
+
+
+class lisa_strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong), ("token", ctypes.c_longlong)]
+
+
+class lisa_axis_rule(ctypes.Structure):
+    _fields_ = [("rule", ctypes.c_int), ("buckets", ctypes.c_int), ("max_distance", ctypes.c_int)]
+
+
+class lisa_rel_bias(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p),
+                ("q_rows", ctypes.c_int), ("q_cols", ctypes.c_int), ("k_rows", ctypes.c_int),
+                ("k_cols", ctypes.c_int), ("key_step_rows", ctypes.c_int), ("key_step_cols", ctypes.c_int),
+                ("start_rows", ctypes.c_int), ("start_cols", ctypes.c_int), ("starts", ctypes.c_void_p),
+                ("rows", lisa_axis_rule), ("cols", lisa_axis_rule)]
+
+
+_lib = None
+
+
+def _library():
+    """The loaded library with this module's signatures set."""
+    global _lib
+    if _lib is None:
+        lib = load()
+        vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        sp, bp = ctypes.POINTER(lisa_strides), ctypes.POINTER(lisa_rel_bias)
+        lib.lisa_relative_bias.argtypes = [bp, i, vp, i, vp]
+        lib.lisa_relative_bias.restype = i
+        lib.lisa_relative_bias_backward_workspace_bytes.argtypes = [bp, i]
+        lib.lisa_relative_bias_backward_workspace_bytes.restype = sz
+        lib.lisa_relative_bias_backward.argtypes = [bp, i, vp, i, vp, vp, sz, vp]
+        lib.lisa_relative_bias_backward.restype = i
+        lib.lisa_cross_attention_workspace_bytes.argtypes = [i] * 7
+        lib.lisa_cross_attention_workspace_bytes.restype = sz
+        lib.lisa_cross_attention.argtypes = [vp, sp, vp, sp, vp, sp, vp, sp, vp, i, i, i, i, i, i, f, vp, bp, i, vp,
+                                             sz, vp]
+        lib.lisa_cross_attention.restype = i
+        lib.lisa_cross_attention_backward_workspace_bytes.argtypes = [i] * 6 + [bp, i]
+        lib.lisa_cross_attention_backward_workspace_bytes.restype = sz
+        lib.lisa_cross_attention_backward.argtypes = [vp, sp, vp, sp, vp, sp, vp, sp, vp, vp, sp, vp, vp, vp, vp, i, i,
+                                                      i, i, i, i, f, vp, bp, i, vp, sz, vp]
+        lib.lisa_cross_attention_backward.restype = i
+        _lib = lib
+    return _lib
+
+
+# -- the C entry points under their own names ---------------------------------------
+# strides: lisa_strides; bias: lisa_rel_bias or None; pointers are ints (device addresses).
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def lisa_relative_bias(bias, heads, out, dtype, stream) -> int:
+    return int(_library().lisa_relative_bias(_ref(bias), heads, out, dtype, stream))
+
+
+def lisa_relative_bias_backward_workspace_bytes(bias, heads) -> int:
+    return int(_library().lisa_relative_bias_backward_workspace_bytes(_ref(bias), heads))
+
+
+def lisa_relative_bias_backward(bias, heads, dbias, dtype, dtable, workspace, workspace_bytes, stream) -> int:
+    return int(_library().lisa_relative_bias_backward(_ref(bias), heads, dbias, dtype, dtable, workspace,
+                                                      workspace_bytes, stream))
+
+
+def lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, dtype) -> int:
+    return int(_library().lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, dtype))
+
+
+def lisa_cross_attention(Q, qs, K, ks, V, vs, O, os, lse, B, heads, kv_heads, n, m, d, scale, kv_lens, bias, dtype,
+                         workspace, workspace_bytes, stream) -> int:
+    return int(_library().lisa_cross_attention(Q, _ref(qs), K, _ref(ks), V, _ref(vs), O, _ref(os), lse, B, heads,
+                                               kv_heads, n, m, d, scale, kv_lens, _ref(bias), dtype, workspace,
+                                               workspace_bytes, stream))
+
+
+def lisa_cross_attention_backward_workspace_bytes(B, heads, kv_heads, n, m, d, bias, dtype) -> int:
+    return int(_library().lisa_cross_attention_backward_workspace_bytes(B, heads, kv_heads, n, m, d, _ref(bias),
+                                                                        dtype))
+
+
+def lisa_cross_attention_backward(Q, qs, K, ks, V, vs, O, os, lse, dO, dos, dQ, dK, dV, dtable, B, heads, kv_heads,
+                                  n, m, d, scale, kv_lens, bias, dtype, workspace, workspace_bytes, stream) -> int:
+    return int(_library().lisa_cross_attention_backward(Q, _ref(qs), K, _ref(ks), V, _ref(vs), O, _ref(os), lse, dO,
+                                                        _ref(dos), dQ, dK, dV, dtable, B, heads, kv_heads, n, m, d,
+                                                        scale, kv_lens, _ref(bias), dtype, workspace,
+                                                        workspace_bytes, stream))
+
+
+# -- tensor-level convenience ---------------------------------------------------------
+
+_DTYPES = {torch.float32: LISA_F32, torch.bfloat16: LISA_BF16}
+
+
+def exact_buckets(max_distance: int) -> lisa_axis_rule:
+    """One bucket for each offset -D .. D of an axis; farther ones share the outermost."""
+    return lisa_axis_rule(LISA_BUCKETS_EXACT, 2 * int(max_distance) + 1, int(max_distance))
+
+
+def log_buckets(buckets: int, max_distance: int) -> lisa_axis_rule:
+    """``buckets`` of an axis, half to each side: near offsets one by one, farther
+    ones in geometrically growing buckets up to ``max_distance``."""
+    return lisa_axis_rule(LISA_BUCKETS_LOG, int(buckets), int(max_distance))
+
+
+class RelativeBias:
+    """A learned relative position bias: the table (fp32 CUDA tensor
+    [rows.buckets * cols.buckets, heads]) and the rule that picks its row.
+
+    Queries are the tokens of the grid ``q_grid`` = (rows, columns), keys those
+    of ``k_grid``; a sequence is a grid of one row.  Query (r, c) stands at
+    ``query_start`` + (r, c), key (r, c) at (key_step[0] r, key_step[1] c).
+    ``query_start`` may be an int32 CUDA tensor [B]: each batch entry's own
+    start on a sequence (forward only).  The table may be updated in place
+    between calls; the object keeps no copy of it."""
+
+    def __init__(self, table: torch.Tensor, q_grid, k_grid, rows: lisa_axis_rule = None,
+                 cols: lisa_axis_rule = None, key_step=(1, 1), query_start=(0, 0)):
+        rows = exact_buckets(0) if rows is None else rows
+        if cols is None:
+            raise ValueError("RelativeBias needs the columns' bucket rule")
+        if not (table.is_cuda and table.dtype == torch.float32 and table.is_contiguous() and table.dim() == 2):
+            raise ValueError("the bias table must be a contiguous fp32 CUDA tensor [buckets, heads]")
+        if table.shape[0] != rows.buckets * cols.buckets:
+            raise ValueError("the bias table has %d rows, the rules give %d buckets"
+                             % (table.shape[0], rows.buckets * cols.buckets))
+        self.table = table
+        self.q_grid = (int(q_grid[0]), int(q_grid[1]))
+        self.k_grid = (int(k_grid[0]), int(k_grid[1]))
+        self.starts = None
+        start = (0, 0)
+        if isinstance(query_start, torch.Tensor):
+            if not (query_start.is_cuda and query_start.dtype == torch.int32 and query_start.is_contiguous()
+                    and query_start.dim() == 1 and query_start.device == table.device):
+                raise ValueError("query_start must be a pair of ints or a contiguous int32 CUDA tensor [B]")
+            self.starts = query_start
+        else:
+            start = (int(query_start[0]), int(query_start[1]))
+        self.struct = lisa_rel_bias(table.data_ptr(), *self.q_grid, *self.k_grid, int(key_step[0]), int(key_step[1]),
+                                    *start, None if self.starts is None else self.starts.data_ptr(), rows, cols)
+
+    @property
+    def heads(self) -> int:
+        return self.table.shape[1]
+
+    @property
+    def n(self) -> int:
+        return self.q_grid[0] * self.q_grid[1]
+
+    @property
+    def m(self) -> int:
+        return self.k_grid[0] * self.k_grid[1]
+
+
+class _On:
+    """The device and the stream of a call made current, so what the call
+    allocates belongs to the stream that uses it."""
+
+    def __init__(self, device, stream):
+        self.device = torch.cuda.device(device)
+        self.other = None
+        if stream is not None:
+            self.other = torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
+        self.of = device
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.other is not None:
+            self.other.__enter__()
+        return torch.cuda.current_stream(self.of).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _workspace(given, nbytes, device):
+    """(tensor to keep, address, bytes) of the call's workspace."""
+    if given is None:
+        if nbytes == 0:
+            return None, None, 0
+        given = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif given.device != device or not given.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on the call's device")
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def _strides(t: torch.Tensor) -> lisa_strides:
+    s = t.stride()
+    if t.shape[3] > 1 and s[3] != 1:
+        raise ValueError("the elements of a token must be contiguous (last stride 1)")
+    return lisa_strides(*(s[x] if t.shape[x] > 1 else t.shape[3] for x in range(3)))
+
+
+def _check(device, dtype, tensors):
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("the cross attention runs on CUDA tensors only")
+        if t.device != device:
+            raise ValueError("tensors must be on one device")
+        if t.dim() != 4 or t.dtype != dtype:
+            raise ValueError("q, k, v, out, dout must be 4-d and share dtype float32 or bfloat16")
+
+
+def _shapes(q, k, v, kv_lens, bias):
+    if q.dtype not in _DTYPES:
+        raise ValueError("q, k, v must share dtype float32 or bfloat16")
+    _check(q.device, q.dtype, (q, k, v))
+    B, heads, n, d = q.shape
+    kv_heads, m = k.shape[1], k.shape[2]
+    if tuple(k.shape) != (B, kv_heads, m, d) or k.shape != v.shape:
+        raise ValueError("k and v must be [B, kv_heads, m, d] for q [B, heads, n, d]")
+    if kv_lens is not None:
+        if not (kv_lens.is_cuda and kv_lens.dtype == torch.int32 and kv_lens.is_contiguous()
+                and tuple(kv_lens.shape) == (B,) and kv_lens.device == q.device):
+            raise ValueError("kv_lens must be a contiguous int32 CUDA tensor [B]")
+    if bias is not None:
+        if bias.table.device != q.device:
+            raise ValueError("tensors must be on one device")
+        if bias.heads != heads or bias.n != n or bias.m != m:
+            raise ValueError("the bias is of %d heads, %d queries and %d keys, the call of %d, %d and %d"
+                             % (bias.heads, bias.n, bias.m, heads, n, m))
+        if bias.starts is not None and bias.starts.shape[0] != B:
+            raise ValueError("query_start must have one entry per batch entry")
+    return B, heads, kv_heads, n, m, d
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale=None, kv_lens=None,
+                    bias: RelativeBias = None, return_lse: bool = False, out=None, workspace=None, stream=None):
+    """Softmax attention of queries [B, heads, n, d] over keys and values
+    [B, kv_heads, m, d] (fp32 or bf16; heads a multiple of kv_heads; strided
+    views are fine, with d contiguous and strides of 16 bytes).  ``scale``
+    defaults to 1 / sqrt(d); ``kv_lens`` (int32 [B]) is the number of valid keys
+    of each batch entry; ``bias`` a RelativeBias.  Returns O [B, heads, n, d]
+    (a new contiguous tensor unless ``out`` is given), with ``return_lse`` also
+    the fp32 log-sum-exp [B, heads, n] that the backward pass reads.
+    ``stream`` is a raw stream handle of the tensors' device."""
+    B, heads, kv_heads, n, m, d = _shapes(q, k, v, kv_lens, bias)
+    dt = _DTYPES[q.dtype]
+    with _On(q.device, stream) as st:
+        if out is None:
+            out = torch.empty((B, heads, n, d), dtype=q.dtype, device=q.device)
+        else:
+            _check(q.device, q.dtype, (out,))
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+        lse = torch.empty((B, heads, n), dtype=torch.float32, device=q.device) if return_lse else None
+        keep, ws, nbytes = _workspace(workspace, lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, dt),
+                                      q.device)
+        status = lisa_cross_attention(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v),
+                                      out.data_ptr(), _strides(out), lse.data_ptr() if return_lse else None, B, heads,
+                                      kv_heads, n, m, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
+                                      None if kv_lens is None else kv_lens.data_ptr(),
+                                      None if bias is None else bias.struct, dt, ws, nbytes, st)
+        del keep
+    if status != LISA_OK:
+        raise LisaError(status)
+    return (out, lse) if return_lse else out
+
+
+def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+                             dout: torch.Tensor, *, scale=None, kv_lens=None, bias: RelativeBias = None,
+                             workspace=None, stream=None):
+    """Gradients of ``cross_attention`` for the upstream gradient ``dout``, given
+    the forward's ``out`` and ``lse``: (dq, dk, dv), with ``bias`` also the
+    table's gradient dtable (fp32, the table's shape), summed over the batch."""
+    B, heads, kv_heads, n, m, d = _shapes(q, k, v, kv_lens, bias)
+    _check(q.device, q.dtype, (out, dout))
+    if out.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("out and dout must have q's shape")
+    if not (lse.is_cuda and lse.device == q.device and lse.dtype == torch.float32 and lse.is_contiguous()
+            and tuple(lse.shape) == (B, heads, n)):
+        raise ValueError("lse must be the forward's contiguous fp32 tensor [B, heads, n]")
+    if bias is not None and bias.starts is not None:
+        raise ValueError("a bias with a start for each batch entry has no backward")
+    dt = _DTYPES[q.dtype]
+    struct = None if bias is None else bias.struct
+    with _On(q.device, stream) as st:
+        dq = torch.empty((B, heads, n, d), dtype=q.dtype, device=q.device)
+        dk = torch.empty((B, kv_heads, m, d), dtype=q.dtype, device=q.device)
+        dv = torch.empty((B, kv_heads, m, d), dtype=q.dtype, device=q.device)
+        dtable = None if bias is None else torch.empty_like(bias.table)
+        need = lisa_cross_attention_backward_workspace_bytes(B, heads, kv_heads, n, m, d, struct, dt)
+        keep, ws, nbytes = _workspace(workspace, need, q.device)
+        status = lisa_cross_attention_backward(
+            q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), out.data_ptr(),
+            _strides(out), lse.data_ptr(), dout.data_ptr(), _strides(dout), dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr(), None if bias is None else dtable.data_ptr(), B, heads, kv_heads, n, m, d,
+            1.0 / math.sqrt(d) if scale is None else float(scale), None if kv_lens is None else kv_lens.data_ptr(),
+            struct, dt, ws, nbytes, st)
+        del keep
+    if status != LISA_OK:
+        raise LisaError(status)
+    return (dq, dk, dv) if bias is None else (dq, dk, dv, dtable)
+
+
+def relative_bias(bias: RelativeBias, dtype: torch.dtype = torch.float32, *, out=None, stream=None) -> torch.Tensor:
+    """The bias as a matrix [heads, n, m] (fp32 or bf16), for a layer that adds it itself."""
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32 or bfloat16")
+    if bias.starts is not None:
+        raise ValueError("a bias with a start for each batch entry has no matrix")
+    shape = (bias.heads, bias.n, bias.m)
+    with _On(bias.table.device, stream) as st:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=bias.table.device)
+        elif not (out.is_cuda and out.device == bias.table.device and out.dtype == dtype and out.is_contiguous()
+                  and tuple(out.shape) == shape):
+            raise ValueError("out must be a contiguous %s CUDA tensor [heads, n, m]" % (dtype,))
+        status = lisa_relative_bias(bias.struct, bias.heads, out.data_ptr(), _DTYPES[dtype], st)
+    if status != LISA_OK:
+        raise LisaError(status)
+    return out
+
+
+def relative_bias_backward(bias: RelativeBias, dbias: torch.Tensor, *, workspace=None, stream=None) -> torch.Tensor:
+    """The table's gradient (fp32, the table's shape): the sums of ``dbias``
+    [heads, n, m] (fp32 or bf16) over the pairs of each bucket."""
+    if bias.starts is not None:
+        raise ValueError("a bias with a start for each batch entry has no matrix")
+    if not (dbias.is_cuda and dbias.device == bias.table.device and dbias.dtype in _DTYPES and dbias.is_contiguous()
+            and tuple(dbias.shape) == (bias.heads, bias.n, bias.m)):
+        raise ValueError("dbias must be a contiguous fp32 or bf16 CUDA tensor [heads, n, m]")
+    with _On(dbias.device, stream) as st:
+        dtable = torch.empty_like(bias.table)
+        keep, ws, nbytes = _workspace(workspace, lisa_relative_bias_backward_workspace_bytes(bias.struct, bias.heads),
+                                      dbias.device)
+        status = lisa_relative_bias_backward(bias.struct, bias.heads, dbias.data_ptr(), _DTYPES[dbias.dtype],
+                                             dtable.data_ptr(), ws, nbytes, st)
+        del keep
+    if status != LISA_OK:
+        raise LisaError(status)
+    return dtable

@@ -1,0 +1,99 @@
+// lisa_attn.h -- host-side problem description of the cross attention and the
+// relative position bias, the device view of the bias rule, and the launcher
+// entry points of the kernels.  Not part of the public ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "lisa_attention.h"
+
+namespace lisa {
+namespace attn {
+
+// One axis of the bucket rule as the kernels read it.  The log rule's borders
+// are whole numbers found on the host: thr[t] is the smallest |x| of far
+// bucket t + 1 (buckets E + 1, E + 2, ...), so no kernel takes a logarithm.
+struct AxisDev {
+    int log_rule;      // 0: exact
+    int half, nexact;  // log: buckets per side, of these one by one
+    int D;
+    int nthr;
+    int thr[32];
+};
+
+// The bias as the kernels read it.  Pair (i, j) has the offset index
+//   sequence  clamp(step_c j - i - start, lo_c, hi_c) - lo_c
+//   grid      a(j) - b(i) + c0, a(j) = step_r P rk + step_c ck, b(i) = P rq + cq
+// into a table of `entries` values, one per offset, that each CTA gathers from
+// the bucket table for its head.  The pitch P is at least the number of column
+// offsets and congruent to q_cols modulo 32: 32 consecutive queries of one key
+// then fall into 32 different shared-memory banks, across row ends too.
+struct BiasDev {
+    int mode;          // 0 none, 1 sequence, 2 grid
+    int entries;
+    const float *table;
+    int heads;
+    int q_cols, k_cols, P, step_r, step_c, c0;
+    int start;         // sequence: column start
+    const int *starts; // sequence: per batch entry
+    int lo_r, lo_c, hi_c;
+    int ncol_off;      // grid: column offsets (entries of a row behind it are padding)
+    int col_buckets;
+    AxisDev rows, cols;
+};
+
+struct Tensor {
+    const void *p;
+    long long sb, sh, st;  // strides in elements
+};
+
+struct Problem {
+    Tensor Q, K, V, O, dO;
+    float *lse;
+    int B, heads, kv_heads, group, n, m, d;
+    float scale;
+    const int *kv_lens;
+    int dtype;
+    BiasDev bias;
+    void *dQ, *dK, *dV;
+    float *delta;          // [B][heads][n]: sum_j p dP, written by the dQ kernel
+    float *dbias;          // [heads][n][m] fp32: dS summed over the batch
+    // forward split over the keys
+    int splits;
+    float *o_part;         // [splits][B][heads][n][d]
+    float *lse_part;       // [splits][B][heads][n]
+    // dK / dV split over the queries
+    int q_splits;
+    float *dk_part, *dv_part;  // [q_splits][B][kv_heads][m][d]
+};
+
+// Dense bias gradient.
+struct BiasGradPlan {
+    int mode_rows;      // row pairs per head (q_rows * k_rows)
+    int chunk;          // query columns of one residue per item
+    int chunks;         // chunks of a row
+    int etiles;         // tiles of diagonals
+    int items;          // items per head
+    size_t part_bytes;
+};
+
+// --- plans -------------------------------------------------------------------
+// Fills `dev` from the public struct; checks everything but the batch.
+lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev);
+
+// --- launchers ---------------------------------------------------------------
+cudaError_t launch_bias_dense(const lisa_rel_bias &b, const BiasDev &dev, void *out, int dtype, cudaStream_t s);
+size_t bias_grad_bytes(const lisa_rel_bias &b, int heads);
+cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int dtype, float *dtable,
+                             void *ws, cudaStream_t s);
+
+cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s);
+cudaError_t launch_simt_dq(const Problem &p, cudaStream_t s);
+cudaError_t launch_simt_dkdv(const Problem &p, cudaStream_t s);
+cudaError_t launch_simt_dbias(const Problem &p, cudaStream_t s);
+
+}  // namespace attn
+}  // namespace lisa

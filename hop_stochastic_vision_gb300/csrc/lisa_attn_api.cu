@@ -1,0 +1,369 @@
+// lisa_attn_api.cu -- the C ABI of the cross attention and the relative
+// position bias: argument checks, the bias rule as the kernels read it, the
+// workspace carve-up and the dispatch.  Every check runs before the first launch.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "lisa_attention.h"
+#include "lisa_attn.h"
+
+namespace lisa {
+namespace attn {
+namespace {
+
+constexpr int kMaxTokens = 1 << 22;      // queries or keys of one head
+constexpr int kMaxGridDim = 65535;       // batch entries and heads
+constexpr int kMaxDistance = 8191;
+constexpr long long kMaxPosition = 1LL << 28;
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+lisa_status axis_dev(const lisa_axis_rule &r, AxisDev &a) {
+    a = AxisDev{};
+    if (r.rule == LISA_BUCKETS_EXACT) {
+        if (r.max_distance < 0 || r.buckets != 2 * (long long)r.max_distance + 1) return LISA_ERR_INVALID_ARG;
+        if (r.max_distance > kMaxDistance) return LISA_ERR_UNSUPPORTED;
+        a.D = r.max_distance;
+        return LISA_OK;
+    }
+    if (r.rule != LISA_BUCKETS_LOG) return LISA_ERR_INVALID_ARG;
+    if (r.buckets < 4 || r.buckets % 4 != 0 || r.max_distance <= r.buckets / 4) return LISA_ERR_INVALID_ARG;
+    if (r.buckets > 128 || r.max_distance > kMaxDistance) return LISA_ERR_UNSUPPORTED;
+    a.log_rule = 1;
+    a.half = r.buckets / 2;
+    a.nexact = r.buckets / 4;
+    a.D = r.max_distance;
+    a.nthr = a.half - a.nexact - 1;
+    const double E = a.nexact, ratio = (double)a.D / E;
+    for (int t = 0; t < a.nthr; ++t) {
+        // far bucket t + 1 begins at E ratio^((t + 1) / E); a border that is a
+        // whole number is one of its own bucket, whatever pow's last bit says
+        const double x = E * std::pow(ratio, (double)(t + 1) / E);
+        const double near = std::nearbyint(x);
+        a.thr[t] = (int)(std::fabs(x - near) <= 1e-12 * x ? near : std::ceil(x));
+    }
+    return LISA_OK;
+}
+
+}  // namespace
+
+lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev) {
+    dev = BiasDev{};
+    if (!b || heads < 1) return LISA_ERR_INVALID_ARG;
+    if (b->q_rows < 1 || b->q_cols < 1 || b->k_rows < 1 || b->k_cols < 1) return LISA_ERR_INVALID_ARG;
+    if (b->key_step_rows < 1 || b->key_step_cols < 1) return LISA_ERR_INVALID_ARG;
+    if (heads > kMaxGridDim) return LISA_ERR_UNSUPPORTED;
+    if ((long long)b->q_rows * b->q_cols > kMaxTokens || (long long)b->k_rows * b->k_cols > kMaxTokens)
+        return LISA_ERR_UNSUPPORTED;
+    lisa_status st = axis_dev(b->rows, dev.rows);
+    if (st == LISA_OK) st = axis_dev(b->cols, dev.cols);
+    if (st != LISA_OK) return st;
+    const long long span_r = (long long)b->key_step_rows * (b->k_rows - 1);
+    const long long span_c = (long long)b->key_step_cols * (b->k_cols - 1);
+    if (span_r > kMaxPosition || span_c > kMaxPosition || std::llabs((long long)b->start_rows) > kMaxPosition ||
+        std::llabs((long long)b->start_cols) > kMaxPosition)
+        return LISA_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(b->table) & 3u) != 0 || (reinterpret_cast<uintptr_t>(b->starts) & 3u) != 0)
+        return LISA_ERR_INVALID_ARG;
+    dev.table = b->table;
+    dev.heads = heads;
+    dev.q_cols = b->q_cols;
+    dev.k_cols = b->k_cols;
+    dev.step_r = b->key_step_rows;
+    dev.step_c = b->key_step_cols;
+    dev.start = b->start_cols;
+    dev.starts = b->starts;
+    dev.col_buckets = b->cols.buckets;
+    if (b->q_rows == 1 && b->k_rows == 1) {
+        dev.mode = 1;
+        dev.lo_r = -b->start_rows;   // the rows' one offset
+        const long long D = dev.cols.D;
+        long long lo = -D, hi = D;
+        if (!b->starts) {
+            lo = std::min(std::max(-(long long)(b->q_cols - 1) - b->start_cols, -D), D);
+            hi = std::min(std::max(span_c - b->start_cols, -D), D);
+        }
+        dev.lo_c = (int)lo;
+        dev.hi_c = (int)hi;
+        dev.entries = (int)(hi - lo + 1);
+        return LISA_OK;
+    }
+    if (b->starts) return LISA_ERR_INVALID_ARG;
+    dev.mode = 2;
+    const long long nr = span_r + b->q_rows, nc = span_c + b->q_cols;
+    const long long P = nc + ((b->q_cols - nc) % 32 + 32) % 32;
+    if (nr * P > LISA_MAX_OFFSETS) return LISA_ERR_UNSUPPORTED;
+    dev.P = (int)P;
+    dev.ncol_off = (int)nc;
+    dev.lo_r = -(b->q_rows - 1) - b->start_rows;
+    dev.lo_c = -(b->q_cols - 1) - b->start_cols;
+    dev.c0 = (b->q_rows - 1) * dev.P + b->q_cols - 1;
+    dev.entries = (int)(nr * P);
+    return LISA_OK;
+}
+
+namespace {
+
+lisa_status check_sizes(int B, int heads, int kv_heads, int n, int m, int d, int dtype) {
+    if (B < 0 || heads < 0 || kv_heads < 0 || n < 0 || m < 0) return LISA_ERR_INVALID_ARG;
+    if (dtype != LISA_F32 && dtype != LISA_BF16) return LISA_ERR_INVALID_ARG;
+    if (d < 1 || (heads > 0 && (kv_heads < 1 || heads % kv_heads != 0))) return LISA_ERR_INVALID_ARG;
+    if (d != 16 && d != 32 && d != 64) return LISA_ERR_UNSUPPORTED;
+    if (n > kMaxTokens || m > kMaxTokens || B > kMaxGridDim || heads > kMaxGridDim) return LISA_ERR_UNSUPPORTED;
+    return LISA_OK;
+}
+
+// Strides of a [B][heads][tokens][d] tensor: multiples of 16 bytes, tokens of a
+// head apart, extents within 63 bits.  `out`: no stride repeats an entry.
+bool good_strides(const lisa_strides *s, int B, int heads, int tokens, int d, size_t esz, bool out) {
+    if (!s) return false;
+    const long long q = 16 / (long long)esz, most = 1LL << 38;
+    for (const long long x : {s->batch, s->head, s->token})
+        if (x < 0 || x > most || x % q != 0) return false;
+    if (tokens > 1 && s->token < d) return false;
+    if (out && ((B > 1 && s->batch < d) || (heads > 1 && s->head < d))) return false;
+    return true;
+}
+
+// Bytes from the first to behind the last element.
+size_t extent(const lisa_strides *s, int B, int heads, int tokens, int d, size_t esz) {
+    return ((size_t)s->batch * (size_t)(B - 1) + (size_t)s->head * (size_t)(heads - 1) +
+            (size_t)s->token * (size_t)(tokens - 1) + (size_t)d) * esz;
+}
+
+struct Span {
+    uintptr_t lo, hi;
+    Span(const void *p, size_t bytes) : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + bytes) {}
+    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Shared by the forward and the backward: everything but the outputs.
+lisa_status fill(Problem &p, const void *Q, const lisa_strides *qs, const void *K, const lisa_strides *ks,
+                 const void *V, const lisa_strides *vs, int B, int heads, int kv_heads, int n, int m, int d,
+                 float scale, const int *kv_lens, const lisa_rel_bias *bias, int dtype) {
+    lisa_status st = check_sizes(B, heads, kv_heads, n, m, d, dtype);
+    if (st != LISA_OK) return st;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return LISA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(kv_lens) & 3u) != 0) return LISA_ERR_INVALID_ARG;
+    p.B = B; p.heads = heads; p.kv_heads = kv_heads;
+    p.group = heads > 0 ? heads / kv_heads : 1;
+    p.n = n; p.m = m; p.d = d;
+    p.scale = scale;
+    p.kv_lens = kv_lens;
+    p.dtype = dtype;
+    p.splits = p.q_splits = 1;
+    if (B == 0 || heads == 0 || n == 0) return LISA_OK;   // the caller deals with empty problems
+    const size_t esz = dtype == LISA_BF16 ? 2 : 4;
+    if (!Q || !aligned16(Q) || !good_strides(qs, B, heads, n, d, esz, false)) return LISA_ERR_INVALID_ARG;
+    p.Q = {Q, qs->batch, qs->head, qs->token};
+    if (m > 0) {
+        if (!K || !V || !aligned16(K) || !aligned16(V) || !good_strides(ks, B, kv_heads, m, d, esz, false) ||
+            !good_strides(vs, B, kv_heads, m, d, esz, false))
+            return LISA_ERR_INVALID_ARG;
+        p.K = {K, ks->batch, ks->head, ks->token};
+        p.V = {V, vs->batch, vs->head, vs->token};
+    }
+    if (bias && m > 0) {
+        if (!bias->table) return LISA_ERR_INVALID_ARG;
+        if ((long long)bias->q_rows * bias->q_cols != n || (long long)bias->k_rows * bias->k_cols != m)
+            return LISA_ERR_INVALID_ARG;
+        st = bias_dev(bias, heads, p.bias);
+        if (st != LISA_OK) return st;
+    }
+    return LISA_OK;
+}
+
+struct BwdPlan {
+    size_t off_delta, off_dbias, off_grad, total;
+};
+
+BwdPlan backward_plan(int B, int heads, int n, int m, const lisa_rel_bias *bias) {
+    BwdPlan pl{};
+    size_t off = 0;
+    pl.off_delta = off;
+    off = align_up(off + (size_t)B * heads * n * sizeof(float));
+    if (bias) {
+        pl.off_dbias = off;
+        off = align_up(off + (size_t)heads * n * m * sizeof(float));
+        pl.off_grad = off;
+        off = align_up(off + bias_grad_bytes(*bias, heads));
+    }
+    pl.total = off;
+    return pl;
+}
+
+lisa_status status_of(cudaError_t e) { return e == cudaSuccess ? LISA_OK : LISA_ERR_CUDA; }
+
+size_t table_floats(const lisa_rel_bias &b, int heads) {
+    return (size_t)b.rows.buckets * (size_t)b.cols.buckets * (size_t)heads;
+}
+
+// Pairs of one head that the bias matrix and its gradient index with 32 bits.
+bool matrix_fits(const lisa_rel_bias &b) {
+    return (long long)b.q_rows * b.q_cols * ((long long)b.k_rows * b.k_cols) <= (1LL << 31) - 1 - 65536 &&
+           (long long)b.q_rows * b.k_rows <= kMaxGridDim;
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace lisa
+
+using namespace lisa::attn;
+
+extern "C" lisa_status lisa_relative_bias(const lisa_rel_bias *bias, int heads, void *out, int dtype, void *stream) {
+    if (dtype != LISA_F32 && dtype != LISA_BF16) return LISA_ERR_INVALID_ARG;
+    BiasDev dev;
+    const lisa_status st = bias_dev(bias, heads, dev);
+    if (st != LISA_OK) return st;
+    if (!matrix_fits(*bias)) return LISA_ERR_UNSUPPORTED;
+    if (!bias->table || !out || bias->starts || !aligned16(out)) return LISA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)heads * bias->q_rows * bias->q_cols * bias->k_rows * bias->k_cols *
+                         (dtype == LISA_BF16 ? 2 : 4);
+    if (Span(out, bytes).meets(Span(bias->table, table_floats(*bias, heads) * 4))) return LISA_ERR_INVALID_ARG;
+    return status_of(launch_bias_dense(*bias, dev, out, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t lisa_relative_bias_backward_workspace_bytes(const lisa_rel_bias *bias, int heads) {
+    BiasDev dev;
+    if (bias_dev(bias, heads, dev) != LISA_OK || !matrix_fits(*bias)) return 0;
+    return bias_grad_bytes(*bias, heads);
+}
+
+extern "C" lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, int heads, const void *dbias, int dtype,
+                                                   float *dtable, void *workspace, size_t workspace_bytes,
+                                                   void *stream) {
+    if (dtype != LISA_F32 && dtype != LISA_BF16) return LISA_ERR_INVALID_ARG;
+    BiasDev dev;
+    const lisa_status st = bias_dev(bias, heads, dev);
+    if (st != LISA_OK) return st;
+    if (!matrix_fits(*bias)) return LISA_ERR_UNSUPPORTED;
+    if (!dbias || !dtable || bias->starts || !aligned16(dbias) || (reinterpret_cast<uintptr_t>(dtable) & 3u) != 0)
+        return LISA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)heads * bias->q_rows * bias->q_cols * bias->k_rows * bias->k_cols *
+                         (dtype == LISA_BF16 ? 2 : 4);
+    if (Span(dtable, table_floats(*bias, heads) * 4).meets(Span(dbias, bytes))) return LISA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < bias_grad_bytes(*bias, heads)) return LISA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
+    return status_of(
+        launch_bias_grad(*bias, dev, dbias, dtype, dtable, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t lisa_cross_attention_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,
+                                                       int dtype) {
+    (void)B; (void)heads; (void)kv_heads; (void)n; (void)m; (void)d; (void)dtype;
+    return 0;
+}
+
+extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q_strides, const void *K,
+                                            const lisa_strides *k_strides, const void *V,
+                                            const lisa_strides *v_strides, void *O, const lisa_strides *o_strides,
+                                            float *lse, int B, int heads, int kv_heads, int n, int m, int d,
+                                            float scale, const int *kv_lens, const lisa_rel_bias *bias, int dtype,
+                                            void *workspace, size_t workspace_bytes, void *stream) {
+    (void)workspace; (void)workspace_bytes;
+    Problem p{};
+    lisa_status st = fill(p, Q, q_strides, K, k_strides, V, v_strides, B, heads, kv_heads, n, m, d, scale, kv_lens,
+                          bias, dtype);
+    if (st != LISA_OK) return st;
+    if (B == 0 || heads == 0 || n == 0) return LISA_OK;
+    const size_t esz = dtype == LISA_BF16 ? 2 : 4;
+    if (!O || !aligned16(O) || !good_strides(o_strides, B, heads, n, d, esz, true)) return LISA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return LISA_ERR_INVALID_ARG;
+    const Span o(O, extent(o_strides, B, heads, n, d, esz));
+    if (o.meets(Span(Q, extent(q_strides, B, heads, n, d, esz)))) return LISA_ERR_INVALID_ARG;
+    if (m > 0 && (o.meets(Span(K, extent(k_strides, B, kv_heads, m, d, esz))) ||
+                  o.meets(Span(V, extent(v_strides, B, kv_heads, m, d, esz)))))
+        return LISA_ERR_INVALID_ARG;
+    p.O = {O, o_strides->batch, o_strides->head, o_strides->token};
+    p.lse = lse;
+    return status_of(launch_simt_forward(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t lisa_cross_attention_backward_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,
+                                                                const lisa_rel_bias *bias, int dtype) {
+    if (check_sizes(B, heads, kv_heads, n, m, d, dtype) != LISA_OK) return 0;
+    if (B == 0 || heads == 0 || n == 0 || m == 0) return 0;
+    if (bias) {
+        BiasDev dev;
+        if (bias_dev(bias, heads, dev) != LISA_OK || !matrix_fits(*bias)) return 0;
+    }
+    return backward_plan(B, heads, n, m, bias).total;
+}
+
+extern "C" lisa_status lisa_cross_attention_backward(
+    const void *Q, const lisa_strides *q_strides, const void *K, const lisa_strides *k_strides, const void *V,
+    const lisa_strides *v_strides, const void *O, const lisa_strides *o_strides, const float *lse, const void *dO,
+    const lisa_strides *do_strides, void *dQ, void *dK, void *dV, float *dtable, int B, int heads, int kv_heads, int n,
+    int m, int d, float scale, const int *kv_lens, const lisa_rel_bias *bias, int dtype, void *workspace,
+    size_t workspace_bytes, void *stream) {
+    Problem p{};
+    lisa_status st = fill(p, Q, q_strides, K, k_strides, V, v_strides, B, heads, kv_heads, n, m, d, scale, kv_lens,
+                          bias, dtype);
+    if (st != LISA_OK) return st;
+    if ((bias == nullptr) != (dtable == nullptr)) return LISA_ERR_INVALID_ARG;
+    if (bias && bias->starts) return LISA_ERR_INVALID_ARG;   // dS is summed over the batch pair by pair
+    if ((reinterpret_cast<uintptr_t>(dtable) & 3u) != 0) return LISA_ERR_INVALID_ARG;
+    const size_t esz = dtype == LISA_BF16 ? 2 : 4;
+    const size_t dq_bytes = (size_t)B * heads * n * d * esz, dk_bytes = (size_t)B * kv_heads * m * d * esz;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (dq_bytes == 0 || dk_bytes == 0) {   // nothing to differentiate: what there is of the gradients is 0
+        if ((dq_bytes && !dQ) || (dk_bytes && (!dK || !dV))) return LISA_ERR_INVALID_ARG;
+        if (bias) {
+            AxisDev a;   // the table's size has to make sense before it is written
+            if (axis_dev(bias->rows, a) != LISA_OK || axis_dev(bias->cols, a) != LISA_OK) return LISA_ERR_INVALID_ARG;
+        }
+        if ((dq_bytes && cudaMemsetAsync(dQ, 0, dq_bytes, cs) != cudaSuccess) ||
+            (dk_bytes && (cudaMemsetAsync(dK, 0, dk_bytes, cs) != cudaSuccess ||
+                          cudaMemsetAsync(dV, 0, dk_bytes, cs) != cudaSuccess)) ||
+            (bias && heads > 0 && cudaMemsetAsync(dtable, 0, table_floats(*bias, heads) * 4, cs) != cudaSuccess))
+            return LISA_ERR_CUDA;
+        return LISA_OK;
+    }
+    if (!O || !lse || !dO || !dQ || !dK || !dV) return LISA_ERR_INVALID_ARG;
+    if (!aligned16(O) || !aligned16(dO) || !aligned16(dQ) || !aligned16(dK) || !aligned16(dV) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+        return LISA_ERR_INVALID_ARG;
+    if (!good_strides(o_strides, B, heads, n, d, esz, false) || !good_strides(do_strides, B, heads, n, d, esz, false))
+        return LISA_ERR_INVALID_ARG;
+    const Span outs[4] = {Span(dQ, dq_bytes), Span(dK, dk_bytes), Span(dV, dk_bytes),
+                          Span(dtable, bias ? table_floats(*bias, heads) * 4 : 0)};
+    const Span ins[7] = {Span(Q, extent(q_strides, B, heads, n, d, esz)),
+                         Span(K, extent(k_strides, B, kv_heads, m, d, esz)),
+                         Span(V, extent(v_strides, B, kv_heads, m, d, esz)),
+                         Span(O, extent(o_strides, B, heads, n, d, esz)),
+                         Span(dO, extent(do_strides, B, heads, n, d, esz)),
+                         Span(lse, (size_t)B * heads * n * 4),
+                         Span(bias ? bias->table : nullptr, bias ? table_floats(*bias, heads) * 4 : 0)};
+    for (int a = 0; a < (bias ? 4 : 3); ++a) {
+        for (const Span &in : ins)
+            if (outs[a].meets(in)) return LISA_ERR_INVALID_ARG;
+        for (int c = 0; c < a; ++c)
+            if (outs[a].meets(outs[c])) return LISA_ERR_INVALID_ARG;
+    }
+    if (bias && !matrix_fits(*bias)) return LISA_ERR_UNSUPPORTED;
+    const BwdPlan pl = backward_plan(B, heads, n, m, bias);
+    if (!workspace || workspace_bytes < pl.total) return LISA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
+    p.O = {O, o_strides->batch, o_strides->head, o_strides->token};
+    p.dO = {dO, do_strides->batch, do_strides->head, do_strides->token};
+    p.lse = const_cast<float *>(lse);
+    p.dQ = dQ;
+    p.dK = dK;
+    p.dV = dV;
+    char *ws = static_cast<char *>(workspace);
+    p.delta = reinterpret_cast<float *>(ws + pl.off_delta);
+    p.dbias = reinterpret_cast<float *>(ws + pl.off_dbias);
+    cudaError_t e = launch_simt_dq(p, cs);
+    if (e == cudaSuccess) e = launch_simt_dkdv(p, cs);
+    if (e == cudaSuccess && bias) e = launch_simt_dbias(p, cs);
+    if (e == cudaSuccess && bias) {
+        // the matrix of the batch's dS, then as the bias matrix's own gradient
+        e = launch_bias_grad(*bias, p.bias, p.dbias, LISA_F32, dtable, ws + pl.off_grad, cs);
+    }
+    return status_of(e);
+}

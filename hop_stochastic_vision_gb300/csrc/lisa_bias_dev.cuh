@@ -1,0 +1,85 @@
+// lisa_bias_dev.cuh -- device side of the bucket rule, shared by the bias
+// matrix kernels and the attention kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "lisa_attn.h"
+
+namespace lisa {
+namespace attn {
+namespace {
+
+__device__ __forceinline__ int axis_bucket(const AxisDev &ax, int x) {
+    if (!ax.log_rule) return min(max(x, -ax.D), ax.D) + ax.D;
+    const int a = abs(x), side = x > 0 ? ax.half : 0;
+    if (a < ax.nexact) return side + a;
+    int b = ax.nexact;
+    for (int t = 0; t < ax.nthr; ++t) b += a >= ax.thr[t] ? 1 : 0;
+    return side + b;
+}
+
+constexpr int kFar = 1 << 30;
+constexpr int kFarStart = 1 << 29;
+
+// The offsets lo .. hi that fall into bucket b (hi < lo: none; open ends at +-kFar).
+__device__ __forceinline__ void bucket_range(const AxisDev &ax, int b, int &lo, int &hi) {
+    if (!ax.log_rule) {
+        lo = b == 0 ? -kFar : b - ax.D;
+        hi = b == 2 * ax.D ? kFar : b - ax.D;
+        return;
+    }
+    const bool pos = b >= ax.half;
+    const int k = pos ? b - ax.half : b;
+    int a0, a1;   // |x| range
+    if (k < ax.nexact) {
+        a0 = a1 = k;
+    } else {
+        const int t = k - ax.nexact;   // far bucket t begins at thr[t - 1] (t = 0: at nexact)
+        a0 = t == 0 ? ax.nexact : ax.thr[t - 1];
+        a1 = t == ax.nthr ? kFar : ax.thr[t] - 1;
+    }
+    if (pos) {   // x > 0
+        lo = max(a0, 1);
+        hi = a1;
+    } else {     // x <= 0
+        lo = -a1;
+        hi = -a0;
+    }
+    if (a1 < a0) { lo = 1; hi = 0; }
+}
+
+// Row of the bucket table behind offset entry e.
+__device__ __forceinline__ int entry_bucket(const BiasDev &b, int e) {
+    int dr = b.lo_r, dc = b.lo_c + e;
+    if (b.mode == 2) {
+        dr = b.lo_r + e / b.P;
+        dc = b.lo_c + e % b.P;
+    }
+    return axis_bucket(b.rows, dr) * b.col_buckets + axis_bucket(b.cols, dc);
+}
+
+// The head's bias of every offset, times `mul`, into shared memory.
+__device__ __forceinline__ void fill_offsets(const BiasDev &b, int head, float mul, float *out, int tid, int nthreads) {
+    for (int e = tid; e < b.entries; e += nthreads)
+        out[e] = __ldg(b.table + (size_t)entry_bucket(b, e) * b.heads + head) * mul;
+}
+
+// Offset index of a pair: off_key(j) - off_query(i), then clamped to the table
+// (sequence) or inside it by construction (grid).
+__device__ __forceinline__ int off_key(const BiasDev &b, int j) {
+    if (b.mode == 1) return b.step_c * j;
+    return b.step_r * b.P * (j / b.k_cols) + b.step_c * (j % b.k_cols);
+}
+__device__ __forceinline__ int off_query(const BiasDev &b, int i, int start) {
+    if (b.mode == 1) return i + start + b.lo_c;
+    return b.P * (i / b.q_cols) + i % b.q_cols - b.c0;
+}
+__device__ __forceinline__ int bias_start(const BiasDev &b, int batch) {
+    // far starts stop where every offset is in the outermost bucket already (and sums fit an int)
+    return b.starts ? min(max(b.starts[batch], -kFarStart), kFarStart) : b.start;
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace lisa

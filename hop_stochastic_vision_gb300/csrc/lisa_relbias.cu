@@ -1,0 +1,249 @@
+// lisa_relbias.cu -- the relative position bias as a matrix, and its gradient.
+#include <algorithm>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "lisa_attn.h"
+#include "lisa_bias_dev.cuh"
+
+namespace lisa {
+namespace attn {
+namespace {
+
+constexpr int kDenseThreads = 256;
+
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// out[h][i][j] = offset table of head h at the pair's offset.  The head's n m
+// elements are written as one run of 16-byte vectors (ragged ends element by
+// element), so rows of any length give full-width stores; a vector finds its
+// first pair by one division and walks from there.
+template <typename T>
+__global__ void __launch_bounds__(kDenseThreads) bias_dense(BiasDev b, T *out, int n, int m) {
+    extern __shared__ __align__(16) float lut[];
+    constexpr int kVec = 16 / (int)sizeof(T);
+    const int h = blockIdx.y, tid = threadIdx.x;
+    fill_offsets(b, h, 1.f, lut, tid, kDenseThreads);
+    __syncthreads();
+    const unsigned count = (unsigned)n * (unsigned)m;
+    T *base = out + (size_t)h * count;
+    const unsigned head = min(count, (unsigned)((16u - (unsigned)(reinterpret_cast<uintptr_t>(base) & 15u)) & 15u) /
+                                         (unsigned)sizeof(T));
+    const unsigned vecs = (count - head) / kVec, tail = head + vecs * kVec;
+    auto value = [&](int i, int j) {
+        return lut[min(max(off_key(b, j) - off_query(b, i, b.start), 0), b.entries - 1)];
+    };
+    if (blockIdx.x == 0) {
+        for (unsigned f = tid; f < head; f += kDenseThreads) put(base + f, value((int)(f / m), (int)(f % m)));
+        for (unsigned f = tail + tid; f < count; f += kDenseThreads) put(base + f, value((int)(f / m), (int)(f % m)));
+    }
+    for (unsigned v = blockIdx.x * kDenseThreads + tid; v < vecs; v += gridDim.x * kDenseThreads) {
+        const unsigned f = head + v * kVec;
+        int i = (int)(f / (unsigned)m), j = (int)(f - (unsigned)i * (unsigned)m);
+        int oq = off_query(b, i, b.start), ok = off_key(b, j), ck = b.mode == 2 ? j % b.k_cols : 0;
+        __align__(16) T x[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            put(x + e, lut[min(max(ok - oq, 0), b.entries - 1)]);
+            if (++j == m) {
+                j = ck = ok = 0;
+                oq = off_query(b, min(++i, n - 1), b.start);
+            } else {
+                ok += b.step_c;
+                if (b.mode == 2 && ++ck == b.k_cols) {
+                    ck = 0;
+                    ok += b.step_r * b.P - b.step_c * b.k_cols;
+                }
+            }
+        }
+        *reinterpret_cast<uint4 *>(base + f) = *reinterpret_cast<const uint4 *>(x);
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// For one pair of rows (rq, rk) of the two grids the q_cols x k_cols block of
+// dbias is summed along its diagonals: with u = q_cols - 1 - cq = s q + r
+// (s the key step, r < s) and e = ck + q, the pair's column offset is
+// s e + r - (q_cols - 1) - start, so a thread that holds (r, e) and walks q
+// adds up one offset in a register, and the threads of a warp read
+// neighbouring keys of one row.  An item is a chunk of q of one row pair; its
+// diagonal sums are folded into the column buckets (each a range of offsets)
+// and left as partials; a second kernel adds the partials of each row bucket
+// in a fixed order.
+struct GradParams {
+    BiasDev b;
+    int q_rows, q_cols, k_rows, k_cols, step_r, step_c, start_r, start_c;
+    int residues, ch, nchunk, etot, ntile, threads;
+    int row_buckets, col_buckets;
+    long long n, m;
+    float *part;   // [heads][q_rows][k_rows][nchunk][ntile][col_buckets]
+};
+
+__device__ __forceinline__ float get(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+
+template <typename T>
+__global__ void __launch_bounds__(256) bias_grad_part(const __grid_constant__ GradParams g, const T *dbias) {
+    __shared__ float diag[256];
+    const int t = threadIdx.x, h = blockIdx.z;
+    const int tile = blockIdx.x % g.ntile, chunk = blockIdx.x / g.ntile;
+    const int rq = blockIdx.y / g.k_rows, rk = blockIdx.y % g.k_rows;
+    const int q0 = chunk * g.ch;
+    const int flat = tile * g.threads + t;
+    const int r = flat / g.etot, e = q0 + flat % g.etot;
+    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+    if (r < g.residues) {
+        const int nr = (g.q_cols - 1 - r) / g.step_c + 1;
+        int q = max(q0, e - g.k_cols + 1);
+        const int q1 = min(min(q0 + g.ch, nr), e + 1);
+        // element (q): query column q_cols - 1 - r - s q, key column e - q
+        const T *p = dbias + ((long long)h * g.n + (long long)rq * g.q_cols + (g.q_cols - 1 - r - (long long)g.step_c * q)) * g.m +
+                     (long long)rk * g.k_cols + (e - q);
+        const long long step = -((long long)g.step_c * g.m + 1);
+        for (; q + 8 <= q1; q += 8) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = get(p + u * step);
+            a0 += v[0] + v[4];
+            a1 += v[1] + v[5];
+            a2 += v[2] + v[6];
+            a3 += v[3] + v[7];
+            p += 8 * step;
+        }
+        for (; q < q1; ++q, p += step) a0 += get(p);
+    }
+    diag[t] = (a0 + a1) + (a2 + a3);
+    __syncthreads();
+    float *out = g.part + ((((size_t)h * g.q_rows + rq) * g.k_rows + rk) * (g.nchunk * g.ntile) + blockIdx.x) *
+                              (size_t)g.col_buckets;
+    const int last = g.step_c * (g.k_cols - 1) + g.q_cols - 1;   // offsets run over o = 0 .. last
+    const int shift = g.q_cols - 1 + g.start_c;
+    for (int cb = t; cb < g.col_buckets; cb += g.threads) {
+        int lo, hi;
+        bucket_range(g.b.cols, cb, lo, hi);
+        // offsets of this chunk: e in [q0, q0 + etot)
+        const int o0 = max(max(lo + shift, 0), g.step_c * q0);
+        const int o1 = min(min(hi + shift, last), g.step_c * (q0 + g.etot) - 1);
+        float s = 0.f;
+        for (int o = o0; o <= o1; ++o) {
+            const int rr = o % g.step_c, at = rr * g.etot + o / g.step_c - q0 - tile * g.threads;
+            if (rr < g.residues && at >= 0 && at < g.threads) s += diag[at];
+        }
+        out[cb] = s;
+    }
+}
+
+// dtable of one row bucket: the partials of its row pairs, `groups` runs of them added side by side.
+__global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ GradParams g, float *dtable, int width,
+                                                      int groups) {
+    __shared__ float acc_s[1024];
+    const int rb = blockIdx.x, h = blockIdx.z;
+    const int c = threadIdx.x % width, grp = threadIdx.x / width;
+    const int cb = blockIdx.y * width + c;
+    const int per = g.nchunk * g.ntile;
+    int lo, hi;
+    bucket_range(g.b.rows, rb, lo, hi);
+    float acc = 0.f;
+    if (cb < g.col_buckets) {
+        const size_t row = (size_t)g.col_buckets;
+        for (int rq = 0; rq < g.q_rows; ++rq) {
+            // row offset step_r rk - rq - start_r in [lo, hi]
+            const long long base = (long long)rq + g.start_r;
+            const long long x0 = lo + base, x1 = hi + base;
+            const int k0 = x0 <= 0 ? 0 : (int)min((x0 + g.step_r - 1) / g.step_r, (long long)g.k_rows);
+            const int k1 = x1 < 0 ? -1 : (int)min(x1 / g.step_r, (long long)g.k_rows - 1);
+            if (k1 < k0) continue;
+            const float *p = g.part + (((size_t)h * g.q_rows + rq) * g.k_rows + k0) * per * row + cb;
+            const int items = (k1 - k0 + 1) * per;
+            int it = grp;
+            float a[4] = {0.f, 0.f, 0.f, 0.f};
+            for (; it + 3 * groups < items; it += 4 * groups) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) a[u] += p[(size_t)(it + u * groups) * row];
+            }
+            for (; it < items; it += groups) a[0] += p[(size_t)it * row];
+            acc += (a[0] + a[1]) + (a[2] + a[3]);
+        }
+    }
+    acc_s[threadIdx.x] = acc;
+    __syncthreads();
+    if (grp == 0 && cb < g.col_buckets) {
+        float s = 0.f;
+        for (int u = 0; u < groups; ++u) s += acc_s[u * width + c];
+        dtable[((size_t)rb * g.col_buckets + cb) * g.b.heads + h] = s;
+    }
+}
+
+void grad_plan(const lisa_rel_bias &b, GradParams &g) {
+    g.q_rows = b.q_rows; g.q_cols = b.q_cols;
+    g.k_rows = b.k_rows; g.k_cols = b.k_cols;
+    g.step_r = b.key_step_rows; g.step_c = b.key_step_cols;
+    g.start_r = b.start_rows; g.start_c = b.start_cols;
+    g.row_buckets = b.rows.buckets; g.col_buckets = b.cols.buckets;
+    g.n = (long long)b.q_rows * b.q_cols;
+    g.m = (long long)b.k_rows * b.k_cols;
+    g.residues = std::min(g.step_c, g.q_cols);
+    const int nmax = (g.q_cols - 1) / g.step_c + 1;
+    g.ch = std::min(nmax, g.col_buckets > 512 ? 256 : 64);   // many buckets: longer chunks, fewer partial rows
+    g.nchunk = (nmax + g.ch - 1) / g.ch;
+    g.etot = g.k_cols + g.ch - 1;
+    const long long flat = (long long)g.residues * g.etot;
+    g.threads = (int)std::min<long long>(256, (flat + 31) / 32 * 32);
+    g.ntile = (int)((flat + g.threads - 1) / g.threads);
+}
+
+}  // namespace
+
+cudaError_t launch_bias_dense(const lisa_rel_bias &b, const BiasDev &dev, void *out, int dtype, cudaStream_t s) {
+    const int n = b.q_rows * b.q_cols, m = b.k_rows * b.k_cols;
+    const size_t esz = dtype == LISA_BF16 ? 2 : 4;
+    const size_t vecs = (size_t)n * m * esz / 16 + 1;
+    // enough vectors for a CTA to pay for its offset table, at most about eight CTAs per SM
+    size_t blocks = (vecs + kDenseThreads * 4 - 1) / (kDenseThreads * 4);
+    blocks = std::max<size_t>(1, std::min<size_t>(blocks, (152 * 8 + dev.heads - 1) / dev.heads));
+    const int bytes = dev.entries * (int)sizeof(float);
+    dim3 grid((unsigned)blocks, (unsigned)dev.heads);
+    if (dtype == LISA_BF16) {
+        cudaError_t e = cudaFuncSetAttribute(bias_dense<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             LISA_MAX_OFFSETS * 4);
+        if (e != cudaSuccess) return e;
+        bias_dense<<<grid, kDenseThreads, bytes, s>>>(dev, static_cast<__nv_bfloat16 *>(out), n, m);
+    } else {
+        cudaError_t e = cudaFuncSetAttribute(bias_dense<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             LISA_MAX_OFFSETS * 4);
+        if (e != cudaSuccess) return e;
+        bias_dense<<<grid, kDenseThreads, bytes, s>>>(dev, static_cast<float *>(out), n, m);
+    }
+    return cudaGetLastError();
+}
+
+size_t bias_grad_bytes(const lisa_rel_bias &b, int heads) {
+    GradParams g{};
+    grad_plan(b, g);
+    return (size_t)heads * g.q_rows * g.k_rows * g.nchunk * g.ntile * g.col_buckets * sizeof(float);
+}
+
+cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int dtype, float *dtable,
+                             void *ws, cudaStream_t s) {
+    GradParams g{};
+    g.b = dev;
+    grad_plan(b, g);
+    g.part = static_cast<float *>(ws);
+    dim3 grid((unsigned)(g.nchunk * g.ntile), (unsigned)(g.q_rows * g.k_rows), (unsigned)dev.heads);
+    if (dtype == LISA_BF16)
+        bias_grad_part<<<grid, g.threads, 0, s>>>(g, static_cast<const __nv_bfloat16 *>(dbias));
+    else
+        bias_grad_part<<<grid, g.threads, 0, s>>>(g, static_cast<const float *>(dbias));
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // 1024 threads as `groups` runs of partials by `width` column buckets
+    const int width = std::min(256, (g.col_buckets + 31) / 32 * 32), groups = 1024 / width;
+    bias_grad_sum<<<dim3((unsigned)g.row_buckets, (unsigned)((g.col_buckets + width - 1) / width), (unsigned)dev.heads),
+                    width * groups, 0, s>>>(g, dtable, width, groups);
+    return cudaGetLastError();
+}
+
+}  // namespace attn
+}  // namespace lisa

@@ -345,3 +345,10 @@ def backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dO: torch.Tensor
     if mlp is not None:
         return dq, dk, dvv, dalpha, pg
     return dq, dk, dvv, dalpha
+
+
+# -- the softmax cross attention and the relative position bias ------------------------
+from .attention import (ATTENTION_EXPORTED, RelativeBias, cross_attention, cross_attention_backward,  # noqa: E402,F401
+                        exact_buckets, log_buckets, relative_bias, relative_bias_backward)
+
+EXPORTED = EXPORTED + ATTENTION_EXPORTED

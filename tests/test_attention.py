@@ -1,0 +1,390 @@
+"""The cross attention and the relative position bias on the GPU against their
+64-bit restatement, elementwise within the bounds derived there
+(attention_ref.py); determinism, streams, graphs, masked garbage."""
+import math
+
+import pytest
+import torch
+
+import attention_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def lisa():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from hop_stochastic_vision_gb300 import build, lisa as binding
+    build.build()
+    binding.load()
+    return binding
+
+
+def _rule(lisa, r):
+    return lisa.exact_buckets(r[1]) if r[0] == "exact" else lisa.log_buckets(r[1], r[2])
+
+
+class Case:
+    def __init__(self, lisa, dtype, B, heads, kv, n, m, d, *, bias=None, lens=None, layout="heads", scale=None, seed=0,
+                 spread=1.0, garbage=False):
+        g = torch.Generator().manual_seed(seed)
+        q_grid, k_grid = (n if isinstance(n, tuple) else (1, n)), (m if isinstance(m, tuple) else (1, m))
+        n, m = q_grid[0] * q_grid[1], k_grid[0] * k_grid[1]
+        self.lisa, self.dtype, self.scale = lisa, dtype, 1 / math.sqrt(d) if scale is None else scale
+        q = (spread * torch.randn(B, heads, n, d, generator=g)).to(dtype)
+        k, v = (torch.randn(B, kv, m, d, generator=g).to(dtype) for _ in range(2))
+        self.dout = torch.randn(B, heads, n, d, generator=g).to(dtype)
+        self.lens = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+        self.k_ref, self.v_ref = k.clone(), v.clone()
+        if garbage:
+            for b, L in enumerate(lens):
+                k[b, :, max(L, 0):], v[b, :, max(L, 0):] = math.nan, math.inf
+        self.q_ref = q
+        if layout == "tokens":      # [B, tokens, heads, d], keys beside values
+            self.q = q.cuda().transpose(1, 2).contiguous().transpose(1, 2)
+            pair = torch.stack((k.transpose(1, 2), v.transpose(1, 2)), 2).contiguous().cuda()
+            self.k, self.v = pair[:, :, 0].transpose(1, 2), pair[:, :, 1].transpose(1, 2)
+            self.do = self.dout.cuda().transpose(1, 2).contiguous().transpose(1, 2)
+        else:
+            self.q, self.k, self.v, self.do = q.cuda(), k.cuda(), v.cuda(), self.dout.cuda()
+        self.bias = self.index = self.table = None
+        if bias is not None:
+            rows, cols = bias.get("rows", ("exact", 0)), bias["cols"]
+            step, start = bias.get("step", (1, 1)), bias.get("start", (0, 0))
+            self.table = torch.randn(ref.buckets(rows) * ref.buckets(cols), heads, generator=g)
+            for row in bias.get("minus_inf", ()):
+                self.table[row] = -math.inf
+            self.index = ref.bucket_index(q_grid, k_grid, rows, cols, step, start)
+            self.bias = lisa.RelativeBias(self.table.cuda(), q_grid, k_grid, rows=_rule(lisa, rows),
+                                          cols=_rule(lisa, cols), key_step=step, query_start=start)
+        self.kw = dict(scale=self.scale, kv_lens=None if self.lens is None else self.lens.cuda(), bias=self.bias)
+
+    def want(self, backward=True):
+        return ref.attention(self.q_ref, self.k_ref, self.v_ref, self.dout if backward else None, scale=self.scale,
+                             lens=None if self.lens is None else self.lens.tolist(), table=self.table,
+                             index=self.index, dtype=self.dtype)
+
+    def forward(self, **kw):
+        return self.lisa.cross_attention(self.q, self.k, self.v, return_lse=True, **{**self.kw, **kw})
+
+    def backward(self, out, lse, **kw):
+        return self.lisa.cross_attention_backward(self.q, self.k, self.v, out, lse, self.do, **{**self.kw, **kw})
+
+    def check(self):
+        out, lse = self.forward()
+        grads = self.backward(out, lse)
+        want = self.want()
+        for name, got in zip(("o", "lse", "dq", "dk", "dv", "dtable"), (out, lse) + tuple(grads)):
+            ref.assert_within(got, want[name], name)
+        assert len(grads) == (3 if self.bias is None else 4)
+        return out, lse, grads
+
+
+LOG = {"cols": ("log", 32, 128)}
+SHORT = {"cols": ("log", 8, 5), "start": (0, 3)}
+NEAR = {"cols": ("exact", 3), "start": (0, -2)}
+
+
+def _grid(q, k, step=1, **kw):
+    D = [max(a - 1, step * (b - 1)) for a, b in zip(q, k)]
+    return {"rows": ("exact", D[0]), "cols": ("exact", D[1]), "step": (step, step), **kw}
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [16, 32, 64])
+@pytest.mark.parametrize("n,m", [(1, 1), (1, 7), (5, 1), (17, 200), (64, 64), (65, 63), (129, 130), (257, 49)])
+def test_lengths_and_widths(lisa, dtype, d, n, m):
+    Case(lisa, dtype, 2, 2, 1, n, m, d, seed=n + m).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("heads,kv", [(4, 4), (4, 2), (6, 1), (3, 3)])
+@pytest.mark.parametrize("layout", ["heads", "tokens"])
+def test_head_layouts(lisa, dtype, heads, kv, layout):
+    Case(lisa, dtype, 3, heads, kv, 70, 150, 64, layout=layout, seed=heads).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bias", [None, LOG, SHORT])
+@pytest.mark.parametrize("garbage", [False, True])
+def test_padded_batches(lisa, dtype, bias, garbage):
+    """Lengths of 0 and 1, ends inside and at a tile; what stands behind them (NaN, inf) plays no part."""
+    Case(lisa, dtype, 6, 2, 1, 90, 300, 64, bias=bias, lens=[0, 1, 128, 129, 299, 300], garbage=garbage).check()
+
+
+def test_lengths_outside_the_range_count_as_its_ends(lisa):
+    c = Case(lisa, BF16, 3, 2, 2, 20, 40, 64, lens=[-5, 40, 1000])
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bias", [LOG, SHORT, NEAR, {"cols": ("exact", 300)}, {"cols": ("log", 128, 1000)},
+                                  {"cols": ("log", 4, 2), "step": (1, 3)}, {"cols": ("exact", 40), "start": (0, 90)}])
+def test_sequence_biases(lisa, dtype, bias):
+    Case(lisa, dtype, 2, 4, 2, 140, 200, 64, bias=bias, seed=3).check()
+
+
+@pytest.mark.parametrize("dtype,d", [(F32, 16), (F32, 64), (BF16, 64), (BF16, 32)])
+@pytest.mark.parametrize("q,k,step", [((14, 14), (14, 14), 1), ((7, 9), (3, 5), 2), ((12, 20), (2, 3), 8),
+                                      ((1, 5), (4, 1), 1), ((5, 1), (1, 6), 3), ((17, 23), (17, 23), 1)])
+def test_grid_biases(lisa, dtype, d, q, k, step):
+    Case(lisa, dtype, 3, 2, 2, q, k, d, bias=_grid(q, k, step), seed=step).check()
+
+
+def test_grid_bias_with_near_and_far_offsets_in_one_bucket(lisa):
+    q, k = (9, 11), (6, 7)
+    for rows, cols in ((("exact", 2), ("log", 8, 5)), (("log", 16, 9), ("exact", 0))):
+        Case(lisa, BF16, 2, 3, 1, q, k, 64, bias={"rows": rows, "cols": cols, "step": (2, 1), "start": (1, -2)}).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_buckets_of_minus_infinity_mask(lisa, dtype):
+    """-inf table entries mask pairs, here whole rows too: o = 0, lse = -inf, no gradient, no NaN."""
+    bias = {"cols": ("exact", 2), "minus_inf": (0, 4)}      # offsets of 2 and more are masked
+    c = Case(lisa, dtype, 2, 2, 2, 150, 140, 64, bias=bias)
+    out, lse, grads = c.check()
+    assert torch.isinf(lse[:, :, 142:]).all() and not out[:, :, 142:].any() and not grads[0][:, :, 142:].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_large_scores(lisa, dtype):
+    """Scores of some hundreds: the maximum moves between tiles and the sum is rescaled."""
+    Case(lisa, dtype, 1, 2, 2, 100, 500, 64, spread=12.0, scale=1.0).check()
+
+
+def test_repeated_inputs(lisa):
+    """One set of states for the whole batch (stride 0), and one key head for all: dk, dv of the repeated tensor."""
+    c = Case(lisa, BF16, 3, 2, 2, 60, 80, 64)
+    c.k, c.v = c.k[:1].expand(3, -1, -1, -1), c.v[:1].expand(3, -1, -1, -1)
+    c.k_ref, c.v_ref = c.k.cpu(), c.v.cpu()
+    c.check()
+    c = Case(lisa, F32, 2, 4, 4, 33, 41, 32)
+    c.k, c.v = c.k[:, :1].expand(-1, 4, -1, -1), c.v[:, :1].expand(-1, 4, -1, -1)
+    c.k_ref, c.v_ref = c.k.cpu(), c.v.cpu()
+    c.check()
+
+
+def test_no_keys_at_all(lisa):
+    q = torch.randn(2, 3, 5, 64, device="cuda", dtype=BF16)
+    k = torch.empty(2, 3, 0, 64, device="cuda", dtype=BF16)
+    out, lse = lisa.cross_attention(q, k, k, return_lse=True)
+    assert not out.any() and torch.isinf(lse).all() and (lse < 0).all()
+    dq, dk, dv = lisa.cross_attention_backward(q, k, k, out, lse, q)
+    assert not dq.any() and dk.shape == k.shape and dv.shape == k.shape
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,heads,kv,m", [(1, 1, 1, 1), (1, 3, 3, 196), (5, 8, 2, 1000), (3, 16, 1, 130),
+                                          (40, 4, 4, 63), (1, 12, 4, 4097), (2, 24, 1, 600)])
+def test_single_tokens(lisa, dtype, B, heads, kv, m):
+    lens = None if B == 1 else [(m * b) // (B - 1) for b in range(B)]
+    for d in (16, 64):
+        c = Case(lisa, dtype, B, heads, kv, 1, m, d, lens=lens, layout="tokens" if d == 64 else "heads",
+                 garbage=lens is not None)
+        want = c.want(backward=False)
+        out, lse = c.forward()
+        ref.assert_within(out, want["o"], "o")
+        ref.assert_within(lse, want["lse"], "lse")
+
+
+@pytest.mark.parametrize("n", [2, 3, 8, 16, 40])
+def test_few_tokens_over_many_keys(lisa, n):
+    c = Case(lisa, BF16, 2, 4, 2, n, 2500, 64, lens=[2500, 777], bias={"cols": ("log", 32, 128), "start": (0, 2000)})
+    want = c.want(backward=False)
+    out, lse = c.forward()
+    ref.assert_within(out, want["o"], "o")
+    ref.assert_within(lse, want["lse"], "lse")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_tokens_at_their_own_positions(lisa, dtype):
+    B, heads, m = 4, 6, 900
+    c = Case(lisa, dtype, B, heads, 2, 1, m, 64, lens=[900, 3, 500, 0])
+    starts = [0, 899, -7, 5]
+    rule = ("log", 32, 128)
+    table = torch.randn(32, heads)
+    c.table, c.index = table, [ref.bucket_index((1, 1), (1, m), ("exact", 0), rule, (1, 1), (0, s)) for s in starts]
+    c.bias = lisa.RelativeBias(table.cuda(), (1, 1), (1, m), cols=_rule(lisa, rule),
+                               query_start=torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    out, lse = c.forward(bias=c.bias)
+    want = c.want(backward=False)
+    ref.assert_within(out, want["o"], "o")
+    ref.assert_within(lse, want["lse"], "lse")
+    with pytest.raises(ValueError):
+        c.backward(out, lse, bias=c.bias)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_same_bits_every_time_whatever_the_workspace_holds(lisa, dtype):
+    from hop_stochastic_vision_gb300 import attention as att
+    c = Case(lisa, dtype, 3, 4, 2, (10, 13), (10, 13), 64, bias=_grid((10, 13), (10, 13)), lens=[130, 55, 0])
+    dt = lisa.LISA_F32 if dtype == F32 else lisa.LISA_BF16
+    out, lse = c.forward()
+    first = c.backward(out, lse)
+    for fill in (0x00, 0xFF):
+        nf = att.lisa_cross_attention_workspace_bytes(3, 4, 2, 130, 130, 64, dt)
+        nb = att.lisa_cross_attention_backward_workspace_bytes(3, 4, 2, 130, 130, 64, c.bias.struct, dt)
+        ws = torch.full((max(nf, nb, 16),), fill, dtype=torch.uint8, device="cuda")
+        out2, lse2 = c.forward(workspace=ws)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+        ws.fill_(fill)
+        for a, b in zip(first, c.backward(out, lse, workspace=ws)):
+            assert torch.equal(a, b)
+
+
+def test_a_given_output_is_written_in_its_own_layout_and_nothing_else(lisa):
+    c = Case(lisa, BF16, 2, 3, 3, 37, 90, 64)
+    wide = torch.full((2, 40, 4, 64), 7.0, dtype=BF16, device="cuda")       # rows and a head to spare
+    view = wide[:, :37, :3].transpose(1, 2)
+    res = lisa.cross_attention(c.q, c.k, c.v, out=view, **c.kw)
+    assert res is view
+    assert torch.equal(view, c.forward()[0])
+    assert (wide[:, 37:] == 7).all() and (wide[:, :, 3] == 7).all()
+
+
+def test_other_streams_and_captured_graphs(lisa):
+    c = Case(lisa, BF16, 2, 4, 2, 100, 260, 64, bias=LOG, lens=[260, 100])
+    out, lse = c.forward()
+    grads = c.backward(out, lse)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o2, l2 = c.forward()
+        g2 = c.backward(o2, l2)
+    o3, l3 = c.forward(stream=side.cuda_stream)
+    g3 = c.backward(o3, l3, stream=side.cuda_stream)
+    side.synchronize()
+    for a, b, x in zip((out, lse) + grads, (o2, l2) + g2, (o3, l3) + g3):
+        assert torch.equal(a, b) and torch.equal(a, x)
+    # captured, replayed on two inputs
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        og, lg = c.forward()
+        gg = c.backward(og, lg)
+    for seed in (0, 9):
+        other = Case(lisa, BF16, 2, 4, 2, 100, 260, 64, bias=LOG, lens=[260, 100], seed=seed)
+        for name in ("q", "k", "v", "do"):
+            getattr(c, name).copy_(getattr(other, name))
+        c.bias.table.copy_(other.bias.table)
+        graph.replay()
+        torch.cuda.synchronize()
+        oe, le = other.forward()
+        for a, b in zip((og, lg) + gg, (oe, le) + other.backward(oe, le)):
+            assert torch.equal(a, b)
+
+
+def test_gradient_against_differences(lisa):
+    """fp32 directional derivatives by central differences.  With L = sum(o dO)
+    and a unit step of h along x the difference quotient is off by h^2 / 6 times
+    the third derivative (of the order of L's scale: 3e-6 at h = 2^-8) and by
+    the rounding of the two sums, at most 2^-23 sum|o dO| (m + d) / h."""
+    c = Case(lisa, F32, 2, 2, 1, 24, 30, 16, bias={"cols": ("exact", 4)})
+    out, lse = c.forward()
+    grads = c.backward(out, lse)
+    h = 2.0 ** -8
+    for x, dx in zip((c.q, c.k, c.v, c.bias.table), grads):
+        dirn = torch.randn(x.shape, generator=torch.Generator().manual_seed(1)).cuda()
+        dirn /= dirn.norm()
+        keep, vals = x.clone(), []
+        for sign in (1, -1):
+            x.copy_(keep + sign * h * dirn)
+            vals.append((c.forward()[0].double() * c.do.double()).sum())
+        x.copy_(keep)
+        got, want = float((dx.double() * dirn.double()).sum()), float((vals[0] - vals[1]) / (2 * h))
+        scale = float((out.abs().double() * c.do.abs().double()).sum())
+        assert abs(got - want) <= h * h * scale + 2.0 ** -23 * scale * (30 + 16) / h
+
+
+# ------------------------------------------------------------------ the bias matrix
+
+MATRICES = [((1, 1), (1, 1), LOG), ((1, 50), (1, 77), LOG), ((1, 300), (1, 5), SHORT), ((1, 40), (1, 600), NEAR),
+            ((1, 33), (1, 20), {"cols": ("log", 16, 60), "step": (1, 5)}), ((14, 14), (14, 14), None),
+            ((24, 24), (24, 24), None), ((13, 7), (3, 2), 4), ((7, 30), (7, 30), None),
+            ((6, 5), (9, 4), {"rows": ("log", 8, 4), "cols": ("exact", 1), "step": (2, 3), "start": (-1, 2)}),
+            ((1, 900), (1, 1100), {"cols": ("exact", 700)})]
+
+
+def _matrix(lisa, q, k, how, heads=3):
+    bias = _grid(q, k, how if isinstance(how, int) else 1) if how is None or isinstance(how, int) else how
+    rows, cols = bias.get("rows", ("exact", 0)), bias["cols"]
+    step, start = bias.get("step", (1, 1)), bias.get("start", (0, 0))
+    table = torch.randn(ref.buckets(rows) * ref.buckets(cols), heads, generator=torch.Generator().manual_seed(2))
+    b = lisa.RelativeBias(table.cuda(), q, k, rows=_rule(lisa, rows), cols=_rule(lisa, cols), key_step=step,
+                          query_start=start)
+    return b, table, ref.bucket_index(q, k, rows, cols, step, start)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("q,k,how", MATRICES)
+def test_bias_matrix(lisa, dtype, q, k, how):
+    b, table, index = _matrix(lisa, q, k, how)
+    got = lisa.relative_bias(b, dtype)
+    assert torch.equal(got.cpu(), table.t()[:, index].to(dtype))      # table values, rounded once
+    wide = torch.full((got.numel() + 64,), 3.0, dtype=dtype, device="cuda")
+    out = wide[16:16 + got.numel()].view(got.shape)
+    assert torch.equal(lisa.relative_bias(b, dtype, out=out), got)
+    assert (wide[:16] == 3).all() and (wide[16 + got.numel():] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("q,k,how", MATRICES)
+def test_bias_matrix_gradient(lisa, dtype, q, k, how):
+    """fp32 sums of N terms in any order are within N 2^-24 sum|x|; a bucket without pairs gives 0."""
+    b, table, index = _matrix(lisa, q, k, how)
+    heads, n, m = 3, b.n, b.m
+    x = torch.randn(heads, n, m, generator=torch.Generator().manual_seed(4)).to(dtype)
+    got = lisa.relative_bias_backward(b, x.cuda()).cpu().double()
+    want, mag, count = (torch.zeros(table.shape, dtype=torch.float64) for _ in range(3))
+    for h in range(heads):
+        want[:, h].index_add_(0, index.reshape(-1), x[h].reshape(-1).double())
+        mag[:, h].index_add_(0, index.reshape(-1), x[h].reshape(-1).double().abs())
+        count[:, h].index_add_(0, index.reshape(-1), torch.ones(n * m, dtype=torch.float64))
+    assert ((got - want).abs() <= count * 2.0 ** -24 * mag).all()
+    again = lisa.relative_bias_backward(b, x.cuda(), workspace=torch.full((1 << 24,), 0xFF, dtype=torch.uint8,
+                                                                          device="cuda"))
+    assert torch.equal(again.cpu().double(), got)
+
+
+def test_bias_of_infinities(lisa):
+    b, table, index = _matrix(lisa, (1, 20), (1, 20), LOG)
+    b.table[3] = -math.inf
+    table[3] = -math.inf
+    assert torch.equal(lisa.relative_bias(b).cpu(), table.t()[:, index])
+
+
+# ------------------------------------------------------------------ as a layer uses them
+
+def test_a_pooled_stage_beside_the_linear_layer(lisa):
+    """One stage as a backbone runs it: the LiSA layer on a 16 x 16 grid, its
+    output as the queries of a pooled attention with a learned bias, trained by
+    both backward passes; the fused bias agrees with the matrix added by hand."""
+    g = torch.Generator().manual_seed(11)
+    B, heads, H, W, d = 2, 2, 16, 16, 64
+    xq, xk, v, do = (torch.randn(B, heads, H * W, d, generator=g).to(BF16).cuda() for _ in range(4))
+    alpha = torch.full((heads,), 0.5).cuda()
+    layer = lisa.forward(xq, xk, v, (H, W), 3, alpha=alpha, beta=0.5)
+    pooled = layer.float().reshape(B, heads, 4, 4, 4, 4, d).mean((3, 5)).reshape(B, heads, 16, d).to(BF16)
+    rule = _grid((H, W), (4, 4), 4)
+    table = torch.randn(ref.buckets(rule["rows"]) * ref.buckets(rule["cols"]), heads, generator=g).cuda()
+    bias = lisa.RelativeBias(table, (H, W), (4, 4), rows=_rule(lisa, rule["rows"]), cols=_rule(lisa, rule["cols"]),
+                             key_step=(4, 4))
+    out, lse = lisa.cross_attention(layer, pooled, pooled, bias=bias, return_lse=True)
+    dq, dk, dv, dtable = lisa.cross_attention_backward(layer, pooled, pooled, out, lse, do, bias=bias)
+    index = ref.bucket_index((H, W), (4, 4), rule["rows"], rule["cols"], (4, 4))
+    want = ref.attention(layer, pooled, pooled, do, scale=1 / 8, table=table, index=index)
+    for name, got in (("o", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv), ("dtable", dtable)):
+        ref.assert_within(got, want[name], name)
+    # dS of the whole batch through the matrix's own gradient
+    matrix = lisa.relative_bias(bias).double()
+    p = torch.softmax(layer.double() @ pooled.double().transpose(-1, -2) / 8 + matrix, -1)
+    dp = do.double() @ pooled.double().transpose(-1, -2)
+    ds = (p * (dp - (p * dp).sum(-1, keepdim=True))).sum(0).float()
+    by_matrix = lisa.relative_bias_backward(bias, ds)
+    ref.assert_within(by_matrix, (want["dtable"][0], want["dtable"][1] + 2.0 ** -24 * 256 * 16 * ds.abs().max().cpu()),
+                      "dtable by the matrix")
+    grads = lisa.backward(xq, xk, v, dq, (H, W), 3, alpha=alpha, beta=0.5)
+    assert all(torch.isfinite(x).all() for x in grads)
