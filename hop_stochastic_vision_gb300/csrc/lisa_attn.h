@@ -70,16 +70,6 @@ struct Problem {
     float *dk_part, *dv_part;  // [q_splits][B][kv_heads][m][d]
 };
 
-// Dense bias gradient.
-struct BiasGradPlan {
-    int mode_rows;      // row pairs per head (q_rows * k_rows)
-    int chunk;          // query columns of one residue per item
-    int chunks;         // chunks of a row
-    int etiles;         // tiles of diagonals
-    int items;          // items per head
-    size_t part_bytes;
-};
-
 // --- plans -------------------------------------------------------------------
 // Fills `dev` from the public struct; checks everything but the batch.
 lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev);
@@ -94,6 +84,12 @@ cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dq(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dkdv(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dbias(const Problem &p, cudaStream_t s);
+
+// bf16 on the tensor cores; `err` is the error word of the call's workspace
+int tc_forward_splits(int B, int heads, int n, int m);
+cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s);
+// joins p.splits partial outputs (o_part, lse_part) into O and lse
+cudaError_t launch_join(const Problem &p, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace lisa

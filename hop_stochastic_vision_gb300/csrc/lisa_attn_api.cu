@@ -178,6 +178,31 @@ lisa_status fill(Problem &p, const void *Q, const lisa_strides *qs, const void *
     return LISA_OK;
 }
 
+// The forward's path and workspace: the tensor cores for bf16, the CUDA cores otherwise.
+struct FwdPlan {
+    bool tc;
+    int splits;
+    size_t off_lse, off_o, total;   // the error word is at 0
+};
+
+FwdPlan forward_plan(int B, int heads, int n, int m, int d, int dtype) {
+    FwdPlan pl{};
+    pl.splits = 1;
+    pl.tc = dtype == LISA_BF16 && m > 0;
+    if (!pl.tc) return pl;
+    pl.splits = tc_forward_splits(B, heads, n, m);
+    size_t off = kAlign;
+    if (pl.splits > 1) {
+        const size_t rows = (size_t)pl.splits * B * heads * n;
+        pl.off_lse = off;
+        off = align_up(off + rows * sizeof(float));
+        pl.off_o = off;
+        off = align_up(off + rows * d * sizeof(float));
+    }
+    pl.total = off;
+    return pl;
+}
+
 struct BwdPlan {
     size_t off_delta, off_dbias, off_grad, total;
 };
@@ -255,8 +280,8 @@ extern "C" lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, in
 
 extern "C" size_t lisa_cross_attention_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,
                                                        int dtype) {
-    (void)B; (void)heads; (void)kv_heads; (void)n; (void)m; (void)d; (void)dtype;
-    return 0;
+    if (check_sizes(B, heads, kv_heads, n, m, d, dtype) != LISA_OK || B == 0 || heads == 0 || n == 0) return 0;
+    return forward_plan(B, heads, n, m, d, dtype).total;
 }
 
 extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q_strides, const void *K,
@@ -265,7 +290,6 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
                                             float *lse, int B, int heads, int kv_heads, int n, int m, int d,
                                             float scale, const int *kv_lens, const lisa_rel_bias *bias, int dtype,
                                             void *workspace, size_t workspace_bytes, void *stream) {
-    (void)workspace; (void)workspace_bytes;
     Problem p{};
     lisa_status st = fill(p, Q, q_strides, K, k_strides, V, v_strides, B, heads, kv_heads, n, m, d, scale, kv_lens,
                           bias, dtype);
@@ -281,7 +305,18 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
         return LISA_ERR_INVALID_ARG;
     p.O = {O, o_strides->batch, o_strides->head, o_strides->token};
     p.lse = lse;
-    return status_of(launch_simt_forward(p, static_cast<cudaStream_t>(stream)));
+    const FwdPlan pl = forward_plan(B, heads, n, m, d, dtype);
+    if (pl.total > 0) {
+        if (!workspace || workspace_bytes < pl.total) return LISA_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
+    }
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (!pl.tc) return status_of(launch_simt_forward(p, cs));
+    char *ws = static_cast<char *>(workspace);
+    p.splits = pl.splits;
+    p.lse_part = reinterpret_cast<float *>(ws + pl.off_lse);
+    p.o_part = reinterpret_cast<float *>(ws + pl.off_o);
+    return status_of(launch_tc_forward(p, reinterpret_cast<int *>(ws), cs));
 }
 
 extern "C" size_t lisa_cross_attention_backward_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,

@@ -1,0 +1,476 @@
+// lisa_attn_tc.cu -- the forward cross attention on the tensor cores (bf16).
+//
+// A persistent CTA takes work items of 256 queries (two tiles of 128 rows) of
+// one (batch, head) and walks the keys in tiles of 128:
+//   warp 9        TMA: the queries, then a ring of K and V tiles
+//   warp 8        one thread issues every product: S_t = Q_t K^T into tensor
+//                 memory, then O_t += P_t V with P_t read from tensor memory
+//   warps 0-3     softmax of tile 0, one thread per row: scores to registers,
+//   warps 4-7     weights to tensor memory as bf16; the same for tile 1
+// While one tile's scores are in the softmax the other's products run.
+// S, P and O of both tiles fill the 512 columns of tensor memory, so S of the
+// next keys can be issued as soon as the scores are in registers.
+//
+// The running maximum is kept only to within 2^8: O and the sum are rescaled
+// when a tile's maximum passes the reference by more, which after the first
+// tile is rare, so the accumulator stays in tensor memory.  exp is 2^x with
+// log2(e) folded into the scale and into the bias table.
+#include "lisa_attn_tc.cuh"
+
+namespace lisa {
+namespace attn {
+namespace {
+
+// 384 threads x 168 registers at launch = 2 x 128 x 208 + 128 x 88 after the split
+constexpr int kFwdThreads = 384;
+constexpr int kRegsSoftmax = 208, kRegsControl = 88;
+constexpr int kMaxStages = 5;
+constexpr float kSlack = 8.f;
+
+struct FwdParams {
+    Problem p;
+    MapUse uq, uk, uv;
+    int *err;
+    int qtiles;      // pairs of 128 queries per (batch, head)
+    int splits;
+    int items;
+    int stages;
+    int off_lut, off_keys;   // dynamic shared memory, behind Q and the ring
+};
+
+struct FwdBars {
+    uint64_t q_full[2], q_empty[2], k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages], v_empty[kMaxStages];
+    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+};
+
+struct Item {
+    int h, b, q0, split, len, t0, t1, nt;
+};
+__device__ __forceinline__ Item item_of(const FwdParams &x, int it) {
+    Item w;
+    w.split = it % x.splits;
+    int r = it / x.splits;
+    w.q0 = (r % x.qtiles) * 2 * kRows;
+    r /= x.qtiles;
+    w.b = r % x.p.B;
+    w.h = r / x.p.B;
+    w.len = keys_of(x.p, w.b);
+    const int tiles = (w.len + kRows - 1) / kRows, per = (tiles + x.splits - 1) / x.splits;
+    w.t0 = min(w.split * per, tiles);
+    w.t1 = min(w.t0 + per, tiles);
+    w.nt = x.p.n - w.q0 > kRows ? 2 : 1;
+    return w;
+}
+// Valid keys of tile `t`, and the columns its products cover.
+__device__ __forceinline__ int tile_keys(int len, int t) { return min(kRows, len - t * kRows); }
+__device__ __forceinline__ int tile_cols(int keys) { return (keys + 15) & ~15; }
+
+template <int kBias>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    tc_forward(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, const __grid_constant__ FwdParams x) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) FwdBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    const Problem &p = x.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_u32(sm);
+    const uint32_t q_smem = base, ring = base + 2 * kTileBytes;
+    float *lut = reinterpret_cast<float *>(sm + x.off_lut);
+    uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_keys);
+    const Guard guard{x.err, &dead};
+
+    if (tid == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&bar.q_full[t]), 1);
+            mbar_init(smem_u32(&bar.q_empty[t]), 1);
+            mbar_init(smem_u32(&bar.s_full[t]), 1);
+            mbar_init(smem_u32(&bar.s_free[t]), 4);
+            mbar_init(smem_u32(&bar.p_full[t]), 4);
+            mbar_init(smem_u32(&bar.pv_done[t]), 1);
+        }
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(smem_u32(&bar.k_full[s]), 1);
+            mbar_init(smem_u32(&bar.v_full[s]), 1);
+            mbar_init(smem_u32(&bar.k_empty[s]), 1);
+            mbar_init(smem_u32(&bar.v_empty[s]), 1);
+        }
+        dead = 0;
+        fence_mbar_init();
+        if (blockIdx.x == 0) *x.err = 0;
+    }
+    if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (kBias == 2)
+        for (int j = tid; j < p.m; j += kFwdThreads) key_off[j] = (uint16_t)off_key(p.bias, j);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp >= 8) set_regs_down<kRegsControl>();
+    if (warp >= 10) {
+        // idle: completes the control warps' group of four
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            int kt = 0, nq[2] = {0, 0};
+            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+                const Item w = item_of(x, it);
+                if (w.t0 >= w.t1) continue;
+                auto load_q = [&](int t) {
+                    const uint32_t f = smem_u32(&bar.q_full[t]);
+                    if (nq[t] > 0) wait_on(smem_u32(&bar.q_empty[t]), (nq[t] - 1) & 1, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(f, kTileBytes);
+                    load_rows(q_smem + t * kTileBytes, &mq, x.uq, w.q0 + t * kRows, w.h, w.b, f);
+                    ++nq[t];
+                };
+                load_q(0);
+                for (int j = w.t0; j < w.t1; ++j, ++kt) {
+                    const int s = kt % x.stages;
+                    const uint32_t ph = (uint32_t)(kt / x.stages) & 1u;
+                    const uint32_t kf = smem_u32(&bar.k_full[s]), vf = smem_u32(&bar.v_full[s]);
+                    if (kt >= x.stages) wait_on(smem_u32(&bar.k_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(kf, kTileBytes);
+                    load_rows(ring + 2 * s * kTileBytes, &mk, x.uk, j * kRows, w.h / p.group, w.b, kf);
+                    if (j == w.t0 && w.nt == 2) load_q(1);
+                    if (kt >= x.stages) wait_on(smem_u32(&bar.v_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(vf, kTileBytes);
+                    load_rows(ring + (2 * s + 1) * kTileBytes, &mv, x.uv, j * kRows, w.h / p.group, w.b, vf);
+                }
+            }
+            // nothing may still arrive on this CTA's barriers once it has gone
+            for (int s = 0; s < x.stages; ++s) {
+                const int uses = kt > s ? (kt - 1 - s) / x.stages + 1 : 0;
+                if (uses == 0) continue;
+                if (!mbar_wait(smem_u32(&bar.k_empty[s]), (uses - 1) & 1) ||
+                    !mbar_wait(smem_u32(&bar.v_empty[s]), (uses - 1) & 1))
+                    atomicOr(x.err, kErrTimeoutMma);
+            }
+            for (int t = 0; t < 2; ++t)
+                if (nq[t] > 0 && !mbar_wait(smem_u32(&bar.q_empty[t]), (nq[t] - 1) & 1))
+                    atomicOr(x.err, kErrTimeoutMma);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // --------------------------------------------------------- products
+        if (lane == 0) {
+            int kt = 0, nq[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0};
+            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+                const Item w = item_of(x, it);
+                if (w.t0 >= w.t1) continue;
+                const int base_kt = kt;
+                auto scores = [&](int t, int j) {
+                    const int k = base_kt + j - w.t0, s = k % x.stages;
+                    if (j == w.t0) wait_on(smem_u32(&bar.q_full[t]), nq[t]++ & 1, guard, kErrTimeoutLoad);
+                    wait_on(smem_u32(&bar.k_full[s]), (k / x.stages) & 1, guard, kErrTimeoutLoad);
+                    if (ns[t] > 0) wait_on(smem_u32(&bar.s_free[t]), (ns[t] - 1) & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_rows_rows(tmem + t * 128, q_smem + t * kTileBytes, ring + 2 * s * kTileBytes,
+                                  tile_cols(tile_keys(w.len, j)));
+                    tc_commit(smem_u32(&bar.s_full[t]));
+                    ++ns[t];
+                    if (j == w.t1 - 1) tc_commit(smem_u32(&bar.q_empty[t]));
+                    if (t == w.nt - 1) tc_commit(smem_u32(&bar.k_empty[s]));
+                };
+                auto values = [&](int t, int j) {
+                    const int k = base_kt + j - w.t0, s = k % x.stages;
+                    wait_on(smem_u32(&bar.v_full[s]), (k / x.stages) & 1, guard, kErrTimeoutLoad);
+                    wait_on(smem_u32(&bar.p_full[t]), np[t] & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_weights_rows(tmem + 384 + t * 64, tmem + 256 + t * 64, ring + (2 * s + 1) * kTileBytes,
+                                     tile_cols(tile_keys(w.len, j)), j > w.t0);
+                    tc_commit(smem_u32(&bar.pv_done[t]));
+                    ++np[t];
+                    if (t == w.nt - 1) tc_commit(smem_u32(&bar.v_empty[s]));
+                };
+                for (int t = 0; t < w.nt; ++t) scores(t, w.t0);
+                for (int j = w.t0; j < w.t1; ++j)
+                    for (int t = 0; t < w.nt; ++t) {
+                        if (j + 1 < w.t1) scores(t, j + 1);
+                        values(t, j);
+                    }
+                kt += w.t1 - w.t0;
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- softmax
+        set_regs_up<kRegsSoftmax>();
+        const int t = warp >> 2, wt = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes per warp
+        const uint32_t s_tm = tmem + t * 128 + lanes, p_tm = tmem + 256 + t * 64 + lanes, o_tm = tmem + 384 + t * 64 + lanes;
+        const float scale2 = p.scale * kLog2e;
+        int kt = 0, ns = 0, np = 0, lut_head = -1;
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(x, it);
+            if (kBias && w.h != lut_head) {
+                // every softmax warp is past its reads of the old head's table
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                fill_offsets(p.bias, w.h, kLog2e, lut, tid, 256);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                lut_head = w.h;
+            }
+            if (t >= w.nt) {   // this tile has no rows
+                kt += w.t1 - w.t0;
+                continue;
+            }
+            const int i = w.q0 + t * kRows + wt;
+            int oq = 0, oq_lo = 0, oq_hi = 0;
+            if (kBias) {
+                const int start = bias_start(p.bias, w.b);
+                oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start);
+                oq_lo = off_query(p.bias, i - lane, start);        // sequence: the warp's first and last row
+                oq_hi = oq_lo + 31;
+            }
+            float ref = -INFINITY, sum = 0.f;
+            for (int j = w.t0; j < w.t1; ++j, ++kt) {
+                const int keys = tile_keys(w.len, j), cols = tile_cols(keys), j0 = j * kRows;
+                float s[128];
+                wait_on(smem_u32(&bar.s_full[t]), ns & 1, guard, kErrTimeoutMma);
+                ++ns;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 128; c += 32)
+                    if (c < cols) tmem_ld32_nowait(s_tm + c, s + c);
+                tc_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar.s_free[t]));
+
+                float mul = scale2, add = 0.f;   // 2^(mul s + add - ref) is the weight
+                if (kBias == 1) {
+                    const int lo = p.bias.step_c * j0 - oq_hi, hi = p.bias.step_c * (j0 + keys - 1) - oq_lo;
+                    const int last = p.bias.entries - 1;
+                    if (hi <= 0 || lo >= last) {          // the whole tile in one outermost bucket
+                        add = lut[hi <= 0 ? 0 : last];
+                    } else {
+                        const int off = p.bias.step_c * j0 - oq;
+                        mul = 1.f;
+                        if (p.bias.step_c == 1 && lo >= 0 && lo + 31 + 127 + 31 <= last) {
+                            const float *l = lut + off;
+#pragma unroll
+                            for (int c = 0; c < 128; ++c)
+                                if ((c & ~31) < cols) s[c] = fmaf(s[c], scale2, l[c]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 128; ++c)
+                                if ((c & ~31) < cols)
+                                    s[c] = fmaf(s[c], scale2, lut[min(max(off + p.bias.step_c * c, 0), last)]);
+                        }
+                    }
+                } else if (kBias == 2) {
+                    mul = 1.f;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 4)
+                        if ((c & ~31) < cols) {
+                            const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
+                            s[c] = fmaf(s[c], scale2, lut[min(max((int)(a.x & 0xFFFFu) - oq, 0), p.bias.entries - 1)]);
+                            s[c + 1] = fmaf(s[c + 1], scale2, lut[min(max((int)(a.x >> 16) - oq, 0), p.bias.entries - 1)]);
+                            s[c + 2] = fmaf(s[c + 2], scale2, lut[min(max((int)(a.y & 0xFFFFu) - oq, 0), p.bias.entries - 1)]);
+                            s[c + 3] = fmaf(s[c + 3], scale2, lut[min(max((int)(a.y >> 16) - oq, 0), p.bias.entries - 1)]);
+                        }
+                }
+                if (keys < kRows) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c >= keys) s[c] = -INFINITY;
+                }
+                float top;
+                {
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if ((c & ~31) < cols) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
+                    top = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul, add);
+                }
+                const bool first = j == w.t0;
+                if (first) {
+                    ref = top;
+                } else if (__any_sync(0xFFFFFFFFu, top > ref + kSlack)) {
+                    const float now = fmaxf(ref, top);
+                    const float f = ref == -INFINITY ? 0.f : ex2_approx(ref - now);
+                    ref = now;
+                    sum *= f;
+                    wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    float o[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        tmem_ld32_nowait(o_tm + c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= f;
+                        tmem_st32(o_tm + c, o);
+                    }
+                    tc_wait_st();
+                }
+                const float shift = add - (ref == -INFINITY ? 0.f : ref);   // a row of -inf so far: weights 0, not NaN
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                // the previous weights have been read (and their products are in O)
+                if (!first) wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
+#pragma unroll
+                for (int c = 0; c < 128; c += 32)
+                    if (c < cols) {
+                        uint32_t w16[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float a = ex2_approx(fmaf(s[c + e], mul, shift));
+                            const float b = ex2_approx(fmaf(s[c + e + 1], mul, shift));
+                            part[e & 2] += a;
+                            part[(e & 2) + 1] += b;
+                            w16[e >> 1] = pack_bf16(a, b);
+                        }
+                        tmem_st16(p_tm + c / 2, w16);
+                    }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                if (t == 0 && keys < cols && w.len < p.m) {
+                    // values behind the last key: whatever stands there times a weight of 0 has to be 0
+                    const int st = kt % x.stages;
+                    wait_on(smem_u32(&bar.v_full[st]), (kt / x.stages) & 1, guard, kErrTimeoutLoad);
+                    zero_rows(ring + (2 * st + 1) * kTileBytes, keys, cols, wt);
+                    fence_proxy_async();
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar.p_full[t]));
+                ++np;
+            }
+            // ------------------------------------------------------ output
+            float o[64];
+            if (w.t0 < w.t1) {
+                wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                tmem_ld32_nowait(o_tm, o);
+                tmem_ld32_nowait(o_tm + 32, o + 32);
+                tc_wait_ld();
+                tc_fence_before();
+            } else {
+#pragma unroll
+                for (int c = 0; c < 64; ++c) o[c] = 0.f;
+            }
+            if (i < p.n) {
+                const float inv = sum != 0.f ? 1.f / sum : 0.f;
+                const float lse = ref == -INFINITY ? -INFINITY : kLn2 * (ref + log2f(sum));
+                const size_t row = ((size_t)w.b * p.heads + w.h) * p.n + i;
+                if (x.splits == 1) {
+                    store_row_bf16(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + (long long)w.b * p.O.sb +
+                                       (long long)w.h * p.O.sh + (long long)i * p.O.st,
+                                   o, inv, p.d);
+                    if (p.lse) p.lse[row] = lse;
+                } else {
+                    const size_t at = (size_t)w.split * ((size_t)p.B * p.heads * p.n) + row;
+                    p.lse_part[at] = lse;
+                    float4 *op = reinterpret_cast<float4 *>(p.o_part + at * p.d);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4)
+                        if (c < p.d) op[c / 4] = make_float4(o[c] * inv, o[c + 1] * inv, o[c + 2] * inv, o[c + 3] * inv);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// o = sum_s w_s o_s with w_s = exp(lse_s - lse): the parts of a row, in order.
+__global__ void __launch_bounds__(256) join_splits(const __grid_constant__ Problem p) {
+    const int vec = p.d / 4;
+    const size_t rows = (size_t)p.B * p.heads * p.n;
+    const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const size_t row = at / vec;
+    const int c = (int)(at % vec) * 4;
+    if (row >= rows) return;
+    float top = -INFINITY;
+    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.lse_part[s * rows + row]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.splits; ++s) {
+        const float w = ex2_approx((p.lse_part[s * rows + row] - ref) * kLog2e);
+        const float4 v = *reinterpret_cast<const float4 *>(p.o_part + (s * rows + row) * p.d + c);
+        sum += w;
+        o[0] = fmaf(w, v.x, o[0]);
+        o[1] = fmaf(w, v.y, o[1]);
+        o[2] = fmaf(w, v.z, o[2]);
+        o[3] = fmaf(w, v.w, o[3]);
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    const int i = (int)(row % p.n), h = (int)(row / p.n % p.heads);
+    const long long b = (long long)(row / p.n / p.heads);
+    const long long out = b * p.O.sb + (long long)h * p.O.sh + (long long)i * p.O.st + c;
+    if (p.dtype == LISA_BF16) {
+        uint2 r;
+        r.x = pack_bf16(o[0] * inv, o[1] * inv);
+        r.y = pack_bf16(o[2] * inv, o[3] * inv);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + out) = r;
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(const_cast<void *>(p.O.p)) + out) =
+            make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    }
+    if (c == 0 && p.lse) p.lse[row] = top == -INFINITY ? -INFINITY : top + logf(sum);
+}
+
+}  // namespace
+
+int tc_forward_splits(int B, int heads, int n, int m) {
+    const long long items = (long long)B * heads * ((n + 2 * kRows - 1) / (2 * kRows));
+    const int tiles = (m + kRows - 1) / kRows;
+    // fewer items than half the SMs: share the keys out, at least two tiles to each part
+    if (items * 2 > 152 || tiles < 4) return 1;
+    return (int)std::min<long long>(152 / items, tiles / 2);
+}
+
+cudaError_t launch_join(const Problem &p, cudaStream_t s) {
+    const size_t vecs = (size_t)p.B * p.heads * p.n * (p.d / 4);
+    join_splits<<<(unsigned)((vecs + 255) / 256), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {
+    FwdParams x{};
+    x.p = p;
+    x.err = err;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, &x.uq, p.Q, p.B, p.heads, p.n, p.d) || !make_map(&mk, &x.uk, p.K, p.B, p.kv_heads, p.m, p.d) ||
+        !make_map(&mv, &x.uv, p.V, p.B, p.kv_heads, p.m, p.d))
+        return cudaErrorInvalidValue;
+    x.qtiles = (p.n + 2 * kRows - 1) / (2 * kRows);
+    x.splits = p.splits;
+    const long long items = (long long)p.B * p.heads * x.qtiles * x.splits;
+    if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
+    x.items = (int)items;
+    const int lut = p.bias.mode ? round1k(p.bias.entries * 4) : 0;
+    const int keys = p.bias.mode == 2 ? round1k((p.m + 128) * 2) : 0;
+    const int fixed = 2 * kTileBytes + lut + keys + 1024;
+    const int tiles = (p.m + kRows - 1) / kRows;
+    x.stages = std::min(std::min(kMaxStages, (kSmemBudget - fixed) / (2 * kTileBytes)), std::max(2, tiles + 1));
+    if (x.stages < 1) return cudaErrorInvalidValue;
+    x.off_lut = (2 + 2 * x.stages) * kTileBytes;
+    x.off_keys = x.off_lut + lut;
+    const int bytes = x.off_keys + keys + 1024;
+    const unsigned grid = (unsigned)std::min(x.items, sms());
+    cudaError_t e;
+    switch (p.bias.mode) {
+        case 0:
+            if ((e = allow_smem<tc_forward<0>>()) != cudaSuccess) return e;
+            tc_forward<0><<<grid, kFwdThreads, bytes, s>>>(mq, mk, mv, x);
+            break;
+        case 1:
+            if ((e = allow_smem<tc_forward<1>>()) != cudaSuccess) return e;
+            tc_forward<1><<<grid, kFwdThreads, bytes, s>>>(mq, mk, mv, x);
+            break;
+        default:
+            if ((e = allow_smem<tc_forward<2>>()) != cudaSuccess) return e;
+            tc_forward<2><<<grid, kFwdThreads, bytes, s>>>(mq, mk, mv, x);
+    }
+    e = cudaGetLastError();
+    if (e == cudaSuccess && p.splits > 1) e = launch_join(p, s);
+    return e;
+}
+
+}  // namespace attn
+}  // namespace lisa

@@ -1,0 +1,203 @@
+// lisa_attn_tc.cuh -- pieces shared by the tensor-core kernels of the cross
+// attention (bf16): bounded waits that give up once per CTA, tensor-memory
+// transfers of whole rows, packed fp32 arithmetic, tensor maps of strided
+// [B][heads][tokens][d] tensors.
+//
+// Head widths 16 and 32 use the kernels of 64: their tiles are loaded with a
+// 64-wide box over a narrower tensor, so TMA fills columns d .. 63 with zeros,
+// which add nothing to any product; only d columns are stored.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "lisa_attn.h"
+#include "lisa_bias_dev.cuh"
+#include "lisa_internal.h"
+#include "lisa_tc_common.cuh"
+
+namespace lisa {
+namespace attn {
+namespace {
+
+using namespace lisa::sm100;
+
+constexpr int kRows = 128;                    // rows of a tile: queries or keys
+constexpr int kTileBytes = kRows * 128;       // 128 tokens x 64 bf16
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// A CTA whose wait gave up stops waiting altogether (its results are undefined
+// and the error word says so), so a failure costs one limit, not one per wait.
+struct Guard {
+    int *err;
+    volatile int *dead;
+};
+__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, const Guard &g, int bit) {
+    if (mbar_test_parity(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!mbar_test_parity_suspend(bar, parity)) {
+        if (*g.dead) return;
+        if (clock64() - t0 > kWaitCycles) {
+            atomicOr(g.err, bit);
+            *g.dead = 1;
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float *r) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
+          "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
+          "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *r) {
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
+        "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
+        "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *u) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+        : "memory");
+}
+// Registers of this warpgroup's threads, out of what the block was launched with.
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's rows are the 128 lanes, two bf16 of a row per 32-bit column.
+__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// [128 x cols] = A (tile of 128 rows, K-major) * B^T (tile of >= cols rows, K-major); K = 64.
+__device__ __forceinline__ void mma_rows_rows(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem, int cols) {
+    const uint32_t idesc = make_idesc_bf16(128, cols, false, false);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+        tc_mma(d_tmem, make_desc_sw128(a_smem + ks * 32, 16, 1024), make_desc_sw128(b_smem + ks * 32, 16, 1024),
+               idesc, ks > 0);
+}
+// [128 x 64] (+)= A (tensor memory, 128 x k) * B (tile of k token rows); k a multiple of 16.
+__device__ __forceinline__ void mma_weights_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_smem, int k,
+                                                 bool accumulate) {
+    const uint32_t idesc = make_idesc_bf16(128, 64, false, true);
+    for (int ks = 0; ks < k / 16; ++ks)
+        tc_mma_ta(d_tmem, a_tmem + ks * 8, make_desc_sw128(b_smem + ks * 2048, 1024, 1024), idesc,
+                  accumulate || ks > 0);
+}
+
+// One token box {64, 128} of a head's slice; coordinates of repeated dimensions stay 0.
+struct MapUse {
+    int hmul, bmul;
+};
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *m, const MapUse &u, int token, int head,
+                                          int batch, uint32_t bar) {
+    tma_load_4d(dst, m, 0, token, head * u.hmul, batch * u.bmul, bar);
+}
+
+// Zeroes rows r0 .. r1 - 1 (at most 15) of a token tile; all 128 threads of a warpgroup.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int r0, int r1, int t) {
+    const int row = r0 + (t >> 3);
+    if (row < r1) st_shared_v4(tile + (uint32_t)row * 128u + (uint32_t)(t & 7) * 16u, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ int keys_of(const Problem &p, int b) {
+    return p.kv_lens ? min(max(p.kv_lens[b], 0), p.m) : p.m;
+}
+
+// 64 (d) fp32 values of a row to bf16 at 16-byte aligned `out`.
+__device__ __forceinline__ void store_row_bf16(__nv_bfloat16 *out, const float *v, float mul, int d) {
+#pragma unroll
+    for (int c = 0; c < 64; c += 8) {
+        if (c >= d) break;
+        uint4 o;
+        o.x = pack_bf16(v[c] * mul, v[c + 1] * mul);
+        o.y = pack_bf16(v[c + 2] * mul, v[c + 3] * mul);
+        o.z = pack_bf16(v[c + 4] * mul, v[c + 5] * mul);
+        o.w = pack_bf16(v[c + 6] * mul, v[c + 7] * mul);
+        *reinterpret_cast<uint4 *>(out + c) = o;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// 4-D map {d, tokens, heads, B} of a strided bf16 tensor, box {64, 128, 1, 1}.
+inline bool make_map(CUtensorMap *m, MapUse *u, const Tensor &t, int B, int heads, int tokens, int d) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    u->hmul = heads > 1 && t.sh > 0 ? 1 : 0;
+    u->bmul = B > 1 && t.sb > 0 ? 1 : 0;
+    const cuuint64_t row = (cuuint64_t)(tokens > 1 ? t.st : d) * 2;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)tokens, (cuuint64_t)(u->hmul ? heads : 1),
+                          (cuuint64_t)(u->bmul ? B : 1)};
+    cuuint64_t strides[3] = {row, u->hmul ? (cuuint64_t)t.sh * 2 : row, u->bmul ? (cuuint64_t)t.sb * 2 : row};
+    cuuint32_t box[4] = {64, kRows, 1, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(t.p), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Raises a kernel's shared-memory limit once per device.
+template <auto kKernel>
+cudaError_t allow_smem() {
+    static std::mutex mu;
+    static bool done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[dev]) return cudaSuccess;
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, kKernel);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             227 * 1024 - (int)a.sharedSizeBytes);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
+}
+
+inline int sms() {
+    static int n[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+    if (n[dev] == 0) n[dev] = sm_count();
+    return n[dev];
+}
+
+constexpr int kSmemBudget = 227 * 1024 - 2048;   // dynamic: behind the barriers
+
+inline int round1k(int x) { return (x + 1023) / 1024 * 1024; }
+
+}  // namespace
+}  // namespace attn
+}  // namespace lisa
