@@ -60,7 +60,8 @@ struct Problem {
     BiasDev bias;
     void *dQ, *dK, *dV;
     float *delta;          // [B][heads][n]: sum_j p dP, written by the dQ kernel
-    float *dbias;          // [heads][n][m] fp32: dS summed over the batch
+    float *dbias;          // [b_splits][heads][n][m] fp32: dS summed over (parts of) the batch
+    int b_splits;
     // forward split over the keys
     int splits;
     float *o_part;         // [splits][B][heads][n][d]
@@ -77,8 +78,9 @@ lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev);
 // --- launchers ---------------------------------------------------------------
 cudaError_t launch_bias_dense(const lisa_rel_bias &b, const BiasDev &dev, void *out, int dtype, cudaStream_t s);
 size_t bias_grad_bytes(const lisa_rel_bias &b, int heads);
-cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int dtype, float *dtable,
-                             void *ws, cudaStream_t s);
+// `parts` matrices one behind the other, added up
+cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int parts, int dtype,
+                             float *dtable, void *ws, cudaStream_t s);
 
 cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dq(const Problem &p, cudaStream_t s);
@@ -88,6 +90,9 @@ cudaError_t launch_simt_dbias(const Problem &p, cudaStream_t s);
 // bf16 on the tensor cores; `err` is the error word of the call's workspace
 int tc_forward_splits(int B, int heads, int n, int m);
 cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s);
+int tc_dkdv_splits(int B, int kv_heads, int group, int n, int m);
+int tc_dbias_splits(int B, int heads, int n, int m);
+cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s);
 // joins p.splits partial outputs (o_part, lse_part) into O and lse
 cudaError_t launch_join(const Problem &p, cudaStream_t s);
 

@@ -204,17 +204,30 @@ FwdPlan forward_plan(int B, int heads, int n, int m, int d, int dtype) {
 }
 
 struct BwdPlan {
-    size_t off_delta, off_dbias, off_grad, total;
+    bool tc;
+    int q_splits, b_splits;
+    size_t off_delta, off_dk, off_dv, off_dbias, off_grad, total;   // the error word is at 0
 };
 
-BwdPlan backward_plan(int B, int heads, int n, int m, const lisa_rel_bias *bias) {
+BwdPlan backward_plan(int B, int heads, int kv_heads, int n, int m, int d, const lisa_rel_bias *bias, int dtype) {
     BwdPlan pl{};
-    size_t off = 0;
+    pl.tc = dtype == LISA_BF16;
+    pl.q_splits = pl.b_splits = 1;
+    size_t off = kAlign;
     pl.off_delta = off;
     off = align_up(off + (size_t)B * heads * n * sizeof(float));
+    if (pl.tc) pl.q_splits = tc_dkdv_splits(B, kv_heads, heads / kv_heads, n, m);
+    if (pl.q_splits > 1) {
+        const size_t part = (size_t)pl.q_splits * B * kv_heads * m * d * sizeof(float);
+        pl.off_dk = off;
+        off = align_up(off + part);
+        pl.off_dv = off;
+        off = align_up(off + part);
+    }
     if (bias) {
+        if (pl.tc) pl.b_splits = tc_dbias_splits(B, heads, n, m);
         pl.off_dbias = off;
-        off = align_up(off + (size_t)heads * n * m * sizeof(float));
+        off = align_up(off + (size_t)pl.b_splits * heads * n * m * sizeof(float));
         pl.off_grad = off;
         off = align_up(off + bias_grad_bytes(*bias, heads));
     }
@@ -275,7 +288,7 @@ extern "C" lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, in
     if (!workspace || workspace_bytes < bias_grad_bytes(*bias, heads)) return LISA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
     return status_of(
-        launch_bias_grad(*bias, dev, dbias, dtype, dtable, workspace, static_cast<cudaStream_t>(stream)));
+        launch_bias_grad(*bias, dev, dbias, 1, dtype, dtable, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" size_t lisa_cross_attention_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,
@@ -327,7 +340,7 @@ extern "C" size_t lisa_cross_attention_backward_workspace_bytes(int B, int heads
         BiasDev dev;
         if (bias_dev(bias, heads, dev) != LISA_OK || !matrix_fits(*bias)) return 0;
     }
-    return backward_plan(B, heads, n, m, bias).total;
+    return backward_plan(B, heads, kv_heads, n, m, d, bias, dtype).total;
 }
 
 extern "C" lisa_status lisa_cross_attention_backward(
@@ -381,7 +394,7 @@ extern "C" lisa_status lisa_cross_attention_backward(
             if (outs[a].meets(outs[c])) return LISA_ERR_INVALID_ARG;
     }
     if (bias && !matrix_fits(*bias)) return LISA_ERR_UNSUPPORTED;
-    const BwdPlan pl = backward_plan(B, heads, n, m, bias);
+    const BwdPlan pl = backward_plan(B, heads, kv_heads, n, m, d, bias, dtype);
     if (!workspace || workspace_bytes < pl.total) return LISA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
     p.O = {O, o_strides->batch, o_strides->head, o_strides->token};
@@ -392,13 +405,21 @@ extern "C" lisa_status lisa_cross_attention_backward(
     p.dV = dV;
     char *ws = static_cast<char *>(workspace);
     p.delta = reinterpret_cast<float *>(ws + pl.off_delta);
+    p.q_splits = pl.q_splits;
+    p.dk_part = reinterpret_cast<float *>(ws + pl.off_dk);
+    p.dv_part = reinterpret_cast<float *>(ws + pl.off_dv);
+    p.b_splits = pl.b_splits;
     p.dbias = reinterpret_cast<float *>(ws + pl.off_dbias);
-    cudaError_t e = launch_simt_dq(p, cs);
-    if (e == cudaSuccess) e = launch_simt_dkdv(p, cs);
-    if (e == cudaSuccess && bias) e = launch_simt_dbias(p, cs);
-    if (e == cudaSuccess && bias) {
-        // the matrix of the batch's dS, then as the bias matrix's own gradient
-        e = launch_bias_grad(*bias, p.bias, p.dbias, LISA_F32, dtable, ws + pl.off_grad, cs);
+    cudaError_t e;
+    if (pl.tc) {
+        e = launch_tc_backward(p, reinterpret_cast<int *>(ws), cs);
+    } else {
+        e = launch_simt_dq(p, cs);
+        if (e == cudaSuccess) e = launch_simt_dkdv(p, cs);
+        if (e == cudaSuccess && bias) e = launch_simt_dbias(p, cs);
     }
+    // the matrix of the batch's dS, then as the bias matrix's own gradient
+    if (e == cudaSuccess && bias)
+        e = launch_bias_grad(*bias, p.bias, p.dbias, pl.b_splits, LISA_F32, dtable, ws + pl.off_grad, cs);
     return status_of(e);
 }

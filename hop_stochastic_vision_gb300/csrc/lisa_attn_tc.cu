@@ -444,7 +444,7 @@ cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {
     if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
     x.items = (int)items;
     const int lut = p.bias.mode ? round1k(p.bias.entries * 4) : 0;
-    const int keys = p.bias.mode == 2 ? round1k((p.m + 128) * 2) : 0;
+    const int keys = p.bias.mode == 2 ? round1k((p.m + 127) / 128 * 256) : 0;
     const int fixed = 2 * kTileBytes + lut + keys + 1024;
     const int tiles = (p.m + kRows - 1) / kRows;
     x.stages = std::min(std::min(kMaxStages, (kSmemBudget - fixed) / (2 * kTileBytes)), std::max(2, tiles + 1));

@@ -1,0 +1,1005 @@
+// lisa_attn_tc_bwd.cu -- the backward cross attention on the tensor cores (bf16).
+//
+// Three kernels of one shape, each a persistent CTA of 12 warps around 128 x 128
+// tiles of pairs whose scores and dP = dO V^T are products into tensor memory:
+//   dQ     128 queries against every key; dS goes back to tensor memory as bf16
+//          for dQ += dS K.  Also leaves delta_i = sum_j p dP in fp32, which the
+//          two others use (the dQ kernel itself takes dO . O from the rounded
+//          output, whose error is one rounding of O against a bf16 result)
+//   dK dV  128 keys against the queries of the heads that share them, the
+//          tile transposed (rows are keys): dV += P^T dO, dK += dS^T Q, the
+//          queries split over CTAs when there are few key tiles, the parts added
+//          in order by a second kernel
+//   dbias  one tile of pairs of a head, the batch one by one, the sum of the
+//          unrounded dS in registers
+// Scores are recomputed in each (7 products for 5) so that every sum has one
+// owner: no atomics, no fp32 dQ in memory, the same bits every time.
+//
+// Two warpgroups share a tile by columns, 64 each, a thread per row.  The
+// threads take S and dP into registers as soon as they are there, so the next
+// tile's products run under this tile's arithmetic.
+#include "lisa_attn_tc.cuh"
+
+namespace lisa {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 384;      // 8 warps of arithmetic, products, loads, two helpers
+constexpr int kRegsMath = 208, kRegsControl = 88;
+constexpr int kMaxStages = 4;
+
+struct BwdParams {
+    Problem p;
+    MapUse uq, uk, uv, ud;
+    int *err;
+    int first;             // this kernel clears the error word
+    int qtiles, ktiles;    // tiles of 128 queries, keys
+    int splits;            // dK dV: over the (head, query tile) pairs; dbias: over the batch
+    int items;
+    int stages;
+    int off_lut, off_aux;
+};
+
+__device__ __forceinline__ int tile_keys(int len, int t) { return min(kRows, len - t * kRows); }
+__device__ __forceinline__ int tile_cols(int keys) { return (keys + 15) & ~15; }
+
+__device__ __forceinline__ float neg_lse2(const float *lse, size_t at, bool in) {
+    const float l = in ? lse[at] : INFINITY;
+    return l == -INFINITY ? -INFINITY : -l * kLog2e;   // rows without keys: every weight 2^-inf = 0
+}
+
+// Weights of 64 columns of a row of queries, in place: s -> 2^(scale2 s + bias - lse).
+// `c0`: first column of the tile, `keys`: valid columns from there (may be <= 0).
+template <int kBias>
+__device__ __forceinline__ void row_weights(float (&s)[64], const BiasDev &b, const float *lut, const uint16_t *key_off,
+                                            int j0, int keys, int oq, int oq_lo, float scale2, float nl) {
+    if (kBias == 0) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, nl);
+    } else if (kBias == 1) {
+        const int oq_hi = oq_lo + 31, last = b.entries - 1;
+        const int lo = b.step_c * j0 - oq_hi, hi = b.step_c * (j0 + max(keys, 1) - 1) - oq_lo;
+        if (hi <= 0 || lo >= last) {
+            const float add = nl + lut[hi <= 0 ? 0 : last];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, add);
+        } else {
+            const int off = b.step_c * j0 - oq;
+            if (b.step_c == 1 && lo >= 0 && lo + 31 + 63 <= last) {
+                const float *l = lut + off;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, l[c]) + nl;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    s[c] = fmaf(s[c], scale2, lut[min(max(off + b.step_c * c, 0), last)]) + nl;
+            }
+        }
+    } else {
+        const int last = b.entries - 1;
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
+            s[c] = fmaf(s[c], scale2, lut[min(max((int)(a.x & 0xFFFFu) - oq, 0), last)]) + nl;
+            s[c + 1] = fmaf(s[c + 1], scale2, lut[min(max((int)(a.x >> 16) - oq, 0), last)]) + nl;
+            s[c + 2] = fmaf(s[c + 2], scale2, lut[min(max((int)(a.y & 0xFFFFu) - oq, 0), last)]) + nl;
+            s[c + 3] = fmaf(s[c + 3], scale2, lut[min(max((int)(a.y >> 16) - oq, 0), last)]) + nl;
+        }
+    }
+    if (keys < 64) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+            if (c >= keys) s[c] = -INFINITY;
+    }
+#pragma unroll
+    for (int c = 0; c < 64; ++c) s[c] = ex2_approx(s[c]);
+}
+
+// Two 32-column halves of a 64-column strip; a strip that the products did not
+// reach (`any` false) is not read.
+__device__ __forceinline__ void load_strip(uint32_t taddr, float (&v)[64], bool any) {
+    if (any) {
+        tmem_ld32_nowait(taddr, v);
+        tmem_ld32_nowait(taddr + 32, v + 32);
+    }
+    tc_wait_ld();
+}
+
+__device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(bar));
+}
+
+__device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// The products' thread waits for the last use of every ring slot, so nothing
+// arrives on the CTA's barriers once it has gone.
+__device__ __forceinline__ void drain(uint64_t *bar, int uses, int *err) {
+    if (uses > 0 && !mbar_wait(smem_u32(bar), (uses - 1) & 1)) atomicOr(err, kErrTimeoutMma);
+}
+__device__ __forceinline__ int uses_of(int total, int slot, int stages) {
+    return total > slot ? (total - 1 - slot) / stages + 1 : 0;
+}
+
+// ------------------------------------------------------------------------ dQ
+struct DqBars {
+    uint64_t q_full[2], q_empty[2], k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages], v_empty[kMaxStages];
+    uint64_t s_full, s_free, dp_full, dp_free, ds_full, dq_done;
+};
+
+template <int kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+    tc_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md,
+          const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+          const __grid_constant__ BwdParams x) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) DqBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    __shared__ float other[kRows];
+    const Problem &p = x.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_u32(sm);
+    const uint32_t qd = base, ring = base + 4 * kTileBytes;   // two slots of (Q, dO); stages of (K, V)
+    float *lut = reinterpret_cast<float *>(sm + x.off_lut);
+    uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_aux);
+    const Guard guard{x.err, &dead};
+
+    if (tid == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&bar.q_full[t]), 1);
+            mbar_init(smem_u32(&bar.q_empty[t]), 1);
+        }
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(smem_u32(&bar.k_full[s]), 1);
+            mbar_init(smem_u32(&bar.v_full[s]), 1);
+            mbar_init(smem_u32(&bar.k_empty[s]), 1);
+            mbar_init(smem_u32(&bar.v_empty[s]), 1);
+        }
+        mbar_init(smem_u32(&bar.s_full), 1);
+        mbar_init(smem_u32(&bar.dp_full), 1);
+        mbar_init(smem_u32(&bar.dq_done), 1);
+        mbar_init(smem_u32(&bar.s_free), 8);
+        mbar_init(smem_u32(&bar.dp_free), 8);
+        mbar_init(smem_u32(&bar.ds_full), 8);
+        dead = 0;
+        fence_mbar_init();
+        if (x.first && blockIdx.x == 0) *x.err = 0;
+    }
+    if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (kBias == 2)
+        for (int j = tid; j < p.m; j += kThreads) key_off[j] = (uint16_t)off_key(p.bias, j);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t tS = tmem, tP = tmem + 128, tDs = tmem + 256, tDq = tmem + 320;
+
+    struct Item {
+        int h, b, q0, len, tiles;
+    };
+    auto item_of = [&](int it) {
+        Item w;
+        w.q0 = (it % x.qtiles) * kRows;
+        const int r = it / x.qtiles;
+        w.b = r % p.B;
+        w.h = r / p.B;
+        w.len = keys_of(p, w.b);
+        w.tiles = (w.len + kRows - 1) / kRows;
+        return w;
+    };
+
+    if (warp >= 8) set_regs_down<kRegsControl>();
+    if (warp >= 10) {
+        // idle: completes the control warps' group of four
+    } else if (warp == 9) {
+        if (lane == 0) {
+            int kt = 0, nq = 0;
+            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+                const Item w = item_of(it);
+                if (w.tiles == 0) continue;
+                const int qs = nq & 1;
+                if (nq >= 2) wait_on(smem_u32(&bar.q_empty[qs]), ((nq >> 1) - 1) & 1, guard, kErrTimeoutMma);
+                const uint32_t f = smem_u32(&bar.q_full[qs]);
+                mbar_arrive_expect_tx(f, 2 * kTileBytes);
+                load_rows(qd + 2 * qs * kTileBytes, &mq, x.uq, w.q0, w.h, w.b, f);
+                load_rows(qd + (2 * qs + 1) * kTileBytes, &md, x.ud, w.q0, w.h, w.b, f);
+                ++nq;
+                for (int j = 0; j < w.tiles; ++j, ++kt) {
+                    const int s = kt % x.stages;
+                    const uint32_t ph = (uint32_t)(kt / x.stages) & 1u;
+                    const uint32_t kf = smem_u32(&bar.k_full[s]), vf = smem_u32(&bar.v_full[s]);
+                    if (kt >= x.stages) wait_on(smem_u32(&bar.k_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(kf, kTileBytes);
+                    load_rows(ring + 2 * s * kTileBytes, &mk, x.uk, j * kRows, w.h / p.group, w.b, kf);
+                    if (kt >= x.stages) wait_on(smem_u32(&bar.v_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(vf, kTileBytes);
+                    load_rows(ring + (2 * s + 1) * kTileBytes, &mv, x.uv, j * kRows, w.h / p.group, w.b, vf);
+                }
+            }
+            for (int s = 0; s < x.stages; ++s) {
+                drain(&bar.k_empty[s], uses_of(kt, s, x.stages), x.err);
+                drain(&bar.v_empty[s], uses_of(kt, s, x.stages), x.err);
+            }
+            for (int t = 0; t < 2; ++t) drain(&bar.q_empty[t], uses_of(nq, t, 2), x.err);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        if (lane == 0) {
+            int kt = 0, nq = 0;
+            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+                const Item w = item_of(it);
+                if (w.tiles == 0) continue;
+                const int qs = nq & 1;
+                wait_on(smem_u32(&bar.q_full[qs]), (nq >> 1) & 1, guard, kErrTimeoutLoad);
+                ++nq;
+                const uint32_t qa = qd + 2 * qs * kTileBytes, da = qa + kTileBytes;
+                auto front = [&](int k, int j) {
+                    const int s = k % x.stages;
+                    const uint32_t ph = (uint32_t)(k / x.stages) & 1u;
+                    const int cols = tile_cols(tile_keys(w.len, j));
+                    wait_on(smem_u32(&bar.k_full[s]), ph, guard, kErrTimeoutLoad);
+                    if (k > 0) wait_on(smem_u32(&bar.s_free), (k - 1) & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_rows_rows(tS, qa, ring + 2 * s * kTileBytes, cols);
+                    tc_commit(smem_u32(&bar.s_full));
+                    wait_on(smem_u32(&bar.v_full[s]), ph, guard, kErrTimeoutLoad);
+                    if (k > 0) wait_on(smem_u32(&bar.dp_free), (k - 1) & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_rows_rows(tP, da, ring + (2 * s + 1) * kTileBytes, cols);
+                    tc_commit(smem_u32(&bar.dp_full));
+                    tc_commit(smem_u32(&bar.v_empty[s]));
+                    if (j == w.tiles - 1) tc_commit(smem_u32(&bar.q_empty[qs]));
+                };
+                front(kt, 0);
+                for (int j = 0; j < w.tiles; ++j, ++kt) {
+                    if (j + 1 < w.tiles) front(kt + 1, j + 1);
+                    const int s = kt % x.stages;
+                    wait_on(smem_u32(&bar.ds_full), kt & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_weights_rows(tDq, tDs, ring + 2 * s * kTileBytes, tile_cols(tile_keys(w.len, j)), j > 0);
+                    tc_commit(smem_u32(&bar.dq_done));
+                    tc_commit(smem_u32(&bar.k_empty[s]));
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        set_regs_up<kRegsMath>();
+        const int half = warp >> 2, wt = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const float scale2 = p.scale * kLog2e;
+        int kt = 0, lut_head = -1;
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(it);
+            if (kBias && w.h != lut_head) {
+                math_barrier();
+                fill_offsets(p.bias, w.h, kLog2e, lut, tid, 256);
+                math_barrier();
+                lut_head = w.h;
+            }
+            const int i = w.q0 + wt;
+            const bool in = i < p.n;
+            const size_t row = ((size_t)w.b * p.heads + w.h) * p.n + i;
+            const float nl = neg_lse2(p.lse, row, in);
+            float delta = 0.f, exact = 0.f;
+            if (in && w.tiles > 0) {
+                const __nv_bfloat16 *o = static_cast<const __nv_bfloat16 *>(p.O.p) + (long long)w.b * p.O.sb +
+                                         (long long)w.h * p.O.sh + (long long)i * p.O.st;
+                const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(p.dO.p) + (long long)w.b * p.dO.sb +
+                                         (long long)w.h * p.dO.sh + (long long)i * p.dO.st;
+#pragma unroll
+                for (int c = 0; c < 64; c += 8) {
+                    if (c >= p.d) break;
+                    const uint4 a = *reinterpret_cast<const uint4 *>(o + c), b = *reinterpret_cast<const uint4 *>(g + c);
+                    delta = fmaf(bf16_lo(a.x), bf16_lo(b.x), delta);
+                    delta = fmaf(bf16_hi(a.x), bf16_hi(b.x), delta);
+                    delta = fmaf(bf16_lo(a.y), bf16_lo(b.y), delta);
+                    delta = fmaf(bf16_hi(a.y), bf16_hi(b.y), delta);
+                    delta = fmaf(bf16_lo(a.z), bf16_lo(b.z), delta);
+                    delta = fmaf(bf16_hi(a.z), bf16_hi(b.z), delta);
+                    delta = fmaf(bf16_lo(a.w), bf16_lo(b.w), delta);
+                    delta = fmaf(bf16_hi(a.w), bf16_hi(b.w), delta);
+                }
+            }
+            int oq = 0, oq_lo = 0;
+            if (kBias) {
+                const int start = bias_start(p.bias, w.b);
+                oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start);
+                oq_lo = off_query(p.bias, i - lane, start);
+            }
+            for (int j = 0; j < w.tiles; ++j, ++kt) {
+                const int keys = tile_keys(w.len, j), cols = tile_cols(keys), j0 = j * kRows + 64 * half;
+                const bool any = 64 * half < cols;
+                float s[64], dp[64];
+                wait_on(smem_u32(&bar.s_full), kt & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                load_strip(tS + 64 * half + lanes, s, any);
+                tc_fence_before();
+                arrive_warp(&bar.s_free, lane);
+                if (any) row_weights<kBias>(s, p.bias, lut, key_off, j0, keys - 64 * half, oq, oq_lo, scale2, nl);
+                wait_on(smem_u32(&bar.dp_full), kt & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                load_strip(tP + 64 * half + lanes, dp, any);
+                tc_fence_before();
+                arrive_warp(&bar.dp_free, lane);
+                // the previous dS has been read; every warp sees every phase, with a strip of its own or not
+                if (kt > 0) wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
+                if (any) {
+                    if (keys - 64 * half < 64) {   // dP of keys behind the last one holds whatever their values hold
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (c >= keys - 64 * half) dp[c] = 0.f;
+                    }
+                    uint32_t ds[32];
+                    float e0 = 0.f, e1 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        const float a = s[c] * dp[c], b = s[c + 1] * dp[c + 1];
+                        e0 += a;
+                        e1 += b;
+                        ds[c >> 1] = pack_bf16(fmaf(-s[c], delta, a), fmaf(-s[c + 1], delta, b));
+                    }
+                    exact += e0 + e1;
+                    tmem_st16(tDs + 32 * half + lanes, ds);
+                    tmem_st16(tDs + 32 * half + 16 + lanes, ds + 16);
+                }
+                if (half == 0 && keys < cols && w.len < p.m) {
+                    // S is done with the tile: what stands behind the last key may not meet dS = 0
+                    zero_rows(ring + 2 * (kt % x.stages) * kTileBytes, keys, cols, wt);
+                    fence_proxy_async();
+                }
+                tc_wait_st();
+                tc_fence_before();
+                arrive_warp(&bar.ds_full, lane);
+            }
+            // the two halves of the keys' share of delta
+            if (half == 1) other[wt] = exact;
+            math_barrier();
+            if (half == 0 && in) p.delta[row] = exact + other[wt];
+            float o[32];
+            if (w.tiles > 0) {
+                wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                tmem_ld32_nowait(tDq + 32 * half + lanes, o);
+                tc_wait_ld();
+                tc_fence_before();
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[c] = 0.f;
+            }
+            math_barrier();   // `other` may be written again; every warp has read dQ before the next ds_full
+            if (in) {
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.dQ) + row * p.d + 32 * half;
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                    if (32 * half + c >= p.d) break;
+                    uint4 v;
+                    v.x = pack_bf16(o[c] * p.scale, o[c + 1] * p.scale);
+                    v.y = pack_bf16(o[c + 2] * p.scale, o[c + 3] * p.scale);
+                    v.z = pack_bf16(o[c + 4] * p.scale, o[c + 5] * p.scale);
+                    v.w = pack_bf16(o[c + 6] * p.scale, o[c + 7] * p.scale);
+                    *reinterpret_cast<uint4 *>(out + c) = v;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// --------------------------------------------------------------------- dK, dV
+struct DkvBars {
+    uint64_t kv_full, kv_empty, q_full[kMaxStages], d_full[kMaxStages], q_empty[kMaxStages], d_empty[kMaxStages];
+    uint64_t aux_full[kMaxStages], aux_empty[kMaxStages];
+    uint64_t s_full, s_free, dp_full, dp_free, p_full, ds_full, dv_done, dk_done;
+};
+
+// What the arithmetic needs of a tile's queries, one entry per column.
+struct QueryAux {
+    float nl[kRows], delta[kRows];
+    int oq[kRows];
+};
+
+template <int kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+    tc_dkdv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md,
+            const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+            const __grid_constant__ BwdParams x) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) DkvBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    const Problem &p = x.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_u32(sm);
+    const uint32_t kv = base, ring = base + 2 * kTileBytes;   // K, V; stages of (Q, dO)
+    float *lut = reinterpret_cast<float *>(sm + x.off_lut);
+    QueryAux *aux = reinterpret_cast<QueryAux *>(sm + x.off_aux);
+    const Guard guard{x.err, &dead};
+
+    if (tid == 0) {
+        mbar_init(smem_u32(&bar.kv_full), 1);
+        mbar_init(smem_u32(&bar.kv_empty), 1);
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(smem_u32(&bar.q_full[s]), 1);
+            mbar_init(smem_u32(&bar.d_full[s]), 1);
+            mbar_init(smem_u32(&bar.q_empty[s]), 1);
+            mbar_init(smem_u32(&bar.d_empty[s]), 1);
+            mbar_init(smem_u32(&bar.aux_full[s]), 2);
+            mbar_init(smem_u32(&bar.aux_empty[s]), 8);
+        }
+        mbar_init(smem_u32(&bar.s_full), 1);
+        mbar_init(smem_u32(&bar.dp_full), 1);
+        mbar_init(smem_u32(&bar.dv_done), 1);
+        mbar_init(smem_u32(&bar.dk_done), 1);
+        mbar_init(smem_u32(&bar.s_free), 8);
+        mbar_init(smem_u32(&bar.dp_free), 8);
+        mbar_init(smem_u32(&bar.p_full), 8);
+        mbar_init(smem_u32(&bar.ds_full), 8);
+        dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t tS = tmem, tD = tmem + 128, tPw = tmem + 256, tDs = tmem + 320, tDv = tmem + 384, tDk = tmem + 448;
+    const int steps = p.group * x.qtiles;   // (head, query tile) pairs of a kv head
+
+    struct Item {
+        int g, b, j0, split, len, u0, u1;
+    };
+    auto item_of = [&](int it) {
+        Item w;
+        w.split = it % x.splits;
+        int r = it / x.splits;
+        w.j0 = (r % x.ktiles) * kRows;
+        r /= x.ktiles;
+        w.b = r % p.B;
+        w.g = r / p.B;
+        w.len = keys_of(p, w.b);
+        const int per = (steps + x.splits - 1) / x.splits;
+        w.u0 = min(w.split * per, steps);
+        w.u1 = w.j0 < w.len ? min(w.u0 + per, steps) : w.u0;
+        return w;
+    };
+
+    if (warp >= 8) set_regs_down<kRegsControl>();
+    if (warp >= 10) {
+        // per-query scalars of each tile, 64 threads
+        const int t = tid - 320;
+        int n = 0;
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(it);
+            const int start = kBias ? bias_start(p.bias, w.b) : 0;
+            for (int u = w.u0; u < w.u1; ++u, ++n) {
+                const int s = n % x.stages;
+                if (n >= x.stages) wait_on(smem_u32(&bar.aux_empty[s]), ((n / x.stages) - 1) & 1, guard, kErrTimeoutMma);
+                const int h = w.g * p.group + u / x.qtiles, q0 = (u % x.qtiles) * kRows;
+                const size_t row0 = ((size_t)w.b * p.heads + h) * p.n;
+#pragma unroll
+                for (int e = t; e < kRows; e += 64) {
+                    const int i = q0 + e;
+                    const bool in = i < p.n;
+                    aux[s].nl[e] = neg_lse2(p.lse, row0 + i, in);
+                    aux[s].delta[e] = in ? p.delta[row0 + i] : 0.f;
+                    if (kBias) aux[s].oq[e] = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start);
+                }
+                arrive_warp(&bar.aux_full[s], lane);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            int n = 0, items = 0;
+            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+                const Item w = item_of(it);
+                if (w.u0 >= w.u1) continue;
+                if (items > 0) wait_on(smem_u32(&bar.kv_empty), (items - 1) & 1, guard, kErrTimeoutMma);
+                ++items;
+                const uint32_t f = smem_u32(&bar.kv_full);
+                mbar_arrive_expect_tx(f, 2 * kTileBytes);
+                load_rows(kv, &mk, x.uk, w.j0, w.g, w.b, f);
+                load_rows(kv + kTileBytes, &mv, x.uv, w.j0, w.g, w.b, f);
+                for (int u = w.u0; u < w.u1; ++u, ++n) {
+                    const int s = n % x.stages;
+                    const uint32_t ph = (uint32_t)(n / x.stages) & 1u;
+                    const int h = w.g * p.group + u / x.qtiles, q0 = (u % x.qtiles) * kRows;
+                    const uint32_t qf = smem_u32(&bar.q_full[s]), df = smem_u32(&bar.d_full[s]);
+                    if (n >= x.stages) wait_on(smem_u32(&bar.q_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(qf, kTileBytes);
+                    load_rows(ring + 2 * s * kTileBytes, &mq, x.uq, q0, h, w.b, qf);
+                    if (n >= x.stages) wait_on(smem_u32(&bar.d_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(df, kTileBytes);
+                    load_rows(ring + (2 * s + 1) * kTileBytes, &md, x.ud, q0, h, w.b, df);
+                }
+            }
+            for (int s = 0; s < x.stages; ++s) {
+                drain(&bar.q_empty[s], uses_of(n, s, x.stages), x.err);
+                drain(&bar.d_empty[s], uses_of(n, s, x.stages), x.err);
+            }
+            drain(&bar.kv_empty, items, x.err);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        if (lane == 0) {
+            int n = 0, items = 0;
+            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+                const Item w = item_of(it);
+                if (w.u0 >= w.u1) continue;
+                wait_on(smem_u32(&bar.kv_full), items & 1, guard, kErrTimeoutLoad);
+                ++items;
+                auto cols_of = [&](int u) { return tile_cols(min(kRows, p.n - (u % x.qtiles) * kRows)); };
+                auto scores = [&](int k, int u) {
+                    const int s = k % x.stages;
+                    wait_on(smem_u32(&bar.q_full[s]), (k / x.stages) & 1, guard, kErrTimeoutLoad);
+                    if (k > 0) wait_on(smem_u32(&bar.s_free), (k - 1) & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_rows_rows(tS, kv, ring + 2 * s * kTileBytes, cols_of(u));
+                    tc_commit(smem_u32(&bar.s_full));
+                };
+                auto slopes = [&](int k, int u) {
+                    const int s = k % x.stages;
+                    wait_on(smem_u32(&bar.d_full[s]), (k / x.stages) & 1, guard, kErrTimeoutLoad);
+                    if (k > 0) wait_on(smem_u32(&bar.dp_free), (k - 1) & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_rows_rows(tD, kv + kTileBytes, ring + (2 * s + 1) * kTileBytes, cols_of(u));
+                    tc_commit(smem_u32(&bar.dp_full));
+                    if (u == w.u1 - 1) tc_commit(smem_u32(&bar.kv_empty));
+                };
+                scores(n, w.u0);
+                slopes(n, w.u0);
+                for (int u = w.u0; u < w.u1; ++u, ++n) {
+                    const int s = n % x.stages;
+                    if (u + 1 < w.u1) scores(n + 1, u + 1);
+                    wait_on(smem_u32(&bar.p_full), n & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_weights_rows(tDv, tPw, ring + (2 * s + 1) * kTileBytes, cols_of(u), u > w.u0);
+                    tc_commit(smem_u32(&bar.dv_done));
+                    tc_commit(smem_u32(&bar.d_empty[s]));
+                    if (u + 1 < w.u1) slopes(n + 1, u + 1);
+                    wait_on(smem_u32(&bar.ds_full), n & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_weights_rows(tDk, tDs, ring + 2 * s * kTileBytes, cols_of(u), u > w.u0);
+                    tc_commit(smem_u32(&bar.dk_done));
+                    tc_commit(smem_u32(&bar.q_empty[s]));
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        set_regs_up<kRegsMath>();
+        const int half = warp >> 2, wt = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const float scale2 = p.scale * kLog2e;
+        int n = 0, lut_head = -1;
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(it);
+            const int j = w.j0 + wt;
+            const int ok = kBias ? off_key(p.bias, min(j, p.m - 1)) : 0;
+            for (int u = w.u0; u < w.u1; ++u, ++n) {
+                const int h = w.g * p.group + u / x.qtiles;
+                if (kBias && h != lut_head) {
+                    math_barrier();
+                    fill_offsets(p.bias, h, kLog2e, lut, tid, 256);
+                    math_barrier();
+                    lut_head = h;
+                }
+                const int cols = tile_cols(min(kRows, p.n - (u % x.qtiles) * kRows));
+                const bool any = 64 * half < cols;
+                const QueryAux &a = aux[n % x.stages];
+                const int c0 = 64 * half;
+                float s[64], dp[64];
+                wait_on(smem_u32(&bar.aux_full[n % x.stages]), (n / x.stages) & 1, guard, kErrTimeoutLoad);
+                wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                load_strip(tS + c0 + lanes, s, any);
+                tc_fence_before();
+                arrive_warp(&bar.s_free, lane);
+                uint32_t out[32];
+                if (any) {
+                    if (kBias == 1) {
+                        const int last = p.bias.entries - 1;
+                        const int off = ok - a.oq[c0];   // column c: off - c
+                        const int off_lo = __shfl_sync(0xFFFFFFFFu, off, 0), off_hi = __shfl_sync(0xFFFFFFFFu, off, 31);
+                        // rows of one warp are 32 keys in order, all offsets of the strip in off_lo - 63 .. off_hi
+                        if (off_hi <= 0 || off_lo - 63 >= last) {
+                            const float add = lut[off_hi <= 0 ? 0 : last];
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, add + a.nl[c0 + c]);
+                        } else if (off_lo - 63 >= 0 && off_hi <= last) {
+                            const float *l = lut + off;
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, l[-c]) + a.nl[c0 + c];
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 64; ++c)
+                                s[c] = fmaf(s[c], scale2, lut[min(max(off - c, 0), last)]) + a.nl[c0 + c];
+                        }
+                    } else if (kBias == 2) {
+                        const int last = p.bias.entries - 1;
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) {
+                            const int4 o = *reinterpret_cast<const int4 *>(a.oq + c0 + c);
+                            const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
+                            s[c] = fmaf(s[c], scale2, lut[min(max(ok - o.x, 0), last)]) + l.x;
+                            s[c + 1] = fmaf(s[c + 1], scale2, lut[min(max(ok - o.y, 0), last)]) + l.y;
+                            s[c + 2] = fmaf(s[c + 2], scale2, lut[min(max(ok - o.z, 0), last)]) + l.z;
+                            s[c + 3] = fmaf(s[c + 3], scale2, lut[min(max(ok - o.w, 0), last)]) + l.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) {
+                            const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
+                            s[c] = fmaf(s[c], scale2, l.x);
+                            s[c + 1] = fmaf(s[c + 1], scale2, l.y);
+                            s[c + 2] = fmaf(s[c + 2], scale2, l.z);
+                            s[c + 3] = fmaf(s[c + 3], scale2, l.w);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        s[c] = ex2_approx(s[c]);
+                        s[c + 1] = ex2_approx(s[c + 1]);
+                        out[c >> 1] = pack_bf16(s[c], s[c + 1]);
+                    }
+                }
+                // the previous P has been read; every warp sees every phase, with a strip of its own or not
+                if (n > 0) wait_on(smem_u32(&bar.dv_done), (n - 1) & 1, guard, kErrTimeoutMma);
+                if (any) {
+                    tmem_st16(tPw + 32 * half + lanes, out);
+                    tmem_st16(tPw + 32 * half + 16 + lanes, out + 16);
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                arrive_warp(&bar.p_full, lane);
+                wait_on(smem_u32(&bar.dp_full), n & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                load_strip(tD + c0 + lanes, dp, any);
+                tc_fence_before();
+                arrive_warp(&bar.dp_free, lane);
+                if (any) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4) {
+                        const float4 d = *reinterpret_cast<const float4 *>(a.delta + c0 + c);
+                        out[c >> 1] = pack_bf16(s[c] * (dp[c] - d.x), s[c + 1] * (dp[c + 1] - d.y));
+                        out[(c >> 1) + 1] = pack_bf16(s[c + 2] * (dp[c + 2] - d.z), s[c + 3] * (dp[c + 3] - d.w));
+                    }
+                }
+                arrive_warp(&bar.aux_empty[n % x.stages], lane);
+                if (n > 0) wait_on(smem_u32(&bar.dk_done), (n - 1) & 1, guard, kErrTimeoutMma);
+                if (any) {
+                    tmem_st16(tDs + 32 * half + lanes, out);
+                    tmem_st16(tDs + 32 * half + 16 + lanes, out + 16);
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                arrive_warp(&bar.ds_full, lane);
+            }
+            // ---- warpgroup 0 stores dV, warpgroup 1 dK; rows behind the last key are 0
+            float o[64];
+            const bool some = w.u0 < w.u1 && j < w.len;
+            if (w.u0 < w.u1) {
+                wait_on(smem_u32(half ? &bar.dk_done : &bar.dv_done), (n - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                load_strip((half ? tDk : tDv) + lanes, o, true);
+                tc_fence_before();
+            }
+#pragma unroll
+            for (int c = 0; c < 64; ++c) o[c] = some ? o[c] : 0.f;
+            if (j < p.m) {
+                const size_t row = ((size_t)w.b * p.kv_heads + w.g) * p.m + j;
+                if (x.splits == 1) {
+                    store_row_bf16(static_cast<__nv_bfloat16 *>(half ? p.dK : p.dV) + row * p.d, o, half ? p.scale : 1.f,
+                                   p.d);
+                } else {
+                    float4 *out = reinterpret_cast<float4 *>(
+                        (half ? p.dk_part : p.dv_part) +
+                        ((size_t)w.split * ((size_t)p.B * p.kv_heads * p.m) + row) * p.d);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4)
+                        if (c < p.d) out[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// dK, dV from the parts of the queries, in order.
+__global__ void __launch_bounds__(256) join_dkdv(const __grid_constant__ Problem p) {
+    const size_t total = (size_t)p.B * p.kv_heads * p.m * p.d;
+    const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (at >= total) return;
+    const float *part = blockIdx.y ? p.dk_part : p.dv_part;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < p.q_splits; ++s) {
+        const float4 a = *reinterpret_cast<const float4 *>(part + s * total + at);
+        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+    }
+    const float mul = blockIdx.y ? p.scale : 1.f;
+    uint2 o;
+    o.x = pack_bf16(v.x * mul, v.y * mul);
+    o.y = pack_bf16(v.z * mul, v.w * mul);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(blockIdx.y ? p.dK : p.dV) + at) = o;
+}
+
+// --------------------------------------------------------------------- dbias
+struct DbBars {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t s_full, s_free, dp_full, dp_free;
+};
+
+template <int kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+    tc_dbias(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md,
+             const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+             const __grid_constant__ BwdParams x) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) DbBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    const Problem &p = x.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t ring = smem_u32(sm);   // stages of (Q, dO, K, V)
+    float *lut = reinterpret_cast<float *>(sm + x.off_lut);
+    uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_aux);
+    const Guard guard{x.err, &dead};
+
+    if (tid == 0) {
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(smem_u32(&bar.full[s]), 1);
+            mbar_init(smem_u32(&bar.empty[s]), 1);
+        }
+        mbar_init(smem_u32(&bar.s_full), 1);
+        mbar_init(smem_u32(&bar.dp_full), 1);
+        mbar_init(smem_u32(&bar.s_free), 8);
+        mbar_init(smem_u32(&bar.dp_free), 8);
+        dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 256);
+    if (kBias == 2)
+        for (int j = tid; j < p.m; j += kThreads) key_off[j] = (uint16_t)off_key(p.bias, j);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t tS = tmem, tD = tmem + 128;
+
+    struct Item {
+        int h, q0, j0, split, b0, b1;
+    };
+    auto item_of = [&](int it) {
+        Item w;
+        w.split = it % x.splits;
+        int r = it / x.splits;
+        w.j0 = (r % x.ktiles) * kRows;
+        r /= x.ktiles;
+        w.q0 = (r % x.qtiles) * kRows;
+        w.h = r / x.qtiles;
+        const int per = (p.B + x.splits - 1) / x.splits;
+        w.b0 = min(w.split * per, p.B);
+        w.b1 = min(w.b0 + per, p.B);
+        return w;
+    };
+
+    if (warp >= 8) set_regs_down<kRegsControl>();
+    if (warp >= 10) {
+        // idle: completes the control warps' group of four
+    } else if (warp == 9) {
+        if (lane == 0) {
+            int n = 0;
+            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+                const Item w = item_of(it);
+                for (int b = w.b0; b < w.b1; ++b) {
+                    if (w.j0 >= keys_of(p, b)) continue;
+                    const int s = n % x.stages;
+                    if (n >= x.stages) wait_on(smem_u32(&bar.empty[s]), ((n / x.stages) - 1) & 1, guard, kErrTimeoutMma);
+                    const uint32_t f = smem_u32(&bar.full[s]), at = ring + 4 * s * kTileBytes;
+                    mbar_arrive_expect_tx(f, 4 * kTileBytes);
+                    load_rows(at, &mq, x.uq, w.q0, w.h, b, f);
+                    load_rows(at + 2 * kTileBytes, &mk, x.uk, w.j0, w.h / p.group, b, f);
+                    load_rows(at + kTileBytes, &md, x.ud, w.q0, w.h, b, f);
+                    load_rows(at + 3 * kTileBytes, &mv, x.uv, w.j0, w.h / p.group, b, f);
+                    ++n;
+                }
+            }
+            for (int s = 0; s < x.stages; ++s) drain(&bar.empty[s], uses_of(n, s, x.stages), x.err);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        if (lane == 0) {
+            int n = 0;
+            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+                const Item w = item_of(it);
+                for (int b = w.b0; b < w.b1; ++b) {
+                    const int len = keys_of(p, b);
+                    if (w.j0 >= len) continue;
+                    const int s = n % x.stages, cols = tile_cols(min(kRows, len - w.j0));
+                    const uint32_t at = ring + 4 * s * kTileBytes;
+                    wait_on(smem_u32(&bar.full[s]), (n / x.stages) & 1, guard, kErrTimeoutLoad);
+                    if (n > 0) wait_on(smem_u32(&bar.s_free), (n - 1) & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_rows_rows(tS, at, at + 2 * kTileBytes, cols);
+                    tc_commit(smem_u32(&bar.s_full));
+                    if (n > 0) wait_on(smem_u32(&bar.dp_free), (n - 1) & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    mma_rows_rows(tD, at + kTileBytes, at + 3 * kTileBytes, cols);
+                    tc_commit(smem_u32(&bar.dp_full));
+                    tc_commit(smem_u32(&bar.empty[s]));
+                    ++n;
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        set_regs_up<kRegsMath>();
+        const int half = warp >> 2, wt = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const float scale2 = p.scale * kLog2e;
+        int n = 0, lut_head = -1;
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(it);
+            if (w.h != lut_head) {
+                math_barrier();
+                fill_offsets(p.bias, w.h, kLog2e, lut, tid, 256);
+                math_barrier();
+                lut_head = w.h;
+            }
+            const int i = w.q0 + wt, j0 = w.j0 + 64 * half;
+            const bool in = i < p.n;
+            const int oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, p.bias.start);
+            const int oq_lo = off_query(p.bias, i - lane, p.bias.start);
+            float acc[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) acc[c] = 0.f;
+            for (int b = w.b0; b < w.b1; ++b) {
+                const int len = keys_of(p, b);
+                if (w.j0 >= len) continue;
+                const int keys = min(64, len - j0);
+                const bool any = keys > 0;
+                const size_t row = ((size_t)b * p.heads + w.h) * p.n + i;
+                const float nl = neg_lse2(p.lse, row, in), delta = in ? p.delta[row] : 0.f;
+                float s[64];
+                wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                load_strip(tS + 64 * half + lanes, s, any);
+                tc_fence_before();
+                arrive_warp(&bar.s_free, lane);
+                if (any) row_weights<kBias>(s, p.bias, lut, key_off, j0, keys, oq, oq_lo, scale2, nl);
+                wait_on(smem_u32(&bar.dp_full), n & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    float dp[32];
+                    if (any) {
+                        tmem_ld32_nowait(tD + 64 * half + c + lanes, dp);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c + e < keys) acc[c + e] = fmaf(s[c + e], dp[e] - delta, acc[c + e]);
+                    }
+                }
+                tc_fence_before();
+                arrive_warp(&bar.dp_free, lane);
+                ++n;
+            }
+            if (in) {
+                float *out = p.dbias + ((size_t)w.split * p.heads + w.h) * ((size_t)p.n * p.m) + (size_t)i * p.m + j0;
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (j0 + c < p.m) out[c] = acc[c];
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 256);
+}
+
+struct Maps {
+    CUtensorMap q, d, k, v;
+};
+bool fill_maps(Maps &m, BwdParams &x, const Problem &p) {
+    x.p = p;
+    x.qtiles = (p.n + kRows - 1) / kRows;
+    x.ktiles = (p.m + kRows - 1) / kRows;
+    return make_map(&m.q, &x.uq, p.Q, p.B, p.heads, p.n, p.d) && make_map(&m.d, &x.ud, p.dO, p.B, p.heads, p.n, p.d) &&
+           make_map(&m.k, &x.uk, p.K, p.B, p.kv_heads, p.m, p.d) &&
+           make_map(&m.v, &x.uv, p.V, p.B, p.kv_heads, p.m, p.d);
+}
+
+template <auto kKernel>
+cudaError_t go(const Maps &m, const BwdParams &x, int bytes, cudaStream_t s) {
+    cudaError_t e = allow_smem<kKernel>();
+    if (e != cudaSuccess) return e;
+    kKernel<<<(unsigned)std::min(x.items, sms()), kThreads, bytes, s>>>(m.q, m.d, m.k, m.v, x);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int tc_dkdv_splits(int B, int kv_heads, int group, int n, int m) {
+    const long long items = (long long)B * kv_heads * ((m + kRows - 1) / kRows);
+    const long long steps = (long long)group * ((n + kRows - 1) / kRows);
+    // fewer items than SMs: share the queries out, at least two tiles to each part
+    if (items >= 152 || steps < 4) return 1;
+    return (int)std::min<long long>((152 + items - 1) / items, steps / 2);
+}
+
+int tc_dbias_splits(int B, int heads, int n, int m) {
+    const long long items = (long long)heads * ((n + kRows - 1) / kRows) * ((m + kRows - 1) / kRows);
+    if (items >= 152 || B < 4) return 1;
+    return (int)std::min<long long>((152 + items - 1) / items, B / 2);
+}
+
+cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
+    Maps m;
+    BwdParams x{};
+    if (!fill_maps(m, x, p)) return cudaErrorInvalidValue;
+    x.err = err;
+    const int lut = p.bias.mode ? round1k(p.bias.entries * 4) : 0;
+    const int keys = p.bias.mode == 2 ? round1k((p.m + 127) / 128 * 256) : 0;
+    cudaError_t e;
+    // ---- dQ and delta
+    long long items = (long long)p.B * p.heads * x.qtiles;
+    if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
+    x.items = (int)items;
+    x.first = 1;
+    x.stages = std::min(kMaxStages, (kSmemBudget - 4 * kTileBytes - lut - keys - 1024) / (2 * kTileBytes));
+    if (x.stages < 2) return cudaErrorInvalidValue;   // a K tile is held until its dQ product, behind the next scores
+    x.off_lut = (4 + 2 * x.stages) * kTileBytes;
+    x.off_aux = x.off_lut + lut;
+    int bytes = x.off_aux + keys + 1024;
+    e = p.bias.mode == 0   ? go<tc_dq<0>>(m, x, bytes, s)
+        : p.bias.mode == 1 ? go<tc_dq<1>>(m, x, bytes, s)
+                           : go<tc_dq<2>>(m, x, bytes, s);
+    if (e != cudaSuccess) return e;
+    // ---- dK, dV
+    items = (long long)p.B * p.kv_heads * x.ktiles * p.q_splits;
+    if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
+    x.items = (int)items;
+    x.first = 0;
+    x.splits = p.q_splits;
+    const int aux = (int)sizeof(QueryAux);
+    x.stages = std::min(kMaxStages, (kSmemBudget - 2 * kTileBytes - lut - 1024) / (2 * kTileBytes + aux));
+    if (x.stages < 2) return cudaErrorInvalidValue;
+    x.off_lut = (2 + 2 * x.stages) * kTileBytes;
+    x.off_aux = x.off_lut + lut;
+    bytes = x.off_aux + x.stages * aux + 1024;
+    e = p.bias.mode == 0   ? go<tc_dkdv<0>>(m, x, bytes, s)
+        : p.bias.mode == 1 ? go<tc_dkdv<1>>(m, x, bytes, s)
+                           : go<tc_dkdv<2>>(m, x, bytes, s);
+    if (e != cudaSuccess) return e;
+    if (p.q_splits > 1) {
+        const size_t vecs = (size_t)p.B * p.kv_heads * p.m * (p.d / 4);
+        join_dkdv<<<dim3((unsigned)((vecs + 255) / 256), 2), 256, 0, s>>>(p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (p.bias.mode == 0) return cudaSuccess;
+    // ---- dS of the batch
+    items = (long long)p.heads * x.qtiles * x.ktiles * p.b_splits;
+    if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
+    x.items = (int)items;
+    x.splits = p.b_splits;
+    x.stages = std::min(kMaxStages, (kSmemBudget - lut - keys - 1024) / (4 * kTileBytes));
+    if (x.stages < 1) return cudaErrorInvalidValue;
+    x.off_lut = 4 * x.stages * kTileBytes;
+    x.off_aux = x.off_lut + lut;
+    bytes = x.off_aux + keys + 1024;
+    return p.bias.mode == 1 ? go<tc_dbias<1>>(m, x, bytes, s) : go<tc_dbias<2>>(m, x, bytes, s);
+}
+
+}  // namespace attn
+}  // namespace lisa

@@ -78,6 +78,7 @@ struct GradParams {
     int residues, ch, nchunk, etot, ntile, threads;
     int row_buckets, col_buckets;
     long long n, m;
+    int parts;     // matrices [heads][n][m] one behind the other, added up
     float *part;   // [heads][q_rows][k_rows][nchunk][ntile][col_buckets]
 };
 
@@ -94,7 +95,8 @@ __global__ void __launch_bounds__(256) bias_grad_part(const __grid_constant__ Gr
     const int flat = tile * g.threads + t;
     const int r = flat / g.etot, e = q0 + flat % g.etot;
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-    if (r < g.residues) {
+    for (int part = 0; part < g.parts; ++part, dbias += (size_t)g.b.heads * g.n * g.m) {
+        if (r >= g.residues) break;
         const int nr = (g.q_cols - 1 - r) / g.step_c + 1;
         int q = max(q0, e - g.k_cols + 1);
         const int q1 = min(min(q0 + g.ch, nr), e + 1);
@@ -225,10 +227,11 @@ size_t bias_grad_bytes(const lisa_rel_bias &b, int heads) {
     return (size_t)heads * g.q_rows * g.k_rows * g.nchunk * g.ntile * g.col_buckets * sizeof(float);
 }
 
-cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int dtype, float *dtable,
-                             void *ws, cudaStream_t s) {
+cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int parts, int dtype,
+                             float *dtable, void *ws, cudaStream_t s) {
     GradParams g{};
     g.b = dev;
+    g.parts = parts;
     grad_plan(b, g);
     g.part = static_cast<float *>(ws);
     dim3 grid((unsigned)(g.nchunk * g.ntile), (unsigned)(g.q_rows * g.k_rows), (unsigned)dev.heads);

@@ -12,10 +12,13 @@ operands add r per rounded operand.  Every bound below is that first-order sum,
 taken 1.05 times for the second order.
 
   s     Es = u (d + 8) (scale |q|.|k| + |b|)
-  p     Ep = p (Es + max_j Es + u (m + 8) + 8 u |s - lse|)
+  p     Ep = p (Es + max_j Es + u (m + 8) + 8 u |s - lse|) + f
+        f = 2^-126: 2^x (and a product) below the smallest normal fp32 number is
+        flushed to 0, an error of up to f in p whatever p is; through dP, q and k
+        it reaches the gradients times their size (some hundreds here) and n terms
   o     Eo = sum_j (Ep + (r + m u) p) |v| + r |o|
   dP    u (d + 2) |dO|.|v|
-  dS    EdS = Ep |dP - delta| + p (EdP + Edelta + 4 u (|dP| + |delta|))
+  dS    EdS = Ep |dP - delta| + p (EdP + Edelta + 4 u (|dP| + |delta|)) + f
         Edelta = |dO|.Eo + u (d + 2) |dO|.|o|   (delta from the rounded output)
         or, where it is summed in fp32, sum_j (Ep + m u p) |dP| + p EdP
   dQ    scale sum_j (EdS + (r + m u) |dS|) |k| + r |dQ|      dK likewise over i
@@ -28,6 +31,7 @@ import torch
 
 U = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -22}
 R = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+F = 2.0 ** -126       # smallest normal fp32 number
 EX2 = 2.0 ** -22      # relative error of the special-function unit's 2^x, in either data type
 
 
@@ -103,7 +107,7 @@ def attention(q, k, v, dout=None, *, scale, lens=None, table=None, index=None, d
             Es = u * (d + 8) * mag
             Esm = Es.amax(1)
             far = torch.where(p > 0, (s - torch.where(some, l, 0.0)[:, None]).abs(), 0.0)
-            Ep = p * (Es + Esm[:, None] + u * (L + 8) + EX2 * 8 + 8 * u * far + 8 * 2.0 ** -24 * l.abs().clamp(max=1e30)[:, None])
+            Ep = p * (Es + Esm[:, None] + u * (L + 8) + EX2 * 8 + 8 * u * far + 8 * 2.0 ** -24 * l.abs().clamp(max=1e30)[:, None]) + F
             o[b, j] = p @ vv
             Eo[b, j] = (Ep + (r + L * u) * p) @ vv.abs() + r * o[b, j].abs()
             lse[b, j] = l
@@ -117,7 +121,7 @@ def attention(q, k, v, dout=None, *, scale, lens=None, table=None, index=None, d
             rounded = (do.abs() * Eo[b, j]).sum(1, keepdim=True) + u * (d + 2) * (do * o[b, j]).abs().sum(1, keepdim=True)
             summed = ((Ep + L * u * p) * dp.abs() + p * Edp).sum(1, keepdim=True)
             ds = p * (dp - delta)
-            common = Ep * (dp - delta).abs() + p * (Edp + 4 * u * (dp.abs() + delta.abs()))
+            common = Ep * (dp - delta).abs() + p * (Edp + 4 * u * (dp.abs() + delta.abs())) + F
             Eds, Edx = common + p * torch.maximum(rounded, summed), common + p * summed
             dq[b, j] = scale * ds @ kk
             Edq[b, j] = scale * (Eds + (r + L * u) * ds.abs()) @ kk.abs() + r * dq[b, j].abs()
