@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
           const __grid_constant__ BwdParams x) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // stays a shared-memory pointer
     __shared__ __align__(8) DqBars bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
             const __grid_constant__ BwdParams x) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // stays a shared-memory pointer
     __shared__ __align__(8) DkvBars bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
              const __grid_constant__ BwdParams x) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // stays a shared-memory pointer
     __shared__ __align__(8) DbBars bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;

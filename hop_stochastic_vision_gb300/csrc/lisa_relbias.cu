@@ -150,7 +150,9 @@ __global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ Gr
     float acc = 0.f;
     if (cb < g.col_buckets) {
         const size_t row = (size_t)g.col_buckets;
-        for (int rq = 0; rq < g.q_rows; ++rq) {
+        // the runs share out the rows of the query grid, or a sequence's items
+        const int by_row = g.q_rows > 1;
+        for (int rq = by_row ? grp : 0; rq < g.q_rows; rq += by_row ? groups : 1) {
             // row offset step_r rk - rq - start_r in [lo, hi]
             const long long base = (long long)rq + g.start_r;
             const long long x0 = lo + base, x1 = hi + base;
@@ -158,14 +160,14 @@ __global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ Gr
             const int k1 = x1 < 0 ? -1 : (int)min(x1 / g.step_r, (long long)g.k_rows - 1);
             if (k1 < k0) continue;
             const float *p = g.part + (((size_t)h * g.q_rows + rq) * g.k_rows + k0) * per * row + cb;
-            const int items = (k1 - k0 + 1) * per;
-            int it = grp;
+            const int items = (k1 - k0 + 1) * per, by = by_row ? 1 : groups;
+            int it = by_row ? 0 : grp;
             float a[4] = {0.f, 0.f, 0.f, 0.f};
-            for (; it + 3 * groups < items; it += 4 * groups) {
+            for (; it + 3 * by < items; it += 4 * by) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) a[u] += p[(size_t)(it + u * groups) * row];
+                for (int u = 0; u < 4; ++u) a[u] += p[(size_t)(it + u * by) * row];
             }
-            for (; it < items; it += groups) a[0] += p[(size_t)it * row];
+            for (; it < items; it += by) a[0] += p[(size_t)it * row];
             acc += (a[0] + a[1]) + (a[2] + a[3]);
         }
     }
