@@ -15,6 +15,8 @@
 // when a tile's maximum passes the reference by more, which after the first
 // tile is rare, so the accumulator stays in tensor memory.  exp is 2^x with
 // log2(e) folded into the scale and into the bias table.
+#include <type_traits>
+
 #include "lisa_attn_tc.cuh"
 
 namespace lisa {
@@ -64,6 +66,60 @@ __device__ __forceinline__ Item item_of(const FwdParams &x, int it) {
 // Valid keys of tile `t`, and the columns its products cover.
 __device__ __forceinline__ int tile_keys(int len, int t) { return min(kRows, len - t * kRows); }
 __device__ __forceinline__ int tile_cols(int keys) { return (keys + 15) & ~15; }
+
+// A row's state over the tiles of an item, and what its bias needs.
+struct RowState {
+    float ref, sum;
+    int oq, oq_lo;
+};
+
+// Bias of 128 columns from key j0: s -> scale2 s + bias, or one value for all of
+// them (the return value's use: 2^(mul s + add)).
+template <int kBias, bool kFull>
+__device__ __forceinline__ void add_bias(float (&s)[128], const BiasDev &b, const float *lut, const uint16_t *key_off,
+                                         int j0, int keys, int cols, const RowState &r, float scale2, float &mul,
+                                         float &add) {
+    mul = scale2;
+    add = 0.f;
+    if (kBias == 1) {
+        const int lo = b.step_c * j0 - r.oq_lo - 31, hi = b.step_c * (j0 + keys - 1) - r.oq_lo, last = b.entries - 1;
+        if (hi <= 0 || lo >= last) {          // the whole tile in one outermost bucket
+            add = lut[hi <= 0 ? 0 : last];
+        } else {
+            const int off = b.step_c * j0 - r.oq;
+            mul = 1.f;
+            if (b.step_c == 1 && lo >= 0 && lo + 31 + 127 <= last) {
+                const float *l = lut + off;
+#pragma unroll
+                for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], scale2, l[c]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], scale2, lut[min(max(off + b.step_c * c, 0), last)]);
+            }
+        }
+    } else if (kBias == 2) {
+        // inside the table by construction; columns behind the last key are clamped into it
+        mul = 1.f;
+        const float *l = lut - r.oq;
+        const int top = b.entries - 1 + r.oq;
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+            if (!kFull && (c & ~31) >= cols) break;
+            const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
+            int i0 = (int)(a.x & 0xFFFFu), i1 = (int)(a.x >> 16), i2 = (int)(a.y & 0xFFFFu), i3 = (int)(a.y >> 16);
+            if (!kFull) {
+                i0 = min(max(i0, r.oq), top);
+                i1 = min(max(i1, r.oq), top);
+                i2 = min(max(i2, r.oq), top);
+                i3 = min(max(i3, r.oq), top);
+            }
+            s[c] = fmaf(s[c], scale2, l[i0]);
+            s[c + 1] = fmaf(s[c + 1], scale2, l[i1]);
+            s[c + 2] = fmaf(s[c + 2], scale2, l[i2]);
+            s[c + 3] = fmaf(s[c + 3], scale2, l[i3]);
+        }
+    }
+}
 
 template <int kBias>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -217,82 +273,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 continue;
             }
             const int i = w.q0 + t * kRows + wt;
-            int oq = 0, oq_lo = 0, oq_hi = 0;
+            RowState r{-INFINITY, 0.f, 0, 0};
             if (kBias) {
                 const int start = bias_start(p.bias, w.b);
-                oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start);
-                oq_lo = off_query(p.bias, i - lane, start);        // sequence: the warp's first and last row
-                oq_hi = oq_lo + 31;
+                r.oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start);
+                r.oq_lo = off_query(p.bias, i - lane, start);   // sequence: the warp's first row
             }
-            float ref = -INFINITY, sum = 0.f;
-            for (int j = w.t0; j < w.t1; ++j, ++kt) {
-                const int keys = tile_keys(w.len, j), cols = tile_cols(keys), j0 = j * kRows;
+            auto tile = [&](int j, auto full) __attribute__((always_inline)) {
+                constexpr bool kFull = decltype(full)::value;
+                const int keys = kFull ? kRows : tile_keys(w.len, j), cols = kFull ? kRows : tile_cols(keys), j0 = j * kRows;
                 float s[128];
                 wait_on(smem_u32(&bar.s_full[t]), ns & 1, guard, kErrTimeoutMma);
                 ++ns;
                 tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < 128; c += 32)
-                    if (c < cols) tmem_ld32_nowait(s_tm + c, s + c);
+                tmem_ld32_nowait(s_tm, s);
+                tmem_ld32_nowait(s_tm + 32, s + 32);
+                tmem_ld32_nowait(s_tm + 64, s + 64);
+                tmem_ld32_nowait(s_tm + 96, s + 96);
                 tc_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar.s_free[t]));
 
-                float mul = scale2, add = 0.f;   // 2^(mul s + add - ref) is the weight
-                if (kBias == 1) {
-                    const int lo = p.bias.step_c * j0 - oq_hi, hi = p.bias.step_c * (j0 + keys - 1) - oq_lo;
-                    const int last = p.bias.entries - 1;
-                    if (hi <= 0 || lo >= last) {          // the whole tile in one outermost bucket
-                        add = lut[hi <= 0 ? 0 : last];
-                    } else {
-                        const int off = p.bias.step_c * j0 - oq;
-                        mul = 1.f;
-                        if (p.bias.step_c == 1 && lo >= 0 && lo + 31 + 127 + 31 <= last) {
-                            const float *l = lut + off;
-#pragma unroll
-                            for (int c = 0; c < 128; ++c)
-                                if ((c & ~31) < cols) s[c] = fmaf(s[c], scale2, l[c]);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 128; ++c)
-                                if ((c & ~31) < cols)
-                                    s[c] = fmaf(s[c], scale2, lut[min(max(off + p.bias.step_c * c, 0), last)]);
-                        }
-                    }
-                } else if (kBias == 2) {
-                    mul = 1.f;
-#pragma unroll
-                    for (int c = 0; c < 128; c += 4)
-                        if ((c & ~31) < cols) {
-                            const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
-                            s[c] = fmaf(s[c], scale2, lut[min(max((int)(a.x & 0xFFFFu) - oq, 0), p.bias.entries - 1)]);
-                            s[c + 1] = fmaf(s[c + 1], scale2, lut[min(max((int)(a.x >> 16) - oq, 0), p.bias.entries - 1)]);
-                            s[c + 2] = fmaf(s[c + 2], scale2, lut[min(max((int)(a.y & 0xFFFFu) - oq, 0), p.bias.entries - 1)]);
-                            s[c + 3] = fmaf(s[c + 3], scale2, lut[min(max((int)(a.y >> 16) - oq, 0), p.bias.entries - 1)]);
-                        }
-                }
-                if (keys < kRows) {
+                float mul, add;   // 2^(mul s + add - ref) is the weight
+                add_bias<kBias, kFull>(s, p.bias, lut, key_off, j0, keys, cols, r, scale2, mul, add);
+                if (!kFull) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
                         if (c >= keys) s[c] = -INFINITY;
                 }
                 float top;
                 {
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if ((c & ~31) < cols) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
+                    for (int c = 4; c < 128; c += 8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            m4[e] = c + e + 4 < 128 ? fmaxf(fmaxf(m4[e], s[c + e]), s[c + e + 4]) : fmaxf(m4[e], s[c + e]);
+                    }
                     top = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul, add);
                 }
                 const bool first = j == w.t0;
                 if (first) {
-                    ref = top;
-                } else if (__any_sync(0xFFFFFFFFu, top > ref + kSlack)) {
-                    const float now = fmaxf(ref, top);
-                    const float f = ref == -INFINITY ? 0.f : ex2_approx(ref - now);
-                    ref = now;
-                    sum *= f;
+                    r.ref = top;
+                } else if (__any_sync(0xFFFFFFFFu, top > r.ref + kSlack)) {
+                    const float now = fmaxf(r.ref, top);
+                    const float f = r.ref == -INFINITY ? 0.f : ex2_approx(r.ref - now);
+                    r.ref = now;
+                    r.sum *= f;
                     wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
                     float o[32];
@@ -306,26 +334,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     }
                     tc_wait_st();
                 }
-                const float shift = add - (ref == -INFINITY ? 0.f : ref);   // a row of -inf so far: weights 0, not NaN
+                const float shift = add - (r.ref == -INFINITY ? 0.f : r.ref);   // a row of -inf so far: weights 0, not NaN
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
                 // the previous weights have been read (and their products are in O)
                 if (!first) wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
 #pragma unroll
                 for (int c = 0; c < 128; c += 32)
-                    if (c < cols) {
+                    if (kFull || c < cols) {
                         uint32_t w16[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float a = ex2_approx(fmaf(s[c + e], mul, shift));
-                            const float b = ex2_approx(fmaf(s[c + e + 1], mul, shift));
-                            part[e & 2] += a;
-                            part[(e & 2) + 1] += b;
+                            float a, b;
+                            fma2(a, b, s[c + e], s[c + e + 1], mul, mul, shift, shift);
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                            add2(part[e & 2], part[(e & 2) + 1], part[e & 2], part[(e & 2) + 1], a, b);
                             w16[e >> 1] = pack_bf16(a, b);
                         }
                         tmem_st16(p_tm + c / 2, w16);
                     }
-                sum += (part[0] + part[1]) + (part[2] + part[3]);
-                if (t == 0 && keys < cols && w.len < p.m) {
+                r.sum += (part[0] + part[1]) + (part[2] + part[3]);
+                if (!kFull && t == 0 && keys < cols && w.len < p.m) {
                     // values behind the last key: whatever stands there times a weight of 0 has to be 0
                     const int st = kt % x.stages;
                     wait_on(smem_u32(&bar.v_full[st]), (kt / x.stages) & 1, guard, kErrTimeoutLoad);
@@ -337,7 +366,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar.p_full[t]));
                 ++np;
+                ++kt;
+            };
+            for (int j = w.t0; j < w.t1; ++j) {
+                if (tile_keys(w.len, j) == kRows)
+                    tile(j, std::true_type{});
+                else
+                    tile(j, std::false_type{});
             }
+            const float ref = r.ref, sum = r.sum;
             // ------------------------------------------------------ output
             float o[64];
             if (w.t0 < w.t1) {

@@ -89,6 +89,27 @@ __device__ __forceinline__ void set_regs_down() {
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two fp32 operations in one instruction, on neighbouring registers.
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float c, float d, float e, float f) {
+    // (x, y) = (a, b) * (c, d) + (e, f)
+    asm("{\n.reg .b64 p, q, r;\nmov.b64 p, {%2, %3};\nmov.b64 q, {%4, %5};\nmov.b64 r, {%6, %7};\n"
+        "fma.rn.f32x2 p, p, q, r;\nmov.b64 {%0, %1}, p;\n}"
+        : "=f"(x), "=f"(y)
+        : "f"(a), "f"(b), "f"(c), "f"(d), "f"(e), "f"(f));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b, float c, float d) {
+    asm("{\n.reg .b64 p, q;\nmov.b64 p, {%2, %3};\nmov.b64 q, {%4, %5};\n"
+        "add.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}"
+        : "=f"(x), "=f"(y)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+__device__ __forceinline__ void mul2(float &x, float &y, float a, float b, float c, float d) {
+    asm("{\n.reg .b64 p, q;\nmov.b64 p, {%2, %3};\nmov.b64 q, {%4, %5};\n"
+        "mul.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}"
+        : "=f"(x), "=f"(y)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]: A's rows are the 128 lanes, two bf16 of a row per 32-bit column.
 __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {

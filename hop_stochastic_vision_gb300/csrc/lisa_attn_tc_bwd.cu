@@ -55,14 +55,14 @@ __device__ __forceinline__ void row_weights(float (&s)[64], const BiasDev &b, co
                                             int j0, int keys, int oq, int oq_lo, float scale2, float nl) {
     if (kBias == 0) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, nl);
+        for (int c = 0; c < 64; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, nl, nl);
     } else if (kBias == 1) {
         const int oq_hi = oq_lo + 31, last = b.entries - 1;
         const int lo = b.step_c * j0 - oq_hi, hi = b.step_c * (j0 + max(keys, 1) - 1) - oq_lo;
         if (hi <= 0 || lo >= last) {
             const float add = nl + lut[hi <= 0 ? 0 : last];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, add);
+            for (int c = 0; c < 64; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, add, add);
         } else {
             const int off = b.step_c * j0 - oq;
             if (b.step_c == 1 && lo >= 0 && lo + 31 + 63 <= last) {
@@ -95,13 +95,11 @@ __device__ __forceinline__ void row_weights(float (&s)[64], const BiasDev &b, co
     for (int c = 0; c < 64; ++c) s[c] = ex2_approx(s[c]);
 }
 
-// Two 32-column halves of a 64-column strip; a strip that the products did not
-// reach (`any` false) is not read.
-__device__ __forceinline__ void load_strip(uint32_t taddr, float (&v)[64], bool any) {
-    if (any) {
-        tmem_ld32_nowait(taddr, v);
-        tmem_ld32_nowait(taddr + 32, v + 32);
-    }
+// A 64-column strip.  Columns that the products did not reach hold whatever was
+// there before and are not used (a load under a condition costs copies of all 64).
+__device__ __forceinline__ void load_strip(uint32_t taddr, float (&v)[64]) {
+    tmem_ld32_nowait(taddr, v);
+    tmem_ld32_nowait(taddr + 32, v + 32);
     tc_wait_ld();
 }
 
@@ -312,39 +310,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < w.tiles; ++j, ++kt) {
                 const int keys = tile_keys(w.len, j), cols = tile_cols(keys), j0 = j * kRows + 64 * half;
                 const bool any = 64 * half < cols;
-                float s[64], dp[64];
+                float s[64];
                 wait_on(smem_u32(&bar.s_full), kt & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip(tS + 64 * half + lanes, s, any);
+                load_strip(tS + 64 * half + lanes, s);
                 tc_fence_before();
                 arrive_warp(&bar.s_free, lane);
                 if (any) row_weights<kBias>(s, p.bias, lut, key_off, j0, keys - 64 * half, oq, oq_lo, scale2, nl);
                 wait_on(smem_u32(&bar.dp_full), kt & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                load_strip(tP + 64 * half + lanes, dp, any);
-                tc_fence_before();
-                arrive_warp(&bar.dp_free, lane);
                 // the previous dS has been read; every warp sees every phase, with a strip of its own or not
                 if (kt > 0) wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
-                if (any) {
-                    if (keys - 64 * half < 64) {   // dP of keys behind the last one holds whatever their values hold
+                tc_fence_after();
+                float e0 = 0.f, e1 = 0.f;
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (c >= keys - 64 * half) dp[c] = 0.f;
+                for (int c = 0; c < 64; c += 32) {
+                    float dp[32];
+                    uint32_t ds[16];
+                    tmem_ld32_nowait(tP + 64 * half + c + lanes, dp);
+                    tc_wait_ld();
+                    if (c == 32) {
+                        tc_fence_before();
+                        arrive_warp(&bar.dp_free, lane);
                     }
-                    uint32_t ds[32];
-                    float e0 = 0.f, e1 = 0.f;
+                    if (any) {
+                        if (keys - 64 * half < 64) {   // dP of keys behind the last one holds whatever their values hold
 #pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
-                        const float a = s[c] * dp[c], b = s[c + 1] * dp[c + 1];
-                        e0 += a;
-                        e1 += b;
-                        ds[c >> 1] = pack_bf16(fmaf(-s[c], delta, a), fmaf(-s[c + 1], delta, b));
+                            for (int e = 0; e < 32; ++e)
+                                if (c + e >= keys - 64 * half) dp[e] = 0.f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float u, v;
+                            mul2(dp[e], dp[e + 1], s[c + e], s[c + e + 1], dp[e], dp[e + 1]);
+                            add2(e0, e1, e0, e1, dp[e], dp[e + 1]);
+                            fma2(u, v, s[c + e], s[c + e + 1], -delta, -delta, dp[e], dp[e + 1]);
+                            ds[e >> 1] = pack_bf16(u, v);
+                        }
+                        tmem_st16(tDs + 32 * half + c / 2 + lanes, ds);
                     }
-                    exact += e0 + e1;
-                    tmem_st16(tDs + 32 * half + lanes, ds);
-                    tmem_st16(tDs + 32 * half + 16 + lanes, ds + 16);
                 }
+                exact += e0 + e1;
                 if (half == 0 && keys < cols && w.len < p.m) {
                     // S is done with the tile: what stands behind the last key may not meet dS = 0
                     zero_rows(ring + 2 * (kt % x.stages) * kTileBytes, keys, cols, wt);
@@ -400,7 +405,7 @@ struct DkvBars {
 
 // What the arithmetic needs of a tile's queries, one entry per column.
 struct QueryAux {
-    float nl[kRows], delta[kRows];
+    float nl[kRows], minus_delta[kRows];
     int oq[kRows];
 };
 
@@ -488,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int i = q0 + e;
                     const bool in = i < p.n;
                     aux[s].nl[e] = neg_lse2(p.lse, row0 + i, in);
-                    aux[s].delta[e] = in ? p.delta[row0 + i] : 0.f;
+                    aux[s].minus_delta[e] = in ? -p.delta[row0 + i] : 0.f;
                     if (kBias) aux[s].oq[e] = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start);
                 }
                 arrive_warp(&bar.aux_full[s], lane);
@@ -594,14 +599,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool any = 64 * half < cols;
                 const QueryAux &a = aux[n % x.stages];
                 const int c0 = 64 * half;
-                float s[64], dp[64];
+                float s[64];
                 wait_on(smem_u32(&bar.aux_full[n % x.stages]), (n / x.stages) & 1, guard, kErrTimeoutLoad);
                 wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip(tS + c0 + lanes, s, any);
+                load_strip(tS + c0 + lanes, s);
                 tc_fence_before();
                 arrive_warp(&bar.s_free, lane);
-                uint32_t out[32];
                 if (any) {
                     if (kBias == 1) {
                         const int last = p.bias.entries - 1;
@@ -611,7 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (off_hi <= 0 || off_lo - 63 >= last) {
                             const float add = lut[off_hi <= 0 ? 0 : last];
 #pragma unroll
-                            for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, add + a.nl[c0 + c]);
+                            for (int c = 0; c < 64; c += 4) {
+                                const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
+                                fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, l.x, l.y);
+                                fma2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], scale2, scale2, l.z, l.w);
+                                add2(s[c], s[c + 1], s[c], s[c + 1], add, add);
+                                add2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], add, add);
+                            }
                         } else if (off_lo - 63 >= 0 && off_hi <= last) {
                             const float *l = lut + off;
 #pragma unroll
@@ -636,48 +646,58 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 64; c += 4) {
                             const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
-                            s[c] = fmaf(s[c], scale2, l.x);
-                            s[c + 1] = fmaf(s[c + 1], scale2, l.y);
-                            s[c + 2] = fmaf(s[c + 2], scale2, l.z);
-                            s[c + 3] = fmaf(s[c + 3], scale2, l.w);
+                            fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, l.x, l.y);
+                            fma2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], scale2, scale2, l.z, l.w);
                         }
-                    }
-#pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
-                        s[c] = ex2_approx(s[c]);
-                        s[c + 1] = ex2_approx(s[c + 1]);
-                        out[c >> 1] = pack_bf16(s[c], s[c + 1]);
                     }
                 }
                 // the previous P has been read; every warp sees every phase, with a strip of its own or not
                 if (n > 0) wait_on(smem_u32(&bar.dv_done), (n - 1) & 1, guard, kErrTimeoutMma);
                 if (any) {
-                    tmem_st16(tPw + 32 * half + lanes, out);
-                    tmem_st16(tPw + 32 * half + 16 + lanes, out + 16);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t out[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            s[c + e] = ex2_approx(s[c + e]);
+                            s[c + e + 1] = ex2_approx(s[c + e + 1]);
+                            out[e >> 1] = pack_bf16(s[c + e], s[c + e + 1]);
+                        }
+                        tmem_st16(tPw + 32 * half + c / 2 + lanes, out);
+                    }
                     tc_wait_st();
                 }
                 tc_fence_before();
                 arrive_warp(&bar.p_full, lane);
                 wait_on(smem_u32(&bar.dp_full), n & 1, guard, kErrTimeoutMma);
+                if (n > 0) wait_on(smem_u32(&bar.dk_done), (n - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip(tD + c0 + lanes, dp, any);
-                tc_fence_before();
-                arrive_warp(&bar.dp_free, lane);
-                if (any) {
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
-                        const float4 d = *reinterpret_cast<const float4 *>(a.delta + c0 + c);
-                        out[c >> 1] = pack_bf16(s[c] * (dp[c] - d.x), s[c + 1] * (dp[c + 1] - d.y));
-                        out[(c >> 1) + 1] = pack_bf16(s[c + 2] * (dp[c + 2] - d.z), s[c + 3] * (dp[c + 3] - d.w));
+                for (int c = 0; c < 64; c += 32) {
+                    float dp[32];
+                    uint32_t out[16];
+                    tmem_ld32_nowait(tD + c0 + c + lanes, dp);
+                    tc_wait_ld();
+                    if (c == 32) {
+                        tc_fence_before();
+                        arrive_warp(&bar.dp_free, lane);
+                    }
+                    if (any) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 d = *reinterpret_cast<const float4 *>(a.minus_delta + c0 + c + e);
+                            add2(dp[e], dp[e + 1], dp[e], dp[e + 1], d.x, d.y);
+                            add2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], d.z, d.w);
+                            mul2(dp[e], dp[e + 1], dp[e], dp[e + 1], s[c + e], s[c + e + 1]);
+                            mul2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], s[c + e + 2], s[c + e + 3]);
+                            out[e >> 1] = pack_bf16(dp[e], dp[e + 1]);
+                            out[(e >> 1) + 1] = pack_bf16(dp[e + 2], dp[e + 3]);
+                        }
+                        tmem_st16(tDs + 32 * half + c / 2 + lanes, out);
                     }
                 }
                 arrive_warp(&bar.aux_empty[n % x.stages], lane);
-                if (n > 0) wait_on(smem_u32(&bar.dk_done), (n - 1) & 1, guard, kErrTimeoutMma);
-                if (any) {
-                    tmem_st16(tDs + 32 * half + lanes, out);
-                    tmem_st16(tDs + 32 * half + 16 + lanes, out + 16);
-                    tc_wait_st();
-                }
+                tc_wait_st();
                 tc_fence_before();
                 arrive_warp(&bar.ds_full, lane);
             }
@@ -687,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w.u0 < w.u1) {
                 wait_on(smem_u32(half ? &bar.dk_done : &bar.dv_done), (n - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip((half ? tDk : tDv) + lanes, o, true);
+                load_strip((half ? tDk : tDv) + lanes, o);
                 tc_fence_before();
             }
 #pragma unroll
@@ -873,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s[64];
                 wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip(tS + 64 * half + lanes, s, any);
+                load_strip(tS + 64 * half + lanes, s);
                 tc_fence_before();
                 arrive_warp(&bar.s_free, lane);
                 if (any) row_weights<kBias>(s, p.bias, lut, key_off, j0, keys, oq, oq_lo, scale2, nl);
@@ -882,12 +902,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
                     float dp[32];
+                    tmem_ld32_nowait(tD + 64 * half + c + lanes, dp);
+                    tc_wait_ld();
                     if (any) {
-                        tmem_ld32_nowait(tD + 64 * half + c + lanes, dp);
-                        tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (c + e < keys) acc[c + e] = fmaf(s[c + e], dp[e] - delta, acc[c + e]);
+                        for (int e = 0; e < 32; e += 2) {
+                            add2(dp[e], dp[e + 1], dp[e], dp[e + 1], -delta, -delta);
+                            if (c + e >= keys) dp[e] = 0.f;
+                            if (c + e + 1 >= keys) dp[e + 1] = 0.f;
+                            fma2(acc[c + e], acc[c + e + 1], s[c + e], s[c + e + 1], dp[e], dp[e + 1], acc[c + e],
+                                 acc[c + e + 1]);
+                        }
                     }
                 }
                 tc_fence_before();
