@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // ------------------------------------------------------------ loads
         if (lane == 0) {
             int kt = 0, nq[2] = {0, 0};
+            Cursor c;
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(x, it);
                 if (w.t0 >= w.t1) continue;
@@ -183,17 +184,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     ++nq[t];
                 };
                 load_q(0);
-                for (int j = w.t0; j < w.t1; ++j, ++kt) {
-                    const int s = kt % x.stages;
-                    const uint32_t ph = (uint32_t)(kt / x.stages) & 1u;
+                const int g = w.h / p.group;
+                for (int j = w.t0; j < w.t1; ++j, ++kt, c.next(x.stages)) {
+                    const int s = c.slot;
                     const uint32_t kf = smem_u32(&bar.k_full[s]), vf = smem_u32(&bar.v_full[s]);
-                    if (kt >= x.stages) wait_on(smem_u32(&bar.k_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
+                    if (kt >= x.stages) wait_on(smem_u32(&bar.k_empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
                     mbar_arrive_expect_tx(kf, kTileBytes);
-                    load_rows(ring + 2 * s * kTileBytes, &mk, x.uk, j * kRows, w.h / p.group, w.b, kf);
+                    load_rows(ring + 2 * s * kTileBytes, &mk, x.uk, j * kRows, g, w.b, kf);
                     if (j == w.t0 && w.nt == 2) load_q(1);
-                    if (kt >= x.stages) wait_on(smem_u32(&bar.v_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
+                    if (kt >= x.stages) wait_on(smem_u32(&bar.v_empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
                     mbar_arrive_expect_tx(vf, kTileBytes);
-                    load_rows(ring + (2 * s + 1) * kTileBytes, &mv, x.uv, j * kRows, w.h / p.group, w.b, vf);
+                    load_rows(ring + (2 * s + 1) * kTileBytes, &mv, x.uv, j * kRows, g, w.b, vf);
                 }
             }
             // nothing may still arrive on this CTA's barriers once it has gone
@@ -212,42 +213,52 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     } else if (warp == 8) {
         // --------------------------------------------------------- products
         if (lane == 0) {
-            int kt = 0, nq[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0};
+            int nq[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0};
+            Cursor ck, cv;
+            const uint64_t dq[2] = {desc_rows(q_smem), desc_rows(q_smem + kTileBytes)};
+            const uint64_t dk = desc_rows(ring), dv = desc_tokens(ring + kTileBytes);
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(x, it);
                 if (w.t0 >= w.t1) continue;
-                const int base_kt = kt;
-                auto scores = [&](int t, int j) {
-                    const int k = base_kt + j - w.t0, s = k % x.stages;
+                auto scores = [&](int t, int j) __attribute__((always_inline)) {
                     if (j == w.t0) wait_on(smem_u32(&bar.q_full[t]), nq[t]++ & 1, guard, kErrTimeoutLoad);
-                    wait_on(smem_u32(&bar.k_full[s]), (k / x.stages) & 1, guard, kErrTimeoutLoad);
+                    if (t == 0) wait_on(smem_u32(&bar.k_full[ck.slot]), ck.phase, guard, kErrTimeoutLoad);
                     if (ns[t] > 0) wait_on(smem_u32(&bar.s_free[t]), (ns[t] - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tmem + t * 128, q_smem + t * kTileBytes, ring + 2 * s * kTileBytes,
+                    mma_rows_rows(tmem + t * 128, dq[t], dk + (uint32_t)ck.slot * (2 * kTileBytes / 16),
                                   tile_cols(tile_keys(w.len, j)));
                     tc_commit(smem_u32(&bar.s_full[t]));
                     ++ns[t];
                     if (j == w.t1 - 1) tc_commit(smem_u32(&bar.q_empty[t]));
-                    if (t == w.nt - 1) tc_commit(smem_u32(&bar.k_empty[s]));
+                    if (t == w.nt - 1) {
+                        tc_commit(smem_u32(&bar.k_empty[ck.slot]));
+                        ck.next(x.stages);
+                    }
                 };
-                auto values = [&](int t, int j) {
-                    const int k = base_kt + j - w.t0, s = k % x.stages;
-                    wait_on(smem_u32(&bar.v_full[s]), (k / x.stages) & 1, guard, kErrTimeoutLoad);
+                auto values = [&](int t, int j) __attribute__((always_inline)) {
+                    if (t == 0) wait_on(smem_u32(&bar.v_full[cv.slot]), cv.phase, guard, kErrTimeoutLoad);
                     wait_on(smem_u32(&bar.p_full[t]), np[t] & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_weights_rows(tmem + 384 + t * 64, tmem + 256 + t * 64, ring + (2 * s + 1) * kTileBytes,
-                                     tile_cols(tile_keys(w.len, j)), j > w.t0);
+                    mma_weights_rows(tmem + 384 + t * 64, tmem + 256 + t * 64,
+                                     dv + (uint32_t)cv.slot * (2 * kTileBytes / 16), tile_cols(tile_keys(w.len, j)),
+                                     j > w.t0);
                     tc_commit(smem_u32(&bar.pv_done[t]));
                     ++np[t];
-                    if (t == w.nt - 1) tc_commit(smem_u32(&bar.v_empty[s]));
-                };
-                for (int t = 0; t < w.nt; ++t) scores(t, w.t0);
-                for (int j = w.t0; j < w.t1; ++j)
-                    for (int t = 0; t < w.nt; ++t) {
-                        if (j + 1 < w.t1) scores(t, j + 1);
-                        values(t, j);
+                    if (t == w.nt - 1) {
+                        tc_commit(smem_u32(&bar.v_empty[cv.slot]));
+                        cv.next(x.stages);
                     }
-                kt += w.t1 - w.t0;
+                };
+                scores(0, w.t0);
+                if (w.nt == 2) scores(1, w.t0);
+                for (int j = w.t0; j < w.t1; ++j) {
+                    if (j + 1 < w.t1) scores(0, j + 1);
+                    values(0, j);
+                    if (w.nt == 2) {
+                        if (j + 1 < w.t1) scores(1, j + 1);
+                        values(1, j);
+                    }
+                }
             }
         }
         __syncwarp();

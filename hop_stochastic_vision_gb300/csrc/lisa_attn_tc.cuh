@@ -120,22 +120,45 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
-// [128 x cols] = A (tile of 128 rows, K-major) * B^T (tile of >= cols rows, K-major); K = 64.
-__device__ __forceinline__ void mma_rows_rows(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem, int cols) {
-    const uint32_t idesc = make_idesc_bf16(128, cols, false, false);
+// Descriptors of a token tile (128-byte rows, 128-byte swizzle): its rows as the
+// M or N side of a product over d (K-major), or as the K side of a product over
+// tokens (MN-major).  One thread issues every product, so the steps along K are
+// additions to a descriptor and the loops are unrolled: building a descriptor
+// for each instruction took 80 cycles of that thread per instruction, three
+// times what the instruction itself takes.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t tile) { return make_desc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_tokens(uint32_t tile) { return make_desc_sw128(tile, 1024, 1024); }
+
+// [128 x cols] = A (tile of 128 rows) * B^T (tile of >= cols rows); K = 64.
+__device__ __forceinline__ void mma_rows_rows(uint32_t d_tmem, uint64_t a, uint64_t b, int cols) {
+    const uint32_t idesc = make_idesc_bf16(128, 0, false, false) | ((uint32_t)(cols >> 3) << 17);
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-        tc_mma(d_tmem, make_desc_sw128(a_smem + ks * 32, 16, 1024), make_desc_sw128(b_smem + ks * 32, 16, 1024),
-               idesc, ks > 0);
+    for (int ks = 0; ks < 4; ++ks) tc_mma(d_tmem, a + 2 * ks, b + 2 * ks, idesc, ks > 0);
 }
 // [128 x 64] (+)= A (tensor memory, 128 x k) * B (tile of k token rows); k a multiple of 16.
-__device__ __forceinline__ void mma_weights_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_smem, int k,
+__device__ __forceinline__ void mma_weights_rows(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, int k,
                                                  bool accumulate) {
-    const uint32_t idesc = make_idesc_bf16(128, 64, false, true);
-    for (int ks = 0; ks < k / 16; ++ks)
-        tc_mma_ta(d_tmem, a_tmem + ks * 8, make_desc_sw128(b_smem + ks * 2048, 1024, 1024), idesc,
-                  accumulate || ks > 0);
+    constexpr uint32_t idesc = make_idesc_bf16(128, 64, false, true);
+    if (k == 128) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) tc_mma_ta(d_tmem, a_tmem + ks * 8, b + 128 * ks, idesc, ks > 0 || accumulate);
+    } else {
+        for (int ks = 0; ks < k / 16; ++ks)
+            tc_mma_ta(d_tmem, a_tmem + ks * 8, b + 128 * ks, idesc, ks > 0 || accumulate);
+    }
 }
+
+// A position in a ring of `stages` slots.
+struct Cursor {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 // One token box {64, 128} of a head's slice; coordinates of repeated dimensions stay 0.
 struct MapUse {

@@ -194,26 +194,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
         if (lane == 0) {
             int kt = 0, nq = 0;
+            Cursor c;
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(it);
                 if (w.tiles == 0) continue;
-                const int qs = nq & 1;
+                const int qs = nq & 1, g = w.h / p.group;
                 if (nq >= 2) wait_on(smem_u32(&bar.q_empty[qs]), ((nq >> 1) - 1) & 1, guard, kErrTimeoutMma);
                 const uint32_t f = smem_u32(&bar.q_full[qs]);
                 mbar_arrive_expect_tx(f, 2 * kTileBytes);
                 load_rows(qd + 2 * qs * kTileBytes, &mq, x.uq, w.q0, w.h, w.b, f);
                 load_rows(qd + (2 * qs + 1) * kTileBytes, &md, x.ud, w.q0, w.h, w.b, f);
                 ++nq;
-                for (int j = 0; j < w.tiles; ++j, ++kt) {
-                    const int s = kt % x.stages;
-                    const uint32_t ph = (uint32_t)(kt / x.stages) & 1u;
+                for (int j = 0; j < w.tiles; ++j, ++kt, c.next(x.stages)) {
+                    const int s = c.slot;
+                    const uint32_t ph = c.phase;
                     const uint32_t kf = smem_u32(&bar.k_full[s]), vf = smem_u32(&bar.v_full[s]);
                     if (kt >= x.stages) wait_on(smem_u32(&bar.k_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
                     mbar_arrive_expect_tx(kf, kTileBytes);
-                    load_rows(ring + 2 * s * kTileBytes, &mk, x.uk, j * kRows, w.h / p.group, w.b, kf);
+                    load_rows(ring + 2 * s * kTileBytes, &mk, x.uk, j * kRows, g, w.b, kf);
                     if (kt >= x.stages) wait_on(smem_u32(&bar.v_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
                     mbar_arrive_expect_tx(vf, kTileBytes);
-                    load_rows(ring + (2 * s + 1) * kTileBytes, &mv, x.uv, j * kRows, w.h / p.group, w.b, vf);
+                    load_rows(ring + (2 * s + 1) * kTileBytes, &mv, x.uv, j * kRows, g, w.b, vf);
                 }
             }
             for (int s = 0; s < x.stages; ++s) {
@@ -226,39 +227,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
         if (lane == 0) {
             int kt = 0, nq = 0;
+            Cursor front, back;
+            const uint64_t q0 = desc_rows(qd), k0 = desc_rows(ring), v0 = desc_rows(ring + kTileBytes),
+                           kt0 = desc_tokens(ring);
+            constexpr uint32_t kPair = 2 * kTileBytes / 16;
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(it);
                 if (w.tiles == 0) continue;
                 const int qs = nq & 1;
                 wait_on(smem_u32(&bar.q_full[qs]), (nq >> 1) & 1, guard, kErrTimeoutLoad);
                 ++nq;
-                const uint32_t qa = qd + 2 * qs * kTileBytes, da = qa + kTileBytes;
-                auto front = [&](int k, int j) {
-                    const int s = k % x.stages;
-                    const uint32_t ph = (uint32_t)(k / x.stages) & 1u;
-                    const int cols = tile_cols(tile_keys(w.len, j));
-                    wait_on(smem_u32(&bar.k_full[s]), ph, guard, kErrTimeoutLoad);
+                const uint64_t qa = q0 + (uint32_t)qs * kPair, da = qa + kTileBytes / 16;
+                auto products = [&](int k, int j) __attribute__((always_inline)) {
+                    const int s = front.slot, cols = tile_cols(tile_keys(w.len, j));
+                    wait_on(smem_u32(&bar.k_full[s]), front.phase, guard, kErrTimeoutLoad);
                     if (k > 0) wait_on(smem_u32(&bar.s_free), (k - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tS, qa, ring + 2 * s * kTileBytes, cols);
+                    mma_rows_rows(tS, qa, k0 + (uint32_t)s * kPair, cols);
                     tc_commit(smem_u32(&bar.s_full));
-                    wait_on(smem_u32(&bar.v_full[s]), ph, guard, kErrTimeoutLoad);
+                    wait_on(smem_u32(&bar.v_full[s]), front.phase, guard, kErrTimeoutLoad);
                     if (k > 0) wait_on(smem_u32(&bar.dp_free), (k - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tP, da, ring + (2 * s + 1) * kTileBytes, cols);
+                    mma_rows_rows(tP, da, v0 + (uint32_t)s * kPair, cols);
                     tc_commit(smem_u32(&bar.dp_full));
                     tc_commit(smem_u32(&bar.v_empty[s]));
                     if (j == w.tiles - 1) tc_commit(smem_u32(&bar.q_empty[qs]));
+                    front.next(x.stages);
                 };
-                front(kt, 0);
+                products(kt, 0);
                 for (int j = 0; j < w.tiles; ++j, ++kt) {
-                    if (j + 1 < w.tiles) front(kt + 1, j + 1);
-                    const int s = kt % x.stages;
+                    if (j + 1 < w.tiles) products(kt + 1, j + 1);
                     wait_on(smem_u32(&bar.ds_full), kt & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_weights_rows(tDq, tDs, ring + 2 * s * kTileBytes, tile_cols(tile_keys(w.len, j)), j > 0);
+                    mma_weights_rows(tDq, tDs, kt0 + (uint32_t)back.slot * kPair, tile_cols(tile_keys(w.len, j)), j > 0);
                     tc_commit(smem_u32(&bar.dq_done));
-                    tc_commit(smem_u32(&bar.k_empty[s]));
+                    tc_commit(smem_u32(&bar.k_empty[back.slot]));
+                    back.next(x.stages);
                 }
             }
         }
@@ -480,12 +484,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // per-query scalars of each tile, 64 threads
         const int t = tid - 320;
         int n = 0;
+        Cursor c;
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
             const int start = kBias ? bias_start(p.bias, w.b) : 0;
-            for (int u = w.u0; u < w.u1; ++u, ++n) {
-                const int s = n % x.stages;
-                if (n >= x.stages) wait_on(smem_u32(&bar.aux_empty[s]), ((n / x.stages) - 1) & 1, guard, kErrTimeoutMma);
+            for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
+                const int s = c.slot;
+                if (n >= x.stages) wait_on(smem_u32(&bar.aux_empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
                 const int h = w.g * p.group + u / x.qtiles, q0 = (u % x.qtiles) * kRows;
                 const size_t row0 = ((size_t)w.b * p.heads + h) * p.n;
 #pragma unroll
@@ -502,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
         if (lane == 0) {
             int n = 0, items = 0;
+            Cursor c;
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(it);
                 if (w.u0 >= w.u1) continue;
@@ -511,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(f, 2 * kTileBytes);
                 load_rows(kv, &mk, x.uk, w.j0, w.g, w.b, f);
                 load_rows(kv + kTileBytes, &mv, x.uv, w.j0, w.g, w.b, f);
-                for (int u = w.u0; u < w.u1; ++u, ++n) {
-                    const int s = n % x.stages;
-                    const uint32_t ph = (uint32_t)(n / x.stages) & 1u;
+                for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
+                    const int s = c.slot;
+                    const uint32_t ph = c.phase;
                     const int h = w.g * p.group + u / x.qtiles, q0 = (u % x.qtiles) * kRows;
                     const uint32_t qf = smem_u32(&bar.q_full[s]), df = smem_u32(&bar.d_full[s]);
                     if (n >= x.stages) wait_on(smem_u32(&bar.q_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
@@ -534,45 +540,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
         if (lane == 0) {
             int n = 0, items = 0;
+            Cursor cq, cd, back;   // the next Q, the next dO, the tile whose weights come next
+            const uint64_t k0 = desc_rows(kv), v0 = desc_rows(kv + kTileBytes), q0 = desc_rows(ring),
+                           d0 = desc_rows(ring + kTileBytes), qt0 = desc_tokens(ring), dt0 = desc_tokens(ring + kTileBytes);
+            constexpr uint32_t kPair = 2 * kTileBytes / 16;
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(it);
                 if (w.u0 >= w.u1) continue;
                 wait_on(smem_u32(&bar.kv_full), items & 1, guard, kErrTimeoutLoad);
                 ++items;
-                auto cols_of = [&](int u) { return tile_cols(min(kRows, p.n - (u % x.qtiles) * kRows)); };
-                auto scores = [&](int k, int u) {
-                    const int s = k % x.stages;
-                    wait_on(smem_u32(&bar.q_full[s]), (k / x.stages) & 1, guard, kErrTimeoutLoad);
+                // columns of a tile: only a head's last one may be short
+                const int tail = tile_cols(p.n - (x.qtiles - 1) * kRows);
+                int qs = w.u0 % x.qtiles, qd = qs, qb = qs;
+                auto cols_of = [&](int &q) __attribute__((always_inline)) {
+                    const int cols = q == x.qtiles - 1 ? tail : kRows;
+                    q = q == x.qtiles - 1 ? 0 : q + 1;
+                    return cols;
+                };
+                auto scores = [&](int k) __attribute__((always_inline)) {
+                    wait_on(smem_u32(&bar.q_full[cq.slot]), cq.phase, guard, kErrTimeoutLoad);
                     if (k > 0) wait_on(smem_u32(&bar.s_free), (k - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tS, kv, ring + 2 * s * kTileBytes, cols_of(u));
+                    mma_rows_rows(tS, k0, q0 + (uint32_t)cq.slot * kPair, cols_of(qs));
                     tc_commit(smem_u32(&bar.s_full));
+                    cq.next(x.stages);
                 };
-                auto slopes = [&](int k, int u) {
-                    const int s = k % x.stages;
-                    wait_on(smem_u32(&bar.d_full[s]), (k / x.stages) & 1, guard, kErrTimeoutLoad);
+                auto slopes = [&](int k, bool last) __attribute__((always_inline)) {
+                    wait_on(smem_u32(&bar.d_full[cd.slot]), cd.phase, guard, kErrTimeoutLoad);
                     if (k > 0) wait_on(smem_u32(&bar.dp_free), (k - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tD, kv + kTileBytes, ring + (2 * s + 1) * kTileBytes, cols_of(u));
+                    mma_rows_rows(tD, v0, d0 + (uint32_t)cd.slot * kPair, cols_of(qd));
                     tc_commit(smem_u32(&bar.dp_full));
-                    if (u == w.u1 - 1) tc_commit(smem_u32(&bar.kv_empty));
+                    if (last) tc_commit(smem_u32(&bar.kv_empty));
+                    cd.next(x.stages);
                 };
-                scores(n, w.u0);
-                slopes(n, w.u0);
+                scores(n);
+                slopes(n, w.u0 == w.u1 - 1);
                 for (int u = w.u0; u < w.u1; ++u, ++n) {
-                    const int s = n % x.stages;
-                    if (u + 1 < w.u1) scores(n + 1, u + 1);
+                    const bool more = u + 1 < w.u1;
+                    const int s = back.slot, cols = cols_of(qb);
+                    if (more) scores(n + 1);
                     wait_on(smem_u32(&bar.p_full), n & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_weights_rows(tDv, tPw, ring + (2 * s + 1) * kTileBytes, cols_of(u), u > w.u0);
+                    mma_weights_rows(tDv, tPw, dt0 + (uint32_t)s * kPair, cols, u > w.u0);
                     tc_commit(smem_u32(&bar.dv_done));
                     tc_commit(smem_u32(&bar.d_empty[s]));
-                    if (u + 1 < w.u1) slopes(n + 1, u + 1);
+                    if (more) slopes(n + 1, u + 2 == w.u1);
                     wait_on(smem_u32(&bar.ds_full), n & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_weights_rows(tDk, tDs, ring + 2 * s * kTileBytes, cols_of(u), u > w.u0);
+                    mma_weights_rows(tDk, tDs, qt0 + (uint32_t)s * kPair, cols, u > w.u0);
                     tc_commit(smem_u32(&bar.dk_done));
                     tc_commit(smem_u32(&bar.q_empty[s]));
+                    back.next(x.stages);
                 }
             }
         }
@@ -583,24 +602,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
         int n = 0, lut_head = -1;
+        Cursor ca;
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
             const int j = w.j0 + wt;
             const int ok = kBias ? off_key(p.bias, min(j, p.m - 1)) : 0;
-            for (int u = w.u0; u < w.u1; ++u, ++n) {
-                const int h = w.g * p.group + u / x.qtiles;
+            int h = w.g * p.group + w.u0 / x.qtiles, qt = w.u0 % x.qtiles;
+            for (int u = w.u0; u < w.u1; ++u, ++n, ca.next(x.stages), h += qt == x.qtiles - 1, qt = qt == x.qtiles - 1 ? 0 : qt + 1) {
                 if (kBias && h != lut_head) {
                     math_barrier();
                     fill_offsets(p.bias, h, kLog2e, lut, tid, 256);
                     math_barrier();
                     lut_head = h;
                 }
-                const int cols = tile_cols(min(kRows, p.n - (u % x.qtiles) * kRows));
+                const int cols = tile_cols(min(kRows, p.n - qt * kRows));
                 const bool any = 64 * half < cols;
-                const QueryAux &a = aux[n % x.stages];
+                const QueryAux &a = aux[ca.slot];
                 const int c0 = 64 * half;
                 float s[64];
-                wait_on(smem_u32(&bar.aux_full[n % x.stages]), (n / x.stages) & 1, guard, kErrTimeoutLoad);
+                wait_on(smem_u32(&bar.aux_full[ca.slot]), ca.phase, guard, kErrTimeoutLoad);
                 wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 load_strip(tS + c0 + lanes, s);
@@ -696,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st16(tDs + 32 * half + c / 2 + lanes, out);
                     }
                 }
-                arrive_warp(&bar.aux_empty[n % x.stages], lane);
+                arrive_warp(&bar.aux_empty[ca.slot], lane);
                 tc_wait_st();
                 tc_fence_before();
                 arrive_warp(&bar.ds_full, lane);
@@ -819,12 +839,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
         if (lane == 0) {
             int n = 0;
+            Cursor c;
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(it);
                 for (int b = w.b0; b < w.b1; ++b) {
                     if (w.j0 >= keys_of(p, b)) continue;
-                    const int s = n % x.stages;
-                    if (n >= x.stages) wait_on(smem_u32(&bar.empty[s]), ((n / x.stages) - 1) & 1, guard, kErrTimeoutMma);
+                    const int s = c.slot;
+                    if (n >= x.stages) wait_on(smem_u32(&bar.empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
                     const uint32_t f = smem_u32(&bar.full[s]), at = ring + 4 * s * kTileBytes;
                     mbar_arrive_expect_tx(f, 4 * kTileBytes);
                     load_rows(at, &mq, x.uq, w.q0, w.h, b, f);
@@ -832,6 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     load_rows(at + kTileBytes, &md, x.ud, w.q0, w.h, b, f);
                     load_rows(at + 3 * kTileBytes, &mv, x.uv, w.j0, w.h / p.group, b, f);
                     ++n;
+                    c.next(x.stages);
                 }
             }
             for (int s = 0; s < x.stages; ++s) drain(&bar.empty[s], uses_of(n, s, x.stages), x.err);
@@ -840,24 +862,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
         if (lane == 0) {
             int n = 0;
+            Cursor c;
+            const uint64_t r0 = desc_rows(ring);
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(it);
                 for (int b = w.b0; b < w.b1; ++b) {
                     const int len = keys_of(p, b);
                     if (w.j0 >= len) continue;
-                    const int s = n % x.stages, cols = tile_cols(min(kRows, len - w.j0));
-                    const uint32_t at = ring + 4 * s * kTileBytes;
-                    wait_on(smem_u32(&bar.full[s]), (n / x.stages) & 1, guard, kErrTimeoutLoad);
+                    const int s = c.slot, cols = tile_cols(min(kRows, len - w.j0));
+                    const uint64_t at = r0 + (uint32_t)s * (4 * kTileBytes / 16);
+                    wait_on(smem_u32(&bar.full[s]), c.phase, guard, kErrTimeoutLoad);
                     if (n > 0) wait_on(smem_u32(&bar.s_free), (n - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tS, at, at + 2 * kTileBytes, cols);
+                    mma_rows_rows(tS, at, at + 2 * kTileBytes / 16, cols);
                     tc_commit(smem_u32(&bar.s_full));
                     if (n > 0) wait_on(smem_u32(&bar.dp_free), (n - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tD, at + kTileBytes, at + 3 * kTileBytes, cols);
+                    mma_rows_rows(tD, at + kTileBytes / 16, at + 3 * kTileBytes / 16, cols);
                     tc_commit(smem_u32(&bar.dp_full));
                     tc_commit(smem_u32(&bar.empty[s]));
                     ++n;
+                    c.next(x.stages);
                 }
             }
         }
