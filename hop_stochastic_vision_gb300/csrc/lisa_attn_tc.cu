@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     const Problem &p = x.p;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
     const uint32_t q_smem = base, ring = base + 2 * kTileBytes;
     float *lut = reinterpret_cast<float *>(sm + x.off_lut);
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         __syncwarp();
     } else if (warp == 8) {
         // --------------------------------------------------------- products
-        if (lane == 0) {
+        {
             int nq[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0};
             Cursor ck, cv;
             const uint64_t dq[2] = {desc_rows(q_smem), desc_rows(q_smem + kTileBytes)};
@@ -225,29 +225,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     if (t == 0) wait_on(smem_u32(&bar.k_full[ck.slot]), ck.phase, guard, kErrTimeoutLoad);
                     if (ns[t] > 0) wait_on(smem_u32(&bar.s_free[t]), (ns[t] - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tmem + t * 128, dq[t], dk + (uint32_t)ck.slot * (2 * kTileBytes / 16),
-                                  tile_cols(tile_keys(w.len, j)));
-                    tc_commit(smem_u32(&bar.s_full[t]));
-                    ++ns[t];
-                    if (j == w.t1 - 1) tc_commit(smem_u32(&bar.q_empty[t]));
-                    if (t == w.nt - 1) {
-                        tc_commit(smem_u32(&bar.k_empty[ck.slot]));
-                        ck.next(x.stages);
+                    if (elect_one()) {
+                        mma_rows_rows(tmem + t * 128, dq[t], dk + (uint32_t)ck.slot * (2 * kTileBytes / 16),
+                                      tile_cols(tile_keys(w.len, j)));
+                        tc_commit(smem_u32(&bar.s_full[t]));
+                        if (j == w.t1 - 1) tc_commit(smem_u32(&bar.q_empty[t]));
+                        if (t == w.nt - 1) tc_commit(smem_u32(&bar.k_empty[ck.slot]));
                     }
+                    __syncwarp();
+                    ++ns[t];
+                    if (t == w.nt - 1) ck.next(x.stages);
                 };
                 auto values = [&](int t, int j) __attribute__((always_inline)) {
                     if (t == 0) wait_on(smem_u32(&bar.v_full[cv.slot]), cv.phase, guard, kErrTimeoutLoad);
                     wait_on(smem_u32(&bar.p_full[t]), np[t] & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_weights_rows(tmem + 384 + t * 64, tmem + 256 + t * 64,
-                                     dv + (uint32_t)cv.slot * (2 * kTileBytes / 16), tile_cols(tile_keys(w.len, j)),
-                                     j > w.t0);
-                    tc_commit(smem_u32(&bar.pv_done[t]));
-                    ++np[t];
-                    if (t == w.nt - 1) {
-                        tc_commit(smem_u32(&bar.v_empty[cv.slot]));
-                        cv.next(x.stages);
+                    if (elect_one()) {
+                        mma_weights_rows(tmem + 384 + t * 64, tmem + 256 + t * 64,
+                                         dv + (uint32_t)cv.slot * (2 * kTileBytes / 16),
+                                         tile_cols(tile_keys(w.len, j)), j > w.t0);
+                        tc_commit(smem_u32(&bar.pv_done[t]));
+                        if (t == w.nt - 1) tc_commit(smem_u32(&bar.v_empty[cv.slot]));
                     }
+                    __syncwarp();
+                    ++np[t];
+                    if (t == w.nt - 1) cv.next(x.stages);
                 };
                 scores(0, w.t0);
                 if (w.nt == 2) scores(1, w.t0);

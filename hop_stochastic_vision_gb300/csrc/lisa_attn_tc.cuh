@@ -129,6 +129,16 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint
 __device__ __forceinline__ uint64_t desc_rows(uint32_t tile) { return make_desc_sw128(tile, 16, 1024); }
 __device__ __forceinline__ uint64_t desc_tokens(uint32_t tile) { return make_desc_sw128(tile, 1024, 1024); }
 
+// One thread of a converged warp, the same one every time.  The warp runs the
+// loops and waits as a whole and only the products and commits are under this:
+// addresses and descriptors then stay in uniform registers, where the
+// instructions want them.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred e;\nelect.sync _|e, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, e;\n}" : "=r"(p));
+    return p != 0;
+}
+
 // [128 x cols] = A (tile of 128 rows) * B^T (tile of >= cols rows); K = 64.
 __device__ __forceinline__ void mma_rows_rows(uint32_t d_tmem, uint64_t a, uint64_t b, int cols) {
     const uint32_t idesc = make_idesc_bf16(128, 0, false, false) | ((uint32_t)(cols >> 3) << 17);

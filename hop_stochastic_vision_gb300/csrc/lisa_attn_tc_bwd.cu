@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int dead;
     __shared__ float other[kRows];
     const Problem &p = x.p;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
     const uint32_t qd = base, ring = base + 4 * kTileBytes;   // two slots of (Q, dO); stages of (K, V)
     float *lut = reinterpret_cast<float *>(sm + x.off_lut);
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 8) {
-        if (lane == 0) {
+        {
             int kt = 0, nq = 0;
             Cursor front, back;
             const uint64_t q0 = desc_rows(qd), k0 = desc_rows(ring), v0 = desc_rows(ring + kTileBytes),
@@ -243,15 +243,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_on(smem_u32(&bar.k_full[s]), front.phase, guard, kErrTimeoutLoad);
                     if (k > 0) wait_on(smem_u32(&bar.s_free), (k - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tS, qa, k0 + (uint32_t)s * kPair, cols);
-                    tc_commit(smem_u32(&bar.s_full));
+                    if (elect_one()) {
+                        mma_rows_rows(tS, qa, k0 + (uint32_t)s * kPair, cols);
+                        tc_commit(smem_u32(&bar.s_full));
+                    }
+                    __syncwarp();
                     wait_on(smem_u32(&bar.v_full[s]), front.phase, guard, kErrTimeoutLoad);
                     if (k > 0) wait_on(smem_u32(&bar.dp_free), (k - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tP, da, v0 + (uint32_t)s * kPair, cols);
-                    tc_commit(smem_u32(&bar.dp_full));
-                    tc_commit(smem_u32(&bar.v_empty[s]));
-                    if (j == w.tiles - 1) tc_commit(smem_u32(&bar.q_empty[qs]));
+                    if (elect_one()) {
+                        mma_rows_rows(tP, da, v0 + (uint32_t)s * kPair, cols);
+                        tc_commit(smem_u32(&bar.dp_full));
+                        tc_commit(smem_u32(&bar.v_empty[s]));
+                        if (j == w.tiles - 1) tc_commit(smem_u32(&bar.q_empty[qs]));
+                    }
+                    __syncwarp();
                     front.next(x.stages);
                 };
                 products(kt, 0);
@@ -259,9 +265,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 1 < w.tiles) products(kt + 1, j + 1);
                     wait_on(smem_u32(&bar.ds_full), kt & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_weights_rows(tDq, tDs, kt0 + (uint32_t)back.slot * kPair, tile_cols(tile_keys(w.len, j)), j > 0);
-                    tc_commit(smem_u32(&bar.dq_done));
-                    tc_commit(smem_u32(&bar.k_empty[back.slot]));
+                    if (elect_one()) {
+                        mma_weights_rows(tDq, tDs, kt0 + (uint32_t)back.slot * kPair, tile_cols(tile_keys(w.len, j)),
+                                         j > 0);
+                        tc_commit(smem_u32(&bar.dq_done));
+                        tc_commit(smem_u32(&bar.k_empty[back.slot]));
+                    }
+                    __syncwarp();
                     back.next(x.stages);
                 }
             }
@@ -424,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     const Problem &p = x.p;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
     const uint32_t kv = base, ring = base + 2 * kTileBytes;   // K, V; stages of (Q, dO)
     float *lut = reinterpret_cast<float *>(sm + x.off_lut);
@@ -538,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 8) {
-        if (lane == 0) {
+        {
             int n = 0, items = 0;
             Cursor cq, cd, back;   // the next Q, the next dO, the tile whose weights come next
             const uint64_t k0 = desc_rows(kv), v0 = desc_rows(kv + kTileBytes), q0 = desc_rows(ring),
@@ -561,17 +571,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_on(smem_u32(&bar.q_full[cq.slot]), cq.phase, guard, kErrTimeoutLoad);
                     if (k > 0) wait_on(smem_u32(&bar.s_free), (k - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tS, k0, q0 + (uint32_t)cq.slot * kPair, cols_of(qs));
-                    tc_commit(smem_u32(&bar.s_full));
+                    const int cols = cols_of(qs);
+                    if (elect_one()) {
+                        mma_rows_rows(tS, k0, q0 + (uint32_t)cq.slot * kPair, cols);
+                        tc_commit(smem_u32(&bar.s_full));
+                    }
+                    __syncwarp();
                     cq.next(x.stages);
                 };
                 auto slopes = [&](int k, bool last) __attribute__((always_inline)) {
                     wait_on(smem_u32(&bar.d_full[cd.slot]), cd.phase, guard, kErrTimeoutLoad);
                     if (k > 0) wait_on(smem_u32(&bar.dp_free), (k - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tD, v0, d0 + (uint32_t)cd.slot * kPair, cols_of(qd));
-                    tc_commit(smem_u32(&bar.dp_full));
-                    if (last) tc_commit(smem_u32(&bar.kv_empty));
+                    const int cols = cols_of(qd);
+                    if (elect_one()) {
+                        mma_rows_rows(tD, v0, d0 + (uint32_t)cd.slot * kPair, cols);
+                        tc_commit(smem_u32(&bar.dp_full));
+                        if (last) tc_commit(smem_u32(&bar.kv_empty));
+                    }
+                    __syncwarp();
                     cd.next(x.stages);
                 };
                 scores(n);
@@ -582,15 +600,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (more) scores(n + 1);
                     wait_on(smem_u32(&bar.p_full), n & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_weights_rows(tDv, tPw, dt0 + (uint32_t)s * kPair, cols, u > w.u0);
-                    tc_commit(smem_u32(&bar.dv_done));
-                    tc_commit(smem_u32(&bar.d_empty[s]));
+                    if (elect_one()) {
+                        mma_weights_rows(tDv, tPw, dt0 + (uint32_t)s * kPair, cols, u > w.u0);
+                        tc_commit(smem_u32(&bar.dv_done));
+                        tc_commit(smem_u32(&bar.d_empty[s]));
+                    }
+                    __syncwarp();
                     if (more) slopes(n + 1, u + 2 == w.u1);
                     wait_on(smem_u32(&bar.ds_full), n & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_weights_rows(tDk, tDs, qt0 + (uint32_t)s * kPair, cols, u > w.u0);
-                    tc_commit(smem_u32(&bar.dk_done));
-                    tc_commit(smem_u32(&bar.q_empty[s]));
+                    if (elect_one()) {
+                        mma_weights_rows(tDk, tDs, qt0 + (uint32_t)s * kPair, cols, u > w.u0);
+                        tc_commit(smem_u32(&bar.dk_done));
+                        tc_commit(smem_u32(&bar.q_empty[s]));
+                    }
+                    __syncwarp();
                     back.next(x.stages);
                 }
             }
@@ -789,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     const Problem &p = x.p;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t ring = smem_u32(sm);   // stages of (Q, dO, K, V)
     float *lut = reinterpret_cast<float *>(sm + x.off_lut);
     uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_aux);
@@ -860,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 8) {
-        if (lane == 0) {
+        {
             int n = 0;
             Cursor c;
             const uint64_t r0 = desc_rows(ring);
@@ -874,13 +898,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_on(smem_u32(&bar.full[s]), c.phase, guard, kErrTimeoutLoad);
                     if (n > 0) wait_on(smem_u32(&bar.s_free), (n - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tS, at, at + 2 * kTileBytes / 16, cols);
-                    tc_commit(smem_u32(&bar.s_full));
+                    if (elect_one()) {
+                        mma_rows_rows(tS, at, at + 2 * kTileBytes / 16, cols);
+                        tc_commit(smem_u32(&bar.s_full));
+                    }
+                    __syncwarp();
                     if (n > 0) wait_on(smem_u32(&bar.dp_free), (n - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
-                    mma_rows_rows(tD, at + kTileBytes / 16, at + 3 * kTileBytes / 16, cols);
-                    tc_commit(smem_u32(&bar.dp_full));
-                    tc_commit(smem_u32(&bar.empty[s]));
+                    if (elect_one()) {
+                        mma_rows_rows(tD, at + kTileBytes / 16, at + 3 * kTileBytes / 16, cols);
+                        tc_commit(smem_u32(&bar.dp_full));
+                        tc_commit(smem_u32(&bar.empty[s]));
+                    }
+                    __syncwarp();
                     ++n;
                     c.next(x.stages);
                 }
