@@ -3,8 +3,10 @@
 // A persistent CTA takes work items of 256 queries (two tiles of 128 rows) of
 // one (batch, head) and walks the keys in tiles of 128:
 //   warp 9        TMA: the queries, then a ring of K and V tiles
-//   warp 8        one thread issues every product: S_t = Q_t K^T into tensor
-//                 memory, then O_t += P_t V with P_t read from tensor memory
+//   warps 8, 10   one thread each issues the products of tile 0, 1: S_t = Q_t K^T
+//                 into tensor memory, then O_t += P_t V with P_t read from there
+//                 (one warp for both tiles spent 2240 cycles on the waits and
+//                 instructions of a pair of tiles whose products take 1024)
 //   warps 0-3     softmax of tile 0, one thread per row: scores to registers,
 //   warps 4-7     weights to tensor memory as bf16; the same for tile 1
 // While one tile's scores are in the softmax the other's products run.
@@ -150,8 +152,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(smem_u32(&bar.k_full[s]), 1);
             mbar_init(smem_u32(&bar.v_full[s]), 1);
-            mbar_init(smem_u32(&bar.k_empty[s]), 1);
-            mbar_init(smem_u32(&bar.v_empty[s]), 1);
+            mbar_init(smem_u32(&bar.k_empty[s]), 2);   // one for each tile
+            mbar_init(smem_u32(&bar.v_empty[s]), 2);
         }
         dead = 0;
         fence_mbar_init();
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t tmem = tmem_slot;
 
     if (warp >= 8) set_regs_down<kRegsControl>();
-    if (warp >= 10) {
+    if (warp == 11) {
         // idle: completes the control warps' group of four
     } else if (warp == 9) {
         // ------------------------------------------------------------ loads
@@ -210,60 +212,61 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     atomicOr(x.err, kErrTimeoutMma);
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp >= 8) {
         // --------------------------------------------------------- products
-        {
-            int nq[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0};
-            Cursor ck, cv;
-            const uint64_t dq[2] = {desc_rows(q_smem), desc_rows(q_smem + kTileBytes)};
-            const uint64_t dk = desc_rows(ring), dv = desc_tokens(ring + kTileBytes);
-            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
-                const Item w = item_of(x, it);
-                if (w.t0 >= w.t1) continue;
-                auto scores = [&](int t, int j) __attribute__((always_inline)) {
-                    if (j == w.t0) wait_on(smem_u32(&bar.q_full[t]), nq[t]++ & 1, guard, kErrTimeoutLoad);
-                    if (t == 0) wait_on(smem_u32(&bar.k_full[ck.slot]), ck.phase, guard, kErrTimeoutLoad);
-                    if (ns[t] > 0) wait_on(smem_u32(&bar.s_free[t]), (ns[t] - 1) & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        mma_rows_rows(tmem + t * 128, dq[t], dk + (uint32_t)ck.slot * (2 * kTileBytes / 16),
-                                      tile_cols(tile_keys(w.len, j)));
-                        tc_commit(smem_u32(&bar.s_full[t]));
-                        if (j == w.t1 - 1) tc_commit(smem_u32(&bar.q_empty[t]));
-                        if (t == w.nt - 1) tc_commit(smem_u32(&bar.k_empty[ck.slot]));
-                    }
-                    __syncwarp();
-                    ++ns[t];
-                    if (t == w.nt - 1) ck.next(x.stages);
-                };
-                auto values = [&](int t, int j) __attribute__((always_inline)) {
-                    if (t == 0) wait_on(smem_u32(&bar.v_full[cv.slot]), cv.phase, guard, kErrTimeoutLoad);
-                    wait_on(smem_u32(&bar.p_full[t]), np[t] & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        mma_weights_rows(tmem + 384 + t * 64, tmem + 256 + t * 64,
-                                         dv + (uint32_t)cv.slot * (2 * kTileBytes / 16),
-                                         tile_cols(tile_keys(w.len, j)), j > w.t0);
-                        tc_commit(smem_u32(&bar.pv_done[t]));
-                        if (t == w.nt - 1) tc_commit(smem_u32(&bar.v_empty[cv.slot]));
-                    }
-                    __syncwarp();
-                    ++np[t];
-                    if (t == w.nt - 1) cv.next(x.stages);
-                };
-                scores(0, w.t0);
-                if (w.nt == 2) scores(1, w.t0);
+        const int t = warp == 8 ? 0 : 1;
+        const uint32_t tS = tmem + t * 128, tP = tmem + 256 + t * 64, tO = tmem + 384 + t * 64;
+        const uint64_t dq = desc_rows(q_smem + t * kTileBytes), dk = desc_rows(ring), dv = desc_tokens(ring + kTileBytes);
+        constexpr uint32_t kPair = 2 * kTileBytes / 16;
+        int nq = 0, ns = 0, np = 0;
+        Cursor ck, cv;
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(x, it);
+            if (w.t0 >= w.t1) continue;
+            if (t >= w.nt) {   // no rows in this tile: pass its share of the ring on
                 for (int j = w.t0; j < w.t1; ++j) {
-                    if (j + 1 < w.t1) scores(0, j + 1);
-                    values(0, j);
-                    if (w.nt == 2) {
-                        if (j + 1 < w.t1) scores(1, j + 1);
-                        values(1, j);
+                    wait_on(smem_u32(&bar.k_full[ck.slot]), ck.phase, guard, kErrTimeoutLoad);
+                    wait_on(smem_u32(&bar.v_full[ck.slot]), ck.phase, guard, kErrTimeoutLoad);
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&bar.k_empty[ck.slot]));
+                        mbar_arrive(smem_u32(&bar.v_empty[ck.slot]));
                     }
+                    ck.next(x.stages);
                 }
+                cv = ck;
+                continue;
+            }
+            wait_on(smem_u32(&bar.q_full[t]), nq++ & 1, guard, kErrTimeoutLoad);
+            auto scores = [&](int j) __attribute__((always_inline)) {
+                wait_on(smem_u32(&bar.k_full[ck.slot]), ck.phase, guard, kErrTimeoutLoad);
+                if (ns > 0) wait_on(smem_u32(&bar.s_free[t]), (ns - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows_rows(tS, dq, dk + (uint32_t)ck.slot * kPair, tile_cols(tile_keys(w.len, j)));
+                    tc_commit(smem_u32(&bar.s_full[t]));
+                    tc_commit(smem_u32(&bar.k_empty[ck.slot]));
+                    if (j == w.t1 - 1) tc_commit(smem_u32(&bar.q_empty[t]));
+                }
+                __syncwarp();
+                ++ns;
+                ck.next(x.stages);
+            };
+            scores(w.t0);
+            for (int j = w.t0; j < w.t1; ++j) {
+                if (j + 1 < w.t1) scores(j + 1);
+                wait_on(smem_u32(&bar.v_full[cv.slot]), cv.phase, guard, kErrTimeoutLoad);
+                wait_on(smem_u32(&bar.p_full[t]), np & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_weights_rows(tO, tP, dv + (uint32_t)cv.slot * kPair, tile_cols(tile_keys(w.len, j)), j > w.t0);
+                    tc_commit(smem_u32(&bar.pv_done[t]));
+                    tc_commit(smem_u32(&bar.v_empty[cv.slot]));
+                }
+                __syncwarp();
+                ++np;
+                cv.next(x.stages);
             }
         }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax
         set_regs_up<kRegsSoftmax>();
@@ -367,8 +370,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         tmem_st16(p_tm + c / 2, w16);
                     }
                 r.sum += (part[0] + part[1]) + (part[2] + part[3]);
-                if (!kFull && t == 0 && keys < cols && w.len < p.m) {
+                if (!kFull && keys < cols && w.len < p.m) {
                     // values behind the last key: whatever stands there times a weight of 0 has to be 0
+                    // (for each tile's own product; the second time zeros meet zeros)
                     const int st = kt % x.stages;
                     wait_on(smem_u32(&bar.v_full[st]), (kt / x.stages) & 1, guard, kErrTimeoutLoad);
                     zero_rows(ring + (2 * st + 1) * kTileBytes, keys, cols, wt);

@@ -24,9 +24,10 @@ namespace lisa {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 384;      // 8 warps of arithmetic, products, loads, two helpers
+constexpr int kThreads = 384;      // 8 warps of arithmetic; products (two warps), loads, a helper
 constexpr int kRegsMath = 208, kRegsControl = 88;
 constexpr int kMaxStages = 4;
+constexpr uint32_t kPair = 2 * kTileBytes / 16;   // a ring stage of two tiles, in descriptor units
 
 struct BwdParams {
     Problem p;
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= 8) set_regs_down<kRegsControl>();
-    if (warp >= 10) {
+    if (warp == 11) {
         // idle: completes the control warps' group of four
     } else if (warp == 9) {
         if (lane == 0) {
@@ -225,58 +226,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 8) {
-        {
-            int kt = 0, nq = 0;
-            Cursor front, back;
-            const uint64_t q0 = desc_rows(qd), k0 = desc_rows(ring), v0 = desc_rows(ring + kTileBytes),
-                           kt0 = desc_tokens(ring);
-            constexpr uint32_t kPair = 2 * kTileBytes / 16;
-            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
-                const Item w = item_of(it);
-                if (w.tiles == 0) continue;
-                const int qs = nq & 1;
-                wait_on(smem_u32(&bar.q_full[qs]), (nq >> 1) & 1, guard, kErrTimeoutLoad);
-                ++nq;
-                const uint64_t qa = q0 + (uint32_t)qs * kPair, da = qa + kTileBytes / 16;
-                auto products = [&](int k, int j) __attribute__((always_inline)) {
-                    const int s = front.slot, cols = tile_cols(tile_keys(w.len, j));
-                    wait_on(smem_u32(&bar.k_full[s]), front.phase, guard, kErrTimeoutLoad);
-                    if (k > 0) wait_on(smem_u32(&bar.s_free), (k - 1) & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        mma_rows_rows(tS, qa, k0 + (uint32_t)s * kPair, cols);
-                        tc_commit(smem_u32(&bar.s_full));
-                    }
-                    __syncwarp();
-                    wait_on(smem_u32(&bar.v_full[s]), front.phase, guard, kErrTimeoutLoad);
-                    if (k > 0) wait_on(smem_u32(&bar.dp_free), (k - 1) & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        mma_rows_rows(tP, da, v0 + (uint32_t)s * kPair, cols);
-                        tc_commit(smem_u32(&bar.dp_full));
-                        tc_commit(smem_u32(&bar.v_empty[s]));
-                        if (j == w.tiles - 1) tc_commit(smem_u32(&bar.q_empty[qs]));
-                    }
-                    __syncwarp();
-                    front.next(x.stages);
-                };
-                products(kt, 0);
-                for (int j = 0; j < w.tiles; ++j, ++kt) {
-                    if (j + 1 < w.tiles) products(kt + 1, j + 1);
-                    wait_on(smem_u32(&bar.ds_full), kt & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        mma_weights_rows(tDq, tDs, kt0 + (uint32_t)back.slot * kPair, tile_cols(tile_keys(w.len, j)),
-                                         j > 0);
-                        tc_commit(smem_u32(&bar.dq_done));
-                        tc_commit(smem_u32(&bar.k_empty[back.slot]));
-                    }
-                    __syncwarp();
-                    back.next(x.stages);
+        // S and dP of each tile
+        int kt = 0, nq = 0;
+        Cursor c;
+        const uint64_t q0 = desc_rows(qd), k0 = desc_rows(ring), v0 = desc_rows(ring + kTileBytes);
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(it);
+            if (w.tiles == 0) continue;
+            const int qs = nq & 1;
+            wait_on(smem_u32(&bar.q_full[qs]), (nq >> 1) & 1, guard, kErrTimeoutLoad);
+            ++nq;
+            const uint64_t qa = q0 + (uint32_t)qs * kPair, da = qa + kTileBytes / 16;
+            for (int j = 0; j < w.tiles; ++j, ++kt, c.next(x.stages)) {
+                const int s = c.slot, cols = tile_cols(tile_keys(w.len, j));
+                wait_on(smem_u32(&bar.k_full[s]), c.phase, guard, kErrTimeoutLoad);
+                if (kt > 0) wait_on(smem_u32(&bar.s_free), (kt - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows_rows(tS, qa, k0 + (uint32_t)s * kPair, cols);
+                    tc_commit(smem_u32(&bar.s_full));
                 }
+                __syncwarp();
+                wait_on(smem_u32(&bar.v_full[s]), c.phase, guard, kErrTimeoutLoad);
+                if (kt > 0) wait_on(smem_u32(&bar.dp_free), (kt - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows_rows(tP, da, v0 + (uint32_t)s * kPair, cols);
+                    tc_commit(smem_u32(&bar.dp_full));
+                    tc_commit(smem_u32(&bar.v_empty[s]));
+                    if (j == w.tiles - 1) tc_commit(smem_u32(&bar.q_empty[qs]));
+                }
+                __syncwarp();
             }
         }
-        __syncwarp();
+    } else if (warp == 10) {
+        // dQ += dS K.  S has read the K tile too: dS comes of it.
+        int kt = 0;
+        Cursor c;
+        const uint64_t kt0 = desc_tokens(ring);
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(it);
+            for (int j = 0; j < w.tiles; ++j, ++kt, c.next(x.stages)) {
+                wait_on(smem_u32(&bar.ds_full), kt & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_weights_rows(tDq, tDs, kt0 + (uint32_t)c.slot * kPair, tile_cols(tile_keys(w.len, j)), j > 0);
+                    tc_commit(smem_u32(&bar.dq_done));
+                    tc_commit(smem_u32(&bar.k_empty[c.slot]));
+                }
+                __syncwarp();
+            }
+        }
     } else {
         set_regs_up<kRegsMath>();
         const int half = warp >> 2, wt = tid & 127;
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // --------------------------------------------------------------------- dK, dV
 struct DkvBars {
-    uint64_t kv_full, kv_empty, q_full[kMaxStages], d_full[kMaxStages], q_empty[kMaxStages], d_empty[kMaxStages];
+    uint64_t kv_full, kv_empty, q_full[kMaxStages], d_full[kMaxStages], q_empty[kMaxStages];
     uint64_t aux_full[kMaxStages], aux_empty[kMaxStages];
     uint64_t s_full, s_free, dp_full, dp_free, p_full, ds_full, dv_done, dk_done;
 };
@@ -448,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bar.q_full[s]), 1);
             mbar_init(smem_u32(&bar.d_full[s]), 1);
             mbar_init(smem_u32(&bar.q_empty[s]), 1);
-            mbar_init(smem_u32(&bar.d_empty[s]), 1);
-            mbar_init(smem_u32(&bar.aux_full[s]), 2);
+            mbar_init(smem_u32(&bar.aux_full[s]), 1);
             mbar_init(smem_u32(&bar.aux_empty[s]), 8);
         }
         mbar_init(smem_u32(&bar.s_full), 1);
@@ -470,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_slot;
     const uint32_t tS = tmem, tD = tmem + 128, tPw = tmem + 256, tDs = tmem + 320, tDv = tmem + 384, tDk = tmem + 448;
     const int steps = p.group * x.qtiles;   // (head, query tile) pairs of a kv head
+    const int tail = tile_cols(p.n - (x.qtiles - 1) * kRows);   // columns of a head's last tile of queries
 
     struct Item {
         int g, b, j0, split, len, u0, u1;
@@ -490,9 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= 8) set_regs_down<kRegsControl>();
-    if (warp >= 10) {
-        // per-query scalars of each tile, 64 threads
-        const int t = tid - 320;
+    if (warp == 11) {
+        // per-query scalars of each tile
         int n = 0;
         Cursor c;
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
@@ -504,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int h = w.g * p.group + u / x.qtiles, q0 = (u % x.qtiles) * kRows;
                 const size_t row0 = ((size_t)w.b * p.heads + h) * p.n;
 #pragma unroll
-                for (int e = t; e < kRows; e += 64) {
+                for (int e = lane; e < kRows; e += 32) {
                     const int i = q0 + e;
                     const bool in = i < p.n;
                     aux[s].nl[e] = neg_lse2(p.lse, row0 + i, in);
@@ -535,91 +534,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (n >= x.stages) wait_on(smem_u32(&bar.q_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
                     mbar_arrive_expect_tx(qf, kTileBytes);
                     load_rows(ring + 2 * s * kTileBytes, &mq, x.uq, q0, h, w.b, qf);
-                    if (n >= x.stages) wait_on(smem_u32(&bar.d_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
                     mbar_arrive_expect_tx(df, kTileBytes);
                     load_rows(ring + (2 * s + 1) * kTileBytes, &md, x.ud, q0, h, w.b, df);
                 }
             }
             for (int s = 0; s < x.stages; ++s) {
                 drain(&bar.q_empty[s], uses_of(n, s, x.stages), x.err);
-                drain(&bar.d_empty[s], uses_of(n, s, x.stages), x.err);
             }
             drain(&bar.kv_empty, items, x.err);
         }
         __syncwarp();
     } else if (warp == 8) {
-        {
-            int n = 0, items = 0;
-            Cursor cq, cd, back;   // the next Q, the next dO, the tile whose weights come next
-            const uint64_t k0 = desc_rows(kv), v0 = desc_rows(kv + kTileBytes), q0 = desc_rows(ring),
-                           d0 = desc_rows(ring + kTileBytes), qt0 = desc_tokens(ring), dt0 = desc_tokens(ring + kTileBytes);
-            constexpr uint32_t kPair = 2 * kTileBytes / 16;
-            for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
-                const Item w = item_of(it);
-                if (w.u0 >= w.u1) continue;
-                wait_on(smem_u32(&bar.kv_full), items & 1, guard, kErrTimeoutLoad);
-                ++items;
-                // columns of a tile: only a head's last one may be short
-                const int tail = tile_cols(p.n - (x.qtiles - 1) * kRows);
-                int qs = w.u0 % x.qtiles, qd = qs, qb = qs;
-                auto cols_of = [&](int &q) __attribute__((always_inline)) {
-                    const int cols = q == x.qtiles - 1 ? tail : kRows;
-                    q = q == x.qtiles - 1 ? 0 : q + 1;
-                    return cols;
-                };
-                auto scores = [&](int k) __attribute__((always_inline)) {
-                    wait_on(smem_u32(&bar.q_full[cq.slot]), cq.phase, guard, kErrTimeoutLoad);
-                    if (k > 0) wait_on(smem_u32(&bar.s_free), (k - 1) & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    const int cols = cols_of(qs);
-                    if (elect_one()) {
-                        mma_rows_rows(tS, k0, q0 + (uint32_t)cq.slot * kPair, cols);
-                        tc_commit(smem_u32(&bar.s_full));
-                    }
-                    __syncwarp();
-                    cq.next(x.stages);
-                };
-                auto slopes = [&](int k, bool last) __attribute__((always_inline)) {
-                    wait_on(smem_u32(&bar.d_full[cd.slot]), cd.phase, guard, kErrTimeoutLoad);
-                    if (k > 0) wait_on(smem_u32(&bar.dp_free), (k - 1) & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    const int cols = cols_of(qd);
-                    if (elect_one()) {
-                        mma_rows_rows(tD, v0, d0 + (uint32_t)cd.slot * kPair, cols);
-                        tc_commit(smem_u32(&bar.dp_full));
-                        if (last) tc_commit(smem_u32(&bar.kv_empty));
-                    }
-                    __syncwarp();
-                    cd.next(x.stages);
-                };
-                scores(n);
-                slopes(n, w.u0 == w.u1 - 1);
-                for (int u = w.u0; u < w.u1; ++u, ++n) {
-                    const bool more = u + 1 < w.u1;
-                    const int s = back.slot, cols = cols_of(qb);
-                    if (more) scores(n + 1);
-                    wait_on(smem_u32(&bar.p_full), n & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        mma_weights_rows(tDv, tPw, dt0 + (uint32_t)s * kPair, cols, u > w.u0);
-                        tc_commit(smem_u32(&bar.dv_done));
-                        tc_commit(smem_u32(&bar.d_empty[s]));
-                    }
-                    __syncwarp();
-                    if (more) slopes(n + 1, u + 2 == w.u1);
-                    wait_on(smem_u32(&bar.ds_full), n & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        mma_weights_rows(tDk, tDs, qt0 + (uint32_t)s * kPair, cols, u > w.u0);
-                        tc_commit(smem_u32(&bar.dk_done));
-                        tc_commit(smem_u32(&bar.q_empty[s]));
-                    }
-                    __syncwarp();
-                    back.next(x.stages);
+        // S^T and dP^T of each tile
+        int n = 0, items = 0;
+        Cursor c;
+        const uint64_t k0 = desc_rows(kv), v0 = desc_rows(kv + kTileBytes), q0 = desc_rows(ring),
+                       d0 = desc_rows(ring + kTileBytes);
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(it);
+            if (w.u0 >= w.u1) continue;
+            wait_on(smem_u32(&bar.kv_full), items & 1, guard, kErrTimeoutLoad);
+            ++items;
+            int qt = w.u0 % x.qtiles;
+            for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
+                const int s = c.slot, cols = qt == x.qtiles - 1 ? tail : kRows;
+                qt = qt == x.qtiles - 1 ? 0 : qt + 1;
+                wait_on(smem_u32(&bar.q_full[s]), c.phase, guard, kErrTimeoutLoad);
+                if (n > 0) wait_on(smem_u32(&bar.s_free), (n - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows_rows(tS, k0, q0 + (uint32_t)s * kPair, cols);
+                    tc_commit(smem_u32(&bar.s_full));
                 }
+                __syncwarp();
+                wait_on(smem_u32(&bar.d_full[s]), c.phase, guard, kErrTimeoutLoad);
+                if (n > 0) wait_on(smem_u32(&bar.dp_free), (n - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows_rows(tD, v0, d0 + (uint32_t)s * kPair, cols);
+                    tc_commit(smem_u32(&bar.dp_full));
+                    if (u == w.u1 - 1) tc_commit(smem_u32(&bar.kv_empty));
+                }
+                __syncwarp();
             }
         }
-        __syncwarp();
+    } else if (warp == 10) {
+        // dV += P^T dO, dK += dS^T Q.  S^T and dP^T have read the tiles too: P and dS come of them.
+        int n = 0;
+        Cursor c;
+        const uint64_t qt0 = desc_tokens(ring), dt0 = desc_tokens(ring + kTileBytes);
+        for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
+            const Item w = item_of(it);
+            int qt = w.u0 % x.qtiles;
+            for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
+                const int s = c.slot, cols = qt == x.qtiles - 1 ? tail : kRows;
+                qt = qt == x.qtiles - 1 ? 0 : qt + 1;
+                wait_on(smem_u32(&bar.p_full), n & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_weights_rows(tDv, tPw, dt0 + (uint32_t)s * kPair, cols, u > w.u0);
+                    tc_commit(smem_u32(&bar.dv_done));
+                }
+                __syncwarp();
+                wait_on(smem_u32(&bar.ds_full), n & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_weights_rows(tDk, tDs, qt0 + (uint32_t)s * kPair, cols, u > w.u0);
+                    tc_commit(smem_u32(&bar.dk_done));
+                    tc_commit(smem_u32(&bar.q_empty[s]));
+                }
+                __syncwarp();
+            }
+        }
     } else {
         set_regs_up<kRegsMath>();
         const int half = warp >> 2, wt = tid & 127;
