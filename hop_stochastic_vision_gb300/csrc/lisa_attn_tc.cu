@@ -39,7 +39,7 @@ struct FwdParams {
     int splits;
     int items;
     int stages;
-    int off_lut, off_keys;   // dynamic shared memory, behind Q and the ring
+    int off_out, off_lut, off_keys;   // dynamic shared memory, behind Q and the ring
 };
 
 struct FwdBars {
@@ -405,23 +405,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 64; ++c) o[c] = 0.f;
             }
-            if (i < p.n) {
-                const float inv = sum != 0.f ? 1.f / sum : 0.f;
-                const float lse = ref == -INFINITY ? -INFINITY : kLn2 * (ref + log2f(sum));
-                const size_t row = ((size_t)w.b * p.heads + w.h) * p.n + i;
-                if (x.splits == 1) {
-                    store_row_bf16(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + (long long)w.b * p.O.sb +
-                                       (long long)w.h * p.O.sh + (long long)i * p.O.st,
-                                   o, inv, p.d);
-                    if (p.lse) p.lse[row] = lse;
-                } else {
-                    const size_t at = (size_t)w.split * ((size_t)p.B * p.heads * p.n) + row;
-                    p.lse_part[at] = lse;
-                    float4 *op = reinterpret_cast<float4 *>(p.o_part + at * p.d);
+            const float inv = sum != 0.f ? 1.f / sum : 0.f;
+            const float lse = ref == -INFINITY ? -INFINITY : kLn2 * (ref + log2f(sum));
+            const size_t row = ((size_t)w.b * p.heads + w.h) * p.n + i;
+            if (x.splits == 1) {
+                const int i0 = i - lane;
+                store_rows_bf16<64>(base + x.off_out + (uint32_t)warp * 4096u, o, inv,
+                                    static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + (long long)w.b * p.O.sb +
+                                        (long long)w.h * p.O.sh + (long long)i0 * p.O.st,
+                                    p.O.st, p.n - i0, p.d, lane);
+                if (p.lse && i < p.n) p.lse[row] = lse;
+            } else if (i < p.n) {
+                const size_t at = (size_t)w.split * ((size_t)p.B * p.heads * p.n) + row;
+                p.lse_part[at] = lse;
+                float4 *op = reinterpret_cast<float4 *>(p.o_part + at * p.d);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4)
-                        if (c < p.d) op[c / 4] = make_float4(o[c] * inv, o[c + 1] * inv, o[c + 2] * inv, o[c + 3] * inv);
-                }
+                for (int c = 0; c < 64; c += 4)
+                    if (c < p.d) op[c / 4] = make_float4(o[c] * inv, o[c + 1] * inv, o[c + 2] * inv, o[c + 3] * inv);
             }
         }
     }
@@ -499,11 +499,13 @@ cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {
     x.items = (int)items;
     const int lut = p.bias.mode ? round1k(p.bias.entries * 4) : 0;
     const int keys = p.bias.mode == 2 ? round1k((p.m + 127) / 128 * 256) : 0;
-    const int fixed = 2 * kTileBytes + lut + keys + 1024;
+    const int out = 8 * 4096;   // a staging block for each softmax warp
+    const int fixed = 2 * kTileBytes + out + lut + keys + 1024;
     const int tiles = (p.m + kRows - 1) / kRows;
     x.stages = std::min(std::min(kMaxStages, (kSmemBudget - fixed) / (2 * kTileBytes)), std::max(2, tiles + 1));
-    if (x.stages < 1) return cudaErrorInvalidValue;
-    x.off_lut = (2 + 2 * x.stages) * kTileBytes;
+    if (x.stages < 2) return cudaErrorInvalidValue;
+    x.off_out = (2 + 2 * x.stages) * kTileBytes;
+    x.off_lut = x.off_out + out;
     x.off_keys = x.off_lut + lut;
     const int bytes = x.off_keys + keys + 1024;
     const unsigned grid = (unsigned)std::min(x.items, sms());

@@ -34,8 +34,17 @@ struct Guard {
     int *err;
     volatile int *dead;
 };
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, const Guard &g, int bit) {
-    if (mbar_test_parity(bar, parity)) return;
+    if (phase_done(bar, parity)) return;
     const long long t0 = clock64();
     while (!mbar_test_parity_suspend(bar, parity)) {
         if (*g.dead) return;
@@ -189,18 +198,32 @@ __device__ __forceinline__ int keys_of(const Problem &p, int b) {
     return p.kv_lens ? min(max(p.kv_lens[b], 0), p.m) : p.m;
 }
 
-// 64 (d) fp32 values of a row to bf16 at 16-byte aligned `out`.
-__device__ __forceinline__ void store_row_bf16(__nv_bfloat16 *out, const float *v, float mul, int d) {
+// 32 rows of a warp, one per lane, to bf16 in memory: through 4 KB of the warp's
+// own shared memory, so that a store instruction writes whole rows (a store per
+// lane and row touches 32 lines each time: 2000 cycles for a tile).
+//   COLS  columns of a lane's row (64 or 32), of which columns < d exist
+//   row0  address of lane 0's row; rows `stride` elements apart, `rows` of them exist
+template <int COLS>
+__device__ __forceinline__ void store_rows_bf16(uint32_t stage, const float *v, float mul, __nv_bfloat16 *row0,
+                                                long long stride, int rows, int d, int lane) {
+    constexpr int kChunks = COLS / 8;
 #pragma unroll
-    for (int c = 0; c < 64; c += 8) {
-        if (c >= d) break;
-        uint4 o;
-        o.x = pack_bf16(v[c] * mul, v[c + 1] * mul);
-        o.y = pack_bf16(v[c + 2] * mul, v[c + 3] * mul);
-        o.z = pack_bf16(v[c + 4] * mul, v[c + 5] * mul);
-        o.w = pack_bf16(v[c + 6] * mul, v[c + 7] * mul);
-        *reinterpret_cast<uint4 *>(out + c) = o;
+    for (int c = 0; c < kChunks; ++c)
+        st_shared_v4(stage + (uint32_t)lane * (COLS * 2) + (uint32_t)((c ^ (lane & (kChunks - 1))) << 4),
+                     pack_bf16(v[8 * c] * mul, v[8 * c + 1] * mul), pack_bf16(v[8 * c + 2] * mul, v[8 * c + 3] * mul),
+                     pack_bf16(v[8 * c + 4] * mul, v[8 * c + 5] * mul), pack_bf16(v[8 * c + 6] * mul, v[8 * c + 7] * mul));
+    __syncwarp();
+    const int c = lane % kChunks;
+#pragma unroll
+    for (int e = 0; e < kChunks; ++e) {
+        const int r = e * (32 / kChunks) + lane / kChunks;
+        if (r < rows && 8 * c < d) {
+            uint4 o;
+            ld_shared_v4(stage + (uint32_t)r * (COLS * 2) + (uint32_t)((c ^ (r & (kChunks - 1))) << 4), o.x, o.y, o.z, o.w);
+            *reinterpret_cast<uint4 *>(row0 + (long long)r * stride + 8 * c) = o;
+        }
     }
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------- host side

@@ -25,6 +25,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 384;      // 8 warps of arithmetic; products (two warps), loads, a helper
+constexpr int kDqOut = 8 * 2048, kDkvOut = 8 * 4096;   // staging blocks of the eight warps
 constexpr int kRegsMath = 208, kRegsControl = 88;
 constexpr int kMaxStages = 4;
 constexpr uint32_t kPair = 2 * kTileBytes / 16;   // a ring stage of two tiles, in descriptor units
@@ -38,7 +39,8 @@ struct BwdParams {
     int splits;            // dK dV: over the (head, query tile) pairs; dbias: over the batch
     int items;
     int stages;
-    int off_lut, off_aux;
+    int q_slots;           // dQ: (Q, dO) pairs held, 2 unless the offset table leaves room for one
+    int off_out, off_lut, off_aux;   // dynamic shared memory, behind the tiles
 };
 
 __device__ __forceinline__ int tile_keys(int len, int t) { return min(kRows, len - t * kRows); }
@@ -136,11 +138,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) DqBars bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
-    __shared__ float other[kRows];
+    __shared__ float other[kRows], rows_delta[kRows];
     const Problem &p = x.p;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
-    const uint32_t qd = base, ring = base + 4 * kTileBytes;   // two slots of (Q, dO); stages of (K, V)
+    const uint32_t qd = base, ring = base + 2 * x.q_slots * kTileBytes;   // slots of (Q, dO); stages of (K, V)
     float *lut = reinterpret_cast<float *>(sm + x.off_lut);
     uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_aux);
     const Guard guard{x.err, &dead};
@@ -195,12 +197,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
         if (lane == 0) {
             int kt = 0, nq = 0;
-            Cursor c;
+            Cursor c, cq;
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(it);
                 if (w.tiles == 0) continue;
-                const int qs = nq & 1, g = w.h / p.group;
-                if (nq >= 2) wait_on(smem_u32(&bar.q_empty[qs]), ((nq >> 1) - 1) & 1, guard, kErrTimeoutMma);
+                const int qs = cq.slot, g = w.h / p.group;
+                if (nq >= x.q_slots) wait_on(smem_u32(&bar.q_empty[qs]), cq.phase ^ 1u, guard, kErrTimeoutMma);
+                cq.next(x.q_slots);
                 const uint32_t f = smem_u32(&bar.q_full[qs]);
                 mbar_arrive_expect_tx(f, 2 * kTileBytes);
                 load_rows(qd + 2 * qs * kTileBytes, &mq, x.uq, w.q0, w.h, w.b, f);
@@ -222,20 +225,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 drain(&bar.k_empty[s], uses_of(kt, s, x.stages), x.err);
                 drain(&bar.v_empty[s], uses_of(kt, s, x.stages), x.err);
             }
-            for (int t = 0; t < 2; ++t) drain(&bar.q_empty[t], uses_of(nq, t, 2), x.err);
+            for (int t = 0; t < x.q_slots; ++t) drain(&bar.q_empty[t], uses_of(nq, t, x.q_slots), x.err);
         }
         __syncwarp();
     } else if (warp == 8) {
         // S and dP of each tile
-        int kt = 0, nq = 0;
-        Cursor c;
+        int kt = 0;
+        Cursor c, cq;
         const uint64_t q0 = desc_rows(qd), k0 = desc_rows(ring), v0 = desc_rows(ring + kTileBytes);
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
             if (w.tiles == 0) continue;
-            const int qs = nq & 1;
-            wait_on(smem_u32(&bar.q_full[qs]), (nq >> 1) & 1, guard, kErrTimeoutLoad);
-            ++nq;
+            const int qs = cq.slot;
+            wait_on(smem_u32(&bar.q_full[qs]), cq.phase, guard, kErrTimeoutLoad);
+            cq.next(x.q_slots);
             const uint64_t qa = q0 + (uint32_t)qs * kPair, da = qa + kTileBytes / 16;
             for (int j = 0; j < w.tiles; ++j, ++kt, c.next(x.stages)) {
                 const int s = c.slot, cols = tile_cols(tile_keys(w.len, j));
@@ -295,26 +298,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool in = i < p.n;
             const size_t row = ((size_t)w.b * p.heads + w.h) * p.n + i;
             const float nl = neg_lse2(p.lse, row, in);
-            float delta = 0.f, exact = 0.f;
-            if (in && w.tiles > 0) {
+            // dO . O of the tile's rows: 8 lanes per row, whole rows per load
+            if (w.tiles > 0) {
                 const __nv_bfloat16 *o = static_cast<const __nv_bfloat16 *>(p.O.p) + (long long)w.b * p.O.sb +
-                                         (long long)w.h * p.O.sh + (long long)i * p.O.st;
+                                         (long long)w.h * p.O.sh;
                 const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(p.dO.p) + (long long)w.b * p.dO.sb +
-                                         (long long)w.h * p.dO.sh + (long long)i * p.dO.st;
+                                         (long long)w.h * p.dO.sh;
+                const int c = 8 * (lane & 7);
+                uint4 a[4], b[4];
 #pragma unroll
-                for (int c = 0; c < 64; c += 8) {
-                    if (c >= p.d) break;
-                    const uint4 a = *reinterpret_cast<const uint4 *>(o + c), b = *reinterpret_cast<const uint4 *>(g + c);
-                    delta = fmaf(bf16_lo(a.x), bf16_lo(b.x), delta);
-                    delta = fmaf(bf16_hi(a.x), bf16_hi(b.x), delta);
-                    delta = fmaf(bf16_lo(a.y), bf16_lo(b.y), delta);
-                    delta = fmaf(bf16_hi(a.y), bf16_hi(b.y), delta);
-                    delta = fmaf(bf16_lo(a.z), bf16_lo(b.z), delta);
-                    delta = fmaf(bf16_hi(a.z), bf16_hi(b.z), delta);
-                    delta = fmaf(bf16_lo(a.w), bf16_lo(b.w), delta);
-                    delta = fmaf(bf16_hi(a.w), bf16_hi(b.w), delta);
+                for (int e = 0; e < 4; ++e) {
+                    const int r = w.q0 + 16 * warp + 4 * e + (lane >> 3);
+                    a[e] = b[e] = make_uint4(0, 0, 0, 0);
+                    if (r < p.n && c < p.d) {
+                        a[e] = *reinterpret_cast<const uint4 *>(o + (long long)r * p.O.st + c);
+                        b[e] = *reinterpret_cast<const uint4 *>(g + (long long)r * p.dO.st + c);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = bf16_lo(a[e].x) * bf16_lo(b[e].x);
+                    v = fmaf(bf16_hi(a[e].x), bf16_hi(b[e].x), v);
+                    v = fmaf(bf16_lo(a[e].y), bf16_lo(b[e].y), v);
+                    v = fmaf(bf16_hi(a[e].y), bf16_hi(b[e].y), v);
+                    v = fmaf(bf16_lo(a[e].z), bf16_lo(b[e].z), v);
+                    v = fmaf(bf16_hi(a[e].z), bf16_hi(b[e].z), v);
+                    v = fmaf(bf16_lo(a[e].w), bf16_lo(b[e].w), v);
+                    v = fmaf(bf16_hi(a[e].w), bf16_hi(b[e].w), v);
+#pragma unroll
+                    for (int m = 4; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+                    if ((lane & 7) == 0) rows_delta[16 * warp + 4 * e + (lane >> 3)] = v;
                 }
             }
+            math_barrier();   // also: the halves of the previous item's delta have been read
+            const float delta = w.tiles > 0 ? rows_delta[wt] : 0.f;
+            float exact = 0.f;
             int oq = 0, oq_lo = 0;
             if (kBias) {
                 const int start = bias_start(p.bias, w.b);
@@ -388,20 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) o[c] = 0.f;
             }
-            math_barrier();   // `other` may be written again; every warp has read dQ before the next ds_full
-            if (in) {
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.dQ) + row * p.d + 32 * half;
-#pragma unroll
-                for (int c = 0; c < 32; c += 8) {
-                    if (32 * half + c >= p.d) break;
-                    uint4 v;
-                    v.x = pack_bf16(o[c] * p.scale, o[c + 1] * p.scale);
-                    v.y = pack_bf16(o[c + 2] * p.scale, o[c + 3] * p.scale);
-                    v.z = pack_bf16(o[c + 4] * p.scale, o[c + 5] * p.scale);
-                    v.w = pack_bf16(o[c + 6] * p.scale, o[c + 7] * p.scale);
-                    *reinterpret_cast<uint4 *>(out + c) = v;
-                }
-            }
+            const int i0 = i - lane;
+            store_rows_bf16<32>(base + x.off_out + (uint32_t)warp * 2048u, o, p.scale,
+                                static_cast<__nv_bfloat16 *>(p.dQ) + (row - lane) * p.d + 32 * half, p.d, p.n - i0,
+                                p.d - 32 * half, lane);
         }
     }
     tc_fence_before();
@@ -742,19 +750,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int c = 0; c < 64; ++c) o[c] = some ? o[c] : 0.f;
-            if (j < p.m) {
-                const size_t row = ((size_t)w.b * p.kv_heads + w.g) * p.m + j;
-                if (x.splits == 1) {
-                    store_row_bf16(static_cast<__nv_bfloat16 *>(half ? p.dK : p.dV) + row * p.d, o, half ? p.scale : 1.f,
-                                   p.d);
-                } else {
-                    float4 *out = reinterpret_cast<float4 *>(
-                        (half ? p.dk_part : p.dv_part) +
-                        ((size_t)w.split * ((size_t)p.B * p.kv_heads * p.m) + row) * p.d);
+            const size_t row = ((size_t)w.b * p.kv_heads + w.g) * p.m + j;
+            if (x.splits == 1) {
+                const int r0 = j - lane;
+                store_rows_bf16<64>(base + x.off_out + (uint32_t)warp * 4096u, o, half ? p.scale : 1.f,
+                                    static_cast<__nv_bfloat16 *>(half ? p.dK : p.dV) + (row - lane) * p.d, p.d,
+                                    p.m - r0, p.d, lane);
+            } else if (j < p.m) {
+                float4 *out = reinterpret_cast<float4 *>(
+                    (half ? p.dk_part : p.dv_part) + ((size_t)w.split * ((size_t)p.B * p.kv_heads * p.m) + row) * p.d);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4)
-                        if (c < p.d) out[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-                }
+                for (int c = 0; c < 64; c += 4)
+                    if (c < p.d) out[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
             }
         }
     }
@@ -1023,9 +1030,14 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
     x.items = (int)items;
     x.first = 1;
-    x.stages = std::min(kMaxStages, (kSmemBudget - 4 * kTileBytes - lut - keys - 1024) / (2 * kTileBytes));
+    for (x.q_slots = 2;; --x.q_slots) {
+        const int left = kSmemBudget - 2 * x.q_slots * kTileBytes - kDqOut - lut - keys - 1024;
+        x.stages = std::min(kMaxStages, left / (2 * kTileBytes));
+        if (x.stages >= 2 || x.q_slots == 1) break;
+    }
     if (x.stages < 2) return cudaErrorInvalidValue;   // a K tile is held until its dQ product, behind the next scores
-    x.off_lut = (4 + 2 * x.stages) * kTileBytes;
+    x.off_out = 2 * (x.q_slots + x.stages) * kTileBytes;
+    x.off_lut = x.off_out + kDqOut;
     x.off_aux = x.off_lut + lut;
     int bytes = x.off_aux + keys + 1024;
     e = p.bias.mode == 0   ? go<tc_dq<0>>(m, x, bytes, s)
@@ -1039,9 +1051,10 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     x.first = 0;
     x.splits = p.q_splits;
     const int aux = (int)sizeof(QueryAux);
-    x.stages = std::min(kMaxStages, (kSmemBudget - 2 * kTileBytes - lut - 1024) / (2 * kTileBytes + aux));
+    x.stages = std::min(kMaxStages, (kSmemBudget - 2 * kTileBytes - kDkvOut - lut - 1024) / (2 * kTileBytes + aux));
     if (x.stages < 2) return cudaErrorInvalidValue;
-    x.off_lut = (2 + 2 * x.stages) * kTileBytes;
+    x.off_out = (2 + 2 * x.stages) * kTileBytes;
+    x.off_lut = x.off_out + kDkvOut;
     x.off_aux = x.off_lut + lut;
     bytes = x.off_aux + x.stages * aux + 1024;
     e = p.bias.mode == 0   ? go<tc_dkdv<0>>(m, x, bytes, s)

@@ -134,6 +134,13 @@ def test_grid_biases(lisa, dtype, d, q, k, step):
     Case(lisa, dtype, 3, 2, 2, q, k, d, bias=_grid(q, k, step), seed=step).check()
 
 
+def test_the_largest_offset_table(lisa):
+    """16296 offsets and as many keys: the shared memory of every kernel at its fullest."""
+    c = Case(lisa, BF16, 1, 1, 1, (1, 1), (168, 97), 64, bias=_grid((1, 1), (168, 97)))
+    c.check()
+    Case(lisa, BF16, 1, 1, 1, (64, 64), (8, 8), 64, bias=_grid((64, 64), (8, 8), 8)).check()
+
+
 def test_grid_bias_with_near_and_far_offsets_in_one_bucket(lisa):
     q, k = (9, 11), (6, 7)
     for rows, cols in ((("exact", 2), ("log", 8, 5)), (("log", 16, 9), ("exact", 0))):
