@@ -13,6 +13,18 @@
 namespace lisa {
 namespace attn {
 
+// Division by a number fixed for the launch: n / d = (umulhi(mul, n) + n) >> shift
+// for 0 <= n < 2^31 (the round-up method for 32-bit dividends, one bit to spare).
+struct FastDiv {
+    unsigned d, mul, shift;
+};
+inline FastDiv fast_div(int d) {
+    FastDiv f{(unsigned)d, 0, 0};
+    while ((1ULL << f.shift) < (unsigned long long)d) ++f.shift;
+    f.mul = (unsigned)((((1ULL << f.shift) - (unsigned long long)d) << 32) / (unsigned long long)d + 1);
+    return f;
+}
+
 // One axis of the bucket rule as the kernels read it.  The log rule's borders
 // are whole numbers found on the host: thr[t] is the smallest |x| of far
 // bucket t + 1 (buckets E + 1, E + 2, ...), so no kernel takes a logarithm.
@@ -37,12 +49,26 @@ struct BiasDev {
     const float *table;
     int heads;
     int q_cols, k_cols, P, step_r, step_c, c0;
+    FastDiv div_q, div_k, div_P;   // by q_cols, k_cols, P
     int start;         // sequence: column start
     const int *starts; // sequence: per batch entry
     int lo_r, lo_c, hi_c;
     int ncol_off;      // grid: column offsets (entries of a row behind it are padding)
     int col_buckets;
     AxisDev rows, cols;
+};
+
+// Sums of pairs over the buckets, tile by tile (lisa_fold.cuh).
+struct FoldDev {
+    int n, m, heads, qtiles, ktiles, parts;   // parts: sums to add up per tile (splits of the batch)
+    FastDiv div_q, div_k;                      // by the grids' columns
+    int start_r, start_c;
+    AxisDev rows, cols;
+    int row_buckets, col_buckets;
+    int nR, K;         // a tile's block: at most nR row differences, K column buckets
+    int units;         // at most so many offsets in a tile
+    int span;          // key tiles that are added side by side for a query tile
+    float *part;       // [parts][heads][qtiles][ktiles][nR][K]
 };
 
 struct Tensor {
@@ -60,7 +86,10 @@ struct Problem {
     BiasDev bias;
     void *dQ, *dK, *dV;
     float *delta;          // [B][heads][n]: sum_j p dP, written by the dQ kernel
-    float *dbias;          // [b_splits][heads][n][m] fp32: dS summed over (parts of) the batch
+    // dS summed over (parts of) the batch: folded tile by tile, or as matrices
+    int folded;
+    FoldDev fold;
+    float *dbias;          // not folded: [b_splits][heads][n][m] fp32
     int b_splits;
     // forward split over the keys
     int splits;
@@ -77,8 +106,14 @@ lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev);
 
 // --- launchers ---------------------------------------------------------------
 cudaError_t launch_bias_dense(const lisa_rel_bias &b, const BiasDev &dev, void *out, int dtype, cudaStream_t s);
+// How the bucket sums of `parts` matrices are taken: tile by tile where the
+// grids have the same spacing, from the matrices otherwise.
+bool fold_plan(const lisa_rel_bias &b, int heads, int parts, FoldDev &f);
+size_t fold_bytes(const FoldDev &f);
+// Adds the tiles' blocks up into dtable.
+cudaError_t launch_fold_sum(const FoldDev &f, float *dtable, cudaStream_t s);
 size_t bias_grad_bytes(const lisa_rel_bias &b, int heads);
-// `parts` matrices one behind the other, added up
+// Bucket sums of `parts` matrices [heads][n][m], one behind the other, added up.
 cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int parts, int dtype,
                              float *dtable, void *ws, cudaStream_t s);
 

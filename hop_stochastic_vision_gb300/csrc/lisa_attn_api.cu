@@ -99,6 +99,9 @@ lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev) {
     const long long P = nc + ((b->q_cols - nc) % 32 + 32) % 32;
     if (nr * P > LISA_MAX_OFFSETS) return LISA_ERR_UNSUPPORTED;
     dev.P = (int)P;
+    dev.div_P = fast_div((int)P);
+    dev.div_q = fast_div(b->q_cols);
+    dev.div_k = fast_div(b->k_cols);
     dev.ncol_off = (int)nc;
     dev.lo_r = -(b->q_rows - 1) - b->start_rows;
     dev.lo_c = -(b->q_cols - 1) - b->start_cols;
@@ -206,6 +209,8 @@ FwdPlan forward_plan(int B, int heads, int n, int m, int d, int dtype) {
 struct BwdPlan {
     bool tc;
     int q_splits, b_splits;
+    bool folded;
+    FoldDev fold;
     size_t off_delta, off_dk, off_dv, off_dbias, off_grad, total;   // the error word is at 0
 };
 
@@ -226,10 +231,11 @@ BwdPlan backward_plan(int B, int heads, int kv_heads, int n, int m, int d, const
     }
     if (bias) {
         if (pl.tc) pl.b_splits = tc_dbias_splits(B, heads, n, m);
+        pl.folded = pl.tc && fold_plan(*bias, heads, pl.b_splits, pl.fold);
         pl.off_dbias = off;
-        off = align_up(off + (size_t)pl.b_splits * heads * n * m * sizeof(float));
+        if (!pl.folded) off = align_up(off + (size_t)pl.b_splits * heads * n * m * sizeof(float));
         pl.off_grad = off;
-        off = align_up(off + bias_grad_bytes(*bias, heads));
+        off = align_up(off + (pl.folded ? fold_bytes(pl.fold) : bias_grad_bytes(*bias, heads)));
     }
     pl.total = off;
     return pl;
@@ -410,6 +416,9 @@ extern "C" lisa_status lisa_cross_attention_backward(
     p.dv_part = reinterpret_cast<float *>(ws + pl.off_dv);
     p.b_splits = pl.b_splits;
     p.dbias = reinterpret_cast<float *>(ws + pl.off_dbias);
+    p.folded = pl.folded;
+    p.fold = pl.fold;
+    p.fold.part = reinterpret_cast<float *>(ws + pl.off_grad);
     cudaError_t e;
     if (pl.tc) {
         e = launch_tc_backward(p, reinterpret_cast<int *>(ws), cs);
@@ -418,8 +427,10 @@ extern "C" lisa_status lisa_cross_attention_backward(
         if (e == cudaSuccess) e = launch_simt_dkdv(p, cs);
         if (e == cudaSuccess && bias) e = launch_simt_dbias(p, cs);
     }
-    // the matrix of the batch's dS, then as the bias matrix's own gradient
-    if (e == cudaSuccess && bias)
+    // the tiles' bucket sums of the batch's dS, or its matrix and then as the bias matrix's own gradient
+    if (e == cudaSuccess && bias && pl.folded)
+        e = launch_fold_sum(p.fold, dtable, cs);
+    else if (e == cudaSuccess && bias)
         e = launch_bias_grad(*bias, p.bias, p.dbias, pl.b_splits, LISA_F32, dtable, ws + pl.off_grad, cs);
     return status_of(e);
 }

@@ -38,6 +38,7 @@ struct FwdParams {
     int qtiles;      // pairs of 128 queries per (batch, head)
     int splits;
     int items;
+    FastDiv div_splits, div_qtiles, div_B, div_group;
     int stages;
     int off_out, off_lut, off_keys;   // dynamic shared memory, behind Q and the ring
 };
@@ -52,14 +53,13 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const FwdParams &x, int it) {
     Item w;
-    w.split = it % x.splits;
-    int r = it / x.splits;
-    w.q0 = (r % x.qtiles) * 2 * kRows;
-    r /= x.qtiles;
-    w.b = r % x.p.B;
-    w.h = r / x.p.B;
+    int qt = split(it, x.div_splits);
+    w.split = it;
+    w.b = split(qt, x.div_qtiles);
+    w.q0 = qt * 2 * kRows;
+    w.h = split(w.b, x.div_B);
     w.len = keys_of(x.p, w.b);
-    const int tiles = (w.len + kRows - 1) / kRows, per = (tiles + x.splits - 1) / x.splits;
+    const int tiles = (w.len + kRows - 1) / kRows, per = quotient(tiles + x.splits - 1, x.div_splits);
     w.t0 = min(w.split * per, tiles);
     w.t1 = min(w.t0 + per, tiles);
     w.nt = x.p.n - w.q0 > kRows ? 2 : 1;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     ++nq[t];
                 };
                 load_q(0);
-                const int g = w.h / p.group;
+                const int g = quotient(w.h, x.div_group);
                 for (int j = w.t0; j < w.t1; ++j, ++kt, c.next(x.stages)) {
                     const int s = c.slot;
                     const uint32_t kf = smem_u32(&bar.k_full[s]), vf = smem_u32(&bar.v_full[s]);
@@ -497,6 +497,10 @@ cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {
     const long long items = (long long)p.B * p.heads * x.qtiles * x.splits;
     if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
     x.items = (int)items;
+    x.div_splits = fast_div(x.splits);
+    x.div_qtiles = fast_div(x.qtiles);
+    x.div_B = fast_div(p.B);
+    x.div_group = fast_div(p.group);
     const int lut = p.bias.mode ? round1k(p.bias.entries * 4) : 0;
     const int keys = p.bias.mode == 2 ? round1k((p.m + 127) / 128 * 256) : 0;
     const int out = 8 * 4096;   // a staging block for each softmax warp

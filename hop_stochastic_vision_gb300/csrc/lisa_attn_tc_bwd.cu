@@ -11,7 +11,8 @@
 //          queries split over CTAs when there are few key tiles, the parts added
 //          in order by a second kernel
 //   dbias  one tile of pairs of a head, the batch one by one, the sum of the
-//          unrounded dS in registers
+//          unrounded dS in registers; then folded over the offsets in shared
+//          memory, so dS never goes to memory
 // Scores are recomputed in each (7 products for 5) so that every sum has one
 // owner: no atomics, no fp32 dQ in memory, the same bits every time.
 //
@@ -19,6 +20,7 @@
 // threads take S and dP into registers as soon as they are there, so the next
 // tile's products run under this tile's arithmetic.
 #include "lisa_attn_tc.cuh"
+#include "lisa_fold.cuh"
 
 namespace lisa {
 namespace attn {
@@ -38,6 +40,7 @@ struct BwdParams {
     int qtiles, ktiles;    // tiles of 128 queries, keys
     int splits;            // dK dV: over the (head, query tile) pairs; dbias: over the batch
     int items;
+    FastDiv div_qtiles, div_ktiles, div_splits, div_B, div_group;
     int stages;
     int q_slots;           // dQ: (Q, dO) pairs held, 2 unless the offset table leaves room for one
     int off_out, off_lut, off_aux;   // dynamic shared memory, behind the tiles
@@ -182,10 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto item_of = [&](int it) {
         Item w;
-        w.q0 = (it % x.qtiles) * kRows;
-        const int r = it / x.qtiles;
-        w.b = r % p.B;
-        w.h = r / p.B;
+        w.b = split(it, x.div_qtiles);
+        w.q0 = it * kRows;
+        w.h = split(w.b, x.div_B);
         w.len = keys_of(p, w.b);
         w.tiles = (w.len + kRows - 1) / kRows;
         return w;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(it);
                 if (w.tiles == 0) continue;
-                const int qs = cq.slot, g = w.h / p.group;
+                const int qs = cq.slot, g = quotient(w.h, x.div_group);
                 if (nq >= x.q_slots) wait_on(smem_u32(&bar.q_empty[qs]), cq.phase ^ 1u, guard, kErrTimeoutMma);
                 cq.next(x.q_slots);
                 const uint32_t f = smem_u32(&bar.q_full[qs]);
@@ -484,14 +486,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto item_of = [&](int it) {
         Item w;
-        w.split = it % x.splits;
-        int r = it / x.splits;
-        w.j0 = (r % x.ktiles) * kRows;
-        r /= x.ktiles;
-        w.b = r % p.B;
-        w.g = r / p.B;
+        int jt = split(it, x.div_splits);
+        w.split = it;
+        w.b = split(jt, x.div_ktiles);
+        w.j0 = jt * kRows;
+        w.g = split(w.b, x.div_B);
         w.len = keys_of(p, w.b);
-        const int per = (steps + x.splits - 1) / x.splits;
+        const int per = quotient(steps + x.splits - 1, x.div_splits);
         w.u0 = min(w.split * per, steps);
         w.u1 = w.j0 < w.len ? min(w.u0 + per, steps) : w.u0;
         return w;
@@ -508,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
                 const int s = c.slot;
                 if (n >= x.stages) wait_on(smem_u32(&bar.aux_empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
-                const int h = w.g * p.group + u / x.qtiles, q0 = (u % x.qtiles) * kRows;
+                int qt = u;
+                    const int h = w.g * p.group + split(qt, x.div_qtiles), q0 = qt * kRows;
                 const size_t row0 = ((size_t)w.b * p.heads + h) * p.n;
 #pragma unroll
                 for (int e = lane; e < kRows; e += 32) {
@@ -537,7 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
                     const int s = c.slot;
                     const uint32_t ph = c.phase;
-                    const int h = w.g * p.group + u / x.qtiles, q0 = (u % x.qtiles) * kRows;
+                    int qt = u;
+                    const int h = w.g * p.group + split(qt, x.div_qtiles), q0 = qt * kRows;
                     const uint32_t qf = smem_u32(&bar.q_full[s]), df = smem_u32(&bar.d_full[s]);
                     if (n >= x.stages) wait_on(smem_u32(&bar.q_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
                     mbar_arrive_expect_tx(qf, kTileBytes);
@@ -563,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w.u0 >= w.u1) continue;
             wait_on(smem_u32(&bar.kv_full), items & 1, guard, kErrTimeoutLoad);
             ++items;
-            int qt = w.u0 % x.qtiles;
+            int qt = w.u0;
+            split(qt, x.div_qtiles);
             for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
                 const int s = c.slot, cols = qt == x.qtiles - 1 ? tail : kRows;
                 qt = qt == x.qtiles - 1 ? 0 : qt + 1;
@@ -593,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t qt0 = desc_tokens(ring), dt0 = desc_tokens(ring + kTileBytes);
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
-            int qt = w.u0 % x.qtiles;
+            int qt = w.u0;
+            split(qt, x.div_qtiles);
             for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
                 const int s = c.slot, cols = qt == x.qtiles - 1 ? tail : kRows;
                 qt = qt == x.qtiles - 1 ? 0 : qt + 1;
@@ -625,7 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item w = item_of(it);
             const int j = w.j0 + wt;
             const int ok = kBias ? off_key(p.bias, min(j, p.m - 1)) : 0;
-            int h = w.g * p.group + w.u0 / x.qtiles, qt = w.u0 % x.qtiles;
+            int qt = w.u0;
+            int h = w.g * p.group + split(qt, x.div_qtiles);
             for (int u = w.u0; u < w.u1; ++u, ++n, ca.next(x.stages), h += qt == x.qtiles - 1, qt = qt == x.qtiles - 1 ? 0 : qt + 1) {
                 if (kBias && h != lut_head) {
                     math_barrier();
@@ -809,7 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t ring = smem_u32(sm);   // stages of (Q, dO, K, V)
     float *lut = reinterpret_cast<float *>(sm + x.off_lut);
-    uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_aux);
+    uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_aux);   // of the item's 128 keys
+    float *tile = reinterpret_cast<float *>(sm + x.off_out), *sums = tile + kFoldTile * kFoldPitch;
     const Guard guard{x.err, &dead};
 
     if (tid == 0) {
@@ -825,8 +832,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 256);
-    if (kBias == 2)
-        for (int j = tid; j < p.m; j += kThreads) key_off[j] = (uint16_t)off_key(p.bias, j);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -838,13 +843,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto item_of = [&](int it) {
         Item w;
-        w.split = it % x.splits;
-        int r = it / x.splits;
-        w.j0 = (r % x.ktiles) * kRows;
-        r /= x.ktiles;
-        w.q0 = (r % x.qtiles) * kRows;
-        w.h = r / x.qtiles;
-        const int per = (p.B + x.splits - 1) / x.splits;
+        int jt = split(it, x.div_splits);
+        w.split = it;
+        int qt = split(jt, x.div_ktiles);
+        w.j0 = jt * kRows;
+        w.h = split(qt, x.div_qtiles);
+        w.q0 = qt * kRows;
+        const int per = quotient(p.B + x.splits - 1, x.div_splits);
         w.b0 = min(w.split * per, p.B);
         w.b1 = min(w.b0 + per, p.B);
         return w;
@@ -866,9 +871,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t f = smem_u32(&bar.full[s]), at = ring + 4 * s * kTileBytes;
                     mbar_arrive_expect_tx(f, 4 * kTileBytes);
                     load_rows(at, &mq, x.uq, w.q0, w.h, b, f);
-                    load_rows(at + 2 * kTileBytes, &mk, x.uk, w.j0, w.h / p.group, b, f);
+                    load_rows(at + 2 * kTileBytes, &mk, x.uk, w.j0, quotient(w.h, x.div_group), b, f);
                     load_rows(at + kTileBytes, &md, x.ud, w.q0, w.h, b, f);
-                    load_rows(at + 3 * kTileBytes, &mv, x.uv, w.j0, w.h / p.group, b, f);
+                    load_rows(at + 3 * kTileBytes, &mv, x.uv, w.j0, quotient(w.h, x.div_group), b, f);
                     ++n;
                     c.next(x.stages);
                 }
@@ -924,6 +929,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 math_barrier();
                 lut_head = w.h;
             }
+            if (kBias == 2) {   // the previous item's are read: every warp has passed its fold
+                if (tid < kRows) key_off[tid] = (uint16_t)off_key(p.bias, min(w.j0 + tid, p.m - 1));
+                math_barrier();
+            }
             const int i = w.q0 + wt, j0 = w.j0 + 64 * half;
             const bool in = i < p.n;
             const int oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, p.bias.start);
@@ -944,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_strip(tS + 64 * half + lanes, s);
                 tc_fence_before();
                 arrive_warp(&bar.s_free, lane);
-                if (any) row_weights<kBias>(s, p.bias, lut, key_off, j0, keys, oq, oq_lo, scale2, nl);
+                if (any) row_weights<kBias>(s, p.bias, lut, key_off - w.j0, j0, keys, oq, oq_lo, scale2, nl);
                 wait_on(smem_u32(&bar.dp_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
 #pragma unroll
@@ -967,11 +976,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 arrive_warp(&bar.dp_free, lane);
                 ++n;
             }
-            if (in) {
-                float *out = p.dbias + ((size_t)w.split * p.heads + w.h) * ((size_t)p.n * p.m) + (size_t)i * p.m + j0;
+            float4 *mine = reinterpret_cast<float4 *>(tile + wt * kFoldPitch + 64 * half);
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (j0 + c < p.m) out[c] = acc[c];
+            for (int c = 0; c < 64; c += 4) mine[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+            math_barrier();
+            if (p.folded) {
+                const TileGeom g = fold_geom(p.fold, w.q0 / kFoldTile, w.j0 / kFoldTile);
+                fold_offsets(p.fold, g, tile, sums, tid, 256);
+                math_barrier();
+                fold_buckets(p.fold, g, sums, fold_block(p.fold, w.split, w.h, w.q0 / kFoldTile, w.j0 / kFoldTile), tid,
+                             256);
+            } else {
+                float *out = p.dbias + ((size_t)w.split * p.heads + w.h) * ((size_t)p.n * p.m) + (size_t)w.q0 * p.m + w.j0;
+                for (int r = warp; r < min(kRows, p.n - w.q0); r += 8)
+                    for (int c = lane; c < min(kRows, p.m - w.j0); c += 32)
+                        out[(size_t)r * p.m + c] = tile[r * kFoldPitch + c];
+                math_barrier();
             }
         }
     }
@@ -988,6 +1008,12 @@ bool fill_maps(Maps &m, BwdParams &x, const Problem &p) {
     x.p = p;
     x.qtiles = (p.n + kRows - 1) / kRows;
     x.ktiles = (p.m + kRows - 1) / kRows;
+    x.splits = 1;
+    x.div_qtiles = fast_div(x.qtiles);
+    x.div_ktiles = fast_div(x.ktiles);
+    x.div_splits = fast_div(1);
+    x.div_B = fast_div(p.B);
+    x.div_group = fast_div(p.group);
     return make_map(&m.q, &x.uq, p.Q, p.B, p.heads, p.n, p.d) && make_map(&m.d, &x.ud, p.dO, p.B, p.heads, p.n, p.d) &&
            make_map(&m.k, &x.uk, p.K, p.B, p.kv_heads, p.m, p.d) &&
            make_map(&m.v, &x.uv, p.V, p.B, p.kv_heads, p.m, p.d);
@@ -1050,6 +1076,7 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     x.items = (int)items;
     x.first = 0;
     x.splits = p.q_splits;
+    x.div_splits = fast_div(x.splits);
     const int aux = (int)sizeof(QueryAux);
     x.stages = std::min(kMaxStages, (kSmemBudget - 2 * kTileBytes - kDkvOut - lut - 1024) / (2 * kTileBytes + aux));
     if (x.stages < 2) return cudaErrorInvalidValue;
@@ -1072,11 +1099,14 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
     x.items = (int)items;
     x.splits = p.b_splits;
-    x.stages = std::min(kMaxStages, (kSmemBudget - lut - keys - 1024) / (4 * kTileBytes));
+    x.div_splits = fast_div(x.splits);
+    const int fold = kFoldTileBytes + (p.folded ? round1k(p.fold.units * 4) : 0);
+    x.stages = std::min(kMaxStages, (kSmemBudget - fold - lut - 2048) / (4 * kTileBytes));
     if (x.stages < 1) return cudaErrorInvalidValue;
-    x.off_lut = 4 * x.stages * kTileBytes;
+    x.off_out = 4 * x.stages * kTileBytes;
+    x.off_lut = round1k(x.off_out + fold);
     x.off_aux = x.off_lut + lut;
-    bytes = x.off_aux + keys + 1024;
+    bytes = x.off_aux + 256 + 1024;
     return p.bias.mode == 1 ? go<tc_dbias<1>>(m, x, bytes, s) : go<tc_dbias<2>>(m, x, bytes, s);
 }
 

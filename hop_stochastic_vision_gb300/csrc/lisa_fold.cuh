@@ -1,0 +1,117 @@
+// lisa_fold.cuh -- sums of a 128 x 128 tile of pairs over the buckets of the
+// relative position, for grids of the same spacing (key steps of 1).
+//
+// The tile is in shared memory.  All its pairs with one offset (dr, dc) lie on
+// diagonals of the blocks that the grids' rows cut it into, so a thread owns an
+// offset and walks them: neighbouring threads read neighbouring keys of one row
+// (no bank conflict, no atomics, a fixed order).  The offsets' sums are then
+// folded into the column buckets and left as one small block per tile,
+// [offset rows][columns]; a second kernel adds the tiles up.  The matrix itself
+// never goes to memory.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "lisa_attn.h"
+#include "lisa_bias_dev.cuh"
+
+namespace lisa {
+namespace attn {
+namespace {
+
+constexpr int kFoldTile = 128;
+constexpr int kFoldPitch = 132;       // floats; rows 16-byte aligned, 4 banks apart
+constexpr int kFoldTileBytes = kFoldTile * kFoldPitch * 4;
+
+struct TileGeom {
+    int q0, j0, nq, nk;
+    int rq0, rq1, rk0, rk1;
+    int dr_lo, dr_n;       // row differences rk - rq
+    int dc_lo, dc_n;       // column differences ck - cq
+    int cb_lo, cb_n;       // column buckets
+};
+
+__device__ __forceinline__ TileGeom fold_geom(const FoldDev &f, int it, int jt) {
+    TileGeom g;
+    g.q0 = it * kFoldTile;
+    g.j0 = jt * kFoldTile;
+    g.nq = min(kFoldTile, f.n - g.q0);
+    g.nk = min(kFoldTile, f.m - g.j0);
+    int c0 = g.q0, c1 = g.q0 + g.nq - 1, e0 = g.j0, e1 = g.j0 + g.nk - 1;
+    g.rq0 = split(c0, f.div_q);
+    g.rq1 = split(c1, f.div_q);
+    g.rk0 = split(e0, f.div_k);
+    g.rk1 = split(e1, f.div_k);
+    if (g.rq0 != g.rq1) { c0 = 0; c1 = (int)f.div_q.d - 1; }
+    if (g.rk0 != g.rk1) { e0 = 0; e1 = (int)f.div_k.d - 1; }
+    g.dr_lo = g.rk0 - g.rq1;
+    g.dr_n = g.rk1 - g.rq0 - g.dr_lo + 1;
+    g.dc_lo = e0 - c1;
+    g.dc_n = e1 - c0 - g.dc_lo + 1;
+    if (f.cols.log_rule) {
+        g.cb_lo = 0;
+        g.cb_n = f.col_buckets;
+    } else {
+        const int D = f.cols.D, lo = g.dc_lo - f.start_c, hi = lo + g.dc_n - 1;
+        g.cb_lo = min(max(lo, -D), D) + D;
+        g.cb_n = min(max(hi, -D), D) + D - g.cb_lo + 1;
+    }
+    return g;
+}
+
+// Sums of the tile's offsets into `sums` (dr_n x dc_n), `threads` threads.
+__device__ __forceinline__ void fold_offsets(const FoldDev &f, const TileGeom &g, const float *tile, float *sums, int tid,
+                                             int threads) {
+    const int wq = (int)f.div_q.d, wk = (int)f.div_k.d;
+    for (int u = tid; u < g.dr_n * g.dc_n; u += threads) {
+        const int dri = u / g.dc_n, dr = g.dr_lo + dri, dc = g.dc_lo + (u - dri * g.dc_n);
+        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+        for (int rq = max(g.rq0, g.rk0 - dr); rq <= min(g.rq1, g.rk1 - dr); ++rq) {
+            const int qb = rq * wq - g.q0, kb = (rq + dr) * wk - g.j0;   // tile row of cq = 0, column of ck = 0
+            const int lo = max(max(0, -qb), max(0, -kb) - dc);
+            const int hi = min(min(wq - 1, g.nq - 1 - qb), min(wk - 1, g.nk - 1 - kb) - dc);
+            const float *p = tile + (qb + lo) * kFoldPitch + kb + lo + dc;
+            int c = lo;
+            for (; c + 3 <= hi; c += 4, p += 4 * (kFoldPitch + 1)) {
+                a0 += p[0];
+                a1 += p[kFoldPitch + 1];
+                a2 += p[2 * (kFoldPitch + 1)];
+                a3 += p[3 * (kFoldPitch + 1)];
+            }
+            for (; c <= hi; ++c, p += kFoldPitch + 1) a0 += *p;
+        }
+        sums[u] = (a0 + a1) + (a2 + a3);
+    }
+}
+
+// The offsets' sums into the tile's block of column buckets, [dr_n][f.K]; eight
+// lanes share a bucket (far buckets hold up to 255 offsets).
+__device__ __forceinline__ void fold_buckets(const FoldDev &f, const TileGeom &g, const float *sums, float *out, int tid,
+                                             int threads) {
+    const int lane = tid & 7;
+    const int total = g.dr_n * g.cb_n, rounds = (total * 8 + threads - 1) / threads;
+    for (int r = 0; r < rounds; ++r) {
+        const int u = (r * threads + tid) >> 3;
+        const int dri = u / g.cb_n, c = u - dri * g.cb_n;
+        float s = 0.f;
+        if (u < total) {
+            int lo, hi;
+            bucket_range(f.cols, g.cb_lo + c, lo, hi);
+            lo = max(lo + f.start_c - g.dc_lo, 0);
+            hi = min(hi + f.start_c - g.dc_lo, g.dc_n - 1);
+            for (int x = lo + lane; x <= hi; x += 8) s += sums[dri * g.dc_n + x];
+        }
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 4);
+        if (u < total && lane == 0) out[dri * f.K + c] = s;
+    }
+}
+
+__device__ __forceinline__ float *fold_block(const FoldDev &f, int part, int h, int it, int jt) {
+    return f.part + ((((size_t)part * f.heads + h) * f.qtiles + it) * f.ktiles + jt) * ((size_t)f.nR * f.K);
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace lisa

@@ -6,12 +6,14 @@
 
 #include "lisa_attn.h"
 #include "lisa_bias_dev.cuh"
+#include "lisa_fold.cuh"
 
 namespace lisa {
 namespace attn {
 namespace {
 
 constexpr int kDenseThreads = 256;
+constexpr int kMaxFoldUnits = 2048;   // offsets of a tile that are folded in shared memory
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
@@ -82,6 +84,8 @@ struct GradParams {
     float *part;   // [heads][q_rows][k_rows][nchunk][ntile][col_buckets]
 };
 
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float get(const float *p) { return __ldg(p); }
 __device__ __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 
@@ -180,6 +184,107 @@ __global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ Gr
     }
 }
 
+// ------------------------------------------------- gradient, tile by tile
+// One 128 x 128 tile of one head: loaded whole (every load of a thread in
+// flight at once, so three CTAs keep some 190 KB per SM on the way), then folded.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) fold_matrix(const __grid_constant__ FoldDev f, const T *dbias, int matrices) {
+    extern __shared__ __align__(16) float fold_smem[];
+    float *tile = fold_smem, *sums = fold_smem + kFoldTile * kFoldPitch;
+    const int tid = threadIdx.x, jt = blockIdx.x, it = blockIdx.y, h = blockIdx.z;
+    const TileGeom g = fold_geom(f, it, jt);
+    constexpr int kPerRow = kFoldTile / VEC, kRowsAtOnce = 256 / kPerRow, kLoads = kFoldTile / kRowsAtOnce;
+    constexpr int kBatch = kLoads < 16 ? kLoads : 16;
+    const int r0 = tid / kPerRow, c = (tid % kPerRow) * VEC;
+    for (int part = 0; part < matrices; ++part) {
+        const T *src = dbias + ((size_t)part * f.heads + h) * ((size_t)f.n * f.m) + (size_t)g.q0 * f.m + g.j0;
+        for (int b = 0; b < kLoads; b += kBatch) {
+            struct __align__(sizeof(T) * VEC) Vec { T v[VEC]; };
+            Vec x[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const int r = r0 + (b + e) * kRowsAtOnce;
+                if (r < g.nq && c < g.nk)   // a vector is whole or absent: m is a multiple of VEC where VEC > 1
+                    x[e] = *reinterpret_cast<const Vec *>(src + (size_t)r * f.m + c);
+                else
+#pragma unroll
+                    for (int u = 0; u < VEC; ++u) put(&x[e].v[u], 0.f);
+            }
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                float *t = tile + (r0 + (b + e) * kRowsAtOnce) * kFoldPitch + c;
+#pragma unroll
+                for (int u = 0; u < VEC; ++u) t[u] = (part > 0 ? t[u] : 0.f) + to_float(x[e].v[u]);
+            }
+        }
+    }
+    __syncthreads();
+    fold_offsets(f, g, tile, sums, tid, 256);
+    __syncthreads();
+    fold_buckets(f, g, sums, fold_block(f, 0, h, it, jt), tid, 256);
+}
+
+// dtable of a row bucket: its share of the tiles' blocks, `groups` runs of tiles
+// added side by side by `width` columns of threads.
+__global__ void __launch_bounds__(1024) fold_sum(const __grid_constant__ FoldDev f, float *dtable, int width, int groups) {
+    __shared__ float acc_s[1024];
+    const int rb = blockIdx.x, h = blockIdx.z;
+    const int c = threadIdx.x % width, grp = threadIdx.x / width;
+    const int cb = blockIdx.y * width + c;
+    int lo, hi;
+    bucket_range(f.rows, rb, lo, hi);
+    lo = max(lo, -kFar / 2) + f.start_r;   // row differences rk - rq of this bucket
+    hi = min(hi, kFar / 2) + f.start_r;
+    float acc = 0.f;
+    if (cb < f.col_buckets) {
+        const int wk = (int)f.div_k.d, last = quotient(f.m - 1, f.div_k);
+        for (int x = grp; x < f.qtiles * f.span; x += groups) {
+            const int it = x / f.span;
+            // key tiles whose rows can hold rq + lo .. rq + hi
+            const int q0 = it * kFoldTile, q1 = min(q0 + kFoldTile, f.n) - 1;
+            const int r0 = quotient(q0, f.div_q) + lo, r1 = quotient(q1, f.div_q) + hi;
+            if (r1 < 0 || r0 > last) continue;
+            const int j1 = min((min(r1, last) * wk + wk - 1) / kFoldTile, f.ktiles - 1);
+            for (int jt = max(r0, 0) * wk / kFoldTile + (x - it * f.span); jt <= j1; jt += f.span) {
+                const TileGeom g = fold_geom(f, it, jt);
+                if (cb < g.cb_lo || cb >= g.cb_lo + g.cb_n) continue;
+                const int d0 = max(lo, g.dr_lo), d1 = min(hi, g.dr_lo + g.dr_n - 1);
+                for (int part = 0; part < f.parts; ++part) {
+                    const float *b = fold_block(f, part, h, it, jt) + cb - g.cb_lo;
+                    for (int d = d0; d <= d1; ++d) acc += b[(size_t)(d - g.dr_lo) * f.K];
+                }
+            }
+        }
+    }
+    acc_s[threadIdx.x] = acc;
+    __syncthreads();
+    if (grp == 0 && cb < f.col_buckets) {
+        float s = 0.f;
+        for (int u = 0; u < groups; ++u) s += acc_s[u * width + c];
+        dtable[((size_t)rb * f.col_buckets + cb) * f.heads + h] = s;
+    }
+}
+
+template <typename T>
+cudaError_t run_fold(const FoldDev &f, const T *dbias, int matrices, cudaStream_t s) {
+    const int bytes = kFoldTileBytes + f.units * 4;
+    const dim3 grid((unsigned)f.ktiles, (unsigned)f.qtiles, (unsigned)f.heads);
+    const auto go = [&](auto kernel) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kFoldTileBytes + kMaxFoldUnits * 4);
+        if (e != cudaSuccess) return e;
+        kernel<<<grid, 256, bytes, s>>>(f, dbias, matrices);
+        return cudaGetLastError();
+    };
+    // the widest vector that every row begins on
+    constexpr int kFull = 16 / (int)sizeof(T);
+    const bool base16 = (reinterpret_cast<uintptr_t>(dbias) & 15u) == 0;
+    if (base16 && f.m % kFull == 0) return go(fold_matrix<T, kFull>);
+    if (base16 && f.m % (kFull / 2) == 0) return go(fold_matrix<T, kFull / 2>);
+    if (sizeof(T) == 2 && base16 && f.m % 2 == 0) return go(fold_matrix<T, 2>);
+    return go(fold_matrix<T, 1>);
+}
+
 void grad_plan(const lisa_rel_bias &b, GradParams &g) {
     g.q_rows = b.q_rows; g.q_cols = b.q_cols;
     g.k_rows = b.k_rows; g.k_cols = b.k_cols;
@@ -223,7 +328,50 @@ cudaError_t launch_bias_dense(const lisa_rel_bias &b, const BiasDev &dev, void *
     return cudaGetLastError();
 }
 
+bool fold_plan(const lisa_rel_bias &b, int heads, int parts, FoldDev &f) {
+    f = FoldDev{};
+    if (b.key_step_rows != 1 || b.key_step_cols != 1) return false;
+    BiasDev dev;
+    if (bias_dev(&b, heads, dev) != LISA_OK) return false;
+    f.n = b.q_rows * b.q_cols;
+    f.m = b.k_rows * b.k_cols;
+    f.heads = heads;
+    f.parts = parts;
+    f.qtiles = (f.n + kFoldTile - 1) / kFoldTile;
+    f.ktiles = (f.m + kFoldTile - 1) / kFoldTile;
+    f.div_q = fast_div(b.q_cols);
+    f.div_k = fast_div(b.k_cols);
+    f.start_r = b.start_rows;
+    f.start_c = b.start_cols;
+    f.rows = dev.rows;
+    f.cols = dev.cols;
+    f.row_buckets = b.rows.buckets;
+    f.col_buckets = b.cols.buckets;
+    // rows of a grid that 128 of its tokens can touch
+    const int qr = std::min(b.q_rows, (kFoldTile - 2) / b.q_cols + 2), kr = std::min(b.k_rows, (kFoldTile - 2) / b.k_cols + 2);
+    f.nR = qr + kr - 1;
+    const int width = std::min(kFoldTile, b.q_cols) + std::min(kFoldTile, b.k_cols) - 1;
+    f.K = dev.cols.log_rule ? b.cols.buckets : std::min(b.cols.buckets, width);
+    f.units = f.nR * width;
+    // key tiles that hold one row difference of a query tile's rows (a bucket of several takes more turns)
+    f.span = (int)std::min<long long>(f.ktiles, ((long long)qr * b.k_cols + kFoldTile - 2) / kFoldTile + 1);
+    return f.units <= kMaxFoldUnits && f.qtiles <= 65535;
+}
+
+size_t fold_bytes(const FoldDev &f) {
+    return (size_t)f.parts * f.heads * f.qtiles * f.ktiles * f.nR * f.K * sizeof(float);
+}
+
+cudaError_t launch_fold_sum(const FoldDev &f, float *dtable, cudaStream_t s) {
+    const int width = std::min(256, (f.col_buckets + 31) / 32 * 32), groups = 1024 / width;
+    fold_sum<<<dim3((unsigned)f.row_buckets, (unsigned)((f.col_buckets + width - 1) / width), (unsigned)f.heads),
+               width * groups, 0, s>>>(f, dtable, width, groups);
+    return cudaGetLastError();
+}
+
 size_t bias_grad_bytes(const lisa_rel_bias &b, int heads) {
+    FoldDev f;
+    if (fold_plan(b, heads, 1, f)) return fold_bytes(f);
     GradParams g{};
     grad_plan(b, g);
     return (size_t)heads * g.q_rows * g.k_rows * g.nchunk * g.ntile * g.col_buckets * sizeof(float);
@@ -231,6 +379,13 @@ size_t bias_grad_bytes(const lisa_rel_bias &b, int heads) {
 
 cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int parts, int dtype,
                              float *dtable, void *ws, cudaStream_t s) {
+    FoldDev f;
+    if (fold_plan(b, dev.heads, 1, f)) {
+        f.part = static_cast<float *>(ws);
+        cudaError_t e = dtype == LISA_BF16 ? run_fold(f, static_cast<const __nv_bfloat16 *>(dbias), parts, s)
+                                           : run_fold(f, static_cast<const float *>(dbias), parts, s);
+        return e != cudaSuccess ? e : launch_fold_sum(f, dtable, s);
+    }
     GradParams g{};
     g.b = dev;
     g.parts = parts;
