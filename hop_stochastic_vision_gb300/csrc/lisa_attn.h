@@ -47,6 +47,8 @@ struct BiasDev {
     int mode;          // 0 none, 1 sequence, 2 grid
     int entries;
     const float *table;
+    const float *offsets;   // tensor-core kernels: [heads][offsets_pitch], the table by offset, times log2(e)
+    int offsets_pitch;
     int heads;
     int q_cols, k_cols, P, step_r, step_c, c0;
     FastDiv div_q, div_k, div_P;   // by q_cols, k_cols, P
@@ -121,6 +123,10 @@ cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dq(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dkdv(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dbias(const Problem &p, cudaStream_t s);
+
+// The table by offset, times log2(e), into bias.offsets.
+size_t offsets_bytes(const BiasDev &b);
+cudaError_t launch_offsets(const BiasDev &b, float *out, cudaStream_t s);
 
 // bf16 on the tensor cores; `err` is the error word of the call's workspace
 int tc_forward_splits(int B, int heads, int n, int m);

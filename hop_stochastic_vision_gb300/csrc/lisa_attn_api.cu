@@ -91,6 +91,7 @@ lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev) {
         dev.lo_c = (int)lo;
         dev.hi_c = (int)hi;
         dev.entries = (int)(hi - lo + 1);
+        dev.offsets_pitch = (dev.entries + 63) / 64 * 64;
         return LISA_OK;
     }
     if (b->starts) return LISA_ERR_INVALID_ARG;
@@ -107,6 +108,7 @@ lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev) {
     dev.lo_c = -(b->q_cols - 1) - b->start_cols;
     dev.c0 = (b->q_rows - 1) * dev.P + b->q_cols - 1;
     dev.entries = (int)(nr * P);
+    dev.offsets_pitch = (dev.entries + 63) / 64 * 64;
     return LISA_OK;
 }
 
@@ -185,10 +187,11 @@ lisa_status fill(Problem &p, const void *Q, const lisa_strides *qs, const void *
 struct FwdPlan {
     bool tc;
     int splits;
-    size_t off_lse, off_o, total;   // the error word is at 0
+    size_t off_lse, off_o, off_table, total;   // the error word is at 0
 };
 
-FwdPlan forward_plan(int B, int heads, int n, int m, int d, int dtype) {
+// `table`: bytes of the bias table by offset.
+FwdPlan forward_plan(int B, int heads, int n, int m, int d, int dtype, size_t table) {
     FwdPlan pl{};
     pl.splits = 1;
     pl.tc = dtype == LISA_BF16 && m > 0;
@@ -202,6 +205,8 @@ FwdPlan forward_plan(int B, int heads, int n, int m, int d, int dtype) {
         pl.off_o = off;
         off = align_up(off + rows * d * sizeof(float));
     }
+    pl.off_table = off;
+    off = align_up(off + table);
     pl.total = off;
     return pl;
 }
@@ -211,7 +216,7 @@ struct BwdPlan {
     int q_splits, b_splits;
     bool folded;
     FoldDev fold;
-    size_t off_delta, off_dk, off_dv, off_dbias, off_grad, total;   // the error word is at 0
+    size_t off_delta, off_dk, off_dv, off_table, off_dbias, off_grad, total;   // the error word is at 0
 };
 
 BwdPlan backward_plan(int B, int heads, int kv_heads, int n, int m, int d, const lisa_rel_bias *bias, int dtype) {
@@ -231,6 +236,9 @@ BwdPlan backward_plan(int B, int heads, int kv_heads, int n, int m, int d, const
     }
     if (bias) {
         if (pl.tc) pl.b_splits = tc_dbias_splits(B, heads, n, m);
+        pl.off_table = off;
+        BiasDev dev;
+        if (pl.tc && bias_dev(bias, heads, dev) == LISA_OK) off = align_up(off + offsets_bytes(dev));
         pl.folded = pl.tc && fold_plan(*bias, heads, pl.b_splits, pl.fold);
         pl.off_dbias = off;
         if (!pl.folded) off = align_up(off + (size_t)pl.b_splits * heads * n * m * sizeof(float));
@@ -300,7 +308,9 @@ extern "C" lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, in
 extern "C" size_t lisa_cross_attention_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,
                                                        int dtype) {
     if (check_sizes(B, heads, kv_heads, n, m, d, dtype) != LISA_OK || B == 0 || heads == 0 || n == 0) return 0;
-    return forward_plan(B, heads, n, m, d, dtype).total;
+    // whatever the bias: its table by offset has at most LISA_MAX_OFFSETS entries per head
+    const size_t table = (size_t)heads * LISA_MAX_OFFSETS * sizeof(float);
+    return forward_plan(B, heads, n, m, d, dtype, table).total;
 }
 
 extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q_strides, const void *K,
@@ -324,7 +334,7 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
         return LISA_ERR_INVALID_ARG;
     p.O = {O, o_strides->batch, o_strides->head, o_strides->token};
     p.lse = lse;
-    const FwdPlan pl = forward_plan(B, heads, n, m, d, dtype);
+    const FwdPlan pl = forward_plan(B, heads, n, m, d, dtype, p.bias.mode ? offsets_bytes(p.bias) : 0);
     if (pl.total > 0) {
         if (!workspace || workspace_bytes < pl.total) return LISA_ERR_WORKSPACE;
         if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
@@ -335,6 +345,12 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
     p.splits = pl.splits;
     p.lse_part = reinterpret_cast<float *>(ws + pl.off_lse);
     p.o_part = reinterpret_cast<float *>(ws + pl.off_o);
+    if (p.bias.mode) {
+        float *t = reinterpret_cast<float *>(ws + pl.off_table);
+        const cudaError_t e = launch_offsets(p.bias, t, cs);
+        if (e != cudaSuccess) return LISA_ERR_CUDA;
+        p.bias.offsets = t;
+    }
     return status_of(launch_tc_forward(p, reinterpret_cast<int *>(ws), cs));
 }
 
@@ -421,7 +437,13 @@ extern "C" lisa_status lisa_cross_attention_backward(
     p.fold.part = reinterpret_cast<float *>(ws + pl.off_grad);
     cudaError_t e;
     if (pl.tc) {
-        e = launch_tc_backward(p, reinterpret_cast<int *>(ws), cs);
+        e = cudaSuccess;
+        if (bias) {
+            float *t = reinterpret_cast<float *>(ws + pl.off_table);
+            e = launch_offsets(p.bias, t, cs);
+            p.bias.offsets = t;
+        }
+        if (e == cudaSuccess) e = launch_tc_backward(p, reinterpret_cast<int *>(ws), cs);
     } else {
         e = launch_simt_dq(p, cs);
         if (e == cudaSuccess) e = launch_simt_dkdv(p, cs);

@@ -45,7 +45,7 @@ struct FwdParams {
 
 struct FwdBars {
     uint64_t q_full[2], q_empty[2], k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages], v_empty[kMaxStages];
-    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], lut_full;
 };
 
 struct Item {
@@ -75,12 +75,11 @@ struct RowState {
     int oq, oq_lo;
 };
 
-// Bias of 128 columns from key j0: s -> scale2 s + bias, or one value for all of
-// them (the return value's use: 2^(mul s + add)).
-template <int kBias, bool kFull>
-__device__ __forceinline__ void add_bias(float (&s)[128], const BiasDev &b, const float *lut, const uint16_t *key_off,
-                                         int j0, int keys, int cols, const RowState &r, float scale2, float &mul,
-                                         float &add) {
+// Bias of N columns from key j0: s -> scale2 s + bias, or one value for all of
+// them (2^(mul s + add) is what comes of it).
+template <int kBias, int N>
+__device__ __forceinline__ void add_bias(float (&s)[N], const BiasDev &b, const float *lut, const uint16_t *key_off,
+                                         int j0, int keys, const RowState &r, float scale2, float &mul, float &add) {
     mul = scale2;
     add = 0.f;
     if (kBias == 1) {
@@ -90,35 +89,26 @@ __device__ __forceinline__ void add_bias(float (&s)[128], const BiasDev &b, cons
         } else {
             const int off = b.step_c * j0 - r.oq;
             mul = 1.f;
-            if (b.step_c == 1 && lo >= 0 && lo + 31 + 127 <= last) {
+            if (b.step_c == 1 && lo >= 0 && lo + 31 + N - 1 <= last) {
                 const float *l = lut + off;
 #pragma unroll
-                for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], scale2, l[c]);
+                for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], scale2, l[c]);
             } else {
 #pragma unroll
-                for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], scale2, lut[min(max(off + b.step_c * c, 0), last)]);
+                for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], scale2, lut[min(max(off + b.step_c * c, 0), last)]);
             }
         }
     } else if (kBias == 2) {
-        // inside the table by construction; columns behind the last key are clamped into it
+        // inside the table by construction (key_off repeats the last key behind the end)
         mul = 1.f;
         const float *l = lut - r.oq;
-        const int top = b.entries - 1 + r.oq;
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-            if (!kFull && (c & ~31) >= cols) break;
+        for (int c = 0; c < N; c += 4) {
             const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
-            int i0 = (int)(a.x & 0xFFFFu), i1 = (int)(a.x >> 16), i2 = (int)(a.y & 0xFFFFu), i3 = (int)(a.y >> 16);
-            if (!kFull) {
-                i0 = min(max(i0, r.oq), top);
-                i1 = min(max(i1, r.oq), top);
-                i2 = min(max(i2, r.oq), top);
-                i3 = min(max(i3, r.oq), top);
-            }
-            s[c] = fmaf(s[c], scale2, l[i0]);
-            s[c + 1] = fmaf(s[c + 1], scale2, l[i1]);
-            s[c + 2] = fmaf(s[c + 2], scale2, l[i2]);
-            s[c + 3] = fmaf(s[c + 3], scale2, l[i3]);
+            s[c] = fmaf(s[c], scale2, l[a.x & 0xFFFFu]);
+            s[c + 1] = fmaf(s[c + 1], scale2, l[a.x >> 16]);
+            s[c + 2] = fmaf(s[c + 2], scale2, l[a.y & 0xFFFFu]);
+            s[c + 3] = fmaf(s[c + 3], scale2, l[a.y >> 16]);
         }
     }
 }
@@ -155,17 +145,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(smem_u32(&bar.k_empty[s]), 2);   // one for each tile
             mbar_init(smem_u32(&bar.v_empty[s]), 2);
         }
+        mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
         fence_mbar_init();
-        if (blockIdx.x == 0) *x.err = 0;
     }
     if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 512);
     if (kBias == 2)
-        for (int j = tid; j < p.m; j += kFwdThreads) key_off[j] = (uint16_t)off_key(p.bias, j);
+        for (int j = tid; j < (p.m + 127) / 128 * 128; j += kFwdThreads) key_off[j] = (uint16_t)off_key(p.bias, min(j, p.m - 1));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    chain_begin();
+    if (blockIdx.x == 0 && tid == 0) *x.err = 0;
 
     if (warp >= 8) set_regs_down<kRegsControl>();
     if (warp == 11) {
@@ -274,14 +266,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes per warp
         const uint32_t s_tm = tmem + t * 128 + lanes, p_tm = tmem + 256 + t * 64 + lanes, o_tm = tmem + 384 + t * 64 + lanes;
         const float scale2 = p.scale * kLog2e;
-        int kt = 0, ns = 0, np = 0, lut_head = -1;
+        int kt = 0, ns = 0, np = 0, lut_head = -1, luts = 0;
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(x, it);
             if (kBias && w.h != lut_head) {
-                // every softmax warp is past its reads of the old head's table
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                fill_offsets(p.bias, w.h, kLog2e, lut, tid, 256);
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                load_offsets(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
                 lut_head = w.h;
             }
             if (t >= w.nt) {   // this tile has no rows
@@ -295,37 +284,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 r.oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start);
                 r.oq_lo = off_query(p.bias, i - lane, start);   // sequence: the warp's first row
             }
-            auto tile = [&](int j, auto full) __attribute__((always_inline)) {
-                constexpr bool kFull = decltype(full)::value;
+            // a whole tile (N = 0), a part of one, a part of at most 64 keys
+            auto tile = [&](int j, auto variant) __attribute__((always_inline)) {
+                constexpr bool kFull = decltype(variant)::value == 0;
+                constexpr int N = kFull ? kRows : decltype(variant)::value;
                 const int keys = kFull ? kRows : tile_keys(w.len, j), cols = kFull ? kRows : tile_cols(keys), j0 = j * kRows;
-                float s[128];
+                float s[N];
                 wait_on(smem_u32(&bar.s_full[t]), ns & 1, guard, kErrTimeoutMma);
                 ++ns;
                 tc_fence_after();
-                tmem_ld32_nowait(s_tm, s);
-                tmem_ld32_nowait(s_tm + 32, s + 32);
-                tmem_ld32_nowait(s_tm + 64, s + 64);
-                tmem_ld32_nowait(s_tm + 96, s + 96);
+#pragma unroll
+                for (int c = 0; c < N; c += 32) tmem_ld32_nowait(s_tm + c, s + c);
                 tc_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar.s_free[t]));
 
                 float mul, add;   // 2^(mul s + add - ref) is the weight
-                add_bias<kBias, kFull>(s, p.bias, lut, key_off, j0, keys, cols, r, scale2, mul, add);
+                add_bias<kBias, N>(s, p.bias, lut, key_off, j0, keys, r, scale2, mul, add);
                 if (!kFull) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
+                    for (int c = 0; c < N; ++c)
                         if (c >= keys) s[c] = -INFINITY;
                 }
                 float top;
                 {
                     float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int c = 4; c < 128; c += 8) {
+                    for (int c = 4; c < N; c += 8) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            m4[e] = c + e + 4 < 128 ? fmaxf(fmaxf(m4[e], s[c + e]), s[c + e + 4]) : fmaxf(m4[e], s[c + e]);
+                            m4[e] = c + e + 4 < N ? fmaxf(fmaxf(m4[e], s[c + e]), s[c + e + 4]) : fmaxf(m4[e], s[c + e]);
                     }
                     top = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul, add);
                 }
@@ -355,7 +344,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 // the previous weights have been read (and their products are in O)
                 if (!first) wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
 #pragma unroll
-                for (int c = 0; c < 128; c += 32)
+                for (int c = 0; c < N; c += 32)
                     if (kFull || c < cols) {
                         uint32_t w16[16];
 #pragma unroll
@@ -386,10 +375,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 ++kt;
             };
             for (int j = w.t0; j < w.t1; ++j) {
-                if (tile_keys(w.len, j) == kRows)
-                    tile(j, std::true_type{});
+                const int keys = tile_keys(w.len, j);
+                if (keys == kRows)
+                    tile(j, std::integral_constant<int, 0>{});
+                else if (keys > 64)
+                    tile(j, std::integral_constant<int, 128>{});
                 else
-                    tile(j, std::false_type{});
+                    tile(j, std::integral_constant<int, 64>{});
             }
             const float ref = r.ref, sum = r.sum;
             // ------------------------------------------------------ output
@@ -433,6 +425,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
 // o = sum_s w_s o_s with w_s = exp(lse_s - lse): the parts of a row, in order.
 __global__ void __launch_bounds__(256) join_splits(const __grid_constant__ Problem p) {
+    chain_begin();
     const int vec = p.d / 4;
     const size_t rows = (size_t)p.B * p.heads * p.n;
     const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -480,8 +473,7 @@ int tc_forward_splits(int B, int heads, int n, int m) {
 
 cudaError_t launch_join(const Problem &p, cudaStream_t s) {
     const size_t vecs = (size_t)p.B * p.heads * p.n * (p.d / 4);
-    join_splits<<<(unsigned)((vecs + 255) / 256), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_chained(join_splits, dim3((unsigned)((vecs + 255) / 256)), 256, 0, s, p);
 }
 
 cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {
@@ -516,18 +508,17 @@ cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {
     cudaError_t e;
     switch (p.bias.mode) {
         case 0:
-            if ((e = allow_smem<tc_forward<0>>()) != cudaSuccess) return e;
-            tc_forward<0><<<grid, kFwdThreads, bytes, s>>>(mq, mk, mv, x);
+            if ((e = allow_smem<tc_forward<0>>()) == cudaSuccess)
+                e = launch_chained(tc_forward<0>, grid, kFwdThreads, bytes, s, mq, mk, mv, x);
             break;
         case 1:
-            if ((e = allow_smem<tc_forward<1>>()) != cudaSuccess) return e;
-            tc_forward<1><<<grid, kFwdThreads, bytes, s>>>(mq, mk, mv, x);
+            if ((e = allow_smem<tc_forward<1>>()) == cudaSuccess)
+                e = launch_chained(tc_forward<1>, grid, kFwdThreads, bytes, s, mq, mk, mv, x);
             break;
         default:
-            if ((e = allow_smem<tc_forward<2>>()) != cudaSuccess) return e;
-            tc_forward<2><<<grid, kFwdThreads, bytes, s>>>(mq, mk, mv, x);
+            if ((e = allow_smem<tc_forward<2>>()) == cudaSuccess)
+                e = launch_chained(tc_forward<2>, grid, kFwdThreads, bytes, s, mq, mk, mv, x);
     }
-    e = cudaGetLastError();
     if (e == cudaSuccess && p.splits > 1) e = launch_join(p, s);
     return e;
 }

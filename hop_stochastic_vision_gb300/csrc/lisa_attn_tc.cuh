@@ -15,6 +15,7 @@
 #include "lisa_attn.h"
 #include "lisa_bias_dev.cuh"
 #include "lisa_internal.h"
+#include "lisa_launch.cuh"
 #include "lisa_tc_common.cuh"
 
 namespace lisa {
@@ -179,6 +180,21 @@ struct Cursor {
     }
 };
 
+// The head's offset table (bias_offsets: fp32, log2(e) folded in) by one bulk
+// copy.  Called by the 256 arithmetic threads together; `count` copies so far.
+__device__ __forceinline__ void load_offsets(const BiasDev &b, int head, float *lut, uint64_t *bar, int &count, int tid,
+                                             const Guard &g) {
+    asm volatile("bar.sync 1, 256;" ::: "memory");   // every warp is past its reads of the old table
+    if (tid == 0) {
+        fence_proxy_async();
+        const uint32_t bytes = (uint32_t)(b.entries + 3) / 4 * 16;
+        mbar_arrive_expect_tx(smem_u32(bar), bytes);
+        bulk_load(smem_u32(lut), b.offsets + (size_t)head * b.offsets_pitch, bytes, smem_u32(bar));
+    }
+    wait_on(smem_u32(bar), count & 1, g, kErrTimeoutLoad);
+    ++count;
+}
+
 // One token box {64, 128} of a head's slice; coordinates of repeated dimensions stay 0.
 struct MapUse {
     int hmul, bmul;
@@ -213,14 +229,17 @@ __device__ __forceinline__ void store_rows_bf16(uint32_t stage, const float *v, 
                      pack_bf16(v[8 * c] * mul, v[8 * c + 1] * mul), pack_bf16(v[8 * c + 2] * mul, v[8 * c + 3] * mul),
                      pack_bf16(v[8 * c + 4] * mul, v[8 * c + 5] * mul), pack_bf16(v[8 * c + 6] * mul, v[8 * c + 7] * mul));
     __syncwarp();
-    const int c = lane % kChunks;
+    const int c = lane % kChunks, r0 = lane / kChunks;
+    row0 += r0 * stride + 8 * c;
+    const long long step = (32 / kChunks) * stride;
+    const int last = 8 * c < d ? rows : 0;
 #pragma unroll
-    for (int e = 0; e < kChunks; ++e) {
-        const int r = e * (32 / kChunks) + lane / kChunks;
-        if (r < rows && 8 * c < d) {
+    for (int e = 0; e < kChunks; ++e, row0 += step) {
+        const int r = e * (32 / kChunks) + r0;
+        if (r < last) {
             uint4 o;
             ld_shared_v4(stage + (uint32_t)r * (COLS * 2) + (uint32_t)((c ^ (r & (kChunks - 1))) << 4), o.x, o.y, o.z, o.w);
-            *reinterpret_cast<uint4 *>(row0 + (long long)r * stride + 8 * c) = o;
+            *reinterpret_cast<uint4 *>(row0) = o;
         }
     }
     __syncwarp();
@@ -241,26 +260,6 @@ inline bool make_map(CUtensorMap *m, MapUse *u, const Tensor &t, int B, int head
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(t.p), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Raises a kernel's shared-memory limit once per device.
-template <auto kKernel>
-cudaError_t allow_smem() {
-    static std::mutex mu;
-    static bool done[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done[dev]) return cudaSuccess;
-    cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, kKernel);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             227 * 1024 - (int)a.sharedSizeBytes);
-    if (e == cudaSuccess) done[dev] = true;
-    return e;
 }
 
 inline int sms() {

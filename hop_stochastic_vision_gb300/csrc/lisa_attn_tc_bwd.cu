@@ -82,14 +82,14 @@ __device__ __forceinline__ void row_weights(float (&s)[64], const BiasDev &b, co
             }
         }
     } else {
-        const int last = b.entries - 1;
+        const float *l = lut - oq;   // inside the table by construction
 #pragma unroll
         for (int c = 0; c < 64; c += 4) {
             const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
-            s[c] = fmaf(s[c], scale2, lut[min(max((int)(a.x & 0xFFFFu) - oq, 0), last)]) + nl;
-            s[c + 1] = fmaf(s[c + 1], scale2, lut[min(max((int)(a.x >> 16) - oq, 0), last)]) + nl;
-            s[c + 2] = fmaf(s[c + 2], scale2, lut[min(max((int)(a.y & 0xFFFFu) - oq, 0), last)]) + nl;
-            s[c + 3] = fmaf(s[c + 3], scale2, lut[min(max((int)(a.y >> 16) - oq, 0), last)]) + nl;
+            s[c] = fmaf(s[c], scale2, l[a.x & 0xFFFFu]) + nl;
+            s[c + 1] = fmaf(s[c + 1], scale2, l[a.x >> 16]) + nl;
+            s[c + 2] = fmaf(s[c + 2], scale2, l[a.y & 0xFFFFu]) + nl;
+            s[c + 3] = fmaf(s[c + 3], scale2, l[a.y >> 16]) + nl;
         }
     }
     if (keys < 64) {
@@ -128,7 +128,7 @@ __device__ __forceinline__ int uses_of(int total, int slot, int stages) {
 // ------------------------------------------------------------------------ dQ
 struct DqBars {
     uint64_t q_full[2], q_empty[2], k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages], v_empty[kMaxStages];
-    uint64_t s_full, s_free, dp_full, dp_free, ds_full, dq_done;
+    uint64_t s_full, s_free, dp_full, dp_free, ds_full, dq_done, lut_full;
 };
 
 template <int kBias>
@@ -167,17 +167,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&bar.s_free), 8);
         mbar_init(smem_u32(&bar.dp_free), 8);
         mbar_init(smem_u32(&bar.ds_full), 8);
+        mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
         fence_mbar_init();
-        if (x.first && blockIdx.x == 0) *x.err = 0;
     }
     if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 512);
     if (kBias == 2)
-        for (int j = tid; j < p.m; j += kThreads) key_off[j] = (uint16_t)off_key(p.bias, j);
+        for (int j = tid; j < (p.m + 127) / 128 * 128; j += kThreads) key_off[j] = (uint16_t)off_key(p.bias, min(j, p.m - 1));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    chain_begin();
+    if (x.first && blockIdx.x == 0 && tid == 0) *x.err = 0;
     const uint32_t tS = tmem, tP = tmem + 128, tDs = tmem + 256, tDq = tmem + 320;
 
     struct Item {
@@ -287,13 +289,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = warp >> 2, wt = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
-        int kt = 0, lut_head = -1;
+        int kt = 0, lut_head = -1, luts = 0;
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
             if (kBias && w.h != lut_head) {
-                math_barrier();
-                fill_offsets(p.bias, w.h, kLog2e, lut, tid, 256);
-                math_barrier();
+                load_offsets(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
                 lut_head = w.h;
             }
             const int i = w.q0 + wt;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct DkvBars {
     uint64_t kv_full, kv_empty, q_full[kMaxStages], d_full[kMaxStages], q_empty[kMaxStages];
     uint64_t aux_full[kMaxStages], aux_empty[kMaxStages];
-    uint64_t s_full, s_free, dp_full, dp_free, p_full, ds_full, dv_done, dk_done;
+    uint64_t s_full, s_free, dp_full, dp_free, p_full, ds_full, dv_done, dk_done, lut_full;
 };
 
 // What the arithmetic needs of a tile's queries, one entry per column.
@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&bar.dp_free), 8);
         mbar_init(smem_u32(&bar.p_full), 8);
         mbar_init(smem_u32(&bar.ds_full), 8);
+        mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
         fence_mbar_init();
     }
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    chain_begin();
     const uint32_t tS = tmem, tD = tmem + 128, tPw = tmem + 256, tDs = tmem + 320, tDv = tmem + 384, tDk = tmem + 448;
     const int steps = p.group * x.qtiles;   // (head, query tile) pairs of a kv head
     const int tail = tile_cols(p.n - (x.qtiles - 1) * kRows);   // columns of a head's last tile of queries
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = warp >> 2, wt = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
-        int n = 0, lut_head = -1;
+        int n = 0, lut_head = -1, luts = 0;
         Cursor ca;
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
@@ -634,9 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int h = w.g * p.group + split(qt, x.div_qtiles);
             for (int u = w.u0; u < w.u1; ++u, ++n, ca.next(x.stages), h += qt == x.qtiles - 1, qt = qt == x.qtiles - 1 ? 0 : qt + 1) {
                 if (kBias && h != lut_head) {
-                    math_barrier();
-                    fill_offsets(p.bias, h, kLog2e, lut, tid, 256);
-                    math_barrier();
+                    load_offsets(p.bias, h, lut, &bar.lut_full, luts, tid, guard);
                     lut_head = h;
                 }
                 const int cols = tile_cols(min(kRows, p.n - qt * kRows));
@@ -676,15 +676,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 s[c] = fmaf(s[c], scale2, lut[min(max(off - c, 0), last)]) + a.nl[c0 + c];
                         }
                     } else if (kBias == 2) {
-                        const int last = p.bias.entries - 1;
+                        const float *l4 = lut + ok;   // inside the table by construction
 #pragma unroll
                         for (int c = 0; c < 64; c += 4) {
                             const int4 o = *reinterpret_cast<const int4 *>(a.oq + c0 + c);
                             const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
-                            s[c] = fmaf(s[c], scale2, lut[min(max(ok - o.x, 0), last)]) + l.x;
-                            s[c + 1] = fmaf(s[c + 1], scale2, lut[min(max(ok - o.y, 0), last)]) + l.y;
-                            s[c + 2] = fmaf(s[c + 2], scale2, lut[min(max(ok - o.z, 0), last)]) + l.z;
-                            s[c + 3] = fmaf(s[c + 3], scale2, lut[min(max(ok - o.w, 0), last)]) + l.w;
+                            s[c] = fmaf(s[c], scale2, l4[-o.x]) + l.x;
+                            s[c + 1] = fmaf(s[c + 1], scale2, l4[-o.y]) + l.y;
+                            s[c + 2] = fmaf(s[c + 2], scale2, l4[-o.z]) + l.z;
+                            s[c + 3] = fmaf(s[c + 3], scale2, l4[-o.w]) + l.w;
                         }
                     } else {
 #pragma unroll
@@ -779,6 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // dK, dV from the parts of the queries, in order.
 __global__ void __launch_bounds__(256) join_dkdv(const __grid_constant__ Problem p) {
+    chain_begin();
     const size_t total = (size_t)p.B * p.kv_heads * p.m * p.d;
     const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (at >= total) return;
@@ -798,7 +799,7 @@ __global__ void __launch_bounds__(256) join_dkdv(const __grid_constant__ Problem
 // --------------------------------------------------------------------- dbias
 struct DbBars {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t s_full, s_free, dp_full, dp_free;
+    uint64_t s_full, s_free, dp_full, dp_free, lut_full;
 };
 
 template <int kBias>
@@ -828,6 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&bar.dp_full), 1);
         mbar_init(smem_u32(&bar.s_free), 8);
         mbar_init(smem_u32(&bar.dp_free), 8);
+        mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
         fence_mbar_init();
     }
@@ -836,6 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    chain_begin();
     const uint32_t tS = tmem, tD = tmem + 128;
 
     struct Item {
@@ -920,13 +923,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = warp >> 2, wt = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
-        int n = 0, lut_head = -1;
+        int n = 0, lut_head = -1, luts = 0;
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
             if (w.h != lut_head) {
-                math_barrier();
-                fill_offsets(p.bias, w.h, kLog2e, lut, tid, 256);
-                math_barrier();
+                load_offsets(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
                 lut_head = w.h;
             }
             if (kBias == 2) {   // the previous item's are read: every warp has passed its fold
@@ -982,10 +983,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             math_barrier();
             if (p.folded) {
                 const TileGeom g = fold_geom(p.fold, w.q0 / kFoldTile, w.j0 / kFoldTile);
-                fold_offsets(p.fold, g, tile, sums, tid, 256);
+                float *out = fold_block(p.fold, w.split, w.h, w.q0 / kFoldTile, w.j0 / kFoldTile);
+                const bool direct = fold_direct(p.fold, g);
+                fold_offsets(p.fold, g, tile, direct ? out : sums, direct ? p.fold.K : g.dc_n, tid, 256);
                 math_barrier();
-                fold_buckets(p.fold, g, sums, fold_block(p.fold, w.split, w.h, w.q0 / kFoldTile, w.j0 / kFoldTile), tid,
-                             256);
+                if (!direct) fold_buckets(p.fold, g, sums, out, tid, 256);
             } else {
                 float *out = p.dbias + ((size_t)w.split * p.heads + w.h) * ((size_t)p.n * p.m) + (size_t)w.q0 * p.m + w.j0;
                 for (int r = warp; r < min(kRows, p.n - w.q0); r += 8)
@@ -1023,8 +1025,7 @@ template <auto kKernel>
 cudaError_t go(const Maps &m, const BwdParams &x, int bytes, cudaStream_t s) {
     cudaError_t e = allow_smem<kKernel>();
     if (e != cudaSuccess) return e;
-    kKernel<<<(unsigned)std::min(x.items, sms()), kThreads, bytes, s>>>(m.q, m.d, m.k, m.v, x);
-    return cudaGetLastError();
+    return launch_chained(kKernel, dim3((unsigned)std::min(x.items, sms())), kThreads, bytes, s, m.q, m.d, m.k, m.v, x);
 }
 
 }  // namespace
@@ -1090,8 +1091,8 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (p.q_splits > 1) {
         const size_t vecs = (size_t)p.B * p.kv_heads * p.m * (p.d / 4);
-        join_dkdv<<<dim3((unsigned)((vecs + 255) / 256), 2), 256, 0, s>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_chained(join_dkdv, dim3((unsigned)((vecs + 255) / 256), 2), 256, 0, s, p);
+        if (e != cudaSuccess) return e;
     }
     if (p.bias.mode == 0) return cudaSuccess;
     // ---- dS of the batch

@@ -59,12 +59,22 @@ __device__ __forceinline__ TileGeom fold_geom(const FoldDev &f, int it, int jt) 
     return g;
 }
 
-// Sums of the tile's offsets into `sums` (dr_n x dc_n), `threads` threads.
-__device__ __forceinline__ void fold_offsets(const FoldDev &f, const TileGeom &g, const float *tile, float *sums, int tid,
-                                             int threads) {
+// u / d for 0 <= u < 2^15, d < 2^12: (u + 1/2) / d is at least 1 / (2 d) > 2^-13 from a whole number, far more than
+// the product's rounding.
+__device__ __forceinline__ int small_div(int u, float inv) { return (int)(((float)u + 0.5f) * inv); }
+
+// Whether every offset of the tile is a column bucket of its own.
+__device__ __forceinline__ bool fold_direct(const FoldDev &f, const TileGeom &g) {
+    return !f.cols.log_rule && g.cb_n == g.dc_n;
+}
+
+// Sums of the tile's offsets, dr_n rows of dc_n, `pitch` apart; `threads` threads.
+__device__ __forceinline__ void fold_offsets(const FoldDev &f, const TileGeom &g, const float *tile, float *sums,
+                                             int pitch, int tid, int threads) {
     const int wq = (int)f.div_q.d, wk = (int)f.div_k.d;
+    const float inv = 1.f / (float)g.dc_n;
     for (int u = tid; u < g.dr_n * g.dc_n; u += threads) {
-        const int dri = u / g.dc_n, dr = g.dr_lo + dri, dc = g.dc_lo + (u - dri * g.dc_n);
+        const int dri = small_div(u, inv), dr = g.dr_lo + dri, dc = g.dc_lo + (u - dri * g.dc_n);
         float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
         for (int rq = max(g.rq0, g.rk0 - dr); rq <= min(g.rq1, g.rk1 - dr); ++rq) {
             const int qb = rq * wq - g.q0, kb = (rq + dr) * wk - g.j0;   // tile row of cq = 0, column of ck = 0
@@ -80,7 +90,7 @@ __device__ __forceinline__ void fold_offsets(const FoldDev &f, const TileGeom &g
             }
             for (; c <= hi; ++c, p += kFoldPitch + 1) a0 += *p;
         }
-        sums[u] = (a0 + a1) + (a2 + a3);
+        sums[dri * pitch + (u - dri * g.dc_n)] = (a0 + a1) + (a2 + a3);
     }
 }
 
@@ -90,9 +100,10 @@ __device__ __forceinline__ void fold_buckets(const FoldDev &f, const TileGeom &g
                                              int threads) {
     const int lane = tid & 7;
     const int total = g.dr_n * g.cb_n, rounds = (total * 8 + threads - 1) / threads;
+    const float inv = 1.f / (float)g.cb_n;
     for (int r = 0; r < rounds; ++r) {
         const int u = (r * threads + tid) >> 3;
-        const int dri = u / g.cb_n, c = u - dri * g.cb_n;
+        const int dri = small_div(u, inv), c = u - dri * g.cb_n;
         float s = 0.f;
         if (u < total) {
             int lo, hi;

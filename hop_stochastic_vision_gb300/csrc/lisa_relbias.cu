@@ -7,6 +7,7 @@
 #include "lisa_attn.h"
 #include "lisa_bias_dev.cuh"
 #include "lisa_fold.cuh"
+#include "lisa_launch.cuh"
 
 namespace lisa {
 namespace attn {
@@ -25,6 +26,7 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 template <typename T>
 __global__ void __launch_bounds__(kDenseThreads) bias_dense(BiasDev b, T *out, int n, int m) {
     extern __shared__ __align__(16) float lut[];
+    chain_begin();
     constexpr int kVec = 16 / (int)sizeof(T);
     const int h = blockIdx.y, tid = threadIdx.x;
     fill_offsets(b, h, 1.f, lut, tid, kDenseThreads);
@@ -64,6 +66,20 @@ __global__ void __launch_bounds__(kDenseThreads) bias_dense(BiasDev b, T *out, i
     }
 }
 
+// The table by offset, times log2(e): thread per offset, all heads of it.
+__global__ void __launch_bounds__(128) bias_offsets(BiasDev b, float *out) {
+    chain_begin();
+    const int e = blockIdx.x * 128 + threadIdx.x, h0 = blockIdx.y * 4;
+    if (e >= b.entries) return;
+    const float *row = b.table + (size_t)entry_bucket(b, e) * b.heads;
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = h0 + u < b.heads ? row[h0 + u] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (h0 + u < b.heads) out[(size_t)(h0 + u) * b.offsets_pitch + e] = v[u] * 1.4426950408889634f;
+}
+
 // ---------------------------------------------------------------- gradient
 // For one pair of rows (rq, rk) of the two grids the q_cols x k_cols block of
 // dbias is summed along its diagonals: with u = q_cols - 1 - cq = s q + r
@@ -92,6 +108,7 @@ __device__ __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat16
 template <typename T>
 __global__ void __launch_bounds__(256) bias_grad_part(const __grid_constant__ GradParams g, const T *dbias) {
     __shared__ float diag[256];
+    chain_begin();
     const int t = threadIdx.x, h = blockIdx.z;
     const int tile = blockIdx.x % g.ntile, chunk = blockIdx.x / g.ntile;
     const int rq = blockIdx.y / g.k_rows, rk = blockIdx.y % g.k_rows;
@@ -145,6 +162,7 @@ __global__ void __launch_bounds__(256) bias_grad_part(const __grid_constant__ Gr
 __global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ GradParams g, float *dtable, int width,
                                                       int groups) {
     __shared__ float acc_s[1024];
+    chain_begin();
     const int rb = blockIdx.x, h = blockIdx.z;
     const int c = threadIdx.x % width, grp = threadIdx.x / width;
     const int cb = blockIdx.y * width + c;
@@ -190,6 +208,7 @@ __global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ Gr
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) fold_matrix(const __grid_constant__ FoldDev f, const T *dbias, int matrices) {
     extern __shared__ __align__(16) float fold_smem[];
+    chain_begin();
     float *tile = fold_smem, *sums = fold_smem + kFoldTile * kFoldPitch;
     const int tid = threadIdx.x, jt = blockIdx.x, it = blockIdx.y, h = blockIdx.z;
     const TileGeom g = fold_geom(f, it, jt);
@@ -219,15 +238,19 @@ __global__ void __launch_bounds__(256) fold_matrix(const __grid_constant__ FoldD
         }
     }
     __syncthreads();
-    fold_offsets(f, g, tile, sums, tid, 256);
+    float *out = fold_block(f, 0, h, it, jt);
+    const bool direct = fold_direct(f, g);
+    fold_offsets(f, g, tile, direct ? out : sums, direct ? f.K : g.dc_n, tid, 256);
+    if (direct) return;
     __syncthreads();
-    fold_buckets(f, g, sums, fold_block(f, 0, h, it, jt), tid, 256);
+    fold_buckets(f, g, sums, out, tid, 256);
 }
 
 // dtable of a row bucket: its share of the tiles' blocks, `groups` runs of tiles
 // added side by side by `width` columns of threads.
 __global__ void __launch_bounds__(1024) fold_sum(const __grid_constant__ FoldDev f, float *dtable, int width, int groups) {
     __shared__ float acc_s[1024];
+    chain_begin();
     const int rb = blockIdx.x, h = blockIdx.z;
     const int c = threadIdx.x % width, grp = threadIdx.x / width;
     const int cb = blockIdx.y * width + c;
@@ -265,24 +288,22 @@ __global__ void __launch_bounds__(1024) fold_sum(const __grid_constant__ FoldDev
     }
 }
 
+template <typename T, int VEC>
+cudaError_t run_fold_vec(const FoldDev &f, const T *dbias, int matrices, cudaStream_t s) {
+    cudaError_t e = allow_smem<fold_matrix<T, VEC>>();
+    if (e != cudaSuccess) return e;
+    return launch_chained(fold_matrix<T, VEC>, dim3((unsigned)f.ktiles, (unsigned)f.qtiles, (unsigned)f.heads), 256,
+                          kFoldTileBytes + f.units * 4, s, f, dbias, matrices);
+}
+
 template <typename T>
 cudaError_t run_fold(const FoldDev &f, const T *dbias, int matrices, cudaStream_t s) {
-    const int bytes = kFoldTileBytes + f.units * 4;
-    const dim3 grid((unsigned)f.ktiles, (unsigned)f.qtiles, (unsigned)f.heads);
-    const auto go = [&](auto kernel) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kFoldTileBytes + kMaxFoldUnits * 4);
-        if (e != cudaSuccess) return e;
-        kernel<<<grid, 256, bytes, s>>>(f, dbias, matrices);
-        return cudaGetLastError();
-    };
     // the widest vector that every row begins on
     constexpr int kFull = 16 / (int)sizeof(T);
-    const bool base16 = (reinterpret_cast<uintptr_t>(dbias) & 15u) == 0;
-    if (base16 && f.m % kFull == 0) return go(fold_matrix<T, kFull>);
-    if (base16 && f.m % (kFull / 2) == 0) return go(fold_matrix<T, kFull / 2>);
-    if (sizeof(T) == 2 && base16 && f.m % 2 == 0) return go(fold_matrix<T, 2>);
-    return go(fold_matrix<T, 1>);
+    if (f.m % kFull == 0) return run_fold_vec<T, kFull>(f, dbias, matrices, s);
+    if (f.m % (kFull / 2) == 0) return run_fold_vec<T, kFull / 2>(f, dbias, matrices, s);
+    if (sizeof(T) == 2 && f.m % 2 == 0) return run_fold_vec<T, 2>(f, dbias, matrices, s);
+    return run_fold_vec<T, 1>(f, dbias, matrices, s);
 }
 
 void grad_plan(const lisa_rel_bias &b, GradParams &g) {
@@ -305,6 +326,15 @@ void grad_plan(const lisa_rel_bias &b, GradParams &g) {
 
 }  // namespace
 
+size_t offsets_bytes(const BiasDev &b) {
+    return (size_t)b.heads * ((b.entries + 63) / 64 * 64) * sizeof(float);
+}
+
+cudaError_t launch_offsets(const BiasDev &b, float *out, cudaStream_t s) {
+    return launch_chained(bias_offsets, dim3((unsigned)((b.entries + 127) / 128), (unsigned)((b.heads + 3) / 4)), 128, 0, s,
+                          b, out);
+}
+
 cudaError_t launch_bias_dense(const lisa_rel_bias &b, const BiasDev &dev, void *out, int dtype, cudaStream_t s) {
     const int n = b.q_rows * b.q_cols, m = b.k_rows * b.k_cols;
     const size_t esz = dtype == LISA_BF16 ? 2 : 4;
@@ -313,19 +343,15 @@ cudaError_t launch_bias_dense(const lisa_rel_bias &b, const BiasDev &dev, void *
     size_t blocks = (vecs + kDenseThreads * 4 - 1) / (kDenseThreads * 4);
     blocks = std::max<size_t>(1, std::min<size_t>(blocks, (152 * 8 + dev.heads - 1) / dev.heads));
     const int bytes = dev.entries * (int)sizeof(float);
-    dim3 grid((unsigned)blocks, (unsigned)dev.heads);
+    const dim3 grid((unsigned)blocks, (unsigned)dev.heads);
+    cudaError_t e;
     if (dtype == LISA_BF16) {
-        cudaError_t e = cudaFuncSetAttribute(bias_dense<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             LISA_MAX_OFFSETS * 4);
-        if (e != cudaSuccess) return e;
-        bias_dense<<<grid, kDenseThreads, bytes, s>>>(dev, static_cast<__nv_bfloat16 *>(out), n, m);
-    } else {
-        cudaError_t e = cudaFuncSetAttribute(bias_dense<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             LISA_MAX_OFFSETS * 4);
-        if (e != cudaSuccess) return e;
-        bias_dense<<<grid, kDenseThreads, bytes, s>>>(dev, static_cast<float *>(out), n, m);
+        if ((e = allow_smem<bias_dense<__nv_bfloat16>>()) != cudaSuccess) return e;
+        return launch_chained(bias_dense<__nv_bfloat16>, grid, kDenseThreads, bytes, s, dev, static_cast<__nv_bfloat16 *>(out),
+                              n, m);
     }
-    return cudaGetLastError();
+    if ((e = allow_smem<bias_dense<float>>()) != cudaSuccess) return e;
+    return launch_chained(bias_dense<float>, grid, kDenseThreads, bytes, s, dev, static_cast<float *>(out), n, m);
 }
 
 bool fold_plan(const lisa_rel_bias &b, int heads, int parts, FoldDev &f) {
@@ -364,9 +390,8 @@ size_t fold_bytes(const FoldDev &f) {
 
 cudaError_t launch_fold_sum(const FoldDev &f, float *dtable, cudaStream_t s) {
     const int width = std::min(256, (f.col_buckets + 31) / 32 * 32), groups = 1024 / width;
-    fold_sum<<<dim3((unsigned)f.row_buckets, (unsigned)((f.col_buckets + width - 1) / width), (unsigned)f.heads),
-               width * groups, 0, s>>>(f, dtable, width, groups);
-    return cudaGetLastError();
+    return launch_chained(fold_sum, dim3((unsigned)f.row_buckets, (unsigned)((f.col_buckets + width - 1) / width), (unsigned)f.heads),
+                          width * groups, 0, s, f, dtable, width, groups);
 }
 
 size_t bias_grad_bytes(const lisa_rel_bias &b, int heads) {
@@ -392,17 +417,14 @@ cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const v
     grad_plan(b, g);
     g.part = static_cast<float *>(ws);
     dim3 grid((unsigned)(g.nchunk * g.ntile), (unsigned)(g.q_rows * g.k_rows), (unsigned)dev.heads);
-    if (dtype == LISA_BF16)
-        bias_grad_part<<<grid, g.threads, 0, s>>>(g, static_cast<const __nv_bfloat16 *>(dbias));
-    else
-        bias_grad_part<<<grid, g.threads, 0, s>>>(g, static_cast<const float *>(dbias));
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = dtype == LISA_BF16
+                        ? launch_chained(bias_grad_part<__nv_bfloat16>, grid, g.threads, 0, s, g, static_cast<const __nv_bfloat16 *>(dbias))
+                        : launch_chained(bias_grad_part<float>, grid, g.threads, 0, s, g, static_cast<const float *>(dbias));
     if (e != cudaSuccess) return e;
     // 1024 threads as `groups` runs of partials by `width` column buckets
     const int width = std::min(256, (g.col_buckets + 31) / 32 * 32), groups = 1024 / width;
-    bias_grad_sum<<<dim3((unsigned)g.row_buckets, (unsigned)((g.col_buckets + width - 1) / width), (unsigned)dev.heads),
-                    width * groups, 0, s>>>(g, dtable, width, groups);
-    return cudaGetLastError();
+    return launch_chained(bias_grad_sum, dim3((unsigned)g.row_buckets, (unsigned)((g.col_buckets + width - 1) / width), (unsigned)dev.heads),
+                          width * groups, 0, s, g, dtable, width, groups);
 }
 
 }  // namespace attn
