@@ -128,6 +128,10 @@ cudaError_t launch_simt_dbias(const Problem &p, cudaStream_t s);
 size_t offsets_bytes(const BiasDev &b);
 cudaError_t launch_offsets(const BiasDev &b, float *out, cudaStream_t s);
 
+// bf16, a few query rows per key head: one pass over the keys
+bool token_applies(const Problem &p);
+cudaError_t launch_token(const Problem &p, int *err, cudaStream_t s);
+
 // bf16 on the tensor cores; `err` is the error word of the call's workspace
 int tc_forward_splits(int B, int heads, int n, int m);
 cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s);

@@ -342,6 +342,7 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (!pl.tc) return status_of(launch_simt_forward(p, cs));
     char *ws = static_cast<char *>(workspace);
+    if (token_applies(p)) return status_of(launch_token(p, reinterpret_cast<int *>(ws), cs));
     p.splits = pl.splits;
     p.lse_part = reinterpret_cast<float *>(ws + pl.off_lse);
     p.o_part = reinterpret_cast<float *>(ws + pl.off_o);
