@@ -7,6 +7,7 @@ streams, every step runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -55,7 +56,7 @@ def _library():
         lib.lisa_relative_bias_backward_workspace_bytes.restype = sz
         lib.lisa_relative_bias_backward.argtypes = [bp, i, vp, i, vp, vp, sz, vp]
         lib.lisa_relative_bias_backward.restype = i
-        lib.lisa_cross_attention_workspace_bytes.argtypes = [i] * 7
+        lib.lisa_cross_attention_workspace_bytes.argtypes = [i] * 6 + [bp, i]
         lib.lisa_cross_attention_workspace_bytes.restype = sz
         lib.lisa_cross_attention.argtypes = [vp, sp, vp, sp, vp, sp, vp, sp, vp, i, i, i, i, i, i, f, vp, bp, i, vp,
                                              sz, vp]
@@ -89,8 +90,8 @@ def lisa_relative_bias_backward(bias, heads, dbias, dtype, dtable, workspace, wo
                                                       workspace_bytes, stream))
 
 
-def lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, dtype) -> int:
-    return int(_library().lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, dtype))
+def lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, bias, dtype) -> int:
+    return int(_library().lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, _ref(bias), dtype))
 
 
 def lisa_cross_attention(Q, qs, K, ks, V, vs, O, os, lse, B, heads, kv_heads, n, m, d, scale, kv_lens, bias, dtype,
@@ -178,27 +179,38 @@ class RelativeBias:
         return self.k_grid[0] * self.k_grid[1]
 
 
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without the Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 class _On:
     """The device and the stream of a call made current, so what the call
     allocates belongs to the stream that uses it."""
 
-    def __init__(self, device, stream):
-        self.device = torch.cuda.device(device)
-        self.other = None
+    def __init__(self, index, stream):
+        self.index = index
+        self.device = self.other = None
+        if torch.cuda.current_device() != index:
+            self.device = torch.cuda.device(index)
         if stream is not None:
-            self.other = torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
-        self.of = device
+            self.other = torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index)))
 
     def __enter__(self):
-        self.device.__enter__()
+        if self.device is not None:
+            self.device.__enter__()
         if self.other is not None:
             self.other.__enter__()
-        return torch.cuda.current_stream(self.of).cuda_stream
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         if self.other is not None:
             self.other.__exit__(*exc)
-        self.device.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
 
 
 def _workspace(given, nbytes, device):
@@ -212,19 +224,30 @@ def _workspace(given, nbytes, device):
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
-def _strides(t: torch.Tensor) -> lisa_strides:
-    s = t.stride()
-    if t.shape[3] > 1 and s[3] != 1:
+@functools.lru_cache(maxsize=1024)
+def _strides_of(batch, head, token):
+    return lisa_strides(batch, head, token)
+
+
+@functools.lru_cache(maxsize=1024)
+def _plain_bytes(B, heads, kv_heads, n, m, d, dtype):
+    return lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, None, dtype)
+
+
+def _strides(t: torch.Tensor, shape) -> lisa_strides:
+    b, h, n, d = t.stride()
+    if d != 1 and shape[3] > 1:
         raise ValueError("the elements of a token must be contiguous (last stride 1)")
-    return lisa_strides(*(s[x] if t.shape[x] > 1 else t.shape[3] for x in range(3)))
+    d = shape[3]      # a stride that no step uses: any legal value
+    return _strides_of(b if shape[0] > 1 else d, h if shape[1] > 1 else d, n if shape[2] > 1 else d)
 
 
-def _check(device, dtype, tensors):
+def _check(index, dtype, tensors):
     for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("the cross attention runs on CUDA tensors only")
-        if t.device != device:
-            raise ValueError("tensors must be on one device")
+        at = t.get_device()
+        if at != index or at < 0:
+            raise ValueError("the cross attention runs on CUDA tensors only" if at < 0
+                             else "tensors must be on one device")
         if t.dim() != 4 or t.dtype != dtype:
             raise ValueError("q, k, v, out, dout must be 4-d and share dtype float32 or bfloat16")
 
@@ -232,24 +255,26 @@ def _check(device, dtype, tensors):
 def _shapes(q, k, v, kv_lens, bias):
     if q.dtype not in _DTYPES:
         raise ValueError("q, k, v must share dtype float32 or bfloat16")
-    _check(q.device, q.dtype, (q, k, v))
-    B, heads, n, d = q.shape
-    kv_heads, m = k.shape[1], k.shape[2]
-    if tuple(k.shape) != (B, kv_heads, m, d) or k.shape != v.shape:
+    index = q.get_device()
+    _check(index, q.dtype, (q, k, v))
+    B, heads, n, d = shape = q.shape
+    kv_shape = k.shape
+    if kv_shape[0] != B or kv_shape[3] != d or v.shape != kv_shape:
         raise ValueError("k and v must be [B, kv_heads, m, d] for q [B, heads, n, d]")
+    kv_heads, m = kv_shape[1], kv_shape[2]
     if kv_lens is not None:
-        if not (kv_lens.is_cuda and kv_lens.dtype == torch.int32 and kv_lens.is_contiguous()
-                and tuple(kv_lens.shape) == (B,) and kv_lens.device == q.device):
+        if not (kv_lens.get_device() == index and kv_lens.dtype == torch.int32 and kv_lens.is_contiguous()
+                and tuple(kv_lens.shape) == (B,)):
             raise ValueError("kv_lens must be a contiguous int32 CUDA tensor [B]")
     if bias is not None:
-        if bias.table.device != q.device:
+        if bias.table.get_device() != index:
             raise ValueError("tensors must be on one device")
         if bias.heads != heads or bias.n != n or bias.m != m:
             raise ValueError("the bias is of %d heads, %d queries and %d keys, the call of %d, %d and %d"
                              % (bias.heads, bias.n, bias.m, heads, n, m))
         if bias.starts is not None and bias.starts.shape[0] != B:
             raise ValueError("query_start must have one entry per batch entry")
-    return B, heads, kv_heads, n, m, d
+    return index, shape, kv_shape, B, heads, kv_heads, n, m, d
 
 
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale=None, kv_lens=None,
@@ -262,23 +287,26 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale=
     (a new contiguous tensor unless ``out`` is given), with ``return_lse`` also
     the fp32 log-sum-exp [B, heads, n] that the backward pass reads.
     ``stream`` is a raw stream handle of the tensors' device."""
-    B, heads, kv_heads, n, m, d = _shapes(q, k, v, kv_lens, bias)
+    index, shape, kv_shape, B, heads, kv_heads, n, m, d = _shapes(q, k, v, kv_lens, bias)
     dt = _DTYPES[q.dtype]
-    with _On(q.device, stream) as st:
+    with _On(index, stream) as st:
+        device = q.device
         if out is None:
-            out = torch.empty((B, heads, n, d), dtype=q.dtype, device=q.device)
+            out = torch.empty(shape, dtype=q.dtype, device=device)
         else:
-            _check(q.device, q.dtype, (out,))
-            if out.shape != q.shape:
+            _check(index, q.dtype, (out,))
+            if out.shape != shape:
                 raise ValueError("out must have q's shape")
-        lse = torch.empty((B, heads, n), dtype=torch.float32, device=q.device) if return_lse else None
-        keep, ws, nbytes = _workspace(workspace, lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, dt),
-                                      q.device)
-        status = lisa_cross_attention(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v),
-                                      out.data_ptr(), _strides(out), lse.data_ptr() if return_lse else None, B, heads,
-                                      kv_heads, n, m, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
-                                      None if kv_lens is None else kv_lens.data_ptr(),
-                                      None if bias is None else bias.struct, dt, ws, nbytes, st)
+        lse = torch.empty((B, heads, n), dtype=torch.float32, device=device) if return_lse else None
+        lib = _library()
+        need = _plain_bytes(B, heads, kv_heads, n, m, d, dt) if bias is None else \
+            lib.lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, bias.struct, dt)
+        keep, ws, nbytes = _workspace(workspace, need, device)
+        status = lib.lisa_cross_attention(
+            q.data_ptr(), _strides(q, shape), k.data_ptr(), _strides(k, kv_shape), v.data_ptr(), _strides(v, kv_shape),
+            out.data_ptr(), _strides(out, shape), lse.data_ptr() if return_lse else None, B, heads, kv_heads, n, m, d,
+            1.0 / math.sqrt(d) if scale is None else float(scale), None if kv_lens is None else kv_lens.data_ptr(),
+            None if bias is None else bias.struct, dt, ws, nbytes, st)
         del keep
     if status != LISA_OK:
         raise LisaError(status)
@@ -291,28 +319,30 @@ def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     """Gradients of ``cross_attention`` for the upstream gradient ``dout``, given
     the forward's ``out`` and ``lse``: (dq, dk, dv), with ``bias`` also the
     table's gradient dtable (fp32, the table's shape), summed over the batch."""
-    B, heads, kv_heads, n, m, d = _shapes(q, k, v, kv_lens, bias)
-    _check(q.device, q.dtype, (out, dout))
-    if out.shape != q.shape or dout.shape != q.shape:
+    index, shape, kv_shape, B, heads, kv_heads, n, m, d = _shapes(q, k, v, kv_lens, bias)
+    _check(index, q.dtype, (out, dout))
+    if out.shape != shape or dout.shape != shape:
         raise ValueError("out and dout must have q's shape")
-    if not (lse.is_cuda and lse.device == q.device and lse.dtype == torch.float32 and lse.is_contiguous()
+    if not (lse.get_device() == index and lse.dtype == torch.float32 and lse.is_contiguous()
             and tuple(lse.shape) == (B, heads, n)):
         raise ValueError("lse must be the forward's contiguous fp32 tensor [B, heads, n]")
     if bias is not None and bias.starts is not None:
         raise ValueError("a bias with a start for each batch entry has no backward")
     dt = _DTYPES[q.dtype]
     struct = None if bias is None else bias.struct
-    with _On(q.device, stream) as st:
-        dq = torch.empty((B, heads, n, d), dtype=q.dtype, device=q.device)
-        dk = torch.empty((B, kv_heads, m, d), dtype=q.dtype, device=q.device)
-        dv = torch.empty((B, kv_heads, m, d), dtype=q.dtype, device=q.device)
+    with _On(index, stream) as st:
+        device = q.device
+        dq = torch.empty(shape, dtype=q.dtype, device=device)
+        dk = torch.empty(kv_shape, dtype=q.dtype, device=device)
+        dv = torch.empty(kv_shape, dtype=q.dtype, device=device)
         dtable = None if bias is None else torch.empty_like(bias.table)
-        need = lisa_cross_attention_backward_workspace_bytes(B, heads, kv_heads, n, m, d, struct, dt)
-        keep, ws, nbytes = _workspace(workspace, need, q.device)
-        status = lisa_cross_attention_backward(
-            q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), out.data_ptr(),
-            _strides(out), lse.data_ptr(), dout.data_ptr(), _strides(dout), dq.data_ptr(), dk.data_ptr(),
-            dv.data_ptr(), None if bias is None else dtable.data_ptr(), B, heads, kv_heads, n, m, d,
+        lib = _library()
+        need = lib.lisa_cross_attention_backward_workspace_bytes(B, heads, kv_heads, n, m, d, struct, dt)
+        keep, ws, nbytes = _workspace(workspace, need, device)
+        status = lib.lisa_cross_attention_backward(
+            q.data_ptr(), _strides(q, shape), k.data_ptr(), _strides(k, kv_shape), v.data_ptr(), _strides(v, kv_shape),
+            out.data_ptr(), _strides(out, shape), lse.data_ptr(), dout.data_ptr(), _strides(dout, shape), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), None if bias is None else dtable.data_ptr(), B, heads, kv_heads, n, m, d,
             1.0 / math.sqrt(d) if scale is None else float(scale), None if kv_lens is None else kv_lens.data_ptr(),
             struct, dt, ws, nbytes, st)
         del keep
@@ -328,13 +358,13 @@ def relative_bias(bias: RelativeBias, dtype: torch.dtype = torch.float32, *, out
     if bias.starts is not None:
         raise ValueError("a bias with a start for each batch entry has no matrix")
     shape = (bias.heads, bias.n, bias.m)
-    with _On(bias.table.device, stream) as st:
+    with _On(bias.table.get_device(), stream) as st:
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=bias.table.device)
         elif not (out.is_cuda and out.device == bias.table.device and out.dtype == dtype and out.is_contiguous()
                   and tuple(out.shape) == shape):
             raise ValueError("out must be a contiguous %s CUDA tensor [heads, n, m]" % (dtype,))
-        status = lisa_relative_bias(bias.struct, bias.heads, out.data_ptr(), _DTYPES[dtype], st)
+        status = _library().lisa_relative_bias(bias.struct, bias.heads, out.data_ptr(), _DTYPES[dtype], st)
     if status != LISA_OK:
         raise LisaError(status)
     return out
@@ -348,11 +378,12 @@ def relative_bias_backward(bias: RelativeBias, dbias: torch.Tensor, *, workspace
     if not (dbias.is_cuda and dbias.device == bias.table.device and dbias.dtype in _DTYPES and dbias.is_contiguous()
             and tuple(dbias.shape) == (bias.heads, bias.n, bias.m)):
         raise ValueError("dbias must be a contiguous fp32 or bf16 CUDA tensor [heads, n, m]")
-    with _On(dbias.device, stream) as st:
+    with _On(dbias.get_device(), stream) as st:
         dtable = torch.empty_like(bias.table)
-        keep, ws, nbytes = _workspace(workspace, lisa_relative_bias_backward_workspace_bytes(bias.struct, bias.heads),
+        lib = _library()
+        keep, ws, nbytes = _workspace(workspace, lib.lisa_relative_bias_backward_workspace_bytes(bias.struct, bias.heads),
                                       dbias.device)
-        status = lisa_relative_bias_backward(bias.struct, bias.heads, dbias.data_ptr(), _DTYPES[dbias.dtype],
+        status = lib.lisa_relative_bias_backward(bias.struct, bias.heads, dbias.data_ptr(), _DTYPES[dbias.dtype],
                                              dtable.data_ptr(), ws, nbytes, st)
         del keep
     if status != LISA_OK:

@@ -129,8 +129,8 @@ size_t offsets_bytes(const BiasDev &b);
 cudaError_t launch_offsets(const BiasDev &b, float *out, cudaStream_t s);
 
 // bf16, a few query rows per key head: one pass over the keys
-bool token_applies(const Problem &p);
-cudaError_t launch_token(const Problem &p, int *err, cudaStream_t s);
+bool token_applies(int kv_heads, int group, int n, const BiasDev &bias);
+cudaError_t launch_token(const Problem &p, cudaStream_t s);
 
 // bf16 on the tensor cores; `err` is the error word of the call's workspace
 int tc_forward_splits(int B, int heads, int n, int m);

@@ -183,19 +183,24 @@ lisa_status fill(Problem &p, const void *Q, const lisa_strides *qs, const void *
     return LISA_OK;
 }
 
-// The forward's path and workspace: the tensor cores for bf16, the CUDA cores otherwise.
+// The forward's path and workspace: CUDA cores for fp32; for bf16 one pass over
+// the keys where few rows share a key head, 128-row tiles otherwise.
+enum class Path { kSimt, kToken, kTiles };
 struct FwdPlan {
-    bool tc;
+    Path path;
     int splits;
-    size_t off_lse, off_o, off_table, total;   // the error word is at 0
+    size_t off_lse, off_o, off_table, total;   // kTiles: the error word is at 0
 };
 
-// `table`: bytes of the bias table by offset.
-FwdPlan forward_plan(int B, int heads, int n, int m, int d, int dtype, size_t table) {
+FwdPlan forward_plan(int B, int heads, int group, int n, int m, int d, int dtype, const BiasDev &bias) {
     FwdPlan pl{};
     pl.splits = 1;
-    pl.tc = dtype == LISA_BF16 && m > 0;
-    if (!pl.tc) return pl;
+    if (dtype != LISA_BF16 || m == 0) return pl;
+    if (token_applies(heads / group, group, n, bias)) {
+        pl.path = Path::kToken;
+        return pl;
+    }
+    pl.path = Path::kTiles;
     pl.splits = tc_forward_splits(B, heads, n, m);
     size_t off = kAlign;
     if (pl.splits > 1) {
@@ -206,7 +211,7 @@ FwdPlan forward_plan(int B, int heads, int n, int m, int d, int dtype, size_t ta
         off = align_up(off + rows * d * sizeof(float));
     }
     pl.off_table = off;
-    off = align_up(off + table);
+    if (bias.mode) off = align_up(off + offsets_bytes(bias));
     pl.total = off;
     return pl;
 }
@@ -306,11 +311,11 @@ extern "C" lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, in
 }
 
 extern "C" size_t lisa_cross_attention_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,
-                                                       int dtype) {
+                                                       const lisa_rel_bias *bias, int dtype) {
     if (check_sizes(B, heads, kv_heads, n, m, d, dtype) != LISA_OK || B == 0 || heads == 0 || n == 0) return 0;
-    // whatever the bias: its table by offset has at most LISA_MAX_OFFSETS entries per head
-    const size_t table = (size_t)heads * LISA_MAX_OFFSETS * sizeof(float);
-    return forward_plan(B, heads, n, m, d, dtype, table).total;
+    BiasDev dev{};
+    if (bias && m > 0 && bias_dev(bias, heads, dev) != LISA_OK) return 0;
+    return forward_plan(B, heads, heads / kv_heads, n, m, d, dtype, dev).total;
 }
 
 extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q_strides, const void *K,
@@ -334,15 +339,15 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
         return LISA_ERR_INVALID_ARG;
     p.O = {O, o_strides->batch, o_strides->head, o_strides->token};
     p.lse = lse;
-    const FwdPlan pl = forward_plan(B, heads, n, m, d, dtype, p.bias.mode ? offsets_bytes(p.bias) : 0);
+    const FwdPlan pl = forward_plan(B, heads, p.group, n, m, d, dtype, p.bias);
     if (pl.total > 0) {
         if (!workspace || workspace_bytes < pl.total) return LISA_ERR_WORKSPACE;
         if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (!pl.tc) return status_of(launch_simt_forward(p, cs));
+    if (pl.path == Path::kSimt) return status_of(launch_simt_forward(p, cs));
+    if (pl.path == Path::kToken) return status_of(launch_token(p, cs));
     char *ws = static_cast<char *>(workspace);
-    if (token_applies(p)) return status_of(launch_token(p, reinterpret_cast<int *>(ws), cs));
     p.splits = pl.splits;
     p.lse_part = reinterpret_cast<float *>(ws + pl.off_lse);
     p.o_part = reinterpret_cast<float *>(ws + pl.off_o);

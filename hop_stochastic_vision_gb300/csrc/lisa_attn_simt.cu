@@ -17,6 +17,7 @@
 
 #include "lisa_attn.h"
 #include "lisa_bias_dev.cuh"
+#include "lisa_launch.cuh"
 
 namespace lisa {
 namespace attn {
@@ -163,6 +164,7 @@ constexpr int kWeights = kTile * (kTile + 4);
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
+    chain_begin();
     float *q_s = sm, *k_s = q_s + tile_floats<D>(), *v_s = k_s + tile_floats<D>(), *p_s = v_s + tile_floats<D>();
     float *lut = p_s + kWeights;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -232,6 +234,7 @@ __device__ __forceinline__ float row_ref(const float *lse, size_t at, bool in) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
+    chain_begin();
     float *q_s = sm, *o_s = q_s + tile_floats<D>(), *k_s = o_s + tile_floats<D>(), *v_s = k_s + tile_floats<D>();
     float *p_s = v_s + tile_floats<D>(), *lut = p_s + kWeights;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -296,6 +299,7 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) simt_dkdv(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
+    chain_begin();
     float *k_s = sm, *v_s = k_s + tile_floats<D>(), *q_s = v_s + tile_floats<D>(), *o_s = q_s + tile_floats<D>();
     float *p_s = o_s + tile_floats<D>(), *d_s = p_s + kWeights, *lut = d_s + kWeights;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -363,6 +367,7 @@ __global__ void __launch_bounds__(kThreads) simt_dkdv(const __grid_constant__ Pr
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) simt_dbias(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
+    chain_begin();
     float *k_s = sm, *v_s = k_s + tile_floats<D>(), *q_s = v_s + tile_floats<D>(), *o_s = q_s + tile_floats<D>();
     float *lut = o_s + tile_floats<D>();
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -409,34 +414,29 @@ __global__ void __launch_bounds__(kThreads) simt_dbias(const __grid_constant__ P
         }
 }
 
-template <typename Kern>
-cudaError_t run(Kern k, dim3 grid, int floats, const Problem &p, cudaStream_t s) {
+template <auto kKernel>
+cudaError_t run(dim3 grid, int floats, const Problem &p, cudaStream_t s) {
     const int bytes = (floats + (p.bias.mode ? p.bias.entries : 0)) * (int)sizeof(float);
-    if (bytes > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-    }
-    k<<<grid, kThreads, bytes, s>>>(p);
-    return cudaGetLastError();
+    cudaError_t e = allow_smem<kKernel>();
+    if (e != cudaSuccess) return e;
+    return launch_chained(kKernel, grid, kThreads, (size_t)bytes, s, p);
 }
-
-constexpr int kMaxGridYZ = 65535;
 
 template <typename T, int D>
 struct Simt {
     static constexpr int t = tile_floats<D>();
     static unsigned tiles(int x) { return (unsigned)((x + kTile - 1) / kTile); }
     static cudaError_t forward(const Problem &p, cudaStream_t s) {
-        return run(simt_forward<T, D>, dim3(tiles(p.n), p.heads, p.B), 3 * t + kWeights, p, s);
+        return run<simt_forward<T, D>>(dim3(tiles(p.n), p.heads, p.B), 3 * t + kWeights, p, s);
     }
     static cudaError_t dq(const Problem &p, cudaStream_t s) {
-        return run(simt_dq<T, D>, dim3(tiles(p.n), p.heads, p.B), 4 * t + kWeights, p, s);
+        return run<simt_dq<T, D>>(dim3(tiles(p.n), p.heads, p.B), 4 * t + kWeights, p, s);
     }
     static cudaError_t dkdv(const Problem &p, cudaStream_t s) {
-        return run(simt_dkdv<T, D>, dim3(tiles(p.m), p.kv_heads, p.B), 4 * t + 2 * kWeights, p, s);
+        return run<simt_dkdv<T, D>>(dim3(tiles(p.m), p.kv_heads, p.B), 4 * t + 2 * kWeights, p, s);
     }
     static cudaError_t dbias(const Problem &p, cudaStream_t s) {
-        return run(simt_dbias<T, D>, dim3(tiles(p.m), tiles(p.n), p.heads), 4 * t, p, s);
+        return run<simt_dbias<T, D>>(dim3(tiles(p.m), tiles(p.n), p.heads), 4 * t, p, s);
     }
 };
 

@@ -941,13 +941,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             float acc[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = 0.f;
+            // lse and delta of the row, one batch entry ahead
+            auto scalars = [&](int b, float &nl, float &delta) __attribute__((always_inline)) {
+                const size_t row = ((size_t)b * p.heads + w.h) * p.n + i;
+                nl = neg_lse2(p.lse, row, in && b < w.b1);
+                delta = in && b < w.b1 ? p.delta[row] : 0.f;
+            };
+            float nl_next, delta_next;
+            scalars(w.b0, nl_next, delta_next);
             for (int b = w.b0; b < w.b1; ++b) {
+                const float nl = nl_next, delta = delta_next;
+                scalars(b + 1, nl_next, delta_next);
                 const int len = keys_of(p, b);
                 if (w.j0 >= len) continue;
                 const int keys = min(64, len - j0);
                 const bool any = keys > 0;
-                const size_t row = ((size_t)b * p.heads + w.h) * p.n + i;
-                const float nl = neg_lse2(p.lse, row, in), delta = in ? p.delta[row] : 0.f;
                 float s[64];
                 wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();

@@ -25,7 +25,6 @@ struct TokenParams {
     Problem p;
     int rows, rtiles;            // query rows per key head, tiles of 16 of them
     int splits;                  // CTAs of a cluster
-    int *err;                    // the workspace's error word: no wait here can give up, so it is only cleared
     FastDiv div_rtiles, div_n;
 };
 
@@ -70,7 +69,6 @@ __global__ void __launch_bounds__(kTokenThreads) token_attention(const __grid_co
     float *lut = reinterpret_cast<float *>(sm + S::kMain);
     const uint32_t ring = smem_u32(sm) + (uint32_t)warp * (kTokenStages * 2 * S::kTileB);
     chain_begin();
-    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && b == 0) *x.err = 0;
 
     const int len = keys_of(p, b);
     const int chunks = (len + kChunk - 1) / kChunk, per = (chunks + x.splits - 1) / x.splits;
@@ -331,18 +329,16 @@ cudaError_t go(const TokenParams &x, cudaStream_t s) {
 
 }  // namespace
 
-bool token_applies(const Problem &p) {
+bool token_applies(int kv_heads, int group, int n, const BiasDev &bias) {
     // up to two row tiles per key head read the keys twice at most (the second
     // time from L2); a sequence's offset tables of the tile's heads fit beside the rings
-    if (p.m < 1 || (long long)p.n * p.group > 32 || p.kv_heads * 2LL > 65535) return false;
-    if (p.bias.mode == 2) return false;
-    return p.bias.mode == 0 || std::min(16, p.group) * p.bias.entries <= 8192;
+    if ((long long)n * group > 32 || kv_heads * 2LL > 65535 || bias.mode == 2) return false;
+    return bias.mode == 0 || std::min(16, group) * bias.entries <= 8192;
 }
 
-cudaError_t launch_token(const Problem &p, int *err, cudaStream_t s) {
+cudaError_t launch_token(const Problem &p, cudaStream_t s) {
     TokenParams x{};
     x.p = p;
-    x.err = err;
     x.rows = p.n * p.group;
     x.rtiles = (x.rows + 15) / 16;
     x.div_rtiles = fast_div(x.rtiles);

@@ -121,10 +121,13 @@ lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, int heads, co
 /*
  * Cross attention.  O and lse are written; lse (fp32 [B][heads][n], contiguous)
  * may be NULL.  bias may be NULL.  scale is finite and > 0 (1 / sqrt(d) as a
- * rule).  O may not overlap an input.  The workspace may be 0 bytes
- * (lisa_cross_attention_workspace_bytes says); it is 16-byte aligned.
+ * rule).  O may not overlap an input.  The workspace, 16-byte aligned, may be 0
+ * bytes (lisa_cross_attention_workspace_bytes says; 0 too for arguments that the
+ * call would reject).  Where it is not, it begins with the call's error word
+ * (lisa_query_status); a call without one has no wait that could give up.
  */
-size_t lisa_cross_attention_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d, int dtype);
+size_t lisa_cross_attention_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,
+                                            const lisa_rel_bias *bias, int dtype);
 lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q_strides, const void *K,
                                  const lisa_strides *k_strides, const void *V, const lisa_strides *v_strides,
                                  void *O, const lisa_strides *o_strides, float *lse, int B, int heads,

@@ -232,7 +232,7 @@ def test_same_bits_every_time_whatever_the_workspace_holds(lisa, dtype):
     out, lse = c.forward()
     first = c.backward(out, lse)
     for fill in (0x00, 0xFF):
-        nf = att.lisa_cross_attention_workspace_bytes(3, 4, 2, 130, 130, 64, dt)
+        nf = att.lisa_cross_attention_workspace_bytes(3, 4, 2, 130, 130, 64, c.bias.struct, dt)
         nb = att.lisa_cross_attention_backward_workspace_bytes(3, 4, 2, 130, 130, 64, c.bias.struct, dt)
         ws = torch.full((max(nf, nb, 16),), fill, dtype=torch.uint8, device="cuda")
         out2, lse2 = c.forward(workspace=ws)

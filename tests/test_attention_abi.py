@@ -120,7 +120,13 @@ def test_workspace_bytes():
     assert ws(2, 4, 2, 8, 8, 16, _bias(), lisa.LISA_F32) > plain
     assert ws(2, 4, 3, 8, 8, 16, None, lisa.LISA_F32) == 0 and ws(2, 4, 2, 8, 8, 48, None, lisa.LISA_F32) == 0
     assert ws(0, 4, 2, 8, 8, 16, None, lisa.LISA_F32) == 0
-    assert att.lisa_cross_attention_workspace_bytes(2, 4, 3, 8, 8, 16, lisa.LISA_F32) == 0
+    ws = att.lisa_cross_attention_workspace_bytes
+    assert ws(2, 4, 3, 8, 8, 16, None, lisa.LISA_F32) == 0                     # heads not shared evenly
+    assert ws(2, 4, 2, 8, 8, 16, None, lisa.LISA_F32) == 0                     # nothing needed
+    plain = ws(2, 4, 2, 200, 8, 16, None, lisa.LISA_BF16)
+    assert plain > 0 and ws(2, 4, 2, 200, 8, 16, _bias((1, 200)), lisa.LISA_BF16) > plain
+    assert ws(2, 4, 2, 1, 800, 16, None, lisa.LISA_BF16) == 0                  # single tokens
+    assert ws(2, 4, 2, 200, 8, 16, _bias((1, 200), step=(1, 0)), lisa.LISA_BF16) == 0
     assert att.lisa_relative_bias_backward_workspace_bytes(_bias(), 4) > 0
     assert att.lisa_relative_bias_backward_workspace_bytes(_bias(step=(1, 0)), 4) == 0
 
