@@ -26,8 +26,6 @@ namespace {
 constexpr int kTile = 64;
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float &o, float x) { o = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16 &o, float x) { o = __float2bfloat16_rn(x); }
 
@@ -419,7 +417,7 @@ cudaError_t run(dim3 grid, int floats, const Problem &p, cudaStream_t s) {
     const int bytes = (floats + (p.bias.mode ? p.bias.entries : 0)) * (int)sizeof(float);
     cudaError_t e = allow_smem<kKernel>();
     if (e != cudaSuccess) return e;
-    return launch_chained(kKernel, grid, kThreads, (size_t)bytes, s, p);
+    return launch_plain(kKernel, grid, kThreads, (size_t)bytes, s, p);
 }
 
 template <typename T, int D>

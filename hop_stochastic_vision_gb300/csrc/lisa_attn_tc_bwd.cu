@@ -1033,7 +1033,7 @@ template <auto kKernel>
 cudaError_t go(const Maps &m, const BwdParams &x, int bytes, cudaStream_t s) {
     cudaError_t e = allow_smem<kKernel>();
     if (e != cudaSuccess) return e;
-    return launch_chained(kKernel, dim3((unsigned)std::min(x.items, sms())), kThreads, bytes, s, m.q, m.d, m.k, m.v, x);
+    return launch_plain(kKernel, dim3((unsigned)std::min(x.items, sms())), kThreads, bytes, s, m.q, m.d, m.k, m.v, x);
 }
 
 }  // namespace
@@ -1099,7 +1099,7 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (p.q_splits > 1) {
         const size_t vecs = (size_t)p.B * p.kv_heads * p.m * (p.d / 4);
-        e = launch_chained(join_dkdv, dim3((unsigned)((vecs + 255) / 256), 2), 256, 0, s, p);
+        e = launch_plain(join_dkdv, dim3((unsigned)((vecs + 255) / 256), 2), 256, 0, s, p);
         if (e != cudaSuccess) return e;
     }
     if (p.bias.mode == 0) return cudaSuccess;

@@ -19,6 +19,12 @@ __device__ __forceinline__ void chain_begin() {
 }
 
 template <typename... KArgs, typename... Args>
+cudaError_t launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
+    kernel<<<grid, block, smem, s>>>(static_cast<KArgs>(args)...);
+    return cudaGetLastError();
+}
+
+template <typename... KArgs, typename... Args>
 cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at;

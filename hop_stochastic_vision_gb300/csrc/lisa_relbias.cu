@@ -292,7 +292,7 @@ template <typename T, int VEC>
 cudaError_t run_fold_vec(const FoldDev &f, const T *dbias, int matrices, cudaStream_t s) {
     cudaError_t e = allow_smem<fold_matrix<T, VEC>>();
     if (e != cudaSuccess) return e;
-    return launch_chained(fold_matrix<T, VEC>, dim3((unsigned)f.ktiles, (unsigned)f.qtiles, (unsigned)f.heads), 256,
+    return launch_plain(fold_matrix<T, VEC>, dim3((unsigned)f.ktiles, (unsigned)f.qtiles, (unsigned)f.heads), 256,
                           kFoldTileBytes + f.units * 4, s, f, dbias, matrices);
 }
 
@@ -390,7 +390,7 @@ size_t fold_bytes(const FoldDev &f) {
 
 cudaError_t launch_fold_sum(const FoldDev &f, float *dtable, cudaStream_t s) {
     const int width = std::min(256, (f.col_buckets + 31) / 32 * 32), groups = 1024 / width;
-    return launch_chained(fold_sum, dim3((unsigned)f.row_buckets, (unsigned)((f.col_buckets + width - 1) / width), (unsigned)f.heads),
+    return launch_plain(fold_sum, dim3((unsigned)f.row_buckets, (unsigned)((f.col_buckets + width - 1) / width), (unsigned)f.heads),
                           width * groups, 0, s, f, dtable, width, groups);
 }
 
@@ -418,12 +418,12 @@ cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const v
     g.part = static_cast<float *>(ws);
     dim3 grid((unsigned)(g.nchunk * g.ntile), (unsigned)(g.q_rows * g.k_rows), (unsigned)dev.heads);
     cudaError_t e = dtype == LISA_BF16
-                        ? launch_chained(bias_grad_part<__nv_bfloat16>, grid, g.threads, 0, s, g, static_cast<const __nv_bfloat16 *>(dbias))
-                        : launch_chained(bias_grad_part<float>, grid, g.threads, 0, s, g, static_cast<const float *>(dbias));
+                        ? launch_plain(bias_grad_part<__nv_bfloat16>, grid, g.threads, 0, s, g, static_cast<const __nv_bfloat16 *>(dbias))
+                        : launch_plain(bias_grad_part<float>, grid, g.threads, 0, s, g, static_cast<const float *>(dbias));
     if (e != cudaSuccess) return e;
     // 1024 threads as `groups` runs of partials by `width` column buckets
     const int width = std::min(256, (g.col_buckets + 31) / 32 * 32), groups = 1024 / width;
-    return launch_chained(bias_grad_sum, dim3((unsigned)g.row_buckets, (unsigned)((g.col_buckets + width - 1) / width), (unsigned)dev.heads),
+    return launch_plain(bias_grad_sum, dim3((unsigned)g.row_buckets, (unsigned)((g.col_buckets + width - 1) / width), (unsigned)dev.heads),
                           width * groups, 0, s, g, dtable, width, groups);
 }
 
