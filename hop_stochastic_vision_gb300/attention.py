@@ -152,8 +152,12 @@ class RelativeBias:
             raise ValueError("the bias table has %d rows, the rules give %d buckets"
                              % (table.shape[0], rows.buckets * cols.buckets))
         self.table = table
+        self.index = table.get_device()
+        self.heads = int(table.shape[1])
         self.q_grid = (int(q_grid[0]), int(q_grid[1]))
         self.k_grid = (int(k_grid[0]), int(k_grid[1]))
+        self.n = self.q_grid[0] * self.q_grid[1]
+        self.m = self.k_grid[0] * self.k_grid[1]
         self.starts = None
         start = (0, 0)
         if isinstance(query_start, torch.Tensor):
@@ -166,25 +170,13 @@ class RelativeBias:
         self.struct = lisa_rel_bias(table.data_ptr(), *self.q_grid, *self.k_grid, int(key_step[0]), int(key_step[1]),
                                     *start, None if self.starts is None else self.starts.data_ptr(), rows, cols)
 
-    @property
-    def heads(self) -> int:
-        return self.table.shape[1]
-
-    @property
-    def n(self) -> int:
-        return self.q_grid[0] * self.q_grid[1]
-
-    @property
-    def m(self) -> int:
-        return self.k_grid[0] * self.k_grid[1]
-
-
 def _raw_stream(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 
 
-# the same handle without the Stream object around it, where torch offers that
+# the same values without the objects and checks around them, where torch offers that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class _On:
@@ -193,24 +185,29 @@ class _On:
 
     def __init__(self, index, stream):
         self.index = index
-        self.device = self.other = None
-        if torch.cuda.current_device() != index:
-            self.device = torch.cuda.device(index)
-        if stream is not None:
-            self.other = torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index)))
+        self.device = torch.cuda.device(index)
+        self.stream = stream
 
     def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
-        if self.other is not None:
+        self.device.__enter__()
+        self.other = None
+        if self.stream is not None:
+            of = torch.device("cuda", self.index)
+            self.other = torch.cuda.stream(torch.cuda.ExternalStream(int(self.stream), device=of))
             self.other.__enter__()
-        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         if self.other is not None:
             self.other.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _run(index, stream, call, *args):
+    """call(raw stream, *args) on the tensors' device and the given or current stream."""
+    if stream is None and _current_device() == index:
+        return call(_raw_stream(index), *args)
+    with _On(index, stream):
+        return call(_raw_stream(index), *args)
 
 
 def _workspace(given, nbytes, device):
@@ -224,9 +221,15 @@ def _workspace(given, nbytes, device):
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
-@functools.lru_cache(maxsize=1024)
-def _strides_of(batch, head, token):
-    return lisa_strides(batch, head, token)
+@functools.lru_cache(maxsize=4096)
+def _strides_of(shape, stride) -> lisa_strides:
+    if len(shape) != 4:
+        raise ValueError("q, k, v, out, dout must be 4-d and share dtype float32 or bfloat16")
+    d = shape[3]
+    if stride[3] != 1 and d > 1:
+        raise ValueError("the elements of a token must be contiguous (last stride 1)")
+    # a stride that no step uses may be anything legal
+    return lisa_strides(*(stride[x] if shape[x] > 1 else d for x in range(3)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -234,47 +237,73 @@ def _plain_bytes(B, heads, kv_heads, n, m, d, dtype):
     return lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, None, dtype)
 
 
-def _strides(t: torch.Tensor, shape) -> lisa_strides:
-    b, h, n, d = t.stride()
-    if d != 1 and shape[3] > 1:
-        raise ValueError("the elements of a token must be contiguous (last stride 1)")
-    d = shape[3]      # a stride that no step uses: any legal value
-    return _strides_of(b if shape[0] > 1 else d, h if shape[1] > 1 else d, n if shape[2] > 1 else d)
+@functools.lru_cache(maxsize=64)
+def _default_scale(d):
+    return 1.0 / math.sqrt(d)
 
 
-def _check(index, dtype, tensors):
-    for t in tensors:
-        at = t.get_device()
-        if at != index or at < 0:
-            raise ValueError("the cross attention runs on CUDA tensors only" if at < 0
-                             else "tensors must be on one device")
-        if t.dim() != 4 or t.dtype != dtype:
-            raise ValueError("q, k, v, out, dout must be 4-d and share dtype float32 or bfloat16")
+def _strides(t, shape, dtype, index) -> lisa_strides:
+    """Strides of a tensor of the call, which has to match its device and type."""
+    if t.dtype != dtype:
+        raise ValueError("q, k, v, out, dout must be 4-d and share dtype float32 or bfloat16")
+    at = t.get_device()
+    if at != index or at < 0:
+        raise ValueError("the cross attention runs on CUDA tensors only" if at < 0
+                         else "tensors must be on one device")
+    return _strides_of(shape, t.stride())
 
 
-def _shapes(q, k, v, kv_lens, bias):
-    if q.dtype not in _DTYPES:
+def _prepare(q, k, v, kv_lens, bias, scale):
+    """Checks and the call's common arguments."""
+    dtype = q.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise ValueError("q, k, v must share dtype float32 or bfloat16")
-    index = q.get_device()
-    _check(index, q.dtype, (q, k, v))
-    B, heads, n, d = shape = q.shape
-    kv_shape = k.shape
+    index, shape, kv_shape = q.get_device(), q.shape, k.shape
+    qs, ks = _strides(q, shape, dtype, index), _strides(k, kv_shape, dtype, index)
+    vs = _strides(v, v.shape, dtype, index)
+    B, heads, n, d = shape
+    kv_heads, m = kv_shape[1], kv_shape[2]
     if kv_shape[0] != B or kv_shape[3] != d or v.shape != kv_shape:
         raise ValueError("k and v must be [B, kv_heads, m, d] for q [B, heads, n, d]")
-    kv_heads, m = kv_shape[1], kv_shape[2]
+    lens = struct = None
     if kv_lens is not None:
         if not (kv_lens.get_device() == index and kv_lens.dtype == torch.int32 and kv_lens.is_contiguous()
-                and tuple(kv_lens.shape) == (B,)):
+                and kv_lens.shape == (B,)):
             raise ValueError("kv_lens must be a contiguous int32 CUDA tensor [B]")
+        lens = kv_lens.data_ptr()
     if bias is not None:
-        if bias.table.get_device() != index:
+        if bias.index != index:
             raise ValueError("tensors must be on one device")
-        if bias.heads != heads or bias.n != n or bias.m != m:
+        if (bias.heads, bias.n, bias.m) != (heads, n, m):
             raise ValueError("the bias is of %d heads, %d queries and %d keys, the call of %d, %d and %d"
                              % (bias.heads, bias.n, bias.m, heads, n, m))
         if bias.starts is not None and bias.starts.shape[0] != B:
             raise ValueError("query_start must have one entry per batch entry")
-    return index, shape, kv_shape, B, heads, kv_heads, n, m, d
+        struct = bias.struct
+    tail = (B, heads, kv_heads, n, m, d, _default_scale(d) if scale is None else float(scale), lens, struct, dt)
+    return index, shape, kv_shape, (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs), tail
+
+
+def _forward(stream, q, index, shape, head, tail, return_lse, out, workspace):
+    device = q.device
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=device)
+    elif out.shape != shape:
+        raise ValueError("out must have q's shape")
+    os = _strides(out, shape, q.dtype, index)
+    B, heads, kv_heads, n, m, d, _, _, struct, dt = tail
+    lse = torch.empty((B, heads, n), dtype=torch.float32, device=device) if return_lse else None
+    lib = _library()
+    need = _plain_bytes(B, heads, kv_heads, n, m, d, dt) if struct is None else \
+        lib.lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, struct, dt)
+    keep, ws, nbytes = _workspace(workspace, need, device)
+    status = lib.lisa_cross_attention(*head, out.data_ptr(), os, lse.data_ptr() if return_lse else None, *tail, ws,
+                                      nbytes, stream)
+    del keep
+    if status != LISA_OK:
+        raise LisaError(status)
+    return (out, lse) if return_lse else out
 
 
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale=None, kv_lens=None,
@@ -287,30 +316,26 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale=
     (a new contiguous tensor unless ``out`` is given), with ``return_lse`` also
     the fp32 log-sum-exp [B, heads, n] that the backward pass reads.
     ``stream`` is a raw stream handle of the tensors' device."""
-    index, shape, kv_shape, B, heads, kv_heads, n, m, d = _shapes(q, k, v, kv_lens, bias)
-    dt = _DTYPES[q.dtype]
-    with _On(index, stream) as st:
-        device = q.device
-        if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=device)
-        else:
-            _check(index, q.dtype, (out,))
-            if out.shape != shape:
-                raise ValueError("out must have q's shape")
-        lse = torch.empty((B, heads, n), dtype=torch.float32, device=device) if return_lse else None
-        lib = _library()
-        need = _plain_bytes(B, heads, kv_heads, n, m, d, dt) if bias is None else \
-            lib.lisa_cross_attention_workspace_bytes(B, heads, kv_heads, n, m, d, bias.struct, dt)
-        keep, ws, nbytes = _workspace(workspace, need, device)
-        status = lib.lisa_cross_attention(
-            q.data_ptr(), _strides(q, shape), k.data_ptr(), _strides(k, kv_shape), v.data_ptr(), _strides(v, kv_shape),
-            out.data_ptr(), _strides(out, shape), lse.data_ptr() if return_lse else None, B, heads, kv_heads, n, m, d,
-            1.0 / math.sqrt(d) if scale is None else float(scale), None if kv_lens is None else kv_lens.data_ptr(),
-            None if bias is None else bias.struct, dt, ws, nbytes, st)
-        del keep
+    index, shape, _, head, tail = _prepare(q, k, v, kv_lens, bias, scale)
+    return _run(index, stream, _forward, q, index, shape, head, tail, return_lse, out, workspace)
+
+
+def _backward(stream, q, shape, kv_shape, head, saved, tail, bias, workspace):
+    device, dtype = q.device, q.dtype
+    dq = torch.empty(shape, dtype=dtype, device=device)
+    dk = torch.empty(kv_shape, dtype=dtype, device=device)
+    dv = torch.empty(kv_shape, dtype=dtype, device=device)
+    dtable = None if bias is None else torch.empty_like(bias.table)
+    B, heads, kv_heads, n, m, d, _, _, struct, dt = tail
+    lib = _library()
+    need = lib.lisa_cross_attention_backward_workspace_bytes(B, heads, kv_heads, n, m, d, struct, dt)
+    keep, ws, nbytes = _workspace(workspace, need, device)
+    status = lib.lisa_cross_attention_backward(*head, *saved, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                               None if bias is None else dtable.data_ptr(), *tail, ws, nbytes, stream)
+    del keep
     if status != LISA_OK:
         raise LisaError(status)
-    return (out, lse) if return_lse else out
+    return (dq, dk, dv) if bias is None else (dq, dk, dv, dtable)
 
 
 def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
@@ -319,36 +344,26 @@ def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     """Gradients of ``cross_attention`` for the upstream gradient ``dout``, given
     the forward's ``out`` and ``lse``: (dq, dk, dv), with ``bias`` also the
     table's gradient dtable (fp32, the table's shape), summed over the batch."""
-    index, shape, kv_shape, B, heads, kv_heads, n, m, d = _shapes(q, k, v, kv_lens, bias)
-    _check(index, q.dtype, (out, dout))
+    index, shape, kv_shape, head, tail = _prepare(q, k, v, kv_lens, bias, scale)
     if out.shape != shape or dout.shape != shape:
         raise ValueError("out and dout must have q's shape")
     if not (lse.get_device() == index and lse.dtype == torch.float32 and lse.is_contiguous()
-            and tuple(lse.shape) == (B, heads, n)):
+            and lse.shape == shape[:3]):
         raise ValueError("lse must be the forward's contiguous fp32 tensor [B, heads, n]")
     if bias is not None and bias.starts is not None:
         raise ValueError("a bias with a start for each batch entry has no backward")
-    dt = _DTYPES[q.dtype]
-    struct = None if bias is None else bias.struct
-    with _On(index, stream) as st:
-        device = q.device
-        dq = torch.empty(shape, dtype=q.dtype, device=device)
-        dk = torch.empty(kv_shape, dtype=q.dtype, device=device)
-        dv = torch.empty(kv_shape, dtype=q.dtype, device=device)
-        dtable = None if bias is None else torch.empty_like(bias.table)
-        lib = _library()
-        need = lib.lisa_cross_attention_backward_workspace_bytes(B, heads, kv_heads, n, m, d, struct, dt)
-        keep, ws, nbytes = _workspace(workspace, need, device)
-        status = lib.lisa_cross_attention_backward(
-            q.data_ptr(), _strides(q, shape), k.data_ptr(), _strides(k, kv_shape), v.data_ptr(), _strides(v, kv_shape),
-            out.data_ptr(), _strides(out, shape), lse.data_ptr(), dout.data_ptr(), _strides(dout, shape), dq.data_ptr(),
-            dk.data_ptr(), dv.data_ptr(), None if bias is None else dtable.data_ptr(), B, heads, kv_heads, n, m, d,
-            1.0 / math.sqrt(d) if scale is None else float(scale), None if kv_lens is None else kv_lens.data_ptr(),
-            struct, dt, ws, nbytes, st)
-        del keep
+    saved = (out.data_ptr(), _strides(out, shape, q.dtype, index), lse.data_ptr(), dout.data_ptr(),
+             _strides(dout, shape, q.dtype, index))
+    return _run(index, stream, _backward, q, shape, kv_shape, head, saved, tail, bias, workspace)
+
+
+def _matrix(stream, bias, dtype, out):
+    if out is None:
+        out = torch.empty((bias.heads, bias.n, bias.m), dtype=dtype, device=bias.table.device)
+    status = _library().lisa_relative_bias(bias.struct, bias.heads, out.data_ptr(), _DTYPES[dtype], stream)
     if status != LISA_OK:
         raise LisaError(status)
-    return (dq, dk, dv) if bias is None else (dq, dk, dv, dtable)
+    return out
 
 
 def relative_bias(bias: RelativeBias, dtype: torch.dtype = torch.float32, *, out=None, stream=None) -> torch.Tensor:
@@ -357,17 +372,23 @@ def relative_bias(bias: RelativeBias, dtype: torch.dtype = torch.float32, *, out
         raise ValueError("dtype must be float32 or bfloat16")
     if bias.starts is not None:
         raise ValueError("a bias with a start for each batch entry has no matrix")
-    shape = (bias.heads, bias.n, bias.m)
-    with _On(bias.table.get_device(), stream) as st:
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=bias.table.device)
-        elif not (out.is_cuda and out.device == bias.table.device and out.dtype == dtype and out.is_contiguous()
-                  and tuple(out.shape) == shape):
-            raise ValueError("out must be a contiguous %s CUDA tensor [heads, n, m]" % (dtype,))
-        status = _library().lisa_relative_bias(bias.struct, bias.heads, out.data_ptr(), _DTYPES[dtype], st)
+    if out is not None and not (out.get_device() == bias.index and out.dtype == dtype and out.is_contiguous()
+                                and out.shape == (bias.heads, bias.n, bias.m)):
+        raise ValueError("out must be a contiguous %s CUDA tensor [heads, n, m]" % (dtype,))
+    return _run(bias.index, stream, _matrix, bias, dtype, out)
+
+
+def _matrix_backward(stream, bias, dbias, workspace):
+    dtable = torch.empty_like(bias.table)
+    lib = _library()
+    keep, ws, nbytes = _workspace(workspace, lib.lisa_relative_bias_backward_workspace_bytes(bias.struct, bias.heads),
+                                  dbias.device)
+    status = lib.lisa_relative_bias_backward(bias.struct, bias.heads, dbias.data_ptr(), _DTYPES[dbias.dtype],
+                                             dtable.data_ptr(), ws, nbytes, stream)
+    del keep
     if status != LISA_OK:
         raise LisaError(status)
-    return out
+    return dtable
 
 
 def relative_bias_backward(bias: RelativeBias, dbias: torch.Tensor, *, workspace=None, stream=None) -> torch.Tensor:
@@ -375,17 +396,7 @@ def relative_bias_backward(bias: RelativeBias, dbias: torch.Tensor, *, workspace
     [heads, n, m] (fp32 or bf16) over the pairs of each bucket."""
     if bias.starts is not None:
         raise ValueError("a bias with a start for each batch entry has no matrix")
-    if not (dbias.is_cuda and dbias.device == bias.table.device and dbias.dtype in _DTYPES and dbias.is_contiguous()
-            and tuple(dbias.shape) == (bias.heads, bias.n, bias.m)):
+    if not (dbias.get_device() == bias.index and dbias.dtype in _DTYPES and dbias.is_contiguous()
+            and dbias.shape == (bias.heads, bias.n, bias.m)):
         raise ValueError("dbias must be a contiguous fp32 or bf16 CUDA tensor [heads, n, m]")
-    with _On(dbias.get_device(), stream) as st:
-        dtable = torch.empty_like(bias.table)
-        lib = _library()
-        keep, ws, nbytes = _workspace(workspace, lib.lisa_relative_bias_backward_workspace_bytes(bias.struct, bias.heads),
-                                      dbias.device)
-        status = lib.lisa_relative_bias_backward(bias.struct, bias.heads, dbias.data_ptr(), _DTYPES[dbias.dtype],
-                                             dtable.data_ptr(), ws, nbytes, st)
-        del keep
-    if status != LISA_OK:
-        raise LisaError(status)
-    return dtable
+    return _run(bias.index, stream, _matrix_backward, bias, dbias, workspace)
