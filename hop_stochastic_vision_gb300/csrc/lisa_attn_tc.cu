@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(x, it);
             if (kBias && w.h != lut_head) {
-                load_offsets(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
+                load_offsets<256>(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
                 lut_head = w.h;
             }
             if (t >= w.nt) {   // this tile has no rows

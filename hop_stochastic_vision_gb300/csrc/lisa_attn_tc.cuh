@@ -181,10 +181,11 @@ struct Cursor {
 };
 
 // The head's offset table (bias_offsets: fp32, log2(e) folded in) by one bulk
-// copy.  Called by the 256 arithmetic threads together; `count` copies so far.
+// copy.  Called by the kThreads arithmetic threads together; `count` copies so far.
+template <int kThreads>
 __device__ __forceinline__ void load_offsets(const BiasDev &b, int head, float *lut, uint64_t *bar, int &count, int tid,
                                              const Guard &g) {
-    asm volatile("bar.sync 1, 256;" ::: "memory");   // every warp is past its reads of the old table
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");   // every warp is past its reads of the old table
     if (tid == 0) {
         fence_proxy_async();
         const uint32_t bytes = (uint32_t)(b.entries + 3) / 4 * 16;

@@ -16,9 +16,10 @@
 // Scores are recomputed in each (7 products for 5) so that every sum has one
 // owner: no atomics, no fp32 dQ in memory, the same bits every time.
 //
-// Two warpgroups share a tile by columns, 64 each, a thread per row.  The
-// threads take S and dP into registers as soon as they are there, so the next
-// tile's products run under this tile's arithmetic.
+// Four warpgroups share a tile by columns, 32 each, a thread per row (with two of
+// 64 columns the schedulers had two warps each and issued one cycle in five).
+// The threads take S and dP into registers as soon as they are there, so the
+// next tile's products run under this tile's arithmetic.
 #include "lisa_attn_tc.cuh"
 #include "lisa_fold.cuh"
 
@@ -26,9 +27,12 @@ namespace lisa {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 384;      // 8 warps of arithmetic; products (two warps), loads, a helper
-constexpr int kDqOut = 8 * 2048, kDkvOut = 8 * 4096;   // staging blocks of the eight warps
-constexpr int kRegsMath = 208, kRegsControl = 88;
+constexpr int kMath = 512;         // threads of arithmetic: 16 warps
+constexpr int kMathWarps = kMath / 32;
+constexpr int kThreads = kMath + 128;   // behind them: products (two warps), loads, a helper
+constexpr int kFront = kMathWarps, kLoads = kMathWarps + 1, kBack = kMathWarps + 2, kHelper = kMathWarps + 3;
+constexpr int kStrip = 32;         // columns of a thread's row
+constexpr int kDqOut = kMathWarps * 1024, kDkvOut = kMathWarps * 2048;   // staging blocks of the math warps
 constexpr int kMaxStages = 4;
 constexpr uint32_t kPair = 2 * kTileBytes / 16;   // a ring stage of two tiles, in descriptor units
 
@@ -54,37 +58,37 @@ __device__ __forceinline__ float neg_lse2(const float *lse, size_t at, bool in) 
     return l == -INFINITY ? -INFINITY : -l * kLog2e;   // rows without keys: every weight 2^-inf = 0
 }
 
-// Weights of 64 columns of a row of queries, in place: s -> 2^(scale2 s + bias - lse).
+// Weights of a strip of a row of queries, in place: s -> 2^(scale2 s + bias - lse).
 // `c0`: first column of the tile, `keys`: valid columns from there (may be <= 0).
 template <int kBias>
-__device__ __forceinline__ void row_weights(float (&s)[64], const BiasDev &b, const float *lut, const uint16_t *key_off,
+__device__ __forceinline__ void row_weights(float (&s)[kStrip], const BiasDev &b, const float *lut, const uint16_t *key_off,
                                             int j0, int keys, int oq, int oq_lo, float scale2, float nl) {
     if (kBias == 0) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, nl, nl);
+        for (int c = 0; c < kStrip; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, nl, nl);
     } else if (kBias == 1) {
         const int oq_hi = oq_lo + 31, last = b.entries - 1;
         const int lo = b.step_c * j0 - oq_hi, hi = b.step_c * (j0 + max(keys, 1) - 1) - oq_lo;
         if (hi <= 0 || lo >= last) {
             const float add = nl + lut[hi <= 0 ? 0 : last];
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, add, add);
+            for (int c = 0; c < kStrip; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, add, add);
         } else {
             const int off = b.step_c * j0 - oq;
-            if (b.step_c == 1 && lo >= 0 && lo + 31 + 63 <= last) {
+            if (b.step_c == 1 && lo >= 0 && lo + 31 + kStrip - 1 <= last) {
                 const float *l = lut + off;
 #pragma unroll
-                for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, l[c]) + nl;
+                for (int c = 0; c < kStrip; ++c) s[c] = fmaf(s[c], scale2, l[c]) + nl;
             } else {
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
+                for (int c = 0; c < kStrip; ++c)
                     s[c] = fmaf(s[c], scale2, lut[min(max(off + b.step_c * c, 0), last)]) + nl;
             }
         }
     } else {
         const float *l = lut - oq;   // inside the table by construction
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < kStrip; c += 4) {
             const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
             s[c] = fmaf(s[c], scale2, l[a.x & 0xFFFFu]) + nl;
             s[c + 1] = fmaf(s[c + 1], scale2, l[a.x >> 16]) + nl;
@@ -92,20 +96,19 @@ __device__ __forceinline__ void row_weights(float (&s)[64], const BiasDev &b, co
             s[c + 3] = fmaf(s[c + 3], scale2, l[a.y >> 16]) + nl;
         }
     }
-    if (keys < 64) {
+    if (keys < kStrip) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
+        for (int c = 0; c < kStrip; ++c)
             if (c >= keys) s[c] = -INFINITY;
     }
 #pragma unroll
-    for (int c = 0; c < 64; ++c) s[c] = ex2_approx(s[c]);
+    for (int c = 0; c < kStrip; ++c) s[c] = ex2_approx(s[c]);
 }
 
-// A 64-column strip.  Columns that the products did not reach hold whatever was
-// there before and are not used (a load under a condition costs copies of all 64).
-__device__ __forceinline__ void load_strip(uint32_t taddr, float (&v)[64]) {
+// A strip.  Columns that the products did not reach hold whatever was
+// there before and are not used (a load under a condition costs copies of all).
+__device__ __forceinline__ void load_strip(uint32_t taddr, float (&v)[kStrip]) {
     tmem_ld32_nowait(taddr, v);
-    tmem_ld32_nowait(taddr + 32, v + 32);
     tc_wait_ld();
 }
 
@@ -114,7 +117,7 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
     if (lane == 0) mbar_arrive(smem_u32(bar));
 }
 
-__device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
 
 // The products' thread waits for the last use of every ring slot, so nothing
 // arrives on the CTA's barriers once it has gone.
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) DqBars bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
-    __shared__ float other[kRows], rows_delta[kRows];
+    __shared__ float other[3][kRows], rows_delta[kRows];
     const Problem &p = x.p;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
@@ -164,14 +167,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&bar.s_full), 1);
         mbar_init(smem_u32(&bar.dp_full), 1);
         mbar_init(smem_u32(&bar.dq_done), 1);
-        mbar_init(smem_u32(&bar.s_free), 8);
-        mbar_init(smem_u32(&bar.dp_free), 8);
-        mbar_init(smem_u32(&bar.ds_full), 8);
+        mbar_init(smem_u32(&bar.s_free), kMathWarps);
+        mbar_init(smem_u32(&bar.dp_free), kMathWarps);
+        mbar_init(smem_u32(&bar.ds_full), kMathWarps);
         mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (warp == kFront) tmem_alloc(smem_u32(&tmem_slot), 512);
     if (kBias == 2)
         for (int j = tid; j < (p.m + 127) / 128 * 128; j += kThreads) key_off[j] = (uint16_t)off_key(p.bias, min(j, p.m - 1));
     tc_fence_before();
@@ -195,10 +198,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return w;
     };
 
-    if (warp >= 8) set_regs_down<kRegsControl>();
-    if (warp == 11) {
-        // idle: completes the control warps' group of four
-    } else if (warp == 9) {
+    if (warp == kHelper) {
+        // nothing to help with here
+    } else if (warp == kLoads) {
         if (lane == 0) {
             int kt = 0, nq = 0;
             Cursor c, cq;
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < x.q_slots; ++t) drain(&bar.q_empty[t], uses_of(nq, t, x.q_slots), x.err);
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == kFront) {
         // S and dP of each tile
         int kt = 0;
         Cursor c, cq;
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (warp == 10) {
+    } else if (warp == kBack) {
         // dQ += dS K.  S has read the K tile too: dS comes of it.
         int kt = 0;
         Cursor c;
@@ -285,15 +287,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        set_regs_up<kRegsMath>();
-        const int half = warp >> 2, wt = tid & 127;
+        const int strip = warp >> 2, c0 = kStrip * strip, wt = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
         int kt = 0, lut_head = -1, luts = 0;
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
             if (kBias && w.h != lut_head) {
-                load_offsets(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
+                load_offsets<kMath>(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
                 lut_head = w.h;
             }
             const int i = w.q0 + wt;
@@ -307,10 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(p.dO.p) + (long long)w.b * p.dO.sb +
                                          (long long)w.h * p.dO.sh;
                 const int c = 8 * (lane & 7);
-                uint4 a[4], b[4];
+                uint4 a[2], b[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = w.q0 + 16 * warp + 4 * e + (lane >> 3);
+                for (int e = 0; e < 2; ++e) {
+                    const int r = w.q0 + 8 * warp + 4 * e + (lane >> 3);
                     a[e] = b[e] = make_uint4(0, 0, 0, 0);
                     if (r < p.n && c < p.d) {
                         a[e] = *reinterpret_cast<const uint4 *>(o + (long long)r * p.O.st + c);
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2; ++e) {
                     float v = bf16_lo(a[e].x) * bf16_lo(b[e].x);
                     v = fmaf(bf16_hi(a[e].x), bf16_hi(b[e].x), v);
                     v = fmaf(bf16_lo(a[e].y), bf16_lo(b[e].y), v);
@@ -329,10 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v = fmaf(bf16_hi(a[e].w), bf16_hi(b[e].w), v);
 #pragma unroll
                     for (int m = 4; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-                    if ((lane & 7) == 0) rows_delta[16 * warp + 4 * e + (lane >> 3)] = v;
+                    if ((lane & 7) == 0) rows_delta[8 * warp + 4 * e + (lane >> 3)] = v;
                 }
             }
-            math_barrier();   // also: the halves of the previous item's delta have been read
+            math_barrier();   // also: the strips of the previous item's delta have been read
             const float delta = w.tiles > 0 ? rows_delta[wt] : 0.f;
             float exact = 0.f;
             int oq = 0, oq_lo = 0;
@@ -342,49 +343,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 oq_lo = off_query(p.bias, i - lane, start);
             }
             for (int j = 0; j < w.tiles; ++j, ++kt) {
-                const int keys = tile_keys(w.len, j), cols = tile_cols(keys), j0 = j * kRows + 64 * half;
-                const bool any = 64 * half < cols;
-                float s[64];
+                const int keys = tile_keys(w.len, j), cols = tile_cols(keys), j0 = j * kRows + c0;
+                float s[kStrip];
                 wait_on(smem_u32(&bar.s_full), kt & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip(tS + 64 * half + lanes, s);
+                load_strip(tS + c0 + lanes, s);
                 tc_fence_before();
                 arrive_warp(&bar.s_free, lane);
-                if (any) row_weights<kBias>(s, p.bias, lut, key_off, j0, keys - 64 * half, oq, oq_lo, scale2, nl);
+                row_weights<kBias>(s, p.bias, lut, key_off, j0, keys - c0, oq, oq_lo, scale2, nl);
+                float dp[kStrip];
                 wait_on(smem_u32(&bar.dp_full), kt & 1, guard, kErrTimeoutMma);
-                // the previous dS has been read; every warp sees every phase, with a strip of its own or not
-                if (kt > 0) wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
+                load_strip(tP + c0 + lanes, dp);
+                tc_fence_before();
+                arrive_warp(&bar.dp_free, lane);
+                // the previous dS has been read
+                if (kt > 0) wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
                 float e0 = 0.f, e1 = 0.f;
+                uint32_t ds[kStrip / 2];
+                if (keys - c0 < kStrip) {   // dP of keys behind the last one holds whatever their values hold
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    float dp[32];
-                    uint32_t ds[16];
-                    tmem_ld32_nowait(tP + 64 * half + c + lanes, dp);
-                    tc_wait_ld();
-                    if (c == 32) {
-                        tc_fence_before();
-                        arrive_warp(&bar.dp_free, lane);
-                    }
-                    if (any) {
-                        if (keys - 64 * half < 64) {   // dP of keys behind the last one holds whatever their values hold
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (c + e >= keys - 64 * half) dp[e] = 0.f;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float u, v;
-                            mul2(dp[e], dp[e + 1], s[c + e], s[c + e + 1], dp[e], dp[e + 1]);
-                            add2(e0, e1, e0, e1, dp[e], dp[e + 1]);
-                            fma2(u, v, s[c + e], s[c + e + 1], -delta, -delta, dp[e], dp[e + 1]);
-                            ds[e >> 1] = pack_bf16(u, v);
-                        }
-                        tmem_st16(tDs + 32 * half + c / 2 + lanes, ds);
-                    }
+                    for (int e = 0; e < kStrip; ++e)
+                        if (e >= keys - c0) dp[e] = 0.f;
                 }
+#pragma unroll
+                for (int e = 0; e < kStrip; e += 2) {
+                    float u, v;
+                    mul2(dp[e], dp[e + 1], s[e], s[e + 1], dp[e], dp[e + 1]);
+                    add2(e0, e1, e0, e1, dp[e], dp[e + 1]);
+                    fma2(u, v, s[e], s[e + 1], -delta, -delta, dp[e], dp[e + 1]);
+                    ds[e >> 1] = pack_bf16(u, v);
+                }
+                tc_fence_after();
+                tmem_st16(tDs + c0 / 2 + lanes, ds);
                 exact += e0 + e1;
-                if (half == 0 && keys < cols && w.len < p.m) {
+                if (strip == 0 && keys < cols && w.len < p.m) {
                     // S is done with the tile: what stands behind the last key may not meet dS = 0
                     zero_rows(ring + 2 * (kt % x.stages) * kTileBytes, keys, cols, wt);
                     fence_proxy_async();
@@ -393,31 +386,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 arrive_warp(&bar.ds_full, lane);
             }
-            // the two halves of the keys' share of delta
-            if (half == 1) other[wt] = exact;
+            // the strips' shares of delta
+            if (strip > 0) other[strip - 1][wt] = exact;
             math_barrier();
-            if (half == 0 && in) p.delta[row] = exact + other[wt];
-            float o[32];
+            if (strip == 0 && in) p.delta[row] = (exact + other[0][wt]) + (other[1][wt] + other[2][wt]);
+            float o[16];
             if (w.tiles > 0) {
                 wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                tmem_ld32_nowait(tDq + 32 * half + lanes, o);
+                uint32_t u[16];
+                tmem_ld16(tDq + 16 * strip + lanes, u);
                 tc_wait_ld();
                 tc_fence_before();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) o[c] = __uint_as_float(u[c]);
             } else {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) o[c] = 0.f;
+                for (int c = 0; c < 16; ++c) o[c] = 0.f;
             }
             const int i0 = i - lane;
-            store_rows_bf16<32>(base + x.off_out + (uint32_t)warp * 2048u, o, p.scale,
-                                static_cast<__nv_bfloat16 *>(p.dQ) + (row - lane) * p.d + 32 * half, p.d, p.n - i0,
-                                p.d - 32 * half, lane);
+            store_rows_bf16<16>(base + x.off_out + (uint32_t)warp * 1024u, o, p.scale,
+                                static_cast<__nv_bfloat16 *>(p.dQ) + (row - lane) * p.d + 16 * strip, p.d, p.n - i0,
+                                p.d - 16 * strip, lane);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == kFront) tmem_dealloc(tmem, 512);
 }
 
 // --------------------------------------------------------------------- dK, dV
@@ -459,21 +455,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bar.d_full[s]), 1);
             mbar_init(smem_u32(&bar.q_empty[s]), 1);
             mbar_init(smem_u32(&bar.aux_full[s]), 1);
-            mbar_init(smem_u32(&bar.aux_empty[s]), 8);
+            mbar_init(smem_u32(&bar.aux_empty[s]), kMathWarps);
         }
         mbar_init(smem_u32(&bar.s_full), 1);
         mbar_init(smem_u32(&bar.dp_full), 1);
         mbar_init(smem_u32(&bar.dv_done), 1);
         mbar_init(smem_u32(&bar.dk_done), 1);
-        mbar_init(smem_u32(&bar.s_free), 8);
-        mbar_init(smem_u32(&bar.dp_free), 8);
-        mbar_init(smem_u32(&bar.p_full), 8);
-        mbar_init(smem_u32(&bar.ds_full), 8);
+        mbar_init(smem_u32(&bar.s_free), kMathWarps);
+        mbar_init(smem_u32(&bar.dp_free), kMathWarps);
+        mbar_init(smem_u32(&bar.p_full), kMathWarps);
+        mbar_init(smem_u32(&bar.ds_full), kMathWarps);
         mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (warp == kFront) tmem_alloc(smem_u32(&tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -500,8 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return w;
     };
 
-    if (warp >= 8) set_regs_down<kRegsControl>();
-    if (warp == 11) {
+    if (warp == kHelper) {
         // per-query scalars of each tile
         int n = 0;
         Cursor c;
@@ -525,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 arrive_warp(&bar.aux_full[s], lane);
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == kLoads) {
         if (lane == 0) {
             int n = 0, items = 0;
             Cursor c;
@@ -557,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain(&bar.kv_empty, items, x.err);
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == kFront) {
         // S^T and dP^T of each tile
         int n = 0, items = 0;
         Cursor c;
@@ -592,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (warp == 10) {
+    } else if (warp == kBack) {
         // dV += P^T dO, dK += dS^T Q.  S^T and dP^T have read the tiles too: P and dS come of them.
         int n = 0;
         Cursor c;
@@ -622,8 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        set_regs_up<kRegsMath>();
-        const int half = warp >> 2, wt = tid & 127;
+        const int strip = warp >> 2, c0 = kStrip * strip, wt = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
         int n = 0, lut_head = -1, luts = 0;
@@ -636,145 +630,128 @@ __global__ void __launch_bounds__(kThreads, 1)
             int h = w.g * p.group + split(qt, x.div_qtiles);
             for (int u = w.u0; u < w.u1; ++u, ++n, ca.next(x.stages), h += qt == x.qtiles - 1, qt = qt == x.qtiles - 1 ? 0 : qt + 1) {
                 if (kBias && h != lut_head) {
-                    load_offsets(p.bias, h, lut, &bar.lut_full, luts, tid, guard);
+                    load_offsets<kMath>(p.bias, h, lut, &bar.lut_full, luts, tid, guard);
                     lut_head = h;
                 }
                 const int cols = tile_cols(min(kRows, p.n - qt * kRows));
-                const bool any = 64 * half < cols;
                 const QueryAux &a = aux[ca.slot];
-                const int c0 = 64 * half;
-                float s[64];
+                float s[kStrip];
                 wait_on(smem_u32(&bar.aux_full[ca.slot]), ca.phase, guard, kErrTimeoutLoad);
                 wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 load_strip(tS + c0 + lanes, s);
                 tc_fence_before();
                 arrive_warp(&bar.s_free, lane);
-                if (any) {
-                    if (kBias == 1) {
-                        const int last = p.bias.entries - 1;
-                        const int off = ok - a.oq[c0];   // column c: off - c
-                        const int off_lo = __shfl_sync(0xFFFFFFFFu, off, 0), off_hi = __shfl_sync(0xFFFFFFFFu, off, 31);
-                        // rows of one warp are 32 keys in order, all offsets of the strip in off_lo - 63 .. off_hi
-                        if (off_hi <= 0 || off_lo - 63 >= last) {
-                            const float add = lut[off_hi <= 0 ? 0 : last];
+                if (kBias == 1) {
+                    const int last = p.bias.entries - 1;
+                    const int off = ok - a.oq[c0];   // column c: off - c
+                    const int off_lo = __shfl_sync(0xFFFFFFFFu, off, 0), off_hi = __shfl_sync(0xFFFFFFFFu, off, 31);
+                    // rows of one warp are 32 keys in order, all offsets of the strip in off_lo - 31 .. off_hi
+                    if (off_hi <= 0 || off_lo - (kStrip - 1) >= last) {
+                        const float add = lut[off_hi <= 0 ? 0 : last];
 #pragma unroll
-                            for (int c = 0; c < 64; c += 4) {
-                                const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
-                                fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, l.x, l.y);
-                                fma2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], scale2, scale2, l.z, l.w);
-                                add2(s[c], s[c + 1], s[c], s[c + 1], add, add);
-                                add2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], add, add);
-                            }
-                        } else if (off_lo - 63 >= 0 && off_hi <= last) {
-                            const float *l = lut + off;
-#pragma unroll
-                            for (int c = 0; c < 64; ++c) s[c] = fmaf(s[c], scale2, l[-c]) + a.nl[c0 + c];
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 64; ++c)
-                                s[c] = fmaf(s[c], scale2, lut[min(max(off - c, 0), last)]) + a.nl[c0 + c];
-                        }
-                    } else if (kBias == 2) {
-                        const float *l4 = lut + ok;   // inside the table by construction
-#pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
-                            const int4 o = *reinterpret_cast<const int4 *>(a.oq + c0 + c);
-                            const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
-                            s[c] = fmaf(s[c], scale2, l4[-o.x]) + l.x;
-                            s[c + 1] = fmaf(s[c + 1], scale2, l4[-o.y]) + l.y;
-                            s[c + 2] = fmaf(s[c + 2], scale2, l4[-o.z]) + l.z;
-                            s[c + 3] = fmaf(s[c + 3], scale2, l4[-o.w]) + l.w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
+                        for (int c = 0; c < kStrip; c += 4) {
                             const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
                             fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, l.x, l.y);
                             fma2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], scale2, scale2, l.z, l.w);
+                            add2(s[c], s[c + 1], s[c], s[c + 1], add, add);
+                            add2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], add, add);
                         }
+                    } else if (off_lo - (kStrip - 1) >= 0 && off_hi <= last) {
+                        const float *l = lut + off;
+#pragma unroll
+                        for (int c = 0; c < kStrip; ++c) s[c] = fmaf(s[c], scale2, l[-c]) + a.nl[c0 + c];
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kStrip; ++c)
+                            s[c] = fmaf(s[c], scale2, lut[min(max(off - c, 0), last)]) + a.nl[c0 + c];
+                    }
+                } else if (kBias == 2) {
+                    const float *l4 = lut + ok;   // inside the table by construction
+#pragma unroll
+                    for (int c = 0; c < kStrip; c += 4) {
+                        const int4 o = *reinterpret_cast<const int4 *>(a.oq + c0 + c);
+                        const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
+                        s[c] = fmaf(s[c], scale2, l4[-o.x]) + l.x;
+                        s[c + 1] = fmaf(s[c + 1], scale2, l4[-o.y]) + l.y;
+                        s[c + 2] = fmaf(s[c + 2], scale2, l4[-o.z]) + l.z;
+                        s[c + 3] = fmaf(s[c + 3], scale2, l4[-o.w]) + l.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kStrip; c += 4) {
+                        const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
+                        fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, l.x, l.y);
+                        fma2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], scale2, scale2, l.z, l.w);
                     }
                 }
-                // the previous P has been read; every warp sees every phase, with a strip of its own or not
+                // the previous P has been read
                 if (n > 0) wait_on(smem_u32(&bar.dv_done), (n - 1) & 1, guard, kErrTimeoutMma);
-                if (any) {
+                uint32_t out[kStrip / 2];
 #pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        uint32_t out[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            s[c + e] = ex2_approx(s[c + e]);
-                            s[c + e + 1] = ex2_approx(s[c + e + 1]);
-                            out[e >> 1] = pack_bf16(s[c + e], s[c + e + 1]);
-                        }
-                        tmem_st16(tPw + 32 * half + c / 2 + lanes, out);
-                    }
-                    tc_wait_st();
+                for (int e = 0; e < kStrip; e += 2) {
+                    s[e] = ex2_approx(s[e]);
+                    s[e + 1] = ex2_approx(s[e + 1]);
+                    out[e >> 1] = pack_bf16(s[e], s[e + 1]);
                 }
+                tc_fence_after();
+                tmem_st16(tPw + c0 / 2 + lanes, out);
+                tc_wait_st();
                 tc_fence_before();
                 arrive_warp(&bar.p_full, lane);
+                float dp[kStrip];
                 wait_on(smem_u32(&bar.dp_full), n & 1, guard, kErrTimeoutMma);
-                if (n > 0) wait_on(smem_u32(&bar.dk_done), (n - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
+                load_strip(tD + c0 + lanes, dp);
+                tc_fence_before();
+                arrive_warp(&bar.dp_free, lane);
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    float dp[32];
-                    uint32_t out[16];
-                    tmem_ld32_nowait(tD + c0 + c + lanes, dp);
-                    tc_wait_ld();
-                    if (c == 32) {
-                        tc_fence_before();
-                        arrive_warp(&bar.dp_free, lane);
-                    }
-                    if (any) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 d = *reinterpret_cast<const float4 *>(a.minus_delta + c0 + c + e);
-                            add2(dp[e], dp[e + 1], dp[e], dp[e + 1], d.x, d.y);
-                            add2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], d.z, d.w);
-                            mul2(dp[e], dp[e + 1], dp[e], dp[e + 1], s[c + e], s[c + e + 1]);
-                            mul2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], s[c + e + 2], s[c + e + 3]);
-                            out[e >> 1] = pack_bf16(dp[e], dp[e + 1]);
-                            out[(e >> 1) + 1] = pack_bf16(dp[e + 2], dp[e + 3]);
-                        }
-                        tmem_st16(tDs + 32 * half + c / 2 + lanes, out);
-                    }
+                for (int e = 0; e < kStrip; e += 4) {
+                    const float4 d = *reinterpret_cast<const float4 *>(a.minus_delta + c0 + e);
+                    add2(dp[e], dp[e + 1], dp[e], dp[e + 1], d.x, d.y);
+                    add2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], d.z, d.w);
+                    mul2(dp[e], dp[e + 1], dp[e], dp[e + 1], s[e], s[e + 1]);
+                    mul2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], s[e + 2], s[e + 3]);
+                    out[e >> 1] = pack_bf16(dp[e], dp[e + 1]);
+                    out[(e >> 1) + 1] = pack_bf16(dp[e + 2], dp[e + 3]);
                 }
                 arrive_warp(&bar.aux_empty[ca.slot], lane);
+                if (n > 0) wait_on(smem_u32(&bar.dk_done), (n - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                tmem_st16(tDs + c0 / 2 + lanes, out);
                 tc_wait_st();
                 tc_fence_before();
                 arrive_warp(&bar.ds_full, lane);
             }
-            // ---- warpgroup 0 stores dV, warpgroup 1 dK; rows behind the last key are 0
-            float o[64];
+            // ---- strips 0, 1 store dV, 2 and 3 dK, 32 columns each; rows behind the last key are 0
+            float o[kStrip];
+            const int dk = strip >> 1, oc = kStrip * (strip & 1);
             const bool some = w.u0 < w.u1 && j < w.len;
-            if (w.u0 < w.u1) {
-                wait_on(smem_u32(half ? &bar.dk_done : &bar.dv_done), (n - 1) & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                load_strip((half ? tDk : tDv) + lanes, o);
-                tc_fence_before();
-            }
+            if (w.u0 < w.u1) wait_on(smem_u32(dk ? &bar.dk_done : &bar.dv_done), (n - 1) & 1, guard, kErrTimeoutMma);
+            tc_fence_after();
+            load_strip((dk ? tDk : tDv) + oc + lanes, o);
+            tc_fence_before();
 #pragma unroll
-            for (int c = 0; c < 64; ++c) o[c] = some ? o[c] : 0.f;
+            for (int c = 0; c < kStrip; ++c) o[c] = some ? o[c] : 0.f;
             const size_t row = ((size_t)w.b * p.kv_heads + w.g) * p.m + j;
             if (x.splits == 1) {
                 const int r0 = j - lane;
-                store_rows_bf16<64>(base + x.off_out + (uint32_t)warp * 4096u, o, half ? p.scale : 1.f,
-                                    static_cast<__nv_bfloat16 *>(half ? p.dK : p.dV) + (row - lane) * p.d, p.d,
-                                    p.m - r0, p.d, lane);
+                store_rows_bf16<kStrip>(base + x.off_out + (uint32_t)warp * 2048u, o, dk ? p.scale : 1.f,
+                                        static_cast<__nv_bfloat16 *>(dk ? p.dK : p.dV) + (row - lane) * p.d + oc, p.d,
+                                        p.m - r0, p.d - oc, lane);
             } else if (j < p.m) {
                 float4 *out = reinterpret_cast<float4 *>(
-                    (half ? p.dk_part : p.dv_part) + ((size_t)w.split * ((size_t)p.B * p.kv_heads * p.m) + row) * p.d);
+                    (dk ? p.dk_part : p.dv_part) + ((size_t)w.split * ((size_t)p.B * p.kv_heads * p.m) + row) * p.d + oc);
 #pragma unroll
-                for (int c = 0; c < 64; c += 4)
-                    if (c < p.d) out[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                for (int c = 0; c < kStrip; c += 4)
+                    if (oc + c < p.d) out[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
             }
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == kFront) tmem_dealloc(tmem, 512);
 }
 
 // dK, dV from the parts of the queries, in order.
@@ -827,13 +804,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(smem_u32(&bar.s_full), 1);
         mbar_init(smem_u32(&bar.dp_full), 1);
-        mbar_init(smem_u32(&bar.s_free), 8);
-        mbar_init(smem_u32(&bar.dp_free), 8);
+        mbar_init(smem_u32(&bar.s_free), kMathWarps);
+        mbar_init(smem_u32(&bar.dp_free), kMathWarps);
         mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 256);
+    if (warp == kFront) tmem_alloc(smem_u32(&tmem_slot), 256);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -858,10 +835,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return w;
     };
 
-    if (warp >= 8) set_regs_down<kRegsControl>();
-    if (warp >= 10) {
-        // idle: completes the control warps' group of four
-    } else if (warp == 9) {
+    if (warp >= kBack) {
+        // nothing to do here
+    } else if (warp == kLoads) {
         if (lane == 0) {
             int n = 0;
             Cursor c;
@@ -884,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < x.stages; ++s) drain(&bar.empty[s], uses_of(n, s, x.stages), x.err);
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == kFront) {
         {
             int n = 0;
             Cursor c;
@@ -919,28 +895,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        set_regs_up<kRegsMath>();
-        const int half = warp >> 2, wt = tid & 127;
+        const int strip = warp >> 2, c0 = kStrip * strip, wt = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
         int n = 0, lut_head = -1, luts = 0;
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
             if (w.h != lut_head) {
-                load_offsets(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
+                load_offsets<kMath>(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
                 lut_head = w.h;
             }
             if (kBias == 2) {   // the previous item's are read: every warp has passed its fold
                 if (tid < kRows) key_off[tid] = (uint16_t)off_key(p.bias, min(w.j0 + tid, p.m - 1));
                 math_barrier();
             }
-            const int i = w.q0 + wt, j0 = w.j0 + 64 * half;
+            const int i = w.q0 + wt, j0 = w.j0 + c0;
             const bool in = i < p.n;
             const int oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, p.bias.start);
             const int oq_lo = off_query(p.bias, i - lane, p.bias.start);
-            float acc[64];
+            float acc[kStrip];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) acc[c] = 0.f;
+            for (int c = 0; c < kStrip; ++c) acc[c] = 0.f;
             // lse and delta of the row, one batch entry ahead
             auto scalars = [&](int b, float &nl, float &delta) __attribute__((always_inline)) {
                 const size_t row = ((size_t)b * p.heads + w.h) * p.n + i;
@@ -954,51 +929,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 scalars(b + 1, nl_next, delta_next);
                 const int len = keys_of(p, b);
                 if (w.j0 >= len) continue;
-                const int keys = min(64, len - j0);
-                const bool any = keys > 0;
-                float s[64];
+                const int keys = min(kStrip, len - j0);
+                float s[kStrip], dp[kStrip];
                 wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip(tS + 64 * half + lanes, s);
+                load_strip(tS + c0 + lanes, s);
                 tc_fence_before();
                 arrive_warp(&bar.s_free, lane);
-                if (any) row_weights<kBias>(s, p.bias, lut, key_off - w.j0, j0, keys, oq, oq_lo, scale2, nl);
+                row_weights<kBias>(s, p.bias, lut, key_off - w.j0, j0, keys, oq, oq_lo, scale2, nl);
                 wait_on(smem_u32(&bar.dp_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    float dp[32];
-                    tmem_ld32_nowait(tD + 64 * half + c + lanes, dp);
-                    tc_wait_ld();
-                    if (any) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            add2(dp[e], dp[e + 1], dp[e], dp[e + 1], -delta, -delta);
-                            if (c + e >= keys) dp[e] = 0.f;
-                            if (c + e + 1 >= keys) dp[e + 1] = 0.f;
-                            fma2(acc[c + e], acc[c + e + 1], s[c + e], s[c + e + 1], dp[e], dp[e + 1], acc[c + e],
-                                 acc[c + e + 1]);
-                        }
-                    }
-                }
+                load_strip(tD + c0 + lanes, dp);
                 tc_fence_before();
                 arrive_warp(&bar.dp_free, lane);
+#pragma unroll
+                for (int e = 0; e < kStrip; e += 2) {
+                    add2(dp[e], dp[e + 1], dp[e], dp[e + 1], -delta, -delta);
+                    if (e >= keys) dp[e] = 0.f;
+                    if (e + 1 >= keys) dp[e + 1] = 0.f;
+                    fma2(acc[e], acc[e + 1], s[e], s[e + 1], dp[e], dp[e + 1], acc[e], acc[e + 1]);
+                }
                 ++n;
             }
-            float4 *mine = reinterpret_cast<float4 *>(tile + wt * kFoldPitch + 64 * half);
+            float4 *mine = reinterpret_cast<float4 *>(tile + wt * kFoldPitch + c0);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) mine[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+            for (int c = 0; c < kStrip; c += 4) mine[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
             math_barrier();
             if (p.folded) {
                 const TileGeom g = fold_geom(p.fold, w.q0 / kFoldTile, w.j0 / kFoldTile);
                 float *out = fold_block(p.fold, w.split, w.h, w.q0 / kFoldTile, w.j0 / kFoldTile);
                 const bool direct = fold_direct(p.fold, g);
-                fold_offsets(p.fold, g, tile, direct ? out : sums, direct ? p.fold.K : g.dc_n, tid, 256);
+                fold_offsets(p.fold, g, tile, direct ? out : sums, direct ? p.fold.K : g.dc_n, tid, kMath);
                 math_barrier();
-                if (!direct) fold_buckets(p.fold, g, sums, out, tid, 256);
+                if (!direct) fold_buckets(p.fold, g, sums, out, tid, kMath);
             } else {
                 float *out = p.dbias + ((size_t)w.split * p.heads + w.h) * ((size_t)p.n * p.m) + (size_t)w.q0 * p.m + w.j0;
-                for (int r = warp; r < min(kRows, p.n - w.q0); r += 8)
+                for (int r = warp; r < min(kRows, p.n - w.q0); r += kMathWarps)
                     for (int c = lane; c < min(kRows, p.m - w.j0); c += 32)
                         out[(size_t)r * p.m + c] = tile[r * kFoldPitch + c];
                 math_barrier();
@@ -1008,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 256);
+    if (warp == kFront) tmem_dealloc(tmem, 256);
 }
 
 struct Maps {
