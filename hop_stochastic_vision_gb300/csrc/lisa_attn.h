@@ -55,7 +55,7 @@ struct BiasDev {
     int start;         // sequence: column start
     const int *starts; // sequence: per batch entry
     int lo_r, lo_c, hi_c;
-    int ncol_off;      // grid: column offsets (entries of a row behind it are padding)
+    int run_q, run_k;  // grid: four queries, keys from a multiple of four have consecutive offsets
     int col_buckets;
     AxisDev rows, cols;
 };

@@ -23,6 +23,9 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Offsets of a head in memory: four zeros behind the last, then up to 256 bytes.
+int offsets_pitch(int entries) { return (entries + 4 + 63) / 64 * 64; }
+
 lisa_status axis_dev(const lisa_axis_rule &r, AxisDev &a) {
     a = AxisDev{};
     if (r.rule == LISA_BUCKETS_EXACT) {
@@ -91,7 +94,7 @@ lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev) {
         dev.lo_c = (int)lo;
         dev.hi_c = (int)hi;
         dev.entries = (int)(hi - lo + 1);
-        dev.offsets_pitch = (dev.entries + 63) / 64 * 64;
+        dev.offsets_pitch = offsets_pitch(dev.entries);
         return LISA_OK;
     }
     if (b->starts) return LISA_ERR_INVALID_ARG;
@@ -103,12 +106,13 @@ lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev) {
     dev.div_P = fast_div((int)P);
     dev.div_q = fast_div(b->q_cols);
     dev.div_k = fast_div(b->k_cols);
-    dev.ncol_off = (int)nc;
+    dev.run_q = b->q_cols % 4 == 0;
+    dev.run_k = b->k_cols % 4 == 0 && b->key_step_cols == 1;
     dev.lo_r = -(b->q_rows - 1) - b->start_rows;
     dev.lo_c = -(b->q_cols - 1) - b->start_cols;
     dev.c0 = (b->q_rows - 1) * dev.P + b->q_cols - 1;
     dev.entries = (int)(nr * P);
-    dev.offsets_pitch = (dev.entries + 63) / 64 * 64;
+    dev.offsets_pitch = offsets_pitch(dev.entries);
     return LISA_OK;
 }
 

@@ -101,15 +101,7 @@ __device__ __forceinline__ void add_bias(float (&s)[N], const BiasDev &b, const 
     } else if (kBias == 2) {
         // inside the table by construction (key_off repeats the last key behind the end)
         mul = 1.f;
-        const float *l = lut - r.oq;
-#pragma unroll
-        for (int c = 0; c < N; c += 4) {
-            const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
-            s[c] = fmaf(s[c], scale2, l[a.x & 0xFFFFu]);
-            s[c + 1] = fmaf(s[c + 1], scale2, l[a.x >> 16]);
-            s[c + 2] = fmaf(s[c + 2], scale2, l[a.y & 0xFFFFu]);
-            s[c + 3] = fmaf(s[c + 3], scale2, l[a.y >> 16]);
-        }
+        grid_bias(s, b, lut - r.oq, key_off, j0, scale2);
     }
 }
 
@@ -493,7 +485,7 @@ cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {
     x.div_qtiles = fast_div(x.qtiles);
     x.div_B = fast_div(p.B);
     x.div_group = fast_div(p.group);
-    const int lut = p.bias.mode ? round1k(p.bias.entries * 4) : 0;
+    const int lut = offsets_smem(p.bias);
     const int keys = p.bias.mode == 2 ? round1k((p.m + 127) / 128 * 256) : 0;
     const int out = 8 * 4096;   // a staging block for each softmax warp
     const int fixed = 2 * kTileBytes + out + lut + keys + 1024;

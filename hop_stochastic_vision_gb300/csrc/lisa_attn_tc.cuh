@@ -188,12 +188,39 @@ __device__ __forceinline__ void load_offsets(const BiasDev &b, int head, float *
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");   // every warp is past its reads of the old table
     if (tid == 0) {
         fence_proxy_async();
-        const uint32_t bytes = (uint32_t)(b.entries + 3) / 4 * 16;
+        const uint32_t bytes = (uint32_t)(b.entries + 4 + 3) / 4 * 16;
         mbar_arrive_expect_tx(smem_u32(bar), bytes);
         bulk_load(smem_u32(lut), b.offsets + (size_t)head * b.offsets_pitch, bytes, smem_u32(bar));
     }
     wait_on(smem_u32(bar), count & 1, g, kErrTimeoutLoad);
     ++count;
+}
+
+// s[c] = scale2 s[c] + bias of N keys from `j0` (grids): key_off holds each key's
+// offset, `l` points at the row's own.  Where a grid's rows are multiples of four
+// keys wide, one offset serves four neighbouring values.
+template <int N>
+__device__ __forceinline__ void grid_bias(float (&s)[N], const BiasDev &b, const float *l, const uint16_t *key_off, int j0,
+                                          float scale2) {
+    if (b.run_k) {
+#pragma unroll
+        for (int c = 0; c < N; c += 4) {
+            const float *v = l + key_off[j0 + c];
+            s[c] = fmaf(s[c], scale2, v[0]);
+            s[c + 1] = fmaf(s[c + 1], scale2, v[1]);
+            s[c + 2] = fmaf(s[c + 2], scale2, v[2]);
+            s[c + 3] = fmaf(s[c + 3], scale2, v[3]);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; c += 4) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
+            s[c] = fmaf(s[c], scale2, l[a.x & 0xFFFFu]);
+            s[c + 1] = fmaf(s[c + 1], scale2, l[a.x >> 16]);
+            s[c + 2] = fmaf(s[c + 2], scale2, l[a.y & 0xFFFFu]);
+            s[c + 3] = fmaf(s[c + 3], scale2, l[a.y >> 16]);
+        }
+    }
 }
 
 // One token box {64, 128} of a head's slice; coordinates of repeated dimensions stay 0.
@@ -272,6 +299,9 @@ inline int sms() {
 }
 
 constexpr int kSmemBudget = 227 * 1024 - 2048;   // dynamic: behind the barriers
+
+// Shared memory of a head's offsets.
+inline int offsets_smem(const BiasDev &b) { return b.mode ? (b.entries * 4 + 32 + 1023) / 1024 * 1024 : 0; }
 
 inline int round1k(int x) { return (x + 1023) / 1024 * 1024; }
 

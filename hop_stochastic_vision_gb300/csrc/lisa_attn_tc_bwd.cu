@@ -3,9 +3,9 @@
 // Three kernels of one shape, each a persistent CTA of 12 warps around 128 x 128
 // tiles of pairs whose scores and dP = dO V^T are products into tensor memory:
 //   dQ     128 queries against every key; dS goes back to tensor memory as bf16
-//          for dQ += dS K.  Also leaves delta_i = sum_j p dP in fp32, which the
-//          two others use (the dQ kernel itself takes dO . O from the rounded
-//          output, whose error is one rounding of O against a bf16 result)
+//          for dQ += dS K.  Also leaves delta_i for the two others: dO . O from
+//          the rounded output (an error of one rounding of O against bf16
+//          results), or with a bias sum_j p dP in fp32, since its gradient is fp32
 //   dK dV  128 keys against the queries of the heads that share them, the
 //          tile transposed (rows are keys): dV += P^T dO, dK += dS^T Q, the
 //          queries split over CTAs when there are few key tiles, the parts added
@@ -18,8 +18,10 @@
 //
 // Four warpgroups share a tile by columns, 32 each, a thread per row (with two of
 // 64 columns the schedulers had two warps each and issued one cycle in five).
-// The threads take S and dP into registers as soon as they are there, so the
-// next tile's products run under this tile's arithmetic.
+// The threads take S and dP into registers as soon as both are there, so the
+// next tile's products run under this tile's arithmetic.  Two barriers to wait for
+// and two to arrive at per tile: a wait costs some 100 cycles even when its phase
+// is long complete, and all warps pay it together.
 #include "lisa_attn_tc.cuh"
 #include "lisa_fold.cuh"
 
@@ -86,15 +88,9 @@ __device__ __forceinline__ void row_weights(float (&s)[kStrip], const BiasDev &b
             }
         }
     } else {
-        const float *l = lut - oq;   // inside the table by construction
+        grid_bias(s, b, lut - oq, key_off, j0, scale2);   // inside the table by construction
 #pragma unroll
-        for (int c = 0; c < kStrip; c += 4) {
-            const uint2 a = *reinterpret_cast<const uint2 *>(key_off + j0 + c);
-            s[c] = fmaf(s[c], scale2, l[a.x & 0xFFFFu]) + nl;
-            s[c + 1] = fmaf(s[c + 1], scale2, l[a.x >> 16]) + nl;
-            s[c + 2] = fmaf(s[c + 2], scale2, l[a.y & 0xFFFFu]) + nl;
-            s[c + 3] = fmaf(s[c + 3], scale2, l[a.y >> 16]) + nl;
-        }
+        for (int c = 0; c < kStrip; c += 2) add2(s[c], s[c + 1], s[c], s[c + 1], nl, nl);
     }
     if (keys < kStrip) {
 #pragma unroll
@@ -109,6 +105,11 @@ __device__ __forceinline__ void row_weights(float (&s)[kStrip], const BiasDev &b
 // there before and are not used (a load under a condition costs copies of all).
 __device__ __forceinline__ void load_strip(uint32_t taddr, float (&v)[kStrip]) {
     tmem_ld32_nowait(taddr, v);
+    tc_wait_ld();
+}
+__device__ __forceinline__ void load_strips(uint32_t ta, float (&a)[kStrip], uint32_t tb, float (&b)[kStrip]) {
+    tmem_ld32_nowait(ta, a);
+    tmem_ld32_nowait(tb, b);
     tc_wait_ld();
 }
 
@@ -130,8 +131,8 @@ __device__ __forceinline__ int uses_of(int total, int slot, int stages) {
 
 // ------------------------------------------------------------------------ dQ
 struct DqBars {
-    uint64_t q_full[2], q_empty[2], k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages], v_empty[kMaxStages];
-    uint64_t s_full, s_free, dp_full, dp_free, ds_full, dq_done, lut_full;
+    uint64_t q_full[2], q_empty[2], kv_full[kMaxStages], kv_empty[kMaxStages];
+    uint64_t full, free, ds_full, dq_done, lut_full;   // S and dP of a tile: there, in registers
 };
 
 template <int kBias>
@@ -159,16 +160,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bar.q_empty[t]), 1);
         }
         for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(smem_u32(&bar.k_full[s]), 1);
-            mbar_init(smem_u32(&bar.v_full[s]), 1);
-            mbar_init(smem_u32(&bar.k_empty[s]), 1);
-            mbar_init(smem_u32(&bar.v_empty[s]), 1);
+            mbar_init(smem_u32(&bar.kv_full[s]), 1);
+            mbar_init(smem_u32(&bar.kv_empty[s]), 1);
         }
-        mbar_init(smem_u32(&bar.s_full), 1);
-        mbar_init(smem_u32(&bar.dp_full), 1);
+        mbar_init(smem_u32(&bar.full), 1);
         mbar_init(smem_u32(&bar.dq_done), 1);
-        mbar_init(smem_u32(&bar.s_free), kMathWarps);
-        mbar_init(smem_u32(&bar.dp_free), kMathWarps);
+        mbar_init(smem_u32(&bar.free), kMathWarps);
         mbar_init(smem_u32(&bar.ds_full), kMathWarps);
         mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
@@ -216,21 +213,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_rows(qd + (2 * qs + 1) * kTileBytes, &md, x.ud, w.q0, w.h, w.b, f);
                 ++nq;
                 for (int j = 0; j < w.tiles; ++j, ++kt, c.next(x.stages)) {
-                    const int s = c.slot;
-                    const uint32_t ph = c.phase;
-                    const uint32_t kf = smem_u32(&bar.k_full[s]), vf = smem_u32(&bar.v_full[s]);
-                    if (kt >= x.stages) wait_on(smem_u32(&bar.k_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
-                    mbar_arrive_expect_tx(kf, kTileBytes);
-                    load_rows(ring + 2 * s * kTileBytes, &mk, x.uk, j * kRows, g, w.b, kf);
-                    if (kt >= x.stages) wait_on(smem_u32(&bar.v_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
-                    mbar_arrive_expect_tx(vf, kTileBytes);
-                    load_rows(ring + (2 * s + 1) * kTileBytes, &mv, x.uv, j * kRows, g, w.b, vf);
+                    const uint32_t f = smem_u32(&bar.kv_full[c.slot]), at = ring + 2 * c.slot * kTileBytes;
+                    if (kt >= x.stages) wait_on(smem_u32(&bar.kv_empty[c.slot]), c.phase ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(f, 2 * kTileBytes);
+                    load_rows(at, &mk, x.uk, j * kRows, g, w.b, f);
+                    load_rows(at + kTileBytes, &mv, x.uv, j * kRows, g, w.b, f);
                 }
             }
-            for (int s = 0; s < x.stages; ++s) {
-                drain(&bar.k_empty[s], uses_of(kt, s, x.stages), x.err);
-                drain(&bar.v_empty[s], uses_of(kt, s, x.stages), x.err);
-            }
+            for (int s = 0; s < x.stages; ++s) drain(&bar.kv_empty[s], uses_of(kt, s, x.stages), x.err);
             for (int t = 0; t < x.q_slots; ++t) drain(&bar.q_empty[t], uses_of(nq, t, x.q_slots), x.err);
         }
         __syncwarp();
@@ -248,28 +238,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t qa = q0 + (uint32_t)qs * kPair, da = qa + kTileBytes / 16;
             for (int j = 0; j < w.tiles; ++j, ++kt, c.next(x.stages)) {
                 const int s = c.slot, cols = tile_cols(tile_keys(w.len, j));
-                wait_on(smem_u32(&bar.k_full[s]), c.phase, guard, kErrTimeoutLoad);
-                if (kt > 0) wait_on(smem_u32(&bar.s_free), (kt - 1) & 1, guard, kErrTimeoutMma);
+                wait_on(smem_u32(&bar.kv_full[s]), c.phase, guard, kErrTimeoutLoad);
+                if (kt > 0) wait_on(smem_u32(&bar.free), (kt - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 if (elect_one()) {
                     mma_rows_rows(tS, qa, k0 + (uint32_t)s * kPair, cols);
-                    tc_commit(smem_u32(&bar.s_full));
-                }
-                __syncwarp();
-                wait_on(smem_u32(&bar.v_full[s]), c.phase, guard, kErrTimeoutLoad);
-                if (kt > 0) wait_on(smem_u32(&bar.dp_free), (kt - 1) & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                if (elect_one()) {
                     mma_rows_rows(tP, da, v0 + (uint32_t)s * kPair, cols);
-                    tc_commit(smem_u32(&bar.dp_full));
-                    tc_commit(smem_u32(&bar.v_empty[s]));
+                    tc_commit(smem_u32(&bar.full));
                     if (j == w.tiles - 1) tc_commit(smem_u32(&bar.q_empty[qs]));
                 }
                 __syncwarp();
             }
         }
     } else if (warp == kBack) {
-        // dQ += dS K.  S has read the K tile too: dS comes of it.
+        // dQ += dS K.  S and dP have read the K and V tiles: dS comes of them.
         int kt = 0;
         Cursor c;
         const uint64_t kt0 = desc_tokens(ring);
@@ -281,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
                     mma_weights_rows(tDq, tDs, kt0 + (uint32_t)c.slot * kPair, tile_cols(tile_keys(w.len, j)), j > 0);
                     tc_commit(smem_u32(&bar.dq_done));
-                    tc_commit(smem_u32(&bar.k_empty[c.slot]));
+                    tc_commit(smem_u32(&bar.kv_empty[c.slot]));
                 }
                 __syncwarp();
             }
@@ -344,39 +326,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int j = 0; j < w.tiles; ++j, ++kt) {
                 const int keys = tile_keys(w.len, j), cols = tile_cols(keys), j0 = j * kRows + c0;
-                float s[kStrip];
-                wait_on(smem_u32(&bar.s_full), kt & 1, guard, kErrTimeoutMma);
+                float s[kStrip], dp[kStrip];
+                wait_on(smem_u32(&bar.full), kt & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip(tS + c0 + lanes, s);
+                load_strips(tS + c0 + lanes, s, tP + c0 + lanes, dp);
                 tc_fence_before();
-                arrive_warp(&bar.s_free, lane);
+                arrive_warp(&bar.free, lane);
                 row_weights<kBias>(s, p.bias, lut, key_off, j0, keys - c0, oq, oq_lo, scale2, nl);
-                float dp[kStrip];
-                wait_on(smem_u32(&bar.dp_full), kt & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                load_strip(tP + c0 + lanes, dp);
-                tc_fence_before();
-                arrive_warp(&bar.dp_free, lane);
-                // the previous dS has been read
-                if (kt > 0) wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
-                float e0 = 0.f, e1 = 0.f;
-                uint32_t ds[kStrip / 2];
                 if (keys - c0 < kStrip) {   // dP of keys behind the last one holds whatever their values hold
 #pragma unroll
                     for (int e = 0; e < kStrip; ++e)
                         if (e >= keys - c0) dp[e] = 0.f;
                 }
+                uint32_t ds[kStrip / 2];
+                if (kBias) {   // the bias gradient wants delta from the unrounded weights
+                    float e0 = 0.f, e1 = 0.f;
 #pragma unroll
-                for (int e = 0; e < kStrip; e += 2) {
-                    float u, v;
-                    mul2(dp[e], dp[e + 1], s[e], s[e + 1], dp[e], dp[e + 1]);
-                    add2(e0, e1, e0, e1, dp[e], dp[e + 1]);
-                    fma2(u, v, s[e], s[e + 1], -delta, -delta, dp[e], dp[e + 1]);
-                    ds[e >> 1] = pack_bf16(u, v);
+                    for (int e = 0; e < kStrip; e += 2) {
+                        float u, v;
+                        mul2(dp[e], dp[e + 1], s[e], s[e + 1], dp[e], dp[e + 1]);
+                        add2(e0, e1, e0, e1, dp[e], dp[e + 1]);
+                        fma2(u, v, s[e], s[e + 1], -delta, -delta, dp[e], dp[e + 1]);
+                        ds[e >> 1] = pack_bf16(u, v);
+                    }
+                    exact += e0 + e1;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kStrip; e += 2) {
+                        add2(dp[e], dp[e + 1], dp[e], dp[e + 1], -delta, -delta);
+                        mul2(dp[e], dp[e + 1], dp[e], dp[e + 1], s[e], s[e + 1]);
+                        ds[e >> 1] = pack_bf16(dp[e], dp[e + 1]);
+                    }
                 }
+                // the previous dS has been read
+                if (kt > 0) wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 tmem_st16(tDs + c0 / 2 + lanes, ds);
-                exact += e0 + e1;
                 if (strip == 0 && keys < cols && w.len < p.m) {
                     // S is done with the tile: what stands behind the last key may not meet dS = 0
                     zero_rows(ring + 2 * (kt % x.stages) * kTileBytes, keys, cols, wt);
@@ -386,10 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 arrive_warp(&bar.ds_full, lane);
             }
-            // the strips' shares of delta
-            if (strip > 0) other[strip - 1][wt] = exact;
-            math_barrier();
-            if (strip == 0 && in) p.delta[row] = (exact + other[0][wt]) + (other[1][wt] + other[2][wt]);
+            if (kBias) {   // the strips' shares of delta
+                if (strip > 0) other[strip - 1][wt] = exact;
+                math_barrier();
+                if (strip == 0 && in) p.delta[row] = (exact + other[0][wt]) + (other[1][wt] + other[2][wt]);
+            } else if (strip == 0 && in) {
+                p.delta[row] = delta;
+            }
             float o[16];
             if (w.tiles > 0) {
                 wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
@@ -418,9 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // --------------------------------------------------------------------- dK, dV
 struct DkvBars {
-    uint64_t kv_full, kv_empty, q_full[kMaxStages], d_full[kMaxStages], q_empty[kMaxStages];
+    uint64_t kv_full, kv_empty, q_full[kMaxStages], q_empty[kMaxStages];
     uint64_t aux_full[kMaxStages], aux_empty[kMaxStages];
-    uint64_t s_full, s_free, dp_full, dp_free, p_full, ds_full, dv_done, dk_done, lut_full;
+    uint64_t full, free, w_full, w_done, lut_full;   // S and dP: there, in registers; P and dS: there, read
 };
 
 // What the arithmetic needs of a tile's queries, one entry per column.
@@ -452,19 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&bar.kv_empty), 1);
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(smem_u32(&bar.q_full[s]), 1);
-            mbar_init(smem_u32(&bar.d_full[s]), 1);
             mbar_init(smem_u32(&bar.q_empty[s]), 1);
             mbar_init(smem_u32(&bar.aux_full[s]), 1);
             mbar_init(smem_u32(&bar.aux_empty[s]), kMathWarps);
         }
-        mbar_init(smem_u32(&bar.s_full), 1);
-        mbar_init(smem_u32(&bar.dp_full), 1);
-        mbar_init(smem_u32(&bar.dv_done), 1);
-        mbar_init(smem_u32(&bar.dk_done), 1);
-        mbar_init(smem_u32(&bar.s_free), kMathWarps);
-        mbar_init(smem_u32(&bar.dp_free), kMathWarps);
-        mbar_init(smem_u32(&bar.p_full), kMathWarps);
-        mbar_init(smem_u32(&bar.ds_full), kMathWarps);
+        mbar_init(smem_u32(&bar.full), 1);
+        mbar_init(smem_u32(&bar.w_done), 1);
+        mbar_init(smem_u32(&bar.free), kMathWarps);
+        mbar_init(smem_u32(&bar.w_full), kMathWarps);
         mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
         fence_mbar_init();
@@ -515,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool in = i < p.n;
                     aux[s].nl[e] = neg_lse2(p.lse, row0 + i, in);
                     aux[s].minus_delta[e] = in ? -p.delta[row0 + i] : 0.f;
-                    if (kBias) aux[s].oq[e] = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start);
+                    // behind the last query: an offset whose three neighbours below are in the table too
+                    if (kBias) aux[s].oq[e] = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start) - (kBias == 2 && !in ? 3 : 0);
                 }
                 arrive_warp(&bar.aux_full[s], lane);
             }
@@ -538,12 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t ph = c.phase;
                     int qt = u;
                     const int h = w.g * p.group + split(qt, x.div_qtiles), q0 = qt * kRows;
-                    const uint32_t qf = smem_u32(&bar.q_full[s]), df = smem_u32(&bar.d_full[s]);
+                    const uint32_t f = smem_u32(&bar.q_full[s]), at = ring + 2 * s * kTileBytes;
                     if (n >= x.stages) wait_on(smem_u32(&bar.q_empty[s]), ph ^ 1u, guard, kErrTimeoutMma);
-                    mbar_arrive_expect_tx(qf, kTileBytes);
-                    load_rows(ring + 2 * s * kTileBytes, &mq, x.uq, q0, h, w.b, qf);
-                    mbar_arrive_expect_tx(df, kTileBytes);
-                    load_rows(ring + (2 * s + 1) * kTileBytes, &md, x.ud, q0, h, w.b, df);
+                    mbar_arrive_expect_tx(f, 2 * kTileBytes);
+                    load_rows(at, &mq, x.uq, q0, h, w.b, f);
+                    load_rows(at + kTileBytes, &md, x.ud, q0, h, w.b, f);
                 }
             }
             for (int s = 0; s < x.stages; ++s) {
@@ -569,19 +552,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s = c.slot, cols = qt == x.qtiles - 1 ? tail : kRows;
                 qt = qt == x.qtiles - 1 ? 0 : qt + 1;
                 wait_on(smem_u32(&bar.q_full[s]), c.phase, guard, kErrTimeoutLoad);
-                if (n > 0) wait_on(smem_u32(&bar.s_free), (n - 1) & 1, guard, kErrTimeoutMma);
+                if (n > 0) wait_on(smem_u32(&bar.free), (n - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 if (elect_one()) {
                     mma_rows_rows(tS, k0, q0 + (uint32_t)s * kPair, cols);
-                    tc_commit(smem_u32(&bar.s_full));
-                }
-                __syncwarp();
-                wait_on(smem_u32(&bar.d_full[s]), c.phase, guard, kErrTimeoutLoad);
-                if (n > 0) wait_on(smem_u32(&bar.dp_free), (n - 1) & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                if (elect_one()) {
                     mma_rows_rows(tD, v0, d0 + (uint32_t)s * kPair, cols);
-                    tc_commit(smem_u32(&bar.dp_full));
+                    tc_commit(smem_u32(&bar.full));
                     if (u == w.u1 - 1) tc_commit(smem_u32(&bar.kv_empty));
                 }
                 __syncwarp();
@@ -599,18 +575,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
                 const int s = c.slot, cols = qt == x.qtiles - 1 ? tail : kRows;
                 qt = qt == x.qtiles - 1 ? 0 : qt + 1;
-                wait_on(smem_u32(&bar.p_full), n & 1, guard, kErrTimeoutMma);
+                wait_on(smem_u32(&bar.w_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 if (elect_one()) {
                     mma_weights_rows(tDv, tPw, dt0 + (uint32_t)s * kPair, cols, u > w.u0);
-                    tc_commit(smem_u32(&bar.dv_done));
-                }
-                __syncwarp();
-                wait_on(smem_u32(&bar.ds_full), n & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                if (elect_one()) {
                     mma_weights_rows(tDk, tDs, qt0 + (uint32_t)s * kPair, cols, u > w.u0);
-                    tc_commit(smem_u32(&bar.dk_done));
+                    tc_commit(smem_u32(&bar.w_done));
                     tc_commit(smem_u32(&bar.q_empty[s]));
                 }
                 __syncwarp();
@@ -635,13 +605,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int cols = tile_cols(min(kRows, p.n - qt * kRows));
                 const QueryAux &a = aux[ca.slot];
-                float s[kStrip];
+                float s[kStrip], dp[kStrip];
                 wait_on(smem_u32(&bar.aux_full[ca.slot]), ca.phase, guard, kErrTimeoutLoad);
-                wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
+                wait_on(smem_u32(&bar.full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip(tS + c0 + lanes, s);
+                load_strips(tS + c0 + lanes, s, tD + c0 + lanes, dp);
                 tc_fence_before();
-                arrive_warp(&bar.s_free, lane);
+                arrive_warp(&bar.free, lane);
                 if (kBias == 1) {
                     const int last = p.bias.entries - 1;
                     const int off = ok - a.oq[c0];   // column c: off - c
@@ -670,12 +640,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float *l4 = lut + ok;   // inside the table by construction
 #pragma unroll
                     for (int c = 0; c < kStrip; c += 4) {
-                        const int4 o = *reinterpret_cast<const int4 *>(a.oq + c0 + c);
                         const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
-                        s[c] = fmaf(s[c], scale2, l4[-o.x]) + l.x;
-                        s[c + 1] = fmaf(s[c + 1], scale2, l4[-o.y]) + l.y;
-                        s[c + 2] = fmaf(s[c + 2], scale2, l4[-o.z]) + l.z;
-                        s[c + 3] = fmaf(s[c + 3], scale2, l4[-o.w]) + l.w;
+                        float v[4];
+                        if (p.bias.run_q) {   // four queries of one row: consecutive offsets, downwards
+                            const float *at = l4 - a.oq[c0 + c];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) v[u] = at[-u];
+                        } else {
+                            const int4 o = *reinterpret_cast<const int4 *>(a.oq + c0 + c);
+                            v[0] = l4[-o.x];
+                            v[1] = l4[-o.y];
+                            v[2] = l4[-o.z];
+                            v[3] = l4[-o.w];
+                        }
+                        fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, v[0], v[1]);
+                        fma2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], scale2, scale2, v[2], v[3]);
+                        add2(s[c], s[c + 1], s[c], s[c + 1], l.x, l.y);
+                        add2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], l.z, l.w);
                     }
                 } else {
 #pragma unroll
@@ -685,49 +666,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fma2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], scale2, scale2, l.z, l.w);
                     }
                 }
-                // the previous P has been read
-                if (n > 0) wait_on(smem_u32(&bar.dv_done), (n - 1) & 1, guard, kErrTimeoutMma);
-                uint32_t out[kStrip / 2];
-#pragma unroll
-                for (int e = 0; e < kStrip; e += 2) {
-                    s[e] = ex2_approx(s[e]);
-                    s[e + 1] = ex2_approx(s[e + 1]);
-                    out[e >> 1] = pack_bf16(s[e], s[e + 1]);
-                }
-                tc_fence_after();
-                tmem_st16(tPw + c0 / 2 + lanes, out);
-                tc_wait_st();
-                tc_fence_before();
-                arrive_warp(&bar.p_full, lane);
-                float dp[kStrip];
-                wait_on(smem_u32(&bar.dp_full), n & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                load_strip(tD + c0 + lanes, dp);
-                tc_fence_before();
-                arrive_warp(&bar.dp_free, lane);
+                uint32_t pw[kStrip / 2], ds[kStrip / 2];
 #pragma unroll
                 for (int e = 0; e < kStrip; e += 4) {
                     const float4 d = *reinterpret_cast<const float4 *>(a.minus_delta + c0 + e);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) s[e + u] = ex2_approx(s[e + u]);
+                    pw[e >> 1] = pack_bf16(s[e], s[e + 1]);
+                    pw[(e >> 1) + 1] = pack_bf16(s[e + 2], s[e + 3]);
                     add2(dp[e], dp[e + 1], dp[e], dp[e + 1], d.x, d.y);
                     add2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], d.z, d.w);
                     mul2(dp[e], dp[e + 1], dp[e], dp[e + 1], s[e], s[e + 1]);
                     mul2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], s[e + 2], s[e + 3]);
-                    out[e >> 1] = pack_bf16(dp[e], dp[e + 1]);
-                    out[(e >> 1) + 1] = pack_bf16(dp[e + 2], dp[e + 3]);
+                    ds[e >> 1] = pack_bf16(dp[e], dp[e + 1]);
+                    ds[(e >> 1) + 1] = pack_bf16(dp[e + 2], dp[e + 3]);
                 }
-                arrive_warp(&bar.aux_empty[ca.slot], lane);
-                if (n > 0) wait_on(smem_u32(&bar.dk_done), (n - 1) & 1, guard, kErrTimeoutMma);
+                // the previous P and dS have been read
+                if (n > 0) wait_on(smem_u32(&bar.w_done), (n - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                tmem_st16(tDs + c0 / 2 + lanes, out);
+                tmem_st16(tPw + c0 / 2 + lanes, pw);
+                tmem_st16(tDs + c0 / 2 + lanes, ds);
                 tc_wait_st();
                 tc_fence_before();
-                arrive_warp(&bar.ds_full, lane);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bar.aux_empty[ca.slot]));
+                    mbar_arrive(smem_u32(&bar.w_full));
+                }
             }
             // ---- strips 0, 1 store dV, 2 and 3 dK, 32 columns each; rows behind the last key are 0
             float o[kStrip];
             const int dk = strip >> 1, oc = kStrip * (strip & 1);
             const bool some = w.u0 < w.u1 && j < w.len;
-            if (w.u0 < w.u1) wait_on(smem_u32(dk ? &bar.dk_done : &bar.dv_done), (n - 1) & 1, guard, kErrTimeoutMma);
+            if (w.u0 < w.u1) wait_on(smem_u32(&bar.w_done), (n - 1) & 1, guard, kErrTimeoutMma);
             tc_fence_after();
             load_strip((dk ? tDk : tDv) + oc + lanes, o);
             tc_fence_before();
@@ -776,7 +747,7 @@ __global__ void __launch_bounds__(256) join_dkdv(const __grid_constant__ Problem
 // --------------------------------------------------------------------- dbias
 struct DbBars {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t s_full, s_free, dp_full, dp_free, lut_full;
+    uint64_t s_full, s_free, lut_full;   // S and dP: there, in registers
 };
 
 template <int kBias>
@@ -803,9 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bar.empty[s]), 1);
         }
         mbar_init(smem_u32(&bar.s_full), 1);
-        mbar_init(smem_u32(&bar.dp_full), 1);
         mbar_init(smem_u32(&bar.s_free), kMathWarps);
-        mbar_init(smem_u32(&bar.dp_free), kMathWarps);
         mbar_init(smem_u32(&bar.lut_full), 1);
         dead = 0;
         fence_mbar_init();
@@ -877,14 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     if (elect_one()) {
                         mma_rows_rows(tS, at, at + 2 * kTileBytes / 16, cols);
-                        tc_commit(smem_u32(&bar.s_full));
-                    }
-                    __syncwarp();
-                    if (n > 0) wait_on(smem_u32(&bar.dp_free), (n - 1) & 1, guard, kErrTimeoutMma);
-                    tc_fence_after();
-                    if (elect_one()) {
                         mma_rows_rows(tD, at + kTileBytes / 16, at + 3 * kTileBytes / 16, cols);
-                        tc_commit(smem_u32(&bar.dp_full));
+                        tc_commit(smem_u32(&bar.s_full));
                         tc_commit(smem_u32(&bar.empty[s]));
                     }
                     __syncwarp();
@@ -933,15 +896,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s[kStrip], dp[kStrip];
                 wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strip(tS + c0 + lanes, s);
+                load_strips(tS + c0 + lanes, s, tD + c0 + lanes, dp);
                 tc_fence_before();
                 arrive_warp(&bar.s_free, lane);
                 row_weights<kBias>(s, p.bias, lut, key_off - w.j0, j0, keys, oq, oq_lo, scale2, nl);
-                wait_on(smem_u32(&bar.dp_full), n & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                load_strip(tD + c0 + lanes, dp);
-                tc_fence_before();
-                arrive_warp(&bar.dp_free, lane);
 #pragma unroll
                 for (int e = 0; e < kStrip; e += 2) {
                     add2(dp[e], dp[e + 1], dp[e], dp[e + 1], -delta, -delta);
@@ -1023,7 +981,7 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     BwdParams x{};
     if (!fill_maps(m, x, p)) return cudaErrorInvalidValue;
     x.err = err;
-    const int lut = p.bias.mode ? round1k(p.bias.entries * 4) : 0;
+    const int lut = offsets_smem(p.bias);
     const int keys = p.bias.mode == 2 ? round1k((p.m + 127) / 128 * 256) : 0;
     cudaError_t e;
     // ---- dQ and delta

@@ -70,11 +70,12 @@ __global__ void __launch_bounds__(kDenseThreads) bias_dense(BiasDev b, T *out, i
 __global__ void __launch_bounds__(128) bias_offsets(BiasDev b, float *out) {
     chain_begin();
     const int e = blockIdx.x * 128 + threadIdx.x, h0 = blockIdx.y * 4;
-    if (e >= b.entries) return;
-    const float *row = b.table + (size_t)entry_bucket(b, e) * b.heads;
+    if (e >= b.entries + 4) return;   // four zeros behind the last offset
+    const bool in = e < b.entries;
+    const float *row = b.table + (size_t)(in ? entry_bucket(b, e) : 0) * b.heads;
     float v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = h0 + u < b.heads ? row[h0 + u] : 0.f;
+    for (int u = 0; u < 4; ++u) v[u] = in && h0 + u < b.heads ? row[h0 + u] : 0.f;
 #pragma unroll
     for (int u = 0; u < 4; ++u)
         if (h0 + u < b.heads) out[(size_t)(h0 + u) * b.offsets_pitch + e] = v[u] * 1.4426950408889634f;
@@ -327,11 +328,11 @@ void grad_plan(const lisa_rel_bias &b, GradParams &g) {
 }  // namespace
 
 size_t offsets_bytes(const BiasDev &b) {
-    return (size_t)b.heads * ((b.entries + 63) / 64 * 64) * sizeof(float);
+    return (size_t)b.heads * b.offsets_pitch * sizeof(float);
 }
 
 cudaError_t launch_offsets(const BiasDev &b, float *out, cudaStream_t s) {
-    return launch_chained(bias_offsets, dim3((unsigned)((b.entries + 127) / 128), (unsigned)((b.heads + 3) / 4)), 128, 0, s,
+    return launch_chained(bias_offsets, dim3((unsigned)((b.entries + 4 + 127) / 128), (unsigned)((b.heads + 3) / 4)), 128, 0, s,
                           b, out);
 }
 
