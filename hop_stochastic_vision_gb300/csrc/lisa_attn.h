@@ -49,6 +49,7 @@ struct BiasDev {
     const float *table;
     const float *offsets;   // tensor-core kernels: [heads][offsets_pitch], the table by offset, times log2(e)
     int offsets_pitch;
+    int pad;                // sequence: the outermost values repeated so often at either end
     int heads;
     int q_cols, k_cols, P, step_r, step_c, c0;
     FastDiv div_q, div_k, div_P;   // by q_cols, k_cols, P

@@ -23,8 +23,11 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// A sequence's offsets continue at both ends, so that a tile of 128 keys and 32
+// queries with any offset inside the table needs no clamping.
+constexpr int kOffsetPad = 192;
 // Offsets of a head in memory: four zeros behind the last, then up to 256 bytes.
-int offsets_pitch(int entries) { return (entries + 4 + 63) / 64 * 64; }
+int offsets_pitch(int entries, int pad) { return (entries + 2 * pad + 4 + 63) / 64 * 64; }
 
 lisa_status axis_dev(const lisa_axis_rule &r, AxisDev &a) {
     a = AxisDev{};
@@ -94,7 +97,8 @@ lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev) {
         dev.lo_c = (int)lo;
         dev.hi_c = (int)hi;
         dev.entries = (int)(hi - lo + 1);
-        dev.offsets_pitch = offsets_pitch(dev.entries);
+        dev.pad = kOffsetPad;
+        dev.offsets_pitch = offsets_pitch(dev.entries, dev.pad);
         return LISA_OK;
     }
     if (b->starts) return LISA_ERR_INVALID_ARG;
@@ -112,7 +116,7 @@ lisa_status bias_dev(const lisa_rel_bias *b, int heads, BiasDev &dev) {
     dev.lo_c = -(b->q_cols - 1) - b->start_cols;
     dev.c0 = (b->q_rows - 1) * dev.P + b->q_cols - 1;
     dev.entries = (int)(nr * P);
-    dev.offsets_pitch = offsets_pitch(dev.entries);
+    dev.offsets_pitch = offsets_pitch(dev.entries, 0);
     return LISA_OK;
 }
 

@@ -89,7 +89,7 @@ __device__ __forceinline__ void add_bias(float (&s)[N], const BiasDev &b, const 
         } else {
             const int off = b.step_c * j0 - r.oq;
             mul = 1.f;
-            if (b.step_c == 1 && lo >= 0 && lo + 31 + N - 1 <= last) {
+            if (b.step_c == 1) {   // inside the padded table
                 const float *l = lut + off;
 #pragma unroll
                 for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], scale2, l[c]);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
     const uint32_t q_smem = base, ring = base + 2 * kTileBytes;
-    float *lut = reinterpret_cast<float *>(sm + x.off_lut);
+    float *lut = reinterpret_cast<float *>(sm + x.off_lut) + p.bias.pad;
     uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_keys);
     const Guard guard{x.err, &dead};
 

@@ -188,9 +188,9 @@ __device__ __forceinline__ void load_offsets(const BiasDev &b, int head, float *
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");   // every warp is past its reads of the old table
     if (tid == 0) {
         fence_proxy_async();
-        const uint32_t bytes = (uint32_t)(b.entries + 4 + 3) / 4 * 16;
+        const uint32_t bytes = (uint32_t)(b.entries + 2 * b.pad + 4 + 3) / 4 * 16;
         mbar_arrive_expect_tx(smem_u32(bar), bytes);
-        bulk_load(smem_u32(lut), b.offsets + (size_t)head * b.offsets_pitch, bytes, smem_u32(bar));
+        bulk_load(smem_u32(lut - b.pad), b.offsets + (size_t)head * b.offsets_pitch, bytes, smem_u32(bar));
     }
     wait_on(smem_u32(bar), count & 1, g, kErrTimeoutLoad);
     ++count;
@@ -301,7 +301,7 @@ inline int sms() {
 constexpr int kSmemBudget = 227 * 1024 - 2048;   // dynamic: behind the barriers
 
 // Shared memory of a head's offsets.
-inline int offsets_smem(const BiasDev &b) { return b.mode ? (b.entries * 4 + 32 + 1023) / 1024 * 1024 : 0; }
+inline int offsets_smem(const BiasDev &b) { return b.mode ? ((b.entries + 2 * b.pad) * 4 + 32 + 1023) / 1024 * 1024 : 0; }
 
 inline int round1k(int x) { return (x + 1023) / 1024 * 1024; }
 

@@ -55,10 +55,10 @@ struct BwdParams {
 __device__ __forceinline__ int tile_keys(int len, int t) { return min(kRows, len - t * kRows); }
 __device__ __forceinline__ int tile_cols(int keys) { return (keys + 15) & ~15; }
 
-__device__ __forceinline__ float neg_lse2(const float *lse, size_t at, bool in) {
-    const float l = in ? lse[at] : INFINITY;
+__device__ __forceinline__ float neg_lse2(float l) {
     return l == -INFINITY ? -INFINITY : -l * kLog2e;   // rows without keys: every weight 2^-inf = 0
 }
+__device__ __forceinline__ float neg_lse2(const float *lse, size_t at, bool in) { return neg_lse2(in ? lse[at] : INFINITY); }
 
 // Weights of a strip of a row of queries, in place: s -> 2^(scale2 s + bias - lse).
 // `c0`: first column of the tile, `keys`: valid columns from there (may be <= 0).
@@ -77,7 +77,7 @@ __device__ __forceinline__ void row_weights(float (&s)[kStrip], const BiasDev &b
             for (int c = 0; c < kStrip; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, add, add);
         } else {
             const int off = b.step_c * j0 - oq;
-            if (b.step_c == 1 && lo >= 0 && lo + 31 + kStrip - 1 <= last) {
+            if (b.step_c == 1) {   // inside the padded table
                 const float *l = lut + off;
 #pragma unroll
                 for (int c = 0; c < kStrip; ++c) s[c] = fmaf(s[c], scale2, l[c]) + nl;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
     const uint32_t qd = base, ring = base + 2 * x.q_slots * kTileBytes;   // slots of (Q, dO); stages of (K, V)
-    float *lut = reinterpret_cast<float *>(sm + x.off_lut);
+    float *lut = reinterpret_cast<float *>(sm + x.off_lut) + p.bias.pad;
     uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_aux);
     const Guard guard{x.err, &dead};
 
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
     const uint32_t kv = base, ring = base + 2 * kTileBytes;   // K, V; stages of (Q, dO)
-    float *lut = reinterpret_cast<float *>(sm + x.off_lut);
+    float *lut = reinterpret_cast<float *>(sm + x.off_lut) + p.bias.pad;
     QueryAux *aux = reinterpret_cast<QueryAux *>(sm + x.off_aux);
     const Guard guard{x.err, &dead};
 
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             add2(s[c], s[c + 1], s[c], s[c + 1], add, add);
                             add2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], add, add);
                         }
-                    } else if (off_lo - (kStrip - 1) >= 0 && off_hi <= last) {
+                    } else if (p.bias.step_c == 1) {   // inside the padded table
                         const float *l = lut + off;
 #pragma unroll
                         for (int c = 0; c < kStrip; ++c) s[c] = fmaf(s[c], scale2, l[-c]) + a.nl[c0 + c];
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Problem &p = x.p;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t ring = smem_u32(sm);   // stages of (Q, dO, K, V)
-    float *lut = reinterpret_cast<float *>(sm + x.off_lut);
+    float *lut = reinterpret_cast<float *>(sm + x.off_lut) + p.bias.pad;
     uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_aux);   // of the item's 128 keys
     float *tile = reinterpret_cast<float *>(sm + x.off_out), *sums = tile + kFoldTile * kFoldPitch;
     const Guard guard{x.err, &dead};
@@ -868,28 +868,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_offsets<kMath>(p.bias, w.h, lut, &bar.lut_full, luts, tid, guard);
                 lut_head = w.h;
             }
+            // lse and delta of the row, one batch entry ahead, as they are in memory (a use would wait for them)
+            const int i = w.q0 + wt, j0 = w.j0 + c0;
+            const bool in = i < p.n;
+            float lse_next = INFINITY, delta_next = 0.f;
+            auto scalars = [&](int b) __attribute__((always_inline)) {
+                const size_t row = ((size_t)b * p.heads + w.h) * p.n + i;
+                lse_next = in && b < w.b1 ? p.lse[row] : INFINITY;
+                delta_next = in && b < w.b1 ? p.delta[row] : 0.f;
+            };
+            scalars(w.b0);
             if (kBias == 2) {   // the previous item's are read: every warp has passed its fold
                 if (tid < kRows) key_off[tid] = (uint16_t)off_key(p.bias, min(w.j0 + tid, p.m - 1));
                 math_barrier();
             }
-            const int i = w.q0 + wt, j0 = w.j0 + c0;
-            const bool in = i < p.n;
             const int oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, p.bias.start);
             const int oq_lo = off_query(p.bias, i - lane, p.bias.start);
             float acc[kStrip];
 #pragma unroll
             for (int c = 0; c < kStrip; ++c) acc[c] = 0.f;
-            // lse and delta of the row, one batch entry ahead
-            auto scalars = [&](int b, float &nl, float &delta) __attribute__((always_inline)) {
-                const size_t row = ((size_t)b * p.heads + w.h) * p.n + i;
-                nl = neg_lse2(p.lse, row, in && b < w.b1);
-                delta = in && b < w.b1 ? p.delta[row] : 0.f;
-            };
-            float nl_next, delta_next;
-            scalars(w.b0, nl_next, delta_next);
             for (int b = w.b0; b < w.b1; ++b) {
-                const float nl = nl_next, delta = delta_next;
-                scalars(b + 1, nl_next, delta_next);
+                const float nl = neg_lse2(lse_next), delta = delta_next;
+                scalars(b + 1);
                 const int len = keys_of(p, b);
                 if (w.j0 >= len) continue;
                 const int keys = min(kStrip, len - j0);

@@ -75,47 +75,45 @@ __device__ __forceinline__ void fold_offsets(const FoldDev &f, const TileGeom &g
     const float inv = 1.f / (float)g.dc_n;
     for (int u = tid; u < g.dr_n * g.dc_n; u += threads) {
         const int dri = small_div(u, inv), dr = g.dr_lo + dri, dc = g.dc_lo + (u - dri * g.dc_n);
-        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+        float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int rq = max(g.rq0, g.rk0 - dr); rq <= min(g.rq1, g.rk1 - dr); ++rq) {
             const int qb = rq * wq - g.q0, kb = (rq + dr) * wk - g.j0;   // tile row of cq = 0, column of ck = 0
             const int lo = max(max(0, -qb), max(0, -kb) - dc);
             const int hi = min(min(wq - 1, g.nq - 1 - qb), min(wk - 1, g.nk - 1 - kb) - dc);
             const float *p = tile + (qb + lo) * kFoldPitch + kb + lo + dc;
             int c = lo;
-            for (; c + 3 <= hi; c += 4, p += 4 * (kFoldPitch + 1)) {
-                a0 += p[0];
-                a1 += p[kFoldPitch + 1];
-                a2 += p[2 * (kFoldPitch + 1)];
-                a3 += p[3 * (kFoldPitch + 1)];
+            for (; c + 7 <= hi; c += 8, p += 8 * (kFoldPitch + 1)) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = p[e * (kFoldPitch + 1)];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) a[e] += v[e];
             }
-            for (; c <= hi; ++c, p += kFoldPitch + 1) a0 += *p;
+            for (; c <= hi; ++c, p += kFoldPitch + 1) a[0] += *p;
         }
-        sums[dri * pitch + (u - dri * g.dc_n)] = (a0 + a1) + (a2 + a3);
+        sums[dri * pitch + (u - dri * g.dc_n)] = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
     }
 }
 
-// The offsets' sums into the tile's block of column buckets, [dr_n][f.K]; eight
-// lanes share a bucket (far buckets hold up to 255 offsets).
+// The offsets' sums into the tile's block of column buckets, [dr_n][f.K]; a warp
+// per bucket (far buckets hold up to 255 offsets).
 __device__ __forceinline__ void fold_buckets(const FoldDev &f, const TileGeom &g, const float *sums, float *out, int tid,
                                              int threads) {
-    const int lane = tid & 7;
-    const int total = g.dr_n * g.cb_n, rounds = (total * 8 + threads - 1) / threads;
+    const int lane = tid & 31, total = g.dr_n * g.cb_n;
     const float inv = 1.f / (float)g.cb_n;
-    for (int r = 0; r < rounds; ++r) {
-        const int u = (r * threads + tid) >> 3;
+    for (int u = tid >> 5; u < total; u += threads >> 5) {
         const int dri = small_div(u, inv), c = u - dri * g.cb_n;
+        int lo, hi;
+        bucket_range(f.cols, g.cb_lo + c, lo, hi);
+        lo = max(lo + f.start_c - g.dc_lo, 0);
+        hi = min(hi + f.start_c - g.dc_lo, g.dc_n - 1);
         float s = 0.f;
-        if (u < total) {
-            int lo, hi;
-            bucket_range(f.cols, g.cb_lo + c, lo, hi);
-            lo = max(lo + f.start_c - g.dc_lo, 0);
-            hi = min(hi + f.start_c - g.dc_lo, g.dc_n - 1);
-            for (int x = lo + lane; x <= hi; x += 8) s += sums[dri * g.dc_n + x];
+        for (int x = lo + lane; x <= hi; x += 32) s += sums[dri * g.dc_n + x];
+        if (hi - lo >= 1) {   // the same for the whole warp
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
         }
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, 4);
-        if (u < total && lane == 0) out[dri * f.K + c] = s;
+        if (lane == 0) out[dri * f.K + c] = s;
     }
 }
 

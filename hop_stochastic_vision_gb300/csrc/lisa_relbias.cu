@@ -69,16 +69,17 @@ __global__ void __launch_bounds__(kDenseThreads) bias_dense(BiasDev b, T *out, i
 // The table by offset, times log2(e): thread per offset, all heads of it.
 __global__ void __launch_bounds__(128) bias_offsets(BiasDev b, float *out) {
     chain_begin();
-    const int e = blockIdx.x * 128 + threadIdx.x, h0 = blockIdx.y * 4;
-    if (e >= b.entries + 4) return;   // four zeros behind the last offset
-    const bool in = e < b.entries;
-    const float *row = b.table + (size_t)(in ? entry_bucket(b, e) : 0) * b.heads;
+    const int at = blockIdx.x * 128 + threadIdx.x, h0 = blockIdx.y * 4;
+    if (at >= b.entries + 2 * b.pad + 4) return;   // four zeros behind the last
+    const bool in = at < b.entries + 2 * b.pad;
+    const int e = min(max(at - b.pad, 0), b.entries - 1);
+    const float *row = b.table + (size_t)entry_bucket(b, e) * b.heads;
     float v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) v[u] = in && h0 + u < b.heads ? row[h0 + u] : 0.f;
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-        if (h0 + u < b.heads) out[(size_t)(h0 + u) * b.offsets_pitch + e] = v[u] * 1.4426950408889634f;
+        if (h0 + u < b.heads) out[(size_t)(h0 + u) * b.offsets_pitch + at] = v[u] * 1.4426950408889634f;
 }
 
 // ---------------------------------------------------------------- gradient
@@ -332,7 +333,7 @@ size_t offsets_bytes(const BiasDev &b) {
 }
 
 cudaError_t launch_offsets(const BiasDev &b, float *out, cudaStream_t s) {
-    return launch_chained(bias_offsets, dim3((unsigned)((b.entries + 4 + 127) / 128), (unsigned)((b.heads + 3) / 4)), 128, 0, s,
+    return launch_chained(bias_offsets, dim3((unsigned)((b.entries + 2 * b.pad + 4 + 127) / 128), (unsigned)((b.heads + 3) / 4)), 128, 0, s,
                           b, out);
 }
 
