@@ -69,6 +69,9 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float *r) {
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, float *r) {
+    tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *r) {
     const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
     asm volatile(

@@ -62,43 +62,44 @@ __device__ __forceinline__ float neg_lse2(const float *lse, size_t at, bool in) 
 
 // Weights of a strip of a row of queries, in place: s -> 2^(scale2 s + bias - lse).
 // `c0`: first column of the tile, `keys`: valid columns from there (may be <= 0).
-template <int kBias>
-__device__ __forceinline__ void row_weights(float (&s)[kStrip], const BiasDev &b, const float *lut, const uint16_t *key_off,
+template <int kBias, int N>
+__device__ __forceinline__ void row_weights(float (&s)[N], const BiasDev &b, const float *lut, const uint16_t *key_off,
                                             int j0, int keys, int oq, int oq_lo, float scale2, float nl) {
     if (kBias == 0) {
 #pragma unroll
-        for (int c = 0; c < kStrip; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, nl, nl);
+        for (int c = 0; c < N; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, nl, nl);
     } else if (kBias == 1) {
         const int oq_hi = oq_lo + 31, last = b.entries - 1;
         const int lo = b.step_c * j0 - oq_hi, hi = b.step_c * (j0 + max(keys, 1) - 1) - oq_lo;
         if (hi <= 0 || lo >= last) {
             const float add = nl + lut[hi <= 0 ? 0 : last];
 #pragma unroll
-            for (int c = 0; c < kStrip; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, add, add);
+            for (int c = 0; c < N; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, add, add);
         } else {
-            const int off = b.step_c * j0 - oq;
+            int off = b.step_c * j0 - oq;
+            asm volatile("" : "+r"(off));   // not hoisted out of a loop over the batch, column by column
             if (b.step_c == 1) {   // inside the padded table
                 const float *l = lut + off;
 #pragma unroll
-                for (int c = 0; c < kStrip; ++c) s[c] = fmaf(s[c], scale2, l[c]) + nl;
+                for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], scale2, l[c]) + nl;
             } else {
 #pragma unroll
-                for (int c = 0; c < kStrip; ++c)
+                for (int c = 0; c < N; ++c)
                     s[c] = fmaf(s[c], scale2, lut[min(max(off + b.step_c * c, 0), last)]) + nl;
             }
         }
     } else {
         grid_bias(s, b, lut - oq, key_off, j0, scale2);   // inside the table by construction
 #pragma unroll
-        for (int c = 0; c < kStrip; c += 2) add2(s[c], s[c + 1], s[c], s[c + 1], nl, nl);
+        for (int c = 0; c < N; c += 2) add2(s[c], s[c + 1], s[c], s[c + 1], nl, nl);
     }
-    if (keys < kStrip) {
+    if (keys < N) {
 #pragma unroll
-        for (int c = 0; c < kStrip; ++c)
+        for (int c = 0; c < N; ++c)
             if (c >= keys) s[c] = -INFINITY;
     }
 #pragma unroll
-    for (int c = 0; c < kStrip; ++c) s[c] = ex2_approx(s[c]);
+    for (int c = 0; c < N; ++c) s[c] = ex2_approx(s[c]);
 }
 
 // A strip.  Columns that the products did not reach hold whatever was
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_strips(tS + c0 + lanes, s, tP + c0 + lanes, dp);
                 tc_fence_before();
                 arrive_warp(&bar.free, lane);
-                row_weights<kBias>(s, p.bias, lut, key_off, j0, keys - c0, oq, oq_lo, scale2, nl);
+                row_weights<kBias, kStrip>(s, p.bias, lut, key_off, j0, keys - c0, oq, oq_lo, scale2, nl);
                 if (keys - c0 < kStrip) {   // dP of keys behind the last one holds whatever their values hold
 #pragma unroll
                     for (int e = 0; e < kStrip; ++e)
@@ -893,19 +894,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int len = keys_of(p, b);
                 if (w.j0 >= len) continue;
                 const int keys = min(kStrip, len - j0);
-                float s[kStrip], dp[kStrip];
                 wait_on(smem_u32(&bar.s_full), n & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
-                load_strips(tS + c0 + lanes, s, tD + c0 + lanes, dp);
-                tc_fence_before();
-                arrive_warp(&bar.s_free, lane);
-                row_weights<kBias>(s, p.bias, lut, key_off - w.j0, j0, keys, oq, oq_lo, scale2, nl);
+                // sixteen columns at a time: with the sums of all 32 a whole strip of S and dP would not stay in
+                // registers, and a spill goes to L2 (shared memory leaves next to no L1)
 #pragma unroll
-                for (int e = 0; e < kStrip; e += 2) {
-                    add2(dp[e], dp[e + 1], dp[e], dp[e + 1], -delta, -delta);
-                    if (e >= keys) dp[e] = 0.f;
-                    if (e + 1 >= keys) dp[e + 1] = 0.f;
-                    fma2(acc[e], acc[e + 1], s[e], s[e + 1], dp[e], dp[e + 1], acc[e], acc[e + 1]);
+                for (int c = 0; c < kStrip; c += 16) {
+                    float s[16], dp[16];
+                    tmem_ld16_nowait(tS + c0 + c + lanes, s);
+                    tmem_ld16_nowait(tD + c0 + c + lanes, dp);
+                    tc_wait_ld();
+                    if (c + 16 == kStrip) {
+                        tc_fence_before();
+                        arrive_warp(&bar.s_free, lane);
+                    }
+                    row_weights<kBias, 16>(s, p.bias, lut, key_off - w.j0, j0 + c, keys - c, oq, oq_lo, scale2, nl);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        add2(dp[e], dp[e + 1], dp[e], dp[e + 1], -delta, -delta);
+                        if (c + e >= keys) dp[e] = 0.f;
+                        if (c + e + 1 >= keys) dp[e + 1] = 0.f;
+                        fma2(acc[c + e], acc[c + e + 1], s[e], s[e + 1], dp[e], dp[e + 1], acc[c + e], acc[c + e + 1]);
+                    }
                 }
                 ++n;
             }
