@@ -70,7 +70,6 @@ struct FoldDev {
     int row_buckets, col_buckets;
     int nR, K;         // a tile's block: at most nR row differences, K column buckets
     int units;         // at most so many offsets in a tile
-    int span;          // key tiles that are added side by side for a query tile
     float *part;       // [parts][heads][qtiles][ktiles][nR][K]
 };
 

@@ -205,17 +205,19 @@ __global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ Gr
 }
 
 // ------------------------------------------------- gradient, tile by tile
-// One 128 x 128 tile of one head: loaded whole (every load of a thread in
-// flight at once, so three CTAs keep some 190 KB per SM on the way), then folded.
+// One 128 x 128 tile of one head: loaded into shared memory, then folded; three
+// CTAs per SM, so one folds while the others load (two of 256 threads and 128
+// registers took 72 us for the 268 MB of a 64 x 64 grid's four heads).
+constexpr int kFoldThreads = 512;
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) fold_matrix(const __grid_constant__ FoldDev f, const T *dbias, int matrices) {
+__global__ void __launch_bounds__(kFoldThreads, 3) fold_matrix(const __grid_constant__ FoldDev f, const T *dbias, int matrices) {
     extern __shared__ __align__(16) float fold_smem[];
     chain_begin();
     float *tile = fold_smem, *sums = fold_smem + kFoldTile * kFoldPitch;
     const int tid = threadIdx.x, jt = blockIdx.x, it = blockIdx.y, h = blockIdx.z;
     const TileGeom g = fold_geom(f, it, jt);
-    constexpr int kPerRow = kFoldTile / VEC, kRowsAtOnce = 256 / kPerRow, kLoads = kFoldTile / kRowsAtOnce;
-    constexpr int kBatch = kLoads < 16 ? kLoads : 16;
+    constexpr int kPerRow = kFoldTile / VEC, kRowsAtOnce = kFoldThreads / kPerRow, kLoads = kFoldTile / kRowsAtOnce;
+    constexpr int kBatch = VEC * (int)sizeof(T) == 16 ? (kLoads < 4 ? kLoads : 4) : (kLoads < 8 ? kLoads : 8);
     const int r0 = tid / kPerRow, c = (tid % kPerRow) * VEC;
     for (int part = 0; part < matrices; ++part) {
         const T *src = dbias + ((size_t)part * f.heads + h) * ((size_t)f.n * f.m) + (size_t)g.q0 * f.m + g.j0;
@@ -242,46 +244,75 @@ __global__ void __launch_bounds__(256) fold_matrix(const __grid_constant__ FoldD
     __syncthreads();
     float *out = fold_block(f, 0, h, it, jt);
     const bool direct = fold_direct(f, g);
-    fold_offsets(f, g, tile, direct ? out : sums, direct ? f.K : g.dc_n, tid, 256);
+    fold_offsets(f, g, tile, direct ? out : sums, direct ? f.K : g.dc_n, tid, kFoldThreads);
     if (direct) return;
     __syncthreads();
-    fold_buckets(f, g, sums, out, tid, 256);
+    fold_buckets(f, g, sums, out, tid, kFoldThreads);
 }
 
-// dtable of a row bucket: its share of the tiles' blocks, `groups` runs of tiles
-// added side by side by `width` columns of threads.
-__global__ void __launch_bounds__(1024) fold_sum(const __grid_constant__ FoldDev f, float *dtable, int width, int groups) {
+// dtable of a row bucket.  1024 tiles at a time: a thread works out whether its
+// tile meets the bucket and where its block stands, the tiles that do are lined
+// up in order, and then `groups` runs of them are added side by side by `width`
+// columns of threads.
+struct FoldShare {
+    int tile, row, rows, cb_lo, cb_n;   // the block, and its rows of this bucket
+};
+__global__ void __launch_bounds__(1024) fold_sum(const __grid_constant__ FoldDev f, float *dtable, int width, int groups,
+                                                 FastDiv div_ktiles) {
     __shared__ float acc_s[1024];
+    __shared__ FoldShare list[1024];
+    __shared__ int ahead[33];
     chain_begin();
-    const int rb = blockIdx.x, h = blockIdx.z;
-    const int c = threadIdx.x % width, grp = threadIdx.x / width;
+    const int rb = blockIdx.x, h = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c = tid % width, grp = tid / width;
     const int cb = blockIdx.y * width + c;
     int lo, hi;
     bucket_range(f.rows, rb, lo, hi);
     lo = max(lo, -kFar / 2) + f.start_r;   // row differences rk - rq of this bucket
     hi = min(hi, kFar / 2) + f.start_r;
+    const int tiles = f.qtiles * f.ktiles;
+    const size_t block = (size_t)f.nR * f.K;
     float acc = 0.f;
-    if (cb < f.col_buckets) {
-        const int wk = (int)f.div_k.d, last = quotient(f.m - 1, f.div_k);
-        for (int x = grp; x < f.qtiles * f.span; x += groups) {
-            const int it = x / f.span;
-            // key tiles whose rows can hold rq + lo .. rq + hi
-            const int q0 = it * kFoldTile, q1 = min(q0 + kFoldTile, f.n) - 1;
-            const int r0 = quotient(q0, f.div_q) + lo, r1 = quotient(q1, f.div_q) + hi;
-            if (r1 < 0 || r0 > last) continue;
-            const int j1 = min((min(r1, last) * wk + wk - 1) / kFoldTile, f.ktiles - 1);
-            for (int jt = max(r0, 0) * wk / kFoldTile + (x - it * f.span); jt <= j1; jt += f.span) {
-                const TileGeom g = fold_geom(f, it, jt);
-                if (cb < g.cb_lo || cb >= g.cb_lo + g.cb_n) continue;
-                const int d0 = max(lo, g.dr_lo), d1 = min(hi, g.dr_lo + g.dr_n - 1);
-                for (int part = 0; part < f.parts; ++part) {
-                    const float *b = fold_block(f, part, h, it, jt) + cb - g.cb_lo;
-                    for (int d = d0; d <= d1; ++d) acc += b[(size_t)(d - g.dr_lo) * f.K];
-                }
+    for (int t0 = 0; t0 < tiles; t0 += 1024) {
+        const int tile = t0 + tid;
+        FoldShare mine{tile, 0, 0, 0, 0};
+        if (tile < tiles) {
+            int jt = tile;
+            const int it = split(jt, div_ktiles);
+            const TileGeom g = fold_geom(f, it, jt);
+            const int d0 = max(lo, g.dr_lo), d1 = min(hi, g.dr_lo + g.dr_n - 1);
+            mine = FoldShare{tile, d0 - g.dr_lo, d1 - d0 + 1, g.cb_lo, g.cb_n};
+        }
+        const unsigned votes = __ballot_sync(0xFFFFFFFFu, mine.rows > 0);
+        __syncthreads();   // the previous list has been read
+        if (lane == 0) ahead[warp + 1] = __popc(votes);
+        if (tid == 0) ahead[0] = 0;
+        __syncthreads();
+        if (warp == 0) {
+            int n = ahead[lane + 1];
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int up = __shfl_up_sync(0xFFFFFFFFu, n, m);
+                if (lane >= m) n += up;
+            }
+            ahead[lane + 1] = n;
+        }
+        __syncthreads();
+        if (mine.rows > 0) list[ahead[warp] + __popc(votes & ((1u << lane) - 1u))] = mine;
+        __syncthreads();
+        const int count = ahead[32];
+        for (int part = 0; part < f.parts; ++part) {
+            const float *base = f.part + ((size_t)part * f.heads + h) * tiles * block + cb;
+#pragma unroll 4
+            for (int e = grp < groups ? grp : count; e < count; e += groups) {
+                const FoldShare s = list[e];
+                if (cb < s.cb_lo || cb >= s.cb_lo + s.cb_n) continue;
+                const float *b = base + s.tile * block + (size_t)s.row * f.K - s.cb_lo;
+                for (int d = 0; d < s.rows; ++d) acc += b[(size_t)d * f.K];
             }
         }
     }
-    acc_s[threadIdx.x] = acc;
+    acc_s[tid] = acc;
     __syncthreads();
     if (grp == 0 && cb < f.col_buckets) {
         float s = 0.f;
@@ -294,7 +325,7 @@ template <typename T, int VEC>
 cudaError_t run_fold_vec(const FoldDev &f, const T *dbias, int matrices, cudaStream_t s) {
     cudaError_t e = allow_smem<fold_matrix<T, VEC>>();
     if (e != cudaSuccess) return e;
-    return launch_plain(fold_matrix<T, VEC>, dim3((unsigned)f.ktiles, (unsigned)f.qtiles, (unsigned)f.heads), 256,
+    return launch_plain(fold_matrix<T, VEC>, dim3((unsigned)f.ktiles, (unsigned)f.qtiles, (unsigned)f.heads), kFoldThreads,
                           kFoldTileBytes + f.units * 4, s, f, dbias, matrices);
 }
 
@@ -381,9 +412,7 @@ bool fold_plan(const lisa_rel_bias &b, int heads, int parts, FoldDev &f) {
     const int width = std::min(kFoldTile, b.q_cols) + std::min(kFoldTile, b.k_cols) - 1;
     f.K = dev.cols.log_rule ? b.cols.buckets : std::min(b.cols.buckets, width);
     f.units = f.nR * width;
-    // key tiles that hold one row difference of a query tile's rows (a bucket of several takes more turns)
-    f.span = (int)std::min<long long>(f.ktiles, ((long long)qr * b.k_cols + kFoldTile - 2) / kFoldTile + 1);
-    return f.units <= kMaxFoldUnits && f.qtiles <= 65535;
+    return f.units <= kMaxFoldUnits && f.qtiles <= 65535 && (long long)f.qtiles * f.ktiles < (1 << 30);
 }
 
 size_t fold_bytes(const FoldDev &f) {
@@ -393,7 +422,7 @@ size_t fold_bytes(const FoldDev &f) {
 cudaError_t launch_fold_sum(const FoldDev &f, float *dtable, cudaStream_t s) {
     const int width = std::min(256, (f.col_buckets + 31) / 32 * 32), groups = 1024 / width;
     return launch_plain(fold_sum, dim3((unsigned)f.row_buckets, (unsigned)((f.col_buckets + width - 1) / width), (unsigned)f.heads),
-                          width * groups, 0, s, f, dtable, width, groups);
+                        1024, 0, s, f, dtable, width, groups, fast_div(f.ktiles));
 }
 
 size_t bias_grad_bytes(const lisa_rel_bias &b, int heads) {
