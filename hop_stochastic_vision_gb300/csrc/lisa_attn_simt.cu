@@ -39,17 +39,34 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
     v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xFFFF0000u);
 }
 
-// Rows t0 .. t0 + 63 of a [tokens][D] slice into out[64][D + 4]; rows at or
-// behind `count` read as zero and are not touched in memory.
+// Rows t0 .. t0 + 63 of a [tokens][D] slice, first into registers (so the loads of
+// the next tile run under this tile's arithmetic), then into out[64][D + 4]; rows
+// at or behind `count` are zero and are not touched in memory.
+template <int D>
+struct Rows {
+    float v[D / 16][4];
+    template <typename T>
+    __device__ __forceinline__ void load(const T *base, long long st, int t0, int count, int tid) {
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+            const int e = tid + u * kThreads, r = e / (D / 4), c = 4 * (e % (D / 4));
+            v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.f;
+            if (t0 + r < count) load4(base + (long long)(t0 + r) * st + c, v[u]);
+        }
+    }
+    __device__ __forceinline__ void store(float *out, int tid) const {
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+            const int e = tid + u * kThreads, r = e / (D / 4), c = 4 * (e % (D / 4));
+            *reinterpret_cast<float4 *>(out + r * (D + 4) + c) = make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
+        }
+    }
+};
 template <typename T, int D>
 __device__ __forceinline__ void load_tile(const T *base, long long st, int t0, int count, float *out, int tid) {
-#pragma unroll
-    for (int e = tid; e < kTile * D / 4; e += kThreads) {
-        const int r = e / (D / 4), c = 4 * (e % (D / 4));
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (t0 + r < count) load4(base + (long long)(t0 + r) * st + c, v);
-        *reinterpret_cast<float4 *>(out + r * (D + 4) + c) = make_float4(v[0], v[1], v[2], v[3]);
-    }
+    Rows<D> r;
+    r.load(base, st, t0, count, tid);
+    r.store(out, tid);
 }
 
 // s[r][c] = sum_d A[4 ty + r][d] B[tx + 16 c][d]
@@ -182,11 +199,16 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) acc[r][c] = 0.f;
     }
+    Rows<D> kr, vr;
+    kr.load(slice<T>(p.K, b, kvh), p.K.st, 0, len, tid);
+    vr.load(slice<T>(p.V, b, kvh), p.V.st, 0, len, tid);
     for (int j0 = 0; j0 < len; j0 += kTile) {
         __syncthreads();
-        load_tile<T, D>(slice<T>(p.K, b, kvh), p.K.st, j0, len, k_s, tid);
-        load_tile<T, D>(slice<T>(p.V, b, kvh), p.V.st, j0, len, v_s, tid);
+        kr.store(k_s, tid);
+        vr.store(v_s, tid);
         __syncthreads();
+        kr.load(slice<T>(p.K, b, kvh), p.K.st, j0 + kTile, len, tid);
+        vr.load(slice<T>(p.V, b, kvh), p.V.st, j0 + kTile, len, tid);
         float s[4][4];
         tile_dot<D>(q_s, k_s, ty, tx, s);
         finish_scores(s, p, lut, j0, len, tx, oq);
@@ -262,11 +284,16 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
     }
     __syncthreads();
     load_tile<T, D>(slice<T>(p.Q, b, h), p.Q.st, i0, p.n, q_s, tid);
+    Rows<D> kr, vr;
+    kr.load(slice<T>(p.K, b, kvh), p.K.st, 0, len, tid);
+    vr.load(slice<T>(p.V, b, kvh), p.V.st, 0, len, tid);
     for (int j0 = 0; j0 < len; j0 += kTile) {
         __syncthreads();
-        load_tile<T, D>(slice<T>(p.K, b, kvh), p.K.st, j0, len, k_s, tid);
-        load_tile<T, D>(slice<T>(p.V, b, kvh), p.V.st, j0, len, v_s, tid);
+        kr.store(k_s, tid);
+        vr.store(v_s, tid);
         __syncthreads();
+        kr.load(slice<T>(p.K, b, kvh), p.K.st, j0 + kTile, len, tid);
+        vr.load(slice<T>(p.V, b, kvh), p.V.st, j0 + kTile, len, tid);
         float s[4][4], dp[4][4];
         tile_dot<D>(q_s, k_s, ty, tx, s);
         tile_dot<D>(o_s, v_s, ty, tx, dp);
@@ -317,11 +344,16 @@ __global__ void __launch_bounds__(kThreads) simt_dkdv(const __grid_constant__ Pr
             const size_t row0 = ((size_t)b * p.heads + h) * p.n;
             __syncthreads();
             if (p.bias.mode) fill_offsets(p.bias, h, 1.f, lut, tid, kThreads);
+            Rows<D> qr, dr;
+            qr.load(slice<T>(p.Q, b, h), p.Q.st, 0, p.n, tid);
+            dr.load(slice<T>(p.dO, b, h), p.dO.st, 0, p.n, tid);
             for (int i0 = 0; i0 < p.n; i0 += kTile) {
                 __syncthreads();
-                load_tile<T, D>(slice<T>(p.Q, b, h), p.Q.st, i0, p.n, q_s, tid);
-                load_tile<T, D>(slice<T>(p.dO, b, h), p.dO.st, i0, p.n, o_s, tid);
+                qr.store(q_s, tid);
+                dr.store(o_s, tid);
                 __syncthreads();
+                qr.load(slice<T>(p.Q, b, h), p.Q.st, i0 + kTile, p.n, tid);
+                dr.load(slice<T>(p.dO, b, h), p.dO.st, i0 + kTile, p.n, tid);
                 float s[4][4], dp[4][4];
                 int oq[4];
 #pragma unroll

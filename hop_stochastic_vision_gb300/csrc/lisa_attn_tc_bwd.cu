@@ -919,9 +919,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++n;
             }
-            float4 *mine = reinterpret_cast<float4 *>(tile + wt * kFoldPitch + c0);
+            float *mine = tile + wt * kFoldPitch + c0;
 #pragma unroll
-            for (int c = 0; c < kStrip; c += 4) mine[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+            for (int c = 0; c < kStrip; ++c) mine[c] = acc[c];
             math_barrier();
             if (p.folded) {
                 const TileGeom g = fold_geom(p.fold, w.q0 / kFoldTile, w.j0 / kFoldTile);
@@ -1043,7 +1043,7 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     x.items = (int)items;
     x.splits = p.b_splits;
     x.div_splits = fast_div(x.splits);
-    const int fold = kFoldTileBytes + (p.folded ? round1k(p.fold.units * 4) : 0);
+    const int fold = kFoldTileBytes + (p.folded ? p.fold.units * 4 : 0);
     x.stages = std::min(kMaxStages, (kSmemBudget - fold - lut - 2048) / (4 * kTileBytes));
     if (x.stages < 1) return cudaErrorInvalidValue;
     x.off_out = 4 * x.stages * kTileBytes;

@@ -7,8 +7,10 @@
 // walks every fourth chunk of 32 keys of its CTA's part with its own ring of
 // asynchronous copies, keeps the running maximum, sum and output in registers,
 // and the warps and then the CTAs of the cluster join in a fixed order.  Bound
-// by the bytes of K and V: no CTA waits for another until the end, and with three
-// chunks of 8 KB in flight per warp two CTAs keep 190 KB per SM on the way.
+// by the bytes of K and V: no CTA waits for another until the end, and with two
+// chunks of 8 KB in flight per warp three CTAs keep 190 KB per SM on the way
+// (64 x 4096 keys, 4 key heads, lengths from 0 up: 46 us; two CTAs with three
+// chunks 52 us).
 #include <algorithm>
 
 #include "lisa_attn_tc.cuh"
@@ -19,7 +21,7 @@ namespace {
 
 constexpr int kTokenThreads = 128, kTokenWarps = 4;
 constexpr int kChunk = 32;       // keys of one step
-constexpr int kTokenStages = 3;
+constexpr int kTokenStages = 2;
 
 struct TokenParams {
     Problem p;
@@ -343,10 +345,10 @@ cudaError_t launch_token(const Problem &p, cudaStream_t s) {
     x.rtiles = (x.rows + 15) / 16;
     x.div_rtiles = fast_div(x.rtiles);
     x.div_n = fast_div(p.n);
-    // about three waves of two CTAs per SM, so lengths that differ even out, but at least 256 keys to a CTA
+    // about two waves of three CTAs per SM, so lengths that differ even out, but at least 256 keys to a CTA
     const long long ctas = (long long)p.B * p.kv_heads * x.rtiles;
     x.splits = 1;
-    while (x.splits < 8 && ctas * x.splits < 3 * 2 * 152 && p.m >= 2 * x.splits * 256) x.splits *= 2;
+    while (x.splits < 8 && ctas * x.splits < 6 * 152 && p.m >= 2 * x.splits * 256) x.splits *= 2;
     if (p.d == 16) return p.bias.mode ? go<16, 1>(x, s) : go<16, 0>(x, s);
     if (p.d == 32) return p.bias.mode ? go<32, 1>(x, s) : go<32, 0>(x, s);
     return p.bias.mode ? go<64, 1>(x, s) : go<64, 0>(x, s);

@@ -20,7 +20,8 @@ namespace attn {
 namespace {
 
 constexpr int kFoldTile = 128;
-constexpr int kFoldPitch = 132;       // floats; rows 16-byte aligned, 4 banks apart
+constexpr int kFoldPitch = 133;       // floats: neighbouring rows 5 banks apart, diagonals 6, so a warp meets no
+                                      // bank twice whether its lanes stand in one row or in one column
 constexpr int kFoldTileBytes = kFoldTile * kFoldPitch * 4;
 
 struct TileGeom {

@@ -205,6 +205,13 @@ __global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ Gr
 }
 
 // ------------------------------------------------- gradient, tile by tile
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// 4 bytes global -> shared, or zeros (nothing is read then)
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // One 128 x 128 tile of one head: loaded into shared memory, then folded; three
 // CTAs per SM, so one folds while the others load (two of 256 threads and 128
 // registers took 72 us for the 268 MB of a 64 x 64 grid's four heads).
@@ -216,22 +223,32 @@ __global__ void __launch_bounds__(kFoldThreads, 3) fold_matrix(const __grid_cons
     float *tile = fold_smem, *sums = fold_smem + kFoldTile * kFoldPitch;
     const int tid = threadIdx.x, jt = blockIdx.x, it = blockIdx.y, h = blockIdx.z;
     const TileGeom g = fold_geom(f, it, jt);
+    // 4 bytes of a row per lane: whole lines per load, and stores that meet no bank twice (two bf16: once more)
     constexpr int kPerRow = kFoldTile / VEC, kRowsAtOnce = kFoldThreads / kPerRow, kLoads = kFoldTile / kRowsAtOnce;
-    constexpr int kBatch = VEC * (int)sizeof(T) == 16 ? (kLoads < 4 ? kLoads : 4) : (kLoads < 8 ? kLoads : 8);
     const int r0 = tid / kPerRow, c = (tid % kPerRow) * VEC;
+    struct __align__(sizeof(T) * VEC) Vec { T v[VEC]; };
     for (int part = 0; part < matrices; ++part) {
-        const T *src = dbias + ((size_t)part * f.heads + h) * ((size_t)f.n * f.m) + (size_t)g.q0 * f.m + g.j0;
+        const T *src = dbias + ((size_t)part * f.heads + h) * ((size_t)f.n * f.m) + (size_t)g.q0 * f.m + g.j0 + c;
+        if (sizeof(T) == 4 && part == 0) {   // straight into shared memory, all of the tile in flight
+#pragma unroll 8
+            for (int e = 0; e < kLoads; ++e) {
+                const int r = r0 + e * kRowsAtOnce;
+                const bool in = r < g.nq && c < g.nk;
+                copy4(smem_at(tile + r * kFoldPitch + c), src + (in ? (size_t)r * f.m : (size_t)0) - (in ? 0 : c), in);
+            }
+            copies_done();
+            continue;
+        }
+        constexpr int kBatch = 16;
         for (int b = 0; b < kLoads; b += kBatch) {
-            struct __align__(sizeof(T) * VEC) Vec { T v[VEC]; };
             Vec x[kBatch];
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
                 const int r = r0 + (b + e) * kRowsAtOnce;
-                if (r < g.nq && c < g.nk)   // a vector is whole or absent: m is a multiple of VEC where VEC > 1
-                    x[e] = *reinterpret_cast<const Vec *>(src + (size_t)r * f.m + c);
-                else
 #pragma unroll
-                    for (int u = 0; u < VEC; ++u) put(&x[e].v[u], 0.f);
+                for (int u = 0; u < VEC; ++u) put(&x[e].v[u], 0.f);
+                // a vector is whole or absent: m is a multiple of VEC
+                if (r < g.nq && c < g.nk) x[e] = *reinterpret_cast<const Vec *>(src + (size_t)r * f.m);
             }
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
@@ -331,10 +348,6 @@ cudaError_t run_fold_vec(const FoldDev &f, const T *dbias, int matrices, cudaStr
 
 template <typename T>
 cudaError_t run_fold(const FoldDev &f, const T *dbias, int matrices, cudaStream_t s) {
-    // the widest vector that every row begins on
-    constexpr int kFull = 16 / (int)sizeof(T);
-    if (f.m % kFull == 0) return run_fold_vec<T, kFull>(f, dbias, matrices, s);
-    if (f.m % (kFull / 2) == 0) return run_fold_vec<T, kFull / 2>(f, dbias, matrices, s);
     if (sizeof(T) == 2 && f.m % 2 == 0) return run_fold_vec<T, 2>(f, dbias, matrices, s);
     return run_fold_vec<T, 1>(f, dbias, matrices, s);
 }
