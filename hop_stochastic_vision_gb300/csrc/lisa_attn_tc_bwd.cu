@@ -34,13 +34,13 @@ constexpr int kMathWarps = kMath / 32;
 constexpr int kThreads = kMath + 128;   // behind them: products (two warps), loads, a helper
 constexpr int kFront = kMathWarps, kLoads = kMathWarps + 1, kBack = kMathWarps + 2, kHelper = kMathWarps + 3;
 constexpr int kStrip = 32;         // columns of a thread's row
-constexpr int kDqOut = kMathWarps * 1024, kDkvOut = kMathWarps * 2048;   // staging blocks of the math warps
+constexpr int kDkvOut = kMathWarps * 2048;   // staging blocks of the math warps
 constexpr int kMaxStages = 4;
 constexpr uint32_t kPair = 2 * kTileBytes / 16;   // a ring stage of two tiles, in descriptor units
 
 struct BwdParams {
     Problem p;
-    MapUse uq, uk, uv, ud;
+    MapUse uq, uk, uv, ud, uo;
     int *err;
     int first;             // this kernel clears the error word
     int qtiles, ktiles;    // tiles of 128 queries, keys
@@ -140,7 +140,7 @@ template <int kBias>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md,
           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-          const __grid_constant__ BwdParams x) {
+          const __grid_constant__ CUtensorMap mo, const __grid_constant__ BwdParams x) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // stays a shared-memory pointer
     __shared__ __align__(8) DqBars bar;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Problem &p = x.p;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
-    const uint32_t qd = base, ring = base + 2 * x.q_slots * kTileBytes;   // slots of (Q, dO); stages of (K, V)
+    const uint32_t qd = base, ring = base + 3 * x.q_slots * kTileBytes;   // slots of (Q, dO, O); stages of (K, V)
     float *lut = reinterpret_cast<float *>(sm + x.off_lut) + p.bias.pad;
     uint16_t *key_off = reinterpret_cast<uint16_t *>(sm + x.off_aux);
     const Guard guard{x.err, &dead};
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&bar.q_full[t]), 1);
-            mbar_init(smem_u32(&bar.q_empty[t]), 1);
+            mbar_init(smem_u32(&bar.q_empty[t]), 1 + kMathWarps);   // the products and delta
         }
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(smem_u32(&bar.kv_full[s]), 1);
@@ -209,9 +209,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (nq >= x.q_slots) wait_on(smem_u32(&bar.q_empty[qs]), cq.phase ^ 1u, guard, kErrTimeoutMma);
                 cq.next(x.q_slots);
                 const uint32_t f = smem_u32(&bar.q_full[qs]);
-                mbar_arrive_expect_tx(f, 2 * kTileBytes);
-                load_rows(qd + 2 * qs * kTileBytes, &mq, x.uq, w.q0, w.h, w.b, f);
-                load_rows(qd + (2 * qs + 1) * kTileBytes, &md, x.ud, w.q0, w.h, w.b, f);
+                mbar_arrive_expect_tx(f, 3 * kTileBytes);
+                load_rows(qd + 3 * qs * kTileBytes, &mq, x.uq, w.q0, w.h, w.b, f);
+                load_rows(qd + (3 * qs + 1) * kTileBytes, &md, x.ud, w.q0, w.h, w.b, f);
+                load_rows(qd + (3 * qs + 2) * kTileBytes, &mo, x.uo, w.q0, w.h, w.b, f);
                 ++nq;
                 for (int j = 0; j < w.tiles; ++j, ++kt, c.next(x.stages)) {
                     const uint32_t f = smem_u32(&bar.kv_full[c.slot]), at = ring + 2 * c.slot * kTileBytes;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int qs = cq.slot;
             wait_on(smem_u32(&bar.q_full[qs]), cq.phase, guard, kErrTimeoutLoad);
             cq.next(x.q_slots);
-            const uint64_t qa = q0 + (uint32_t)qs * kPair, da = qa + kTileBytes / 16;
+            const uint64_t qa = q0 + (uint32_t)qs * (3 * kTileBytes / 16), da = qa + kTileBytes / 16;
             for (int j = 0; j < w.tiles; ++j, ++kt, c.next(x.stages)) {
                 const int s = c.slot, cols = tile_cols(tile_keys(w.len, j));
                 wait_on(smem_u32(&bar.kv_full[s]), c.phase, guard, kErrTimeoutLoad);
@@ -274,6 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
         int kt = 0, lut_head = -1, luts = 0;
+        Cursor cq;
+        float lse_next = INFINITY;
+        if ((int)blockIdx.x < x.items) {
+            const Item w = item_of(blockIdx.x);
+            if (w.q0 + wt < p.n) lse_next = p.lse[((size_t)w.b * p.heads + w.h) * p.n + w.q0 + wt];
+        }
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
             if (kBias && w.h != lut_head) {
@@ -283,37 +290,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int i = w.q0 + wt;
             const bool in = i < p.n;
             const size_t row = ((size_t)w.b * p.heads + w.h) * p.n + i;
-            const float nl = neg_lse2(p.lse, row, in);
-            // dO . O of the tile's rows: 8 lanes per row, whole rows per load
-            if (w.tiles > 0) {
-                const __nv_bfloat16 *o = static_cast<const __nv_bfloat16 *>(p.O.p) + (long long)w.b * p.O.sb +
-                                         (long long)w.h * p.O.sh;
-                const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(p.dO.p) + (long long)w.b * p.dO.sb +
-                                         (long long)w.h * p.dO.sh;
-                const int c = 8 * (lane & 7);
-                uint4 a[2], b[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = w.q0 + 8 * warp + 4 * e + (lane >> 3);
-                    a[e] = b[e] = make_uint4(0, 0, 0, 0);
-                    if (r < p.n && c < p.d) {
-                        a[e] = *reinterpret_cast<const uint4 *>(o + (long long)r * p.O.st + c);
-                        b[e] = *reinterpret_cast<const uint4 *>(g + (long long)r * p.dO.st + c);
-                    }
+            const float nl = neg_lse2(lse_next);
+            {   // the next item's, as it is in memory (a use would wait for it)
+                const int next = it + gridDim.x;
+                lse_next = INFINITY;
+                if (next < x.items) {
+                    const Item y = item_of(next);
+                    if (y.q0 + wt < p.n) lse_next = p.lse[((size_t)y.b * p.heads + y.h) * p.n + y.q0 + wt];
                 }
+            }
+            // dO . O of the tile's rows, 8 lanes per row
+            if (w.tiles > 0) {
+                wait_on(smem_u32(&bar.q_full[cq.slot]), cq.phase, guard, kErrTimeoutLoad);
+                const uint32_t g_s = qd + (3 * cq.slot + 1) * kTileBytes, o_s = g_s + kTileBytes;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float v = bf16_lo(a[e].x) * bf16_lo(b[e].x);
-                    v = fmaf(bf16_hi(a[e].x), bf16_hi(b[e].x), v);
-                    v = fmaf(bf16_lo(a[e].y), bf16_lo(b[e].y), v);
-                    v = fmaf(bf16_hi(a[e].y), bf16_hi(b[e].y), v);
-                    v = fmaf(bf16_lo(a[e].z), bf16_lo(b[e].z), v);
-                    v = fmaf(bf16_hi(a[e].z), bf16_hi(b[e].z), v);
-                    v = fmaf(bf16_lo(a[e].w), bf16_lo(b[e].w), v);
-                    v = fmaf(bf16_hi(a[e].w), bf16_hi(b[e].w), v);
+                    const int r = 8 * warp + 4 * e + (lane >> 3);
+                    const uint32_t at = sw128_offset(r, lane & 7);
+                    uint4 a, b;
+                    ld_shared_v4(o_s + at, a.x, a.y, a.z, a.w);
+                    ld_shared_v4(g_s + at, b.x, b.y, b.z, b.w);
+                    float v = bf16_lo(a.x) * bf16_lo(b.x);
+                    v = fmaf(bf16_hi(a.x), bf16_hi(b.x), v);
+                    v = fmaf(bf16_lo(a.y), bf16_lo(b.y), v);
+                    v = fmaf(bf16_hi(a.y), bf16_hi(b.y), v);
+                    v = fmaf(bf16_lo(a.z), bf16_lo(b.z), v);
+                    v = fmaf(bf16_hi(a.z), bf16_hi(b.z), v);
+                    v = fmaf(bf16_lo(a.w), bf16_lo(b.w), v);
+                    v = fmaf(bf16_hi(a.w), bf16_hi(b.w), v);
 #pragma unroll
                     for (int m = 4; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-                    if ((lane & 7) == 0) rows_delta[8 * warp + 4 * e + (lane >> 3)] = v;
+                    if ((lane & 7) == 0) rows_delta[r] = v;
                 }
             }
             math_barrier();   // also: the strips of the previous item's delta have been read
@@ -379,24 +386,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if (strip == 0 && in) {
                 p.delta[row] = delta;
             }
-            float o[16];
-            if (w.tiles > 0) {
-                wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                uint32_t u[16];
-                tmem_ld16(tDq + 16 * strip + lanes, u);
-                tc_wait_ld();
-                tc_fence_before();
-#pragma unroll
-                for (int c = 0; c < 16; ++c) o[c] = __uint_as_float(u[c]);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 16; ++c) o[c] = 0.f;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.dQ) + (row - lane) * p.d + 16 * strip;
+            if (w.tiles == 0) {   // no key: no gradient
+                if (in && 16 * strip < p.d) {
+                    uint4 *z = reinterpret_cast<uint4 *>(out + (size_t)lane * p.d);
+                    z[0] = z[1] = make_uint4(0, 0, 0, 0);
+                }
+                continue;
             }
-            const int i0 = i - lane;
-            store_rows_bf16<16>(base + x.off_out + (uint32_t)warp * 1024u, o, p.scale,
-                                static_cast<__nv_bfloat16 *>(p.dQ) + (row - lane) * p.d + 16 * strip, p.d, p.n - i0,
-                                p.d - 16 * strip, lane);
+            wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
+            tc_fence_after();
+            float o[16];
+            tmem_ld16_nowait(tDq + 16 * strip + lanes, o);
+            tc_wait_ld();
+            tc_fence_before();
+            // staged where the item's O was: its last reader was delta, a barrier ago
+            store_rows_bf16<16>(qd + (3 * cq.slot + 2) * kTileBytes + (uint32_t)warp * 1024u, o, p.scale, out, p.d,
+                                p.n - (i - lane), p.d - 16 * strip, lane);
+            fence_proxy_async();
+            arrive_warp(&bar.q_empty[cq.slot], lane);
+            cq.next(x.q_slots);
         }
     }
     tc_fence_before();
@@ -946,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 struct Maps {
-    CUtensorMap q, d, k, v;
+    CUtensorMap q, d, k, v, o;
 };
 bool fill_maps(Maps &m, BwdParams &x, const Problem &p) {
     x.p = p;
@@ -960,7 +969,14 @@ bool fill_maps(Maps &m, BwdParams &x, const Problem &p) {
     x.div_group = fast_div(p.group);
     return make_map(&m.q, &x.uq, p.Q, p.B, p.heads, p.n, p.d) && make_map(&m.d, &x.ud, p.dO, p.B, p.heads, p.n, p.d) &&
            make_map(&m.k, &x.uk, p.K, p.B, p.kv_heads, p.m, p.d) &&
-           make_map(&m.v, &x.uv, p.V, p.B, p.kv_heads, p.m, p.d);
+           make_map(&m.v, &x.uv, p.V, p.B, p.kv_heads, p.m, p.d) && make_map(&m.o, &x.uo, p.O, p.B, p.heads, p.n, p.d);
+}
+
+template <auto kKernel>
+cudaError_t go_dq(const Maps &m, const BwdParams &x, int bytes, cudaStream_t s) {
+    cudaError_t e = allow_smem<kKernel>();
+    if (e != cudaSuccess) return e;
+    return launch_plain(kKernel, dim3((unsigned)std::min(x.items, sms())), kThreads, bytes, s, m.q, m.d, m.k, m.v, m.o, x);
 }
 
 template <auto kKernel>
@@ -975,15 +991,15 @@ cudaError_t go(const Maps &m, const BwdParams &x, int bytes, cudaStream_t s) {
 int tc_dkdv_splits(int B, int kv_heads, int group, int n, int m) {
     const long long items = (long long)B * kv_heads * ((m + kRows - 1) / kRows);
     const long long steps = (long long)group * ((n + kRows - 1) / kRows);
-    // fewer items than SMs: share the queries out, at least two tiles to each part
-    if (items >= 152 || steps < 4) return 1;
-    return (int)std::min<long long>((152 + items - 1) / items, steps / 2);
+    // at most half as many items as SMs: share the queries out in one round, at least two tiles to each part
+    if (2 * items > 152 || steps < 4) return 1;
+    return (int)std::min<long long>(152 / items, steps / 2);
 }
 
 int tc_dbias_splits(int B, int heads, int n, int m) {
     const long long items = (long long)heads * ((n + kRows - 1) / kRows) * ((m + kRows - 1) / kRows);
-    if (items >= 152 || B < 4) return 1;
-    return (int)std::min<long long>((152 + items - 1) / items, B / 2);
+    if (2 * items > 152 || B < 4) return 1;
+    return (int)std::min<long long>(152 / items, B / 2);
 }
 
 cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
@@ -1000,18 +1016,17 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     x.items = (int)items;
     x.first = 1;
     for (x.q_slots = 2;; --x.q_slots) {
-        const int left = kSmemBudget - 2 * x.q_slots * kTileBytes - kDqOut - lut - keys - 1024;
+        const int left = kSmemBudget - 3 * x.q_slots * kTileBytes - lut - keys - 1024;
         x.stages = std::min(kMaxStages, left / (2 * kTileBytes));
         if (x.stages >= 2 || x.q_slots == 1) break;
     }
     if (x.stages < 2) return cudaErrorInvalidValue;   // a K tile is held until its dQ product, behind the next scores
-    x.off_out = 2 * (x.q_slots + x.stages) * kTileBytes;
-    x.off_lut = x.off_out + kDqOut;
+    x.off_lut = (3 * x.q_slots + 2 * x.stages) * kTileBytes;
     x.off_aux = x.off_lut + lut;
     int bytes = x.off_aux + keys + 1024;
-    e = p.bias.mode == 0   ? go<tc_dq<0>>(m, x, bytes, s)
-        : p.bias.mode == 1 ? go<tc_dq<1>>(m, x, bytes, s)
-                           : go<tc_dq<2>>(m, x, bytes, s);
+    e = p.bias.mode == 0   ? go_dq<tc_dq<0>>(m, x, bytes, s)
+        : p.bias.mode == 1 ? go_dq<tc_dq<1>>(m, x, bytes, s)
+                           : go_dq<tc_dq<2>>(m, x, bytes, s);
     if (e != cudaSuccess) return e;
     // ---- dK, dV
     items = (long long)p.B * p.kv_heads * x.ktiles * p.q_splits;
