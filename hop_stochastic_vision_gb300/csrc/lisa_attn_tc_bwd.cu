@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // --------------------------------------------------------------------- dK, dV
 struct DkvBars {
-    uint64_t kv_full, kv_empty, q_full[kMaxStages], q_empty[kMaxStages];
+    uint64_t kv_full[2], kv_empty[2], q_full[kMaxStages], q_empty[kMaxStages];
     uint64_t aux_full[kMaxStages], aux_empty[kMaxStages];
     uint64_t full, free, w_full, w_done, lut_full;   // S and dP: there, in registers; P and dS: there, read
 };
@@ -440,14 +440,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Problem &p = x.p;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
-    const uint32_t kv = base, ring = base + 2 * kTileBytes;   // K, V; stages of (Q, dO)
+    const uint32_t kv = base, ring = base + 2 * x.q_slots * kTileBytes;   // slots of (K, V); stages of (Q, dO)
     float *lut = reinterpret_cast<float *>(sm + x.off_lut) + p.bias.pad;
     QueryAux *aux = reinterpret_cast<QueryAux *>(sm + x.off_aux);
     const Guard guard{x.err, &dead};
 
     if (tid == 0) {
-        mbar_init(smem_u32(&bar.kv_full), 1);
-        mbar_init(smem_u32(&bar.kv_empty), 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&bar.kv_full[t]), 1);
+            mbar_init(smem_u32(&bar.kv_empty[t]), 1);
+        }
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(smem_u32(&bar.q_full[s]), 1);
             mbar_init(smem_u32(&bar.q_empty[s]), 1);
@@ -517,16 +519,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kLoads) {
         if (lane == 0) {
             int n = 0, items = 0;
-            Cursor c;
+            Cursor c, ck;
             for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
                 const Item w = item_of(it);
                 if (w.u0 >= w.u1) continue;
-                if (items > 0) wait_on(smem_u32(&bar.kv_empty), (items - 1) & 1, guard, kErrTimeoutMma);
+                if (items >= x.q_slots) wait_on(smem_u32(&bar.kv_empty[ck.slot]), ck.phase ^ 1u, guard, kErrTimeoutMma);
                 ++items;
-                const uint32_t f = smem_u32(&bar.kv_full);
+                const uint32_t f = smem_u32(&bar.kv_full[ck.slot]), kv_at = kv + 2 * ck.slot * kTileBytes;
+                ck.next(x.q_slots);
                 mbar_arrive_expect_tx(f, 2 * kTileBytes);
-                load_rows(kv, &mk, x.uk, w.j0, w.g, w.b, f);
-                load_rows(kv + kTileBytes, &mv, x.uv, w.j0, w.g, w.b, f);
+                load_rows(kv_at, &mk, x.uk, w.j0, w.g, w.b, f);
+                load_rows(kv_at + kTileBytes, &mv, x.uv, w.j0, w.g, w.b, f);
                 for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
                     const int s = c.slot;
                     const uint32_t ph = c.phase;
@@ -542,20 +545,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < x.stages; ++s) {
                 drain(&bar.q_empty[s], uses_of(n, s, x.stages), x.err);
             }
-            drain(&bar.kv_empty, items, x.err);
+            for (int t = 0; t < x.q_slots; ++t) drain(&bar.kv_empty[t], uses_of(items, t, x.q_slots), x.err);
         }
         __syncwarp();
     } else if (warp == kFront) {
         // S^T and dP^T of each tile
-        int n = 0, items = 0;
-        Cursor c;
+        int n = 0;
+        Cursor c, ck;
         const uint64_t k0 = desc_rows(kv), v0 = desc_rows(kv + kTileBytes), q0 = desc_rows(ring),
                        d0 = desc_rows(ring + kTileBytes);
         for (int it = blockIdx.x; it < x.items; it += gridDim.x) {
             const Item w = item_of(it);
             if (w.u0 >= w.u1) continue;
-            wait_on(smem_u32(&bar.kv_full), items & 1, guard, kErrTimeoutLoad);
-            ++items;
+            const int ks = ck.slot;
+            wait_on(smem_u32(&bar.kv_full[ks]), ck.phase, guard, kErrTimeoutLoad);
+            ck.next(x.q_slots);
+            const uint64_t ka = k0 + (uint32_t)ks * kPair, va = v0 + (uint32_t)ks * kPair;
             int qt = w.u0;
             split(qt, x.div_qtiles);
             for (int u = w.u0; u < w.u1; ++u, ++n, c.next(x.stages)) {
@@ -565,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n > 0) wait_on(smem_u32(&bar.free), (n - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 if (elect_one()) {
-                    mma_rows_rows(tS, k0, q0 + (uint32_t)s * kPair, cols);
-                    mma_rows_rows(tD, v0, d0 + (uint32_t)s * kPair, cols);
+                    mma_rows_rows(tS, ka, q0 + (uint32_t)s * kPair, cols);
+                    mma_rows_rows(tD, va, d0 + (uint32_t)s * kPair, cols);
                     tc_commit(smem_u32(&bar.full));
-                    if (u == w.u1 - 1) tc_commit(smem_u32(&bar.kv_empty));
+                    if (u == w.u1 - 1) tc_commit(smem_u32(&bar.kv_empty[ks]));
                 }
                 __syncwarp();
             }
@@ -1036,9 +1041,13 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     x.splits = p.q_splits;
     x.div_splits = fast_div(x.splits);
     const int aux = (int)sizeof(QueryAux);
-    x.stages = std::min(kMaxStages, (kSmemBudget - 2 * kTileBytes - kDkvOut - lut - 1024) / (2 * kTileBytes + aux));
+    for (x.q_slots = 2;; --x.q_slots) {
+        const int left = kSmemBudget - 2 * x.q_slots * kTileBytes - kDkvOut - lut - 1024;
+        x.stages = std::min(kMaxStages, left / (2 * kTileBytes + aux));
+        if (x.stages >= 2 || x.q_slots == 1) break;
+    }
     if (x.stages < 2) return cudaErrorInvalidValue;
-    x.off_out = (2 + 2 * x.stages) * kTileBytes;
+    x.off_out = 2 * (x.q_slots + x.stages) * kTileBytes;
     x.off_lut = x.off_out + kDkvOut;
     x.off_aux = x.off_lut + lut;
     bytes = x.off_aux + x.stages * aux + 1024;
