@@ -98,7 +98,7 @@ __device__ __forceinline__ void tile_dot(const float *A, const float *B, int ty,
 // acc[r][c] += sum_k P[4 ty + r][k] V[k][tx + 16 c]   (P rows of kTile + 4)
 template <int D>
 __device__ __forceinline__ void tile_mul(const float *P, const float *V, int ty, int tx, float (&acc)[4][D / 16]) {
-#pragma unroll 2
+#pragma unroll (D == 16 ? 8 : 2)
     for (int k = 0; k < kTile; k += 4) {
         float4 p[4];
 #pragma unroll
@@ -135,10 +135,12 @@ __device__ __forceinline__ void tile_mul_t(const float *P, const float *X, int t
     }
 }
 
-__device__ __forceinline__ float half_max(float v) {
+// Maximum over the 16 threads of each of four rows, the rows' exchanges side by side.
+__device__ __forceinline__ void half_max(float (&v)[4]) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = fmaxf(v[r], __shfl_xor_sync(0xFFFFFFFFu, v[r], o));
 }
 __device__ __forceinline__ float half_sum(float v) {
 #pragma unroll
@@ -212,19 +214,22 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
         float s[4][4];
         tile_dot<D>(q_s, k_s, ty, tx, s);
         finish_scores(s, p, lut, j0, len, tx, oq);
+        float tile_top[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) tile_top[r] = fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]));
+        half_max(tile_top);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float t = fmaxf(top[r], half_max(fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]))));
+            const float t = fmaxf(top[r], tile_top[r]);
             const float ref = t == -INFINITY ? 0.f : t;   // a row of -inf scores so far: weights 0, not NaN
             const float old = __expf(top[r] - ref);
-            float w = 0.f;
+            sum[r] *= old;                                // this thread's columns; joined at the end
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float e = __expf(s[r][c] - ref);
-                w += e;
+                sum[r] += e;
                 p_s[(4 * ty + r) * (kTile + 4) + tx + 16 * c] = e;
             }
-            sum[r] = sum[r] * old + half_sum(w);
             top[r] = t;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) acc[r][c] *= old;
@@ -236,6 +241,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int i = i0 + 4 * ty + r;
+        sum[r] = half_sum(sum[r]);
         if (i >= p.n) continue;
         const float inv = sum[r] != 0.f ? 1.f / sum[r] : 0.f;
 #pragma unroll

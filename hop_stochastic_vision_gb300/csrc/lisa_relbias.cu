@@ -118,26 +118,37 @@ __global__ void __launch_bounds__(256) bias_grad_part(const __grid_constant__ Gr
     const int flat = tile * g.threads + t;
     const int r = flat / g.etot, e = q0 + flat % g.etot;
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-    for (int part = 0; part < g.parts; ++part, dbias += (size_t)g.b.heads * g.n * g.m) {
-        if (r >= g.residues) break;
+    if (r < g.residues) {
         const int nr = (g.q_cols - 1 - r) / g.step_c + 1;
         int q = max(q0, e - g.k_cols + 1);
         const int q1 = min(min(q0 + g.ch, nr), e + 1);
         // element (q): query column q_cols - 1 - r - s q, key column e - q
         const T *p = dbias + ((long long)h * g.n + (long long)rq * g.q_cols + (g.q_cols - 1 - r - (long long)g.step_c * q)) * g.m +
                      (long long)rk * g.k_cols + (e - q);
-        const long long step = -((long long)g.step_c * g.m + 1);
-        for (; q + 8 <= q1; q += 8) {
-            float v[8];
+        const long long step = -((long long)g.step_c * g.m + 1), matrix = (long long)g.b.heads * g.n * g.m;
+        if (g.parts == 1) {
+            for (; q + 8 <= q1; q += 8) {
+                float v[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = get(p + u * step);
-            a0 += v[0] + v[4];
-            a1 += v[1] + v[5];
-            a2 += v[2] + v[6];
-            a3 += v[3] + v[7];
-            p += 8 * step;
+                for (int u = 0; u < 8; ++u) v[u] = get(p + u * step);
+                a0 += v[0] + v[4];
+                a1 += v[1] + v[5];
+                a2 += v[2] + v[6];
+                a3 += v[3] + v[7];
+                p += 8 * step;
+            }
         }
-        for (; q < q1; ++q, p += step) a0 += get(p);
+        for (; q < q1; ++q, p += step) {   // the matrices side by side
+            for (int part = 0; part < g.parts; part += 8) {
+                float v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] = part + u < g.parts ? get(p + (part + u) * matrix) : 0.f;
+                a0 += v[0] + v[4];
+                a1 += v[1] + v[5];
+                a2 += v[2] + v[6];
+                a3 += v[3] + v[7];
+            }
+        }
     }
     diag[t] = (a0 + a1) + (a2 + a3);
     __syncthreads();
@@ -174,24 +185,31 @@ __global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ Gr
     float acc = 0.f;
     if (cb < g.col_buckets) {
         const size_t row = (size_t)g.col_buckets;
-        // the runs share out the rows of the query grid, or a sequence's items
-        const int by_row = g.q_rows > 1;
-        for (int rq = by_row ? grp : 0; rq < g.q_rows; rq += by_row ? groups : 1) {
-            // row offset step_r rk - rq - start_r in [lo, hi]
-            const long long base = (long long)rq + g.start_r;
-            const long long x0 = lo + base, x1 = hi + base;
-            const int k0 = x0 <= 0 ? 0 : (int)min((x0 + g.step_r - 1) / g.step_r, (long long)g.k_rows);
-            const int k1 = x1 < 0 ? -1 : (int)min(x1 / g.step_r, (long long)g.k_rows - 1);
-            if (k1 < k0) continue;
-            const float *p = g.part + (((size_t)h * g.q_rows + rq) * g.k_rows + k0) * per * row + cb;
-            const int items = (k1 - k0 + 1) * per, by = by_row ? 1 : groups;
-            int it = by_row ? 0 : grp;
-            float a[4] = {0.f, 0.f, 0.f, 0.f};
-            for (; it + 3 * by < items; it += 4 * by) {
+        // the runs share out the rows of the query grid (four at a time, their first items side by side), or a
+        // sequence's items
+        const int by_row = g.q_rows > 1, by = by_row ? 1 : groups;
+        for (int rq0 = by_row ? grp : 0; rq0 < g.q_rows; rq0 += by_row ? 4 * groups : 1) {
+            const float *p[4];
+            int items[4];
+            float a[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) a[u] += p[(size_t)(it + u * by) * row];
+            for (int u = 0; u < 4; ++u) {
+                // row offset step_r rk - rq - start_r in [lo, hi]
+                const int rq = rq0 + u * groups;
+                const long long base = (long long)rq + g.start_r;
+                const long long x0 = lo + base, x1 = hi + base;
+                const int k0 = x0 <= 0 ? 0 : (int)min((x0 + g.step_r - 1) / g.step_r, (long long)g.k_rows);
+                const int k1 = x1 < 0 ? -1 : (int)min(x1 / g.step_r, (long long)g.k_rows - 1);
+                items[u] = (u == 0 || by_row) && rq < g.q_rows && k1 >= k0 ? (k1 - k0 + 1) * per : 0;
+                p[u] = g.part + (((size_t)h * g.q_rows + rq) * g.k_rows + k0) * per * row + cb;
+                const int first = by_row ? 0 : grp;
+                a[u] = first < items[u] ? p[u][(size_t)first * row] : 0.f;
             }
-            for (; it < items; it += by) a[0] += p[(size_t)it * row];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll 4
+                for (int it = (by_row ? 0 : grp) + by; it < items[u]; it += by) a[u] += p[u][(size_t)it * row];
+            }
             acc += (a[0] + a[1]) + (a[2] + a[3]);
         }
     }
