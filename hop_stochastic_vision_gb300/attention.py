@@ -138,8 +138,8 @@ class RelativeBias:
     of ``k_grid``; a sequence is a grid of one row.  Query (r, c) stands at
     ``query_start`` + (r, c), key (r, c) at (key_step[0] r, key_step[1] c).
     ``query_start`` may be an int32 CUDA tensor [B]: each batch entry's own
-    start on a sequence (forward only).  The table may be updated in place
-    between calls; the object keeps no copy of it."""
+    start on a sequence (forward only).  The table may be updated between calls;
+    the object keeps no copy of it."""
 
     def __init__(self, table: torch.Tensor, q_grid, k_grid, rows: lisa_axis_rule = None,
                  cols: lisa_axis_rule = None, key_step=(1, 1), query_start=(0, 0)):
@@ -152,7 +152,6 @@ class RelativeBias:
             raise ValueError("the bias table has %d rows, the rules give %d buckets"
                              % (table.shape[0], rows.buckets * cols.buckets))
         self.table = table
-        self.index = table.get_device()
         self.heads = int(table.shape[1])
         self.q_grid = (int(q_grid[0]), int(q_grid[1]))
         self.k_grid = (int(k_grid[0]), int(k_grid[1]))
@@ -167,8 +166,25 @@ class RelativeBias:
             self.starts = query_start
         else:
             start = (int(query_start[0]), int(query_start[1]))
-        self.struct = lisa_rel_bias(table.data_ptr(), *self.q_grid, *self.k_grid, int(key_step[0]), int(key_step[1]),
-                                    *start, None if self.starts is None else self.starts.data_ptr(), rows, cols)
+        self.struct = lisa_rel_bias(None, *self.q_grid, *self.k_grid, int(key_step[0]), int(key_step[1]), *start,
+                                    None, rows, cols)
+        self.current()
+
+    def current(self) -> lisa_rel_bias:
+        """The C struct, with the table and the starts where they are now (an
+        optimiser or a module may have moved the storage behind them)."""
+        s, table = self.struct, self.table
+        if table.data_ptr() != s.table:
+            rows = s.rows.buckets * s.cols.buckets
+            if not (table.is_cuda and table.dtype == torch.float32 and table.is_contiguous()
+                    and table.shape == (rows, self.heads)):
+                raise ValueError("the bias table must stay a contiguous fp32 CUDA tensor [%d, %d]" % (rows, self.heads))
+            s.table = table.data_ptr()
+            self.index = table.get_device()
+        if self.starts is not None and self.starts.data_ptr() != s.starts:
+            s.starts = self.starts.data_ptr()
+        return s
+
 
 def _raw_stream(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
@@ -239,7 +255,7 @@ def _plain_bytes(B, heads, kv_heads, n, m, d, dtype):
 
 @functools.lru_cache(maxsize=64)
 def _default_scale(d):
-    return 1.0 / math.sqrt(d)
+    return 1.0 / math.sqrt(d) if d > 0 else 1.0   # a width of 0 is refused by the call
 
 
 def _strides(t, shape, dtype, index) -> lisa_strides:
@@ -273,6 +289,7 @@ def _prepare(q, k, v, kv_lens, bias, scale):
             raise ValueError("kv_lens must be a contiguous int32 CUDA tensor [B]")
         lens = kv_lens.data_ptr()
     if bias is not None:
+        struct = bias.current()
         if bias.index != index:
             raise ValueError("tensors must be on one device")
         if (bias.heads, bias.n, bias.m) != (heads, n, m):
@@ -280,7 +297,6 @@ def _prepare(q, k, v, kv_lens, bias, scale):
                              % (bias.heads, bias.n, bias.m, heads, n, m))
         if bias.starts is not None and bias.starts.shape[0] != B:
             raise ValueError("query_start must have one entry per batch entry")
-        struct = bias.struct
     tail = (B, heads, kv_heads, n, m, d, _default_scale(d) if scale is None else float(scale), lens, struct, dt)
     return index, shape, kv_shape, (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs), tail
 
@@ -372,6 +388,7 @@ def relative_bias(bias: RelativeBias, dtype: torch.dtype = torch.float32, *, out
         raise ValueError("dtype must be float32 or bfloat16")
     if bias.starts is not None:
         raise ValueError("a bias with a start for each batch entry has no matrix")
+    bias.current()
     if out is not None and not (out.get_device() == bias.index and out.dtype == dtype and out.is_contiguous()
                                 and out.shape == (bias.heads, bias.n, bias.m)):
         raise ValueError("out must be a contiguous %s CUDA tensor [heads, n, m]" % (dtype,))
@@ -396,6 +413,7 @@ def relative_bias_backward(bias: RelativeBias, dbias: torch.Tensor, *, workspace
     [heads, n, m] (fp32 or bf16) over the pairs of each bucket."""
     if bias.starts is not None:
         raise ValueError("a bias with a start for each batch entry has no matrix")
+    bias.current()
     if not (dbias.get_device() == bias.index and dbias.dtype in _DTYPES and dbias.is_contiguous()
             and dbias.shape == (bias.heads, bias.n, bias.m)):
         raise ValueError("dbias must be a contiguous fp32 or bf16 CUDA tensor [heads, n, m]")

@@ -87,6 +87,7 @@ struct Problem {
     int dtype;
     BiasDev bias;
     void *dQ, *dK, *dV;
+    int *err;              // fp32 backward: the workspace's error word, cleared
     float *delta;          // [B][heads][n]: sum_j p dP, written by the dQ kernel
     // dS summed over (parts of) the batch: folded tile by tile, or as matrices
     int folded;

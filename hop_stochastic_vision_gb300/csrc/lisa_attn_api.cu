@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kMaxTokens = 1 << 22;      // queries or keys of one head
 constexpr int kMaxGridDim = 65535;       // batch entries and heads
+constexpr long long kMaxItems = 1LL << 28;
 constexpr int kMaxDistance = 8191;
 constexpr long long kMaxPosition = 1LL << 28;
 constexpr size_t kAlign = 256;
@@ -128,18 +129,30 @@ lisa_status check_sizes(int B, int heads, int kv_heads, int n, int m, int d, int
     if (d < 1 || (heads > 0 && (kv_heads < 1 || heads % kv_heads != 0))) return LISA_ERR_INVALID_ARG;
     if (d != 16 && d != 32 && d != 64) return LISA_ERR_UNSUPPORTED;
     if (n > kMaxTokens || m > kMaxTokens || B > kMaxGridDim || heads > kMaxGridDim) return LISA_ERR_UNSUPPORTED;
+    // work items of 64 rows or more, shared out by ints
+    if ((long long)B * heads * (n / 64 + 1) > kMaxItems || (long long)B * kv_heads * (m / 64 + 1) > kMaxItems)
+        return LISA_ERR_UNSUPPORTED;
     return LISA_OK;
 }
 
 // Strides of a [B][heads][tokens][d] tensor: multiples of 16 bytes, tokens of a
-// head apart, extents within 63 bits.  `out`: no stride repeats an entry.
+// head apart, extents within 63 bits.  `out`: no two elements in one place.
 bool good_strides(const lisa_strides *s, int B, int heads, int tokens, int d, size_t esz, bool out) {
     if (!s) return false;
     const long long q = 16 / (long long)esz, most = 1LL << 38;
     for (const long long x : {s->batch, s->head, s->token})
         if (x < 0 || x > most || x % q != 0) return false;
     if (tokens > 1 && s->token < d) return false;
-    if (out && ((B > 1 && s->batch < d) || (heads > 1 && s->head < d))) return false;
+    if (!out) return true;
+    // the axes from the narrowest stride up: each steps over all of the ones below
+    struct Axis { long long stride; int count; } ax[3] = {{s->batch, B}, {s->head, heads}, {s->token, tokens}};
+    std::sort(ax, ax + 3, [](const Axis &a, const Axis &b) { return a.stride < b.stride; });
+    long long inner = d;
+    for (const Axis &a : ax) {
+        if (a.count <= 1) continue;
+        if (a.stride < inner) return false;
+        inner += a.stride * (a.count - 1);
+    }
     return true;
 }
 
@@ -152,7 +165,7 @@ size_t extent(const lisa_strides *s, int B, int heads, int tokens, int d, size_t
 struct Span {
     uintptr_t lo, hi;
     Span(const void *p, size_t bytes) : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + bytes) {}
-    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
+    bool meets(const Span &o) const { return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi; }
 };
 
 // Shared by the forward and the backward: everything but the outputs.
@@ -268,10 +281,12 @@ size_t table_floats(const lisa_rel_bias &b, int heads) {
     return (size_t)b.rows.buckets * (size_t)b.cols.buckets * (size_t)heads;
 }
 
-// Pairs of one head that the bias matrix and its gradient index with 32 bits.
-bool matrix_fits(const lisa_rel_bias &b) {
-    return (long long)b.q_rows * b.q_cols * ((long long)b.k_rows * b.k_cols) <= (1LL << 31) - 1 - 65536 &&
-           (long long)b.q_rows * b.k_rows <= kMaxGridDim;
+// Pairs of one head that the bias matrix and its gradient index with 32 bits,
+// and tiles of all heads that they share out.
+bool matrix_fits(const lisa_rel_bias &b, int heads) {
+    const long long n = (long long)b.q_rows * b.q_cols, m = (long long)b.k_rows * b.k_cols;
+    return n * m <= (1LL << 31) - 1 - 65536 && (long long)b.q_rows * b.k_rows <= kMaxGridDim &&
+           heads * ((n + 127) / 128) * ((m + 127) / 128) <= kMaxItems;
 }
 
 }  // namespace
@@ -285,7 +300,7 @@ extern "C" lisa_status lisa_relative_bias(const lisa_rel_bias *bias, int heads, 
     BiasDev dev;
     const lisa_status st = bias_dev(bias, heads, dev);
     if (st != LISA_OK) return st;
-    if (!matrix_fits(*bias)) return LISA_ERR_UNSUPPORTED;
+    if (!matrix_fits(*bias, heads)) return LISA_ERR_UNSUPPORTED;
     if (!bias->table || !out || bias->starts || !aligned16(out)) return LISA_ERR_INVALID_ARG;
     const size_t bytes = (size_t)heads * bias->q_rows * bias->q_cols * bias->k_rows * bias->k_cols *
                          (dtype == LISA_BF16 ? 2 : 4);
@@ -295,7 +310,7 @@ extern "C" lisa_status lisa_relative_bias(const lisa_rel_bias *bias, int heads, 
 
 extern "C" size_t lisa_relative_bias_backward_workspace_bytes(const lisa_rel_bias *bias, int heads) {
     BiasDev dev;
-    if (bias_dev(bias, heads, dev) != LISA_OK || !matrix_fits(*bias)) return 0;
+    if (bias_dev(bias, heads, dev) != LISA_OK || !matrix_fits(*bias, heads)) return 0;
     return bias_grad_bytes(*bias, heads);
 }
 
@@ -306,7 +321,7 @@ extern "C" lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, in
     BiasDev dev;
     const lisa_status st = bias_dev(bias, heads, dev);
     if (st != LISA_OK) return st;
-    if (!matrix_fits(*bias)) return LISA_ERR_UNSUPPORTED;
+    if (!matrix_fits(*bias, heads)) return LISA_ERR_UNSUPPORTED;
     if (!dbias || !dtable || bias->starts || !aligned16(dbias) || (reinterpret_cast<uintptr_t>(dtable) & 3u) != 0)
         return LISA_ERR_INVALID_ARG;
     const size_t bytes = (size_t)heads * bias->q_rows * bias->q_cols * bias->k_rows * bias->k_cols *
@@ -340,11 +355,16 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
     const size_t esz = dtype == LISA_BF16 ? 2 : 4;
     if (!O || !aligned16(O) || !good_strides(o_strides, B, heads, n, d, esz, true)) return LISA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return LISA_ERR_INVALID_ARG;
-    const Span o(O, extent(o_strides, B, heads, n, d, esz));
-    if (o.meets(Span(Q, extent(q_strides, B, heads, n, d, esz)))) return LISA_ERR_INVALID_ARG;
-    if (m > 0 && (o.meets(Span(K, extent(k_strides, B, kv_heads, m, d, esz))) ||
-                  o.meets(Span(V, extent(v_strides, B, kv_heads, m, d, esz)))))
-        return LISA_ERR_INVALID_ARG;
+    const Span outs[2] = {Span(O, extent(o_strides, B, heads, n, d, esz)), Span(lse, lse ? (size_t)B * heads * n * 4 : 0)};
+    const Span ins[5] = {Span(Q, extent(q_strides, B, heads, n, d, esz)),
+                         Span(K, m > 0 ? extent(k_strides, B, kv_heads, m, d, esz) : 0),
+                         Span(V, m > 0 ? extent(v_strides, B, kv_heads, m, d, esz) : 0),
+                         Span(kv_lens, kv_lens ? (size_t)B * 4 : 0),
+                         Span(bias ? bias->table : nullptr, p.bias.mode ? table_floats(*bias, heads) * 4 : 0)};
+    if (outs[0].meets(outs[1])) return LISA_ERR_INVALID_ARG;
+    for (const Span &x : outs)
+        for (const Span &in : ins)
+            if (x.meets(in)) return LISA_ERR_INVALID_ARG;
     p.O = {O, o_strides->batch, o_strides->head, o_strides->token};
     p.lse = lse;
     const FwdPlan pl = forward_plan(B, heads, p.group, n, m, d, dtype, p.bias);
@@ -374,7 +394,7 @@ extern "C" size_t lisa_cross_attention_backward_workspace_bytes(int B, int heads
     if (B == 0 || heads == 0 || n == 0 || m == 0) return 0;
     if (bias) {
         BiasDev dev;
-        if (bias_dev(bias, heads, dev) != LISA_OK || !matrix_fits(*bias)) return 0;
+        if (bias_dev(bias, heads, dev) != LISA_OK || !matrix_fits(*bias, heads)) return 0;
     }
     return backward_plan(B, heads, kv_heads, n, m, d, bias, dtype).total;
 }
@@ -416,12 +436,13 @@ extern "C" lisa_status lisa_cross_attention_backward(
         return LISA_ERR_INVALID_ARG;
     const Span outs[4] = {Span(dQ, dq_bytes), Span(dK, dk_bytes), Span(dV, dk_bytes),
                           Span(dtable, bias ? table_floats(*bias, heads) * 4 : 0)};
-    const Span ins[7] = {Span(Q, extent(q_strides, B, heads, n, d, esz)),
+    const Span ins[8] = {Span(Q, extent(q_strides, B, heads, n, d, esz)),
                          Span(K, extent(k_strides, B, kv_heads, m, d, esz)),
                          Span(V, extent(v_strides, B, kv_heads, m, d, esz)),
                          Span(O, extent(o_strides, B, heads, n, d, esz)),
                          Span(dO, extent(do_strides, B, heads, n, d, esz)),
                          Span(lse, (size_t)B * heads * n * 4),
+                         Span(kv_lens, kv_lens ? (size_t)B * 4 : 0),
                          Span(bias ? bias->table : nullptr, bias ? table_floats(*bias, heads) * 4 : 0)};
     for (int a = 0; a < (bias ? 4 : 3); ++a) {
         for (const Span &in : ins)
@@ -429,7 +450,7 @@ extern "C" lisa_status lisa_cross_attention_backward(
         for (int c = 0; c < a; ++c)
             if (outs[a].meets(outs[c])) return LISA_ERR_INVALID_ARG;
     }
-    if (bias && !matrix_fits(*bias)) return LISA_ERR_UNSUPPORTED;
+    if (bias && !matrix_fits(*bias, heads)) return LISA_ERR_UNSUPPORTED;
     const BwdPlan pl = backward_plan(B, heads, kv_heads, n, m, d, bias, dtype);
     if (!workspace || workspace_bytes < pl.total) return LISA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
@@ -440,6 +461,7 @@ extern "C" lisa_status lisa_cross_attention_backward(
     p.dK = dK;
     p.dV = dV;
     char *ws = static_cast<char *>(workspace);
+    p.err = reinterpret_cast<int *>(ws);
     p.delta = reinterpret_cast<float *>(ws + pl.off_delta);
     p.q_splits = pl.q_splits;
     p.dk_part = reinterpret_cast<float *>(ws + pl.off_dk);

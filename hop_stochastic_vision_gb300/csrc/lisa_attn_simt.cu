@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int i0 = blockIdx.x * kTile, h = blockIdx.y, b = blockIdx.z, kvh = h / p.group;
     const int len = valid_keys(p, b);
-    if (p.bias.mode) fill_offsets(p.bias, h, 1.f, lut, tid, kThreads);
+    if (p.bias.mode) fill_offsets<true>(p.bias, h, lut, tid, kThreads);
     load_tile<T, D>(slice<T>(p.Q, b, h), p.Q.st, i0, p.n, q_s, tid);
     int oq[4];
     const int start = p.bias.mode ? bias_start(p.bias, b) : 0;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
 // p_ij = exp(s_ij - lse_i); rows without a valid key (lse = -inf) give 0.
 __device__ __forceinline__ float row_ref(const float *lse, size_t at, bool in) {
     const float l = in ? lse[at] : INFINITY;
-    return l == -INFINITY ? INFINITY : l;
+    return fabsf(l) > kMaxLse ? INFINITY : l;
 }
 
 template <typename T, int D>
@@ -266,7 +266,8 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int i0 = blockIdx.x * kTile, h = blockIdx.y, b = blockIdx.z, kvh = h / p.group;
     const int len = valid_keys(p, b);
-    if (p.bias.mode) fill_offsets(p.bias, h, 1.f, lut, tid, kThreads);
+    if (i0 == 0 && h == 0 && b == 0 && tid == 0) *p.err = 0;   // these kernels have no wait that could give up
+    if (p.bias.mode) fill_offsets<true>(p.bias, h, lut, tid, kThreads);
     // delta~_i = dO_i . O_i from the forward's (rounded) output
     load_tile<T, D>(slice<T>(p.O, b, h), p.O.st, i0, p.n, q_s, tid);
     load_tile<T, D>(slice<T>(p.dO, b, h), p.dO.st, i0, p.n, o_s, tid);
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kThreads) simt_dkdv(const __grid_constant__ Pr
             const int h = kvh * p.group + g;
             const size_t row0 = ((size_t)b * p.heads + h) * p.n;
             __syncthreads();
-            if (p.bias.mode) fill_offsets(p.bias, h, 1.f, lut, tid, kThreads);
+            if (p.bias.mode) fill_offsets<true>(p.bias, h, lut, tid, kThreads);
             Rows<D> qr, dr;
             qr.load(slice<T>(p.Q, b, h), p.Q.st, 0, p.n, tid);
             dr.load(slice<T>(p.dO, b, h), p.dO.st, 0, p.n, tid);
@@ -407,8 +408,10 @@ __global__ void __launch_bounds__(kThreads) simt_dbias(const __grid_constant__ P
     float *k_s = sm, *v_s = k_s + tile_floats<D>(), *q_s = v_s + tile_floats<D>(), *o_s = q_s + tile_floats<D>();
     float *lut = o_s + tile_floats<D>();
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const int j0 = blockIdx.x * kTile, i0 = blockIdx.y * kTile, h = blockIdx.z, kvh = h / p.group;
-    fill_offsets(p.bias, h, 1.f, lut, tid, kThreads);
+    const int jtiles = (p.m + kTile - 1) / kTile;   // both in x: up to 65536 tiles of queries
+    const int j0 = (int)(blockIdx.x % jtiles) * kTile, i0 = (int)(blockIdx.x / jtiles) * kTile;
+    const int h = blockIdx.z, kvh = h / p.group;
+    fill_offsets<true>(p.bias, h, lut, tid, kThreads);
     float acc[4][4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -472,7 +475,7 @@ struct Simt {
         return run<simt_dkdv<T, D>>(dim3(tiles(p.m), p.kv_heads, p.B), 4 * t + 2 * kWeights, p, s);
     }
     static cudaError_t dbias(const Problem &p, cudaStream_t s) {
-        return run<simt_dbias<T, D>>(dim3(tiles(p.m), tiles(p.n), p.heads), 4 * t, p, s);
+        return run<simt_dbias<T, D>>(dim3(tiles(p.m) * tiles(p.n), 1, p.heads), 4 * t, p, s);
     }
 };
 

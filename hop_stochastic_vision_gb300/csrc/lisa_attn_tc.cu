@@ -479,7 +479,6 @@ cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {
     x.qtiles = (p.n + 2 * kRows - 1) / (2 * kRows);
     x.splits = p.splits;
     const long long items = (long long)p.B * p.heads * x.qtiles * x.splits;
-    if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
     x.items = (int)items;
     x.div_splits = fast_div(x.splits);
     x.div_qtiles = fast_div(x.qtiles);

@@ -8,6 +8,8 @@
 // which add nothing to any product; only d columns are stored.
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -294,11 +296,12 @@ inline bool make_map(CUtensorMap *m, MapUse *u, const Tensor &t, int B, int head
 }
 
 inline int sms() {
-    static int n[64];
+    static std::atomic<int> n[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-    if (n[dev] == 0) n[dev] = sm_count();
-    return n[dev];
+    int v = n[dev].load(std::memory_order_relaxed);
+    if (v == 0) n[dev].store(v = sm_count(), std::memory_order_relaxed);
+    return v;
 }
 
 constexpr int kSmemBudget = 227 * 1024 - 2048;   // dynamic: behind the barriers

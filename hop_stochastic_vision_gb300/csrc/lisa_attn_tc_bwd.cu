@@ -56,7 +56,7 @@ __device__ __forceinline__ int tile_keys(int len, int t) { return min(kRows, len
 __device__ __forceinline__ int tile_cols(int keys) { return (keys + 15) & ~15; }
 
 __device__ __forceinline__ float neg_lse2(float l) {
-    return l == -INFINITY ? -INFINITY : -l * kLog2e;   // rows without keys: every weight 2^-inf = 0
+    return fabsf(l) > kMaxLse ? -INFINITY : -l * kLog2e;   // rows without keys among them: every weight 2^-inf = 0
 }
 __device__ __forceinline__ float neg_lse2(const float *lse, size_t at, bool in) { return neg_lse2(in ? lse[at] : INFINITY); }
 
@@ -1017,7 +1017,6 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     cudaError_t e;
     // ---- dQ and delta
     long long items = (long long)p.B * p.heads * x.qtiles;
-    if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
     x.items = (int)items;
     x.first = 1;
     for (x.q_slots = 2;; --x.q_slots) {
@@ -1035,7 +1034,6 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // ---- dK, dV
     items = (long long)p.B * p.kv_heads * x.ktiles * p.q_splits;
-    if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
     x.items = (int)items;
     x.first = 0;
     x.splits = p.q_splits;
@@ -1063,7 +1061,6 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     if (p.bias.mode == 0) return cudaSuccess;
     // ---- dS of the batch
     items = (long long)p.heads * x.qtiles * x.ktiles * p.b_splits;
-    if (items > 0x3FFFFFFF) return cudaErrorInvalidValue;
     x.items = (int)items;
     x.splits = p.b_splits;
     x.div_splits = fast_div(x.splits);

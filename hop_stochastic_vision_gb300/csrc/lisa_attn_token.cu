@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_attention(const __grid_co
         const int total = (h1 - h0 + 1) * lutn;
         for (int e = tid; e < total; e += kTokenThreads) {
             const int hh = e / lutn, o = e - hh * lutn;
-            lut[e] = __ldg(p.bias.table + (size_t)entry_bucket(p.bias, lut0 + o) * p.bias.heads + h0 + hh) * kLog2e;
+            lut[e] = masked_entry(__ldg(p.bias.table + (size_t)entry_bucket(p.bias, lut0 + o) * p.bias.heads + h0 + hh)) * kLog2e;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) off[e] = (min(head[e], h1) - h0) * lutn;

@@ -70,9 +70,15 @@ __device__ __forceinline__ int entry_bucket(const BiasDev &b, int e) {
     return axis_bucket(b.rows, dr) * b.col_buckets + axis_bucket(b.cols, dc);
 }
 
-// The head's bias of every offset, times `mul`, into shared memory; eight loads
-// in flight per thread (one at a time took 15 us for 12480 offsets).
-__device__ __forceinline__ void fill_offsets(const BiasDev &b, int head, float mul, float *out, int tid, int nthreads) {
+// Entries of -2^120 and less, the types' lowest values among them, mask as -inf
+// does: in units of log2(e) they would overflow to it, or not, path by path.
+__device__ __forceinline__ float masked_entry(float v) { return v <= -0x1p120f ? -INFINITY : v; }
+
+// The head's bias of every offset into shared memory, as scores (kMask) or as
+// it stands; eight loads in flight per thread (one at a time took 15 us for
+// 12480 offsets).
+template <bool kMask>
+__device__ __forceinline__ void fill_offsets(const BiasDev &b, int head, float *out, int tid, int nthreads) {
     const float *t = b.table + head;
     for (int e0 = tid; e0 < b.entries; e0 += 8 * nthreads) {
         float v[8];
@@ -81,9 +87,13 @@ __device__ __forceinline__ void fill_offsets(const BiasDev &b, int head, float m
             v[u] = e0 + u * nthreads < b.entries ? __ldg(t + (size_t)entry_bucket(b, e0 + u * nthreads) * b.heads) : 0.f;
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-            if (e0 + u * nthreads < b.entries) out[e0 + u * nthreads] = v[u] * mul;
+            if (e0 + u * nthreads < b.entries) out[e0 + u * nthreads] = kMask ? masked_entry(v[u]) : v[u];
     }
 }
+
+// Beyond this |lse| the weights can no longer be had from fp32 scores and lse
+// (their last places are 1/8 and more): such a row gives no gradient.
+constexpr float kMaxLse = 0x1p20f;
 
 // Offset index of a pair: off_key(j) - off_query(i), then clamped to the table
 // (sequence) or inside it by construction (grid).

@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kDenseThreads) bias_dense(BiasDev b, T *out, i
     chain_begin();
     constexpr int kVec = 16 / (int)sizeof(T);
     const int h = blockIdx.y, tid = threadIdx.x;
-    fill_offsets(b, h, 1.f, lut, tid, kDenseThreads);
+    fill_offsets<false>(b, h, lut, tid, kDenseThreads);
     __syncthreads();
     const unsigned count = (unsigned)n * (unsigned)m;
     T *base = out + (size_t)h * count;
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(128) bias_offsets(BiasDev b, float *out) {
     for (int u = 0; u < 4; ++u) v[u] = in && h0 + u < b.heads ? row[h0 + u] : 0.f;
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-        if (h0 + u < b.heads) out[(size_t)(h0 + u) * b.offsets_pitch + at] = v[u] * 1.4426950408889634f;
+        if (h0 + u < b.heads) out[(size_t)(h0 + u) * b.offsets_pitch + at] = masked_entry(v[u]) * 1.4426950408889634f;
 }
 
 // ---------------------------------------------------------------- gradient
@@ -155,17 +155,19 @@ __global__ void __launch_bounds__(256) bias_grad_part(const __grid_constant__ Gr
     float *out = g.part + ((((size_t)h * g.q_rows + rq) * g.k_rows + rk) * (g.nchunk * g.ntile) + blockIdx.x) *
                               (size_t)g.col_buckets;
     const int last = g.step_c * (g.k_cols - 1) + g.q_cols - 1;   // offsets run over o = 0 .. last
-    const int shift = g.q_cols - 1 + g.start_c;
+    const int shift = g.q_cols - 1 + g.start_c, first = tile * g.threads;
     for (int cb = t; cb < g.col_buckets; cb += g.threads) {
         int lo, hi;
         bucket_range(g.b.cols, cb, lo, hi);
-        // offsets of this chunk: e in [q0, q0 + etot)
-        const int o0 = max(max(lo + shift, 0), g.step_c * q0);
-        const int o1 = min(min(hi + shift, last), g.step_c * (q0 + g.etot) - 1);
+        const int o0 = max(lo + shift, 0), o1 = min(hi + shift, last);
         float s = 0.f;
-        for (int o = o0; o <= o1; ++o) {
-            const int rr = o % g.step_c, at = rr * g.etot + o / g.step_c - q0 - tile * g.threads;
-            if (rr < g.residues && at >= 0 && at < g.threads) s += diag[at];
+        // of each residue that the tile holds, the run of e whose offsets s e + r are in [o0, o1]
+        for (int rr = first / g.etot; rr < g.residues && rr * g.etot < first + g.threads; ++rr) {
+            const int row = rr * g.etot - first;
+            int e0 = max(0, -row), e1 = min(g.etot, g.threads - row) - 1;
+            e0 = max(e0, (o0 <= rr ? 0 : (o0 - rr - 1) / g.step_c + 1) - q0);
+            e1 = min(e1, (o1 < rr ? -1 : (o1 - rr) / g.step_c) - q0);
+            for (int e = e0; e <= e1; ++e) s += diag[row + e];
         }
         out[cb] = s;
     }

@@ -26,17 +26,24 @@
  *     bf16) with fp32 accumulation, except that the bias gradient sums the
  *     unrounded dS.  Softmax statistics and every sum are fp32 or wider, in a
  *     fixed order: the same call gives the same bits.
- *   - d is 16, 32 or 64.  n and m are any lengths, 0 and 1 among them.
+ *   - d is 16, 32 or 64.  n and m are any lengths from 0 to 2^22, B and heads
+ *     at most 65535, with B heads (n / 64 + 1) and B kv_heads (m / 64 + 1) at
+ *     most 2^28; what is larger is LISA_ERR_UNSUPPORTED.
  *   - A tensor [B][heads][tokens][d] is given as a pointer and its strides in
  *     elements; the d elements of a token are contiguous.  Pointers and strides
  *     are multiples of 16 bytes.  A batch or head stride of 0 repeats one entry
- *     (inputs only).  Tokens of one head may not overlap.
+ *     (inputs only).  Tokens of one head may not overlap, nor any two
+ *     elements of an output: each of its strides has to step over the axes of
+ *     smaller strides.
  *   - kv_lens (device int32 [B], or NULL for m everywhere) says how many keys of
  *     a batch entry are valid; a value outside 0..m counts as the nearer end.
  *     Keys and values behind it are never used, whatever they hold (NaN
  *     included); their dK and dV are written as 0.
- *   - A row without any key that counts (length 0, or only -inf scores) has
+ *   - A row without any key that counts (length 0, or only masked scores) has
  *     o = 0, lse = -inf and gives no gradient.
+ *   - The backward takes p from fp32 scores and lse, so p is good to about
+ *     |lse| 2^-23 relative; a row of |lse| > 2^20, as only masks of large finite
+ *     numbers over a whole row bring it about, gives no gradient.
  *   - The library allocates no device memory.  Every argument is checked on the
  *     host before anything is launched.  Calls are asynchronous on `stream`
  *     (make its device current), never synchronise, and can be captured.  A
@@ -81,7 +88,8 @@ typedef struct lisa_axis_rule {
  * Query (r, c) stands at (start_rows + r, start_cols + c), key (r, c) at
  * (key_step_rows r, key_step_cols c): keys pooled by s have step s.
  *   table   device fp32 [rows.buckets * cols.buckets][heads]; the pair's row is
- *           row_bucket * cols.buckets + column_bucket.  -inf entries mask.
+ *           row_bucket * cols.buckets + column_bucket.  Entries of -inf, and of
+ *           -2^120 or less (a type's lowest value), mask a pair in the attention.
  *   starts  device int32 [B], or NULL: a column start of each batch entry that
  *           replaces start_cols (a token of each sequence at its own position).
  *           Sequences only, and forward only (serving): the bias matrix, its
@@ -104,7 +112,9 @@ typedef struct lisa_rel_bias {
 
 /*
  * The bias matrix: out [heads][n][m] (contiguous, dtype), out[h][i][j] =
- * table[bucket(i, j)][h], rounded once.
+ * table[bucket(i, j)][h], rounded once.  It, its gradient and the attention's
+ * backward with a bias take n m < 2^31 - 65536, q_rows k_rows <= 65535 and
+ * heads ceil(n / 128) ceil(m / 128) <= 2^28 (else LISA_ERR_UNSUPPORTED).
  */
 lisa_status lisa_relative_bias(const lisa_rel_bias *bias, int heads, void *out, int dtype, void *stream);
 
@@ -112,7 +122,8 @@ lisa_status lisa_relative_bias(const lisa_rel_bias *bias, int heads, void *out, 
  * Its gradient: dtable [rows.buckets * cols.buckets][heads] fp32, written (not
  * accumulated), the sums of dbias [heads][n][m] (contiguous, dtype) over the
  * pairs of each bucket; 0 for a bucket without pairs.  bias->table is not read
- * and may be NULL.
+ * and may be NULL.  The workspace holds sums of parts of the matrix and no error
+ * word: the kernels have no wait that could give up.
  */
 size_t lisa_relative_bias_backward_workspace_bytes(const lisa_rel_bias *bias, int heads);
 lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, int heads, const void *dbias, int dtype,
@@ -121,7 +132,7 @@ lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, int heads, co
 /*
  * Cross attention.  O and lse are written; lse (fp32 [B][heads][n], contiguous)
  * may be NULL.  bias may be NULL.  scale is finite and > 0 (1 / sqrt(d) as a
- * rule).  O may not overlap an input.  The workspace, 16-byte aligned, may be 0
+ * rule).  O and lse may not overlap an input or each other.  The workspace, 16-byte aligned, may be 0
  * bytes (lisa_cross_attention_workspace_bytes says; 0 too for arguments that the
  * call would reject).  Where it is not, it begins with the call's error word
  * (lisa_query_status); a call without one has no wait that could give up.
@@ -141,7 +152,7 @@ lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q_strides, c
  * with a bias, dtable are written, never accumulated, and may not overlap each
  * other or an input.  Where K or V repeats an entry (stride 0), dK and dV are
  * those of the repeated tensor, one entry for each repeat.  dtable is NULL
- * exactly when bias is.
+ * exactly when bias is.  The workspace begins with the call's error word.
  */
 size_t lisa_cross_attention_backward_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,
                                                      const lisa_rel_bias *bias, int dtype);

@@ -306,13 +306,200 @@ def test_gradient_against_differences(lisa):
         assert abs(got - want) <= h * h * scale + 2.0 ** -23 * scale * (30 + 16) / h
 
 
+LOWEST = (torch.finfo(F32).min, torch.finfo(BF16).min)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 150])
+def test_the_types_lowest_values_mask(lisa, dtype, n):
+    """Entries of the lowest finite value mask as -inf does, on every path, rows that they leave empty too."""
+    c = Case(lisa, dtype, 2, 2, 2, n, 140, 64, bias={"cols": ("exact", 2), "start": (0, 0 if n > 1 else 137),
+                                                     "minus_inf": (0, 4)})
+    want = c.want(backward=n > 1)
+    for e, row in enumerate((0, 4)):
+        c.bias.table[row] = LOWEST[e]
+    out, lse = c.forward()
+    ref.assert_within(out, want["o"], "o")
+    ref.assert_within(lse, want["lse"], "lse")
+    if n > 1:
+        assert torch.isinf(lse[:, :, 142:]).all() and not out[:, :, 142:].any()
+        for name, got in zip(("dq", "dk", "dv", "dtable"), c.backward(out, lse)):
+            ref.assert_within(got, want[name], name)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_masked_by_large_finite_numbers(lisa, dtype):
+    """-1e9 over a whole row leaves fp32 nothing of the scores: finite outputs, and
+    the gradients are those of a row without keys (rows 141 and on: offsets of -2 and less)."""
+    c = Case(lisa, dtype, 2, 2, 2, 150, 140, 64, bias={"cols": ("exact", 2), "minus_inf": (0, 4)})
+    out, lse = c.forward()
+    want = c.backward(out, lse)
+    for row in (0, 4):
+        c.bias.table[row] = -1e9
+    o2, l2 = c.forward()
+    assert torch.isfinite(o2).all() and torch.equal(o2[:, :, :141], out[:, :, :141])
+    assert torch.isfinite(l2).all() and torch.equal(l2[:, :, :141], lse[:, :, :141])
+    for a, b in zip(c.backward(o2, l2), want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_the_error_word_is_cleared(lisa, dtype):
+    from hop_stochastic_vision_gb300 import attention as att
+    c = Case(lisa, dtype, 2, 2, 2, 70, 90, 64)
+    dt = lisa.LISA_F32 if dtype == F32 else lisa.LISA_BF16
+    stream = torch.cuda.current_stream().cuda_stream
+    out, lse = c.forward()
+    sizes = (att.lisa_cross_attention_workspace_bytes(2, 2, 2, 70, 90, 64, None, dt),
+             att.lisa_cross_attention_backward_workspace_bytes(2, 2, 2, 70, 90, 64, None, dt))
+    for nbytes, call in zip(sizes, (lambda w: c.forward(workspace=w), lambda w: c.backward(out, lse, workspace=w))):
+        if nbytes:
+            ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
+            call(ws)
+            assert lisa.lisa_query_status(ws.data_ptr(), stream) == lisa.LISA_OK
+
+
+@pytest.mark.parametrize("dtype,n", [(F32, 70), (BF16, 70), (BF16, 1)])
+def test_offsets_beyond_32_bits(lisa, dtype, n):
+    """Keys a million elements apart: the last ones stand 2^31 elements and more from the first."""
+    m, gap = 2200, 1 << 20
+    c = Case(lisa, dtype, 1, 1, 1, n, m, 64)
+    out, lse = c.forward()
+    grads = c.backward(out, lse)
+    wide = torch.empty(m * gap, dtype=dtype, device="cuda").view(1, 1, m, gap)
+    for at, name in ((0, "k"), (64, "v")):
+        wide[..., at:at + 64] = getattr(c, name)
+        setattr(c, name, wide[..., at:at + 64])
+    o2, l2 = c.forward()
+    for a, b in zip((out, lse) + grads, (o2, l2) + c.backward(o2, l2)):
+        assert torch.equal(a, b)
+
+
+def test_the_most_queries(lisa):
+    """2^22 queries of two keys, fp32 with a bias: more tiles than a grid's second axis holds."""
+    n = 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q, do = (torch.randn(1, 1, n, 16, generator=g, device="cuda") for _ in range(2))
+    k, v = (torch.randn(1, 1, 2, 16, generator=g, device="cuda") for _ in range(2))
+    table = torch.randn(3, 1, generator=g, device="cuda")
+    bias = lisa.RelativeBias(table, (1, n), (1, 2), cols=lisa.exact_buckets(1))
+    out, lse = lisa.cross_attention(q, k, v, bias=bias, return_lse=True)
+    dtable = lisa.cross_attention_backward(q, k, v, out, lse, do, bias=bias)[3]
+    s = q[0, 0].double() @ k[0, 0].double().t() / 4 + table.double()[0, 0]
+    s[:2] = q[0, 0, :2].double() @ k[0, 0].double().t() / 4 + table.double()[[[1, 2], [0, 1]], 0]
+    p = torch.softmax(s, -1)
+    dp = do[0, 0].double() @ v[0, 0].double().t()
+    ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+    want = torch.stack((ds[2:].sum() + ds[1, 0], ds[0, 0] + ds[1, 1], ds[0, 1]))
+    # a term is off by a few 2^-24 of the scores' and dP's magnitudes (|s| to 30, |dP| to 60: 64 of them), the sum of
+    # the n terms in runs of at most 2^13 by 2^-24 2^13 of the terms' magnitude
+    bound = 2.0 ** -24 * (64 * 30 + 2 ** 13) * ds.abs().sum()
+    assert ((dtable[:, 0].double() - want).abs() <= bound).all()
+    assert (out[0, 0].double() - p @ v[0, 0].double()).abs().max() <= 2.0 ** -24 * 64 * 30 * v.abs().max()
+
+
+def test_two_graphs_share_a_workspace(lisa):
+    from hop_stochastic_vision_gb300 import attention as att
+    cases = [Case(lisa, BF16, 2, 4, 2, n, 260, 64, bias=LOG, seed=n) for n in (100, 333)]
+    nbytes = max(att.lisa_cross_attention_backward_workspace_bytes(2, 4, 2, n, 260, 64, c.bias.struct, lisa.LISA_BF16)
+                 for n, c in zip((100, 333), cases))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    want, graphs, got = [], [], []
+    for c in cases:
+        out, lse = c.forward()
+        want.append((out, lse) + c.backward(out, lse))
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            out, lse = c.forward(workspace=ws)
+            got.append((out, lse) + c.backward(out, lse, workspace=ws))
+    for which in (0, 1, 1, 0, 1):
+        for x in got[which]:
+            x.fill_(7)
+        graphs[which].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[which], want[which]))
+
+
+def test_calls_side_by_side(lisa):
+    """Calls on two streams at once, each with its own workspace."""
+    cases = [Case(lisa, BF16, 4, 4, 2, 500, 600, 64, bias=LOG, seed=s) for s in (1, 2)]
+    want = []
+    for c in cases:
+        out, lse = c.forward()
+        want.append((out, lse) + c.backward(out, lse))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cases], [[], []]
+    for _ in range(8):
+        for c, s, res in zip(cases, streams, got):
+            with torch.cuda.stream(s):
+                out, lse = c.forward()
+                res.append((out, lse) + c.backward(out, lse))
+    torch.cuda.synchronize()
+    for res, w in zip(got, want):
+        assert all(torch.equal(a, b) for r in res for a, b in zip(r, w))
+
+
+def test_a_table_that_moved(lisa):
+    c = Case(lisa, BF16, 1, 2, 2, 40, 50, 64, bias=NEAR)
+    out = c.forward()[0]
+    c.bias.table.data = c.bias.table.clone()
+    assert torch.equal(c.forward()[0], out)
+    c.bias.table = c.bias.table.cpu()
+    with pytest.raises(ValueError):
+        c.forward()
+
+
+def test_refusals(lisa):
+    q, k = (torch.randn(2, 2, n, 64, device="cuda", dtype=BF16) for n in (8, 9))
+    ok = lisa.cross_attention(q, k, k)
+    bad = [(q.float(), k, k), (q, k[:, :, :8], k), (q, k, k.float()), (q, k.cpu(), k), (q[0], k, k), (q.half(), k, k),
+           (q, k.transpose(2, 3).contiguous().transpose(2, 3), k), (q[:1], k, k)]
+    for args in bad:
+        with pytest.raises(ValueError):
+            lisa.cross_attention(*args)
+    off = torch.randn(2 * 2 * 8 * 64 + 1, device="cuda", dtype=BF16)[1:].view(2, 2, 8, 64)     # 2 bytes off
+    narrow = torch.randn(2, 2, 8, 40, device="cuda", dtype=BF16)
+    none = torch.empty(2, 2, 8, 0, device="cuda", dtype=BF16)
+    odd = torch.randn(2, 2, 8, 68, device="cuda", dtype=BF16)[..., :64]                       # rows of 136 bytes
+    for args in ((off, k, k), (narrow, narrow, narrow), (none, none, none), (odd, k, k), (q, q[:, :, :0], q[:, :, :1])):
+        with pytest.raises((lisa.LisaError, ValueError)):
+            lisa.cross_attention(*args)
+    with pytest.raises(lisa.LisaError):
+        lisa.cross_attention(q, k, k, out=q)
+    with pytest.raises(lisa.LisaError):
+        lisa.cross_attention(q, k, k, scale=-1.0)
+    with pytest.raises(lisa.LisaError):
+        lisa.cross_attention(q, q.new_empty(2, 3, 9, 64), q.new_empty(2, 3, 9, 64))            # 2 heads over 3
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    out, lse = lisa.cross_attention(torch.cat((q,) * 8, 2), k, k, return_lse=True)
+    with pytest.raises(lisa.LisaError):
+        lisa.cross_attention(torch.cat((q,) * 8, 2), k, k, workspace=small)
+    with pytest.raises(ValueError):
+        lisa.cross_attention_backward(q, k, k, ok, lse, q)                                     # another call's lse
+    for lens in (torch.ones(2, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda"),
+                 torch.ones(2, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            lisa.cross_attention(q, k, k, kv_lens=lens)
+    table = torch.zeros(32, 2, device="cuda")
+    with pytest.raises(ValueError):
+        lisa.cross_attention(q, k, k, bias=lisa.RelativeBias(table, (1, 8), (1, 8), cols=lisa.log_buckets(32, 128)))
+    for args in ((table[:31], (1, 8), (1, 9)), (table.double(), (1, 8), (1, 9)), (table.t(), (1, 8), (1, 9)),
+                 (table.cpu(), (1, 8), (1, 9))):
+        with pytest.raises(ValueError):
+            lisa.RelativeBias(*args, cols=lisa.log_buckets(32, 128))
+    assert torch.equal(lisa.cross_attention(q, k, k), ok)
+
+
 # ------------------------------------------------------------------ the bias matrix
 
 MATRICES = [((1, 1), (1, 1), LOG), ((1, 50), (1, 77), LOG), ((1, 300), (1, 5), SHORT), ((1, 40), (1, 600), NEAR),
             ((1, 33), (1, 20), {"cols": ("log", 16, 60), "step": (1, 5)}), ((14, 14), (14, 14), None),
             ((24, 24), (24, 24), None), ((13, 7), (3, 2), 4), ((7, 30), (7, 30), None),
             ((6, 5), (9, 4), {"rows": ("log", 8, 4), "cols": ("exact", 1), "step": (2, 3), "start": (-1, 2)}),
-            ((1, 900), (1, 1100), {"cols": ("exact", 700)})]
+            ((1, 900), (1, 1100), {"cols": ("exact", 700)}),
+            ((1, 1000), (1, 1500), {"cols": ("exact", 8), "step": (1, 300), "start": (0, 40000)}),
+            ((1, 90), (1, 40), {"cols": ("log", 8, 5), "step": (1, 5000), "start": (0, 60)})]
 
 
 def _matrix(lisa, q, k, how, heads=3):

@@ -70,6 +70,10 @@ BAD = [
     (dict(O=0), INV), (dict(O=FAKE + (3 << 20) + 8), INV), (dict(lse=FAKE + 1), INV),
     (dict(O=FAKE), INV), (dict(O=FAKE + (1 << 20) + 256), INV),         # overlaps Q, K
     (dict(os=_strides(4, 8, 16, batch=0)), INV),                        # an output entry repeated
+    (dict(os=_strides(4, 8, 16, head=16)), INV),                        # heads and tokens in one place
+    (dict(os=att.lisa_strides(8 * 64, 16, 60)), INV), (dict(os=att.lisa_strides(7 * 64, 16, 64)), INV),
+    (dict(lse=FAKE + 64), INV), (dict(lse=FAKE + (3 << 20) + 64), INV), (dict(O=FAKE + (64 << 20), bias=_bias()), INV),
+    (dict(B=60000, heads=60000, kv_heads=60000), UNS),
 ])
 def test_forward_rejects_before_launch(over, status):
     assert _forward(**over) == status
