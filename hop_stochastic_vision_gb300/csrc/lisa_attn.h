@@ -123,6 +123,7 @@ cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const v
 cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dq(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dkdv(const Problem &p, cudaStream_t s);
+int simt_dbias_splits(int B, int heads, int n, int m);
 cudaError_t launch_simt_dbias(const Problem &p, cudaStream_t s);
 
 // The table by offset, times log2(e), into bias.offsets.

@@ -261,7 +261,7 @@ BwdPlan backward_plan(int B, int heads, int kv_heads, int n, int m, int d, const
         off = align_up(off + part);
     }
     if (bias) {
-        if (pl.tc) pl.b_splits = tc_dbias_splits(B, heads, n, m);
+        pl.b_splits = pl.tc ? tc_dbias_splits(B, heads, n, m) : simt_dbias_splits(B, heads, n, m);
         pl.off_table = off;
         BiasDev dev;
         if (pl.tc && bias_dev(bias, heads, dev) == LISA_OK) off = align_up(off + offsets_bytes(dev));

@@ -12,6 +12,8 @@
 // 256 threads as 16 x 16; thread (ty, tx) owns rows 4 ty .. 4 ty + 3 and
 // columns tx + 16 c of a 64 x 64 tile, so the 16 threads of a row are one half
 // of a warp and its maximum and sum are shuffles.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -417,7 +419,8 @@ __global__ void __launch_bounds__(kThreads) simt_dbias(const __grid_constant__ P
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
-    for (int b = 0; b < p.B; ++b) {
+    const int b1 = (int)((long long)p.B * (blockIdx.y + 1) / gridDim.y);
+    for (int b = (int)((long long)p.B * blockIdx.y / gridDim.y); b < b1; ++b) {   // this part of the batch
         const int len = valid_keys(p, b);
         if (j0 >= len) continue;
         const size_t row0 = ((size_t)b * p.heads + h) * p.n;
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kThreads) simt_dbias(const __grid_constant__ P
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int i = i0 + 4 * ty + r, j = j0 + tx + 16 * c;
-            if (i < p.n && j < p.m) p.dbias[((size_t)h * p.n + i) * p.m + j] = acc[r][c];
+            if (i < p.n && j < p.m) p.dbias[(((size_t)blockIdx.y * p.heads + h) * p.n + i) * p.m + j] = acc[r][c];
         }
 }
 
@@ -475,7 +478,7 @@ struct Simt {
         return run<simt_dkdv<T, D>>(dim3(tiles(p.m), p.kv_heads, p.B), 4 * t + 2 * kWeights, p, s);
     }
     static cudaError_t dbias(const Problem &p, cudaStream_t s) {
-        return run<simt_dbias<T, D>>(dim3(tiles(p.m) * tiles(p.n), 1, p.heads), 4 * t, p, s);
+        return run<simt_dbias<T, D>>(dim3(tiles(p.m) * tiles(p.n), p.b_splits, p.heads), 4 * t, p, s);
     }
 };
 
@@ -488,6 +491,12 @@ struct Simt {
                          : (p.d == 16   ? Simt<__nv_bfloat16, 16>::fn(p, s)                      \
                             : p.d == 32 ? Simt<__nv_bfloat16, 32>::fn(p, s)                      \
                                         : Simt<__nv_bfloat16, 64>::fn(p, s)))
+
+int simt_dbias_splits(int B, int heads, int n, int m) {
+    // fewer tiles than SMs: share the batch out, a matrix for each part
+    const long long tiles = (long long)heads * ((n + kTile - 1) / kTile) * ((m + kTile - 1) / kTile);
+    return (int)std::max<long long>(1, std::min<long long>(152 / tiles, B));
+}
 
 cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s) { return LISA_ATTN_DISPATCH(forward); }
 cudaError_t launch_simt_dq(const Problem &p, cudaStream_t s) { return LISA_ATTN_DISPATCH(dq); }

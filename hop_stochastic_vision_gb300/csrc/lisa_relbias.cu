@@ -454,7 +454,7 @@ size_t fold_bytes(const FoldDev &f) {
 
 cudaError_t launch_fold_sum(const FoldDev &f, float *dtable, cudaStream_t s) {
     const int width = std::min(256, (f.col_buckets + 31) / 32 * 32), groups = 1024 / width;
-    return launch_plain(fold_sum, dim3((unsigned)f.row_buckets, (unsigned)((f.col_buckets + width - 1) / width), (unsigned)f.heads),
+    return launch_chained(fold_sum, dim3((unsigned)f.row_buckets, (unsigned)((f.col_buckets + width - 1) / width), (unsigned)f.heads),
                         1024, 0, s, f, dtable, width, groups, fast_div(f.ktiles));
 }
 
