@@ -7,10 +7,11 @@
 // walks every fourth chunk of 32 keys of its CTA's part with its own ring of
 // asynchronous copies, keeps the running maximum, sum and output in registers,
 // and the warps and then the CTAs of the cluster join in a fixed order.  Bound
-// by the bytes of K and V: no CTA waits for another until the end, and with two
-// chunks of 8 KB in flight per warp three CTAs keep 190 KB per SM on the way
-// (64 x 4096 keys, 4 key heads, lengths from 0 up: 46 us; two CTAs with three
-// chunks 52 us).
+// by the bytes of K and V: no CTA waits for another until the end, and each warp
+// has two chunks of 8 KB in flight (three chunks, so fewer CTAs per SM, were
+// slower: 52 us against 46 at one setting of the rest).  64 x 4096 keys, 4 key
+// heads, lengths from 0 up: 40 us for 137 MB, 3.4 TB/s; 256 x 4096 keys at full
+// length 185 us, 5.8 TB/s.
 #include <algorithm>
 
 #include "lisa_attn_tc.cuh"
@@ -345,10 +346,15 @@ cudaError_t launch_token(const Problem &p, cudaStream_t s) {
     x.rtiles = (x.rows + 15) / 16;
     x.div_rtiles = fast_div(x.rtiles);
     x.div_n = fast_div(p.n);
-    // about two waves of three CTAs per SM, so lengths that differ even out, but at least 256 keys to a CTA
+    // Two CTAs per SM at most, of 256 keys at least: a CTA's start and the join cost some microseconds, so a second
+    // wave does not pay (256 key heads of 4096 keys: 60 us whole, 75 in two parts, 69 in four; 64 of them 34 us
+    // whole, 24 in four parts, 30 in eight; 8 of 32768 keys 183 and 34 us whole and in eight).  Lengths that differ
+    // even out with twice as many, while 1024 keys are left to each (256 key heads, lengths from 0 to 4096: 44 us
+    // whole, 38 in two parts, 40 in three; from 0 to 1000: 20, 22 and 24).
     const long long ctas = (long long)p.B * p.kv_heads * x.rtiles;
-    x.splits = 1;
-    while (x.splits < 8 && ctas * x.splits < 6 * 152 && p.m >= 2 * x.splits * 256) x.splits *= 2;
+    long long splits = std::min<long long>(2 * 152 / ctas, p.m / 256);
+    if (p.kv_lens) splits = std::max(splits, std::min<long long>(4 * 152 / ctas, p.m / 1024));
+    x.splits = (int)std::max<long long>(1, std::min<long long>(8, splits));
     if (p.d == 16) return p.bias.mode ? go<16, 1>(x, s) : go<16, 0>(x, s);
     if (p.d == 32) return p.bias.mode ? go<32, 1>(x, s) : go<32, 0>(x, s);
     return p.bias.mode ? go<64, 1>(x, s) : go<64, 0>(x, s);
