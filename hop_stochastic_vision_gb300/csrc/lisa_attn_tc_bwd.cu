@@ -5,7 +5,8 @@
 //   dQ     128 queries against every key; dS goes back to tensor memory as bf16
 //          for dQ += dS K.  Also leaves delta_i for the two others: dO . O from
 //          the rounded output (an error of one rounding of O against bf16
-//          results), or with a bias sum_j p dP in fp32, since its gradient is fp32
+//          results), or sum_j p dP in fp32 with a bias, since its gradient is fp32,
+//          and where all keys are one tile
 //   dK dV  128 keys against the queries of the heads that share them, the
 //          tile transposed (rows are keys): dV += P^T dO, dK += dS^T Q, the
 //          queries split over CTAs when there are few key tiles, the parts added
@@ -299,9 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (y.q0 + wt < p.n) lse_next = p.lse[((size_t)y.b * p.heads + y.h) * p.n + y.q0 + wt];
                 }
             }
+            const bool single = w.tiles == 1;   // delta from the tile itself, below
+            if (w.tiles > 0) wait_on(smem_u32(&bar.q_full[cq.slot]), cq.phase, guard, kErrTimeoutLoad);
             // dO . O of the tile's rows, 8 lanes per row
-            if (w.tiles > 0) {
-                wait_on(smem_u32(&bar.q_full[cq.slot]), cq.phase, guard, kErrTimeoutLoad);
+            if (w.tiles > 1) {
                 const uint32_t g_s = qd + (3 * cq.slot + 1) * kTileBytes, o_s = g_s + kTileBytes;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -324,8 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             math_barrier();   // also: the strips of the previous item's delta have been read
-            const float delta = w.tiles > 0 ? rows_delta[wt] : 0.f;
-            float exact = 0.f;
+            float delta = w.tiles > 1 ? rows_delta[wt] : 0.f, exact = 0.f;
             int oq = 0, oq_lo = 0;
             if (kBias) {
                 const int start = bias_start(p.bias, w.b);
@@ -347,17 +348,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (e >= keys - c0) dp[e] = 0.f;
                 }
                 uint32_t ds[kStrip / 2];
-                if (kBias) {   // the bias gradient wants delta from the unrounded weights
+                if (kBias || single) {   // delta from the unrounded weights: the bias gradient wants it, and few keys,
+                                         // where dP - delta cancels most, do without the rounding of O
                     float e0 = 0.f, e1 = 0.f;
 #pragma unroll
                     for (int e = 0; e < kStrip; e += 2) {
-                        float u, v;
                         mul2(dp[e], dp[e + 1], s[e], s[e + 1], dp[e], dp[e + 1]);
                         add2(e0, e1, e0, e1, dp[e], dp[e + 1]);
+                    }
+                    exact += e0 + e1;
+                    if (single) {   // the strips' shares, where the item's O is: nothing reads that now
+                        float *share = reinterpret_cast<float *>(sm + (3 * cq.slot + 2) * kTileBytes) + wt;
+                        share[strip * kRows] = exact;
+                        math_barrier();
+                        delta = (share[0] + share[kRows]) + (share[2 * kRows] + share[3 * kRows]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kStrip; e += 2) {
+                        float u, v;
                         fma2(u, v, s[e], s[e + 1], -delta, -delta, dp[e], dp[e + 1]);
                         ds[e >> 1] = pack_bf16(u, v);
                     }
-                    exact += e0 + e1;
                 } else {
 #pragma unroll
                     for (int e = 0; e < kStrip; e += 2) {
@@ -379,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 arrive_warp(&bar.ds_full, lane);
             }
-            if (kBias) {   // the strips' shares of delta
+            if (kBias && !single) {   // the strips' shares of delta
                 if (strip > 0) other[strip - 1][wt] = exact;
                 math_barrier();
                 if (strip == 0 && in) p.delta[row] = (exact + other[0][wt]) + (other[1][wt] + other[2][wt]);
@@ -400,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld16_nowait(tDq + 16 * strip + lanes, o);
             tc_wait_ld();
             tc_fence_before();
-            // staged where the item's O was: its last reader was delta, a barrier ago
+            // staged where the item's O was: its last reader was delta, before every warp's dS
             store_rows_bf16<16>(qd + (3 * cq.slot + 2) * kTileBytes + (uint32_t)warp * 1024u, o, p.scale, out, p.d,
                                 p.n - (i - lane), p.d - 16 * strip, lane);
             fence_proxy_async();
@@ -1020,7 +1031,8 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     x.items = (int)items;
     x.first = 1;
     for (x.q_slots = 2;; --x.q_slots) {
-        const int left = kSmemBudget - 3 * x.q_slots * kTileBytes - lut - keys - 1024;
+        // with a bias the kernel holds 2192 bytes of its own
+        const int left = kSmemBudget - (lut > 0 ? 256 : 0) - 3 * x.q_slots * kTileBytes - lut - keys - 1024;
         x.stages = std::min(kMaxStages, left / (2 * kTileBytes));
         if (x.stages >= 2 || x.q_slots == 1) break;
     }

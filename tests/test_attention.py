@@ -141,6 +141,34 @@ def test_the_largest_offset_table(lisa):
     Case(lisa, BF16, 1, 1, 1, (64, 64), (8, 8), 64, bias=_grid((64, 64), (8, 8), 8)).check()
 
 
+def test_an_offset_table_that_fills_the_shared_memory(lisa):
+    """32 KB of offsets: with whole stages of tiles the dQ kernel's memory to the last KB."""
+    Case(lisa, BF16, 1, 1, 1, 3900, 3900, 64, bias={"cols": ("exact", 3850)}).check()
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 128])
+def test_few_keys_keep_small_differences(lisa, m):
+    """One tile of keys: delta is the sum of the unrounded p dP, so dQ = scale sum dS k is
+    good to the rounding of dS and of dQ alone, however much of dP - delta cancels."""
+    for bias in (None, {"cols": ("exact", 2)}):
+        c = Case(lisa, BF16, 3, 2, 2, 40, m, 64, bias=bias, spread=4.0)
+        out, lse = c.forward()
+        dq = c.backward(out, lse)[0].double().cpu()
+        s = c.q_ref.double() @ c.k_ref.double().transpose(-1, -2) * c.scale
+        if bias:
+            s = s + c.table.double().t()[:, c.index]
+        p = torch.softmax(s, -1)
+        dp = c.dout.double() @ c.v_ref.double().transpose(-1, -2)
+        ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+        want = c.scale * ds @ c.k_ref.double()
+        mag = c.scale * ds.abs() @ c.k_ref.double().abs()
+        # dS and dQ rounded, half a step 2^-8 each; behind them fp32: s of magnitude up to 150 with a few 2^-24 of it in
+        # the exponent (2^-14 of p), dP - delta with 64 2^-24 of |dO| |v| (below 2^-12 of sum |dO v|), both of p dP
+        noise = c.scale * ((p * (2.0 ** -14 * (dp.abs() + (p * dp).abs().sum(-1, keepdim=True)) + 2.0 ** -16 * (
+            c.dout.double().abs() @ c.v_ref.double().abs().transpose(-1, -2)))) @ c.k_ref.double().abs())
+        assert ((dq - want).abs() <= (2.0 ** -8 + 2.0 ** -8 * 1.01) * mag + noise + 2.0 ** -126).all()
+
+
 def test_grid_bias_with_near_and_far_offsets_in_one_bucket(lisa):
     q, k = (9, 11), (6, 7)
     for rows, cols in ((("exact", 2), ("log", 8, 5)), (("log", 16, 9), ("exact", 0))):
