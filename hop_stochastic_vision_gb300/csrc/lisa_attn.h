@@ -115,7 +115,7 @@ bool fold_plan(const lisa_rel_bias &b, int heads, int parts, FoldDev &f);
 size_t fold_bytes(const FoldDev &f);
 // Adds the tiles' blocks up into dtable.
 cudaError_t launch_fold_sum(const FoldDev &f, float *dtable, cudaStream_t s);
-size_t bias_grad_bytes(const lisa_rel_bias &b, int heads);
+size_t bias_grad_bytes(const lisa_rel_bias &b, int heads, int parts);
 // Bucket sums of `parts` matrices [heads][n][m], one behind the other, added up.
 cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int parts, int dtype,
                              float *dtable, void *ws, cudaStream_t s);

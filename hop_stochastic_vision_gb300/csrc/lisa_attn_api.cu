@@ -269,7 +269,7 @@ BwdPlan backward_plan(int B, int heads, int kv_heads, int n, int m, int d, const
         pl.off_dbias = off;
         if (!pl.folded) off = align_up(off + (size_t)pl.b_splits * heads * n * m * sizeof(float));
         pl.off_grad = off;
-        off = align_up(off + (pl.folded ? fold_bytes(pl.fold) : bias_grad_bytes(*bias, heads)));
+        off = align_up(off + (pl.folded ? fold_bytes(pl.fold) : bias_grad_bytes(*bias, heads, pl.b_splits)));
     }
     pl.total = off;
     return pl;
@@ -311,7 +311,7 @@ extern "C" lisa_status lisa_relative_bias(const lisa_rel_bias *bias, int heads, 
 extern "C" size_t lisa_relative_bias_backward_workspace_bytes(const lisa_rel_bias *bias, int heads) {
     BiasDev dev;
     if (bias_dev(bias, heads, dev) != LISA_OK || !matrix_fits(*bias, heads)) return 0;
-    return bias_grad_bytes(*bias, heads);
+    return bias_grad_bytes(*bias, heads, 1);
 }
 
 extern "C" lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, int heads, const void *dbias, int dtype,
@@ -327,7 +327,7 @@ extern "C" lisa_status lisa_relative_bias_backward(const lisa_rel_bias *bias, in
     const size_t bytes = (size_t)heads * bias->q_rows * bias->q_cols * bias->k_rows * bias->k_cols *
                          (dtype == LISA_BF16 ? 2 : 4);
     if (Span(dtable, table_floats(*bias, heads) * 4).meets(Span(dbias, bytes))) return LISA_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < bias_grad_bytes(*bias, heads)) return LISA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < bias_grad_bytes(*bias, heads, 1)) return LISA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
     return status_of(
         launch_bias_grad(*bias, dev, dbias, 1, dtype, dtable, workspace, static_cast<cudaStream_t>(stream)));

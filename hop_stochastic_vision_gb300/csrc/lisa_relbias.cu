@@ -226,60 +226,58 @@ __global__ void __launch_bounds__(1024) bias_grad_sum(const __grid_constant__ Gr
 
 // ------------------------------------------------- gradient, tile by tile
 __device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// 4 bytes global -> shared, or zeros (nothing is read then)
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+// 4 bytes global -> shared
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// One 128 x 128 tile of one head: loaded into shared memory, then folded; three
-// CTAs per SM, so one folds while the others load (two of 256 threads and 128
-// registers took 72 us for the 268 MB of a 64 x 64 grid's four heads).
+// One 128 x 128 tile of one head's matrix (blockIdx.z: part, head): loaded into
+// shared memory, then folded; three CTAs per SM, so one folds while the others
+// load.  Bound by the instructions of both: a whole tile's fp32 loads are one
+// copy and one address step each.  The 268 MB of a 64 x 64 grid's four heads:
+// KFIG us.
 constexpr int kFoldThreads = 512;
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kFoldThreads, 3) fold_matrix(const __grid_constant__ FoldDev f, const T *dbias, int matrices) {
+__global__ void __launch_bounds__(kFoldThreads, 3) fold_matrix(const __grid_constant__ FoldDev f, const T *dbias) {
     extern __shared__ __align__(16) float fold_smem[];
     chain_begin();
     float *tile = fold_smem, *sums = fold_smem + kFoldTile * kFoldPitch;
-    const int tid = threadIdx.x, jt = blockIdx.x, it = blockIdx.y, h = blockIdx.z;
+    const int tid = threadIdx.x, jt = blockIdx.x, it = blockIdx.y;
+    const int part = blockIdx.z / f.heads, h = blockIdx.z % f.heads;
     const TileGeom g = fold_geom(f, it, jt);
     // 4 bytes of a row per lane: whole lines per load, and stores that meet no bank twice (two bf16: once more)
     constexpr int kPerRow = kFoldTile / VEC, kRowsAtOnce = kFoldThreads / kPerRow, kLoads = kFoldTile / kRowsAtOnce;
     const int r0 = tid / kPerRow, c = (tid % kPerRow) * VEC;
     struct __align__(sizeof(T) * VEC) Vec { T v[VEC]; };
-    for (int part = 0; part < matrices; ++part) {
-        const T *src = dbias + ((size_t)part * f.heads + h) * ((size_t)f.n * f.m) + (size_t)g.q0 * f.m + g.j0 + c;
-        if (sizeof(T) == 4 && part == 0) {   // straight into shared memory, all of the tile in flight
-#pragma unroll 8
-            for (int e = 0; e < kLoads; ++e) {
-                const int r = r0 + e * kRowsAtOnce;
-                const bool in = r < g.nq && c < g.nk;
-                copy4(smem_at(tile + r * kFoldPitch + c), src + (in ? (size_t)r * f.m : (size_t)0) - (in ? 0 : c), in);
-            }
-            copies_done();
-            continue;
-        }
+    const T *src = dbias + (size_t)blockIdx.z * ((size_t)f.n * f.m) + (size_t)(g.q0 + r0) * f.m + g.j0 + c;
+    const size_t step = (size_t)kRowsAtOnce * f.m;
+    if (sizeof(T) == 4 && g.nq == kFoldTile && g.nk == kFoldTile) {   // straight into shared memory, all of it in flight
+        const uint32_t dst = smem_at(tile + r0 * kFoldPitch + c);
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e, src += step) copy4(dst + e * (kRowsAtOnce * kFoldPitch * 4), src);
+        copies_done();
+    } else {
         constexpr int kBatch = 16;
         for (int b = 0; b < kLoads; b += kBatch) {
             Vec x[kBatch];
 #pragma unroll
-            for (int e = 0; e < kBatch; ++e) {
-                const int r = r0 + (b + e) * kRowsAtOnce;
+            for (int e = 0; e < kBatch; ++e, src += step) {
 #pragma unroll
                 for (int u = 0; u < VEC; ++u) put(&x[e].v[u], 0.f);
                 // a vector is whole or absent: m is a multiple of VEC
-                if (r < g.nq && c < g.nk) x[e] = *reinterpret_cast<const Vec *>(src + (size_t)r * f.m);
+                if (r0 + (b + e) * kRowsAtOnce < g.nq && c < g.nk) x[e] = *reinterpret_cast<const Vec *>(src);
             }
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
                 float *t = tile + (r0 + (b + e) * kRowsAtOnce) * kFoldPitch + c;
 #pragma unroll
-                for (int u = 0; u < VEC; ++u) t[u] = (part > 0 ? t[u] : 0.f) + to_float(x[e].v[u]);
+                for (int u = 0; u < VEC; ++u) t[u] = to_float(x[e].v[u]);
             }
         }
     }
     __syncthreads();
-    float *out = fold_block(f, 0, h, it, jt);
+    float *out = fold_block(f, part, h, it, jt);
     const bool direct = fold_direct(f, g);
     fold_offsets(f, g, tile, direct ? out : sums, direct ? f.K : g.dc_n, tid, kFoldThreads);
     if (direct) return;
@@ -359,17 +357,17 @@ __global__ void __launch_bounds__(1024) fold_sum(const __grid_constant__ FoldDev
 }
 
 template <typename T, int VEC>
-cudaError_t run_fold_vec(const FoldDev &f, const T *dbias, int matrices, cudaStream_t s) {
+cudaError_t run_fold_vec(const FoldDev &f, const T *dbias, cudaStream_t s) {
     cudaError_t e = allow_smem<fold_matrix<T, VEC>>();
     if (e != cudaSuccess) return e;
-    return launch_plain(fold_matrix<T, VEC>, dim3((unsigned)f.ktiles, (unsigned)f.qtiles, (unsigned)f.heads), kFoldThreads,
-                          kFoldTileBytes + f.units * 4, s, f, dbias, matrices);
+    return launch_plain(fold_matrix<T, VEC>, dim3((unsigned)f.ktiles, (unsigned)f.qtiles, (unsigned)(f.heads * f.parts)), kFoldThreads,
+                          kFoldTileBytes + f.units * 4, s, f, dbias);
 }
 
 template <typename T>
-cudaError_t run_fold(const FoldDev &f, const T *dbias, int matrices, cudaStream_t s) {
-    if (sizeof(T) == 2 && f.m % 2 == 0) return run_fold_vec<T, 2>(f, dbias, matrices, s);
-    return run_fold_vec<T, 1>(f, dbias, matrices, s);
+cudaError_t run_fold(const FoldDev &f, const T *dbias, cudaStream_t s) {
+    if (sizeof(T) == 2 && f.m % 2 == 0) return run_fold_vec<T, 2>(f, dbias, s);
+    return run_fold_vec<T, 1>(f, dbias, s);
 }
 
 void grad_plan(const lisa_rel_bias &b, GradParams &g) {
@@ -445,7 +443,7 @@ bool fold_plan(const lisa_rel_bias &b, int heads, int parts, FoldDev &f) {
     const int width = std::min(kFoldTile, b.q_cols) + std::min(kFoldTile, b.k_cols) - 1;
     f.K = dev.cols.log_rule ? b.cols.buckets : std::min(b.cols.buckets, width);
     f.units = f.nR * width;
-    return f.units <= kMaxFoldUnits && f.qtiles <= 65535 && (long long)f.qtiles * f.ktiles < (1 << 30);
+    return f.units <= kMaxFoldUnits && f.qtiles <= 65535 && (long long)heads * parts <= 65535 && (long long)f.qtiles * f.ktiles < (1 << 30);
 }
 
 size_t fold_bytes(const FoldDev &f) {
@@ -458,9 +456,9 @@ cudaError_t launch_fold_sum(const FoldDev &f, float *dtable, cudaStream_t s) {
                         1024, 0, s, f, dtable, width, groups, fast_div(f.ktiles));
 }
 
-size_t bias_grad_bytes(const lisa_rel_bias &b, int heads) {
+size_t bias_grad_bytes(const lisa_rel_bias &b, int heads, int parts) {
     FoldDev f;
-    if (fold_plan(b, heads, 1, f)) return fold_bytes(f);
+    if (fold_plan(b, heads, parts, f)) return fold_bytes(f);
     GradParams g{};
     grad_plan(b, g);
     return (size_t)heads * g.q_rows * g.k_rows * g.nchunk * g.ntile * g.col_buckets * sizeof(float);
@@ -469,10 +467,10 @@ size_t bias_grad_bytes(const lisa_rel_bias &b, int heads) {
 cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int parts, int dtype,
                              float *dtable, void *ws, cudaStream_t s) {
     FoldDev f;
-    if (fold_plan(b, dev.heads, 1, f)) {
+    if (fold_plan(b, dev.heads, parts, f)) {
         f.part = static_cast<float *>(ws);
-        cudaError_t e = dtype == LISA_BF16 ? run_fold(f, static_cast<const __nv_bfloat16 *>(dbias), parts, s)
-                                           : run_fold(f, static_cast<const float *>(dbias), parts, s);
+        cudaError_t e = dtype == LISA_BF16 ? run_fold(f, static_cast<const __nv_bfloat16 *>(dbias), s)
+                                           : run_fold(f, static_cast<const float *>(dbias), s);
         return e != cudaSuccess ? e : launch_fold_sum(f, dtable, s);
     }
     GradParams g{};
