@@ -338,12 +338,22 @@ __global__ void __launch_bounds__(1024) fold_sum(const __grid_constant__ FoldDev
         const int count = ahead[32];
         for (int part = 0; part < f.parts; ++part) {
             const float *base = f.part + ((size_t)part * f.heads + h) * tiles * block + cb;
-#pragma unroll 4
-            for (int e = grp < groups ? grp : count; e < count; e += groups) {
-                const FoldShare s = list[e];
-                if (cb < s.cb_lo || cb >= s.cb_lo + s.cb_n) continue;
-                const float *b = base + s.tile * block + (size_t)s.row * f.K - s.cb_lo;
-                for (int d = 0; d < s.rows; ++d) acc += b[(size_t)d * f.K];
+            for (int e0 = grp < groups ? grp : count; e0 < count; e0 += 8 * groups) {   // eight tiles' loads in flight
+                const float *b[8];
+                int rows[8];
+                float v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int e = e0 + u * groups;
+                    const FoldShare s = list[min(e, count - 1)];
+                    rows[u] = e < count && cb >= s.cb_lo && cb < s.cb_lo + s.cb_n ? s.rows : 0;
+                    b[u] = base + s.tile * block + (size_t)s.row * f.K - s.cb_lo;
+                    v[u] = rows[u] > 0 ? *b[u] : 0.f;
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    for (int d = 1; d < rows[u]; ++d) v[u] += b[u][(size_t)d * f.K];
+                acc += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
             }
         }
     }
