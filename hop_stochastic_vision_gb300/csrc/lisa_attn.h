@@ -120,6 +120,7 @@ size_t bias_grad_bytes(const lisa_rel_bias &b, int heads, int parts);
 cudaError_t launch_bias_grad(const lisa_rel_bias &b, const BiasDev &dev, const void *dbias, int parts, int dtype,
                              float *dtable, void *ws, cudaStream_t s);
 
+cudaError_t launch_no_keys(const Problem &p, cudaStream_t s);   // m = 0
 cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dq(const Problem &p, cudaStream_t s);
 cudaError_t launch_simt_dkdv(const Problem &p, cudaStream_t s);

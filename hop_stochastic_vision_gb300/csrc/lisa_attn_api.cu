@@ -206,7 +206,7 @@ lisa_status fill(Problem &p, const void *Q, const lisa_strides *qs, const void *
 
 // The forward's path and workspace: CUDA cores for fp32; for bf16 one pass over
 // the keys where few rows share a key head, 128-row tiles otherwise.
-enum class Path { kSimt, kToken, kTiles };
+enum class Path { kNoKeys, kSimt, kToken, kTiles };
 struct FwdPlan {
     Path path;
     int splits;
@@ -216,6 +216,7 @@ struct FwdPlan {
 FwdPlan forward_plan(int B, int heads, int group, int n, int m, int d, int dtype, const BiasDev &bias) {
     FwdPlan pl{};
     pl.splits = 1;
+    pl.path = m == 0 ? Path::kNoKeys : Path::kSimt;
     if (dtype != LISA_BF16 || m == 0) return pl;
     if (token_applies(heads / group, group, n, bias)) {
         pl.path = Path::kToken;
@@ -373,6 +374,7 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
         if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (pl.path == Path::kNoKeys) return status_of(launch_no_keys(p, cs));
     if (pl.path == Path::kSimt) return status_of(launch_simt_forward(p, cs));
     if (pl.path == Path::kToken) return status_of(launch_token(p, cs));
     char *ws = static_cast<char *>(workspace);

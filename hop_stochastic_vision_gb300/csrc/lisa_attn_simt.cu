@@ -1,5 +1,5 @@
-// lisa_attn_simt.cu -- cross attention on the CUDA cores: fp32 arithmetic for
-// either data type, head widths 16, 32 and 64, any lengths and strides.
+// lisa_attn_simt.cu -- cross attention on the CUDA cores: fp32, head widths 16,
+// 32 and 64, any lengths and strides.
 //
 // Forward, per 64 queries of one (batch, head): one pass over the keys in tiles
 // of 64 with the running maximum and sum of the softmax; scores and weights
@@ -14,7 +14,6 @@
 // of a warp and its maximum and sum are shuffles.
 #include <algorithm>
 
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "lisa_attn.h"
@@ -28,17 +27,9 @@ namespace {
 constexpr int kTile = 64;
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void from_f(float &o, float x) { o = x; }
-__device__ __forceinline__ void from_f(__nv_bfloat16 &o, float x) { o = __float2bfloat16_rn(x); }
-
 __device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
     const float4 x = *reinterpret_cast<const float4 *>(p);
     v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
-    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-    v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xFFFF0000u);
 }
 
 // Rows t0 .. t0 + 63 of a [tokens][D] slice, first into registers (so the loads of
@@ -47,8 +38,7 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
 template <int D>
 struct Rows {
     float v[D / 16][4];
-    template <typename T>
-    __device__ __forceinline__ void load(const T *base, long long st, int t0, int count, int tid) {
+    __device__ __forceinline__ void load(const float *base, long long st, int t0, int count, int tid) {
 #pragma unroll
         for (int u = 0; u < D / 16; ++u) {
             const int e = tid + u * kThreads, r = e / (D / 4), c = 4 * (e % (D / 4));
@@ -64,8 +54,8 @@ struct Rows {
         }
     }
 };
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(const T *base, long long st, int t0, int count, float *out, int tid) {
+template <int D>
+__device__ __forceinline__ void load_tile(const float *base, long long st, int t0, int count, float *out, int tid) {
     Rows<D> r;
     r.load(base, st, t0, count, tid);
     r.store(out, tid);
@@ -170,9 +160,8 @@ __device__ __forceinline__ void finish_scores(float (&s)[4][4], const Problem &p
     }
 }
 
-template <typename T>
-__device__ __forceinline__ const T *slice(const Tensor &t, int b, int h) {
-    return static_cast<const T *>(t.p) + (long long)b * t.sb + (long long)h * t.sh;
+__device__ __forceinline__ const float *slice(const Tensor &t, int b, int h) {
+    return static_cast<const float *>(t.p) + (long long)b * t.sb + (long long)h * t.sh;
 }
 
 // Shared memory: Q, K, V (dO) tiles [64][D + 4], weights [64][68], the offset table.
@@ -180,7 +169,7 @@ template <int D>
 constexpr int tile_floats() { return kTile * (D + 4); }
 constexpr int kWeights = kTile * (kTile + 4);
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
     chain_begin();
@@ -190,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
     const int i0 = blockIdx.x * kTile, h = blockIdx.y, b = blockIdx.z, kvh = h / p.group;
     const int len = valid_keys(p, b);
     if (p.bias.mode) fill_offsets<true>(p.bias, h, lut, tid, kThreads);
-    load_tile<T, D>(slice<T>(p.Q, b, h), p.Q.st, i0, p.n, q_s, tid);
+    load_tile<D>(slice(p.Q, b, h), p.Q.st, i0, p.n, q_s, tid);
     int oq[4];
     const int start = p.bias.mode ? bias_start(p.bias, b) : 0;
 #pragma unroll
@@ -204,15 +193,15 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
         for (int c = 0; c < D / 16; ++c) acc[r][c] = 0.f;
     }
     Rows<D> kr, vr;
-    kr.load(slice<T>(p.K, b, kvh), p.K.st, 0, len, tid);
-    vr.load(slice<T>(p.V, b, kvh), p.V.st, 0, len, tid);
+    kr.load(slice(p.K, b, kvh), p.K.st, 0, len, tid);
+    vr.load(slice(p.V, b, kvh), p.V.st, 0, len, tid);
     for (int j0 = 0; j0 < len; j0 += kTile) {
         __syncthreads();
         kr.store(k_s, tid);
         vr.store(v_s, tid);
         __syncthreads();
-        kr.load(slice<T>(p.K, b, kvh), p.K.st, j0 + kTile, len, tid);
-        vr.load(slice<T>(p.V, b, kvh), p.V.st, j0 + kTile, len, tid);
+        kr.load(slice(p.K, b, kvh), p.K.st, j0 + kTile, len, tid);
+        vr.load(slice(p.V, b, kvh), p.V.st, j0 + kTile, len, tid);
         float s[4][4];
         tile_dot<D>(q_s, k_s, ty, tx, s);
         finish_scores(s, p, lut, j0, len, tx, oq);
@@ -239,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
         __syncwarp();   // a row's weights are written and read by one warp
         tile_mul<D>(p_s, v_s, ty, tx, acc);
     }
-    T *out = const_cast<T *>(slice<T>(p.O, b, h));
+    float *out = const_cast<float *>(slice(p.O, b, h));
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int i = i0 + 4 * ty + r;
@@ -247,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
         if (i >= p.n) continue;
         const float inv = sum[r] != 0.f ? 1.f / sum[r] : 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) from_f(out[(long long)i * p.O.st + tx + 16 * c], acc[r][c] * inv);
+        for (int c = 0; c < D / 16; ++c) out[(long long)i * p.O.st + tx + 16 * c] = acc[r][c] * inv;
         if (p.lse && tx == 0)
             p.lse[((size_t)b * p.heads + h) * p.n + i] = top[r] == -INFINITY ? -INFINITY : top[r] + logf(sum[r]);
     }
@@ -259,7 +248,7 @@ __device__ __forceinline__ float row_ref(const float *lse, size_t at, bool in) {
     return fabsf(l) > kMaxLse ? INFINITY : l;
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
     chain_begin();
@@ -271,8 +260,8 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
     if (i0 == 0 && h == 0 && b == 0 && tid == 0) *p.err = 0;   // these kernels have no wait that could give up
     if (p.bias.mode) fill_offsets<true>(p.bias, h, lut, tid, kThreads);
     // delta~_i = dO_i . O_i from the forward's (rounded) output
-    load_tile<T, D>(slice<T>(p.O, b, h), p.O.st, i0, p.n, q_s, tid);
-    load_tile<T, D>(slice<T>(p.dO, b, h), p.dO.st, i0, p.n, o_s, tid);
+    load_tile<D>(slice(p.O, b, h), p.O.st, i0, p.n, q_s, tid);
+    load_tile<D>(slice(p.dO, b, h), p.dO.st, i0, p.n, o_s, tid);
     __syncthreads();
     float delta[4], exact[4], ref[4], acc[4][D / 16];
     int oq[4];
@@ -292,17 +281,17 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
         for (int c = 0; c < D / 16; ++c) acc[r][c] = 0.f;
     }
     __syncthreads();
-    load_tile<T, D>(slice<T>(p.Q, b, h), p.Q.st, i0, p.n, q_s, tid);
+    load_tile<D>(slice(p.Q, b, h), p.Q.st, i0, p.n, q_s, tid);
     Rows<D> kr, vr;
-    kr.load(slice<T>(p.K, b, kvh), p.K.st, 0, len, tid);
-    vr.load(slice<T>(p.V, b, kvh), p.V.st, 0, len, tid);
+    kr.load(slice(p.K, b, kvh), p.K.st, 0, len, tid);
+    vr.load(slice(p.V, b, kvh), p.V.st, 0, len, tid);
     for (int j0 = 0; j0 < len; j0 += kTile) {
         __syncthreads();
         kr.store(k_s, tid);
         vr.store(v_s, tid);
         __syncthreads();
-        kr.load(slice<T>(p.K, b, kvh), p.K.st, j0 + kTile, len, tid);
-        vr.load(slice<T>(p.V, b, kvh), p.V.st, j0 + kTile, len, tid);
+        kr.load(slice(p.K, b, kvh), p.K.st, j0 + kTile, len, tid);
+        vr.load(slice(p.V, b, kvh), p.V.st, j0 + kTile, len, tid);
         float s[4][4], dp[4][4];
         tile_dot<D>(q_s, k_s, ty, tx, s);
         tile_dot<D>(o_s, v_s, ty, tx, dp);
@@ -318,19 +307,19 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
         __syncwarp();
         tile_mul<D>(p_s, k_s, ty, tx, acc);
     }
-    T *out = static_cast<T *>(p.dQ) + row0 * D;
+    float *out = static_cast<float *>(p.dQ) + row0 * D;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int i = i0 + 4 * ty + r;
         const float e = half_sum(exact[r]);
         if (i >= p.n) continue;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) from_f(out[(size_t)i * D + tx + 16 * c], acc[r][c] * p.scale);
+        for (int c = 0; c < D / 16; ++c) out[(size_t)i * D + tx + 16 * c] = acc[r][c] * p.scale;
         if (tx == 0) p.delta[row0 + i] = e;
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) simt_dkdv(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
     chain_begin();
@@ -345,8 +334,8 @@ __global__ void __launch_bounds__(kThreads) simt_dkdv(const __grid_constant__ Pr
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) dk[r][c] = dv[r][c] = 0.f;
     if (j0 < len) {
-        load_tile<T, D>(slice<T>(p.K, b, kvh), p.K.st, j0, len, k_s, tid);
-        load_tile<T, D>(slice<T>(p.V, b, kvh), p.V.st, j0, len, v_s, tid);
+        load_tile<D>(slice(p.K, b, kvh), p.K.st, j0, len, k_s, tid);
+        load_tile<D>(slice(p.V, b, kvh), p.V.st, j0, len, v_s, tid);
         const int start = p.bias.mode ? bias_start(p.bias, b) : 0;
         for (int g = 0; g < p.group; ++g) {
             const int h = kvh * p.group + g;
@@ -354,15 +343,15 @@ __global__ void __launch_bounds__(kThreads) simt_dkdv(const __grid_constant__ Pr
             __syncthreads();
             if (p.bias.mode) fill_offsets<true>(p.bias, h, lut, tid, kThreads);
             Rows<D> qr, dr;
-            qr.load(slice<T>(p.Q, b, h), p.Q.st, 0, p.n, tid);
-            dr.load(slice<T>(p.dO, b, h), p.dO.st, 0, p.n, tid);
+            qr.load(slice(p.Q, b, h), p.Q.st, 0, p.n, tid);
+            dr.load(slice(p.dO, b, h), p.dO.st, 0, p.n, tid);
             for (int i0 = 0; i0 < p.n; i0 += kTile) {
                 __syncthreads();
                 qr.store(q_s, tid);
                 dr.store(o_s, tid);
                 __syncthreads();
-                qr.load(slice<T>(p.Q, b, h), p.Q.st, i0 + kTile, p.n, tid);
-                dr.load(slice<T>(p.dO, b, h), p.dO.st, i0 + kTile, p.n, tid);
+                qr.load(slice(p.Q, b, h), p.Q.st, i0 + kTile, p.n, tid);
+                dr.load(slice(p.dO, b, h), p.dO.st, i0 + kTile, p.n, tid);
                 float s[4][4], dp[4][4];
                 int oq[4];
 #pragma unroll
@@ -396,14 +385,14 @@ __global__ void __launch_bounds__(kThreads) simt_dkdv(const __grid_constant__ Pr
         if (j >= p.m) continue;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-            from_f(static_cast<T *>(p.dK)[(row0 + j) * D + tx + 16 * c], dk[r][c] * p.scale);
-            from_f(static_cast<T *>(p.dV)[(row0 + j) * D + tx + 16 * c], dv[r][c]);
+            static_cast<float *>(p.dK)[(row0 + j) * D + tx + 16 * c] = dk[r][c] * p.scale;
+            static_cast<float *>(p.dV)[(row0 + j) * D + tx + 16 * c] = dv[r][c];
         }
     }
 }
 
 // dS summed over the batch for one 64 x 64 tile of pairs of one head.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) simt_dbias(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
     chain_begin();
@@ -425,10 +414,10 @@ __global__ void __launch_bounds__(kThreads) simt_dbias(const __grid_constant__ P
         if (j0 >= len) continue;
         const size_t row0 = ((size_t)b * p.heads + h) * p.n;
         __syncthreads();
-        load_tile<T, D>(slice<T>(p.K, b, kvh), p.K.st, j0, len, k_s, tid);
-        load_tile<T, D>(slice<T>(p.V, b, kvh), p.V.st, j0, len, v_s, tid);
-        load_tile<T, D>(slice<T>(p.Q, b, h), p.Q.st, i0, p.n, q_s, tid);
-        load_tile<T, D>(slice<T>(p.dO, b, h), p.dO.st, i0, p.n, o_s, tid);
+        load_tile<D>(slice(p.K, b, kvh), p.K.st, j0, len, k_s, tid);
+        load_tile<D>(slice(p.V, b, kvh), p.V.st, j0, len, v_s, tid);
+        load_tile<D>(slice(p.Q, b, h), p.Q.st, i0, p.n, q_s, tid);
+        load_tile<D>(slice(p.dO, b, h), p.dO.st, i0, p.n, o_s, tid);
         __syncthreads();
         float s[4][4], dp[4][4];
         int oq[4];
@@ -456,6 +445,21 @@ __global__ void __launch_bounds__(kThreads) simt_dbias(const __grid_constant__ P
         }
 }
 
+// No keys at all (either type): o = 0, lse = -inf; 16 bytes per thread.
+__global__ void __launch_bounds__(kThreads) no_keys(const __grid_constant__ Problem p, int esz) {
+    chain_begin();
+    const int pieces = p.d * esz / 16;
+    const size_t count = (size_t)p.B * p.heads * p.n * pieces;
+    for (size_t e = (size_t)blockIdx.x * kThreads + threadIdx.x; e < count; e += (size_t)gridDim.x * kThreads) {
+        const size_t row = e / pieces, bh = row / p.n;
+        const int piece = (int)(e % pieces), i = (int)(row % p.n), h = (int)(bh % p.heads), b = (int)(bh / p.heads);
+        char *o = static_cast<char *>(const_cast<void *>(p.O.p));
+        o += ((long long)b * p.O.sb + (long long)h * p.O.sh + (long long)i * p.O.st) * esz + 16 * piece;
+        *reinterpret_cast<uint4 *>(o) = make_uint4(0, 0, 0, 0);
+        if (piece == 0 && p.lse) p.lse[row] = -INFINITY;
+    }
+}
+
 template <auto kKernel>
 cudaError_t run(dim3 grid, int floats, const Problem &p, cudaStream_t s) {
     const int bytes = (floats + (p.bias.mode ? p.bias.entries : 0)) * (int)sizeof(float);
@@ -464,38 +468,40 @@ cudaError_t run(dim3 grid, int floats, const Problem &p, cudaStream_t s) {
     return launch_plain(kKernel, grid, kThreads, (size_t)bytes, s, p);
 }
 
-template <typename T, int D>
+template <int D>
 struct Simt {
     static constexpr int t = tile_floats<D>();
     static unsigned tiles(int x) { return (unsigned)((x + kTile - 1) / kTile); }
     static cudaError_t forward(const Problem &p, cudaStream_t s) {
-        return run<simt_forward<T, D>>(dim3(tiles(p.n), p.heads, p.B), 3 * t + kWeights, p, s);
+        return run<simt_forward<D>>(dim3(tiles(p.n), p.heads, p.B), 3 * t + kWeights, p, s);
     }
     static cudaError_t dq(const Problem &p, cudaStream_t s) {
-        return run<simt_dq<T, D>>(dim3(tiles(p.n), p.heads, p.B), 4 * t + kWeights, p, s);
+        return run<simt_dq<D>>(dim3(tiles(p.n), p.heads, p.B), 4 * t + kWeights, p, s);
     }
     static cudaError_t dkdv(const Problem &p, cudaStream_t s) {
-        return run<simt_dkdv<T, D>>(dim3(tiles(p.m), p.kv_heads, p.B), 4 * t + 2 * kWeights, p, s);
+        return run<simt_dkdv<D>>(dim3(tiles(p.m), p.kv_heads, p.B), 4 * t + 2 * kWeights, p, s);
     }
     static cudaError_t dbias(const Problem &p, cudaStream_t s) {
-        return run<simt_dbias<T, D>>(dim3(tiles(p.m) * tiles(p.n), p.b_splits, p.heads), 4 * t, p, s);
+        return run<simt_dbias<D>>(dim3(tiles(p.m) * tiles(p.n), p.b_splits, p.heads), 4 * t, p, s);
     }
 };
 
 }  // namespace
 
-#define LISA_ATTN_DISPATCH(fn)                                                                   \
-    (p.dtype == LISA_F32 ? (p.d == 16   ? Simt<float, 16>::fn(p, s)                              \
-                            : p.d == 32 ? Simt<float, 32>::fn(p, s)                              \
-                                        : Simt<float, 64>::fn(p, s))                             \
-                         : (p.d == 16   ? Simt<__nv_bfloat16, 16>::fn(p, s)                      \
-                            : p.d == 32 ? Simt<__nv_bfloat16, 32>::fn(p, s)                      \
-                                        : Simt<__nv_bfloat16, 64>::fn(p, s)))
+#define LISA_ATTN_DISPATCH(fn) \
+    (p.d == 16 ? Simt<16>::fn(p, s) : p.d == 32 ? Simt<32>::fn(p, s) : Simt<64>::fn(p, s))
 
 int simt_dbias_splits(int B, int heads, int n, int m) {
     // fewer tiles than SMs: share the batch out, a matrix for each part
     const long long tiles = (long long)heads * ((n + kTile - 1) / kTile) * ((m + kTile - 1) / kTile);
     return (int)std::max<long long>(1, std::min<long long>(152 / tiles, B));
+}
+
+cudaError_t launch_no_keys(const Problem &p, cudaStream_t s) {
+    const int esz = p.dtype == LISA_BF16 ? 2 : 4;
+    const size_t count = (size_t)p.B * p.heads * p.n * (p.d * esz / 16);
+    return launch_plain(no_keys, dim3((unsigned)std::min<size_t>((count + kThreads - 1) / kThreads, 152 * 8)), kThreads, 0,
+                        s, p, esz);
 }
 
 cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s) { return LISA_ATTN_DISPATCH(forward); }

@@ -212,6 +212,17 @@ def test_no_keys_at_all(lisa):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_no_keys_into_a_given_layout(lisa, dtype):
+    q = torch.randn(2, 3, 700, 32, device="cuda", dtype=dtype)
+    k = torch.empty(2, 1, 0, 32, device="cuda", dtype=dtype)
+    wide = torch.full((2, 700, 4, 32), 7.0, dtype=dtype, device="cuda")
+    lisa.cross_attention(q, k, k, out=wide[:, :, :3].transpose(1, 2))
+    assert not wide[:, :, :3].any() and (wide[:, :, 3] == 7).all()
+    _, lse = lisa.cross_attention(q, k, k, return_lse=True)
+    assert (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("B,heads,kv,m", [(1, 1, 1, 1), (1, 3, 3, 196), (5, 8, 2, 1000), (3, 16, 1, 130),
                                           (40, 4, 4, 63), (1, 12, 4, 4097), (2, 24, 1, 600)])
 def test_single_tokens(lisa, dtype, B, heads, kv, m):
