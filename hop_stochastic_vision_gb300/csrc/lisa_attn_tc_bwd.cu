@@ -1,6 +1,6 @@
 // lisa_attn_tc_bwd.cu -- the backward cross attention on the tensor cores (bf16).
 //
-// Three kernels of one shape, each a persistent CTA of 12 warps around 128 x 128
+// Three kernels of one shape, each a persistent CTA of 20 warps around 128 x 128
 // tiles of pairs whose scores and dP = dO V^T are products into tensor memory:
 //   dQ     128 queries against every key; dS goes back to tensor memory as bf16
 //          for dQ += dS K.  Also leaves delta_i for the two others: dO . O from
@@ -18,11 +18,17 @@
 // owner: no atomics, no fp32 dQ in memory, the same bits every time.
 //
 // Four warpgroups share a tile by columns, 32 each, a thread per row (with two of
-// 64 columns the schedulers had two warps each and issued one cycle in five).
+// 64 columns the schedulers had two warps each and issued one cycle in five:
+// dK, dV 88 us against 74, dQ 75 against 67 at 8 x 4096 x 4096).
 // The threads take S and dP into registers as soon as both are there, so the
 // next tile's products run under this tile's arithmetic.  Two barriers to wait for
 // and two to arrive at per tile: a wait costs some 100 cycles even when its phase
 // is long complete, and all warps pay it together.
+//
+// Bound by that arithmetic and its hand-overs: a tile costs about 1900 cycles in
+// dQ and 2150 in dK, dV, its products 768 and 1024; the warps issue on half of the
+// cycles, tensor cores 26% and 34% busy, DRAM below 8% (8 entries, 12 heads, 500
+// queries on up to 1500 keys: dQ 39 us, dK, dV 53, dbias 44).
 #include "lisa_attn_tc.cuh"
 #include "lisa_fold.cuh"
 

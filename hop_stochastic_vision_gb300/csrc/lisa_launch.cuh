@@ -2,7 +2,8 @@
 // it on the stream: the kernel's set-up overlaps that one's tail.  Every kernel
 // launched this way calls chain_begin() before it touches memory that another
 // kernel may have written (or may still read), so a chain of them orders like
-// plain launches.
+// plain launches.  It pays for the forward (a 56 x 56 pooled call 2 us), not between
+// the backward's persistent kernels (14 of 121 us lost): those launch plainly.
 #pragma once
 
 #include <mutex>

@@ -621,3 +621,35 @@ def test_a_pooled_stage_beside_the_linear_layer(lisa):
                       "dtable by the matrix")
     grads = lisa.backward(xq, xk, v, dq, (H, W), 3, alpha=alpha, beta=0.5)
     assert all(torch.isfinite(x).all() for x in grads)
+
+
+def test_bias_matrix_refusals(lisa):
+    b, _, _ = _matrix(lisa, (1, 20), (1, 24), LOG)
+    own = lisa.RelativeBias(b.table, (1, 1), (1, 24), cols=lisa.log_buckets(32, 128),
+                            query_start=torch.zeros(4, dtype=torch.int32, device="cuda"))
+    good = torch.zeros(3, 20, 24, device="cuda")
+    for call in (lambda: lisa.relative_bias(b, torch.float16), lambda: lisa.relative_bias(own),
+                 lambda: lisa.relative_bias(b, out=good.to(BF16)), lambda: lisa.relative_bias(b, out=good[:, :, :23]),
+                 lambda: lisa.relative_bias(b, out=good.cpu()), lambda: lisa.relative_bias_backward(b, good.double()),
+                 lambda: lisa.relative_bias_backward(b, good[:2]), lambda: lisa.relative_bias_backward(b, good.cpu()),
+                 lambda: lisa.relative_bias_backward(b, good.transpose(1, 2).contiguous().transpose(1, 2)),
+                 lambda: lisa.relative_bias_backward(own, good)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(lisa.LisaError):       # too small a workspace
+        lisa.relative_bias_backward(b, good, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    far = lisa.RelativeBias(torch.zeros(129 * 129, 3, device="cuda"), (65, 65), (65, 65), rows=lisa.exact_buckets(64),
+                            cols=lisa.exact_buckets(64))
+    with pytest.raises(lisa.LisaError):       # more offsets than the shared memory holds
+        lisa.relative_bias(far)
+
+
+def test_empty_batches(lisa):
+    for dtype in (F32, BF16):
+        q, k = torch.empty(0, 2, 5, 64, device="cuda", dtype=dtype), torch.empty(0, 1, 9, 64, device="cuda", dtype=dtype)
+        table = torch.randn(7, 2, device="cuda")
+        bias = lisa.RelativeBias(table, (1, 5), (1, 9), cols=lisa.exact_buckets(3))
+        out, lse = lisa.cross_attention(q, k, k, bias=bias, return_lse=True)
+        assert out.shape == q.shape and lse.shape == (0, 2, 5)
+        dq, dk, dv, dtable = lisa.cross_attention_backward(q, k, k, out, lse, out, bias=bias)
+        assert dq.shape == q.shape and dk.shape == k.shape and not dtable.any() and torch.isfinite(dtable).all()
