@@ -4,7 +4,7 @@
 // Forward, per 64 queries of one (batch, head): one pass over the keys in tiles
 // of 64 with the running maximum and sum of the softmax; scores and weights
 // stay in shared memory.  Backward: the dQ kernel walks the keys of 64 queries
-// and also leaves delta_i = sum_j p_ij dP_ij; the dK / dV kernel walks the
+// and also leaves delta_i = sum_j p_ij dP_ij / sum_j p_ij; the dK / dV kernel walks the
 // queries (and the heads that share the keys) of 64 keys; the bias kernel
 // walks the batch for one 64 x 64 tile of pairs and keeps the tile's dS sum in
 // registers, so the sum over the batch has a fixed order.
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
     load_tile<D>(slice(p.O, b, h), p.O.st, i0, p.n, q_s, tid);
     load_tile<D>(slice(p.dO, b, h), p.dO.st, i0, p.n, o_s, tid);
     __syncthreads();
-    float delta[4], exact[4], ref[4], acc[4][D / 16];
+    float delta[4], exact[4], total[4], ref[4], acc[4][D / 16];
     int oq[4];
     const size_t row0 = ((size_t)b * p.heads + h) * p.n;
     const int start = p.bias.mode ? bias_start(p.bias, b) : 0;
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
         for (int c = 0; c < D / 16; ++c)
             v = fmaf(q_s[(4 * ty + r) * (D + 4) + tx + 16 * c], o_s[(4 * ty + r) * (D + 4) + tx + 16 * c], v);
         delta[r] = half_sum(v);
-        exact[r] = 0.f;
+        exact[r] = total[r] = 0.f;
         ref[r] = row_ref(p.lse, row0 + i0 + 4 * ty + r, i0 + 4 * ty + r < p.n);
         oq[r] = p.bias.mode ? off_query(p.bias, min(i0 + 4 * ty + r, p.n - 1), start) : 0;
 #pragma unroll
@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
             for (int c = 0; c < 4; ++c) {
                 const float w = __expf(s[r][c] - ref[r]);
                 exact[r] = fmaf(w, dp[r][c], exact[r]);
+                total[r] += w;
                 p_s[(4 * ty + r) * (kTile + 4) + tx + 16 * c] = w * (dp[r][c] - delta[r]);
             }
         __syncwarp();
@@ -316,11 +317,12 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int i = i0 + 4 * ty + r;
-        const float e = half_sum(exact[r]);
+        const float e = half_sum(exact[r]), t = half_sum(total[r]);
         if (i >= p.n) continue;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) out[(size_t)i * D + tx + 16 * c] = acc[r][c] * p.scale;
-        if (tx == 0) p.delta[row0 + i] = e;
+        // over sum p, which takes the rounding of lse out: the dS of a row add up to 0
+        if (tx == 0) p.delta[row0 + i] = t > 0.f ? e / t : e;
     }
 }
 

@@ -5,7 +5,7 @@
 //   dQ     128 queries against every key; dS goes back to tensor memory as bf16
 //          for dQ += dS K.  Also leaves delta_i for the two others: dO . O from
 //          the rounded output (an error of one rounding of O against bf16
-//          results), or sum_j p dP in fp32 with a bias, since its gradient is fp32,
+//          results), or sum_j p dP / sum_j p in fp32 with a bias, since its gradient is fp32,
 //          and where all keys are one tile
 //   dK dV  128 keys against the queries of the heads that share them, the
 //          tile transposed (rows are keys): dV += P^T dO, dK += dS^T Q, the
@@ -61,6 +61,14 @@ struct BwdParams {
 
 __device__ __forceinline__ int tile_keys(int len, int t) { return min(kRows, len - t * kRows); }
 __device__ __forceinline__ int tile_cols(int keys) { return (keys + 15) & ~15; }
+
+// sum p dP / sum p from the strips' (sum p dP, sum p): the division takes the
+// rounding of lse out, so the dS of a row add up to 0, as they do when one far
+// bucket holds all of them (16000 rows of 6 keys: dtable 9e-6 off without it).
+__device__ __forceinline__ float quotient_of(float2 a, float2 b, float2 c, float2 d) {
+    const float total = (a.y + b.y) + (c.y + d.y);
+    return total > 0.f ? ((a.x + b.x) + (c.x + d.x)) / total : (a.x + b.x) + (c.x + d.x);
+}
 
 __device__ __forceinline__ float neg_lse2(float l) {
     return fabsf(l) > kMaxLse ? -INFINITY : -l * kLog2e;   // rows without keys among them: every weight 2^-inf = 0
@@ -153,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) DqBars bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
-    __shared__ float other[3][kRows], rows_delta[kRows];
+    __shared__ float2 other[3][kRows];
+    __shared__ float rows_delta[kRows];
     const Problem &p = x.p;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             math_barrier();   // also: the strips of the previous item's delta have been read
-            float delta = w.tiles > 1 ? rows_delta[wt] : 0.f, exact = 0.f;
+            float delta = w.tiles > 1 ? rows_delta[wt] : 0.f, exact = 0.f, total = 0.f;
             int oq = 0, oq_lo = 0;
             if (kBias) {
                 const int start = bias_start(p.bias, w.b);
@@ -356,18 +365,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t ds[kStrip / 2];
                 if (kBias || single) {   // delta from the unrounded weights: the bias gradient wants it, and few keys,
                                          // where dP - delta cancels most, do without the rounding of O
-                    float e0 = 0.f, e1 = 0.f;
+                    float e0 = 0.f, e1 = 0.f, t0 = 0.f, t1 = 0.f;
 #pragma unroll
                     for (int e = 0; e < kStrip; e += 2) {
                         mul2(dp[e], dp[e + 1], s[e], s[e + 1], dp[e], dp[e + 1]);
                         add2(e0, e1, e0, e1, dp[e], dp[e + 1]);
+                        add2(t0, t1, t0, t1, s[e], s[e + 1]);
                     }
                     exact += e0 + e1;
+                    total += t0 + t1;
                     if (single) {   // the strips' shares, where the item's O is: nothing reads that now
-                        float *share = reinterpret_cast<float *>(sm + (3 * cq.slot + 2) * kTileBytes) + wt;
-                        share[strip * kRows] = exact;
+                        float2 *share = reinterpret_cast<float2 *>(sm + (3 * cq.slot + 2) * kTileBytes) + wt;
+                        share[strip * kRows] = make_float2(exact, total);
                         math_barrier();
-                        delta = (share[0] + share[kRows]) + (share[2 * kRows] + share[3 * kRows]);
+                        delta = quotient_of(share[0], share[kRows], share[2 * kRows], share[3 * kRows]);
                     }
 #pragma unroll
                     for (int e = 0; e < kStrip; e += 2) {
@@ -397,9 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 arrive_warp(&bar.ds_full, lane);
             }
             if (kBias && !single) {   // the strips' shares of delta
-                if (strip > 0) other[strip - 1][wt] = exact;
+                if (strip > 0) other[strip - 1][wt] = make_float2(exact, total);
                 math_barrier();
-                if (strip == 0 && in) p.delta[row] = (exact + other[0][wt]) + (other[1][wt] + other[2][wt]);
+                if (strip == 0 && in)
+                    p.delta[row] = quotient_of(make_float2(exact, total), other[0][wt], other[1][wt], other[2][wt]);
             } else if (strip == 0 && in) {
                 p.delta[row] = delta;
             }
@@ -1037,8 +1049,8 @@ cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {
     x.items = (int)items;
     x.first = 1;
     for (x.q_slots = 2;; --x.q_slots) {
-        // with a bias the kernel holds 2192 bytes of its own
-        const int left = kSmemBudget - (lut > 0 ? 256 : 0) - 3 * x.q_slots * kTileBytes - lut - keys - 1024;
+        // with a bias the kernel holds 3728 bytes of its own
+        const int left = kSmemBudget - (lut > 0 ? 1792 : 0) - 3 * x.q_slots * kTileBytes - lut - keys - 1024;
         x.stages = std::min(kMaxStages, left / (2 * kTileBytes));
         if (x.stages >= 2 || x.q_slots == 1) break;
     }
