@@ -34,6 +34,7 @@ constexpr int kFwdThreads = 384;
 constexpr int kRegsSoftmax = 208, kRegsControl = 88;
 constexpr int kMaxStages = 5;
 constexpr float kSlack = 8.f;
+constexpr float kFarRef = 0x1p24f;
 
 struct FwdParams {
     Problem p;
@@ -76,6 +77,7 @@ __device__ __forceinline__ int tile_cols(int keys) { return (keys + 15) & ~15; }
 // A row's state over the tiles of an item, and what its bias needs.
 struct RowState {
     float ref, sum;
+    float limit;     // a maximum above it moves the reference: ref + kSlack, -inf where ref is far from 0
     int oq, oq_lo;
 };
 
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 continue;
             }
             const int i = w.q0 + t * kRows + wt;
-            RowState r{-INFINITY, 0.f, 0, 0};
+            RowState r{-INFINITY, 0.f, -INFINITY, 0, 0};
             if (kBias) {
                 const int start = bias_start(p.bias, w.b);
                 r.oq = off_query(p.bias, kBias == 2 ? min(i, p.n - 1) : i, start);
@@ -315,12 +317,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     top = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul, add);
                 }
                 const bool first = j == w.t0;
+                // The maximum's rounding in `ref` is a power of two common to the row's weights and goes out with the sum
+                // while it is small.  Further out (half a unit in the last place of 2^24 is 1, of 2^33 is 512) the scores
+                // are rounded as the maximum was, in every tile, so that the largest weight is 2^0 whatever their size.
+                auto refer = [&](float now) __attribute__((always_inline)) {
+                    r.ref = now;
+                    const bool far = fabsf(now) > kFarRef;
+                    r.limit = far ? -INFINITY : now + kSlack;
+                    if (kBias != 2 && __any_sync(0xFFFFFFFFu, far)) {
+#pragma unroll
+                        for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], mul, add);
+                        mul = 1.f;
+                        add = 0.f;
+                    }
+                };
                 if (first) {
-                    r.ref = top;
-                } else if (__any_sync(0xFFFFFFFFu, top > r.ref + kSlack)) {
+                    refer(top);
+                } else if (__any_sync(0xFFFFFFFFu, top > r.limit)) {
                     const float now = fmaxf(r.ref, top);
                     const float f = r.ref == -INFINITY ? 0.f : ex2_approx(r.ref - now);
-                    r.ref = now;
+                    refer(now);
                     r.sum *= f;
                     wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
                     tc_fence_after();

@@ -653,3 +653,51 @@ def test_empty_batches(lisa):
         assert out.shape == q.shape and lse.shape == (0, 2, 5)
         dq, dk, dv, dtable = lisa.cross_attention_backward(q, k, k, out, lse, out, bias=bias)
         assert dq.shape == q.shape and dk.shape == k.shape and not dtable.any() and torch.isfinite(dtable).all()
+
+
+# ------------------------------------------------------------------ scores far from 0
+
+class Far(Case):
+    """Scores 2^exponent r_i k_j with whole r_i, k_j of 8 bits: exact in fp32, in every order. One key of a row stands at
+    least 2^exponent 128 above the rest (2^12 and more), whose weights are 0 in any precision: o is that key's value and lse
+    its score."""
+
+    def __init__(self, lisa, dtype, n, m, exponent, *, bias=None, signs="both"):
+        super().__init__(lisa, dtype, 2, 2, 2, n, m, 64, bias=bias, scale=1.0)
+        g = torch.Generator().manual_seed(exponent)
+        r = torch.randint(128, 256, (2, 2, n), generator=g) * (2 * torch.randint(0, 2, (2, 2, n), generator=g) - 1)
+        w = torch.randint(-100, 100, (2, 2, m), generator=g)
+        top = torch.stack([torch.randperm(m, generator=g)[:2] for _ in range(4)]).view(2, 2, 2)
+        w.scatter_(2, top, torch.tensor([127, -127]).expand(2, 2, 2))
+        if signs == "negative":     # every score of a row below 0
+            r, w = -r.abs(), w + 128
+        self.q_ref, self.k_ref = torch.zeros_like(self.q_ref), torch.zeros_like(self.k_ref)
+        self.q_ref[..., 5], self.k_ref[..., 5] = (r * 2.0 ** exponent).to(dtype), w.to(dtype)
+        assert torch.equal(self.q_ref[..., 5].double(), r.double() * 2.0 ** exponent)
+        self.q.copy_(self.q_ref)
+        self.k.copy_(self.k_ref)
+        self.s = self.q_ref.double() @ self.k_ref.double().transpose(-1, -2)
+        self.best = self.s.argmax(-1)
+        if bias is not None:
+            self.s += self.table.double().t()[:, self.index]
+
+
+@pytest.mark.parametrize("signs", ["both", "negative"])
+@pytest.mark.parametrize("exponent", [5, 15, 20, 26, 60, 100])
+@pytest.mark.parametrize("dtype,n,m,bias", [(BF16, 150, 300, None), (BF16, 150, 1100, None), (BF16, 300, 90, None),
+                                            (BF16, 150, 1100, LOG), (BF16, 150, 300, NEAR), (BF16, 1, 700, None),
+                                            (BF16, 3, 700, LOG), (F32, 70, 300, None), (F32, 70, 300, LOG)])
+def test_finite_scores_of_any_size(lisa, dtype, n, m, bias, exponent, signs):
+    """Up to 2^116: the outputs stay those of a softmax. lse is off by the roundings of log2(e) times the scale, of the
+    score, of its product with ln 2 and of ln 2 itself, 2^-24 each, and one in fp32 beside them; the other keys' part of it
+    (below 2^-4000) and log2 of a sum of 1 are nothing."""
+    c = Far(lisa, dtype, n, m, exponent, bias=bias, signs=signs)
+    out, lse = c.forward()
+    value = c.v_ref.gather(2, c.best[..., None].expand(-1, -1, -1, 64))
+    # its weight may stand at another power of two than 1 and is rounded for the product, the result once more
+    off = 2.02 * 2.0 ** -8 if dtype == BF16 else 4 * 2.0 ** -24
+    assert ((out.double().cpu() - value.double()).abs() <= off * value.double().abs()).all()
+    want = c.s.amax(-1)
+    assert ((lse.double().cpu() - want).abs() <= 5.1 * 2.0 ** -24 * (want.abs() + 8)).all()
+    if n > 1 and exponent >= 15:     # |lse| > 2^20: no gradient
+        assert not any(x.any() for x in c.backward(out, lse))
