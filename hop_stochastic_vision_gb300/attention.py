@@ -160,10 +160,7 @@ class RelativeBias:
         self.starts = None
         start = (0, 0)
         if isinstance(query_start, torch.Tensor):
-            if not (query_start.is_cuda and query_start.dtype == torch.int32 and query_start.is_contiguous()
-                    and query_start.dim() == 1 and query_start.device == table.device):
-                raise ValueError("query_start must be a pair of ints or a contiguous int32 CUDA tensor [B]")
-            self.starts = query_start
+            self.starts = query_start   # checked with the table, below
         else:
             start = (int(query_start[0]), int(query_start[1]))
         self.struct = lisa_rel_bias(None, *self.q_grid, *self.k_grid, int(key_step[0]), int(key_step[1]), *start,
@@ -181,8 +178,14 @@ class RelativeBias:
                 raise ValueError("the bias table must stay a contiguous fp32 CUDA tensor [%d, %d]" % (rows, self.heads))
             s.table = table.data_ptr()
             self.index = table.get_device()
-        if self.starts is not None and self.starts.data_ptr() != s.starts:
-            s.starts = self.starts.data_ptr()
+        starts = self.starts
+        if starts is None:
+            s.starts = None
+        else:
+            if not (starts.get_device() == self.index and starts.dtype == torch.int32 and starts.is_contiguous()
+                    and starts.dim() == 1):
+                raise ValueError("query_start must be a pair of ints or a contiguous int32 CUDA tensor [B]")
+            s.starts = starts.data_ptr()
         return s
 
 

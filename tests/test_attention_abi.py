@@ -177,3 +177,40 @@ def test_tensor_calls_refuse_what_is_not_on_a_gpu():
         lisa.cross_attention(x.half(), x.half(), x.half())
     with pytest.raises(ValueError):
         lisa.RelativeBias(torch.zeros(32, 4), (1, 4), (1, 4), cols=lisa.log_buckets(32, 128))
+
+
+# ------------------------------------------------------------------ a bias whose tensors change between calls
+
+class OnGpu(torch.Tensor):
+    """A tensor of the host that calls itself one of cuda:0, for checks that launch nothing."""
+    is_cuda = True
+    device = property(lambda self: torch.device("cuda", 0))
+
+    def get_device(self):
+        return 0
+
+
+def _on_gpu(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+def _tokens(starts):
+    return lisa.RelativeBias(_on_gpu(32, 4), (1, 1), (1, 9), cols=lisa.log_buckets(32, 128), query_start=starts)
+
+
+BAD_STARTS = {"int64": lambda: _on_gpu(6, dtype=torch.int64), "host": lambda: torch.zeros(6, dtype=torch.int32),
+              "strided": lambda: _on_gpu(12, dtype=torch.int32)[::2], "matrix": lambda: _on_gpu(6, 1, dtype=torch.int32)}
+
+
+@pytest.mark.parametrize("what", BAD_STARTS)
+def test_starts_are_checked_whenever_they_are_used(what):
+    with pytest.raises(ValueError):
+        _tokens(BAD_STARTS[what]())
+    b = _tokens(_on_gpu(6, dtype=torch.int32))
+    b.starts = BAD_STARTS[what]()
+    with pytest.raises(ValueError):
+        b.current()
+    good = b.starts = _on_gpu(7, dtype=torch.int32)
+    assert b.current().starts == good.data_ptr()
+    b.starts = None
+    assert b.current().starts is None
