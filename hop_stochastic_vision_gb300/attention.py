@@ -152,7 +152,8 @@ class RelativeBias:
             raise ValueError("the bias table has %d rows, the rules give %d buckets"
                              % (table.shape[0], rows.buckets * cols.buckets))
         self.table = table
-        self.heads = int(table.shape[1])
+        self.shape = (int(table.shape[0]), int(table.shape[1]))
+        self.heads = self.shape[1]
         self.q_grid = (int(q_grid[0]), int(q_grid[1]))
         self.k_grid = (int(k_grid[0]), int(k_grid[1]))
         self.n = self.q_grid[0] * self.q_grid[1]
@@ -171,13 +172,10 @@ class RelativeBias:
         """The C struct, with the table and the starts where they are now (an
         optimiser or a module may have moved the storage behind them)."""
         s, table = self.struct, self.table
-        if table.data_ptr() != s.table:
-            rows = s.rows.buckets * s.cols.buckets
-            if not (table.is_cuda and table.dtype == torch.float32 and table.is_contiguous()
-                    and table.shape == (rows, self.heads)):
-                raise ValueError("the bias table must stay a contiguous fp32 CUDA tensor [%d, %d]" % (rows, self.heads))
-            s.table = table.data_ptr()
-            self.index = table.get_device()
+        if not (table.is_cuda and table.dtype == torch.float32 and table.is_contiguous() and table.shape == self.shape):
+            raise ValueError("the bias table must stay a contiguous fp32 CUDA tensor [%d, %d]" % self.shape)
+        s.table = table.data_ptr()
+        self.index = table.get_device()
         starts = self.starts
         if starts is None:
             s.starts = None
@@ -344,7 +342,7 @@ def _backward(stream, q, shape, kv_shape, head, saved, tail, bias, workspace):
     dq = torch.empty(shape, dtype=dtype, device=device)
     dk = torch.empty(kv_shape, dtype=dtype, device=device)
     dv = torch.empty(kv_shape, dtype=dtype, device=device)
-    dtable = None if bias is None else torch.empty_like(bias.table)
+    dtable = None if bias is None else torch.empty(bias.shape, dtype=torch.float32, device=device)
     B, heads, kv_heads, n, m, d, _, _, struct, dt = tail
     lib = _library()
     need = lib.lisa_cross_attention_backward_workspace_bytes(B, heads, kv_heads, n, m, d, struct, dt)
@@ -399,7 +397,7 @@ def relative_bias(bias: RelativeBias, dtype: torch.dtype = torch.float32, *, out
 
 
 def _matrix_backward(stream, bias, dbias, workspace):
-    dtable = torch.empty_like(bias.table)
+    dtable = torch.empty(bias.shape, dtype=torch.float32, device=dbias.device)
     lib = _library()
     keep, ws, nbytes = _workspace(workspace, lib.lisa_relative_bias_backward_workspace_bytes(bias.struct, bias.heads),
                                   dbias.device)

@@ -214,3 +214,22 @@ def test_starts_are_checked_whenever_they_are_used(what):
     assert b.current().starts == good.data_ptr()
     b.starts = None
     assert b.current().starts is None
+
+
+SAME_PLACE = {"fewer rows": lambda t: t[:20], "transposed": lambda t: t.t(), "one dimension": lambda t: t.view(-1),
+              "other type": lambda t: t.view(torch.int32), "other shape": lambda t: t.view(4, 32),
+              "fewer heads": lambda t: t[:, :3], "host": lambda t: t.as_subclass(torch.Tensor)}
+
+
+@pytest.mark.parametrize("how", SAME_PLACE)
+def test_the_table_is_checked_whenever_it_is_used(how):
+    """Another tensor at the same address is another table."""
+    table = _on_gpu(32, 4)
+    b = lisa.RelativeBias(table, (1, 5), (1, 9), cols=lisa.log_buckets(32, 128))
+    b.table = SAME_PLACE[how](table)
+    assert b.table.data_ptr() == table.data_ptr()
+    for use in (b.current, lambda: lisa.relative_bias(b), lambda: lisa.relative_bias_backward(b, table)):
+        with pytest.raises(ValueError):
+            use()
+    b.table = table
+    assert b.current().table == table.data_ptr()
