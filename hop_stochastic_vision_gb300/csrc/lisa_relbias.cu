@@ -452,10 +452,13 @@ bool fold_plan(const lisa_rel_bias &b, int heads, int parts, FoldDev &f) {
     // rows of a grid that 128 of its tokens can touch
     const int qr = std::min(b.q_rows, (kFoldTile - 2) / b.q_cols + 2), kr = std::min(b.k_rows, (kFoldTile - 2) / b.k_cols + 2);
     f.nR = qr + kr - 1;
-    const int width = std::min(kFoldTile, b.q_cols) + std::min(kFoldTile, b.k_cols) - 1;
+    // columns that they can span: 128 tokens that cross a row's end, all of the grid's
+    const auto span = [](int rows, int cols) { return rows == 1 ? std::min(kFoldTile, cols) : cols; };
+    const int width = span(b.q_rows, b.q_cols) + span(b.k_rows, b.k_cols) - 1;
     f.K = dev.cols.log_rule ? b.cols.buckets : std::min(b.cols.buckets, width);
-    f.units = f.nR * width;
-    return f.units <= kMaxFoldUnits && f.qtiles <= 65535 && (long long)heads * parts <= 65535 && (long long)f.qtiles * f.ktiles < (1 << 30);
+    const long long units = (long long)f.nR * width;
+    f.units = (int)std::min<long long>(units, kMaxFoldUnits);
+    return units <= kMaxFoldUnits && f.qtiles <= 65535 && (long long)heads * parts <= 65535 && (long long)f.qtiles * f.ktiles < (1 << 30);
 }
 
 size_t fold_bytes(const FoldDev &f) {

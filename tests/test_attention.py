@@ -701,3 +701,29 @@ def test_finite_scores_of_any_size(lisa, dtype, n, m, bias, exponent, signs):
     assert ((lse.double().cpu() - want).abs() <= 5.1 * 2.0 ** -24 * (want.abs() + 8)).all()
     if n > 1 and exponent >= 15:     # |lse| > 2^20: no gradient
         assert not any(x.any() for x in c.backward(out, lse))
+
+
+# ------------------------------------------------------------------ grids wider than a tile
+
+WIDE = [((2, 200), (2, 200), ("exact", 199)), ((3, 130), (1, 129), ("exact", 129)), ((2, 300), (3, 150), ("exact", 40)),
+        ((2, 200), (2, 150), ("log", 32, 128)), ((1, 1), (2, 500), ("log", 32, 128)), ((3, 2), (5, 380), ("exact", 379)),
+        ((2, 400), (2, 700), ("exact", 699))]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("q,k,cols", WIDE)
+def test_bias_gradient_of_grids_wider_than_a_tile(lisa, dtype, q, k, cols):
+    """Whole numbers 1 to 8: sums below 2^24, so exact, and one pair too few or too many shows."""
+    b, table, index = _matrix(lisa, q, k, {"rows": ("exact", max(q[0], k[0]) - 1), "cols": cols})
+    x = torch.randint(1, 9, (3, b.n, b.m), generator=torch.Generator().manual_seed(7))
+    want = torch.zeros(table.shape, dtype=torch.int64)
+    for h in range(3):
+        want[:, h].index_add_(0, index.reshape(-1), x[h].reshape(-1))
+    assert want.max() < 1 << 24
+    assert torch.equal(lisa.relative_bias_backward(b, x.to(dtype).cuda()).cpu().long(), want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("q,k,cols", [WIDE[0], WIDE[3], WIDE[5], WIDE[6]])
+def test_attention_on_grids_wider_than_a_tile(lisa, dtype, q, k, cols):
+    Case(lisa, dtype, 2, 2, 1, q, k, 64, bias={"rows": ("exact", max(q[0], k[0]) - 1), "cols": cols}).check()

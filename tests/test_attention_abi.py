@@ -233,3 +233,22 @@ def test_the_table_is_checked_whenever_it_is_used(how):
             use()
     b.table = table
     assert b.current().table == table.data_ptr()
+
+
+@pytest.mark.parametrize("q,k", [((2, 200), (2, 200)), ((3, 130), (1, 129)), ((1, 1), (127, 129)), ((2, 1), (2, 300)),
+                                 ((3, 2), (5, 380))])
+@pytest.mark.parametrize("rule", ["exact", "log"])
+def test_the_gradients_workspace_holds_what_a_tile_of_a_wide_grid_spans(q, k, rule):
+    """128 tokens that cross the end of a row stand in all columns of a grid, however many those are."""
+    n, m = q[0] * q[1], k[0] * k[1]
+
+    def spans(count, cols):        # per tile: the rows and the columns of its tokens
+        tiles = [[(t // cols, t % cols) for t in range(t0, min(t0 + 128, count))] for t0 in range(0, count, 128)]
+        return [(max(r) - min(r), max(c) - min(c)) for r, c in (zip(*t) for t in tiles)]
+
+    cols = att.exact_buckets(max(q[1], k[1]) - 1) if rule == "exact" else att.log_buckets(32, 128)
+    rows = att.exact_buckets(max(q[0], k[0]) - 1)
+    most = max((a[0] + b[0] + 1) * (min(a[1] + b[1] + 1, cols.buckets) if rule == "exact" else 32)
+               for a in spans(n, q[1]) for b in spans(m, k[1]))
+    tiles = -(-n // 128) * -(-m // 128)
+    assert att.lisa_relative_bias_backward_workspace_bytes(_bias(q, k, rows, cols), 3) >= 3 * tiles * most * 4
