@@ -48,6 +48,17 @@ struct FwdParams {
     int off_out, off_lut, off_keys;   // dynamic shared memory, behind Q and the ring
 };
 
+// Dynamic shared memory: the barriers and what else is static fit in 1 KB.  Behind the tiles come the softmax warps'
+// staging blocks, the offsets (with the four zeros behind them) and the keys' offsets, packed: the largest grids' leave
+// room for two stages with 992 bytes to spare.
+constexpr int kFwdSmem = 226 * 1024;
+constexpr int kStaging = 8 * 4096;
+constexpr int offsets_bytes_smem(int entries) { return entries ? (entries * 4 + 32 + 15) / 16 * 16 : 0; }
+constexpr int keys_bytes_smem(int m) { return (m + kRows - 1) / kRows * kRows * 2; }
+static_assert((2 + 2 * 2) * kTileBytes + kStaging + offsets_bytes_smem(LISA_MAX_OFFSETS) +
+                      keys_bytes_smem(LISA_MAX_OFFSETS) + 1024 <= kFwdSmem,
+              "every bias that the argument checks accept has room for two stages");
+
 struct FwdBars {
     uint64_t q_full[2], q_empty[2], k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages], v_empty[kMaxStages];
     uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], lut_full;
@@ -504,15 +515,13 @@ cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {
     x.div_qtiles = fast_div(x.qtiles);
     x.div_B = fast_div(p.B);
     x.div_group = fast_div(p.group);
-    const int lut = offsets_smem(p.bias);
-    const int keys = p.bias.mode == 2 ? round1k((p.m + 127) / 128 * 256) : 0;
-    const int out = 8 * 4096;   // a staging block for each softmax warp
-    const int fixed = 2 * kTileBytes + out + lut + keys + 1024;
+    const int lut = offsets_bytes_smem(p.bias.mode ? p.bias.entries + 2 * p.bias.pad : 0);
+    const int keys = p.bias.mode == 2 ? keys_bytes_smem(p.m) : 0;
+    const int fixed = 2 * kTileBytes + kStaging + lut + keys + 1024;
     const int tiles = (p.m + kRows - 1) / kRows;
-    x.stages = std::min(std::min(kMaxStages, (kSmemBudget - fixed) / (2 * kTileBytes)), std::max(2, tiles + 1));
-    if (x.stages < 2) return cudaErrorInvalidValue;
+    x.stages = std::min(std::min(kMaxStages, (kFwdSmem - fixed) / (2 * kTileBytes)), std::max(2, tiles + 1));
     x.off_out = (2 + 2 * x.stages) * kTileBytes;
-    x.off_lut = x.off_out + out;
+    x.off_lut = x.off_out + kStaging;
     x.off_keys = x.off_lut + lut;
     const int bytes = x.off_keys + keys + 1024;
     const unsigned grid = (unsigned)std::min(x.items, sms());

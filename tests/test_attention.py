@@ -727,3 +727,11 @@ def test_bias_gradient_of_grids_wider_than_a_tile(lisa, dtype, q, k, cols):
 @pytest.mark.parametrize("q,k,cols", [WIDE[0], WIDE[3], WIDE[5], WIDE[6]])
 def test_attention_on_grids_wider_than_a_tile(lisa, dtype, q, k, cols):
     Case(lisa, dtype, 2, 2, 1, q, k, 64, bias={"rows": ("exact", max(q[0], k[0]) - 1), "cols": cols}).check()
+
+
+@pytest.mark.parametrize("q,k,how", [((1, 1), (127, 129), None), ((1, 1), (16384, 1), ("exact", 50)),
+                                     ((1, 32), (2, 8161), None)])
+def test_every_grid_of_the_most_offsets_launches(lisa, q, k, how):
+    """16383 and 16384 offsets with 16322 to 16384 keys: offsets and key offsets at their largest at once."""
+    bias = _grid(q, k) if how is None else {"rows": how, "cols": ("exact", 0)}
+    Case(lisa, BF16, 1, 1, 1, q, k, 64, bias=bias).check()
