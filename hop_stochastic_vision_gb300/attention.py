@@ -12,7 +12,7 @@ import math
 
 import torch
 
-from .lisa import LISA_BF16, LISA_F32, LISA_OK, LisaError, load
+from .lisa import LISA_BF16, LISA_ERR_UNSUPPORTED, LISA_F32, LISA_OK, LisaError, load
 
 LISA_BUCKETS_EXACT = 0
 LISA_BUCKETS_LOG = 1
@@ -119,15 +119,23 @@ def lisa_cross_attention_backward(Q, qs, K, ks, V, vs, O, os, lse, dO, dos, dQ, 
 _DTYPES = {torch.float32: LISA_F32, torch.bfloat16: LISA_BF16}
 
 
+def _int32(x) -> int:
+    """x as one of the C ABI's 32-bit numbers (ctypes would drop the bits above)."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError("%d is beyond 32 bits" % x)
+    return x
+
+
 def exact_buckets(max_distance: int) -> lisa_axis_rule:
     """One bucket for each offset -D .. D of an axis; farther ones share the outermost."""
-    return lisa_axis_rule(LISA_BUCKETS_EXACT, 2 * int(max_distance) + 1, int(max_distance))
+    return lisa_axis_rule(LISA_BUCKETS_EXACT, _int32(2 * int(max_distance) + 1), _int32(max_distance))
 
 
 def log_buckets(buckets: int, max_distance: int) -> lisa_axis_rule:
     """``buckets`` of an axis, half to each side: near offsets one by one, farther
     ones in geometrically growing buckets up to ``max_distance``."""
-    return lisa_axis_rule(LISA_BUCKETS_LOG, int(buckets), int(max_distance))
+    return lisa_axis_rule(LISA_BUCKETS_LOG, _int32(buckets), _int32(max_distance))
 
 
 class RelativeBias:
@@ -154,8 +162,8 @@ class RelativeBias:
         self.table = table
         self.shape = (int(table.shape[0]), int(table.shape[1]))
         self.heads = self.shape[1]
-        self.q_grid = (int(q_grid[0]), int(q_grid[1]))
-        self.k_grid = (int(k_grid[0]), int(k_grid[1]))
+        self.q_grid = (_int32(q_grid[0]), _int32(q_grid[1]))
+        self.k_grid = (_int32(k_grid[0]), _int32(k_grid[1]))
         self.n = self.q_grid[0] * self.q_grid[1]
         self.m = self.k_grid[0] * self.k_grid[1]
         self.starts = None
@@ -163,9 +171,9 @@ class RelativeBias:
         if isinstance(query_start, torch.Tensor):
             self.starts = query_start   # checked with the table, below
         else:
-            start = (int(query_start[0]), int(query_start[1]))
-        self.struct = lisa_rel_bias(None, *self.q_grid, *self.k_grid, int(key_step[0]), int(key_step[1]), *start,
-                                    None, rows, cols)
+            start = (_int32(query_start[0]), _int32(query_start[1]))
+        self.struct = lisa_rel_bias(None, *self.q_grid, *self.k_grid, _int32(key_step[0]), _int32(key_step[1]),
+                                    *start, None, rows, cols)
         self.current()
 
     def current(self) -> lisa_rel_bias:
@@ -283,6 +291,8 @@ def _prepare(q, k, v, kv_lens, bias, scale):
     kv_heads, m = kv_shape[1], kv_shape[2]
     if kv_shape[0] != B or kv_shape[3] != d or v.shape != kv_shape:
         raise ValueError("k and v must be [B, kv_heads, m, d] for q [B, heads, n, d]")
+    if max(shape) >> 31 or max(kv_shape) >> 31:   # the call itself refuses far less, if it gets to see it
+        raise LisaError(LISA_ERR_UNSUPPORTED)
     lens = struct = None
     if kv_lens is not None:
         if not (kv_lens.get_device() == index and kv_lens.dtype == torch.int32 and kv_lens.is_contiguous()

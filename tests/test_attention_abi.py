@@ -252,3 +252,34 @@ def test_the_gradients_workspace_holds_what_a_tile_of_a_wide_grid_spans(q, k, ru
                for a in spans(n, q[1]) for b in spans(m, k[1]))
     tiles = -(-n // 128) * -(-m // 128)
     assert att.lisa_relative_bias_backward_workspace_bytes(_bias(q, k, rows, cols), 3) >= 3 * tiles * most * 4
+
+
+BEYOND = 1 << 32       # times anything: 0 in 32 bits
+
+
+@pytest.mark.parametrize("which", ["queries", "keys", "batch", "heads"])
+def test_sizes_beyond_32_bits_are_refused(which):
+    many = {"queries": (1, 1, BEYOND + 1, 16), "keys": (1, 1, 1, 16), "batch": (BEYOND + 1, 1, 1, 16),
+            "heads": (1, BEYOND + 1, 1, 16)}[which]
+    q = _on_gpu(1, 1, 1, 16).expand(*many)
+    k = {"queries": _on_gpu(1, 1, 1, 16), "keys": _on_gpu(1, 1, 1, 16).expand(1, 1, BEYOND + 1, 16)}.get(which, q)
+    for call in (lambda: lisa.cross_attention(q, k, k, out=q),
+                 lambda: lisa.cross_attention_backward(q, k, k, q, _on_gpu(1).expand(q.shape[:3]), q)):
+        with pytest.raises(lisa.LisaError) as e:
+            call()
+        assert e.value.status == UNS
+
+
+@pytest.mark.parametrize("over", [dict(q_grid=(1, BEYOND + 5)), dict(k_grid=(BEYOND + 1, 9)), dict(key_step=(1, BEYOND + 1)),
+                                  dict(query_start=(0, BEYOND)), dict(query_start=(-BEYOND - 1, 0))])
+def test_positions_beyond_32_bits_are_refused(over):
+    args = {**dict(q_grid=(1, 5), k_grid=(1, 9), cols=lisa.log_buckets(32, 128)), **over}
+    with pytest.raises(ValueError):
+        lisa.RelativeBias(_on_gpu(32, 4), **args)
+
+
+def test_bucket_rules_beyond_32_bits_are_refused():
+    for call in (lambda: lisa.exact_buckets(BEYOND), lambda: lisa.exact_buckets(1 << 30),
+                 lambda: lisa.log_buckets(BEYOND + 32, 128), lambda: lisa.log_buckets(32, BEYOND + 128)):
+        with pytest.raises(ValueError):
+            call()
