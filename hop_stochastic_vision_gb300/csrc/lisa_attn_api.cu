@@ -357,11 +357,12 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
     if (!O || !aligned16(O) || !good_strides(o_strides, B, heads, n, d, esz, true)) return LISA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return LISA_ERR_INVALID_ARG;
     const Span outs[2] = {Span(O, extent(o_strides, B, heads, n, d, esz)), Span(lse, lse ? (size_t)B * heads * n * 4 : 0)};
-    const Span ins[5] = {Span(Q, extent(q_strides, B, heads, n, d, esz)),
+    const Span ins[6] = {Span(Q, extent(q_strides, B, heads, n, d, esz)),
                          Span(K, m > 0 ? extent(k_strides, B, kv_heads, m, d, esz) : 0),
                          Span(V, m > 0 ? extent(v_strides, B, kv_heads, m, d, esz) : 0),
                          Span(kv_lens, kv_lens ? (size_t)B * 4 : 0),
-                         Span(bias ? bias->table : nullptr, p.bias.mode ? table_floats(*bias, heads) * 4 : 0)};
+                         Span(bias ? bias->table : nullptr, p.bias.mode ? table_floats(*bias, heads) * 4 : 0),
+                         Span(p.bias.starts, p.bias.starts ? (size_t)B * 4 : 0)};
     if (outs[0].meets(outs[1])) return LISA_ERR_INVALID_ARG;
     for (const Span &x : outs)
         for (const Span &in : ins)
@@ -417,40 +418,43 @@ extern "C" lisa_status lisa_cross_attention_backward(
     const size_t esz = dtype == LISA_BF16 ? 2 : 4;
     const size_t dq_bytes = (size_t)B * heads * n * d * esz, dk_bytes = (size_t)B * kv_heads * m * d * esz;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (dq_bytes == 0 || dk_bytes == 0) {   // nothing to differentiate: what there is of the gradients is 0
-        if ((dq_bytes && !dQ) || (dk_bytes && (!dK || !dV))) return LISA_ERR_INVALID_ARG;
-        if (bias) {
-            AxisDev a;   // the table's size has to make sense before it is written
-            if (axis_dev(bias->rows, a) != LISA_OK || axis_dev(bias->cols, a) != LISA_OK) return LISA_ERR_INVALID_ARG;
-        }
+    const bool empty = dq_bytes == 0 || dk_bytes == 0;
+    if (empty && bias) {   // the table's size has to make sense before it is written
+        AxisDev a;
+        st = axis_dev(bias->rows, a);
+        if (st == LISA_OK) st = axis_dev(bias->cols, a);
+        if (st != LISA_OK) return st;
+    }
+    if ((dq_bytes && !dQ) || (dk_bytes && (!dK || !dV)) || (!empty && (!O || !lse || !dO))) return LISA_ERR_INVALID_ARG;
+    if (!aligned16(O) || !aligned16(dO) || !aligned16(dQ) || !aligned16(dK) || !aligned16(dV) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+        return LISA_ERR_INVALID_ARG;
+    if (!empty &&
+        (!good_strides(o_strides, B, heads, n, d, esz, false) || !good_strides(do_strides, B, heads, n, d, esz, false)))
+        return LISA_ERR_INVALID_ARG;
+    // an empty problem's inputs need not be there, but where they are they are not written
+    const auto span = [&](const void *t, const lisa_strides *s, int h, int tokens) {
+        return Span(t, t && s && B > 0 && h > 0 && tokens > 0 ? extent(s, B, h, tokens, d, esz) : 0);
+    };
+    const Span outs[4] = {Span(dQ, dq_bytes), Span(dK, dk_bytes), Span(dV, dk_bytes),
+                          Span(dtable, bias ? table_floats(*bias, heads) * 4 : 0)};
+    const Span ins[8] = {span(Q, q_strides, heads, n), span(K, k_strides, kv_heads, m), span(V, v_strides, kv_heads, m),
+                         span(O, o_strides, heads, n), span(dO, do_strides, heads, n),
+                         Span(lse, lse ? (size_t)B * heads * n * 4 : 0), Span(kv_lens, kv_lens ? (size_t)B * 4 : 0),
+                         Span(bias ? bias->table : nullptr, bias && bias->table ? table_floats(*bias, heads) * 4 : 0)};
+    for (int a = 0; a < (bias ? 4 : 3); ++a) {
+        for (const Span &in : ins)
+            if (outs[a].meets(in)) return LISA_ERR_INVALID_ARG;
+        for (int c = 0; c < a; ++c)
+            if (outs[a].meets(outs[c])) return LISA_ERR_INVALID_ARG;
+    }
+    if (empty) {   // nothing to differentiate: what there is of the gradients is 0
         if ((dq_bytes && cudaMemsetAsync(dQ, 0, dq_bytes, cs) != cudaSuccess) ||
             (dk_bytes && (cudaMemsetAsync(dK, 0, dk_bytes, cs) != cudaSuccess ||
                           cudaMemsetAsync(dV, 0, dk_bytes, cs) != cudaSuccess)) ||
             (bias && heads > 0 && cudaMemsetAsync(dtable, 0, table_floats(*bias, heads) * 4, cs) != cudaSuccess))
             return LISA_ERR_CUDA;
         return LISA_OK;
-    }
-    if (!O || !lse || !dO || !dQ || !dK || !dV) return LISA_ERR_INVALID_ARG;
-    if (!aligned16(O) || !aligned16(dO) || !aligned16(dQ) || !aligned16(dK) || !aligned16(dV) ||
-        (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
-        return LISA_ERR_INVALID_ARG;
-    if (!good_strides(o_strides, B, heads, n, d, esz, false) || !good_strides(do_strides, B, heads, n, d, esz, false))
-        return LISA_ERR_INVALID_ARG;
-    const Span outs[4] = {Span(dQ, dq_bytes), Span(dK, dk_bytes), Span(dV, dk_bytes),
-                          Span(dtable, bias ? table_floats(*bias, heads) * 4 : 0)};
-    const Span ins[8] = {Span(Q, extent(q_strides, B, heads, n, d, esz)),
-                         Span(K, extent(k_strides, B, kv_heads, m, d, esz)),
-                         Span(V, extent(v_strides, B, kv_heads, m, d, esz)),
-                         Span(O, extent(o_strides, B, heads, n, d, esz)),
-                         Span(dO, extent(do_strides, B, heads, n, d, esz)),
-                         Span(lse, (size_t)B * heads * n * 4),
-                         Span(kv_lens, kv_lens ? (size_t)B * 4 : 0),
-                         Span(bias ? bias->table : nullptr, bias ? table_floats(*bias, heads) * 4 : 0)};
-    for (int a = 0; a < (bias ? 4 : 3); ++a) {
-        for (const Span &in : ins)
-            if (outs[a].meets(in)) return LISA_ERR_INVALID_ARG;
-        for (int c = 0; c < a; ++c)
-            if (outs[a].meets(outs[c])) return LISA_ERR_INVALID_ARG;
     }
     if (bias && !matrix_fits(*bias, heads)) return LISA_ERR_UNSUPPORTED;
     const BwdPlan pl = backward_plan(B, heads, kv_heads, n, m, d, bias, dtype);

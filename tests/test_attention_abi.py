@@ -283,3 +283,23 @@ def test_bucket_rules_beyond_32_bits_are_refused():
                  lambda: lisa.log_buckets(BEYOND + 32, 128), lambda: lisa.log_buckets(32, BEYOND + 128)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("over", [dict(O=FAKE + (80 << 20)), dict(lse=FAKE + (80 << 20) - 64)])
+def test_outputs_over_the_starts_are_refused(over):
+    b = _bias(starts=FAKE + (80 << 20))
+    assert _forward(bias=b, **over) == INV
+
+
+@pytest.mark.parametrize("over", [
+    dict(m=0, dQ=FAKE), dict(m=0, dQ=FAKE + (3 << 20)), dict(m=0, dQ=FAKE + (4 << 20)), dict(m=0, dQ=FAKE + (5 << 20)),
+    dict(m=0, dQ=FAKE + (6 << 20) + 8), dict(m=0, dQ=FAKE + (9 << 20), bias=_bias()),
+    dict(m=0, dQ=FAKE + (64 << 20), bias=_bias()), dict(n=0, dK=FAKE + (1 << 20)), dict(n=0, dV=FAKE + (1 << 20) + 64),
+    dict(n=0, dV=FAKE + (7 << 20)), dict(n=0, dK=FAKE + (7 << 20) + 4)])
+def test_empty_problems_zero_no_input_and_no_output_twice(over):
+    assert _backward(**over) == INV
+
+
+def test_empty_problems_take_the_rules_that_the_others_take():
+    assert _backward(m=0, bias=_bias(cols=att.exact_buckets(8192))) == UNS
+    assert _backward(m=0, bias=_bias(cols=att.lisa_axis_rule(0, 4, 2))) == INV
