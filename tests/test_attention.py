@@ -735,3 +735,78 @@ def test_every_grid_of_the_most_offsets_launches(lisa, q, k, how):
     """16383 and 16384 offsets with 16322 to 16384 keys: offsets and key offsets at their largest at once."""
     bias = _grid(q, k) if how is None else {"rows": how, "cols": ("exact", 0)}
     Case(lisa, BF16, 1, 1, 1, q, k, 64, bias=bias).check()
+
+
+# ------------------------------------------------------------------ long sums
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("q,k,how", MATRICES)
+def test_bias_matrix_gradient_misses_no_pair(lisa, dtype, q, k, how):
+    """Whole numbers 1 to 8, exact in either type, whose sums stay below 2^24: every partial sum is exact in fp32, so the
+    gradient is the exact sum, and one pair too few or too many shows."""
+    b, table, index = _matrix(lisa, q, k, how)
+    x = torch.randint(1, 9, (3, b.n, b.m), generator=torch.Generator().manual_seed(6))
+    want = torch.zeros(table.shape, dtype=torch.int64)
+    for h in range(3):
+        want[:, h].index_add_(0, index.reshape(-1), x[h].reshape(-1))
+    assert want.max() < 1 << 24
+    assert torch.equal(lisa.relative_bias_backward(b, x.to(dtype).cuda()).cpu().long(), want)
+
+
+@pytest.mark.parametrize("step", [1, 1 << 23])
+def test_bias_matrix_gradient_of_the_most_queries(lisa, step):
+    """2^22 x 2 pairs, of 1 and 2: sums below 2^24, exact."""
+    n = 1 << 22
+    b = lisa.RelativeBias(torch.zeros(3, 1, device="cuda"), (1, n), (1, 2), cols=lisa.exact_buckets(1), key_step=(1, step))
+    x = torch.randint(1, 3, (1, n, 2), generator=torch.Generator(device="cuda").manual_seed(8), device="cuda")
+    offset = step * torch.arange(2, device="cuda") - torch.arange(n, device="cuda")[:, None]
+    want = torch.zeros(3, dtype=torch.int64, device="cuda")
+    want.index_add_(0, (offset.clamp(-1, 1) + 1).reshape(-1), x.reshape(-1))
+    assert want.max() < 1 << 24
+    assert torch.equal(lisa.relative_bias_backward(b, x.float())[:, 0].long(), want)
+
+
+def test_the_most_queries_with_sums_that_add_up(lisa):
+    """2^22 queries of two keys, fp32, one key in the bucket before the query and one in the bucket behind it, and dO along
+    v_1 - v_0: every dS of a key has the same sign, so each sum is as large as its terms together.
+
+    A term's error, in units of 2^-24: a weight's score has 18 roundings of sum |q k| / 4 <= 32, 576 for each of the two
+    weights, lse 32 each, exp 40 each, and dP, delta and their difference 18 each of |dO| |v|, at most 8 times
+    dP_1 - dP_0 here: 2048 units of dS hold all of it.
+    A bucket's sum: runs of 128 in a tile, 1024 of the tiles, 32 of those, so at most 1184 further units of the sum.
+    dK and dV add n terms one by one: each addition is off by at most 2^-24 of the sum so far, one way or the other, which
+    comes to sqrt(n / 3) units rms; 8 sqrt(n) is taken."""
+    n, d = 1 << 22, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = 1 + torch.randn(1, 1, n, d, generator=g, device="cuda")
+    k, v = (torch.randn(1, 1, 2, d, generator=g, device="cuda") for _ in range(2))
+    do = (0.5 + torch.rand(1, 1, n, 1, generator=g, device="cuda")) * (v[:, :, 1:] - v[:, :, :1])
+    table = torch.randn(3, 1, generator=g, device="cuda")
+    bias = lisa.RelativeBias(table, (1, n), (1, 2), cols=lisa.exact_buckets(1), key_step=(1, 1 << 23), query_start=(0, 1))
+    out, lse = lisa.cross_attention(q, k, v, bias=bias, return_lse=True)
+    dq, dk, dv, dtable = lisa.cross_attention_backward(q, k, v, out, lse, do, bias=bias)
+    Q, K, V, G = (x[0, 0].double() for x in (q, k, v, do))
+    s = Q @ K.t() / 4 + table.double()[[0, 2], 0]
+    assert (Q.abs() @ K.abs().t() / 4).max() <= 32
+    p = torch.softmax(s, -1)
+    dp = G @ V.t()
+    size = G.norm(dim=1, keepdim=True) * V.norm(dim=1)
+    assert (size.amax(1) <= 8 * (dp[:, 1] - dp[:, 0])).all()
+    ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+    assert (ds[:, 1] > 0).all() and (ds[:, 0] < 0).all()
+    unit, run = 2.0 ** -24, 8 * n ** 0.5
+    most = ds.abs().amax(1, keepdim=True)
+    term = 2048 * unit * most
+    want = torch.stack((ds[:, 0].sum(), ds[:, 1].sum()))
+    bound = term.sum() + 1184 * unit * want.abs()
+    assert (bound <= 3e-4 * want.abs()).all()
+    assert ((dtable[[0, 2], 0].double() - want).abs() <= bound).all() and dtable[1, 0] == 0
+    assert ((dq[0, 0].double() - ds @ K / 4).abs() <= (term * 2 + 4 * unit * most) @ K.abs().amax(0, keepdim=True) / 4).all()
+    off = (term.sum() + run * unit * ds.abs().sum(0))[:, None]
+    mag = Q.abs().amax() / 4
+    want_k = ds.t() @ Q / 4
+    assert ((dk[0, 0].double() - want_k).abs() <= off * mag).all() and (off * mag <= 0.05 * want_k.abs()).all()
+    want_v = p.t() @ G
+    # the error of p: less than that of dS, which holds both weights' and dP's
+    assert ((dv[0, 0].double() - want_v).abs() <= (2048 + run) * unit * (p.t() @ G.abs())).all()
+    assert ((2048 + run) * unit * (p.t() @ G.abs()) <= 2e-3 * want_v.abs()).all()
