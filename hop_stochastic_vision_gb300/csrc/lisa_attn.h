@@ -13,6 +13,10 @@
 namespace lisa {
 namespace attn {
 
+// The plans share work out over GB300's SMs without asking the device: a workspace's size is
+// known before there is one.
+constexpr int kSms = 152;
+
 // Division by a number fixed for the launch: n / d = (umulhi(mul, n) + n) >> shift
 // for 0 <= n < 2^31 (the round-up method for 32-bit dividends, one bit to spare).
 struct FastDiv {
@@ -141,8 +145,6 @@ cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s);
 int tc_dkdv_splits(int B, int kv_heads, int group, int n, int m);
 int tc_dbias_splits(int B, int heads, int n, int m);
 cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s);
-// joins p.splits partial outputs (o_part, lse_part) into O and lse
-cudaError_t launch_join(const Problem &p, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace lisa

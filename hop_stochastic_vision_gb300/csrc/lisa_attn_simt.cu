@@ -501,13 +501,13 @@ struct Simt {
 int simt_dbias_splits(int B, int heads, int n, int m) {
     // fewer tiles than SMs: share the batch out, a matrix for each part
     const long long tiles = (long long)heads * ((n + kTile - 1) / kTile) * ((m + kTile - 1) / kTile);
-    return (int)std::max<long long>(1, std::min<long long>(152 / tiles, B));
+    return (int)std::max<long long>(1, std::min<long long>(kSms / tiles, B));
 }
 
 cudaError_t launch_no_keys(const Problem &p, cudaStream_t s) {
     const int esz = p.dtype == LISA_BF16 ? 2 : 4;
     const size_t count = (size_t)p.B * p.heads * p.n * (p.d * esz / 16);
-    return launch_plain(no_keys, dim3((unsigned)std::min<size_t>((count + kThreads - 1) / kThreads, 152 * 8)), kThreads, 0,
+    return launch_plain(no_keys, dim3((unsigned)std::min<size_t>((count + kThreads - 1) / kThreads, kSms * 8)), kThreads, 0,
                         s, p, esz);
 }
 

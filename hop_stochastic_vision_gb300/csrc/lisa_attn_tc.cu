@@ -472,16 +472,17 @@ __global__ void __launch_bounds__(256) join_splits(const __grid_constant__ Probl
     const int i = (int)(row % p.n), h = (int)(row / p.n % p.heads);
     const long long b = (long long)(row / p.n / p.heads);
     const long long out = b * p.O.sb + (long long)h * p.O.sh + (long long)i * p.O.st + c;
-    if (p.dtype == LISA_BF16) {
-        uint2 r;
-        r.x = pack_bf16(o[0] * inv, o[1] * inv);
-        r.y = pack_bf16(o[2] * inv, o[3] * inv);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + out) = r;
-    } else {
-        *reinterpret_cast<float4 *>(static_cast<float *>(const_cast<void *>(p.O.p)) + out) =
-            make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-    }
+    uint2 r;
+    r.x = pack_bf16(o[0] * inv, o[1] * inv);
+    r.y = pack_bf16(o[2] * inv, o[3] * inv);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + out) = r;
     if (c == 0 && p.lse) p.lse[row] = top == -INFINITY ? -INFINITY : top + logf(sum);
+}
+
+// Joins p.splits partial outputs (o_part, lse_part) into O and lse.
+cudaError_t launch_join(const Problem &p, cudaStream_t s) {
+    const size_t vecs = (size_t)p.B * p.heads * p.n * (p.d / 4);
+    return launch_chained(join_splits, dim3((unsigned)((vecs + 255) / 256)), 256, 0, s, p);
 }
 
 }  // namespace
@@ -490,13 +491,8 @@ int tc_forward_splits(int B, int heads, int n, int m) {
     const long long items = (long long)B * heads * ((n + 2 * kRows - 1) / (2 * kRows));
     const int tiles = (m + kRows - 1) / kRows;
     // fewer items than half the SMs: share the keys out, at least two tiles to each part
-    if (items * 2 > 152 || tiles < 4) return 1;
-    return (int)std::min<long long>(152 / items, tiles / 2);
-}
-
-cudaError_t launch_join(const Problem &p, cudaStream_t s) {
-    const size_t vecs = (size_t)p.B * p.heads * p.n * (p.d / 4);
-    return launch_chained(join_splits, dim3((unsigned)((vecs + 255) / 256)), 256, 0, s, p);
+    if (items * 2 > kSms || tiles < 4) return 1;
+    return (int)std::min<long long>(kSms / items, tiles / 2);
 }
 
 cudaError_t launch_tc_forward(const Problem &p, int *err, cudaStream_t s) {

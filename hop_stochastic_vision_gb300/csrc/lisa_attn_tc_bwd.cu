@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s = c.slot;
                 if (n >= x.stages) wait_on(smem_u32(&bar.aux_empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
                 int qt = u;
-                    const int h = w.g * p.group + split(qt, x.div_qtiles), q0 = qt * kRows;
+                const int h = w.g * p.group + split(qt, x.div_qtiles), q0 = qt * kRows;
                 const size_t row0 = ((size_t)w.b * p.heads + h) * p.n;
 #pragma unroll
                 for (int e = lane; e < kRows; e += 32) {
@@ -1026,14 +1026,14 @@ int tc_dkdv_splits(int B, int kv_heads, int group, int n, int m) {
     const long long items = (long long)B * kv_heads * ((m + kRows - 1) / kRows);
     const long long steps = (long long)group * ((n + kRows - 1) / kRows);
     // at most half as many items as SMs: share the queries out in one round, at least two tiles to each part
-    if (2 * items > 152 || steps < 4) return 1;
-    return (int)std::min<long long>(152 / items, steps / 2);
+    if (2 * items > kSms || steps < 4) return 1;
+    return (int)std::min<long long>(kSms / items, steps / 2);
 }
 
 int tc_dbias_splits(int B, int heads, int n, int m) {
     const long long items = (long long)heads * ((n + kRows - 1) / kRows) * ((m + kRows - 1) / kRows);
-    if (2 * items > 152 || B < 4) return 1;
-    return (int)std::min<long long>(152 / items, B / 2);
+    if (2 * items > kSms || B < 4) return 1;
+    return (int)std::min<long long>(kSms / items, B / 2);
 }
 
 cudaError_t launch_tc_backward(const Problem &p, int *err, cudaStream_t s) {

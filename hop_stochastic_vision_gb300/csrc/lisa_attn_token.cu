@@ -352,8 +352,8 @@ cudaError_t launch_token(const Problem &p, cudaStream_t s) {
     // even out with twice as many, while 1024 keys are left to each (256 key heads, lengths from 0 to 4096: 44 us
     // whole, 38 in two parts, 40 in three; from 0 to 1000: 20, 22 and 24).
     const long long ctas = (long long)p.B * p.kv_heads * x.rtiles;
-    long long splits = std::min<long long>(2 * 152 / ctas, p.m / 256);
-    if (p.kv_lens) splits = std::max(splits, std::min<long long>(4 * 152 / ctas, p.m / 1024));
+    long long splits = std::min<long long>(2 * kSms / ctas, p.m / 256);
+    if (p.kv_lens) splits = std::max(splits, std::min<long long>(4 * kSms / ctas, p.m / 1024));
     x.splits = (int)std::max<long long>(1, std::min<long long>(8, splits));
     if (p.d == 16) return p.bias.mode ? go<16, 1>(x, s) : go<16, 0>(x, s);
     if (p.d == 32) return p.bias.mode ? go<32, 1>(x, s) : go<32, 0>(x, s);

@@ -417,7 +417,7 @@ cudaError_t launch_bias_dense(const lisa_rel_bias &b, const BiasDev &dev, void *
     const size_t vecs = (size_t)n * m * esz / 16 + 1;
     // enough vectors for a CTA to pay for its offset table, at most about eight CTAs per SM
     size_t blocks = (vecs + kDenseThreads * 4 - 1) / (kDenseThreads * 4);
-    blocks = std::max<size_t>(1, std::min<size_t>(blocks, (152 * 8 + dev.heads - 1) / dev.heads));
+    blocks = std::max<size_t>(1, std::min<size_t>(blocks, (kSms * 8 + dev.heads - 1) / dev.heads));
     const int bytes = dev.entries * (int)sizeof(float);
     const dim3 grid((unsigned)blocks, (unsigned)dev.heads);
     cudaError_t e;
