@@ -100,8 +100,8 @@ struct Problem {
     int b_splits;
     // forward split over the keys
     int splits;
-    float *o_part;         // [splits][B][heads][n][d]
-    float *lse_part;       // [splits][B][heads][n]
+    float *o_part;         // [splits][B][heads][n][d], each over its own sum
+    float2 *stat_part;     // [splits][B][heads][n]: reference (in units of log 2), sum
     // dK / dV split over the queries
     int q_splits;
     float *dk_part, *dv_part;  // [q_splits][B][kv_heads][m][d]

@@ -210,7 +210,7 @@ enum class Path { kNoKeys, kSimt, kToken, kTiles };
 struct FwdPlan {
     Path path;
     int splits;
-    size_t off_lse, off_o, off_table, total;   // kTiles: the error word is at 0
+    size_t off_stat, off_o, off_table, total;   // kTiles: the error word is at 0
 };
 
 FwdPlan forward_plan(int B, int heads, int group, int n, int m, int d, int dtype, const BiasDev &bias) {
@@ -227,8 +227,8 @@ FwdPlan forward_plan(int B, int heads, int group, int n, int m, int d, int dtype
     size_t off = kAlign;
     if (pl.splits > 1) {
         const size_t rows = (size_t)pl.splits * B * heads * n;
-        pl.off_lse = off;
-        off = align_up(off + rows * sizeof(float));
+        pl.off_stat = off;
+        off = align_up(off + rows * sizeof(float2));
         pl.off_o = off;
         off = align_up(off + rows * d * sizeof(float));
     }
@@ -380,7 +380,7 @@ extern "C" lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q
     if (pl.path == Path::kToken) return status_of(launch_token(p, cs));
     char *ws = static_cast<char *>(workspace);
     p.splits = pl.splits;
-    p.lse_part = reinterpret_cast<float *>(ws + pl.off_lse);
+    p.stat_part = reinterpret_cast<float2 *>(ws + pl.off_stat);
     p.o_part = reinterpret_cast<float *>(ws + pl.off_o);
     if (p.bias.mode) {
         float *t = reinterpret_cast<float *>(ws + pl.off_table);

@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (p.lse && i < p.n) p.lse[row] = lse;
             } else if (i < p.n) {
                 const size_t at = (size_t)w.split * ((size_t)p.B * p.heads * p.n) + row;
-                p.lse_part[at] = lse;
+                p.stat_part[at] = make_float2(ref, sum);
                 float4 *op = reinterpret_cast<float4 *>(p.o_part + at * p.d);
 #pragma unroll
                 for (int c = 0; c < 64; c += 4)
@@ -446,7 +446,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// o = sum_s w_s o_s with w_s = exp(lse_s - lse): the parts of a row, in order.
+// o = sum_s w_s o_s / sum_s w_s with w_s = 2^(ref_s - ref) sum_s: the parts of a row, in order.  Reference and sum come
+// apart: far from 0 their lse would have lost the sum (at 2^24 the last place is 2), and parts of unequal lengths would
+// weigh the same.
 __global__ void __launch_bounds__(256) join_splits(const __grid_constant__ Problem p) {
     chain_begin();
     const int vec = p.d / 4;
@@ -456,11 +458,12 @@ __global__ void __launch_bounds__(256) join_splits(const __grid_constant__ Probl
     const int c = (int)(at % vec) * 4;
     if (row >= rows) return;
     float top = -INFINITY;
-    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.lse_part[s * rows + row]);
+    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.stat_part[s * rows + row].x);
     const float ref = top == -INFINITY ? 0.f : top;
     float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < p.splits; ++s) {
-        const float w = ex2_approx((p.lse_part[s * rows + row] - ref) * kLog2e);
+        const float2 st = p.stat_part[s * rows + row];
+        const float w = ex2_approx(st.x - ref) * st.y;
         const float4 v = *reinterpret_cast<const float4 *>(p.o_part + (s * rows + row) * p.d + c);
         sum += w;
         o[0] = fmaf(w, v.x, o[0]);
@@ -476,10 +479,10 @@ __global__ void __launch_bounds__(256) join_splits(const __grid_constant__ Probl
     r.x = pack_bf16(o[0] * inv, o[1] * inv);
     r.y = pack_bf16(o[2] * inv, o[3] * inv);
     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + out) = r;
-    if (c == 0 && p.lse) p.lse[row] = top == -INFINITY ? -INFINITY : top + logf(sum);
+    if (c == 0 && p.lse) p.lse[row] = top == -INFINITY ? -INFINITY : kLn2 * (top + log2f(sum));
 }
 
-// Joins p.splits partial outputs (o_part, lse_part) into O and lse.
+// Joins p.splits partial outputs (o_part, stat_part) into O and lse.
 cudaError_t launch_join(const Problem &p, cudaStream_t s) {
     const size_t vecs = (size_t)p.B * p.heads * p.n * (p.d / 4);
     return launch_chained(join_splits, dim3((unsigned)((vecs + 255) / 256)), 256, 0, s, p);

@@ -810,3 +810,35 @@ def test_the_most_queries_with_sums_that_add_up(lisa):
     # the error of p: less than that of dS, which holds both weights' and dP's
     assert ((dv[0, 0].double() - want_v).abs() <= (2048 + run) * unit * (p.t() @ G.abs())).all()
     assert ((2048 + run) * unit * (p.t() @ G.abs()) <= 2e-3 * want_v.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("score", [0.0, 3e5, -3e5, -1e9, 2.0 ** 40, "bias"])
+@pytest.mark.parametrize("n", [1, 150])
+def test_equal_scores_of_any_size_weigh_every_key_alike(lisa, dtype, score, n):
+    """Every key has the same score, of any size: o is the mean of the valid values, whatever parts the keys are taken in.
+    Weights of one size are exact up to a common factor that p's rounding may miss by half a step; the rest is the
+    sums' and the result's rounding."""
+    lens = [1100, 129, 257, 1000, 0, 513]
+    c = Case(lisa, dtype, 6, 2, 2, n, 1100, 64, lens=lens, scale=1.0, garbage=True,
+             bias={"cols": ("exact", 0)} if score == "bias" else None)
+    if score == "bias":     # -1e9 for every pair: nothing of the scores (below 128 / 64 units) is left beside it in fp32
+        c.q.mul_(0.25)
+        c.bias.table.fill_(-1e9)
+        score = -1e9
+    else:
+        c.q.zero_()
+        c.q[..., 0] = score
+        c.k[..., 0] = 1.0
+        score = float(c.q[0, 0, 0, 0])
+    out, lse = c.forward()
+    for b, L in enumerate(lens):
+        if L == 0:
+            assert not out[b].any() and (lse[b] == -math.inf).all()
+            continue
+        v = c.v_ref[b, :, :L].double()
+        r = ref.R[dtype]
+        bound = 2.02 * r * v.mean(1).abs() + (L + 8) * ref.U[dtype] * v.abs().mean(1)
+        assert ((out[b].double().cpu() - v.mean(1)[:, None]).abs() <= bound[:, None]).all(), L
+        want = score + math.log(L)
+        assert ((lse[b].double() - want).abs() <= 5.1 * 2.0 ** -24 * (abs(score) + 8) + (L + 8) * ref.U[dtype] + 8 * ref.EX2).all()
