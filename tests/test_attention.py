@@ -842,3 +842,16 @@ def test_equal_scores_of_any_size_weigh_every_key_alike(lisa, dtype, score, n):
         assert ((out[b].double().cpu() - v.mean(1)[:, None]).abs() <= bound[:, None]).all(), L
         want = score + math.log(L)
         assert ((lse[b].double() - want).abs() <= 5.1 * 2.0 ** -24 * (abs(score) + 8) + (L + 8) * ref.U[dtype] + 8 * ref.EX2).all()
+
+
+def test_long_sums_over_queries_and_heads_fp32(lisa):
+    """One key, so every weight is exactly 1 and dV is the sum of dO over 16384 queries of 4 heads: 65536 terms of
+    1025 units of 2^-10.  A tile's 64 terms add up exactly (65600 units); the 1024 tiles are off by at most 2^-24 of the sum
+    each.  Term by term the sum would lose a unit with every addition past 2^24 units, 7e-4 of it in all."""
+    n, heads, d = 16384, 4, 64
+    q, k = torch.randn(1, heads, n, d, device="cuda"), torch.randn(1, 1, 1, d, device="cuda")
+    dout = torch.full_like(q, 1 + 2.0 ** -10)
+    out, lse = lisa.cross_attention(q, k, k, return_lse=True)
+    dv = lisa.cross_attention_backward(q, k, k, out, lse, dout)[2]
+    want = n * heads * (1 + 2.0 ** -10)
+    assert ((dv.double() - want).abs() <= 1024 * 2.0 ** -24 * want).all()
