@@ -92,9 +92,16 @@ __device__ __forceinline__ void tile_dot(const float *A, const float *B, int ty,
     }
 }
 
-// acc[r][c] += sum_k P[4 ty + r][k] V[k][tx + 16 c]   (P rows of kTile + 4)
+// acc[r][c] += sum_k P[4 ty + r][k] V[k][tx + 16 c]   (P rows of kTile + 4).  Here and below the tile's sum by itself and
+// then one addition: N terms lose the rounding of 64 + N / 64 additions, not of N (8192 keys: o 1.9e-6 off one by one;
+// 16384 queries of 4 heads that share a key: dK and dV 4.6e-6).
 template <int D>
 __device__ __forceinline__ void tile_mul(const float *P, const float *V, int ty, int tx, float (&acc)[4][D / 16]) {
+    float sum[4][D / 16];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) sum[r][c] = 0.f;
 #pragma unroll (D == 16 ? 8 : 2)
     for (int k = 0; k < kTile; k += 4) {
         float4 p[4];
@@ -106,18 +113,20 @@ __device__ __forceinline__ void tile_mul(const float *P, const float *V, int ty,
             const float v2 = V[(k + 2) * (D + 4) + tx + 16 * c], v3 = V[(k + 3) * (D + 4) + tx + 16 * c];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                acc[r][c] = fmaf(p[r].x, v0, acc[r][c]);
-                acc[r][c] = fmaf(p[r].y, v1, acc[r][c]);
-                acc[r][c] = fmaf(p[r].z, v2, acc[r][c]);
-                acc[r][c] = fmaf(p[r].w, v3, acc[r][c]);
+                sum[r][c] = fmaf(p[r].x, v0, sum[r][c]);
+                sum[r][c] = fmaf(p[r].y, v1, sum[r][c]);
+                sum[r][c] = fmaf(p[r].z, v2, sum[r][c]);
+                sum[r][c] = fmaf(p[r].w, v3, sum[r][c]);
             }
         }
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) acc[r][c] += sum[r][c];
 }
 
-// acc[r][c] += sum_q P[q][4 ty + r] X[q][tx + 16 c]   (transposed weights).  The tile's sum by itself and then one
-// addition: n terms (of all the heads that share a key) lose the rounding of 64 + n / 64 additions, not of n (16384
-// queries of 4 heads: dK and dV 4.6e-6 off one by one).
+// acc[r][c] += sum_q P[q][4 ty + r] X[q][tx + 16 c]   (transposed weights)
 template <int D>
 __device__ __forceinline__ void tile_mul_t(const float *P, const float *X, int ty, int tx, float (&acc)[4][D / 16]) {
     float sum[4][D / 16];
@@ -230,13 +239,14 @@ __global__ void __launch_bounds__(kThreads) simt_forward(const __grid_constant__
             const float t = fmaxf(top[r], tile_top[r]);
             const float ref = t == -INFINITY ? 0.f : t;   // a row of -inf scores so far: weights 0, not NaN
             const float old = __expf(top[r] - ref);
-            sum[r] *= old;                                // this thread's columns; joined at the end
+            float share = 0.f;                            // this thread's columns; joined at the end
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float e = __expf(s[r][c] - ref);
-                sum[r] += e;
+                share += e;
                 p_s[(4 * ty + r) * (kTile + 4) + tx + 16 * c] = e;
             }
+            sum[r] = fmaf(sum[r], old, share);
             top[r] = t;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) acc[r][c] *= old;
@@ -313,14 +323,18 @@ __global__ void __launch_bounds__(kThreads) simt_dq(const __grid_constant__ Prob
         tile_dot<D>(o_s, v_s, ty, tx, dp);
         finish_scores(s, p, lut, j0, len, tx, oq);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) {
+            float e = 0.f, t = 0.f;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float w = __expf(s[r][c] - ref[r]);
-                exact[r] = fmaf(w, dp[r][c], exact[r]);
-                total[r] += w;
+                e = fmaf(w, dp[r][c], e);
+                t += w;
                 p_s[(4 * ty + r) * (kTile + 4) + tx + 16 * c] = w * (dp[r][c] - delta[r]);
             }
+            exact[r] += e;
+            total[r] += t;
+        }
         __syncwarp();
         tile_mul<D>(p_s, k_s, ty, tx, acc);
     }

@@ -855,3 +855,16 @@ def test_long_sums_over_queries_and_heads_fp32(lisa):
     dv = lisa.cross_attention_backward(q, k, k, out, lse, dout)[2]
     want = n * heads * (1 + 2.0 ** -10)
     assert ((dv.double() - want).abs() <= 1024 * 2.0 ** -24 * want).all()
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_long_sums_over_keys_fp32(lisa, n):
+    """65536 keys of one score: unscaled weights of exactly 1, values of 1025 units of 2^-10, so o is 1025 units as well.
+    A tile's 64 terms add up exactly; the 1024 tiles are off by at most 2^-24 of the sum each, the division and the result
+    by 2^-24 each.  Term by term the sum would be 7e-4 off."""
+    m = 1 << 16
+    q, k = torch.zeros(1, 1, n, 16, device="cuda"), torch.randn(1, 1, m, 16, device="cuda")
+    v = torch.full_like(k, 1 + 2.0 ** -10)
+    out, lse = lisa.cross_attention(q, k, v, return_lse=True)
+    assert ((out.double() - (1 + 2.0 ** -10)).abs() <= 1027 * 2.0 ** -24 * (1 + 2.0 ** -10)).all()
+    assert ((lse.double() - math.log(m)).abs() <= 4 * 2.0 ** -24 * math.log(m)).all()
