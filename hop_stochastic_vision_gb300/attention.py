@@ -146,8 +146,9 @@ class RelativeBias:
     of ``k_grid``; a sequence is a grid of one row.  Query (r, c) stands at
     ``query_start`` + (r, c), key (r, c) at (key_step[0] r, key_step[1] c).
     ``query_start`` may be an int32 CUDA tensor [B]: each batch entry's own
-    start on a sequence (forward only).  The table may be updated between calls;
-    the object keeps no copy of it."""
+    start on a sequence (forward only).  The table may be updated between calls,
+    and it and ``starts`` replaced by tensors of the same kind; every call checks
+    them and the object keeps no copy."""
 
     def __init__(self, table: torch.Tensor, q_grid, k_grid, rows: lisa_axis_rule = None,
                  cols: lisa_axis_rule = None, key_step=(1, 1), query_start=(0, 0)):

@@ -14,9 +14,9 @@
 // of a warp and its maximum and sum are shuffles.
 //
 // Bound by fp32 arithmetic and shared-memory loads where there are tiles enough
-// (8 entries, 8 heads of 64, 512 x 512: forward 138 us, 31 TFLOP/s, backward 491 us),
+// (8 entries, 8 heads of 64, 512 x 512: forward 148 us, 29 TFLOP/s, backward 510 us),
 // by a tile's latency where there are few (4 entries, 2 heads of 16, 196 x 196, 32
-// CTAs: 10 and 28 us).
+// CTAs: 16 and 39 us), all from cold caches.
 #include <algorithm>
 
 #include <cuda_runtime.h>

@@ -18,9 +18,9 @@
 // tile is rare, so the accumulator stays in tensor memory.  exp is 2^x with
 // log2(e) folded into the scale and into the bias table.
 //
-// 65536 queries on 1024 keys, 4 heads of 64: 77 us, 890 TFLOP/s, 47% of the
-// measured bf16 rate.  A 128 x 128 tile costs about 1300 cycles, 512 of products
-// and 512 on the exponential unit; both are 43% busy.
+// 65536 queries on 1024 keys, 4 heads of 64: 77 us from cold caches, 890 TFLOP/s,
+// 47% of the measured bf16 rate.  A 128 x 128 tile costs about 1300 cycles, 512 of
+// products and 512 on the exponential unit; both are 42% busy.
 #include <type_traits>
 
 #include "lisa_attn_tc.cuh"
@@ -493,7 +493,10 @@ cudaError_t launch_join(const Problem &p, cudaStream_t s) {
 int tc_forward_splits(int B, int heads, int n, int m) {
     const long long items = (long long)B * heads * ((n + 2 * kRows - 1) / (2 * kRows));
     const int tiles = (m + kRows - 1) / kRows;
-    // fewer items than half the SMs: share the keys out, at least two tiles to each part
+    // Fewer items than half the SMs: share the keys out in one round, at least two tiles to each part (the parts' outputs
+    // go through memory).  From cold caches, whole and as here: one item of 32 tiles 42 and 22 us, 16 items of 32 tiles 42
+    // and 26, 48 of 16 tiles 28 and 26, 72 of 16 tiles 28 and 30.  Fewer parts would do better where one
+    // item has 256 tiles: whole 256 us, 128 parts as here 61, 32 parts 34.
     if (items * 2 > kSms || tiles < 4) return 1;
     return (int)std::min<long long>(kSms / items, tiles / 2);
 }

@@ -28,7 +28,7 @@
 // Bound by that arithmetic and its hand-overs: a tile costs about 1900 cycles in
 // dQ and 2150 in dK, dV, its products 768 and 1024; the warps issue on half of the
 // cycles, tensor cores 26% and 34% busy, DRAM below 8% (8 entries, 12 heads, 500
-// queries on up to 1500 keys: dQ 39 us, dK, dV 53, dbias 44).
+// queries on up to 1500 keys: dQ 42 us, dK, dV 52, dbias 43).
 #include "lisa_attn_tc.cuh"
 #include "lisa_fold.cuh"
 
@@ -1025,13 +1025,18 @@ cudaError_t go(const Maps &m, const BwdParams &x, int bytes, cudaStream_t s) {
 int tc_dkdv_splits(int B, int kv_heads, int group, int n, int m) {
     const long long items = (long long)B * kv_heads * ((m + kRows - 1) / kRows);
     const long long steps = (long long)group * ((n + kRows - 1) / kRows);
-    // at most half as many items as SMs: share the queries out in one round, at least two tiles to each part
+    // At most half as many items as SMs: share the queries out in one round, at least two tiles to each part.  The
+    // backward from cold caches, whole and as here: 2 items of 32 tiles 41 and 25 us, 32 of 25 tiles 52 and 40, 64 of
+    // 8 tiles 33 and 36; 80 of 16 tiles 53 whole, 63 in two parts.
     if (2 * items > kSms || steps < 4) return 1;
     return (int)std::min<long long>(kSms / items, steps / 2);
 }
 
 int tc_dbias_splits(int B, int heads, int n, int m) {
     const long long items = (long long)heads * ((n + kRows - 1) / kRows) * ((m + kRows - 1) / kRows);
+    // As above, over the batch, at least two entries to each part.  The backward from cold caches, whole and as here:
+    // 4 items of 64 entries 102 and 53 us (46 in sixteen parts), 32 of 32 entries 92 and 70; 80 of 64 entries 237 whole,
+    // 239 in two parts.
     if (2 * items > kSms || B < 4) return 1;
     return (int)std::min<long long>(kSms / items, B / 2);
 }

@@ -9,9 +9,9 @@
 // and the warps and then the CTAs of the cluster join in a fixed order.  Bound
 // by the bytes of K and V: no CTA waits for another until the end, and each warp
 // has two chunks of 8 KB in flight (three chunks, so fewer CTAs per SM, were
-// slower: 52 us against 46 at one setting of the rest).  64 x 4096 keys, 4 key
-// heads, lengths from 0 up: 40 us for 137 MB, 3.4 TB/s; 256 x 4096 keys at full
-// length 185 us, 5.8 TB/s.
+// slower: 52 us against 46 at one setting of the rest).  64 x 4096 keys, 12 heads
+// on 4, lengths from 0 up, from cold caches: 43 us for 137 MB, 3.2 TB/s; 256 x 4096
+// keys at full length 184 us, 5.8 TB/s.
 #include <algorithm>
 
 #include "lisa_attn_tc.cuh"
@@ -333,8 +333,10 @@ cudaError_t go(const TokenParams &x, cudaStream_t s) {
 }  // namespace
 
 bool token_applies(int kv_heads, int group, int n, const BiasDev &bias) {
-    // up to two row tiles per key head read the keys twice at most (the second
-    // time from L2); a sequence's offset tables of the tile's heads fit beside the rings
+    // Up to two row tiles per key head read the keys twice at most (the second time from L2); a sequence's offset tables
+    // of the tile's heads fit beside the rings.  From cold caches, this path and tiles: 32 rows (8 heads of a group, 4
+    // queries) of 256 key heads on 2048 keys 45 and 182 us, 32 rows of one head on 512 keys 21 and 20, 48 rows of one head
+    // 24 and 20.  Rows of many heads would do well here beyond 32 (48 rows of 12 heads: 59 and 269).
     if ((long long)n * group > 32 || kv_heads * 2LL > 65535 || bias.mode == 2) return false;
     return bias.mode == 0 || std::min(16, group) * bias.entries <= 8192;
 }
@@ -347,10 +349,10 @@ cudaError_t launch_token(const Problem &p, cudaStream_t s) {
     x.div_rtiles = fast_div(x.rtiles);
     x.div_n = fast_div(p.n);
     // Two CTAs per SM at most, of 256 keys at least: a CTA's start and the join cost some microseconds, so a second
-    // wave does not pay (256 key heads of 4096 keys: 60 us whole, 75 in two parts, 69 in four; 64 of them 34 us
-    // whole, 24 in four parts, 30 in eight; 8 of 32768 keys 183 and 34 us whole and in eight).  Lengths that differ
+    // wave does not pay (from cold caches: 256 key heads of 4096 keys 59 us whole, 75 in two parts, 69 in four; 64 of them
+    // 33 us whole, 23 in four parts, 29 in eight; 8 of 32768 keys 184 and 34 us whole and in eight).  Lengths that differ
     // even out with twice as many, while 1024 keys are left to each (256 key heads, lengths from 0 to 4096: 44 us
-    // whole, 38 in two parts, 40 in three; from 0 to 1000: 20, 22 and 24).
+    // whole, 42 in two to four parts, 50 in eight; from 0 to 1000: 19 us whole, 21 in two parts, 24 in four).
     const long long ctas = (long long)p.B * p.kv_heads * x.rtiles;
     long long splits = std::min<long long>(2 * kSms / ctas, p.m / 256);
     if (p.kv_lens) splits = std::max(splits, std::min<long long>(4 * kSms / ctas, p.m / 1024));

@@ -14,7 +14,10 @@ namespace attn {
 namespace {
 
 constexpr int kDenseThreads = 256;
-constexpr int kMaxFoldUnits = 2048;   // offsets of a tile that are folded in shared memory
+// Offsets of a tile that are folded in shared memory: three CTAs of fold_matrix share an SM up to 2176.  From cold caches,
+// folded and by row pairs: 2 x 300 on 2 x 300 (1797 offsets, 4 heads) 16 and 34 us, 64 x 40 on 64 x 40 (711) 52 and 104,
+// 16 x 16 on 16 x 16 13 both ways; beyond, the fold would still win (2 x 500 on 2 x 500, 2997: 20 and 35; 2 x 650: 26 and 37).
+constexpr int kMaxFoldUnits = 2048;
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
@@ -22,9 +25,11 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 // out[h][i][j] = offset table of head h at the pair's offset.  The head's n m
 // elements are written as one run of 16-byte vectors (ragged ends element by
 // element), so rows of any length give full-width stores; a vector finds its
-// first pair by one division and walks from there.  Bound by the stores once the
-// matrix is large; three heads of 576 x 576 (2 MB) take 12 us from cold caches, most
-// of it the launch and the offset table.
+// first pair by one division and walks from there.  Three heads of 576 x 576 (2 MB)
+// take 12 us from cold caches, most of it the launch and the offset table.  Bound by
+// the instructions of the walk once the matrix is large, a table look-up and a step
+// per element: four heads of 4096 x 4096 take 130 us in fp32 (268 MB, 2.1 TB/s) and
+// 118 in bf16 (134 MB).
 template <typename T>
 __global__ void __launch_bounds__(kDenseThreads) bias_dense(BiasDev b, T *out, int n, int m) {
     extern __shared__ __align__(16) float lut[];
@@ -237,8 +242,9 @@ __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;
 // One 128 x 128 tile of one head's matrix (blockIdx.z: part, head): loaded into
 // shared memory, then folded; three CTAs per SM, so one folds while the others
 // load.  Bound by the instructions of both: a whole tile's fp32 loads are one
-// copy and one address step each.  The 268 MB of a 64 x 64 grid's four heads:
-// 92 us with the sums behind it (97 with a check and an address for each copy).
+// copy and one address step each (with a check and an address for each, 5 us more).
+// The 268 MB of a 64 x 64 grid's four heads from cold caches: 61 us, 87 with the sums
+// behind it.
 constexpr int kFoldThreads = 512;
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kFoldThreads, 3) fold_matrix(const __grid_constant__ FoldDev f, const T *dbias) {
@@ -392,7 +398,10 @@ void grad_plan(const lisa_rel_bias &b, GradParams &g) {
     g.m = (long long)b.k_rows * b.k_cols;
     g.residues = std::min(g.step_c, g.q_cols);
     const int nmax = (g.q_cols - 1) / g.step_c + 1;
-    g.ch = std::min(nmax, g.col_buckets > 512 ? 256 : 64);   // many buckets: longer chunks, fewer partial rows
+    // Many buckets: longer chunks, so fewer partial rows of them.  From cold caches, chunks of 64 and of 256: 33 buckets
+    // (4 heads, 4096 x 512, step 8) 23 and 35 us, 513 buckets (8 heads, 2048 x 1024, step 2) 39 and 40, 2049 (4 heads,
+    // 4096 x 1024, step 2) 51 and 45, 8193 of the same 84 and 64.
+    g.ch = std::min(nmax, g.col_buckets > 512 ? 256 : 64);
     g.nchunk = (nmax + g.ch - 1) / g.ch;
     g.etot = g.k_cols + g.ch - 1;
     const long long flat = (long long)g.residues * g.etot;

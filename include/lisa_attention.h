@@ -34,13 +34,21 @@
  *     are multiples of 16 bytes.  A batch or head stride of 0 repeats one entry
  *     (inputs only).  Tokens of one head may not overlap, nor any two
  *     elements of an output: each of its strides has to step over the axes of
- *     smaller strides.
+ *     smaller strides.  Whether an output overlaps something is told by the
+ *     extents, from the first to the last element: an output that lies between
+ *     an input's heads or tokens without touching them is refused as well.
  *   - kv_lens (device int32 [B], or NULL for m everywhere) says how many keys of
  *     a batch entry are valid; a value outside 0..m counts as the nearer end.
  *     Keys and values behind it are never used, whatever they hold (NaN
  *     included); their dK and dV are written as 0.
  *   - A row without any key that counts (length 0, or only masked scores) has
  *     o = 0, lse = -inf and gives no gradient.
+ *   - Scores (and the bias) of any finite size up to 2^126 give the softmax of the
+ *     fp32 scores.
+ *   - LISA_BF16's backward takes sum_j p_ij dP_ij as dO_i . o_i from the rounded
+ *     output where there are more than 128 keys (without a bias for dQ, dK; with
+ *     one for dQ), from the unrounded weights otherwise: what is left of dP there
+ *     after that sum is good to one rounding of o.
  *   - The backward takes p from fp32 scores and lse, so p is good to about
  *     |lse| 2^-23 relative; a row of |lse| > 2^20, as only masks of large finite
  *     numbers over a whole row bring it about, gives no gradient.
@@ -152,7 +160,11 @@ lisa_status lisa_cross_attention(const void *Q, const lisa_strides *q_strides, c
  * with a bias, dtable are written, never accumulated, and may not overlap each
  * other or an input.  Where K or V repeats an entry (stride 0), dK and dV are
  * those of the repeated tensor, one entry for each repeat.  dtable is NULL
- * exactly when bias is.  The workspace begins with the call's error word.
+ * exactly when bias is.  The workspace begins with the call's error word.  With a
+ * bias it may be large: LISA_F32, and LISA_BF16 where a key step is above 1 or
+ * 128 tokens span more than 2048 offsets, hold dS as matrices of heads n m
+ * floats, one for each part of the batch that runs side by side (12 heads of
+ * 16384 x 4096: 3.2 GB).
  */
 size_t lisa_cross_attention_backward_workspace_bytes(int B, int heads, int kv_heads, int n, int m, int d,
                                                      const lisa_rel_bias *bias, int dtype);
