@@ -384,7 +384,7 @@ extern "C" const char *lisa_status_string(int status) {
     }
 }
 
-extern "C" int lisa_abi_version(void) { return 105; }
+extern "C" int lisa_abi_version(void) { return 106; }
 
 extern "C" lisa_status lisa_query_status(const void *workspace, void *stream) {
     if (!workspace || !aligned16(workspace)) return LISA_ERR_INVALID_ARG;

@@ -7,6 +7,7 @@
 
 #include <cuda_runtime.h>
 
+#include "lisa_args.h"
 #include "lisa_attention.h"
 #include "lisa_attn.h"
 
@@ -19,10 +20,6 @@ constexpr int kMaxGridDim = 65535;       // batch entries and heads
 constexpr long long kMaxItems = 1LL << 28;
 constexpr int kMaxDistance = 8191;
 constexpr long long kMaxPosition = 1LL << 28;
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // A sequence's offsets continue at both ends, so that a tile of 128 keys and 32
 // queries with any offset inside the table needs no clamping.
@@ -135,39 +132,6 @@ lisa_status check_sizes(int B, int heads, int kv_heads, int n, int m, int d, int
     return LISA_OK;
 }
 
-// Strides of a [B][heads][tokens][d] tensor: multiples of 16 bytes, tokens of a
-// head apart, extents within 63 bits.  `out`: no two elements in one place.
-bool good_strides(const lisa_strides *s, int B, int heads, int tokens, int d, size_t esz, bool out) {
-    if (!s) return false;
-    const long long q = 16 / (long long)esz, most = 1LL << 38;
-    for (const long long x : {s->batch, s->head, s->token})
-        if (x < 0 || x > most || x % q != 0) return false;
-    if (tokens > 1 && s->token < d) return false;
-    if (!out) return true;
-    // the axes from the narrowest stride up: each steps over all of the ones below
-    struct Axis { long long stride; int count; } ax[3] = {{s->batch, B}, {s->head, heads}, {s->token, tokens}};
-    std::sort(ax, ax + 3, [](const Axis &a, const Axis &b) { return a.stride < b.stride; });
-    long long inner = d;
-    for (const Axis &a : ax) {
-        if (a.count <= 1) continue;
-        if (a.stride < inner) return false;
-        inner += a.stride * (a.count - 1);
-    }
-    return true;
-}
-
-// Bytes from the first to behind the last element.
-size_t extent(const lisa_strides *s, int B, int heads, int tokens, int d, size_t esz) {
-    return ((size_t)s->batch * (size_t)(B - 1) + (size_t)s->head * (size_t)(heads - 1) +
-            (size_t)s->token * (size_t)(tokens - 1) + (size_t)d) * esz;
-}
-
-struct Span {
-    uintptr_t lo, hi;
-    Span(const void *p, size_t bytes) : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + bytes) {}
-    bool meets(const Span &o) const { return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi; }
-};
-
 // Shared by the forward and the backward: everything but the outputs.
 lisa_status fill(Problem &p, const void *Q, const lisa_strides *qs, const void *K, const lisa_strides *ks,
                  const void *V, const lisa_strides *vs, int B, int heads, int kv_heads, int n, int m, int d,
@@ -275,8 +239,6 @@ BwdPlan backward_plan(int B, int heads, int kv_heads, int n, int m, int d, const
     pl.total = off;
     return pl;
 }
-
-lisa_status status_of(cudaError_t e) { return e == cudaSuccess ? LISA_OK : LISA_ERR_CUDA; }
 
 size_t table_floats(const lisa_rel_bias &b, int heads) {
     return (size_t)b.rows.buckets * (size_t)b.cols.buckets * (size_t)heads;

@@ -1,0 +1,69 @@
+// lisa_packed.h -- host-side problem description of the attention over packed
+// prompts, the plan's lists as the kernels read them, and the launchers.  Not
+// part of the public ABI.
+#pragma once
+
+#include <cstddef>
+
+#include <cuda_runtime.h>
+
+#include "lisa_attn.h"
+#include "lisa_prompt.h"
+
+namespace lisa {
+namespace packed {
+
+using attn::FastDiv;
+using attn::Tensor;
+
+// The passes' units of work.  A step is a tile of 128 tokens of the other side.
+//   forward  256 queries; steps are tiles of keys
+//   dQ       128 queries; steps are tiles of keys
+//   dK dV    128 keys; steps are tiles of queries, head by head of those that share the keys
+enum Pass { kForward = 0, kDq = 1, kDkv = 2 };
+constexpr int kPasses = 3;
+constexpr int kStep = 128;
+constexpr int unit_rows(int pass) { return pass == kForward ? 256 : 128; }
+
+// One unit's steps t0 .. t1 - 1.  A unit that is long beside the others is cut
+// into parts, which leave their sums in the workspace for a join.
+struct Item {
+    int row0, len;    // the sequence: its first token, its tokens
+    int first;        // the unit's first row in the sequence
+    int t0, t1;
+    int part;         // slot of the partial sums, -1 where the unit is whole
+    int steps;        // of the whole unit
+    int pad;
+};
+struct Join {
+    int row, rows;    // the unit's tokens
+    int part, parts;  // its slots
+};
+
+// One pass's lists in the plan: the items, longest first; the joins; for each of
+// kSms workers its (item, head) pairs, item * heads + head, longest first.
+struct Lists {
+    const Item *items;
+    const Join *joins;
+    const int *order, *starts;   // [items * heads], [kSms + 1]
+    int n_items, n_joins, n_parts;
+};
+
+struct Problem {
+    Tensor Q, K, V, O, dO, dQ, dK, dV;   // sb is not used
+    float *lse;
+    long long lse_stride;
+    int tokens, heads, kv_heads, group, d, causal;
+    float scale;
+    Lists lists[kPasses];
+    int *err;
+    float *delta;          // [heads][tokens]
+    float2 *stat_part;     // forward: [part][head][256] reference (in units of log 2), sum
+    float *part[2];        // [part][head][unit_rows][d]: O; dQ; dV, dK
+};
+
+cudaError_t launch_simt_forward(const Problem &p, int dtype, cudaStream_t s);
+cudaError_t launch_simt_backward(const Problem &p, int dtype, cudaStream_t s);
+
+}  // namespace packed
+}  // namespace lisa

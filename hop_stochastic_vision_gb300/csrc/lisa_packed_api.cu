@@ -1,0 +1,411 @@
+// lisa_packed_api.cu -- the C ABI of the attention over packed prompts: the plan
+// (which unit of work goes to which worker), argument checks, the workspace
+// carve-up and the dispatch.  Every check runs before the first launch.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "lisa_args.h"
+#include "lisa_packed.h"
+
+namespace lisa {
+namespace packed {
+namespace {
+
+using attn::align_up;
+using attn::aligned16;
+using attn::aligned4;
+using attn::kSms;
+
+constexpr int kMaxSequences = 1 << 20;
+constexpr long long kMaxTokens = 1 << 22;
+constexpr int kMaxHeads = 65535;
+constexpr long long kMaxOrder = 1 << 24;   // (item, head) pairs of a pass
+
+struct Batch {
+    const int *lengths;
+    int sequences, tokens, heads, kv_heads, group, causal;
+    int heads_of(int pass) const { return pass == kDkv ? kv_heads : heads; }
+};
+
+// Calls f(sequence's first token, its length, unit's first row, steps) for every unit of a pass.
+template <typename F>
+void each_unit(const Batch &b, int pass, F f) {
+    int row0 = 0;
+    for (int s = 0; s < b.sequences; row0 += b.lengths[s++]) {
+        const int len = b.lengths[s], tiles = (len + kStep - 1) / kStep, rows = unit_rows(pass);
+        for (int first = 0; first < len; first += rows) {
+            int steps = tiles;
+            if (b.causal && pass == kDkv) steps = tiles - first / kStep;
+            else if (b.causal) steps = std::min(tiles, (first + rows) / kStep);
+            if (pass == kDkv) steps *= b.group;
+            f(row0, len, first, steps);
+        }
+    }
+}
+
+// Steps of a part.  Units go to kSms workers, the longest first, each to the one
+// with the least to do.  That evens out while the longest unit is below an even
+// share of the whole; where it is not, units are cut into parts of at most half
+// a share, of four steps at least (a part's sums go through memory).
+int part_steps(const Batch &b, int pass) {
+    long long sum = 0;
+    int longest = 0;
+    each_unit(b, pass, [&](int, int, int, int steps) {
+        sum += steps;
+        longest = std::max(longest, steps);
+    });
+    const long long share = (sum * b.heads_of(pass) + kSms - 1) / kSms;
+    if (longest <= std::max<long long>(share, 4)) return longest;
+    return (int)std::max<long long>((share + 1) / 2, 4);
+}
+
+struct Counts {
+    int items, joins, parts;
+};
+// Calls item(Item) and join(Join) in order; returns their numbers.
+template <typename I, typename J>
+Counts each_item(const Batch &b, int pass, I item, J join) {
+    const int most = part_steps(b, pass);
+    Counts n{};
+    each_unit(b, pass, [&](int row0, int len, int first, int steps) {
+        const int parts = most > 0 ? (steps + most - 1) / most : 1;
+        if (parts > 1) {
+            join(Join{row0 + first, std::min(unit_rows(pass), len - first), n.parts, parts});
+            ++n.joins;
+        }
+        for (int k = 0; k < parts; ++k) {
+            const int t0 = (int)((long long)steps * k / parts), t1 = (int)((long long)steps * (k + 1) / parts);
+            item(Item{row0, len, first, t0, t1, parts > 1 ? n.parts++ : -1, steps, 0});
+            ++n.items;
+        }
+    });
+    return n;
+}
+
+struct Layout {
+    size_t items, joins, order, starts, end;
+};
+Layout layout_of(size_t at, long long n_items, long long n_joins, long long pairs) {
+    Layout l;
+    l.items = at;
+    l.joins = align_up(l.items + (size_t)n_items * sizeof(Item));
+    l.order = align_up(l.joins + (size_t)n_joins * sizeof(Join));
+    l.starts = align_up(l.order + (size_t)pairs * sizeof(int));
+    l.end = align_up(l.starts + (kSms + 1) * sizeof(int));
+    return l;
+}
+
+lisa_status batch_of(const int *lengths, int sequences, int heads, int kv_heads, int causal, Batch &b) {
+    if (sequences < 0 || heads < 0 || kv_heads < 0 || causal < 0 || causal > 1 || (sequences > 0 && !lengths))
+        return LISA_ERR_INVALID_ARG;
+    if (heads > 0 && (kv_heads < 1 || heads % kv_heads != 0)) return LISA_ERR_INVALID_ARG;
+    if (sequences > kMaxSequences || heads > kMaxHeads) return LISA_ERR_UNSUPPORTED;
+    long long tokens = 0;
+    for (int s = 0; s < sequences; ++s) {
+        if (lengths[s] < 0) return LISA_ERR_INVALID_ARG;
+        tokens += lengths[s];
+    }
+    if (tokens > kMaxTokens) return LISA_ERR_UNSUPPORTED;
+    b = Batch{lengths, sequences, (int)tokens, heads, kv_heads, heads > 0 ? heads / kv_heads : 1, causal};
+    return LISA_OK;
+}
+
+// The plan's size, and its counts in `out` (pairs of a pass beyond kMaxOrder: false).
+bool measure(const Batch &b, lisa_packed &out, size_t &bytes) {
+    bytes = 0;
+    for (int pass = 0; pass < kPasses; ++pass) {
+        const Counts n = each_item(b, pass, [](const Item &) {}, [](const Join &) {});
+        const long long pairs = (long long)n.items * b.heads_of(pass);
+        if (pairs > kMaxOrder) return false;
+        out.items[pass] = n.items;
+        out.joins[pass] = n.joins;
+        out.parts[pass] = n.parts;
+        bytes = layout_of(bytes, n.items, n.joins, pairs).end;
+    }
+    return true;
+}
+
+// (item, head) pairs to the workers: each to the one with the least to do, of equals the lowest.
+template <typename F>
+void deal(const Item *items, int n, int heads, F f) {
+    struct Worker { long long load; int id; } heap[kSms];
+    for (int w = 0; w < kSms; ++w) heap[w] = {0, w};
+    const auto before = [](const Worker &a, const Worker &c) { return a.load < c.load || (a.load == c.load && a.id < c.id); };
+    for (int e = 0; e < n; ++e)
+        for (int h = 0; h < heads; ++h) {
+            f(heap[0].id, e * heads + h);
+            heap[0].load += items[e].t1 - items[e].t0 + 1;   // one for an item's start and end
+            for (int at = 0;;) {   // sift down
+                int least = at;
+                for (int c = 2 * at + 1; c <= 2 * at + 2 && c < kSms; ++c)
+                    if (before(heap[c], heap[least])) least = c;
+                if (least == at) break;
+                std::swap(heap[at], heap[least]);
+                at = least;
+            }
+        }
+}
+
+// A number that changes with any of the struct's sizes (FNV-1a over them).
+unsigned seal_of(const lisa_packed &s) {
+    unsigned x = 2166136261u;
+    const auto add = [&](unsigned v) { x = (x ^ v) * 16777619u; };
+    add((unsigned)s.plan_bytes);
+    add((unsigned)(s.plan_bytes >> 32));
+    for (const int v : {s.sequences, s.tokens, s.heads, s.kv_heads, s.causal}) add((unsigned)v);
+    for (int pass = 0; pass < kPasses; ++pass)
+        for (const int v : {s.items[pass], s.joins[pass], s.parts[pass]}) add((unsigned)v);
+    return x;
+}
+
+}  // namespace
+}  // namespace packed
+}  // namespace lisa
+
+using namespace lisa::packed;
+
+extern "C" size_t lisa_packed_plan_bytes(const int *lengths, int sequences, int heads, int kv_heads, int causal) {
+    Batch b;
+    lisa_packed counts;
+    size_t bytes;
+    if (batch_of(lengths, sequences, heads, kv_heads, causal, b) != LISA_OK || !measure(b, counts, bytes)) return 0;
+    return bytes;
+}
+
+extern "C" lisa_status lisa_packed_plan(const int *lengths, int sequences, int heads, int kv_heads, int causal,
+                                        void *plan, size_t plan_bytes, lisa_packed *packed) {
+    Batch b;
+    const lisa_status st = batch_of(lengths, sequences, heads, kv_heads, causal, b);
+    if (st != LISA_OK) return st;
+    lisa_packed out{};
+    size_t bytes;
+    if (!measure(b, out, bytes)) return LISA_ERR_UNSUPPORTED;
+    if (!packed || !plan || !aligned16(plan)) return LISA_ERR_INVALID_ARG;
+    if (plan_bytes < bytes) return LISA_ERR_WORKSPACE;
+    out.plan_bytes = bytes;
+    out.sequences = sequences;
+    out.tokens = b.tokens;
+    out.heads = heads;
+    out.kv_heads = kv_heads;
+    out.causal = causal;
+    out.seal = seal_of(out);
+    std::memset(plan, 0, bytes);
+    char *base = static_cast<char *>(plan);
+    size_t at = 0;
+    for (int pass = 0; pass < kPasses; ++pass) {
+        const int h = b.heads_of(pass);
+        const Layout l = layout_of(at, out.items[pass], out.joins[pass], (long long)out.items[pass] * h);
+        at = l.end;
+        Item *items = reinterpret_cast<Item *>(base + l.items), *next = items;
+        Join *join = reinterpret_cast<Join *>(base + l.joins);
+        int *order = reinterpret_cast<int *>(base + l.order), *starts = reinterpret_cast<int *>(base + l.starts);
+        each_item(b, pass, [&](const Item &i) { *next++ = i; }, [&](const Join &j) { *join++ = j; });
+        std::sort(items, next, [](const Item &x, const Item &y) {
+            const int cx = x.t1 - x.t0, cy = y.t1 - y.t0;
+            if (cx != cy) return cx > cy;
+            if (x.row0 != y.row0) return x.row0 < y.row0;
+            return x.first != y.first ? x.first < y.first : x.t0 < y.t0;
+        });
+        deal(items, out.items[pass], h, [&](int w, int) { ++starts[w + 1]; });
+        for (int w = 0; w < lisa::attn::kSms; ++w) starts[w + 1] += starts[w];
+        int fill[lisa::attn::kSms];
+        std::memcpy(fill, starts, sizeof(fill));
+        deal(items, out.items[pass], h, [&](int w, int pair) { order[fill[w]++] = pair; });
+    }
+    *packed = out;
+    return LISA_OK;
+}
+
+namespace lisa {
+namespace packed {
+namespace {
+
+using attn::Span;
+
+// The struct is as lisa_packed_plan left it, so its sizes are within the limits there.
+lisa_status check_packed(const lisa_packed *s, int d, int dtype) {
+    if (!s || (dtype != LISA_F32 && dtype != LISA_BF16) || d < 1 || s->seal != seal_of(*s)) return LISA_ERR_INVALID_ARG;
+    if (d != 16 && d != 32 && d != 64) return LISA_ERR_UNSUPPORTED;
+    return LISA_OK;
+}
+
+Lists lists_of(const lisa_packed &s, int pass) {
+    const char *base = static_cast<const char *>(s.plan);
+    Layout l{};
+    for (int k = 0; k <= pass; ++k)
+        l = layout_of(l.end, s.items[k], s.joins[k], (long long)s.items[k] * (k == kDkv ? s.kv_heads : s.heads));
+    return Lists{reinterpret_cast<const Item *>(base + l.items), reinterpret_cast<const Join *>(base + l.joins),
+                 reinterpret_cast<const int *>(base + l.order), reinterpret_cast<const int *>(base + l.starts),
+                 s.items[pass], s.joins[pass], s.parts[pass]};
+}
+
+struct Workspace {
+    size_t delta, stat, part[2], total;   // the error word is at 0
+};
+Workspace forward_workspace(const lisa_packed &s, int d, int dtype) {
+    Workspace w{};
+    if (dtype != LISA_BF16) return w;
+    size_t off = attn::kAlign;
+    const size_t rows = (size_t)s.parts[kForward] * s.heads * unit_rows(kForward);
+    w.stat = off;
+    off = align_up(off + rows * sizeof(float2));
+    w.part[0] = off;
+    w.total = align_up(off + rows * d * sizeof(float));
+    return w;
+}
+Workspace backward_workspace(const lisa_packed &s, int d, int dtype) {
+    Workspace w{};
+    size_t off = attn::kAlign;
+    w.delta = off;
+    off = align_up(off + (size_t)s.heads * s.tokens * sizeof(float));
+    if (dtype == LISA_BF16) {
+        // dQ's parts are joined before dK's and dV's are written
+        const size_t dq = (size_t)s.parts[kDq] * s.heads * unit_rows(kDq) * d * sizeof(float);
+        const size_t kv = align_up((size_t)s.parts[kDkv] * s.kv_heads * unit_rows(kDkv) * d * sizeof(float));
+        w.part[0] = off;
+        w.part[1] = off + kv;
+        off = align_up(off + std::max(dq, 2 * kv));
+    }
+    w.total = off;
+    return w;
+}
+
+struct View {
+    const void *p;
+    const lisa_strides *s;
+    int heads;
+    bool out;
+};
+// Pointers and strides of a packed call's tensors, and that no output meets an input or another output.
+bool good_views(const View *v, int count, const Span *more, int more_outs, int more_count, int tokens, int d, size_t esz) {
+    Span span[16];
+    bool out[16];
+    int n = 0;
+    for (int k = 0; k < count; ++k) {
+        const lisa_strides one = v[k].s ? lisa_strides{0, v[k].s->head, v[k].s->token} : lisa_strides{};
+        if (!v[k].p || !v[k].s || !aligned16(v[k].p) || !attn::good_strides(&one, 1, v[k].heads, tokens, d, esz, v[k].out))
+            return false;
+        out[n] = v[k].out;
+        span[n++] = Span(v[k].p, attn::extent(&one, 1, v[k].heads, tokens, d, esz));
+    }
+    for (int k = 0; k < more_count; ++k) {
+        out[n] = k < more_outs;
+        span[n++] = more[k];
+    }
+    for (int a = 0; a < n; ++a)
+        for (int c = 0; c < n; ++c)
+            if (a != c && out[a] && span[a].meets(span[c])) return false;
+    return true;
+}
+
+Tensor tensor_of(const void *p, const lisa_strides *s) { return Tensor{p, 0, s->head, s->token}; }
+
+Problem problem_of(const lisa_packed &s, int d, float scale) {
+    Problem p{};
+    p.tokens = s.tokens;
+    p.heads = s.heads;
+    p.kv_heads = s.kv_heads;
+    p.group = s.heads / s.kv_heads;
+    p.d = d;
+    p.causal = s.causal;
+    p.scale = scale;
+    for (int pass = 0; pass < kPasses; ++pass) p.lists[pass] = lists_of(s, pass);
+    return p;
+}
+
+}  // namespace
+}  // namespace packed
+}  // namespace lisa
+
+extern "C" size_t lisa_prompt_attention_workspace_bytes(const lisa_packed *packed, int d, int dtype) {
+    if (check_packed(packed, d, dtype) != LISA_OK || packed->tokens == 0 || packed->heads == 0) return 0;
+    return forward_workspace(*packed, d, dtype).total;
+}
+
+extern "C" lisa_status lisa_prompt_attention(const void *Q, const lisa_strides *q_strides, const void *K,
+                                             const lisa_strides *k_strides, const void *V,
+                                             const lisa_strides *v_strides, void *O, const lisa_strides *o_strides,
+                                             float *lse, long long lse_stride, const lisa_packed *packed, int d,
+                                             float scale, int dtype, void *workspace, size_t workspace_bytes,
+                                             void *stream) {
+    const lisa_status st = check_packed(packed, d, dtype);
+    if (st != LISA_OK) return st;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return LISA_ERR_INVALID_ARG;
+    const lisa_packed &s = *packed;
+    if (s.tokens == 0 || s.heads == 0) return LISA_OK;
+    const size_t esz = dtype == LISA_BF16 ? 2 : 4;
+    if (!aligned4(lse) || (lse && (lse_stride < s.tokens || lse_stride > 1LL << 38)) || !s.plan || !aligned16(s.plan))
+        return LISA_ERR_INVALID_ARG;
+    const View v[4] = {{Q, q_strides, s.heads, false}, {K, k_strides, s.kv_heads, false},
+                       {V, v_strides, s.kv_heads, false}, {O, o_strides, s.heads, true}};
+    const Span more[2] = {Span(lse, lse ? ((size_t)lse_stride * (s.heads - 1) + s.tokens) * 4 : 0),
+                          Span(s.plan, s.plan_bytes)};
+    if (!good_views(v, 4, more, 1, 2, s.tokens, d, esz)) return LISA_ERR_INVALID_ARG;
+    const Workspace w = forward_workspace(s, d, dtype);
+    if (w.total > 0) {
+        if (!workspace || workspace_bytes < w.total) return LISA_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
+    }
+    Problem p = problem_of(s, d, scale);
+    p.Q = tensor_of(Q, q_strides);
+    p.K = tensor_of(K, k_strides);
+    p.V = tensor_of(V, v_strides);
+    p.O = tensor_of(O, o_strides);
+    p.lse = lse;
+    p.lse_stride = lse_stride;
+    char *ws = static_cast<char *>(workspace);
+    p.err = reinterpret_cast<int *>(ws);
+    p.stat_part = reinterpret_cast<float2 *>(ws + w.stat);
+    p.part[0] = reinterpret_cast<float *>(ws + w.part[0]);
+    return lisa::attn::status_of(launch_simt_forward(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t lisa_prompt_attention_backward_workspace_bytes(const lisa_packed *packed, int d, int dtype) {
+    if (check_packed(packed, d, dtype) != LISA_OK || packed->tokens == 0 || packed->heads == 0) return 0;
+    return backward_workspace(*packed, d, dtype).total;
+}
+
+extern "C" lisa_status lisa_prompt_attention_backward(
+    const void *Q, const lisa_strides *q_strides, const void *K, const lisa_strides *k_strides, const void *V,
+    const lisa_strides *v_strides, const void *O, const lisa_strides *o_strides, const float *lse, long long lse_stride,
+    const void *dO, const lisa_strides *do_strides, void *dQ, const lisa_strides *dq_strides, void *dK,
+    const lisa_strides *dk_strides, void *dV, const lisa_strides *dv_strides, const lisa_packed *packed, int d,
+    float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    const lisa_status st = check_packed(packed, d, dtype);
+    if (st != LISA_OK) return st;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return LISA_ERR_INVALID_ARG;
+    const lisa_packed &s = *packed;
+    if (s.tokens == 0 || s.heads == 0) return LISA_OK;
+    const size_t esz = dtype == LISA_BF16 ? 2 : 4;
+    if (!lse || !aligned4(lse) || lse_stride < s.tokens || lse_stride > 1LL << 38 || !s.plan || !aligned16(s.plan))
+        return LISA_ERR_INVALID_ARG;
+    const View v[8] = {{Q, q_strides, s.heads, false},    {K, k_strides, s.kv_heads, false},
+                       {V, v_strides, s.kv_heads, false}, {O, o_strides, s.heads, false},
+                       {dO, do_strides, s.heads, false},  {dQ, dq_strides, s.heads, true},
+                       {dK, dk_strides, s.kv_heads, true}, {dV, dv_strides, s.kv_heads, true}};
+    const Span more[2] = {Span(lse, ((size_t)lse_stride * (s.heads - 1) + s.tokens) * 4), Span(s.plan, s.plan_bytes)};
+    if (!good_views(v, 8, more, 0, 2, s.tokens, d, esz)) return LISA_ERR_INVALID_ARG;
+    const Workspace w = backward_workspace(s, d, dtype);
+    if (!workspace || workspace_bytes < w.total) return LISA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return LISA_ERR_INVALID_ARG;
+    Problem p = problem_of(s, d, scale);
+    p.Q = tensor_of(Q, q_strides);
+    p.K = tensor_of(K, k_strides);
+    p.V = tensor_of(V, v_strides);
+    p.O = tensor_of(O, o_strides);
+    p.dO = tensor_of(dO, do_strides);
+    p.dQ = tensor_of(dQ, dq_strides);
+    p.dK = tensor_of(dK, dk_strides);
+    p.dV = tensor_of(dV, dv_strides);
+    p.lse = const_cast<float *>(lse);
+    p.lse_stride = lse_stride;
+    char *ws = static_cast<char *>(workspace);
+    p.err = reinterpret_cast<int *>(ws);
+    p.delta = reinterpret_cast<float *>(ws + w.delta);
+    for (int k = 0; k < 2; ++k) p.part[k] = reinterpret_cast<float *>(ws + w.part[k]);
+    return lisa::attn::status_of(launch_simt_backward(p, dtype, static_cast<cudaStream_t>(stream)));
+}

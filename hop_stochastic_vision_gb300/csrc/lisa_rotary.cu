@@ -1,0 +1,303 @@
+// lisa_rotary.cu -- rotary positions with several axes, and the gradients'
+// opposite turn: one pass over the queries and keys.
+//
+// The angle of a pair is position * frequency modulo one turn.  With the
+// frequency in turns as a 64-bit binary fraction F = 2^64 f / 2 pi, the 64-bit
+// product position * F drops whole turns by itself, so the angle of a far
+// position is as good as that of a near one and costs one integer product.  It
+// is taken to the nearest quarter turn first; what is left, at most an eighth of
+// a turn, becomes an fp32 number, so sin and cos are taken of small arguments only.
+//
+// A thread holds the sines and cosines of the pairs in one 16-byte vector of a
+// token and turns that vector of every head in its share of the heads, four
+// heads in flight.  Bound by the bytes of Q and K, read and written once; the
+// heads are shared out only where the tokens alone do not fill the SMs, since
+// every share takes its sines anew.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "lisa_args.h"
+#include "lisa_attn.h"
+#include "lisa_bias_dev.cuh"
+#include "lisa_launch.cuh"
+#include "lisa_prompt.h"
+
+namespace lisa {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 128;
+
+struct RotaryParams {
+    Tensor Q, K, Qo, Ko;
+    const int *positions;
+    long long axis_stride, batch_stride;
+    long long threads;             // tokens times the vectors of a token
+    FastDiv div_n;
+    int heads, rows;               // query heads; with the key heads
+    int share;                     // of the rows, for one thread
+    int units, pairs, axes;        // vectors of a token; pairs that turn
+    int log_units;
+    unsigned long long turns[LISA_MAX_PAIRS];
+    unsigned char axis[LISA_MAX_PAIRS];
+};
+
+// N consecutive elements of a token as fp32.
+template <typename T, int N>
+struct Elements {
+    static constexpr int kBytes = N * (int)sizeof(T);
+    alignas(kBytes < 16 ? kBytes : 16) T v[N];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int e = 0; e < kBytes / 16; ++e) reinterpret_cast<uint4 *>(v)[e] = reinterpret_cast<const uint4 *>(p)[e];
+        } else if constexpr (kBytes == 8) {
+            *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
+        } else if constexpr (kBytes == 4) {
+            *reinterpret_cast<uint32_t *>(v) = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            v[0] = p[0];
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int e = 0; e < kBytes / 16; ++e) reinterpret_cast<uint4 *>(p)[e] = reinterpret_cast<const uint4 *>(v)[e];
+        } else if constexpr (kBytes == 8) {
+            *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(v);
+        } else if constexpr (kBytes == 4) {
+            *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(v);
+        } else {
+            p[0] = v[0];
+        }
+    }
+};
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_float(float &o, float x) { o = x; }
+__device__ __forceinline__ void from_float(__nv_bfloat16 &o, float x) { o = __float2bfloat16_rn(x); }
+
+// sin and cos of a 64-bit fraction of a turn.  bf16: the special-function unit's, 2^-20.9 off at most, far below the
+// half step 2^-9 of what is stored; fp32: the library's, of an argument within an eighth of a turn.
+template <typename T>
+__device__ __forceinline__ void sin_cos(unsigned long long phase, float &s, float &c) {
+    const unsigned quarter = (unsigned)((phase + (1ULL << 61)) >> 62);
+    const int rest = (int)((long long)(phase - ((unsigned long long)quarter << 62)) >> 32);   // 2^-32 turns, |.| <= 2^29
+    float sr, cr;
+    if constexpr (sizeof(T) == 2) {
+        const float x = (float)rest * 1.4629180792671596e-9f;   // 2 pi 2^-32
+        sr = __sinf(x);
+        cr = __cosf(x);
+    } else {
+        sincospif((float)rest * 0x1p-31f, &sr, &cr);
+    }
+    const bool swap = quarter & 1u;
+    s = swap ? cr : sr;
+    c = swap ? sr : cr;
+    if (quarter & 2u) s = -s;
+    if ((quarter + 1u) & 2u) c = -c;
+}
+
+template <typename T, int V, bool kNeighbours>
+__global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ RotaryParams x, int inverse) {
+    __shared__ unsigned long long turns[LISA_MAX_PAIRS];
+    __shared__ int axis[LISA_MAX_PAIRS];
+    if (threadIdx.x < LISA_MAX_PAIRS) {
+        turns[threadIdx.x] = x.turns[threadIdx.x];
+        axis[threadIdx.x] = x.axis[threadIdx.x];
+    }
+    __syncthreads();
+    chain_begin();
+    const long long at = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (at >= x.threads) return;
+    const int unit = (int)(at & (x.units - 1)), p0 = unit * V;
+    int i = (int)(at >> x.log_units);
+    const int b = split(i, x.div_n);
+    const bool turn = p0 < x.pairs;   // a vector is of one kind: V divides the pairs
+    float s[V], c[V];
+    if (turn) {
+        int pos[LISA_MAX_AXES];
+#pragma unroll
+        for (int a = 0; a < LISA_MAX_AXES; ++a)
+            pos[a] = a < x.axes ? x.positions[a * x.axis_stride + b * x.batch_stride + i] : 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int a = axis[p0 + e];
+            const int place = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
+            sin_cos<T>((unsigned long long)(long long)place * turns[p0 + e], s[e], c[e]);
+            if (inverse) s[e] = -s[e];
+        }
+    }
+    // the vector's two parts: x and y of its pairs, or 2 V elements side by side
+    const int lo = kNeighbours || !turn ? 2 * p0 : p0, hi = kNeighbours || !turn ? 2 * p0 + V : x.pairs + p0;
+    const int r0 = blockIdx.y * x.share, r1 = min(r0 + x.share, x.rows);
+    for (int r = r0; r < r1; r += 4) {
+        Elements<T, V> u[4], w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (r + e >= r1) break;
+            const bool key = r + e >= x.heads;
+            const Tensor &t = key ? x.K : x.Q;
+            const T *p = static_cast<const T *>(t.p) + b * t.sb + (long long)(key ? r + e - x.heads : r + e) * t.sh + i * t.st;
+            u[e].load(p + lo);
+            w[e].load(p + hi);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (r + e >= r1) break;
+            if (turn) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    // pair k: (a[k], d[k]), or elements 2 k and 2 k + 1 of the two parts together
+                    T &px = !kNeighbours ? u[e].v[k] : (2 * k < V ? u[e].v[2 * k < V ? 2 * k : 0] : w[e].v[2 * k >= V ? 2 * k - V : 0]);
+                    T &py = !kNeighbours ? w[e].v[k]
+                                         : (2 * k + 1 < V ? u[e].v[2 * k + 1 < V ? 2 * k + 1 : 0]
+                                                          : w[e].v[2 * k + 1 >= V ? 2 * k + 1 - V : 0]);
+                    const float vx = to_float(px), vy = to_float(py);
+                    from_float(px, fmaf(vx, c[k], -vy * s[k]));
+                    from_float(py, fmaf(vx, s[k], vy * c[k]));
+                }
+            }
+            const bool key = r + e >= x.heads;
+            const Tensor &t = key ? x.Ko : x.Qo;
+            T *p = static_cast<T *>(const_cast<void *>(t.p)) + b * t.sb +
+                   (long long)(key ? r + e - x.heads : r + e) * t.sh + i * t.st;
+            u[e].store(p + lo);
+            w[e].store(p + hi);
+        }
+    }
+}
+
+template <typename T, int V>
+cudaError_t go(RotaryParams &x, const lisa_rotary_rule &rule, int d, long long tokens, int inverse, cudaStream_t s) {
+    x.units = d / 2 / V;
+    for (x.log_units = 0; 1 << x.log_units < x.units; ++x.log_units) {}
+    x.threads = tokens * x.units;
+    const long long blocks = (x.threads + kThreads - 1) / kThreads;
+    // Shares of the heads while there are fewer than eight blocks per SM, a head each at least.
+    long long shares = std::min<long long>(x.rows, (8LL * kSms + blocks - 1) / blocks);
+    x.share = (int)((x.rows + shares - 1) / shares);
+    shares = (x.rows + x.share - 1) / x.share;
+    const dim3 grid((unsigned)blocks, (unsigned)shares);
+    return rule.neighbours ? launch_chained(rotary<T, V, true>, grid, kThreads, 0, s, x, inverse)
+                           : launch_chained(rotary<T, V, false>, grid, kThreads, 0, s, x, inverse);
+}
+
+// A vector of 16 bytes where the pairs are whole vectors, else of four pairs, else pair by pair (rules whose pairs are
+// no multiple of four; an access then is one element).
+template <typename T>
+cudaError_t go(RotaryParams &x, const lisa_rotary_rule &rule, int d, long long tokens, int inverse, cudaStream_t s) {
+    if (sizeof(T) == 2 && rule.pairs % 8 == 0) return go<T, sizeof(T) == 2 ? 8 : 4>(x, rule, d, tokens, inverse, s);
+    if (rule.pairs % 4 == 0) return go<T, 4>(x, rule, d, tokens, inverse, s);
+    return go<T, 1>(x, rule, d, tokens, inverse, s);
+}
+
+// A strided tensor's footprint.  Two views of one tensor whose tokens take turns do not meet although their extents do:
+// with the same token stride S (and batch strides that are multiples of it), each occupies a window of every S elements.
+struct Footprint {
+    Span span;
+    uintptr_t first;
+    size_t window, token, batch;   // bytes; token 0: no windows
+    Footprint(const void *p, const lisa_strides *s, int B, int heads, int n, int d, size_t esz) {
+        if (!p || B == 0 || heads == 0 || n == 0) {
+            first = 0;
+            window = token = batch = 0;
+            return;
+        }
+        span = Span(p, extent(s, B, heads, n, d, esz));
+        first = span.lo;
+        window = ((size_t)s->head * (heads - 1) + d) * esz;
+        token = (size_t)s->token * esz;
+        batch = B > 1 ? (size_t)s->batch * esz : 0;
+        if (n <= 1 || window > token || (token && batch % token != 0)) token = 0;
+    }
+    bool meets(const Footprint &o) const {
+        if (!span.meets(o.span)) return false;
+        if (token == 0 || token != o.token) return true;
+        const size_t gap = o.first >= first ? (o.first - first) % token : (token - (first - o.first) % token) % token;
+        return !(gap >= window && gap + o.window <= token);
+    }
+};
+
+bool same(const void *a, const lisa_strides *as, const void *b, const lisa_strides *bs, int B, int heads, int n) {
+    return a == b && (B <= 1 || as->batch == bs->batch) && (heads <= 1 || as->head == bs->head) &&
+           (n <= 1 || as->token == bs->token);
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace lisa
+
+using namespace lisa::attn;
+
+extern "C" lisa_status lisa_rotary(const void *Q, const lisa_strides *q_strides, const void *K,
+                                   const lisa_strides *k_strides, void *Qo, const lisa_strides *qo_strides, void *Ko,
+                                   const lisa_strides *ko_strides, const int *positions, long long axis_stride,
+                                   long long batch_stride, int B, int heads, int kv_heads, int n, int d,
+                                   const lisa_rotary_rule *rule, int inverse, int dtype, void *stream) {
+    if (B < 0 || heads < 0 || kv_heads < 0 || n < 0 || d < 1 || !rule) return LISA_ERR_INVALID_ARG;
+    if (dtype != LISA_F32 && dtype != LISA_BF16) return LISA_ERR_INVALID_ARG;
+    if (rule->axes < 1 || rule->axes > LISA_MAX_AXES || rule->pairs < 1 || rule->pairs > LISA_MAX_PAIRS ||
+        rule->neighbours < 0 || rule->neighbours > 1 || 2 * (long long)rule->pairs > d)
+        return LISA_ERR_INVALID_ARG;
+    if (d != 16 && d != 32 && d != 64) return LISA_ERR_UNSUPPORTED;
+    if (heads > 65535 || kv_heads > 65535 || (long long)B * n >= 1LL << 31) return LISA_ERR_UNSUPPORTED;
+    RotaryParams x{};
+    for (int p = 0; p < rule->pairs; ++p) {
+        const double f = rule->frequency[p];
+        if (rule->axis[p] < 0 || rule->axis[p] >= rule->axes || !std::isfinite(f) || std::fabs(f) > 0x1p20)
+            return LISA_ERR_INVALID_ARG;
+        double t = f * 0.15915494309189533577;   // turns per position; whole turns do not count
+        t -= std::floor(t);
+        x.turns[p] = t < 1.0 ? (unsigned long long)std::ldexp(t, 64) : 0ULL;
+        x.axis[p] = (unsigned char)rule->axis[p];
+    }
+    if (B == 0 || n == 0 || heads + kv_heads == 0) return LISA_OK;
+    const size_t esz = dtype == LISA_BF16 ? 2 : 4;
+    const struct { const void *in; const lisa_strides *is; void *out; const lisa_strides *os; int heads; } pair[2] = {
+        {Q, q_strides, Qo, qo_strides, heads}, {K, k_strides, Ko, ko_strides, kv_heads}};
+    for (const auto &t : pair)
+        if (t.heads > 0 && (!t.in || !t.out || !aligned16(t.in) || !aligned16(t.out) ||
+                            !good_strides(t.is, B, t.heads, n, d, esz, false) ||
+                            !good_strides(t.os, B, t.heads, n, d, esz, true)))
+            return LISA_ERR_INVALID_ARG;
+    if (!positions || !aligned4(positions) || axis_stride < 0 || batch_stride < 0 || axis_stride > 1LL << 38 ||
+        batch_stride > 1LL << 38)
+        return LISA_ERR_INVALID_ARG;
+    const Span where(positions, ((size_t)axis_stride * (rule->axes - 1) + (size_t)batch_stride * (B - 1) + n) * 4);
+    const Footprint ins[2] = {{heads ? Q : nullptr, q_strides, B, heads, n, d, esz},
+                              {kv_heads ? K : nullptr, k_strides, B, kv_heads, n, d, esz}};
+    const Footprint outs[2] = {{heads ? Qo : nullptr, qo_strides, B, heads, n, d, esz},
+                               {kv_heads ? Ko : nullptr, ko_strides, B, kv_heads, n, d, esz}};
+    if (outs[0].meets(outs[1])) return LISA_ERR_INVALID_ARG;
+    for (int a = 0; a < 2; ++a) {
+        if (outs[a].span.meets(where) || outs[a].meets(ins[1 - a])) return LISA_ERR_INVALID_ARG;
+        if (pair[a].heads > 0 && outs[a].meets(ins[a]) &&
+            !same(pair[a].in, pair[a].is, pair[a].out, pair[a].os, B, pair[a].heads, n))
+            return LISA_ERR_INVALID_ARG;
+    }
+    if (heads) {
+        x.Q = {Q, q_strides->batch, q_strides->head, q_strides->token};
+        x.Qo = {Qo, qo_strides->batch, qo_strides->head, qo_strides->token};
+    }
+    if (kv_heads) {
+        x.K = {K, k_strides->batch, k_strides->head, k_strides->token};
+        x.Ko = {Ko, ko_strides->batch, ko_strides->head, ko_strides->token};
+    }
+    x.positions = positions;
+    x.axis_stride = axis_stride;
+    x.batch_stride = batch_stride;
+    x.div_n = fast_div(n);
+    x.heads = heads;
+    x.rows = heads + kv_heads;
+    x.pairs = rule->pairs;
+    x.axes = rule->axes;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const long long tokens = (long long)B * n;
+    return status_of(dtype == LISA_BF16 ? go<__nv_bfloat16>(x, *rule, d, tokens, inverse ? 1 : 0, cs)
+                                        : go<float>(x, *rule, d, tokens, inverse ? 1 : 0, cs));
+}

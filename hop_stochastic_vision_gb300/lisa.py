@@ -352,3 +352,10 @@ from .attention import (ATTENTION_EXPORTED, RelativeBias, cross_attention, cross
                         exact_buckets, log_buckets, relative_bias, relative_bias_backward)
 
 EXPORTED = EXPORTED + ATTENTION_EXPORTED
+
+
+# -- rotary positions, packed prompts, the cache in 4 bits ------------------------------
+from .prompt import (PROMPT_EXPORTED, PackedSequences, RotaryAxes, prompt_attention,  # noqa: E402,F401
+                     prompt_attention_backward, rotary, rotary_backward)
+
+EXPORTED = EXPORTED + PROMPT_EXPORTED

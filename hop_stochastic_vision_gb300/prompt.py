@@ -1,0 +1,352 @@
+"""What a backbone needs around a prompt: rotary positions with several axes,
+attention over packed sequences of different lengths, and a key/value cache in
+4 bits (C ABI in include/lisa_prompt.h), on CUDA tensors.
+
+Argument marshalling only, as in ``lisa``: torch supplies device memory and
+streams, every step runs in the library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import math
+
+import torch
+
+from .attention import _DTYPES, _default_scale, _int32, _ref, _run, _workspace, lisa_strides
+from .lisa import LISA_ERR_UNSUPPORTED, LISA_OK, LisaError, load
+
+LISA_MAX_PAIRS = 32
+LISA_MAX_AXES = 4
+
+PROMPT_EXPORTED = ("lisa_rotary", "lisa_packed_plan_bytes", "lisa_packed_plan",
+                   "lisa_prompt_attention_workspace_bytes", "lisa_prompt_attention",
+                   "lisa_prompt_attention_backward_workspace_bytes", "lisa_prompt_attention_backward")
+
+
+class lisa_rotary_rule(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int), ("pairs", ctypes.c_int), ("neighbours", ctypes.c_int),
+                ("axis", ctypes.c_int * LISA_MAX_PAIRS), ("frequency", ctypes.c_double * LISA_MAX_PAIRS)]
+
+
+class lisa_packed(ctypes.Structure):
+    _fields_ = [("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t), ("sequences", ctypes.c_int),
+                ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("causal", ctypes.c_int), ("items", ctypes.c_int * 3), ("joins", ctypes.c_int * 3),
+                ("parts", ctypes.c_int * 3), ("seal", ctypes.c_uint)]
+
+
+_lib = None
+
+
+def _library():
+    """The loaded library with this module's signatures set."""
+    global _lib
+    if _lib is None:
+        lib = load()
+        vp, i, f, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
+        sp, pp = ctypes.POINTER(lisa_strides), ctypes.POINTER(lisa_packed)
+        lib.lisa_rotary.argtypes = [vp, sp, vp, sp, vp, sp, vp, sp, vp, ll, ll, i, i, i, i, i,
+                                    ctypes.POINTER(lisa_rotary_rule), i, i, vp]
+        lib.lisa_rotary.restype = i
+        lib.lisa_packed_plan_bytes.argtypes = [ctypes.POINTER(i), i, i, i, i]
+        lib.lisa_packed_plan_bytes.restype = sz
+        lib.lisa_packed_plan.argtypes = [ctypes.POINTER(i), i, i, i, i, vp, sz, pp]
+        lib.lisa_packed_plan.restype = i
+        lib.lisa_prompt_attention_workspace_bytes.argtypes = [pp, i, i]
+        lib.lisa_prompt_attention_workspace_bytes.restype = sz
+        lib.lisa_prompt_attention.argtypes = [vp, sp, vp, sp, vp, sp, vp, sp, vp, ll, pp, i, f, i, vp, sz, vp]
+        lib.lisa_prompt_attention.restype = i
+        lib.lisa_prompt_attention_backward_workspace_bytes.argtypes = [pp, i, i]
+        lib.lisa_prompt_attention_backward_workspace_bytes.restype = sz
+        lib.lisa_prompt_attention_backward.argtypes = [vp, sp, vp, sp, vp, sp, vp, sp, vp, ll, vp, sp, vp, sp, vp, sp,
+                                                       vp, sp, pp, i, f, i, vp, sz, vp]
+        lib.lisa_prompt_attention_backward.restype = i
+        _lib = lib
+    return _lib
+
+
+# -- the C entry points under their own names ---------------------------------------
+# strides: lisa_strides; pointers are ints (device addresses, but for lengths and the plan: host).
+
+def lisa_rotary(Q, qs, K, ks, Qo, qos, Ko, kos, positions, axis_stride, batch_stride, B, heads, kv_heads, n, d, rule,
+                inverse, dtype, stream) -> int:
+    return int(_library().lisa_rotary(Q, _ref(qs), K, _ref(ks), Qo, _ref(qos), Ko, _ref(kos), positions, axis_stride,
+                                      batch_stride, B, heads, kv_heads, n, d, _ref(rule), inverse, dtype, stream))
+
+
+def _lengths(lengths):
+    return None if lengths is None else (ctypes.c_int * max(1, len(lengths)))(*lengths)
+
+
+def lisa_packed_plan_bytes(lengths, sequences, heads, kv_heads, causal) -> int:
+    return int(_library().lisa_packed_plan_bytes(_lengths(lengths), sequences, heads, kv_heads, causal))
+
+
+def lisa_packed_plan(lengths, sequences, heads, kv_heads, causal, plan, plan_bytes, packed) -> int:
+    return int(_library().lisa_packed_plan(_lengths(lengths), sequences, heads, kv_heads, causal, plan, plan_bytes,
+                                           _ref(packed)))
+
+
+def lisa_prompt_attention_workspace_bytes(packed, d, dtype) -> int:
+    return int(_library().lisa_prompt_attention_workspace_bytes(_ref(packed), d, dtype))
+
+
+def lisa_prompt_attention(Q, qs, K, ks, V, vs, O, os, lse, lse_stride, packed, d, scale, dtype, workspace,
+                          workspace_bytes, stream) -> int:
+    return int(_library().lisa_prompt_attention(Q, _ref(qs), K, _ref(ks), V, _ref(vs), O, _ref(os), lse, lse_stride,
+                                                _ref(packed), d, scale, dtype, workspace, workspace_bytes, stream))
+
+
+def lisa_prompt_attention_backward_workspace_bytes(packed, d, dtype) -> int:
+    return int(_library().lisa_prompt_attention_backward_workspace_bytes(_ref(packed), d, dtype))
+
+
+def lisa_prompt_attention_backward(Q, qs, K, ks, V, vs, O, os, lse, lse_stride, dO, dos, dQ, dqs, dK, dks, dV, dvs,
+                                   packed, d, scale, dtype, workspace, workspace_bytes, stream) -> int:
+    return int(_library().lisa_prompt_attention_backward(
+        Q, _ref(qs), K, _ref(ks), V, _ref(vs), O, _ref(os), lse, lse_stride, dO, _ref(dos), dQ, _ref(dqs), dK,
+        _ref(dks), dV, _ref(dvs), _ref(packed), d, scale, dtype, workspace, workspace_bytes, stream))
+
+
+# -- tensors of a call ------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=4096)
+def _strides_of(shape, stride) -> lisa_strides:
+    """Strides of [.., heads, tokens, d], 3-d or 4-d; one that no step uses may be anything legal."""
+    d = shape[-1]
+    if stride[-1] != 1 and d > 1:
+        raise ValueError("the elements of a token must be contiguous (last stride 1)")
+    used = tuple(t if s > 1 else d for s, t in zip(shape[:-1], stride[:-1]))
+    return lisa_strides(*((0,) + used if len(used) == 2 else used))
+
+
+def _strides(t, name, dims, dtype, index) -> lisa_strides:
+    if t.dtype != dtype or dtype not in _DTYPES:
+        raise ValueError("%s must be of the call's type, float32 or bfloat16" % name)
+    if t.dim() not in dims:
+        raise ValueError("%s must have %s dimensions" % (name, " or ".join(map(str, dims))))
+    at = t.get_device()
+    if at != index or at < 0:
+        raise ValueError("these operators run on CUDA tensors only" if at < 0 else "tensors must be on one device")
+    if max(t.shape) >> 31:      # the call itself refuses far less, if it gets to see it
+        raise LisaError(LISA_ERR_UNSUPPORTED)
+    return _strides_of(tuple(t.shape), t.stride())
+
+
+# -- rotary positions ---------------------------------------------------------------------
+
+class RotaryAxes:
+    """Which pairs of a token's elements turn with which axis, and how fast.
+
+    ``sections`` are the numbers of pairs of the axes, in order (their sum P at
+    most d / 2; elements behind 2 P are left as they are).  Pair i of an axis's s
+    pairs turns by base ** (-i / s) per position, with ``shared`` pair p of all P
+    by base ** (-p / P).  ``pairing`` "halves" joins elements p and P + p,
+    "neighbours" 2 p and 2 p + 1.  ``frequencies``, P radians per position, replaces
+    the rule of the base."""
+
+    def __init__(self, d: int, sections, base: float = 10000.0, pairing: str = "halves", shared: bool = False,
+                 frequencies=None):
+        sections = [_int32(s) for s in sections]
+        if not 1 <= len(sections) <= LISA_MAX_AXES or min(sections) < 0:
+            raise ValueError("sections must be the pairs of 1 to %d axes" % LISA_MAX_AXES)
+        total = sum(sections)
+        if not 1 <= total <= min(LISA_MAX_PAIRS, int(d) // 2):
+            raise ValueError("%d pairs do not fit a width of %d" % (total, d))
+        if pairing not in ("halves", "neighbours"):
+            raise ValueError('pairing must be "halves" or "neighbours"')
+        axis = [a for a, s in enumerate(sections) for _ in range(s)]
+        if frequencies is None:
+            if not base > 0 or not math.isfinite(base):
+                raise ValueError("base must be positive")
+            steps = [p / total for p in range(total)] if shared else [i / s for s in sections for i in range(s)]
+            frequencies = [math.pow(base, -x) for x in steps]
+        frequencies = [float(f) for f in frequencies]
+        if len(frequencies) != total or not all(math.isfinite(f) and abs(f) <= 2.0 ** 20 for f in frequencies):
+            raise ValueError("frequencies must be %d finite numbers of at most 2^20" % total)
+        self.d, self.axes, self.pairs, self.frequencies = int(d), len(sections), total, tuple(frequencies)
+        self.struct = lisa_rotary_rule(len(sections), total, int(pairing == "neighbours"),
+                                       (ctypes.c_int * LISA_MAX_PAIRS)(*axis),
+                                       (ctypes.c_double * LISA_MAX_PAIRS)(*frequencies))
+
+
+def _rotary(stream, q, k, qs, ks, positions, where, rule, out, inverse):
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    qo, ko = out
+    index = q.get_device()
+    qos = _strides(qo, "out", (q.dim(),), q.dtype, index)
+    kos = None if k is None else _strides(ko, "out", (q.dim(),), q.dtype, index)
+    B, heads, n, d = q.shape if q.dim() == 4 else (1,) + tuple(q.shape)
+    status = _library().lisa_rotary(q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, qo.data_ptr(), qos,
+                                    None if k is None else ko.data_ptr(), kos, positions.data_ptr(), *where, B, heads,
+                                    0 if k is None else k.shape[-3], n, d, rule.struct, inverse, _DTYPES[q.dtype],
+                                    stream)
+    if status != LISA_OK:
+        raise LisaError(status)
+    return qo if k is None else (qo, ko)
+
+
+def _turn(q, k, positions, rule, out, stream, inverse):
+    index = q.get_device()
+    qs = _strides(q, "q", (3, 4), q.dtype, index)
+    ks = None if k is None else _strides(k, "k", (q.dim(),), q.dtype, index)
+    d, n = q.shape[-1], q.shape[-2]
+    B = q.shape[0] if q.dim() == 4 else 1
+    if d != rule.d:
+        raise ValueError("the rule is of width %d, q of %d" % (rule.d, d))
+    if k is not None and (k.shape[:-3] != q.shape[:-3] or k.shape[-2:] != q.shape[-2:]):
+        raise ValueError("k must be [B, kv_heads, n, d] for q [B, heads, n, d]")
+    if positions.get_device() != index or positions.dtype != torch.int32:
+        raise ValueError("positions must be an int32 CUDA tensor on q's device")
+    shape, stride = tuple(positions.shape), positions.stride()
+    if shape == (rule.axes, n):
+        where = (stride[0] if rule.axes > 1 else 0, 0)
+    elif shape == (rule.axes, B, n) and q.dim() == 4:
+        where = (stride[0] if rule.axes > 1 else 0, stride[1] if B > 1 else 0)
+    else:
+        raise ValueError("positions must be [%d, %d] or [%d, %d, %d]" % (rule.axes, n, rule.axes, B, n))
+    if n > 1 and stride[-1] != 1:
+        raise ValueError("the positions of an axis must be contiguous")
+    if out is not None:
+        if k is None:
+            out = (out, None)
+        if out[0].shape != q.shape or (k is not None and out[1].shape != k.shape):
+            raise ValueError("out must have the shapes of q and k")
+    return _run(index, stream, _rotary, q, k, qs, ks, positions, where, rule, out, inverse)
+
+
+def rotary(q: torch.Tensor, k, positions: torch.Tensor, rule: RotaryAxes, *, out=None, stream=None):
+    """q [B, heads, n, d] and k [B, kv_heads, n, d] (fp32 or bf16, strided views are
+    fine; without the batch for packed tokens; k may be None) turned by their
+    tokens' positions (int32 [axes, B, n], or [axes, n] for every batch entry).
+    Returns (q', k'), or q' alone without k: new contiguous tensors, or ``out``
+    (the same form; q and k themselves turn in place)."""
+    return _turn(q, k, positions, rule, out, stream, 0)
+
+
+def rotary_backward(dq: torch.Tensor, dk, positions: torch.Tensor, rule: RotaryAxes, *, out=None, stream=None):
+    """Gradients of ``rotary``'s q and k for those of its results: the opposite turn."""
+    return _turn(dq, dk, positions, rule, out, stream, 1)
+
+
+# -- attention over packed prompts ---------------------------------------------------------
+
+class PackedSequences:
+    """Sequences of the given lengths (whole numbers, on the host), one behind the
+    other along the tokens, and how the work on them is shared out for ``heads``
+    query heads on ``kv_heads`` key heads; ``causal``: a query reads the keys up to
+    itself, else all of its sequence.  Made once for a batch, for every layer and
+    every captured graph that has it; making it copies a table to ``device``."""
+
+    def __init__(self, lengths, heads: int, kv_heads: int = None, *, causal: bool = True, device="cuda"):
+        lengths = [_int32(x) for x in lengths]
+        heads = _int32(heads)
+        kv_heads = heads if kv_heads is None else _int32(kv_heads)
+        array, causal = _lengths(lengths), int(bool(causal))
+        lib = _library()
+        nbytes = lib.lisa_packed_plan_bytes(array, len(lengths), heads, kv_heads, causal)
+        table = torch.empty(max(nbytes, 16), dtype=torch.uint8)
+        self.struct = lisa_packed()
+        status = lib.lisa_packed_plan(array, len(lengths), heads, kv_heads, causal, table.data_ptr(), nbytes,
+                                      ctypes.byref(self.struct))
+        if status != LISA_OK:
+            raise LisaError(status)
+        self.table = table.to(device)
+        if not self.table.is_cuda:
+            raise ValueError("a packed batch lives on a CUDA device")
+        self.index = self.table.get_device()
+        self.struct.plan = self.table.data_ptr()
+        self.lengths, self.tokens = tuple(lengths), self.struct.tokens
+        self.heads, self.kv_heads, self.causal = heads, kv_heads, bool(causal)
+        self._bytes = {}
+
+    def workspace_bytes(self, d: int, dtype: int, backward: bool = False) -> int:
+        """Workspace of a call, by its width and the ABI's type."""
+        key = (d, dtype, backward)
+        if key not in self._bytes:
+            call = lisa_prompt_attention_backward_workspace_bytes if backward else lisa_prompt_attention_workspace_bytes
+            self._bytes[key] = call(self.struct, d, dtype)
+        return self._bytes[key]
+
+
+def _packed_args(q, k, v, seqs, scale):
+    index, dtype = q.get_device(), q.dtype
+    qs, ks, vs = (_strides(t, name, (3,), dtype, index) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    heads, tokens, d = q.shape
+    if heads != seqs.heads or k.shape != (seqs.kv_heads, tokens, d) or v.shape != k.shape:
+        raise ValueError("q must be [%d, tokens, d], k and v [%d, tokens, d] for these sequences"
+                         % (seqs.heads, seqs.kv_heads))
+    if tokens < seqs.tokens:
+        raise ValueError("the sequences have %d tokens, the tensors %d" % (seqs.tokens, tokens))
+    if seqs.index != index:
+        raise ValueError("tensors must be on one device")
+    scale = _default_scale(d) if scale is None else float(scale)
+    return index, (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs), (seqs.struct, d, scale, _DTYPES[dtype])
+
+
+def _fresh(shape, dtype, device, seqs):
+    """A result; what stands behind the sequences is 0 in one that the call makes."""
+    make = torch.empty if shape[1] == seqs.tokens else torch.zeros
+    return make(shape, dtype=dtype, device=device)
+
+
+def _prompt_forward(stream, q, head, tail, seqs, return_lse, out, workspace):
+    if out is None:
+        out = _fresh(q.shape, q.dtype, q.device, seqs)
+    os = _strides(out, "out", (3,), q.dtype, q.get_device())
+    lse = _fresh(q.shape[:2], torch.float32, q.device, seqs) if return_lse else None
+    keep, ws, nbytes = _workspace(workspace, seqs.workspace_bytes(tail[1], tail[3]), q.device)
+    status = _library().lisa_prompt_attention(*head, out.data_ptr(), os, lse.data_ptr() if return_lse else None,
+                                              q.shape[1], *tail, ws, nbytes, stream)
+    del keep
+    if status != LISA_OK:
+        raise LisaError(status)
+    return (out, lse) if return_lse else out
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqs: PackedSequences, *, scale=None,
+                     return_lse: bool = False, out=None, workspace=None, stream=None):
+    """Softmax attention within the packed sequences ``seqs``: queries [heads,
+    tokens, d] over keys and values [kv_heads, tokens, d] (fp32 or bf16; strided
+    views are fine, with d contiguous and strides of 16 bytes; tokens may go on
+    behind the sequences).  ``scale`` defaults to 1 / sqrt(d).  Returns O [heads,
+    tokens, d] (a new contiguous tensor, 0 behind the sequences, unless ``out`` is
+    given, which is left as it was there), with ``return_lse`` also the fp32
+    log-sum-exp [heads, tokens] that the backward pass reads."""
+    index, head, tail = _packed_args(q, k, v, seqs, scale)
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    return _run(index, stream, _prompt_forward, q, head, tail, seqs, return_lse, out, workspace)
+
+
+def _prompt_backward(stream, q, k, head, saved, tail, seqs, workspace):
+    dq = _fresh(q.shape, q.dtype, q.device, seqs)
+    dk, dv = (_fresh(k.shape, q.dtype, q.device, seqs) for _ in range(2))
+    index = q.get_device()
+    grads = []
+    for t in (dq, dk, dv):
+        grads += [t.data_ptr(), _strides(t, "gradients", (3,), q.dtype, index)]
+    keep, ws, nbytes = _workspace(workspace, seqs.workspace_bytes(tail[1], tail[3], True), q.device)
+    status = _library().lisa_prompt_attention_backward(*head, *saved, *grads, *tail, ws, nbytes, stream)
+    del keep
+    if status != LISA_OK:
+        raise LisaError(status)
+    return dq, dk, dv
+
+
+def prompt_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+                              dout: torch.Tensor, seqs: PackedSequences, *, scale=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of ``prompt_attention`` for the upstream gradient
+    ``dout``, given the forward's ``out`` and ``lse``; 0 behind the sequences."""
+    index, head, tail = _packed_args(q, k, v, seqs, scale)
+    if out.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("out and dout must have q's shape")
+    if not (lse.get_device() == index and lse.dtype == torch.float32 and lse.is_contiguous()
+            and lse.shape == q.shape[:2]):
+        raise ValueError("lse must be the forward's contiguous fp32 tensor [heads, tokens]")
+    saved = (out.data_ptr(), _strides(out, "out", (3,), q.dtype, index), lse.data_ptr(), q.shape[1], dout.data_ptr(),
+             _strides(dout, "dout", (3,), q.dtype, index))
+    return _run(index, stream, _prompt_backward, q, k, head, saved, tail, seqs, workspace)

@@ -1,0 +1,127 @@
+/*
+ * lisa_prompt.h -- C ABI of what a backbone needs around a prompt of image,
+ * video or text tokens, beside the cross attention (lisa_attention.h): rotary
+ * positions with several axes, attention over packed sequences of different
+ * lengths, and a key/value cache held in 4 bits.
+ *
+ * Conventions are those of lisa_attention.h (types, strides, alignment,
+ * overlaps told by extents, errors, streams, workspaces) unless stated here.
+ */
+#ifndef LISA_PROMPT_H_
+#define LISA_PROMPT_H_
+
+#include <stddef.h>
+
+#include "lisa_attention.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define LISA_MAX_PAIRS 32
+#define LISA_MAX_AXES 4
+
+/*
+ * Rotary positions.  The first 2 P elements of a token are P pairs (x, y): the
+ * elements (p, P + p), or (2 p, 2 p + 1) with `neighbours`.  Pair p belongs to
+ * the axis axis[p] and turns by the angle t = position[axis[p]] frequency[p]:
+ *
+ *   (x, y) -> (x cos t - y sin t, x sin t + y cos t)
+ *
+ * `inverse` turns by -t: the backward pass, given the gradients of the turned
+ * tensors.  Elements behind the pairs are copied.  The angle is reduced to a
+ * turn in whole numbers, so positions of any size keep the accuracy that the
+ * frequency has in 64 bits.  LISA_F32: sin and cos good to 2^-22; LISA_BF16: to
+ * 2^-20, the result rounded once.
+ */
+typedef struct lisa_rotary_rule {
+    int axes;                          /* 1 .. LISA_MAX_AXES */
+    int pairs;                         /* P: 1 .. d / 2 */
+    int neighbours;                    /* 0 or 1 */
+    int axis[LISA_MAX_PAIRS];          /* 0 .. axes - 1 */
+    double frequency[LISA_MAX_PAIRS];  /* radians per position, |f| <= 2^20 */
+} lisa_rotary_rule;
+
+/*
+ * Q [B][heads][n][d] and K [B][kv_heads][n][d] (NULL with kv_heads 0: none)
+ * into Qo, Ko.  positions (device int32, any values): token i of entry b stands
+ * at positions[a axis_stride + b batch_stride + i] on axis a (a batch stride of
+ * 0 repeats one entry).  d is 16, 32 or 64, B n below 2^31.  An output may be its own input
+ * (same pointer and strides); what else overlaps is refused, except that views
+ * of one tensor whose tokens take turns (heads of queries and keys side by side
+ * in a token) are told apart.
+ */
+lisa_status lisa_rotary(const void *Q, const lisa_strides *q_strides, const void *K, const lisa_strides *k_strides,
+                        void *Qo, const lisa_strides *qo_strides, void *Ko, const lisa_strides *ko_strides,
+                        const int *positions, long long axis_stride, long long batch_stride, int B, int heads,
+                        int kv_heads, int n, int d, const lisa_rotary_rule *rule, int inverse, int dtype, void *stream);
+
+/*
+ * Attention over packed prompts.  Sequences of any lengths stand one behind the
+ * other along the tokens of Q [heads][tokens][d], K and V [kv_heads][tokens][d]
+ * (batch strides are not read).  A query reads the keys of its own sequence,
+ * with `causal` those up to itself:
+ *
+ *   s_ij = scale q_i . k_j,  p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j
+ *
+ * The lengths are known on the host, so the work is shared out there, once: the
+ * plan is a table that lisa_packed_plan writes into host memory and the caller
+ * copies to the device (16-byte aligned), for as many calls, layers and captured
+ * graphs as have these lengths and heads.  The calls read it and the struct and
+ * keep nothing.  The struct is as lisa_packed_plan left it, but for `plan`; the
+ * table at `plan` is that plan's bytes.
+ */
+typedef struct lisa_packed {
+    const void *plan;          /* device address of the table; 0 tokens need none */
+    size_t plan_bytes;
+    int sequences, tokens;     /* tokens: the lengths' sum */
+    int heads, kv_heads, causal;
+    /* sizes of the plan's lists: the passes' items, items cut into parts, all parts */
+    int items[3], joins[3], parts[3];
+    unsigned seal;             /* of the numbers above: a struct that was changed is refused */
+} lisa_packed;
+
+/*
+ * lengths: host, `sequences` of them (0 .. 2^20), each from 0, 2^22 in all;
+ * causal 0 or 1.  The bytes of the plan (0 for arguments that lisa_packed_plan
+ * would reject), and the plan with its struct (`plan` left NULL).
+ */
+size_t lisa_packed_plan_bytes(const int *lengths, int sequences, int heads, int kv_heads, int causal);
+lisa_status lisa_packed_plan(const int *lengths, int sequences, int heads, int kv_heads, int causal, void *plan,
+                             size_t plan_bytes, lisa_packed *packed);
+
+/*
+ * The forward pass.  Tensors may hold more tokens than the sequences: O and lse
+ * (fp32 [heads][lse_stride], may be NULL; lse_stride >= tokens) are written for
+ * the sequences' tokens and left as they were behind them.  d is 16, 32 or 64.
+ * Arithmetic, masks and limits are those of lisa_cross_attention; the tokens of
+ * other sequences are never used, whatever they hold.  Within a sequence a NaN
+ * or an infinity may reach any of its rows, earlier ones too.  The workspace
+ * (16-byte aligned) begins with the call's error word; LISA_F32 needs none.
+ */
+size_t lisa_prompt_attention_workspace_bytes(const lisa_packed *packed, int d, int dtype);
+lisa_status lisa_prompt_attention(const void *Q, const lisa_strides *q_strides, const void *K,
+                                  const lisa_strides *k_strides, const void *V, const lisa_strides *v_strides, void *O,
+                                  const lisa_strides *o_strides, float *lse, long long lse_stride,
+                                  const lisa_packed *packed, int d, float scale, int dtype, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/*
+ * The backward pass: O and lse as the forward wrote them, dO the upstream
+ * gradient; dQ like Q, dK and dV like K, with strides, written for the
+ * sequences' tokens.  dK and dV are summed over the heads that share a key head,
+ * in a fixed order.  The workspace begins with the call's error word.
+ */
+size_t lisa_prompt_attention_backward_workspace_bytes(const lisa_packed *packed, int d, int dtype);
+lisa_status lisa_prompt_attention_backward(
+    const void *Q, const lisa_strides *q_strides, const void *K, const lisa_strides *k_strides, const void *V,
+    const lisa_strides *v_strides, const void *O, const lisa_strides *o_strides, const float *lse, long long lse_stride,
+    const void *dO, const lisa_strides *do_strides, void *dQ, const lisa_strides *dq_strides, void *dK,
+    const lisa_strides *dk_strides, void *dV, const lisa_strides *dv_strides, const lisa_packed *packed, int d,
+    float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LISA_PROMPT_H_ */

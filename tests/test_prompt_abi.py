@@ -1,0 +1,259 @@
+"""The C ABI of the rotary positions and the packed prompts on the host:
+refusals, sizes and plans, decided before anything is launched (no GPU)."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+from hop_stochastic_vision_gb300 import attention as att
+from hop_stochastic_vision_gb300 import build as lisa_build
+from hop_stochastic_vision_gb300 import lisa
+from hop_stochastic_vision_gb300 import prompt
+
+FAKE = 1 << 20          # 16-byte aligned, never dereferenced
+OK, INV, UNS, WSP = lisa.LISA_OK, lisa.LISA_ERR_INVALID_ARG, lisa.LISA_ERR_UNSUPPORTED, lisa.LISA_ERR_WORKSPACE
+MB = 1 << 20
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    lisa_build.build()
+    lisa.load()
+
+
+def _strides(h, t, d, **over):
+    return att.lisa_strides(over.get("batch", h * t * d), over.get("head", t * d), over.get("token", d))
+
+
+def _rule(axes=2, pairs=8, neighbours=0, axis=None, frequency=None):
+    axis = [p % max(axes, 1) for p in range(32)] if axis is None else axis
+    frequency = [0.5] * 32 if frequency is None else frequency
+    return prompt.lisa_rotary_rule(axes, pairs, neighbours, (ctypes.c_int * 32)(*axis),
+                                   (ctypes.c_double * 32)(*frequency))
+
+
+def _rotary(**over):
+    a = dict(Q=FAKE, K=FAKE + MB, Qo=FAKE + 2 * MB, Ko=FAKE + 3 * MB, positions=FAKE + 4 * MB, axis_stride=16,
+             batch_stride=8, B=2, heads=4, kv_heads=2, n=8, d=16, rule=_rule(), inverse=0, dtype=lisa.LISA_F32)
+    a.update(over)
+    qs, ks = _strides(a["heads"], a["n"], a["d"]), _strides(a["kv_heads"], a["n"], a["d"])
+    return prompt.lisa_rotary(a["Q"], a.get("qs", qs), a["K"], a.get("ks", ks), a["Qo"], a.get("qos", qs), a["Ko"],
+                              a.get("kos", ks), a["positions"], a["axis_stride"], a["batch_stride"], a["B"], a["heads"],
+                              a["kv_heads"], a["n"], a["d"], a["rule"], a["inverse"], a["dtype"], 0)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(Q=0), INV), (dict(K=0), INV), (dict(Qo=0), INV), (dict(Ko=0), INV), (dict(positions=0), INV),
+    (dict(Q=FAKE + 8), INV), (dict(Ko=FAKE + 3 * MB + 4), INV), (dict(positions=FAKE + 4 * MB + 2), INV),
+    (dict(qs=None), INV), (dict(kos=None), INV), (dict(qs=_strides(4, 8, 16, token=18)), INV),
+    (dict(qs=_strides(4, 8, 16, token=12)), INV), (dict(qos=_strides(4, 8, 16, batch=0)), INV),
+    (dict(qos=_strides(4, 8, 16, head=16)), INV), (dict(axis_stride=-1), INV), (dict(batch_stride=-8), INV),
+    (dict(B=-1), INV), (dict(n=-1), INV), (dict(heads=-1), INV), (dict(kv_heads=-2), INV), (dict(d=0), INV),
+    (dict(dtype=2), INV), (dict(d=48), UNS), (dict(d=128), UNS), (dict(heads=70000), UNS), (dict(B=1 << 20, n=1 << 11), UNS),
+    (dict(rule=None), INV), (dict(rule=_rule(axes=0)), INV), (dict(rule=_rule(axes=5)), INV), (dict(rule=_rule(pairs=0)), INV),
+    (dict(rule=_rule(pairs=9)), INV), (dict(rule=_rule(pairs=33), d=64), INV), (dict(rule=_rule(neighbours=2)), INV),
+    (dict(rule=_rule(axis=[2] * 32)), INV), (dict(rule=_rule(axis=[-1] * 32)), INV),
+    (dict(rule=_rule(frequency=[math.nan] * 32)), INV), (dict(rule=_rule(frequency=[2.0 ** 21] * 32)), INV),
+    (dict(Qo=FAKE + MB), INV), (dict(Ko=FAKE), INV), (dict(Qo=FAKE + 64), INV),      # over K, over Q, beside itself
+    (dict(Ko=FAKE + 2 * MB), INV), (dict(Qo=FAKE + 4 * MB), INV),                    # both in one place; the positions
+    (dict(Qo=FAKE, qos=_strides(4, 8, 16, token=32, head=256, batch=1024)), INV),    # in place, other strides
+    (dict(Q=FAKE, Qo=FAKE, K=FAKE + 64 * 4, Ko=FAKE + 64 * 4, qs=att.lisa_strides(8 * 64, 16, 64),
+          qos=att.lisa_strides(8 * 64, 16, 64), ks=att.lisa_strides(8 * 64, 16, 64), kos=att.lisa_strides(8 * 64, 16, 64)), INV),
+])
+def test_rotary_rejects_before_launch(over, status):
+    assert _rotary(**over) == status
+
+
+def test_empty_rotary_launches_nothing():
+    assert _rotary(B=0, Q=0, K=0, Qo=0, Ko=0, positions=0) == OK
+    assert _rotary(n=0, Q=0, K=0, Qo=0, Ko=0, positions=0) == OK
+    assert _rotary(heads=0, kv_heads=0, Q=0, K=0, Qo=0, Ko=0, positions=0) == OK
+
+
+# ---------------------------------------------------------------- the plan
+
+def _plan(lengths, heads, kv_heads, causal):
+    nbytes = prompt.lisa_packed_plan_bytes(lengths, len(lengths), heads, kv_heads, causal)
+    raw = np.zeros(nbytes + 64, dtype=np.uint8)
+    at = (-raw.ctypes.data) % 16
+    packed = prompt.lisa_packed()
+    assert prompt.lisa_packed_plan(lengths, len(lengths), heads, kv_heads, causal, raw.ctypes.data + at, nbytes, packed) == OK
+    return raw[at:at + nbytes], packed
+
+
+def _lists(table, packed):
+    """(items, joins, order, starts) of each pass, as the kernels find them."""
+    up = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    at, out = 0, []
+    for p in range(3):
+        heads = packed.kv_heads if p == 2 else packed.heads
+        spans = []
+        for count, width in ((packed.items[p], 8), (packed.joins[p], 4), (packed.items[p] * heads, 1), (153, 1)):
+            spans.append(table[at:at + 4 * count * width].view(np.int32).reshape(-1, width))
+            at = up(at + 4 * count * width)
+        out.append(spans)
+    assert at == packed.plan_bytes
+    return out
+
+
+@pytest.mark.parametrize("lengths,heads,kv,causal", [
+    ([1], 1, 1, 1), ([0, 0], 2, 1, 1), ([], 3, 3, 0), ([4096], 12, 4, 1), ([2000], 1, 1, 0), ([16384], 4, 4, 1),
+    ([127, 1, 0, 128, 129, 300, 1000, 5], 6, 2, 1), ([127, 1, 0, 128, 129, 300, 1000, 5], 6, 2, 0), ([50000], 2, 1, 1),
+    ([3] * 500, 8, 8, 1)])
+def test_a_plan_covers_every_pair_of_tiles_once(lengths, heads, kv, causal):
+    table, packed = _plan(lengths, heads, kv, causal)
+    assert packed.tokens == sum(lengths)
+    starts_of = np.cumsum([0] + lengths)
+    for p, (items, joins, order, starts) in enumerate(_lists(table, packed)):
+        rows, h = (256 if p == 0 else 128), (kv if p == 2 else heads)
+        units, slots = {}, {}
+        for row0, length, first, t0, t1, part, steps, _ in items.tolist():
+            assert lengths[list(starts_of).index(row0) if length and row0 in starts_of else 0] >= 0
+            assert first % rows == 0 and first < length and 0 <= t0 < t1 <= steps
+            units.setdefault((row0, length, first, steps), []).append((t0, t1, part))
+            if part >= 0:
+                assert part not in slots
+                slots[part] = (row0 + first, min(rows, length - first))
+        want = set()
+        for s, length in enumerate(lengths):
+            tiles = -(-length // 128)
+            for first in range(0, length, rows):
+                steps = tiles if not causal else tiles - first // 128 if p == 2 else min(tiles, (first + rows) // 128)
+                want.add((int(starts_of[s]), length, first, steps * (heads // kv if p == 2 else 1)))
+        assert set(units) == want
+        cut = 0
+        for (row0, length, first, steps), parts in units.items():
+            parts.sort()
+            assert parts[0][0] == 0 and parts[-1][1] == steps
+            assert all(a[1] == b[0] for a, b in zip(parts, parts[1:]))
+            assert (len(parts) == 1) == (parts[0][2] == -1)
+            cut += len(parts) if len(parts) > 1 else 0
+        assert sorted(slots) == list(range(packed.parts[p])) and cut == packed.parts[p]
+        named = []
+        for row, count, part0, parts in joins.tolist():
+            named += range(part0, part0 + parts)
+            assert all(slots[x] == (row, count) for x in range(part0, part0 + parts))
+        assert sorted(named) == sorted(slots)
+        # every (item, head) pair has one worker, who takes the longer ones first
+        assert sorted(order[:, 0].tolist()) == list(range(len(items) * h))
+        assert starts[0, 0] == 0 and starts[-1, 0] == len(items) * h and (np.diff(starts[:, 0]) >= 0).all()
+        cost = (items[:, 4] - items[:, 3])[order[:, 0] // max(h, 1)] if len(items) and h else np.zeros(0)
+        loads = []
+        for w in range(152):
+            mine = cost[starts[w, 0]:starts[w + 1, 0]]
+            assert (np.diff(mine) <= 0).all()
+            loads.append((mine + 1).sum())
+        if len(cost):   # the longest-first rule's own bound: an even share and one item more
+            assert max(loads) <= sum(loads) / 152 + cost.max() + 1
+
+
+@pytest.mark.parametrize("args,status", [
+    (([-1], 1, 2, 1, 1), INV), ((None, 1, 2, 1, 1), INV), (([1], 1, 3, 2, 1), INV), (([1], 1, 2, 0, 1), INV),
+    (([1], 1, -2, 1, 1), INV), (([1], 1, 2, 1, 2), INV), (([1], -1, 2, 1, 1), INV), (([1], 1, 70000, 1, 1), UNS),
+    (([1 << 22, 1], 2, 1, 1, 1), UNS), (([1 << 22], 1, 60000, 60000, 0), UNS), (([1], (1 << 20) + 1, 1, 1, 0), UNS)])
+def test_plans_that_are_refused(args, status):
+    lengths, n, heads, kv, causal = args      # (2^20 + 1 sequences are refused before their lengths are read)
+    raw = np.zeros(1 << 16, dtype=np.uint8)
+    assert prompt.lisa_packed_plan_bytes(lengths, n, heads, kv, causal) == 0
+    assert prompt.lisa_packed_plan(lengths, n, heads, kv, causal, raw.ctypes.data + (-raw.ctypes.data) % 16, 1 << 15,
+                                   prompt.lisa_packed()) == status
+
+
+def test_plans_into_too_little_memory():
+    n = prompt.lisa_packed_plan_bytes([300], 1, 2, 1, 1)
+    raw = np.zeros(n + 64, dtype=np.uint8)
+    at = raw.ctypes.data + (-raw.ctypes.data) % 16
+    assert prompt.lisa_packed_plan([300], 1, 2, 1, 1, at, n - 1, prompt.lisa_packed()) == WSP
+    assert prompt.lisa_packed_plan([300], 1, 2, 1, 1, at + 4, n, prompt.lisa_packed()) == INV
+    assert prompt.lisa_packed_plan([300], 1, 2, 1, 1, 0, n, prompt.lisa_packed()) == INV
+    assert prompt.lisa_packed_plan([300], 1, 2, 1, 1, at, n, None) == INV
+
+
+# ----------------------------------------------------------- packed attention
+
+def _packed(lengths=(300, 5), heads=4, kv=2, causal=1, plan=FAKE + 64 * MB, changed=()):
+    _, packed = _plan(list(lengths), heads, kv, causal)
+    packed.plan = plan
+    for name, value in dict(changed).items():
+        setattr(packed, name, value)
+    return packed
+
+
+def _forward(**over):
+    a = dict(Q=FAKE, K=FAKE + MB, V=FAKE + 2 * MB, O=FAKE + 3 * MB, lse=FAKE + 4 * MB, lse_stride=305, packed=_packed(),
+             d=64, scale=0.125, dtype=lisa.LISA_BF16, ws=FAKE + 32 * MB, wbytes=1 << 40)
+    a.update(over)
+    qs, ks = att.lisa_strides(0, 305 * 64, 64), att.lisa_strides(0, 305 * 64, 64)
+    return prompt.lisa_prompt_attention(a["Q"], a.get("qs", qs), a["K"], a.get("ks", ks), a["V"], a.get("vs", ks), a["O"],
+                                        a.get("os", qs), a["lse"], a["lse_stride"], a["packed"], a["d"], a["scale"],
+                                        a["dtype"], a["ws"], a["wbytes"], 0)
+
+
+def _backward(**over):
+    a = dict(Q=FAKE, K=FAKE + MB, V=FAKE + 2 * MB, O=FAKE + 3 * MB, lse=FAKE + 4 * MB, lse_stride=305, packed=_packed(),
+             dO=FAKE + 5 * MB, dQ=FAKE + 6 * MB, dK=FAKE + 7 * MB, dV=FAKE + 8 * MB, d=64, scale=0.125,
+             dtype=lisa.LISA_BF16, ws=FAKE + 32 * MB, wbytes=1 << 40)
+    a.update(over)
+    qs, ks = att.lisa_strides(0, 305 * 64, 64), att.lisa_strides(0, 305 * 64, 64)
+    return prompt.lisa_prompt_attention_backward(
+        a["Q"], a.get("qs", qs), a["K"], a.get("ks", ks), a["V"], a.get("vs", ks), a["O"], a.get("os", qs), a["lse"],
+        a["lse_stride"], a["dO"], a.get("dos", qs), a["dQ"], a.get("dqs", qs), a["dK"], a.get("dks", ks), a["dV"],
+        a.get("dvs", ks), a["packed"], a["d"], a["scale"], a["dtype"], a["ws"], a["wbytes"], 0)
+
+
+BAD = [
+    (dict(Q=0), INV), (dict(K=0), INV), (dict(V=0), INV), (dict(O=0), INV), (dict(Q=FAKE + 8), INV),
+    (dict(qs=None), INV), (dict(vs=None), INV), (dict(qs=att.lisa_strides(0, 305 * 64, 60)), INV),
+    (dict(ks=att.lisa_strides(0, 305 * 64, 32)), INV), (dict(ks=att.lisa_strides(0, -64, 64)), INV),
+    (dict(lse=FAKE + 2), INV), (dict(lse_stride=304), INV), (dict(packed=None), INV), (dict(d=0), INV), (dict(dtype=3), INV),
+    (dict(d=48), UNS), (dict(scale=0.0), INV), (dict(scale=math.nan), INV), (dict(scale=math.inf), INV),
+    (dict(packed=_packed), INV), (dict(ws=0), WSP), (dict(wbytes=16), WSP), (dict(ws=FAKE + 32 * MB + 8), INV),
+]
+BAD_PACKED = [dict(plan=0), dict(plan=FAKE + 8), dict(tokens=306), dict(tokens=-1), dict(heads=5), dict(kv_heads=4),
+              dict(kv_heads=0), dict(causal=0), dict(plan_bytes=16), dict(heads=1 << 20), dict(sequences=3), dict(seal=0),
+              dict(items=(ctypes.c_int * 3)(9, 9, 9)), dict(parts=(ctypes.c_int * 3)(9, 9, 9))]
+
+
+def _over(over):
+    return {k: (v(plan=FAKE + 8) if callable(v) else v) for k, v in over.items()}
+
+
+@pytest.mark.parametrize("over,status", BAD + [
+    (dict(O=FAKE), INV), (dict(O=FAKE + MB + 256), INV), (dict(lse=FAKE + 3 * MB + 64), INV), (dict(lse=FAKE + 64), INV),
+    (dict(O=FAKE + 64 * MB), INV), (dict(os=att.lisa_strides(0, 64, 64)), INV),
+])
+def test_forward_rejects_before_launch(over, status):
+    assert _forward(**_over(over)) == status
+
+
+@pytest.mark.parametrize("over,status", BAD + [
+    (dict(dO=0), INV), (dict(dQ=0), INV), (dict(dK=0), INV), (dict(dV=0), INV), (dict(lse=0), INV),
+    (dict(dQ=FAKE + 7 * MB), INV), (dict(dK=FAKE + 8 * MB), INV), (dict(dV=FAKE + 4 * MB), INV),
+    (dict(dK=FAKE + 64 * MB), INV), (dict(dqs=None), INV), (dict(dqs=att.lisa_strides(0, 64, 64)), INV),
+    (dict(dos=None), INV), (dict(dos=att.lisa_strides(0, 305 * 64, 63)), INV),
+])
+def test_backward_rejects_before_launch(over, status):
+    assert _backward(**_over(over)) == status
+
+
+@pytest.mark.parametrize("over", BAD_PACKED)
+def test_structs_that_no_plan_left(over):
+    for call in (_forward, _backward):
+        assert call(packed=_packed(changed=over)) == INV
+
+
+def test_empty_prompts_launch_nothing():
+    for packed in (_packed((0,)), _packed(()), _packed((5,), heads=0, kv=0)):
+        none = dict(Q=0, K=0, V=0, O=0, ws=0, wbytes=0, lse_stride=1 << 20)
+        assert _forward(packed=packed, **none) == OK
+        assert _backward(packed=packed, dO=0, dQ=0, dK=0, dV=0, **none) == OK
+        assert prompt.lisa_prompt_attention_workspace_bytes(packed, 64, lisa.LISA_BF16) == 0
+
+
+def test_workspace_bytes():
+    ws, back = prompt.lisa_prompt_attention_workspace_bytes, prompt.lisa_prompt_attention_backward_workspace_bytes
+    p = _packed()
+    assert ws(p, 64, lisa.LISA_F32) == 0 and back(p, 64, lisa.LISA_F32) >= 4 * 305 * 4
+    assert ws(p, 64, lisa.LISA_BF16) > 0 and ws(p, 48, lisa.LISA_BF16) == 0 and back(p, 48, lisa.LISA_BF16) == 0
+    assert ws(_packed((4000,), 1, 1), 64, lisa.LISA_BF16) > 256 * 64 * 4

@@ -1,0 +1,284 @@
+"""Attention over packed prompts on the GPU, sequence by sequence against the
+64-bit restatement and its elementwise bounds (attention_ref.py; the causal mask
+is a bias of -inf there)."""
+import math
+
+import pytest
+import torch
+
+import attention_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def lisa():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from hop_stochastic_vision_gb300 import build, lisa as binding
+    build.build()
+    binding.load()
+    return binding
+
+
+class Case:
+    def __init__(self, lisa, dtype, lengths, heads, kv, d, *, causal=True, layout="heads", scale=None, spread=1.0, seed=0,
+                 behind=0):
+        g = torch.Generator().manual_seed(seed)
+        T = sum(lengths) + behind
+        self.lisa, self.dtype, self.lengths, self.causal = lisa, dtype, lengths, causal
+        self.scale = 1 / math.sqrt(d) if scale is None else scale
+        self.ref = [(spread * torch.randn(heads, T, d, generator=g)).to(dtype)]
+        self.ref += [torch.randn(kv, T, d, generator=g).to(dtype) for _ in range(2)]
+        self.ref += [torch.randn(heads, T, d, generator=g).to(dtype)]
+        if layout == "tokens":
+            self.q, self.do = (x.cuda().transpose(0, 1).contiguous().transpose(0, 1) for x in (self.ref[0], self.ref[3]))
+            pair = torch.stack((self.ref[1].transpose(0, 1), self.ref[2].transpose(0, 1)), 1).contiguous().cuda()
+            self.k, self.v = pair[:, 0].transpose(0, 1), pair[:, 1].transpose(0, 1)
+        else:
+            self.q, self.k, self.v, self.do = (x.cuda() for x in self.ref)
+        self.seqs = lisa.PackedSequences(lengths, heads, kv, causal=causal)
+
+    def forward(self, **kw):
+        return self.lisa.prompt_attention(self.q, self.k, self.v, self.seqs, scale=self.scale, return_lse=True, **kw)
+
+    def backward(self, out, lse, **kw):
+        return self.lisa.prompt_attention_backward(self.q, self.k, self.v, out, lse, self.do, self.seqs,
+                                                   scale=self.scale, **kw)
+
+    def check(self, which=None):
+        out, lse = self.forward()
+        got = (out, lse) + tuple(self.backward(out, lse))
+        at = 0
+        for s, L in enumerate(self.lengths):
+            rows, at = slice(at, at + L), at + L
+            if L == 0 or (which is not None and s not in which):
+                continue
+            q, k, v, do = (x[None, :, rows] for x in self.ref)
+            mask = dict(table=torch.tensor([[0.0] * q.shape[1], [-math.inf] * q.shape[1]]),
+                        index=torch.ones(L, L).triu(1).long()) if self.causal else {}
+            want = ref.attention(q, k, v, do, scale=self.scale, dtype=self.dtype, **mask)
+            for name, x in zip(("o", "lse", "dq", "dk", "dv"), got):
+                ref.assert_within(x[None, :, rows], want[name], "%s of sequence %d" % (name, s))
+        return got
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [16, 32, 64])
+@pytest.mark.parametrize("lengths", [[1], [2], [63], [64], [65], [127, 1, 0, 128, 129], [0, 0, 3, 0], [257], [300, 1, 1, 17]])
+def test_lengths_and_widths(lisa, dtype, causal, d, lengths):
+    Case(lisa, dtype, lengths, 2, 1, d, causal=causal, seed=len(lengths) + d).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads,kv", [(4, 4), (4, 2), (6, 1), (3, 3), (12, 4)])
+@pytest.mark.parametrize("layout", ["heads", "tokens"])
+def test_head_layouts(lisa, dtype, causal, heads, kv, layout):
+    Case(lisa, dtype, [70, 150, 5], heads, kv, 64, causal=causal, layout=layout, seed=heads).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_sequences(lisa, dtype, causal):
+    g = torch.Generator().manual_seed(3)
+    lengths = torch.randint(0, 150, (60,), generator=g).tolist()
+    Case(lisa, dtype, lengths, 3, 3, 32, causal=causal, layout="tokens").check()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths,heads,kv", [([2000], 1, 1), ([1500, 3, 900], 2, 1), ([1030, 40], 6, 2)])
+def test_long_sequences_of_few_heads(lisa, causal, lengths, heads, kv):
+    """Units cut into parts, in every pass."""
+    c = Case(lisa, BF16, lengths, heads, kv, 64, causal=causal, seed=5)
+    s = c.seqs.struct
+    assert all(s.parts[p] > 0 for p in range(3))
+    c.check()
+    Case(lisa, BF16, lengths, heads, kv, 32, causal=causal, seed=6, layout="tokens").check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+def test_other_sequences_play_no_part(lisa, dtype, causal):
+    """NaN and infinities in one sequence, and behind the last, leave the others as they are."""
+    lengths = [100, 37, 190, 1, 129, 0, 260, 33]
+    c = Case(lisa, dtype, lengths, 2, 1, 64, causal=causal, behind=50)
+    clean = c.check()
+    bad = [slice(100, 137), slice(328, 457), slice(sum(lengths), None)]
+    for t, what in ((c.q, math.nan), (c.k, math.inf), (c.v, math.nan), (c.do, -math.inf)):
+        for rows in bad:
+            t[:, rows] = what
+    out, lse = c.forward()
+    grads = c.backward(out, lse)
+    for a, b in zip(clean, (out, lse) + tuple(grads)):
+        good = torch.ones(a.shape[1], dtype=torch.bool)
+        for rows in bad:
+            good[rows] = False
+        assert torch.equal(a[:, good.cuda()], b[:, good.cuda()])
+        assert not b[:, sum(lengths):].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_behind_the_last_sequence_are_left(lisa, dtype):
+    c = Case(lisa, dtype, [70, 130], 2, 2, 32, behind=40)
+    wide = torch.full((240, 4, 32), 7.0, dtype=dtype, device="cuda")
+    view = wide[:, :2].transpose(0, 1)
+    out, _ = c.forward(out=view)
+    assert out is view and (wide[200:] == 7).all() and (wide[:, 2:] == 7).all()
+    assert torch.equal(view[:, :200], c.forward()[0][:, :200])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+def test_large_scores(lisa, dtype, causal):
+    """Scores of some hundreds: the maximum moves between tiles and the sum is rescaled."""
+    Case(lisa, dtype, [500, 90], 2, 2, 64, causal=causal, spread=12.0, scale=1.0).check()
+
+
+def test_rising_scores(lisa):
+    """Every tile of keys outdoes the one before, by more and more."""
+    c = Case(lisa, BF16, [700], 1, 1, 64)
+    ramp = torch.linspace(0, 40, 700).to(BF16)
+    for ref_t, t in ((c.ref[0], c.q), (c.ref[1], c.k)):
+        ref_t[..., 0] = ramp if t is c.k else 4.0
+        t.copy_(ref_t)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_keys_of_minus_infinity(lisa, dtype):
+    """A query whose scores are all -inf has o = 0, lse = -inf and no gradient."""
+    c = Case(lisa, dtype, [40, 9], 2, 1, 64)
+    c.q.zero_()
+    c.q[:, :, 0] = 1.0
+    c.k.zero_()
+    c.k[:, 3:7, 0] = -math.inf
+    c.q[:, 40:, 1] = -1.0
+    c.k[:, 40:, 0] = -math.inf
+    out, lse = c.forward()
+    assert (lse[:, 40:] == -math.inf).all() and not out[:, 40:].any()
+    assert torch.isfinite(lse[:, :40]).all() and torch.isfinite(out[:, :40]).all()
+    seen = torch.tensor([j for j in range(40) if not 3 <= j < 7])
+    want = c.ref[2][0, seen].double().cumsum(0)[-1] / 36
+    assert ((out[0, 39].double().cpu() - want).abs() <= 2.0 ** -7 * c.ref[2][0, seen].double().abs().mean(0)).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+def test_same_bits_every_time_whatever_the_workspace_holds(lisa, dtype, causal):
+    c = Case(lisa, dtype, [1300, 60], 2, 1, 64, causal=causal)
+    dt = lisa.LISA_F32 if dtype == F32 else lisa.LISA_BF16
+    out, lse = c.forward()
+    first = c.backward(out, lse)
+    for fill in (0x00, 0xFF):
+        ws = torch.full((max(c.seqs.workspace_bytes(64, dt), c.seqs.workspace_bytes(64, dt, True)),), fill,
+                        dtype=torch.uint8, device="cuda")
+        out2, lse2 = c.forward(workspace=ws)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+        ws.fill_(fill)
+        for a, b in zip(first, c.backward(out, lse, workspace=ws)):
+            assert torch.equal(a, b)
+        assert lisa.lisa_query_status(ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == lisa.LISA_OK
+
+
+def test_repeated_keys_of_all_heads(lisa):
+    c = Case(lisa, BF16, [90, 200], 4, 4, 64)
+    for n in (1, 2):
+        c.ref[n] = c.ref[n][:1].expand(4, -1, -1)
+    c.k, c.v = (c.ref[n][:1].cuda().expand(4, -1, -1) for n in (1, 2))
+    c.check()
+
+
+def test_other_streams_and_captured_graphs(lisa):
+    lengths = [260, 100, 0, 900]
+    c = Case(lisa, BF16, lengths, 4, 2, 64)
+    out, lse = c.forward()
+    grads = c.backward(out, lse)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o2, l2 = c.forward()
+        g2 = c.backward(o2, l2)
+    o3, l3 = c.forward(stream=side.cuda_stream)
+    g3 = c.backward(o3, l3, stream=side.cuda_stream)
+    side.synchronize()
+    for a, b, x in zip((out, lse) + grads, (o2, l2) + g2, (o3, l3) + g3):
+        assert torch.equal(a, b) and torch.equal(a, x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        og, lg = c.forward()
+        gg = c.backward(og, lg)
+    for seed in (0, 9):
+        other = Case(lisa, BF16, lengths, 4, 2, 64, seed=seed)
+        for name in ("q", "k", "v", "do"):
+            getattr(c, name).copy_(getattr(other, name))
+        graph.replay()
+        torch.cuda.synchronize()
+        oe, le = other.forward()
+        for a, b in zip((og, lg) + gg, (oe, le) + other.backward(oe, le)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_gradient_against_differences(lisa, causal):
+    """fp32 directional derivatives by central differences, as for the cross attention: off by h^2 / 6 of the third
+    derivative and by the rounding of the two sums, 2^-23 sum |o dO| (L + d) / h at most."""
+    c = Case(lisa, F32, [33, 1, 20], 2, 1, 16, causal=causal)
+    out, lse = c.forward()
+    grads = dict(zip("qkv", c.backward(out, lse)))
+    h = 2.0 ** -6
+    for name in "qkv":
+        x = getattr(c, name)
+        e = torch.randn(x.shape, generator=torch.Generator().manual_seed(7)).cuda()
+        e /= e.norm()
+        base = x.clone()
+        sums = []
+        for sign in (1, -1):
+            x.copy_(base + sign * h * e)
+            o, _ = c.forward()
+            sums.append(float((o.double() * c.do.double()).sum()))
+        x.copy_(base)
+        scale = float((out.double() * c.do.double()).abs().sum())
+        want = float((grads[name].double() * e.double()).sum())
+        assert abs((sums[0] - sums[1]) / (2 * h) - want) <= scale * (h * h + 2.0 ** -23 * 50 / h)
+
+
+def test_empty_batches(lisa):
+    for lengths in ([], [0], [0, 0]):
+        seqs = lisa.PackedSequences(lengths, 2)
+        x = torch.randn(2, 0, 64, device="cuda")
+        out, lse = lisa.prompt_attention(x, x, x, seqs, return_lse=True)
+        assert out.shape == x.shape and lse.shape == (2, 0)
+        assert all(g.shape == x.shape for g in lisa.prompt_attention_backward(x, x, x, out, lse, x, seqs))
+        x = torch.randn(2, 5, 64, device="cuda")
+        assert not lisa.prompt_attention(x, x, x, seqs).any()
+
+
+def test_refusals(lisa):
+    seqs = lisa.PackedSequences([5, 3], 4, 2)
+    q, k = torch.randn(4, 8, 64, device="cuda"), torch.randn(2, 8, 64, device="cuda")
+    out, lse = lisa.prompt_attention(q, k, k, seqs, return_lse=True)
+    for args in ((q.half(), k, k), (q, k.bfloat16(), k), (q.cpu(), k, k), (q[:, :7], k[:, :7], k[:, :7]), (q[:2], k, k),
+                 (q, k[:1], k[:1]), (q, k, k[:, :7]), (q[None], k, k), (q[..., :32], k, k)):
+        with pytest.raises(ValueError):
+            lisa.prompt_attention(*args, seqs)
+    with pytest.raises(lisa.LisaError):
+        lisa.prompt_attention(q, k, k, seqs, scale=0.0)
+    with pytest.raises(lisa.LisaError):
+        lisa.prompt_attention(q, k, k, seqs, out=q)
+    with pytest.raises(ValueError):
+        lisa.prompt_attention(q, k, k, seqs, out=q[:, :4])
+    with pytest.raises(ValueError):
+        lisa.prompt_attention_backward(q, k, k, out, lse.double(), out, seqs)
+    with pytest.raises(ValueError):
+        lisa.prompt_attention_backward(q, k, k, out, lse, out[:, :4], seqs)
+    wide = torch.randn(4, 8, 48, device="cuda")
+    with pytest.raises(lisa.LisaError):
+        lisa.prompt_attention(wide, wide[:2], wide[:2], seqs)
+    for bad in ((["a"], 2, 2), ([-1], 2, 2), ([3], 3, 2), ([1 << 23], 1, 1), ([1], -1, 1), ([1 << 40], 1, 1)):
+        with pytest.raises((ValueError, lisa.LisaError)):
+            lisa.PackedSequences(*bad)

@@ -1,0 +1,229 @@
+"""Rotary positions with several axes on the GPU against their definition in 64
+bits, elementwise.
+
+Bounds.  sin and cos are off by at most 2^-22 (fp32: the remainder of the angle
+rounded to fp32, within an eighth of a turn, 2^-24.3, and the library's two units
+in the last place) or 2^-20 (bf16: the special-function unit's 2^-20.9 on top of that); the two
+products and the sum round three times, 2^-24 of |x| + |y| each; the result is
+rounded once to its type, 2^-24 or 2^-8 of itself.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+SIN = {F32: 2.0 ** -22, BF16: 2.0 ** -20}
+R = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module")
+def lisa():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from hop_stochastic_vision_gb300 import build, lisa as binding
+    build.build()
+    binding.load()
+    return binding
+
+
+def want(x, positions, rule, pairing, sections, inverse=False):
+    """(value, bound) of x [.., heads, n, d] with positions [axes, (B,) n]."""
+    axis = [a for a, s in enumerate(sections) for _ in range(s)]
+    P = len(axis)
+    angle = torch.stack([positions[a].double().cpu() * f for a, f in zip(axis, rule.frequencies)], -1)   # [.., n, P]
+    if inverse:
+        angle = -angle
+    if angle.dim() == 3:
+        angle = angle[:, None]
+    v = x.double().cpu()
+    lo = [p if pairing == "halves" else 2 * p for p in range(P)]
+    hi = [P + p if pairing == "halves" else 2 * p + 1 for p in range(P)]
+    out, mag = v.clone(), torch.zeros_like(v)
+    a, b = v[..., lo], v[..., hi]
+    out[..., lo], out[..., hi] = a * angle.cos() - b * angle.sin(), a * angle.sin() + b * angle.cos()
+    mag[..., lo] = mag[..., hi] = a.abs() + b.abs()
+    return out, mag * (SIN[x.dtype] + 3 * 2.0 ** -24) + R[x.dtype] * out.abs() * (mag > 0) * 1.01 + 2.0 ** -126 * (mag > 0)
+
+
+def check(got, ref):
+    value, bound = ref
+    off = (got.double().cpu() - value).abs()
+    assert got.shape == value.shape and bool((off <= bound).all()), float((off / bound.clamp(min=1e-300)).max())
+
+
+def rand(shape, dtype, seed, layout="heads"):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(*shape, generator=g).to(dtype).cuda()
+    return x if layout == "heads" else x.transpose(-3, -2).contiguous().transpose(-3, -2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("pairing", ["halves", "neighbours"])
+@pytest.mark.parametrize("d,sections", [(16, [8]), (16, [3, 4]), (32, [8, 8]), (32, [1]), (64, [32]), (64, [16, 16]),
+                                        (64, [8, 12, 12]), (64, [8, 8, 8]), (64, [4, 4, 4, 8]), (64, [5, 7, 9]),
+                                        (64, [0, 12]), (64, [31])])
+def test_widths_sections_and_pairings(lisa, dtype, pairing, d, sections):
+    rule = lisa.RotaryAxes(d, sections, pairing=pairing)
+    q, k = rand((2, 3, 37, d), dtype, 1), rand((2, 1, 37, d), dtype, 2, "tokens")
+    pos = torch.randint(-50, 3000, (len(sections), 2, 37), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    a, b = lisa.rotary(q, k, pos.cuda(), rule)
+    check(a, want(q, pos, rule, pairing, sections))
+    check(b, want(k, pos, rule, pairing, sections))
+    a, b = lisa.rotary_backward(q, k, pos.cuda(), rule)
+    check(a, want(q, pos, rule, pairing, sections, True))
+    check(b, want(k, pos, rule, pairing, sections, True))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,heads,kv,n", [(1, 1, 1, 1), (64, 12, 4, 1), (3, 5, 5, 7), (1, 8, 1, 4099), (2, 1, 1, 3136),
+                                          (5, 33, 3, 17)])
+def test_batches_heads_and_lengths(lisa, dtype, B, heads, kv, n):
+    rule = lisa.RotaryAxes(64, [16, 16], shared=True, base=500.0)
+    q, k = rand((B, heads, n, 64), dtype, n, "tokens"), rand((B, kv, n, 64), dtype, n + 1)
+    i = torch.arange(n, dtype=torch.int32)
+    pos = torch.stack((i // 7, i % 7))          # the batch's entries at the same places
+    a, b = lisa.rotary(q, k, pos.cuda(), rule)
+    check(a, want(q, pos, rule, "halves", [16, 16]))
+    check(b, want(k, pos, rule, "halves", [16, 16]))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_far_positions(lisa, dtype):
+    """Up to 2^22 the 64-bit angle itself is good to 2^-30; the largest positions turn too (checked by length)."""
+    rule = lisa.RotaryAxes(64, [32])
+    pos = torch.tensor([[0, 1, -1, 1 << 20, (1 << 22) - 1, -(1 << 22), 99991, 7]], dtype=torch.int32)
+    q = rand((1, 2, 8, 64), dtype, 5)
+    check(lisa.rotary(q, None, pos.cuda(), rule), want(q, pos, rule, "halves", [32]))
+    pos = torch.tensor([[2 ** 31 - 1, -2 ** 31, 2 ** 31 - 2]], dtype=torch.int32)
+    q = rand((1, 2, 3, 64), F32, 6)
+    out = lisa.rotary(q, None, pos.cuda(), rule).double()
+    length = lambda x: (x[..., :32].double() ** 2 + x[..., 32:].double() ** 2)  # noqa: E731
+    assert bool(((length(out) - length(q)).abs() <= 2.0 ** -20 * length(q)).all())
+
+
+def test_whole_turns_and_slow_frequencies(lisa):
+    """A frequency of a whole turn leaves everything, a negative one turns the other way, 0 not at all."""
+    pos = torch.arange(11, dtype=torch.int32)[None]
+    for f in ([2 * math.pi, -0.3, 0.0, 1e-12, 40.0, -2.0 ** 20, 3.0, 2.0 ** -30],):
+        rule = lisa.RotaryAxes(16, [8], frequencies=f)
+        q = rand((1, 1, 11, 16), F32, 7)
+        check(lisa.rotary(q, None, pos.cuda(), rule), want(q, pos, rule, "halves", [8]))
+
+
+def test_packed_tokens_without_a_batch(lisa):
+    rule = lisa.RotaryAxes(64, [8, 12, 12], pairing="neighbours")
+    q, k = rand((4, 130, 64), BF16, 8, "tokens"), rand((2, 130, 64), BF16, 9)
+    pos = torch.randint(0, 60, (3, 130), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    a, b = lisa.rotary(q, k, pos.cuda(), rule)
+    check(a, want(q, pos, rule, "neighbours", [8, 12, 12]))
+    check(b, want(k, pos, rule, "neighbours", [8, 12, 12]))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_in_place_within_one_projection(lisa, dtype):
+    """q and k as views of one projection's result, turned where they are; the values beside them stay."""
+    B, n, h, g, d = 2, 29, 6, 2, 32
+    rule = lisa.RotaryAxes(d, [16])
+    qkv = rand((B, n, h + 2 * g, d), dtype, 10)
+    before = qkv.clone()
+    q, k = qkv[:, :, :h].transpose(1, 2), qkv[:, :, h:h + g].transpose(1, 2)
+    pos = torch.arange(n, dtype=torch.int32)[None]
+    ref_q, ref_k = want(q, pos, rule, "halves", [16]), want(k, pos, rule, "halves", [16])
+    a, b = lisa.rotary(q, k, pos.cuda(), rule, out=(q, k))
+    assert a is q and b is k
+    check(q, ref_q)
+    check(k, ref_k)
+    assert torch.equal(qkv[:, :, h + g:], before[:, :, h + g:])
+
+
+def test_outputs_in_another_layout(lisa):
+    rule = lisa.RotaryAxes(64, [32])
+    q = rand((2, 3, 10, 64), BF16, 11)
+    wide = torch.full((2, 12, 4, 64), 7.0, dtype=BF16, device="cuda")
+    view = wide[:, :10, :3].transpose(1, 2)
+    pos = torch.arange(10, dtype=torch.int32, device="cuda")[None]
+    assert lisa.rotary(q, None, pos, rule, out=view) is view
+    assert torch.equal(view, lisa.rotary(q, None, pos, rule))
+    assert (wide[:, 10:] == 7).all() and (wide[:, :, 3] == 7).all()
+
+
+def test_repeated_inputs_and_empty_ones(lisa):
+    rule = lisa.RotaryAxes(16, [8])
+    q = rand((1, 1, 6, 16), F32, 12).expand(3, 4, 6, 16)
+    pos = torch.arange(18, dtype=torch.int32).reshape(1, 3, 6)
+    check(lisa.rotary(q, None, pos.cuda(), rule), want(q, pos, rule, "halves", [8]))
+    for shape in ((0, 4, 6, 16), (3, 0, 6, 16), (3, 4, 0, 16)):
+        x = torch.empty(shape, device="cuda")
+        assert lisa.rotary(x, None, torch.zeros(1, shape[2], dtype=torch.int32, device="cuda"), rule).shape == shape
+
+
+def test_not_a_number_stays_in_its_pair(lisa):
+    rule = lisa.RotaryAxes(16, [8])
+    q = rand((1, 1, 3, 16), F32, 13)
+    q[0, 0, 1, 2] = math.nan
+    out = lisa.rotary(q, None, torch.arange(3, dtype=torch.int32, device="cuda")[None], rule)
+    bad = torch.isnan(out).nonzero().tolist()
+    assert bad == [[0, 0, 1, 2], [0, 0, 1, 10]]
+
+
+def test_gradient_by_differences(lisa):
+    """rotary is linear: its gradient along a direction is its value there, and the backward its transpose."""
+    rule = lisa.RotaryAxes(64, [8, 12, 12])
+    x, y = rand((2, 2, 9, 64), F32, 14), rand((2, 2, 9, 64), F32, 15)
+    pos = torch.randint(0, 90, (3, 2, 9), dtype=torch.int32, device="cuda")
+    step = 2.0 ** -7
+    e = torch.zeros_like(x)
+    e[1, 0, 3, 5] = 1.0
+    diff = (lisa.rotary(x + step * e, None, pos, rule).double() - lisa.rotary(x - step * e, None, pos, rule).double()) / (2 * step)
+    grad = lisa.rotary_backward(y, None, pos, rule).double()
+    # the quotient's two fp32 results are each off by 2^-21 (|x| + |y|) at most, over 2^-6
+    bound = float((y.double() ** 2).sum().sqrt()) * 2 * 2.0 ** -21 * 8 * 2.0 ** 6
+    assert abs(float((diff * y.double()).sum()) - float(grad[1, 0, 3, 5])) <= bound
+
+
+def test_streams_and_graphs(lisa):
+    rule = lisa.RotaryAxes(64, [16, 16])
+    q, k = rand((2, 3, 50, 64), BF16, 16), rand((2, 3, 50, 64), BF16, 17)
+    pos = torch.randint(0, 90, (2, 50), dtype=torch.int32, device="cuda")
+    a, b = lisa.rotary(q, k, pos, rule)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        a2, b2 = lisa.rotary(q, k, pos, rule)
+    a3, b3 = lisa.rotary(q, k, pos, rule, stream=side.cuda_stream)
+    side.synchronize()
+    assert all(torch.equal(a, x) for x in (a2, a3)) and all(torch.equal(b, x) for x in (b2, b3))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ag, bg = lisa.rotary(q, k, pos, rule)
+    q.copy_(rand((2, 3, 50, 64), BF16, 18))
+    pos.add_(5)
+    graph.replay()
+    torch.cuda.synchronize()
+    a4, b4 = lisa.rotary(q, k, pos, rule)
+    assert torch.equal(ag, a4) and torch.equal(bg, b4)
+
+
+def test_refusals(lisa):
+    rule = lisa.RotaryAxes(64, [16, 16])
+    q, pos = rand((2, 3, 5, 64), BF16, 19), torch.zeros(2, 2, 5, dtype=torch.int32, device="cuda")
+    lisa.rotary(q, None, pos, rule)
+    for args in ((q.half(), None, pos), (q.cpu(), None, pos), (q, q.float(), pos), (q, q[:, :, :4], pos),
+                 (q[..., :32], None, pos), (q, None, pos.long()), (q, None, pos[:1]), (q, None, pos[:, :, :4]),
+                 (q, None, pos.cpu()), (q[0], None, pos), (q, q[0], pos),
+                 (q.transpose(2, 3).contiguous().transpose(2, 3), None, pos)):
+        with pytest.raises(ValueError):
+            lisa.rotary(*args, rule)
+    with pytest.raises(lisa.LisaError):
+        lisa.rotary(q, q, pos, rule, out=(q, q))                       # both into one place
+    with pytest.raises(lisa.LisaError):
+        lisa.rotary(q[:, :, 1:], None, pos[:, :, 1:].contiguous(), rule, out=q[:, :, :4])   # beside itself
+    for bad in (dict(sections=[]), dict(sections=[33]), dict(sections=[0]), dict(sections=[-1, 8]),
+                dict(sections=[1] * 5), dict(sections=[8], pairing="quarters"), dict(sections=[8], base=0.0),
+                dict(sections=[2], frequencies=[1.0]), dict(sections=[2], frequencies=[1.0, math.inf]),
+                dict(sections=[1], frequencies=[2.0 ** 21])):
+        with pytest.raises(ValueError):
+            lisa.RotaryAxes(64, **bad)
