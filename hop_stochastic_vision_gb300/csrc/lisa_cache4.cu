@@ -1,0 +1,299 @@
+// lisa_cache4.cu -- the key/value cache in 4 bits: storing tokens and reading them
+// back, and the argument checks of its entry points.
+//
+// Four threads take the 32 elements of a group, eight each: 16 or 32 bytes of a
+// token in, one word of codes out.  Bound by the bytes of the tokens in their own
+// type (a group of bf16 is 64 bytes, held in 18).
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "lisa_args.h"
+#include "lisa_attn.h"
+#include "lisa_bias_dev.cuh"
+#include "lisa_cache4.cuh"
+#include "lisa_cache4_attn.h"
+#include "lisa_launch.cuh"
+
+namespace lisa {
+namespace cache4 {
+namespace {
+
+using namespace lisa::attn;
+
+constexpr int kThreads = 256;
+
+struct TokenParams {
+    Cache c;
+    Tensor K, V;                 // read: written
+    const int *positions, *sequences;
+    long long positions_stride;
+    long long threads;           // 4 G per token, key head and side
+    FastDiv div_n, div_rows;     // by n and by kv_heads
+    int n;
+};
+
+// Which eight elements a thread has: in order of side, quarter, group, head, token (heads side by side in a token) or
+// side, quarter, group, token, head (tokens side by side in a head).
+struct Place {
+    int b, i, head, q, group, value;
+};
+template <int D>
+__device__ __forceinline__ Place place_of(const TokenParams &x, long long at, bool heads_first) {
+    constexpr int G = D / kGroup;
+    Place p;
+    p.q = (int)(at & 3);
+    p.group = G == 2 ? (int)(at >> 2 & 1) : 0;
+    at >>= G == 2 ? 3 : 2;
+    p.value = (int)(at & 1);
+    int rest = (int)(at >> 1);   // (token, head) pairs: below 2^31
+    if (heads_first) {
+        int t = split(rest, x.div_rows);
+        p.head = rest;
+        p.b = split(t, x.div_n);
+        p.i = t;
+    } else {
+        int t = split(rest, x.div_n);
+        p.i = rest;
+        p.b = split(t, x.div_rows);
+        p.head = t;
+    }
+    return p;
+}
+
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(u[e] << 16);
+        v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        u[e] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) store_tokens(const __grid_constant__ TokenParams x, bool heads_first) {
+    chain_begin();
+    const long long at = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const bool in = at < x.threads;   // every lane stays for the exchange
+    const Place p = place_of<D>(x, in ? at : 0, heads_first);
+    const long long where = p.b * x.positions_stride + p.i;
+    const int position = in ? x.positions[where] : -1;
+    const int page = page_of(x.c, in && x.sequences ? x.sequences[where] : p.b, position);
+    float v[8] = {};
+    const Tensor &t = p.value ? x.V : x.K;
+    if (page >= 0)
+        load8(static_cast<const T *>(t.p) + (long long)p.b * t.sb + (long long)p.head * t.sh + (long long)p.i * t.st +
+                  p.group * kGroup + p.q * 8, v);
+    // the largest magnitude by its bits, which order like the numbers, infinity and then NaN above all
+    unsigned top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    if (page < 0) return;
+    const bool finite = top < 0x7F800000u;
+    const __nv_bfloat16 held = __float2bfloat16_rn(finite ? __fdiv_rn(__uint_as_float(top), 7.f) : __uint_as_float(0x7FFFFFFFu));
+    const float scale = __bfloat162float(held);
+    uint32_t word = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        // beyond 7 only where the scale is a subnormal bf16 number, coarser than its rounding elsewhere
+        const float code = finite && scale > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(v[e], scale)), -7.f), 7.f) : 0.f;
+        word |= (uint32_t)((int)code + 8) << (4 * e);
+    }
+    using B = Block<D>;
+    const int token = position % kPage;
+    uint8_t *block = x.c.store + ((long long)page * x.c.kv_heads + p.head) * B::kBytes;
+    if (p.value) {
+        *reinterpret_cast<uint16_t *>(block + B::off_v + B::value_half(token, 2 * p.q, p.group)) = (uint16_t)word;
+        *reinterpret_cast<uint16_t *>(block + B::off_v + B::value_half(token, 2 * p.q + 1, p.group)) = (uint16_t)(word >> 16);
+    } else {
+        *reinterpret_cast<uint32_t *>(block + B::key_word(token, p.q, p.group)) = word;
+    }
+    if (p.q == 0)
+        *reinterpret_cast<__nv_bfloat16 *>(block + (p.value ? B::off_vs : B::off_ks) + (token * B::G + p.group) * 2) = held;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) read_tokens(const __grid_constant__ TokenParams x, bool heads_first) {
+    chain_begin();
+    const long long at = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (at >= x.threads) return;
+    const Place p = place_of<D>(x, at, heads_first);
+    const long long where = p.b * x.positions_stride + p.i;
+    const int position = x.positions[where];
+    const int page = page_of(x.c, x.sequences ? x.sequences[where] : p.b, position);
+    float v[8] = {};
+    if (page >= 0) {
+        using B = Block<D>;
+        const int token = position % kPage;
+        const uint8_t *block = x.c.store + ((long long)page * x.c.kv_heads + p.head) * B::kBytes;
+        uint32_t word;
+        if (p.value) {
+            word = *reinterpret_cast<const uint16_t *>(block + B::off_v + B::value_half(token, 2 * p.q, p.group));
+            word |= (uint32_t)*reinterpret_cast<const uint16_t *>(block + B::off_v + B::value_half(token, 2 * p.q + 1, p.group)) << 16;
+        } else {
+            word = *reinterpret_cast<const uint32_t *>(block + B::key_word(token, p.q, p.group));
+        }
+        const float scale = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(
+            block + (p.value ? B::off_vs : B::off_ks) + (token * B::G + p.group) * 2));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (float)((int)(word >> (4 * e) & 15u) - 8) * scale;
+    }
+    const Tensor &t = p.value ? x.V : x.K;
+    store8(static_cast<T *>(const_cast<void *>(t.p)) + (long long)p.b * t.sb + (long long)p.head * t.sh +
+               (long long)p.i * t.st + p.group * kGroup + p.q * 8, v);
+}
+
+// The struct by itself.
+lisa_status check_cache(const lisa_cache4 *c) {
+    if (!c || c->pages < 0 || c->kv_heads < 0 || c->sequences < 0 || c->width < 0 || c->d < 1 || c->table_stride < 0)
+        return LISA_ERR_INVALID_ARG;
+    if (c->d != 32 && c->d != 64) return LISA_ERR_UNSUPPORTED;
+    if (c->pages >= 1 << 25 || c->width >= 1 << 25 || c->kv_heads > 65535 || c->table_stride > 1LL << 38)
+        return LISA_ERR_UNSUPPORTED;
+    if (c->pages > 0 && c->kv_heads > 0 && (!c->store || !aligned16(c->store))) return LISA_ERR_INVALID_ARG;
+    if (c->sequences > 0 && c->width > 0 && (!c->table || !aligned4(c->table))) return LISA_ERR_INVALID_ARG;
+    return LISA_OK;
+}
+Span store_span(const lisa_cache4 &c) { return Span(c.store, (size_t)c.pages * c.kv_heads * block_bytes(c.d)); }
+Span table_span(const lisa_cache4 &c) {
+    return Span(c.table, c.sequences > 0 && c.width > 0 ? ((size_t)c.table_stride * (c.sequences - 1) + c.width) * 4 : 0);
+}
+Cache cache_of(const lisa_cache4 &c) {
+    return Cache{static_cast<uint8_t *>(c.store), c.table, c.table_stride, c.pages, c.kv_heads, c.sequences, c.width};
+}
+
+template <bool kStore>
+lisa_status tokens(const lisa_cache4 *cache, const void *K, const lisa_strides *ks, const void *V, const lisa_strides *vs,
+                   const int *positions, const int *sequences, long long positions_stride, int B, int n, int dtype,
+                   cudaStream_t s) {
+    const lisa_status st = check_cache(cache);
+    if (st != LISA_OK) return st;
+    if (B < 0 || n < 0 || (dtype != LISA_F32 && dtype != LISA_BF16) || positions_stride < 0) return LISA_ERR_INVALID_ARG;
+    const int heads = cache->kv_heads, d = cache->d;
+    if (B == 0 || n == 0 || heads == 0) return LISA_OK;
+    if ((long long)B * n >= 1LL << 31 || (long long)B * n * heads >= 1LL << 31 || positions_stride > 1LL << 38)
+        return LISA_ERR_UNSUPPORTED;
+    const size_t esz = dtype == LISA_BF16 ? 2 : 4;
+    if (!K || !V || !aligned16(K) || !aligned16(V) || !good_strides(ks, B, heads, n, d, esz, !kStore) ||
+        !good_strides(vs, B, heads, n, d, esz, !kStore) || !positions || !aligned4(positions) || !aligned4(sequences))
+        return LISA_ERR_INVALID_ARG;
+    const Span k(K, extent(ks, B, heads, n, d, esz)), v(V, extent(vs, B, heads, n, d, esz));
+    const size_t listed = ((size_t)positions_stride * (B - 1) + n) * 4;
+    const Span lists[2] = {Span(positions, listed), Span(sequences, sequences ? listed : 0)};
+    const Span store = store_span(*cache), table = table_span(*cache);
+    const Span outs[2] = {kStore ? store : k, kStore ? Span() : v};
+    const Span ins[5] = {kStore ? k : store, kStore ? v : Span(), table, lists[0], lists[1]};
+    if (outs[0].meets(outs[1])) return LISA_ERR_INVALID_ARG;
+    for (const Span &o : outs)
+        for (const Span &i : ins)
+            if (o.meets(i)) return LISA_ERR_INVALID_ARG;
+    TokenParams x{};
+    x.c = cache_of(*cache);
+    x.K = {K, ks->batch, ks->head, ks->token};
+    x.V = {V, vs->batch, vs->head, vs->token};
+    x.positions = positions;
+    x.sequences = sequences;
+    x.positions_stride = positions_stride;
+    x.threads = (long long)B * n * heads * 2 * (d / 8);
+    x.div_n = fast_div(n);
+    x.div_rows = fast_div(heads);
+    x.n = n;
+    const bool heads_first = ks->head < ks->token;
+    const dim3 grid((unsigned)((x.threads + kThreads - 1) / kThreads));
+    cudaError_t e;
+    if (dtype == LISA_BF16)
+        e = d == 64 ? launch_chained(kStore ? store_tokens<64, __nv_bfloat16> : read_tokens<64, __nv_bfloat16>, grid, kThreads, 0, s, x, heads_first)
+                    : launch_chained(kStore ? store_tokens<32, __nv_bfloat16> : read_tokens<32, __nv_bfloat16>, grid, kThreads, 0, s, x, heads_first);
+    else
+        e = d == 64 ? launch_chained(kStore ? store_tokens<64, float> : read_tokens<64, float>, grid, kThreads, 0, s, x, heads_first)
+                    : launch_chained(kStore ? store_tokens<32, float> : read_tokens<32, float>, grid, kThreads, 0, s, x, heads_first);
+    return status_of(e);
+}
+
+}  // namespace
+}  // namespace cache4
+}  // namespace lisa
+
+using namespace lisa::cache4;
+
+extern "C" size_t lisa_cache4_bytes(int pages, int kv_heads, int d) {
+    if (pages < 0 || pages >= 1 << 25 || kv_heads < 0 || kv_heads > 65535 || (d != 32 && d != 64)) return 0;
+    return (size_t)pages * kv_heads * block_bytes(d);
+}
+
+extern "C" lisa_status lisa_cache4_store(const lisa_cache4 *cache, const void *K, const lisa_strides *k_strides,
+                                         const void *V, const lisa_strides *v_strides, const int *positions,
+                                         const int *sequences, long long positions_stride, int B, int n, int dtype,
+                                         void *stream) {
+    return tokens<true>(cache, K, k_strides, V, v_strides, positions, sequences, positions_stride, B, n, dtype,
+                        static_cast<cudaStream_t>(stream));
+}
+
+extern "C" lisa_status lisa_cache4_read(const lisa_cache4 *cache, void *K, const lisa_strides *k_strides, void *V,
+                                        const lisa_strides *v_strides, const int *positions, const int *sequences,
+                                        long long positions_stride, int B, int n, int dtype, void *stream) {
+    return tokens<false>(cache, K, k_strides, V, v_strides, positions, sequences, positions_stride, B, n, dtype,
+                         static_cast<cudaStream_t>(stream));
+}
+
+extern "C" lisa_status lisa_cache4_attention(const lisa_cache4 *cache, const void *Q, const lisa_strides *q_strides,
+                                             void *O, const lisa_strides *o_strides, float *lse, const int *lens, int B,
+                                             int heads, int n, float scale, int dtype, void *stream) {
+    using namespace lisa::attn;
+    const lisa_status st = check_cache(cache);
+    if (st != LISA_OK) return st;
+    const lisa_cache4 &c = *cache;
+    if (B < 0 || heads < 0 || n < 0 || (dtype != LISA_F32 && dtype != LISA_BF16)) return LISA_ERR_INVALID_ARG;
+    if (heads > 0 && (c.kv_heads < 1 || heads % c.kv_heads != 0)) return LISA_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return LISA_ERR_INVALID_ARG;
+    if (B > c.sequences) return LISA_ERR_INVALID_ARG;
+    if (dtype != LISA_BF16 || B > 65535 || heads > 65535) return LISA_ERR_UNSUPPORTED;
+    if (B == 0 || heads == 0 || n == 0) return LISA_OK;
+    const long long rows = (long long)n * (heads / c.kv_heads);
+    if (rows > 1024 || c.kv_heads * ((rows + 15) / 16) > 65535) return LISA_ERR_UNSUPPORTED;
+    if (!Q || !O || !aligned16(Q) || !aligned16(O) || !good_strides(q_strides, B, heads, n, c.d, 2, false) ||
+        !good_strides(o_strides, B, heads, n, c.d, 2, true) || !aligned4(lse) || !lens || !aligned4(lens))
+        return LISA_ERR_INVALID_ARG;
+    const Span outs[2] = {Span(O, extent(o_strides, B, heads, n, c.d, 2)), Span(lse, lse ? (size_t)B * heads * n * 4 : 0)};
+    const Span ins[4] = {Span(Q, extent(q_strides, B, heads, n, c.d, 2)), store_span(c), table_span(c), Span(lens, (size_t)B * 4)};
+    if (outs[0].meets(outs[1])) return LISA_ERR_INVALID_ARG;
+    for (const Span &o : outs)
+        for (const Span &i : ins)
+            if (o.meets(i)) return LISA_ERR_INVALID_ARG;
+    AttnProblem p{};
+    p.c = cache_of(c);
+    p.Q = {Q, q_strides->batch, q_strides->head, q_strides->token};
+    p.O = {O, o_strides->batch, o_strides->head, o_strides->token};
+    p.lse = lse;
+    p.lens = lens;
+    p.B = B;
+    p.heads = heads;
+    p.group = heads / c.kv_heads;
+    p.n = n;
+    p.scale = scale;
+    return status_of(launch_attention(p, c.d, static_cast<cudaStream_t>(stream)));
+}

@@ -355,7 +355,7 @@ EXPORTED = EXPORTED + ATTENTION_EXPORTED
 
 
 # -- rotary positions, packed prompts, the cache in 4 bits ------------------------------
-from .prompt import (PROMPT_EXPORTED, PackedSequences, RotaryAxes, prompt_attention,  # noqa: E402,F401
-                     prompt_attention_backward, rotary, rotary_backward)
+from .prompt import (PROMPT_EXPORTED, Cache4, PackedSequences, RotaryAxes, cache_attention,  # noqa: E402,F401
+                     cache_read, cache_store, prompt_attention, prompt_attention_backward, rotary, rotary_backward)
 
 EXPORTED = EXPORTED + PROMPT_EXPORTED

@@ -18,10 +18,12 @@ from .lisa import LISA_ERR_UNSUPPORTED, LISA_OK, LisaError, load
 
 LISA_MAX_PAIRS = 32
 LISA_MAX_AXES = 4
+LISA_CACHE4_PAGE = 64
 
 PROMPT_EXPORTED = ("lisa_rotary", "lisa_packed_plan_bytes", "lisa_packed_plan",
                    "lisa_prompt_attention_workspace_bytes", "lisa_prompt_attention",
-                   "lisa_prompt_attention_backward_workspace_bytes", "lisa_prompt_attention_backward")
+                   "lisa_prompt_attention_backward_workspace_bytes", "lisa_prompt_attention_backward",
+                   "lisa_cache4_bytes", "lisa_cache4_store", "lisa_cache4_read", "lisa_cache4_attention")
 
 
 class lisa_rotary_rule(ctypes.Structure):
@@ -34,6 +36,12 @@ class lisa_packed(ctypes.Structure):
                 ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
                 ("causal", ctypes.c_int), ("items", ctypes.c_int * 3), ("joins", ctypes.c_int * 3),
                 ("parts", ctypes.c_int * 3), ("seal", ctypes.c_uint)]
+
+
+class lisa_cache4(ctypes.Structure):
+    _fields_ = [("store", ctypes.c_void_p), ("pages", ctypes.c_int), ("kv_heads", ctypes.c_int), ("d", ctypes.c_int),
+                ("table", ctypes.c_void_p), ("sequences", ctypes.c_int), ("width", ctypes.c_int),
+                ("table_stride", ctypes.c_longlong)]
 
 
 _lib = None
@@ -62,6 +70,14 @@ def _library():
         lib.lisa_prompt_attention_backward.argtypes = [vp, sp, vp, sp, vp, sp, vp, sp, vp, ll, vp, sp, vp, sp, vp, sp,
                                                        vp, sp, pp, i, f, i, vp, sz, vp]
         lib.lisa_prompt_attention_backward.restype = i
+        cp = ctypes.POINTER(lisa_cache4)
+        lib.lisa_cache4_bytes.argtypes = [i, i, i]
+        lib.lisa_cache4_bytes.restype = sz
+        for call in (lib.lisa_cache4_store, lib.lisa_cache4_read):
+            call.argtypes = [cp, vp, sp, vp, sp, vp, vp, ll, i, i, i, vp]
+            call.restype = i
+        lib.lisa_cache4_attention.argtypes = [cp, vp, sp, vp, sp, vp, vp, i, i, i, f, i, vp]
+        lib.lisa_cache4_attention.restype = i
         _lib = lib
     return _lib
 
@@ -107,6 +123,25 @@ def lisa_prompt_attention_backward(Q, qs, K, ks, V, vs, O, os, lse, lse_stride, 
     return int(_library().lisa_prompt_attention_backward(
         Q, _ref(qs), K, _ref(ks), V, _ref(vs), O, _ref(os), lse, lse_stride, dO, _ref(dos), dQ, _ref(dqs), dK,
         _ref(dks), dV, _ref(dvs), _ref(packed), d, scale, dtype, workspace, workspace_bytes, stream))
+
+
+def lisa_cache4_bytes(pages, kv_heads, d) -> int:
+    return int(_library().lisa_cache4_bytes(pages, kv_heads, d))
+
+
+def lisa_cache4_store(cache, K, ks, V, vs, positions, sequences, positions_stride, B, n, dtype, stream) -> int:
+    return int(_library().lisa_cache4_store(_ref(cache), K, _ref(ks), V, _ref(vs), positions, sequences,
+                                            positions_stride, B, n, dtype, stream))
+
+
+def lisa_cache4_read(cache, K, ks, V, vs, positions, sequences, positions_stride, B, n, dtype, stream) -> int:
+    return int(_library().lisa_cache4_read(_ref(cache), K, _ref(ks), V, _ref(vs), positions, sequences,
+                                           positions_stride, B, n, dtype, stream))
+
+
+def lisa_cache4_attention(cache, Q, qs, O, os, lse, lens, B, heads, n, scale, dtype, stream) -> int:
+    return int(_library().lisa_cache4_attention(_ref(cache), Q, _ref(qs), O, _ref(os), lse, lens, B, heads, n, scale,
+                                                dtype, stream))
 
 
 # -- tensors of a call ------------------------------------------------------------------
@@ -350,3 +385,137 @@ def prompt_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     saved = (out.data_ptr(), _strides(out, "out", (3,), q.dtype, index), lse.data_ptr(), q.shape[1], dout.data_ptr(),
              _strides(dout, "dout", (3,), q.dtype, index))
     return _run(index, stream, _prompt_backward, q, k, head, saved, tail, seqs, workspace)
+
+
+# -- the cache in 4 bits -------------------------------------------------------------------
+
+class Cache4:
+    """Memory of a key/value cache in 4 bits: ``pages`` pages of 64 tokens of
+    ``kv_heads`` key heads of width ``d`` (32 or 64).  Which pages a sequence has
+    is the caller's table (int32 [sequences, width]: page of its tokens 0 .. 63,
+    64 .. 127 and so on), given to every call."""
+
+    def __init__(self, pages: int, kv_heads: int, d: int, *, device="cuda"):
+        self.pages, self.kv_heads, self.d = _int32(pages), _int32(kv_heads), _int32(d)
+        nbytes = lisa_cache4_bytes(self.pages, self.kv_heads, self.d)
+        if nbytes == 0 and not (self.pages == 0 or self.kv_heads == 0):
+            raise LisaError(LISA_ERR_UNSUPPORTED)
+        self.store = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        if not self.store.is_cuda:
+            raise ValueError("a cache lives on a CUDA device")
+        self.index = self.store.get_device()
+
+    def struct(self, table: torch.Tensor) -> lisa_cache4:
+        """The C struct of the cache with this table."""
+        if not (table.get_device() == self.index and table.dtype == torch.int32 and table.dim() == 2
+                and (table.shape[1] <= 1 or table.stride(1) == 1)):
+            raise ValueError("the table must be an int32 CUDA tensor [sequences, width] on the cache's device")
+        sequences, width = table.shape
+        if max(sequences, width) >> 31:
+            raise LisaError(LISA_ERR_UNSUPPORTED)
+        return lisa_cache4(self.store.data_ptr(), self.pages, self.kv_heads, self.d, table.data_ptr(), sequences, width,
+                           table.stride(0) if sequences > 1 else 0)
+
+
+def _places(cache, positions, sequences):
+    """(B, n, address, address, stride) of tokens given by positions [B, n], or [tokens] with their sequences."""
+    for t in (positions, sequences):
+        if t is not None and not (t.get_device() == cache.index and t.dtype == torch.int32):
+            raise ValueError("positions and sequences must be int32 CUDA tensors on the cache's device")
+    packed = positions.dim() == 1
+    if positions.dim() not in (1, 2) or packed != (sequences is not None):
+        raise ValueError("positions must be [B, n], or [tokens] with the tokens' sequences")
+    if sequences is not None and (sequences.shape != positions.shape or sequences.stride() != positions.stride()):
+        raise ValueError("sequences must be laid out like the positions")
+    n = positions.shape[-1]
+    if n > 1 and positions.stride(-1) != 1:
+        raise ValueError("the positions of an entry must be contiguous")
+    B = 1 if packed else positions.shape[0]
+    return (B, n, positions.data_ptr(), None if sequences is None else sequences.data_ptr(),
+            positions.stride(0) if B > 1 and not packed else 0)
+
+
+def _cache_call(stream, call, struct, k, v, ks, vs, places):
+    B, n, at, sequences, stride = places
+    status = call(struct, k.data_ptr(), ks, v.data_ptr(), vs, at, sequences, stride, B, n, _DTYPES[k.dtype], stream)
+    if status != LISA_OK:
+        raise LisaError(status)
+
+
+def _cache_tensors(cache, k, v, positions):
+    dims = (positions.dim() + 2,)
+    ks, vs = (_strides(t, name, dims, k.dtype, cache.index) for t, name in ((k, "k"), (v, "v")))
+    shape = (cache.kv_heads, positions.shape[-1], cache.d)
+    shape = shape if positions.dim() == 1 else (positions.shape[0],) + shape
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("k and v must be %s for these positions" % (list(shape),))
+    return ks, vs
+
+
+def cache_store(cache: Cache4, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, positions: torch.Tensor,
+                sequences: torch.Tensor = None, *, stream=None) -> None:
+    """k and v [B, kv_heads, n, d] (fp32 or bf16, strided views are fine) into the
+    cache, entry b at ``positions`` [B, n] (int32) of sequence b of the table; packed
+    tokens [kv_heads, tokens, d] at positions [tokens] of ``sequences`` [tokens].  A
+    position below 0 or beyond the table, or without a page, stores nothing; those
+    that a sequence gets in one call have to differ."""
+    places = _places(cache, positions, sequences)
+    ks, vs = _cache_tensors(cache, k, v, positions)
+    _run(cache.index, stream, _cache_call, _library().lisa_cache4_store, cache.struct(table), k, v, ks, vs, places)
+
+
+def _cache_read(stream, cache, struct, shape, dtype, out, positions, places):
+    if out is None:
+        device = cache.store.device
+        out = tuple(torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+    ks, vs = _cache_tensors(cache, *out, positions)
+    _cache_call(stream, _library().lisa_cache4_read, struct, *out, ks, vs, places)
+    return out
+
+
+def cache_read(cache: Cache4, table: torch.Tensor, positions: torch.Tensor, sequences: torch.Tensor = None, *,
+               dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """What the cache stands for at these positions (given as for ``cache_store``):
+    (k, v) [B, kv_heads, n, d], or [kv_heads, tokens, d]; zeros where there is no
+    token."""
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32 or bfloat16")
+    places = _places(cache, positions, sequences)
+    shape = (cache.kv_heads, positions.shape[-1], cache.d)
+    shape = shape if positions.dim() == 1 else (positions.shape[0],) + shape
+    return _run(cache.index, stream, _cache_read, cache, cache.struct(table), shape, dtype, out, positions, places)
+
+
+def _cache_attention(stream, q, qs, cache, struct, lens, scale, return_lse, out):
+    B, heads, n, _ = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    os = _strides(out, "out", (4,), q.dtype, cache.index)
+    lse = torch.empty((B, heads, n), dtype=torch.float32, device=q.device) if return_lse else None
+    status = _library().lisa_cache4_attention(struct, q.data_ptr(), qs, out.data_ptr(), os,
+                                              lse.data_ptr() if return_lse else None, lens.data_ptr(), B, heads, n,
+                                              scale, _DTYPES[q.dtype], stream)
+    if status != LISA_OK:
+        raise LisaError(status)
+    return (out, lse) if return_lse else out
+
+
+def cache_attention(q: torch.Tensor, cache: Cache4, table: torch.Tensor, lens: torch.Tensor, *, scale=None,
+                    return_lse: bool = False, out=None, stream=None):
+    """Attention of the newest n tokens of each sequence, q [B, heads, n, d] (bf16),
+    over the cache, which holds them too: entry b reads sequence b of the table,
+    ``lens`` [B] tokens (int32), and query i the tokens up to its own, lens - n + i.
+    ``scale`` defaults to 1 / sqrt(d).  Returns O like q, with ``return_lse`` also
+    the fp32 log-sum-exp [B, heads, n]."""
+    qs = _strides(q, "q", (4,), torch.bfloat16, cache.index)
+    B, heads, n, d = q.shape
+    if d != cache.d:
+        raise ValueError("the cache is of width %d, q of %d" % (cache.d, d))
+    struct = cache.struct(table)
+    if table.shape[0] != B or not (lens.get_device() == cache.index and lens.dtype == torch.int32
+                                   and lens.is_contiguous() and lens.shape == (B,)):
+        raise ValueError("lens must be a contiguous int32 CUDA tensor [B], and the table have B rows")
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    return _run(cache.index, stream, _cache_attention, q, qs, cache, struct, lens,
+                _default_scale(d) if scale is None else float(scale), return_lse, out)

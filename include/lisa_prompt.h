@@ -120,6 +120,67 @@ lisa_status lisa_prompt_attention_backward(
     const lisa_strides *dk_strides, void *dV, const lisa_strides *dv_strides, const lisa_packed *packed, int d,
     float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * A key/value cache in 4 bits.  The d elements of a token's key (or value) of one
+ * key head are held in groups of 32:
+ *
+ *   scale = bf16(max |x| / 7)      code = x / scale to the nearest whole number
+ *                                  of -7 .. 7, ties to even
+ *
+ * (both quotients rounded to fp32 first), and stand for code * scale.  A group of
+ * zeros, or of numbers so small that the scale is 0, stands for zeros; one with a
+ * NaN or an infinity stands for NaN.  4.5 bits an element.
+ *
+ * Tokens stand in pages of LISA_CACHE4_PAGE.  Token p of sequence s is token
+ * p % LISA_CACHE4_PAGE of page table[s table_stride + p / LISA_CACHE4_PAGE].  A
+ * token whose sequence, position or page is outside its range does not exist:
+ * nothing is stored for it, it reads as zeros, and no query sees it.  Sequences
+ * may share pages that they only read.  The memory needs no initialisation; what
+ * stands in a page is this library's own (a page of one key head is one block of
+ * lisa_cache4_bytes(1, 1, d)).
+ */
+#define LISA_CACHE4_PAGE 64
+
+typedef struct lisa_cache4 {
+    void *store;               /* device, 16-byte aligned, lisa_cache4_bytes(pages, kv_heads, d) */
+    int pages, kv_heads, d;    /* d: 32 or 64; pages * LISA_CACHE4_PAGE below 2^31 */
+    const int *table;          /* device [sequences][table_stride], `width` entries of each row */
+    int sequences, width;      /* width * LISA_CACHE4_PAGE below 2^31 */
+    long long table_stride;
+} lisa_cache4;
+
+/* 0 for sizes that the calls would reject. */
+size_t lisa_cache4_bytes(int pages, int kv_heads, int d);
+
+/*
+ * K, V [B][kv_heads][n][d] into the cache (store), or what it stands for out of
+ * it (read: written in `dtype`, exact in both types but for bf16 products rounded
+ * once).  Token i of entry b has the position positions[b positions_stride + i] of
+ * sequence b, or with `sequences` (device int32, laid out like the positions) of
+ * the sequence given there.  The positions that one store gives to one sequence
+ * have to differ: of two tokens in one place either's bytes may stay, mixed.
+ */
+lisa_status lisa_cache4_store(const lisa_cache4 *cache, const void *K, const lisa_strides *k_strides, const void *V,
+                              const lisa_strides *v_strides, const int *positions, const int *sequences,
+                              long long positions_stride, int B, int n, int dtype, void *stream);
+lisa_status lisa_cache4_read(const lisa_cache4 *cache, void *K, const lisa_strides *k_strides, void *V,
+                             const lisa_strides *v_strides, const int *positions, const int *sequences,
+                             long long positions_stride, int B, int n, int dtype, void *stream);
+
+/*
+ * Attention of the newest n tokens of each sequence over the cache that holds
+ * them too: Q [B][heads][n][d] (LISA_BF16), entry b on sequence b of lens[b]
+ * tokens (device int32 [B], taken to 0 .. width * LISA_CACHE4_PAGE).  Query i
+ * stands at lens[b] - n + i and sees the tokens up to there; one that stands
+ * before the first sees none: o = 0, lse = -inf.  O and lse (fp32 [B][heads][n],
+ * may be NULL) are written.  scale is finite and > 0.  Made for few queries: every
+ * 16 rows (queries times the heads that share a key head) read the cache anew;
+ * n heads / kv_heads is at most 1024.
+ */
+lisa_status lisa_cache4_attention(const lisa_cache4 *cache, const void *Q, const lisa_strides *q_strides, void *O,
+                                  const lisa_strides *o_strides, float *lse, const int *lens, int B, int heads, int n,
+                                  float scale, int dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,361 @@
+"""The key/value cache in 4 bits on the GPU: what is stored stands for the exact
+values of the definition, bit by bit; attention over it against the 64-bit
+restatement and its elementwise bounds (attention_ref.py).
+
+The keys' codes enter the products with an offset of 136, which the
+accumulator's first value takes out: the products' terms are up to 144 / 7 times
+the values' own, so a score's bound is the plain one of keys of 144 steps each.
+The weights are rounded to bf16 times their value's scale, one rounding as before.
+"""
+import math
+
+import pytest
+import torch
+
+import attention_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+PAGE = 64
+
+
+@pytest.fixture(scope="module")
+def lisa():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from hop_stochastic_vision_gb300 import build, lisa as binding
+    build.build()
+    binding.load()
+    return binding
+
+
+def stands_for(x):
+    """What the cache makes of x, from the definition: (values, scales), 64 bits."""
+    x = x.double().cpu().unflatten(-1, (-1, 32))
+    scale = (x.abs().amax(-1, keepdim=True) / 7).float().to(BF16).double()
+    code = torch.round((x / torch.where(scale == 0, 1.0, scale)).float()).double().clamp(-7, 7)
+    code = torch.where(scale == 0, 0.0, code)
+    bad = ~torch.isfinite(x).all(-1, keepdim=True)
+    return torch.where(bad, math.nan, code * scale).flatten(-2), torch.where(bad, math.nan, scale).expand_as(x).flatten(-2)
+
+
+def pages_of(lens, spare=2, seed=0, width=None):
+    """(table, pages): every sequence's pages anywhere in the pool, -1 behind them."""
+    need = [-(-x // PAGE) for x in lens]
+    width = max(need + [1]) if width is None else width
+    order = torch.randperm(sum(need) + spare, generator=torch.Generator().manual_seed(seed)).tolist()
+    table = torch.full((len(lens), width), -1, dtype=torch.int32)
+    for b, n in enumerate(need):
+        table[b, :n] = torch.tensor([order.pop() for _ in range(n)], dtype=torch.int32)
+    return table, sum(need) + spare
+
+
+def filled(lisa, k, v, lens, **kw):
+    """A cache that holds tokens 0 .. lens[b] - 1 of k, v [B, kv, m, d]."""
+    table, pages = pages_of(lens, **kw)
+    cache = lisa.Cache4(pages, k.shape[1], k.shape[3])
+    cache.store.fill_(0xFF)             # scales of NaN wherever nothing is stored
+    at = torch.arange(k.shape[2], dtype=torch.int32).repeat(k.shape[0], 1)
+    at = torch.where(at < torch.tensor(lens)[:, None], at, -1).to(torch.int32)
+    lisa.cache_store(cache, k.cuda(), v.cuda(), table.cuda(), at.cuda())
+    return cache, table.cuda()
+
+
+def rand(*shape, dtype=BF16, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("B,kv,n", [(1, 1, 1), (2, 3, 63), (3, 1, 64), (1, 4, 200), (5, 2, 7)])
+@pytest.mark.parametrize("layout", ["heads", "tokens"])
+def test_stored_and_read_back(lisa, dtype, d, B, kv, n, layout):
+    k, v = rand(B, kv, n, d, dtype=dtype, seed=n), 3 * rand(B, kv, n, d, dtype=dtype, seed=n + 1)
+    kc, vc = ((x.cuda().transpose(1, 2).contiguous().transpose(1, 2) if layout == "tokens" else x.cuda()) for x in (k, v))
+    table, pages = pages_of([n + 5] * B)
+    cache = lisa.Cache4(pages, kv, d)
+    at = (torch.arange(n, dtype=torch.int32) + 5).repeat(B, 1).cuda()
+    lisa.cache_store(cache, kc, vc, table.cuda(), at)
+    for out in (F32, BF16):
+        got = lisa.cache_read(cache, table.cuda(), at, dtype=out)
+        for x, y in zip((k, v), got):
+            assert torch.equal(stands_for(x)[0].to(out), y.cpu())
+
+
+def test_values_at_the_borders(lisa):
+    """Ties go to the even code; zeros, the smallest and the largest numbers, NaN and infinities."""
+    x = torch.zeros(1, 1, 12, 32)
+    x[0, 0, 0, :15] = torch.arange(-7, 8).float() * 0.5          # scale 1 (times 7 there): halves are ties
+    x[0, 0, 0, 20] = 7.0
+    x[0, 0, 1, 3] = 2.0 ** -149
+    x[0, 0, 2] = 2.0 ** -130
+    x[0, 0, 3, :2] = torch.tensor([3.4e38, -3.4e38])
+    x[0, 0, 4, 9] = math.nan
+    x[0, 0, 5, 9] = -math.inf
+    x[0, 0, 6, 9], x[0, 0, 6, 10] = math.inf, math.nan
+    x[0, 0, 7] = -1.0
+    x[0, 0, 8, 31] = 1e-30
+    x[0, 0, 9] = torch.linspace(-1, 1, 32)
+    x[0, 0, 10, :3] = torch.tensor([7.0, 6.5, -6.5]) * 2.0 ** -126
+    x[0, 0, 11, 0] = 7 * 2.0 ** -133
+    table, pages = pages_of([12])
+    for dtype in (F32, BF16):
+        y = x.to(dtype)
+        cache = lisa.Cache4(pages, 1, 32)
+        at = torch.arange(12, dtype=torch.int32, device="cuda")[None]
+        lisa.cache_store(cache, y.cuda(), y.cuda(), table.cuda(), at)
+        for got in lisa.cache_read(cache, table.cuda(), at, dtype=F32):
+            want = stands_for(y)[0].float()
+            assert torch.equal(torch.isnan(want), torch.isnan(got.cpu()))
+            assert torch.equal(want.nan_to_num(5.0), got.cpu().nan_to_num(5.0))
+
+
+def test_one_token_at_a_time_and_packed_ones(lisa):
+    """Tokens stored alone, in any order, or packed with their sequences: the same cache as all at once."""
+    B, kv, n, d = 3, 2, 130, 64
+    k, v = rand(B, kv, n, d, seed=1), rand(B, kv, n, d, seed=2)
+    whole, table = filled(lisa, k, v, [n] * B)
+    one, packed = lisa.Cache4(whole.pages, kv, d), lisa.Cache4(whole.pages, kv, d)
+    one.store.fill_(0xFF)
+    packed.store.fill_(0xFF)
+    for i in torch.randperm(n, generator=torch.Generator().manual_seed(3)).tolist():
+        lisa.cache_store(one, k[:, :, i:i + 1].cuda(), v[:, :, i:i + 1].cuda(), table,
+                         torch.full((B, 1), i, dtype=torch.int32, device="cuda"))
+    order = torch.randperm(B * n, generator=torch.Generator().manual_seed(4))
+    kk, vv = (x.transpose(0, 1).reshape(kv, B * n, d)[:, order].cuda() for x in (k, v))
+    pos, seq = (order % n).int().cuda(), (order // n).int().cuda()
+    lisa.cache_store(packed, kk, vv, table, pos, seq)
+    assert torch.equal(one.store, whole.store) and torch.equal(packed.store, whole.store)
+    a, b = lisa.cache_read(whole, table, pos, seq)
+    assert torch.equal(a.cpu(), stands_for(kk)[0].to(BF16)) and torch.equal(b.cpu(), stands_for(vv)[0].to(BF16))
+
+
+def test_tokens_and_pages_that_do_not_exist(lisa):
+    """Positions below 0 and beyond the table, pages and sequences outside their range: nothing stored, zeros read, and
+    nobody sees them."""
+    kv, d, n = 2, 64, 6
+    k, v = rand(2, kv, n, d, seed=5), rand(2, kv, n, d, seed=6)
+    table = torch.tensor([[1, 7, -1], [3, 1 << 30, 2]], dtype=torch.int32, device="cuda")     # of 4 pages
+    cache = lisa.Cache4(4, kv, d)
+    before = cache.store.clone()
+    pos = torch.tensor([[-1, 70, 130, 192, 2 ** 31 - 1, -2 ** 31], [64, 127, 200, -5, 3 * 64, 100]], dtype=torch.int32, device="cuda")
+    lisa.cache_store(cache, k.cuda(), v.cuda(), table, pos)
+    assert torch.equal(cache.store, before)
+    for x in lisa.cache_read(cache, table, pos):
+        assert not x.any()
+    kk, vv = k[0].cuda(), v[0].cuda()
+    for seq in (-1, 2, 2 ** 31 - 1):
+        lisa.cache_store(cache, kk, vv, table, torch.arange(6, dtype=torch.int32, device="cuda"),
+                         torch.full((6,), seq, dtype=torch.int32, device="cuda"))
+    assert torch.equal(cache.store, before)
+    # sequence 1: tokens 0 .. 63 and 128 .. 149 exist, the page between them does not
+    K, V = rand(1, kv, 150, d, seed=7), rand(1, kv, 150, d, seed=8)
+    at = torch.arange(150, dtype=torch.int32, device="cuda")[None]
+    lisa.cache_store(cache, K.cuda(), V.cuda(), table[1:], at)
+    q = rand(1, 4, 1, d, seed=9)
+    out, lse = lisa.cache_attention(q.cuda(), cache, table[1:], torch.tensor([150], dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    seen = torch.tensor([j for j in range(150) if not 64 <= j < 128])
+    Check(K[:, :, seen], V[:, :, seen], q, [len(seen)]).against(out, lse)
+
+
+class Check:
+    """Values and bounds of attention over what the cache stands for."""
+
+    def __init__(self, k, v, q, lens, scale=None):
+        (self.k, ks), (self.v, _) = stands_for(k), stands_for(v)
+        self.steps = 144 * ks.abs()
+        self.q, self.lens, self.scale = q.double(), lens, 1 / math.sqrt(q.shape[-1]) if scale is None else scale
+
+    def against(self, out, lse=None):
+        B, h, n, d = self.q.shape
+        u, r = ref.U[BF16], ref.R[BF16]
+        g = h // self.k.shape[1]
+        out = out.double().cpu()
+        for b in range(B):
+            for i in range(n):
+                L = self.lens[b] - (n - 1 - i)
+                for j in range(h):
+                    if L <= 0:
+                        assert not out[b, j, i].any()
+                        assert lse is None or float(lse[b, j, i]) == -math.inf
+                        continue
+                    k, v, q = self.k[b, j // g, :L], self.v[b, j // g, :L], self.q[b, j, i]
+                    s = self.scale * (k @ q)
+                    top = torch.logsumexp(s, 0)
+                    p = torch.exp(s - top)
+                    Es = u * (d + 8) * self.scale * (self.steps[b, j // g, :L] @ q.abs())
+                    Ep = p * (Es + Es.max() + u * (L + 8) + 8 * ref.EX2 + 8 * u * (s - top).abs()) + ref.F
+                    o = p @ v
+                    Eo = 1.05 * ((Ep + (r + L * u) * p) @ v.abs() + r * o.abs()) + 2.0 ** -126
+                    off = (out[b, j, i] - o).abs() / Eo
+                    assert float(off.max()) <= 1.0, (b, i, j, float(off.max()))
+                    if lse is not None:
+                        El = 1.05 * (Es.max() + u * (L + 8) + 8 * ref.EX2 + 8 * 2.0 ** -24 * top.abs())
+                        assert abs(float(lse[b, j, i]) - float(top)) <= float(El)
+
+
+@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("heads,kv", [(1, 1), (3, 3), (12, 4), (8, 1), (9, 1), (16, 1), (24, 1)])
+@pytest.mark.parametrize("lens", [[1], [63, 64, 65], [0, 200, 130, 1, 64], [700]])
+def test_single_tokens(lisa, d, heads, kv, lens):
+    B, m = len(lens), max(max(lens), 1)
+    k, v, q = rand(B, kv, m, d, seed=heads), rand(B, kv, m, d, seed=heads + 1), rand(B, heads, 1, d, seed=m)
+    cache, table = filled(lisa, k, v, lens)
+    out, lse = lisa.cache_attention(q.cuda(), cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    Check(k, v, q, lens).against(out, lse)
+
+
+@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("n,heads,kv", [(2, 4, 2), (3, 3, 3), (5, 4, 1), (8, 2, 2), (17, 4, 2), (40, 2, 1)])
+def test_the_newest_tokens_see_up_to_themselves(lisa, n, heads, kv, d):
+    lens = [300, n, 3, 64, 0, 129]
+    B, m = len(lens), 300
+    k, v, q = rand(B, kv, m, d, seed=n), rand(B, kv, m, d, seed=n + 1), rand(B, heads, n, d, seed=n + 2)
+    cache, table = filled(lisa, k, v, lens)
+    out, lse = lisa.cache_attention(q.cuda(), cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    Check(k, v, q, lens).against(out, lse)
+
+
+@pytest.mark.parametrize("B,heads,kv,m", [(1, 2, 1, 9000), (2, 4, 4, 5000), (40, 4, 2, 1000)])
+def test_long_caches(lisa, B, heads, kv, m):
+    """Pages shared out over a cluster, more of them for a warp than it looks up at once."""
+    lens = [m - 37 * b % m for b in range(B)]
+    k, v, q = rand(B, kv, m, 64, seed=1), rand(B, kv, m, 64, seed=2), rand(B, heads, 1, 64, seed=3)
+    cache, table = filled(lisa, k, v, lens, width=-(-m // PAGE) + 9)
+    out, lse = lisa.cache_attention(q.cuda(), cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    some = [0, B - 1]
+    Check(k[some], v[some], q[some], [lens[b] for b in some]).against(out[some], lse[some])
+
+
+def test_large_scores_and_scale(lisa):
+    k, v, q = 6 * rand(2, 1, 500, 64, seed=1), rand(2, 1, 500, 64, seed=2), 6 * rand(2, 3, 1, 64, seed=3)
+    cache, table = filled(lisa, k, v, [500, 77])
+    lens = torch.tensor([500, 77], dtype=torch.int32, device="cuda")
+    out, lse = lisa.cache_attention(q.cuda(), cache, table, lens, scale=1.0, return_lse=True)
+    Check(k, v, q, [500, 77], scale=1.0).against(out, lse)
+
+
+def test_lengths_outside_the_range_count_as_its_ends(lisa):
+    k, v, q = rand(3, 1, 128, 64, seed=1), rand(3, 1, 128, 64, seed=2), rand(3, 2, 1, 64, seed=3)
+    cache, table = filled(lisa, k, v, [128] * 3)
+    out = lisa.cache_attention(q.cuda(), cache, table, torch.tensor([-4, 128, 10 ** 9], dtype=torch.int32, device="cuda"))
+    Check(k, v, q, [0, 128, 128]).against(out)
+
+
+def test_not_a_number_in_tokens_that_a_row_does_not_see(lisa):
+    """The newest token holds NaN: earlier rows stay clean, its own row is NaN; behind the length nothing counts."""
+    k, v, q = rand(1, 1, 70, 64, seed=1), rand(1, 1, 70, 64, seed=2), rand(1, 2, 3, 64, seed=3)
+    clean, table = filled(lisa, k, v, [70])
+    lens = torch.tensor([69], dtype=torch.int32, device="cuda")
+    want = lisa.cache_attention(q.cuda(), clean, table, lens)
+    k[0, 0, 68], v[0, 0, 68] = math.nan, math.inf
+    k[0, 0, 69], v[0, 0, 69] = math.inf, math.nan
+    cache, table = filled(lisa, k, v, [70])
+    got = lisa.cache_attention(q.cuda(), cache, table, lens)
+    assert torch.equal(got[:, :, :2], want[:, :, :2]) and torch.isnan(got[:, :, 2]).all()
+
+
+def test_layouts_and_given_outputs(lisa):
+    k, v, q = rand(2, 2, 90, 32, seed=1), rand(2, 2, 90, 32, seed=2), rand(2, 4, 3, 32, seed=3)
+    cache, table = filled(lisa, k, v, [90, 50])
+    lens = torch.tensor([90, 50], dtype=torch.int32, device="cuda")
+    wide = torch.full((2, 3, 6, 32), 7.0, dtype=BF16, device="cuda")
+    view = wide[:, :, 1:5].transpose(1, 2)
+    qt = q.cuda().transpose(1, 2).contiguous().transpose(1, 2)
+    assert lisa.cache_attention(qt, cache, table, lens, out=view) is view
+    assert torch.equal(view, lisa.cache_attention(q.cuda(), cache, table, lens))
+    assert (wide[:, :, 0] == 7).all() and (wide[:, :, 5] == 7).all()
+    # a table with rows further apart than its width, and pages shared by two sequences
+    broad = torch.full((2, 8), 999, dtype=torch.int32, device="cuda")
+    broad[:, :2] = table
+    assert torch.equal(view, lisa.cache_attention(q.cuda(), cache, broad[:, :2], lens))
+    both = lisa.cache_attention(q[:1].cuda().expand(2, -1, -1, -1), cache, table[:1].expand(2, -1).contiguous(),
+                                lens[:1].expand(2).contiguous())
+    assert torch.equal(both[0], both[1]) and torch.equal(both[0], view[0])
+
+
+def test_empty_calls(lisa):
+    cache = lisa.Cache4(0, 2, 64)
+    table = torch.zeros(0, 0, dtype=torch.int32, device="cuda")
+    x = torch.empty(0, 2, 0, 64, dtype=BF16, device="cuda")
+    lisa.cache_store(cache, x, x, table, torch.empty(0, 0, dtype=torch.int32, device="cuda"))
+    assert lisa.cache_attention(x, cache, table, torch.empty(0, dtype=torch.int32, device="cuda")).shape == x.shape
+    q = rand(2, 2, 1, 64).cuda()
+    table = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    out, lse = lisa.cache_attention(q, cache, table, torch.tensor([0, 5], dtype=torch.int32, device="cuda"), return_lse=True)
+    assert not out.any() and (lse == -math.inf).all()
+
+
+def test_streams_and_graphs(lisa):
+    """A captured step: the new token into the cache, then attention over it; the length grows between replays."""
+    B, kv, m, d = 3, 2, 200, 64
+    k, v = rand(B, kv, m, d, seed=1), rand(B, kv, m, d, seed=2)
+    cache, table = filled(lisa, k, v, [m] * B)
+    other, _ = filled(lisa, k, v, [m] * B)
+    other.store.copy_(cache.store)
+    q = rand(B, 4, 1, d, seed=3).cuda()
+    kn, vn = k[:, :, :1].cuda().contiguous(), v[:, :, :1].cuda().contiguous()
+    lens = torch.full((B,), 100, dtype=torch.int32, device="cuda")
+    pos = torch.full((B, 1), 99, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def step(c, **kw):
+        lisa.cache_store(c, kn, vn, table, pos, **kw)
+        return lisa.cache_attention(q, c, table, lens, **kw)
+
+    want = step(other)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        a = step(cache)
+    b = step(cache, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(cache)
+    for i in range(100, 104):
+        lens.fill_(i + 1)
+        pos.fill_(i)
+        kn.copy_(rand(B, kv, 1, d, seed=i))
+        vn.copy_(rand(B, kv, 1, d, seed=i + 50))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(captured, step(other)) and torch.equal(cache.store, other.store)
+
+
+def test_refusals(lisa):
+    k = rand(2, 2, 9, 64).cuda()
+    cache, table = filled(lisa, k.cpu(), k.cpu(), [9, 9])
+    pos = torch.arange(9, dtype=torch.int32, device="cuda").repeat(2, 1)
+    lens = torch.tensor([9, 9], dtype=torch.int32, device="cuda")
+    for args in ((k.half(), k, table, pos), (k, k.float(), table, pos), (k.cpu(), k, table, pos), (k[:, :1], k[:, :1], table, pos),
+                 (k[..., :32], k[..., :32], table, pos), (k, k, table.long(), pos), (k, k, table[0], pos), (k, k, table.cpu(), pos),
+                 (k, k, table, pos.long()), (k, k, table, pos[:, :8]), (k, k, table, pos[0]), (k, k, table, pos, pos),
+                 (k[0], k[0], table, pos[0]), (k[0], k[0], table, pos[0], pos[0, :8])):
+        with pytest.raises(ValueError):
+            lisa.cache_store(cache, *args)
+    with pytest.raises(ValueError):
+        lisa.cache_read(cache, table, pos, dtype=torch.float16)
+    with pytest.raises(lisa.LisaError):
+        lisa.cache_read(cache, table, pos, out=(k, k))
+    q = rand(2, 4, 1, 64).cuda()
+    for args in ((q.float(), cache, table, lens), (q[:1], cache, table, lens), (q, cache, table[:1], lens),
+                 (q, cache, table, lens.long()), (q, cache, table, lens[:1]), (q[0], cache, table, lens),
+                 (q[..., :32], cache, table, lens)):
+        with pytest.raises(ValueError):
+            lisa.cache_attention(*args)
+    with pytest.raises(lisa.LisaError):
+        lisa.cache_attention(q[:, :3], cache, table, lens)             # 3 heads on 2
+    with pytest.raises(lisa.LisaError):
+        lisa.cache_attention(q, cache, table, lens, out=q)
+    with pytest.raises(lisa.LisaError):
+        lisa.cache_attention(q, cache, table, lens, scale=-1.0)
+    for bad in ((4, 2, 16), (4, 2, 128), (-1, 2, 64), (1 << 25, 1, 32)):
+        with pytest.raises(lisa.LisaError):
+            lisa.Cache4(*bad)

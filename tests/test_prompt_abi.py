@@ -257,3 +257,82 @@ def test_workspace_bytes():
     assert ws(p, 64, lisa.LISA_F32) == 0 and back(p, 64, lisa.LISA_F32) >= 4 * 305 * 4
     assert ws(p, 64, lisa.LISA_BF16) > 0 and ws(p, 48, lisa.LISA_BF16) == 0 and back(p, 48, lisa.LISA_BF16) == 0
     assert ws(_packed((4000,), 1, 1), 64, lisa.LISA_BF16) > 256 * 64 * 4
+
+
+# ----------------------------------------------------------- the cache in 4 bits
+
+def _cache(**over):
+    a = dict(store=FAKE, pages=8, kv_heads=2, d=64, table=FAKE + 64 * MB, sequences=2, width=4, table_stride=4)
+    a.update(over)
+    return prompt.lisa_cache4(a["store"], a["pages"], a["kv_heads"], a["d"], a["table"], a["sequences"], a["width"],
+                              a["table_stride"])
+
+
+def _tokens(call, **over):
+    a = dict(cache=_cache(), K=FAKE + MB, V=FAKE + 2 * MB, positions=FAKE + 3 * MB, sequences=None, stride=8, B=2, n=8,
+             dtype=lisa.LISA_BF16)
+    a.update(over)
+    ks = a.get("ks", _strides(2, 8, 64))
+    return call(a["cache"], a["K"], ks, a["V"], a.get("vs", ks), a["positions"], a["sequences"], a["stride"], a["B"],
+                a["n"], a["dtype"], 0)
+
+
+BAD_CACHE = [
+    (dict(cache=None), INV), (dict(cache=_cache(store=0)), INV), (dict(cache=_cache(store=FAKE + 8)), INV),
+    (dict(cache=_cache(table=0)), INV), (dict(cache=_cache(table=FAKE + 2)), INV), (dict(cache=_cache(pages=-1)), INV),
+    (dict(cache=_cache(width=-1)), INV), (dict(cache=_cache(sequences=-1)), INV), (dict(cache=_cache(table_stride=-4)), INV),
+    (dict(cache=_cache(d=0)), INV), (dict(cache=_cache(d=16)), UNS), (dict(cache=_cache(d=128)), UNS),
+    (dict(cache=_cache(pages=1 << 25)), UNS), (dict(cache=_cache(width=1 << 25)), UNS),
+    (dict(B=-1), INV), (dict(n=-1), INV), (dict(dtype=2), INV),
+]
+
+
+@pytest.mark.parametrize("over,status", BAD_CACHE + [
+    (dict(K=0), INV), (dict(V=0), INV), (dict(K=FAKE + MB + 8), INV), (dict(positions=0), INV),
+    (dict(positions=FAKE + 3 * MB + 2), INV), (dict(sequences=FAKE + 2), INV), (dict(ks=None), INV),
+    (dict(ks=_strides(2, 8, 64, token=60)), INV), (dict(stride=-1), INV), (dict(B=1 << 20, n=1 << 11), UNS),
+])
+def test_store_and_read_reject_before_launch(over, status):
+    for call in (prompt.lisa_cache4_store, prompt.lisa_cache4_read):
+        assert _tokens(call, **over) == status
+
+
+def test_the_cache_overlaps_nothing():
+    held = prompt.lisa_cache4_bytes(8, 2, 64)
+    assert held == 8 * 2 * 4608 and prompt.lisa_cache4_bytes(1, 1, 32) == 2304
+    assert prompt.lisa_cache4_bytes(1, 1, 16) == 0 and prompt.lisa_cache4_bytes(-1, 1, 64) == 0
+    store, read = prompt.lisa_cache4_store, prompt.lisa_cache4_read
+    assert _tokens(store, K=FAKE + held - 16) == INV and _tokens(store, positions=FAKE + 4) == INV
+    assert _tokens(store, cache=_cache(table=FAKE + 64)) == INV
+    assert _tokens(read, K=FAKE) == INV and _tokens(read, V=FAKE + MB) == INV and _tokens(read, K=FAKE + 64 * MB) == INV
+    assert _tokens(read, V=FAKE + 3 * MB - 64) == INV and _tokens(read, ks=_strides(2, 8, 64, batch=0)) == INV
+
+
+def _attend(**over):
+    a = dict(cache=_cache(), Q=FAKE + MB, O=FAKE + 2 * MB, lse=FAKE + 3 * MB, lens=FAKE + 4 * MB, B=2, heads=4, n=2,
+             scale=0.125, dtype=lisa.LISA_BF16)
+    a.update(over)
+    qs = a.get("qs", _strides(4, 2, 64))
+    return prompt.lisa_cache4_attention(a["cache"], a["Q"], qs, a["O"], a.get("os", qs), a["lse"], a["lens"], a["B"],
+                                        a["heads"], a["n"], a["scale"], a["dtype"], 0)
+
+
+@pytest.mark.parametrize("over,status", BAD_CACHE + [
+    (dict(Q=0), INV), (dict(O=0), INV), (dict(Q=FAKE + MB + 8), INV), (dict(lens=0), INV), (dict(lens=FAKE + 2), INV),
+    (dict(lse=FAKE + 2), INV), (dict(heads=3), INV), (dict(heads=-1), INV), (dict(cache=_cache(kv_heads=0)), INV),
+    (dict(B=3), INV), (dict(scale=0.0), INV), (dict(scale=math.inf), INV), (dict(dtype=lisa.LISA_F32), UNS),
+    (dict(n=600), UNS), (dict(O=FAKE + MB), INV), (dict(O=FAKE), INV), (dict(O=FAKE + 64 * MB), INV),
+    (dict(lse=FAKE + 2 * MB), INV), (dict(lse=FAKE + 4 * MB), INV), (dict(qs=None), INV),
+    (dict(os=_strides(4, 2, 64, head=0)), INV),
+])
+def test_cache_attention_rejects_before_launch(over, status):
+    assert _attend(**over) == status
+
+
+def test_empty_caches_launch_nothing():
+    none = dict(cache=_cache(pages=0, store=0, sequences=0, table=0), B=0)
+    for call in (prompt.lisa_cache4_store, prompt.lisa_cache4_read):
+        assert _tokens(call, K=0, V=0, positions=0, **none) == OK
+        assert _tokens(call, K=0, V=0, positions=0, n=0) == OK
+    assert _attend(Q=0, O=0, lens=0, **none) == OK and _attend(Q=0, O=0, lens=0, n=0) == OK
+    assert _attend(Q=0, O=0, lens=0, heads=0) == OK
