@@ -361,7 +361,8 @@ extern "C" lisa_status lisa_prompt_attention(const void *Q, const lisa_strides *
     p.err = reinterpret_cast<int *>(ws);
     p.stat_part = reinterpret_cast<float2 *>(ws + w.stat);
     p.part[0] = reinterpret_cast<float *>(ws + w.part[0]);
-    return lisa::attn::status_of(launch_simt_forward(p, dtype, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return lisa::attn::status_of(dtype == LISA_BF16 ? launch_tc_forward(p, cs) : launch_simt_forward(p, dtype, cs));
 }
 
 extern "C" size_t lisa_prompt_attention_backward_workspace_bytes(const lisa_packed *packed, int d, int dtype) {

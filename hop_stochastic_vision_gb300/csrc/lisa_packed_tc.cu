@@ -1,0 +1,428 @@
+// lisa_packed_tc.cu -- the forward attention over packed prompts on the tensor
+// cores (bf16).
+//
+// A persistent CTA takes the items of its list in the plan: 256 queries (two
+// tiles of 128 rows) of one sequence and head, with their keys in tiles of 128.
+//   warp 9        TMA: the queries, then a ring of K and V tiles
+//   warps 8, 10   one thread each issues the products of tile 0, 1: S_t = Q_t K^T
+//                 into tensor memory, then O_t += P_t V with P_t read from there
+//   warps 0-3     softmax of tile 0, one thread per row: scores to registers,
+//   warps 4-7     weights to tensor memory as bf16; the same for tile 1
+// While one tile's scores are in the softmax the other's products run.  Under the
+// causal mask tile 0 ends a tile of keys before tile 1; only the tile of keys that
+// the diagonal or the sequence's end crosses is masked element by element.
+//
+// Tiles are loaded from wherever the sequence begins, so a tile may hold tokens of
+// the next one: their scores are masked, and their values, whatever they are, are
+// set to 0 before the product meets them with weights of 0.
+//
+// The running maximum is kept only to within 2^8: O and the sum are rescaled when
+// a tile's maximum passes the reference by more, which after the first tile is
+// rare, so the accumulator stays in tensor memory.  exp is 2^x with log2(e) folded
+// into the scale.
+#include <type_traits>
+
+#include "lisa_packed_tc.cuh"
+
+namespace lisa {
+namespace packed {
+namespace {
+
+// 384 threads x 168 registers at launch = 2 x 128 x 208 + 128 x 88 after the split
+constexpr int kFwdThreads = 384;
+constexpr int kRegsSoftmax = 208, kRegsControl = 88;
+constexpr int kMaxStages = 5;
+constexpr float kSlack = 8.f;
+constexpr float kFarRef = 0x1p24f;
+constexpr int kStaging = 8 * 4096;
+constexpr int kFwdSmem = (2 + 2 * kMaxStages) * kTileBytes + kStaging + 1024;
+static_assert(kFwdSmem <= 226 * 1024, "beside the barriers");
+
+struct FwdParams {
+    Problem p;
+    MapUse uq, uk, uv;
+    FastDiv div_heads, div_group;
+};
+
+struct FwdBars {
+    uint64_t q_full[2], q_empty[2], k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages], v_empty[kMaxStages];
+    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+};
+
+// Where tile t of an item ends: its steps are w.t0 .. end - 1 (none if end <= w.t0).
+__device__ __forceinline__ int tile_end(const Work &w, int t, int causal) {
+    if (w.first + t * kRows >= w.len) return w.t0;
+    return causal ? min(w.t1, w.first / kRows + t + 1) : w.t1;
+}
+
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    packed_tc_forward(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ FwdParams x) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // stays a shared-memory pointer
+    __shared__ __align__(8) FwdBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    const Problem &p = x.p;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t base = smem_u32(sm);
+    const uint32_t q_smem = base, ring = base + 2 * kTileBytes, staging = ring + 2 * kMaxStages * kTileBytes;
+    const Guard guard{p.err, &dead};
+
+    if (tid == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&bar.q_full[t]), 1);
+            mbar_init(smem_u32(&bar.q_empty[t]), 1);
+            mbar_init(smem_u32(&bar.s_full[t]), 1);
+            mbar_init(smem_u32(&bar.s_free[t]), 4);
+            mbar_init(smem_u32(&bar.p_full[t]), 4);
+            mbar_init(smem_u32(&bar.pv_done[t]), 1);
+        }
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(smem_u32(&bar.k_full[s]), 1);
+            mbar_init(smem_u32(&bar.v_full[s]), 1);
+            mbar_init(smem_u32(&bar.k_empty[s]), 2);   // one for each tile
+            mbar_init(smem_u32(&bar.v_empty[s]), 2);
+        }
+        dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    chain_begin();
+    if (blockIdx.x == 0 && tid == 0) *p.err = 0;
+    const Walk walk = walk_of(p.lists[kForward], x.div_heads);
+
+    if (warp >= 8) set_regs_down<kRegsControl>();
+    if (warp == 11) {
+        // idle: completes the control warps' group of four
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            int kt = 0, nq[2] = {0, 0};
+            Cursor c;
+            for (int k = walk.begin; k < walk.end; ++k) {
+                const Work w = walk.at(k);
+                const bool has0 = tile_end(w, 0, p.causal) > w.t0, has1 = tile_end(w, 1, p.causal) > w.t0;
+                auto load_q = [&](int t) {
+                    const uint32_t f = smem_u32(&bar.q_full[t]);
+                    if (nq[t] > 0) wait_on(smem_u32(&bar.q_empty[t]), (nq[t] - 1) & 1, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(f, kTileBytes);
+                    load_rows(q_smem + t * kTileBytes, &mq, x.uq, w.row0 + w.first + t * kRows, w.h, 0, f);
+                    ++nq[t];
+                };
+                if (has0) load_q(0);
+                const int g = quotient(w.h, x.div_group);
+                for (int j = w.t0; j < w.t1; ++j, ++kt, c.next(kMaxStages)) {
+                    const int s = c.slot;
+                    const uint32_t kf = smem_u32(&bar.k_full[s]), vf = smem_u32(&bar.v_full[s]);
+                    if (kt >= kMaxStages) wait_on(smem_u32(&bar.k_empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(kf, kTileBytes);
+                    load_rows(ring + 2 * s * kTileBytes, &mk, x.uk, w.row0 + j * kRows, g, 0, kf);
+                    if (j == w.t0 && has1) load_q(1);
+                    if (kt >= kMaxStages) wait_on(smem_u32(&bar.v_empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(vf, kTileBytes);
+                    load_rows(ring + (2 * s + 1) * kTileBytes, &mv, x.uv, w.row0 + j * kRows, g, 0, vf);
+                }
+            }
+            // nothing may still arrive on this CTA's barriers once it has gone
+            for (int s = 0; s < kMaxStages; ++s) {
+                const int uses = kt > s ? (kt - 1 - s) / kMaxStages + 1 : 0;
+                if (uses == 0) continue;
+                if (!mbar_wait(smem_u32(&bar.k_empty[s]), (uses - 1) & 1) ||
+                    !mbar_wait(smem_u32(&bar.v_empty[s]), (uses - 1) & 1))
+                    atomicOr(p.err, kErrTimeoutMma);
+            }
+            for (int t = 0; t < 2; ++t)
+                if (nq[t] > 0 && !mbar_wait(smem_u32(&bar.q_empty[t]), (nq[t] - 1) & 1))
+                    atomicOr(p.err, kErrTimeoutMma);
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // --------------------------------------------------------- products
+        const int t = warp == 8 ? 0 : 1;
+        const uint32_t tS = tmem + t * 128, tP = tmem + 256 + t * 64, tO = tmem + 384 + t * 64;
+        const uint64_t dq = desc_rows(q_smem + t * kTileBytes), dk = desc_rows(ring), dv = desc_tokens(ring + kTileBytes);
+        constexpr uint32_t kPair = 2 * kTileBytes / 16;
+        int nq = 0, ns = 0, np = 0;
+        Cursor ck, cv;
+        for (int k = walk.begin; k < walk.end; ++k) {
+            const Work w = walk.at(k);
+            const int end = tile_end(w, t, p.causal);
+            auto scores = [&](int j) __attribute__((always_inline)) {
+                wait_on(smem_u32(&bar.k_full[ck.slot]), ck.phase, guard, kErrTimeoutLoad);
+                if (ns > 0) wait_on(smem_u32(&bar.s_free[t]), (ns - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows_rows(tS, dq, dk + (uint32_t)ck.slot * kPair, tile_cols(tile_rows(w.len, j * kRows)));
+                    tc_commit(smem_u32(&bar.s_full[t]));
+                    tc_commit(smem_u32(&bar.k_empty[ck.slot]));
+                    if (j == end - 1) tc_commit(smem_u32(&bar.q_empty[t]));
+                }
+                __syncwarp();
+                ++ns;
+                ck.next(kMaxStages);
+            };
+            if (w.t0 < end) {
+                wait_on(smem_u32(&bar.q_full[t]), nq++ & 1, guard, kErrTimeoutLoad);
+                scores(w.t0);
+            }
+            for (int j = w.t0; j < end; ++j) {
+                if (j + 1 < end) scores(j + 1);
+                wait_on(smem_u32(&bar.v_full[cv.slot]), cv.phase, guard, kErrTimeoutLoad);
+                wait_on(smem_u32(&bar.p_full[t]), np & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_weights_rows(tO, tP, dv + (uint32_t)cv.slot * kPair, tile_cols(tile_rows(w.len, j * kRows)), j > w.t0);
+                    tc_commit(smem_u32(&bar.pv_done[t]));
+                    tc_commit(smem_u32(&bar.v_empty[cv.slot]));
+                }
+                __syncwarp();
+                ++np;
+                cv.next(kMaxStages);
+            }
+            for (int j = max(end, w.t0); j < w.t1; ++j) {   // keys that this tile does not read: its share of the ring passes on
+                wait_on(smem_u32(&bar.k_full[ck.slot]), ck.phase, guard, kErrTimeoutLoad);
+                wait_on(smem_u32(&bar.v_full[ck.slot]), ck.phase, guard, kErrTimeoutLoad);
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bar.k_empty[ck.slot]));
+                    mbar_arrive(smem_u32(&bar.v_empty[ck.slot]));
+                }
+                __syncwarp();
+                ck.next(kMaxStages);
+            }
+            cv = ck;
+        }
+    } else {
+        // ---------------------------------------------------------- softmax
+        set_regs_up<kRegsSoftmax>();
+        const int t = warp >> 2, wt = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes per warp
+        const uint32_t s_tm = tmem + t * 128 + lanes, p_tm = tmem + 256 + t * 64 + lanes, o_tm = tmem + 384 + t * 64 + lanes;
+        const float scale2 = p.scale * kLog2e;
+        int kt = 0, ns = 0, np = 0;
+        for (int k = walk.begin; k < walk.end; ++k) {
+            const Work w = walk.at(k);
+            const int end = tile_end(w, t, p.causal), i = w.first + t * kRows + wt;   // the thread's row
+            // a maximum above `limit` moves the reference: ref + kSlack, -inf where ref is far from 0
+            float ref = -INFINITY, limit = -INFINITY, sum = 0.f;
+            // a whole tile (N = 0), a part of one, a part of at most 64 keys
+            auto tile = [&](int j, auto variant) __attribute__((always_inline)) {
+                constexpr bool kFull = decltype(variant)::value == 0;
+                constexpr int N = kFull ? kRows : decltype(variant)::value;
+                const int rows = kFull ? kRows : tile_rows(w.len, j * kRows), cols = kFull ? kRows : tile_cols(rows);
+                // columns that this row sees
+                const int keys = kFull ? kRows : p.causal ? min(rows, i - j * kRows + 1) : rows;
+                float s[N];
+                wait_on(smem_u32(&bar.s_full[t]), ns & 1, guard, kErrTimeoutMma);
+                ++ns;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < N; c += 32) tmem_ld32_nowait(s_tm + c, s + c);
+                tc_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar.s_free[t]));
+
+                if (!kFull) {
+#pragma unroll
+                    for (int c = 0; c < N; ++c)
+                        if (c >= keys) s[c] = -INFINITY;
+                }
+                float top;
+                {
+                    float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int c = 4; c < N; c += 8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            m4[e] = c + e + 4 < N ? fmaxf(fmaxf(m4[e], s[c + e]), s[c + e + 4]) : fmaxf(m4[e], s[c + e]);
+                    }
+                    top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale2;
+                }
+                float mul = scale2;   // 2^(mul s - ref) is the weight
+                const bool first = j == w.t0;
+                // The maximum's rounding in `ref` is a power of two common to the row's weights and goes out with the sum
+                // while it is small.  Further out (half a unit in the last place of 2^24 is 1, of 2^33 is 512) the scores
+                // are rounded as the maximum was, in every tile, so that the largest weight is 2^0 whatever their size.
+                auto refer = [&](float now) __attribute__((always_inline)) {
+                    ref = now;
+                    const bool far = fabsf(now) > kFarRef;
+                    limit = far ? -INFINITY : now + kSlack;
+                    if (__any_sync(0xFFFFFFFFu, far)) {
+#pragma unroll
+                        for (int c = 0; c < N; ++c) s[c] *= mul;
+                        mul = 1.f;
+                    }
+                };
+                if (first) {
+                    refer(top);
+                } else if (__any_sync(0xFFFFFFFFu, top > limit)) {
+                    const float now = fmaxf(ref, top);
+                    const float f = ref == -INFINITY ? 0.f : ex2_approx(ref - now);
+                    refer(now);
+                    sum *= f;
+                    wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    float o[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        tmem_ld32_nowait(o_tm + c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= f;
+                        tmem_st32(o_tm + c, o);
+                    }
+                    tc_wait_st();
+                }
+                const float shift = ref == -INFINITY ? 0.f : -ref;   // a row of -inf so far: weights 0, not NaN
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                // the previous weights have been read (and their products are in O)
+                if (!first) wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
+#pragma unroll
+                for (int c = 0; c < N; c += 32)
+                    if (kFull || c < cols) {
+                        uint32_t w16[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a, b;
+                            fma2(a, b, s[c + e], s[c + e + 1], mul, mul, shift, shift);
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                            add2(part[e & 2], part[(e & 2) + 1], part[e & 2], part[(e & 2) + 1], a, b);
+                            w16[e >> 1] = pack_bf16(a, b);
+                        }
+                        tmem_st16(p_tm + c / 2, w16);
+                    }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                if (!kFull && rows < cols && w.row0 + w.len < p.tokens) {
+                    // the next sequence's values: whatever stands there times a weight of 0 has to be 0
+                    // (for each tile's own product; the second time zeros meet zeros)
+                    const int at = kt + j - w.t0, st = at % kMaxStages;
+                    wait_on(smem_u32(&bar.v_full[st]), (at / kMaxStages) & 1, guard, kErrTimeoutLoad);
+                    zero_rows(ring + (2 * st + 1) * kTileBytes, rows, cols, wt);
+                    fence_proxy_async();
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar.p_full[t]));
+                ++np;
+            };
+            for (int j = w.t0; j < end; ++j) {
+                const int rows = tile_rows(w.len, j * kRows);
+                // the diagonal crosses the tile of keys that the tile of queries begins with
+                if (rows == kRows && !(p.causal && j * kRows == w.first + t * kRows))
+                    tile(j, std::integral_constant<int, 0>{});
+                else if (rows > 64)
+                    tile(j, std::integral_constant<int, 128>{});
+                else
+                    tile(j, std::integral_constant<int, 64>{});
+            }
+            kt += w.t1 - w.t0;
+            // ------------------------------------------------------ output
+            const bool rows_here = w.first + t * kRows < w.len;
+            if (w.part < 0 && !rows_here) continue;
+            float o[64];
+            if (w.t0 < end) {
+                wait_on(smem_u32(&bar.pv_done[t]), (np - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                tmem_ld32_nowait(o_tm, o);
+                tmem_ld32_nowait(o_tm + 32, o + 32);
+                tc_wait_ld();
+                tc_fence_before();
+            } else {
+#pragma unroll
+                for (int c = 0; c < 64; ++c) o[c] = 0.f;
+            }
+            const float inv = sum != 0.f ? 1.f / sum : 0.f;
+            if (w.part < 0) {
+                const int i0 = i - lane;
+                store_rows_bf16<64>(staging + (uint32_t)warp * 4096u, o, inv,
+                                    static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + (long long)w.h * p.O.sh +
+                                        (long long)(w.row0 + i0) * p.O.st,
+                                    p.O.st, w.len - i0, p.d, lane);
+                if (p.lse && i < w.len)
+                    p.lse[(long long)w.h * p.lse_stride + w.row0 + i] = ref == -INFINITY ? -INFINITY : kLn2 * (ref + log2f(sum));
+            } else if (i < w.len) {
+                const size_t at = ((size_t)w.part * p.heads + w.h) * unit_rows(kForward) + t * kRows + wt;
+                p.stat_part[at] = make_float2(ref, sum);
+                float4 *op = reinterpret_cast<float4 *>(p.part[0] + at * p.d);
+#pragma unroll
+                for (int c = 0; c < 64; c += 4)
+                    if (c < p.d) op[c / 4] = make_float4(o[c] * inv, o[c + 1] * inv, o[c + 2] * inv, o[c + 3] * inv);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// o = sum_s w_s o_s / sum_s w_s with w_s = 2^(ref_s - ref) sum_s: the parts of a row, in order.  Reference and sum come
+// apart: far from 0 their lse would have lost the sum (at 2^24 the last place is 2), and parts of unequal lengths would
+// weigh the same.  A CTA takes 32 rows of one cut unit and head, a thread four elements at a time.
+constexpr int kJoinRows = 32;
+__global__ void __launch_bounds__(256) join_forward(const __grid_constant__ Problem p) {
+    chain_begin();
+    const Lists &l = p.lists[kForward];
+    const Join j = l.joins[blockIdx.x / (unit_rows(kForward) / kJoinRows)];
+    const int r0 = (int)(blockIdx.x % (unit_rows(kForward) / kJoinRows)) * kJoinRows, h = blockIdx.y, vec = p.d / 4;
+    for (int e = threadIdx.x; e < kJoinRows * vec; e += 256) {
+        const int r = r0 + e / vec, c = e % vec * 4;
+        if (r >= j.rows) continue;
+        const size_t at0 = ((size_t)j.part * p.heads + h) * unit_rows(kForward) + r;
+        const size_t step = (size_t)p.heads * unit_rows(kForward);
+        float top = -INFINITY;
+        for (int s = 0; s < j.parts; ++s) top = fmaxf(top, p.stat_part[at0 + s * step].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < j.parts; ++s) {
+            const float2 st = p.stat_part[at0 + s * step];
+            const float w = ex2_approx(st.x - ref) * st.y;
+            const float4 v = *reinterpret_cast<const float4 *>(p.part[0] + (at0 + s * step) * p.d + c);
+            sum += w;
+            o[0] = fmaf(w, v.x, o[0]);
+            o[1] = fmaf(w, v.y, o[1]);
+            o[2] = fmaf(w, v.z, o[2]);
+            o[3] = fmaf(w, v.w, o[3]);
+        }
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+        uint2 out;
+        out.x = pack_bf16(o[0] * inv, o[1] * inv);
+        out.y = pack_bf16(o[2] * inv, o[3] * inv);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + (long long)h * p.O.sh +
+                                   (long long)(j.row + r) * p.O.st + c) = out;
+        if (c == 0 && p.lse)
+            p.lse[(long long)h * p.lse_stride + j.row + r] = top == -INFINITY ? -INFINITY : kLn2 * (top + log2f(sum));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_tc_forward(const Problem &p, cudaStream_t s) {
+    FwdParams x{};
+    x.p = p;
+    CUtensorMap mq, mk, mv;
+    if (!make_packed_map(&mq, &x.uq, p.Q, p.heads, p.tokens, p.d) ||
+        !make_packed_map(&mk, &x.uk, p.K, p.kv_heads, p.tokens, p.d) ||
+        !make_packed_map(&mv, &x.uv, p.V, p.kv_heads, p.tokens, p.d))
+        return cudaErrorInvalidValue;
+    x.div_heads = fast_div(p.heads);
+    x.div_group = fast_div(p.group);
+    cudaError_t e = allow_smem<packed_tc_forward>();
+    if (e == cudaSuccess)
+        e = launch_chained(packed_tc_forward, workers(p.lists[kForward], p.heads), kFwdThreads, kFwdSmem, s, mq, mk, mv, x);
+    if (e == cudaSuccess && p.lists[kForward].n_joins > 0)
+        e = launch_chained(join_forward,
+                           dim3((unsigned)p.lists[kForward].n_joins * (unit_rows(kForward) / kJoinRows), (unsigned)p.heads),
+                           256, 0, s, p);
+    return e;
+}
+
+}  // namespace packed
+}  // namespace lisa
