@@ -5,7 +5,6 @@
 // columns tx + 16 c of a 64 x 64 tile.
 #pragma once
 
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "lisa_attn.h"
@@ -22,11 +21,6 @@ __device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
     const float4 x = *reinterpret_cast<const float4 *>(p);
     v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
-    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-    v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xFFFF0000u);
-}
 
 // Rows t0 .. t0 + 63 of a [tokens][D] slice, first into registers (so the loads of
 // the next tile run under this tile's arithmetic), then into out[64][D + 4]; rows
@@ -34,8 +28,7 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
 template <int D>
 struct Rows {
     float v[D / 16][4];
-    template <typename T>
-    __device__ __forceinline__ void load(const T *base, long long st, int t0, int count, int tid) {
+    __device__ __forceinline__ void load(const float *base, long long st, int t0, int count, int tid) {
 #pragma unroll
         for (int u = 0; u < D / 16; ++u) {
             const int e = tid + u * kThreads, r = e / (D / 4), c = 4 * (e % (D / 4));
@@ -51,8 +44,8 @@ struct Rows {
         }
     }
 };
-template <int D, typename T>
-__device__ __forceinline__ void load_tile(const T *base, long long st, int t0, int count, float *out, int tid) {
+template <int D>
+__device__ __forceinline__ void load_tile(const float *base, long long st, int t0, int count, float *out, int tid) {
     Rows<D> r;
     r.load(base, st, t0, count, tid);
     r.store(out, tid);

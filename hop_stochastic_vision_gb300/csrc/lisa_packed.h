@@ -62,10 +62,11 @@ struct Problem {
     float *part[2];        // [part][head][unit_rows][d]: O; dQ; dV, dK
 };
 
-// bf16 on the tensor cores
+// bf16 on the tensor cores, fp32 on the CUDA cores
 cudaError_t launch_tc_forward(const Problem &p, cudaStream_t s);
-cudaError_t launch_simt_forward(const Problem &p, int dtype, cudaStream_t s);
-cudaError_t launch_simt_backward(const Problem &p, int dtype, cudaStream_t s);
+cudaError_t launch_tc_backward(const Problem &p, cudaStream_t s);
+cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s);
+cudaError_t launch_simt_backward(const Problem &p, cudaStream_t s);
 
 }  // namespace packed
 }  // namespace lisa

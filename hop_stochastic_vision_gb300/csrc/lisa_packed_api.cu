@@ -362,7 +362,7 @@ extern "C" lisa_status lisa_prompt_attention(const void *Q, const lisa_strides *
     p.stat_part = reinterpret_cast<float2 *>(ws + w.stat);
     p.part[0] = reinterpret_cast<float *>(ws + w.part[0]);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return lisa::attn::status_of(dtype == LISA_BF16 ? launch_tc_forward(p, cs) : launch_simt_forward(p, dtype, cs));
+    return lisa::attn::status_of(dtype == LISA_BF16 ? launch_tc_forward(p, cs) : launch_simt_forward(p, cs));
 }
 
 extern "C" size_t lisa_prompt_attention_backward_workspace_bytes(const lisa_packed *packed, int d, int dtype) {
@@ -408,5 +408,6 @@ extern "C" lisa_status lisa_prompt_attention_backward(
     p.err = reinterpret_cast<int *>(ws);
     p.delta = reinterpret_cast<float *>(ws + w.delta);
     for (int k = 0; k < 2; ++k) p.part[k] = reinterpret_cast<float *>(ws + w.part[k]);
-    return lisa::attn::status_of(launch_simt_backward(p, dtype, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return lisa::attn::status_of(dtype == LISA_BF16 ? launch_tc_backward(p, cs) : launch_simt_backward(p, cs));
 }

@@ -1,11 +1,10 @@
 // lisa_packed_simt.cu -- attention over packed prompts on the CUDA cores: 64 x 64
-// tiles in shared memory (lisa_attn_simt.cuh), any type, head widths 16, 32, 64.
+// tiles in shared memory (lisa_attn_simt.cuh), fp32, head widths 16, 32, 64.
 //
 // A CTA takes 64 queries (forward, dQ) or 64 keys (dK, dV) of one sequence and
 // head and walks the tiles of the other side that its mask leaves; a tile that
 // the diagonal or the sequence's end crosses is masked pair by pair.  The units
 // come from the plan's lists, whole (parts are for the tensor-core kernels).
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "lisa_attn_simt.cuh"
@@ -19,12 +18,9 @@ namespace {
 using namespace lisa::attn;
 using lisa::packed::Problem;
 
-template <typename T>
-__device__ __forceinline__ const T *head_of(const Tensor &t, int h, int row0) {
-    return static_cast<const T *>(t.p) + (long long)h * t.sh + (long long)row0 * t.st;
+__device__ __forceinline__ const float *head_of(const Tensor &t, int h, int row0) {
+    return static_cast<const float *>(t.p) + (long long)h * t.sh + (long long)row0 * t.st;
 }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // The CTA's 64 rows of a unit; false where there are none (the unit ends, or is another part of one).
 struct Rows64 {
@@ -49,7 +45,7 @@ __device__ __forceinline__ void masked_scores(float (&s)[4][4], float scale, int
     }
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kThreads) packed_forward(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
     chain_begin();
@@ -58,8 +54,8 @@ __global__ void __launch_bounds__(kThreads) packed_forward(const __grid_constant
     Rows64 w;
     if (!w.of<unit_rows(kForward) / kTile>(p.lists[kForward])) return;
     const int i0 = w.first, len = w.len, end = p.causal ? min(len, i0 + kTile) : len;
-    const T *K = head_of<T>(p.K, kvh, w.row0), *V = head_of<T>(p.V, kvh, w.row0);
-    load_tile<D>(head_of<T>(p.Q, h, w.row0), p.Q.st, i0, len, q_s, tid);
+    const float *K = head_of(p.K, kvh, w.row0), *V = head_of(p.V, kvh, w.row0);
+    load_tile<D>(head_of(p.Q, h, w.row0), p.Q.st, i0, len, q_s, tid);
     float top[4], sum[4], acc[4][D / 16];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -105,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) packed_forward(const __grid_constant
         __syncwarp();   // a row's weights are written and read by one warp
         tile_mul<D>(p_s, v_s, ty, tx, acc);
     }
-    T *out = const_cast<T *>(head_of<T>(p.O, h, w.row0));
+    float *out = const_cast<float *>(head_of(p.O, h, w.row0));
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int i = i0 + 4 * ty + r;
@@ -113,13 +109,13 @@ __global__ void __launch_bounds__(kThreads) packed_forward(const __grid_constant
         if (i >= len) continue;
         const float inv = sum[r] != 0.f ? 1.f / sum[r] : 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) put(out + (long long)i * p.O.st + tx + 16 * c, acc[r][c] * inv);
+        for (int c = 0; c < D / 16; ++c) out[(long long)i * p.O.st + tx + 16 * c] = acc[r][c] * inv;
         if (p.lse && tx == 0)
             p.lse[h * p.lse_stride + w.row0 + i] = top[r] == -INFINITY ? -INFINITY : top[r] + logf(sum[r]);
     }
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kThreads) packed_dq(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
     chain_begin();
@@ -130,10 +126,10 @@ __global__ void __launch_bounds__(kThreads) packed_dq(const __grid_constant__ Pr
     Rows64 w;
     if (!w.of<unit_rows(kDq) / kTile>(p.lists[kDq])) return;
     const int i0 = w.first, len = w.len, end = p.causal ? min(len, i0 + kTile) : len;
-    const T *K = head_of<T>(p.K, kvh, w.row0), *V = head_of<T>(p.V, kvh, w.row0);
+    const float *K = head_of(p.K, kvh, w.row0), *V = head_of(p.V, kvh, w.row0);
     // delta~_i = dO_i . O_i from the forward's (rounded) output
-    load_tile<D>(head_of<T>(p.O, h, w.row0), p.O.st, i0, len, q_s, tid);
-    load_tile<D>(head_of<T>(p.dO, h, w.row0), p.dO.st, i0, len, o_s, tid);
+    load_tile<D>(head_of(p.O, h, w.row0), p.O.st, i0, len, q_s, tid);
+    load_tile<D>(head_of(p.dO, h, w.row0), p.dO.st, i0, len, o_s, tid);
     __syncthreads();
     float delta[4], exact[4], total[4], ref[4], acc[4][D / 16];
     const long long at0 = h * p.lse_stride + w.row0;
@@ -150,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) packed_dq(const __grid_constant__ Pr
         for (int c = 0; c < D / 16; ++c) acc[r][c] = 0.f;
     }
     __syncthreads();
-    load_tile<D>(head_of<T>(p.Q, h, w.row0), p.Q.st, i0, len, q_s, tid);
+    load_tile<D>(head_of(p.Q, h, w.row0), p.Q.st, i0, len, q_s, tid);
     Rows<D> kr, vr;
     kr.load(K, p.K.st, 0, end, tid);
     vr.load(V, p.V.st, 0, end, tid);
@@ -181,20 +177,20 @@ __global__ void __launch_bounds__(kThreads) packed_dq(const __grid_constant__ Pr
         __syncwarp();
         tile_mul<D>(p_s, k_s, ty, tx, acc);
     }
-    T *out = const_cast<T *>(head_of<T>(p.dQ, h, w.row0));
+    float *out = const_cast<float *>(head_of(p.dQ, h, w.row0));
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int i = i0 + 4 * ty + r;
         const float e = half_sum(exact[r]), t = half_sum(total[r]);
         if (i >= len) continue;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) put(out + (long long)i * p.dQ.st + tx + 16 * c, acc[r][c] * p.scale);
+        for (int c = 0; c < D / 16; ++c) out[(long long)i * p.dQ.st + tx + 16 * c] = acc[r][c] * p.scale;
         // over sum p, which takes the rounding of lse out: the dS of a row add up to 0
         if (tx == 0) p.delta[(size_t)h * p.tokens + w.row0 + i] = t > 0.f ? e / t : e;
     }
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kThreads) packed_dkdv(const __grid_constant__ Problem p) {
     extern __shared__ __align__(16) float sm[];
     chain_begin();
@@ -209,11 +205,11 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv(const __grid_constant__ 
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) dk[r][c] = dv[r][c] = 0.f;
-    load_tile<D>(head_of<T>(p.K, kvh, w.row0), p.K.st, j0, len, k_s, tid);
-    load_tile<D>(head_of<T>(p.V, kvh, w.row0), p.V.st, j0, len, v_s, tid);
+    load_tile<D>(head_of(p.K, kvh, w.row0), p.K.st, j0, len, k_s, tid);
+    load_tile<D>(head_of(p.V, kvh, w.row0), p.V.st, j0, len, v_s, tid);
     for (int g = 0; g < p.group; ++g) {
         const int h = kvh * p.group + g, start = p.causal ? j0 : 0;
-        const T *Q = head_of<T>(p.Q, h, w.row0), *dO = head_of<T>(p.dO, h, w.row0);
+        const float *Q = head_of(p.Q, h, w.row0), *dO = head_of(p.dO, h, w.row0);
         const long long at0 = h * p.lse_stride + w.row0;
         const float *delta_h = p.delta + (size_t)h * p.tokens + w.row0;
         Rows<D> qr, dr;
@@ -247,15 +243,15 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv(const __grid_constant__ 
             tile_mul_t<D>(d_s, q_s, ty, tx, dk);
         }
     }
-    T *out_k = const_cast<T *>(head_of<T>(p.dK, kvh, w.row0)), *out_v = const_cast<T *>(head_of<T>(p.dV, kvh, w.row0));
+    float *out_k = const_cast<float *>(head_of(p.dK, kvh, w.row0)), *out_v = const_cast<float *>(head_of(p.dV, kvh, w.row0));
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int j = j0 + 4 * ty + r;
         if (j >= len) continue;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-            put(out_k + (long long)j * p.dK.st + tx + 16 * c, dk[r][c] * p.scale);
-            put(out_v + (long long)j * p.dV.st + tx + 16 * c, dv[r][c]);
+            out_k[(long long)j * p.dK.st + tx + 16 * c] = dk[r][c] * p.scale;
+            out_v[(long long)j * p.dV.st + tx + 16 * c] = dv[r][c];
         }
     }
 }
@@ -268,29 +264,24 @@ cudaError_t run(int pass, int heads, int floats, const Problem &p, cudaStream_t 
     return launch_plain(kKernel, dim3(blocks, (unsigned)heads), kThreads, (size_t)floats * sizeof(float), s, p);
 }
 
-template <int D, typename T>
+template <int D>
 struct Simt {
     static constexpr int t = tile_floats<D>();
     static cudaError_t forward(const Problem &p, cudaStream_t s) {
-        return run<packed_forward<D, T>>(kForward, p.heads, 3 * t + kWeights, p, s);
+        return run<packed_forward<D>>(kForward, p.heads, 3 * t + kWeights, p, s);
     }
     static cudaError_t backward(const Problem &p, cudaStream_t s) {
-        const cudaError_t e = run<packed_dq<D, T>>(kDq, p.heads, 4 * t + kWeights, p, s);
-        return e != cudaSuccess ? e : run<packed_dkdv<D, T>>(kDkv, p.kv_heads, 4 * t + 2 * kWeights, p, s);
+        const cudaError_t e = run<packed_dq<D>>(kDq, p.heads, 4 * t + kWeights, p, s);
+        return e != cudaSuccess ? e : run<packed_dkdv<D>>(kDkv, p.kv_heads, 4 * t + 2 * kWeights, p, s);
     }
 };
 
 }  // namespace
 
-#define LISA_PACKED_DISPATCH(T, fn) \
-    (p.d == 16 ? Simt<16, T>::fn(p, s) : p.d == 32 ? Simt<32, T>::fn(p, s) : Simt<64, T>::fn(p, s))
+#define LISA_PACKED_DISPATCH(fn) (p.d == 16 ? Simt<16>::fn(p, s) : p.d == 32 ? Simt<32>::fn(p, s) : Simt<64>::fn(p, s))
 
-cudaError_t launch_simt_forward(const Problem &p, int dtype, cudaStream_t s) {
-    return dtype == LISA_BF16 ? LISA_PACKED_DISPATCH(__nv_bfloat16, forward) : LISA_PACKED_DISPATCH(float, forward);
-}
-cudaError_t launch_simt_backward(const Problem &p, int dtype, cudaStream_t s) {
-    return dtype == LISA_BF16 ? LISA_PACKED_DISPATCH(__nv_bfloat16, backward) : LISA_PACKED_DISPATCH(float, backward);
-}
+cudaError_t launch_simt_forward(const Problem &p, cudaStream_t s) { return LISA_PACKED_DISPATCH(forward); }
+cudaError_t launch_simt_backward(const Problem &p, cudaStream_t s) { return LISA_PACKED_DISPATCH(backward); }
 
 }  // namespace packed
 }  // namespace lisa

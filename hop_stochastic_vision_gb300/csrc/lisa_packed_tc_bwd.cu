@@ -1,0 +1,677 @@
+// lisa_packed_tc_bwd.cu -- the backward attention over packed prompts on the
+// tensor cores (bf16).
+//
+// Two kernels of one shape, each a persistent CTA of 20 warps around 128 x 128
+// tiles of pairs whose scores and dP = dO V^T are products into tensor memory:
+//   dQ     128 queries against their keys; dS goes back to tensor memory as bf16
+//          for dQ += dS K.  Also leaves delta_i for the other: dO . O from the
+//          rounded output (an error of one rounding of O against bf16 results),
+//          or sum_j p dP / sum_j p in fp32 where all keys of a row are one tile
+//   dK dV  128 keys against the queries that see them, of every head that shares
+//          them, the tile transposed (rows are keys): dV += P^T dO, dK += dS^T Q
+// Scores are recomputed in each (7 products for 5) so that every sum has one
+// owner: no atomics, no fp32 dQ in memory, the same bits every time.  A unit cut
+// into parts leaves its sums in memory for a join that adds them in order.
+//
+// Four warpgroups share a tile by columns, 32 each, a thread per row.  The threads
+// take S and dP into registers as soon as both are there, so the next tile's
+// products run under this tile's arithmetic.
+//
+// Tiles are loaded from wherever the sequence begins, so a tile may hold tokens of
+// the next one.  Their weights and dS are set to 0 whatever the products say, and
+// the rows that the second products would multiply with those zeros are set to 0.
+#include "lisa_packed_tc.cuh"
+
+namespace lisa {
+namespace packed {
+namespace {
+
+constexpr int kMath = 512;         // threads of arithmetic: 16 warps
+constexpr int kMathWarps = kMath / 32;
+constexpr int kThreads = kMath + 128;   // behind them: products (two warps), loads, a helper
+constexpr int kFront = kMathWarps, kLoads = kMathWarps + 1, kBack = kMathWarps + 2, kHelper = kMathWarps + 3;
+constexpr int kStrip = 32;         // columns of a thread's row
+constexpr uint32_t kPair = 2 * kTileBytes / 16;   // a ring stage of two tiles, in descriptor units
+constexpr int kSlots = 2;          // items' own tiles held
+constexpr int kDqStages = 3, kDkvStages = 3;
+constexpr int kDkvOut = kMathWarps * 2048;   // staging blocks of the math warps
+
+struct BwdParams {
+    Problem p;
+    MapUse uq, uk, uv, ud, uo;
+    FastDiv div_heads, div_group;   // of the pass
+};
+
+__device__ __forceinline__ float neg_lse2(float l) {
+    return fabsf(l) > kMaxLse ? -INFINITY : -l * kLog2e;   // rows without keys among them: every weight 2^-inf = 0
+}
+
+// A strip of S and of dP.  Columns that the products did not reach hold whatever was there before and are not used.
+__device__ __forceinline__ void load_strips(uint32_t ta, float (&a)[kStrip], uint32_t tb, float (&b)[kStrip]) {
+    tmem_ld32_nowait(ta, a);
+    tmem_ld32_nowait(tb, b);
+    tc_wait_ld();
+}
+__device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(bar));
+}
+__device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
+
+// The loading thread waits for the last use of every slot, so nothing arrives on the CTA's barriers once it has gone.
+__device__ __forceinline__ void drain(uint64_t *bar, int uses, int *err) {
+    if (uses > 0 && !mbar_wait(smem_u32(bar), (uses - 1) & 1)) atomicOr(err, kErrTimeoutMma);
+}
+__device__ __forceinline__ int uses_of(int total, int slot, int stages) {
+    return total > slot ? (total - 1 - slot) / stages + 1 : 0;
+}
+
+// ------------------------------------------------------------------------ dQ
+struct DqBars {
+    uint64_t q_full[kSlots], q_empty[kSlots], kv_full[kDqStages], kv_empty[kDqStages];
+    uint64_t full, free, ds_full, dq_done;   // S and dP of a tile: there, in registers
+};
+constexpr int kDqSmem = (3 * kSlots + 2 * kDqStages) * kTileBytes + 1024;
+
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_tc_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md,
+                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                 const __grid_constant__ CUtensorMap mo, const __grid_constant__ BwdParams x) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // stays a shared-memory pointer
+    __shared__ __align__(8) DqBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    __shared__ float rows_delta[kRows];
+    const Problem &p = x.p;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t base = smem_u32(sm);
+    const uint32_t qd = base, ring = base + 3 * kSlots * kTileBytes;   // slots of (Q, dO, O); stages of (K, V)
+    const Guard guard{p.err, &dead};
+
+    if (tid == 0) {
+        for (int t = 0; t < kSlots; ++t) {
+            mbar_init(smem_u32(&bar.q_full[t]), 1);
+            mbar_init(smem_u32(&bar.q_empty[t]), 1 + kMathWarps);   // the products and delta
+        }
+        for (int s = 0; s < kDqStages; ++s) {
+            mbar_init(smem_u32(&bar.kv_full[s]), 1);
+            mbar_init(smem_u32(&bar.kv_empty[s]), 1);
+        }
+        mbar_init(smem_u32(&bar.full), 1);
+        mbar_init(smem_u32(&bar.dq_done), 1);
+        mbar_init(smem_u32(&bar.free), kMathWarps);
+        mbar_init(smem_u32(&bar.ds_full), kMathWarps);
+        dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == kFront) tmem_alloc(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    chain_begin();
+    if (blockIdx.x == 0 && tid == 0) *p.err = 0;
+    const uint32_t tS = tmem, tP = tmem + 128, tDs = tmem + 256, tDq = tmem + 320;
+    const Walk walk = walk_of(p.lists[kDq], x.div_heads);
+
+    if (warp == kHelper) {
+        // nothing to help with here
+    } else if (warp == kLoads) {
+        if (lane == 0) {
+            int kt = 0, nq = 0;
+            Cursor c, cq;
+            for (int k = walk.begin; k < walk.end; ++k) {
+                const Work w = walk.at(k);
+                const int qs = cq.slot, g = quotient(w.h, x.div_group), row = w.row0 + w.first;
+                if (nq >= kSlots) wait_on(smem_u32(&bar.q_empty[qs]), cq.phase ^ 1u, guard, kErrTimeoutMma);
+                cq.next(kSlots);
+                const uint32_t f = smem_u32(&bar.q_full[qs]);
+                mbar_arrive_expect_tx(f, 3 * kTileBytes);
+                load_rows(qd + 3 * qs * kTileBytes, &mq, x.uq, row, w.h, 0, f);
+                load_rows(qd + (3 * qs + 1) * kTileBytes, &md, x.ud, row, w.h, 0, f);
+                load_rows(qd + (3 * qs + 2) * kTileBytes, &mo, x.uo, row, w.h, 0, f);
+                ++nq;
+                for (int j = w.t0; j < w.t1; ++j, ++kt, c.next(kDqStages)) {
+                    const uint32_t f = smem_u32(&bar.kv_full[c.slot]), at = ring + 2 * c.slot * kTileBytes;
+                    if (kt >= kDqStages) wait_on(smem_u32(&bar.kv_empty[c.slot]), c.phase ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(f, 2 * kTileBytes);
+                    load_rows(at, &mk, x.uk, w.row0 + j * kRows, g, 0, f);
+                    load_rows(at + kTileBytes, &mv, x.uv, w.row0 + j * kRows, g, 0, f);
+                }
+            }
+            for (int s = 0; s < kDqStages; ++s) drain(&bar.kv_empty[s], uses_of(kt, s, kDqStages), p.err);
+            for (int t = 0; t < kSlots; ++t) drain(&bar.q_empty[t], uses_of(nq, t, kSlots), p.err);
+        }
+        __syncwarp();
+    } else if (warp == kFront) {
+        // S and dP of each tile
+        int kt = 0;
+        Cursor c, cq;
+        const uint64_t q0 = desc_rows(qd), k0 = desc_rows(ring), v0 = desc_rows(ring + kTileBytes);
+        for (int k = walk.begin; k < walk.end; ++k) {
+            const Work w = walk.at(k);
+            const int qs = cq.slot;
+            wait_on(smem_u32(&bar.q_full[qs]), cq.phase, guard, kErrTimeoutLoad);
+            cq.next(kSlots);
+            const uint64_t qa = q0 + (uint32_t)qs * (3 * kTileBytes / 16), da = qa + kTileBytes / 16;
+            for (int j = w.t0; j < w.t1; ++j, ++kt, c.next(kDqStages)) {
+                const int s = c.slot, cols = tile_cols(tile_rows(w.len, j * kRows));
+                wait_on(smem_u32(&bar.kv_full[s]), c.phase, guard, kErrTimeoutLoad);
+                if (kt > 0) wait_on(smem_u32(&bar.free), (kt - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows_rows(tS, qa, k0 + (uint32_t)s * kPair, cols);
+                    mma_rows_rows(tP, da, v0 + (uint32_t)s * kPair, cols);
+                    tc_commit(smem_u32(&bar.full));
+                    if (j == w.t1 - 1) tc_commit(smem_u32(&bar.q_empty[qs]));
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp == kBack) {
+        // dQ += dS K.  S and dP have read the K and V tiles: dS comes of them.
+        int kt = 0;
+        Cursor c;
+        const uint64_t kt0 = desc_tokens(ring);
+        for (int k = walk.begin; k < walk.end; ++k) {
+            const Work w = walk.at(k);
+            for (int j = w.t0; j < w.t1; ++j, ++kt, c.next(kDqStages)) {
+                wait_on(smem_u32(&bar.ds_full), kt & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_weights_rows(tDq, tDs, kt0 + (uint32_t)c.slot * kPair, tile_cols(tile_rows(w.len, j * kRows)), j > w.t0);
+                    tc_commit(smem_u32(&bar.dq_done));
+                    tc_commit(smem_u32(&bar.kv_empty[c.slot]));
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        const int strip = warp >> 2, c0 = kStrip * strip, wt = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const float scale2 = p.scale * kLog2e;
+        int kt = 0;
+        Cursor cq;
+        // the row's lse of a pair of the list, as it is in memory (a use would wait for it)
+        auto lse_of = [&](int k) {
+            if (k >= walk.end) return INFINITY;
+            const Work y = walk.at(k);
+            const int i = y.first + wt;
+            return i < y.len ? p.lse[(long long)y.h * p.lse_stride + y.row0 + i] : INFINITY;
+        };
+        float lse_next = lse_of(walk.begin);
+        for (int k = walk.begin; k < walk.end; ++k) {
+            const Work w = walk.at(k);
+            const int i = w.first + wt;
+            const bool in = i < w.len;
+            const float nl = neg_lse2(lse_next);
+            lse_next = lse_of(k + 1);
+            const bool single = w.steps == 1;   // delta from the tile itself, below
+            wait_on(smem_u32(&bar.q_full[cq.slot]), cq.phase, guard, kErrTimeoutLoad);
+            // dO . O of the tile's rows, 8 lanes per row
+            if (!single) {
+                const uint32_t g_s = qd + (3 * cq.slot + 1) * kTileBytes, o_s = g_s + kTileBytes;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * warp + 4 * e + (lane >> 3);
+                    const uint32_t at = sw128_offset(r, lane & 7);
+                    uint4 a, b;
+                    ld_shared_v4(o_s + at, a.x, a.y, a.z, a.w);
+                    ld_shared_v4(g_s + at, b.x, b.y, b.z, b.w);
+                    float v = bf16_lo(a.x) * bf16_lo(b.x);
+                    v = fmaf(bf16_hi(a.x), bf16_hi(b.x), v);
+                    v = fmaf(bf16_lo(a.y), bf16_lo(b.y), v);
+                    v = fmaf(bf16_hi(a.y), bf16_hi(b.y), v);
+                    v = fmaf(bf16_lo(a.z), bf16_lo(b.z), v);
+                    v = fmaf(bf16_hi(a.z), bf16_hi(b.z), v);
+                    v = fmaf(bf16_lo(a.w), bf16_lo(b.w), v);
+                    v = fmaf(bf16_hi(a.w), bf16_hi(b.w), v);
+#pragma unroll
+                    for (int m = 4; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+                    if ((lane & 7) == 0) rows_delta[r] = v;
+                }
+            }
+            math_barrier();   // also: the strips of the previous item's delta have been read
+            float delta = single ? 0.f : rows_delta[wt];
+            for (int j = w.t0; j < w.t1; ++j, ++kt) {
+                const int rows = tile_rows(w.len, j * kRows), cols = tile_cols(rows);
+                const bool diagonal = p.causal && j * kRows == w.first;
+                const int keys = (diagonal ? min(rows, wt + 1) : rows) - c0;   // of this strip, that the row sees
+                float s[kStrip], dp[kStrip];
+                wait_on(smem_u32(&bar.full), kt & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                load_strips(tS + c0 + lanes, s, tP + c0 + lanes, dp);
+                tc_fence_before();
+                arrive_warp(&bar.free, lane);
+#pragma unroll
+                for (int c = 0; c < kStrip; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, nl, nl);
+                if (diagonal || rows < kRows) {   // dP of keys behind the last one holds whatever their values hold
+#pragma unroll
+                    for (int c = 0; c < kStrip; ++c)
+                        if (c >= keys) {
+                            s[c] = -INFINITY;
+                            dp[c] = 0.f;
+                        }
+                }
+#pragma unroll
+                for (int c = 0; c < kStrip; ++c) s[c] = ex2_approx(s[c]);
+                uint32_t ds[kStrip / 2];
+                if (single) {   // delta from the unrounded weights: few keys, where dP - delta cancels most, do without
+                                // the rounding of O
+                    float e0 = 0.f, e1 = 0.f, t0 = 0.f, t1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < kStrip; e += 2) {
+                        mul2(dp[e], dp[e + 1], s[e], s[e + 1], dp[e], dp[e + 1]);
+                        add2(e0, e1, e0, e1, dp[e], dp[e + 1]);
+                        add2(t0, t1, t0, t1, s[e], s[e + 1]);
+                    }
+                    // the strips' shares, where the item's O is: nothing reads that now
+                    float2 *share = reinterpret_cast<float2 *>(sm + (3 * cq.slot + 2) * kTileBytes) + wt;
+                    share[strip * kRows] = make_float2(e0 + e1, t0 + t1);
+                    math_barrier();
+                    // sum p dP / sum p: the division takes the rounding of lse out
+                    const float2 a = share[0], b = share[kRows], c = share[2 * kRows], d = share[3 * kRows];
+                    const float total = (a.y + b.y) + (c.y + d.y);
+                    delta = ((a.x + b.x) + (c.x + d.x)) / (total > 0.f ? total : 1.f);
+#pragma unroll
+                    for (int e = 0; e < kStrip; e += 2) {
+                        float u, v;
+                        fma2(u, v, s[e], s[e + 1], -delta, -delta, dp[e], dp[e + 1]);
+                        ds[e >> 1] = pack_bf16(u, v);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kStrip; e += 2) {
+                        add2(dp[e], dp[e + 1], dp[e], dp[e + 1], -delta, -delta);
+                        mul2(dp[e], dp[e + 1], dp[e], dp[e + 1], s[e], s[e + 1]);
+                        ds[e >> 1] = pack_bf16(dp[e], dp[e + 1]);
+                    }
+                }
+                // the previous dS has been read
+                if (kt > 0) wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                tmem_st16(tDs + c0 / 2 + lanes, ds);
+                if (strip == 0 && rows < cols && w.row0 + w.len < p.tokens) {
+                    // S is done with the tile: what the next sequence holds may not meet dS = 0
+                    zero_rows(ring + 2 * (kt % kDqStages) * kTileBytes, rows, cols, wt);
+                    fence_proxy_async();
+                }
+                tc_wait_st();
+                tc_fence_before();
+                arrive_warp(&bar.ds_full, lane);
+            }
+            if (strip == 0 && in && w.t0 == 0) p.delta[(size_t)w.h * p.tokens + w.row0 + i] = delta;
+            wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
+            tc_fence_after();
+            float o[16];
+            tmem_ld16_nowait(tDq + 16 * strip + lanes, o);
+            tc_wait_ld();
+            tc_fence_before();
+            if (w.part < 0) {
+                // staged where the item's O was: its last reader was delta, before every warp's dS
+                store_rows_bf16<16>(qd + (3 * cq.slot + 2) * kTileBytes + (uint32_t)warp * 1024u, o, p.scale,
+                                    static_cast<__nv_bfloat16 *>(const_cast<void *>(p.dQ.p)) + (long long)w.h * p.dQ.sh +
+                                        (long long)(w.row0 + i - lane) * p.dQ.st + 16 * strip,
+                                    p.dQ.st, w.len - (i - lane), p.d - 16 * strip, lane);
+            } else if (in && 16 * strip < p.d) {
+                float4 *out = reinterpret_cast<float4 *>(
+                    p.part[0] + (((size_t)w.part * p.heads + w.h) * unit_rows(kDq) + wt) * p.d + 16 * strip);
+#pragma unroll
+                for (int c = 0; c < 16; c += 4) out[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+            }
+            fence_proxy_async();
+            arrive_warp(&bar.q_empty[cq.slot], lane);
+            cq.next(kSlots);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kFront) tmem_dealloc(tmem, 512);
+}
+
+// --------------------------------------------------------------------- dK, dV
+struct DkvBars {
+    uint64_t kv_full[kSlots], kv_empty[kSlots], q_full[kDkvStages], q_empty[kDkvStages];
+    uint64_t aux_full[kDkvStages], aux_empty[kDkvStages];
+    uint64_t full, free, w_full, w_done;   // S and dP: there, in registers; P and dS: there, read
+};
+// What the arithmetic needs of a tile's queries, one entry per column.
+struct QueryAux {
+    float nl[kRows], minus_delta[kRows];
+};
+constexpr int kDkvAux = 2 * (kSlots + kDkvStages) * kTileBytes + kDkvOut;
+constexpr int kDkvSmem = kDkvAux + kDkvStages * (int)sizeof(QueryAux) + 1024;
+static_assert(kDqSmem <= 226 * 1024 && kDkvSmem <= 226 * 1024, "beside the barriers");
+
+// The steps of a unit of keys: for each head that shares them, the tiles of queries that see them.
+struct Steps {
+    int first, tiles;   // tiles of queries: the first that sees the keys, how many
+    int h, qt;          // of the current step
+    __device__ __forceinline__ Steps(const Work &w, int group, int causal) {
+        first = causal ? w.first / kRows : 0;
+        tiles = (w.len + kRows - 1) / kRows - first;
+        const int head = w.t0 / tiles;
+        h = w.h * group + head;
+        qt = first + w.t0 - head * tiles;
+    }
+    __device__ __forceinline__ void next() {
+        if (++qt == first + tiles) {
+            qt = first;
+            ++h;
+        }
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_tc_dkdv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md,
+                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                   const __grid_constant__ BwdParams x) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // stays a shared-memory pointer
+    __shared__ __align__(8) DkvBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    const Problem &p = x.p;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t base = smem_u32(sm);
+    const uint32_t kv = base, ring = base + 2 * kSlots * kTileBytes;   // slots of (K, V); stages of (Q, dO)
+    const uint32_t staging = ring + 2 * kDkvStages * kTileBytes;
+    QueryAux *aux = reinterpret_cast<QueryAux *>(sm + kDkvAux);
+    const Guard guard{p.err, &dead};
+
+    if (tid == 0) {
+        for (int t = 0; t < kSlots; ++t) {
+            mbar_init(smem_u32(&bar.kv_full[t]), 1);
+            mbar_init(smem_u32(&bar.kv_empty[t]), 1);
+        }
+        for (int s = 0; s < kDkvStages; ++s) {
+            mbar_init(smem_u32(&bar.q_full[s]), 1);
+            mbar_init(smem_u32(&bar.q_empty[s]), 1);
+            mbar_init(smem_u32(&bar.aux_full[s]), 1);
+            mbar_init(smem_u32(&bar.aux_empty[s]), kMathWarps);
+        }
+        mbar_init(smem_u32(&bar.full), 1);
+        mbar_init(smem_u32(&bar.w_done), 1);
+        mbar_init(smem_u32(&bar.free), kMathWarps);
+        mbar_init(smem_u32(&bar.w_full), kMathWarps);
+        dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == kFront) tmem_alloc(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    chain_begin();
+    const uint32_t tS = tmem, tD = tmem + 128, tPw = tmem + 256, tDs = tmem + 320, tDv = tmem + 384, tDk = tmem + 448;
+    const Walk walk = walk_of(p.lists[kDkv], x.div_heads);
+
+    if (warp == kHelper) {
+        // per-query scalars of each tile
+        int n = 0;
+        Cursor c;
+        for (int k = walk.begin; k < walk.end; ++k) {
+            const Work w = walk.at(k);
+            Steps st(w, p.group, p.causal);
+            for (int u = w.t0; u < w.t1; ++u, ++n, c.next(kDkvStages), st.next()) {
+                const int s = c.slot;
+                if (n >= kDkvStages) wait_on(smem_u32(&bar.aux_empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
+                const float *lse = p.lse + (long long)st.h * p.lse_stride + w.row0;
+                const float *delta = p.delta + (size_t)st.h * p.tokens + w.row0;
+#pragma unroll
+                for (int e = lane; e < kRows; e += 32) {
+                    const int i = st.qt * kRows + e;
+                    const bool in = i < w.len;
+                    aux[s].nl[e] = neg_lse2(in ? lse[i] : INFINITY);
+                    aux[s].minus_delta[e] = in ? -delta[i] : 0.f;
+                }
+                arrive_warp(&bar.aux_full[s], lane);
+            }
+        }
+    } else if (warp == kLoads) {
+        if (lane == 0) {
+            int n = 0, items = 0;
+            Cursor c, ck;
+            for (int k = walk.begin; k < walk.end; ++k) {
+                const Work w = walk.at(k);
+                if (items >= kSlots) wait_on(smem_u32(&bar.kv_empty[ck.slot]), ck.phase ^ 1u, guard, kErrTimeoutMma);
+                ++items;
+                const uint32_t f = smem_u32(&bar.kv_full[ck.slot]), kv_at = kv + 2 * ck.slot * kTileBytes;
+                ck.next(kSlots);
+                mbar_arrive_expect_tx(f, 2 * kTileBytes);
+                load_rows(kv_at, &mk, x.uk, w.row0 + w.first, w.h, 0, f);
+                load_rows(kv_at + kTileBytes, &mv, x.uv, w.row0 + w.first, w.h, 0, f);
+                Steps st(w, p.group, p.causal);
+                for (int u = w.t0; u < w.t1; ++u, ++n, c.next(kDkvStages), st.next()) {
+                    const int s = c.slot;
+                    const uint32_t f = smem_u32(&bar.q_full[s]), at = ring + 2 * s * kTileBytes;
+                    if (n >= kDkvStages) wait_on(smem_u32(&bar.q_empty[s]), c.phase ^ 1u, guard, kErrTimeoutMma);
+                    mbar_arrive_expect_tx(f, 2 * kTileBytes);
+                    load_rows(at, &mq, x.uq, w.row0 + st.qt * kRows, st.h, 0, f);
+                    load_rows(at + kTileBytes, &md, x.ud, w.row0 + st.qt * kRows, st.h, 0, f);
+                }
+            }
+            for (int s = 0; s < kDkvStages; ++s) drain(&bar.q_empty[s], uses_of(n, s, kDkvStages), p.err);
+            for (int t = 0; t < kSlots; ++t) drain(&bar.kv_empty[t], uses_of(items, t, kSlots), p.err);
+        }
+        __syncwarp();
+    } else if (warp == kFront) {
+        // S^T and dP^T of each tile
+        int n = 0;
+        Cursor c, ck;
+        const uint64_t k0 = desc_rows(kv), v0 = desc_rows(kv + kTileBytes), q0 = desc_rows(ring),
+                       d0 = desc_rows(ring + kTileBytes);
+        for (int k = walk.begin; k < walk.end; ++k) {
+            const Work w = walk.at(k);
+            const int ks = ck.slot;
+            wait_on(smem_u32(&bar.kv_full[ks]), ck.phase, guard, kErrTimeoutLoad);
+            ck.next(kSlots);
+            const uint64_t ka = k0 + (uint32_t)ks * kPair, va = v0 + (uint32_t)ks * kPair;
+            Steps st(w, p.group, p.causal);
+            for (int u = w.t0; u < w.t1; ++u, ++n, c.next(kDkvStages), st.next()) {
+                const int s = c.slot, cols = tile_cols(tile_rows(w.len, st.qt * kRows));
+                wait_on(smem_u32(&bar.q_full[s]), c.phase, guard, kErrTimeoutLoad);
+                if (n > 0) wait_on(smem_u32(&bar.free), (n - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows_rows(tS, ka, q0 + (uint32_t)s * kPair, cols);
+                    mma_rows_rows(tD, va, d0 + (uint32_t)s * kPair, cols);
+                    tc_commit(smem_u32(&bar.full));
+                    if (u == w.t1 - 1) tc_commit(smem_u32(&bar.kv_empty[ks]));
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp == kBack) {
+        // dV += P^T dO, dK += dS^T Q.  S^T and dP^T have read the tiles too: P and dS come of them.
+        int n = 0;
+        Cursor c;
+        const uint64_t qt0 = desc_tokens(ring), dt0 = desc_tokens(ring + kTileBytes);
+        for (int k = walk.begin; k < walk.end; ++k) {
+            const Work w = walk.at(k);
+            Steps st(w, p.group, p.causal);
+            for (int u = w.t0; u < w.t1; ++u, ++n, c.next(kDkvStages), st.next()) {
+                const int s = c.slot, cols = tile_cols(tile_rows(w.len, st.qt * kRows));
+                wait_on(smem_u32(&bar.w_full), n & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_weights_rows(tDv, tPw, dt0 + (uint32_t)s * kPair, cols, u > w.t0);
+                    mma_weights_rows(tDk, tDs, qt0 + (uint32_t)s * kPair, cols, u > w.t0);
+                    tc_commit(smem_u32(&bar.w_done));
+                    tc_commit(smem_u32(&bar.q_empty[s]));
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        const int strip = warp >> 2, c0 = kStrip * strip, wt = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const float scale2 = p.scale * kLog2e;
+        int n = 0;
+        Cursor ca;
+        for (int k = walk.begin; k < walk.end; ++k) {
+            const Work w = walk.at(k);
+            const int j = w.first + wt;
+            Steps st(w, p.group, p.causal);
+            for (int u = w.t0; u < w.t1; ++u, ++n, ca.next(kDkvStages), st.next()) {
+                const int rows = tile_rows(w.len, st.qt * kRows), cols = tile_cols(rows);
+                const bool diagonal = p.causal && st.qt * kRows == w.first;
+                const QueryAux &a = aux[ca.slot];
+                float s[kStrip], dp[kStrip];
+                wait_on(smem_u32(&bar.aux_full[ca.slot]), ca.phase, guard, kErrTimeoutLoad);
+                wait_on(smem_u32(&bar.full), n & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                load_strips(tS + c0 + lanes, s, tD + c0 + lanes, dp);
+                tc_fence_before();
+                arrive_warp(&bar.free, lane);
+#pragma unroll
+                for (int c = 0; c < kStrip; c += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
+                    fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, l.x, l.y);
+                    fma2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], scale2, scale2, l.z, l.w);
+                }
+                if (diagonal || rows < kRows) {
+                    // queries before the key, and behind the sequence's last: those hold whatever the next one's do
+                    const int lo = diagonal ? wt - c0 : 0, hi = rows - c0;
+#pragma unroll
+                    for (int c = 0; c < kStrip; ++c)
+                        if (c < lo || c >= hi) {
+                            s[c] = -INFINITY;
+                            dp[c] = 0.f;
+                        }
+                }
+                uint32_t pw[kStrip / 2], ds[kStrip / 2];
+#pragma unroll
+                for (int e = 0; e < kStrip; e += 4) {
+                    const float4 d = *reinterpret_cast<const float4 *>(a.minus_delta + c0 + e);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) s[e + v] = ex2_approx(s[e + v]);
+                    pw[e >> 1] = pack_bf16(s[e], s[e + 1]);
+                    pw[(e >> 1) + 1] = pack_bf16(s[e + 2], s[e + 3]);
+                    add2(dp[e], dp[e + 1], dp[e], dp[e + 1], d.x, d.y);
+                    add2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], d.z, d.w);
+                    mul2(dp[e], dp[e + 1], dp[e], dp[e + 1], s[e], s[e + 1]);
+                    mul2(dp[e + 2], dp[e + 3], dp[e + 2], dp[e + 3], s[e + 2], s[e + 3]);
+                    ds[e >> 1] = pack_bf16(dp[e], dp[e + 1]);
+                    ds[(e >> 1) + 1] = pack_bf16(dp[e + 2], dp[e + 3]);
+                }
+                // the previous P and dS have been read
+                if (n > 0) wait_on(smem_u32(&bar.w_done), (n - 1) & 1, guard, kErrTimeoutMma);
+                tc_fence_after();
+                tmem_st16(tPw + c0 / 2 + lanes, pw);
+                tmem_st16(tDs + c0 / 2 + lanes, ds);
+                if (strip < 2 && rows < cols && w.row0 + w.len < p.tokens) {
+                    // S and dP are done with the tiles: what the next sequence holds may not meet weights of 0
+                    zero_rows(ring + (2 * ca.slot + strip) * kTileBytes, rows, cols, wt);
+                    fence_proxy_async();
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bar.aux_empty[ca.slot]));
+                    mbar_arrive(smem_u32(&bar.w_full));
+                }
+            }
+            // ---- strips 0, 1 store dV, 2 and 3 dK, 32 columns each
+            float o[kStrip];
+            const int dk = strip >> 1, oc = kStrip * (strip & 1);
+            wait_on(smem_u32(&bar.w_done), (n - 1) & 1, guard, kErrTimeoutMma);
+            tc_fence_after();
+            tmem_ld32_nowait((dk ? tDk : tDv) + oc + lanes, o);
+            tc_wait_ld();
+            tc_fence_before();
+            if (w.part < 0) {
+                const Tensor &t = dk ? p.dK : p.dV;
+                const int r0 = j - lane;
+                store_rows_bf16<kStrip>(staging + (uint32_t)warp * 2048u, o, dk ? p.scale : 1.f,
+                                        static_cast<__nv_bfloat16 *>(const_cast<void *>(t.p)) + (long long)w.h * t.sh +
+                                            (long long)(w.row0 + r0) * t.st + oc,
+                                        t.st, w.len - r0, p.d - oc, lane);
+            } else if (j < w.len) {
+                float4 *out = reinterpret_cast<float4 *>(
+                    p.part[dk] + (((size_t)w.part * p.kv_heads + w.h) * unit_rows(kDkv) + wt) * p.d + oc);
+#pragma unroll
+                for (int c = 0; c < kStrip; c += 4)
+                    if (oc + c < p.d) out[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kFront) tmem_dealloc(tmem, 512);
+}
+
+// A cut unit's gradient from its parts, in order.  A CTA takes 32 rows of one unit and head, a thread four elements.
+constexpr int kJoinRows = 32;
+struct JoinParams {
+    Lists l;
+    const float *part[2];
+    Tensor out[2];
+    float mul[2];
+    int heads, d;
+};
+__global__ void __launch_bounds__(256) join_gradients(const __grid_constant__ JoinParams x) {
+    chain_begin();
+    constexpr int kBlocks = unit_rows(kDq) / kJoinRows;
+    static_assert(unit_rows(kDq) == unit_rows(kDkv), "one join for both passes");
+    const Join j = x.l.joins[blockIdx.x / kBlocks];
+    const int r0 = (int)(blockIdx.x % kBlocks) * kJoinRows, h = blockIdx.y, which = blockIdx.z, vec = x.d / 4;
+    const size_t step = (size_t)x.heads * unit_rows(kDq) * x.d;
+    const Tensor &t = x.out[which];
+    for (int e = threadIdx.x; e < kJoinRows * vec; e += 256) {
+        const int r = r0 + e / vec, c = e % vec * 4;
+        if (r >= j.rows) continue;
+        const float *at = x.part[which] + (((size_t)j.part * x.heads + h) * unit_rows(kDq) + r) * x.d + c;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < j.parts; ++s, at += step) {
+            const float4 a = *reinterpret_cast<const float4 *>(at);
+            v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+        }
+        const float mul = x.mul[which];
+        uint2 o;
+        o.x = pack_bf16(v.x * mul, v.y * mul);
+        o.y = pack_bf16(v.z * mul, v.w * mul);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(t.p)) + (long long)h * t.sh +
+                                   (long long)(j.row + r) * t.st + c) = o;
+    }
+}
+cudaError_t launch_join(const JoinParams &x, int outs, cudaStream_t s) {
+    if (x.l.n_joins == 0) return cudaSuccess;
+    const dim3 grid((unsigned)x.l.n_joins * (unit_rows(kDq) / kJoinRows), (unsigned)x.heads, (unsigned)outs);
+    return launch_plain(join_gradients, grid, 256, 0, s, x);
+}
+
+}  // namespace
+
+cudaError_t launch_tc_backward(const Problem &p, cudaStream_t s) {
+    BwdParams x{};
+    x.p = p;
+    CUtensorMap mq, md, mk, mv, mo;
+    if (!make_packed_map(&mq, &x.uq, p.Q, p.heads, p.tokens, p.d) ||
+        !make_packed_map(&md, &x.ud, p.dO, p.heads, p.tokens, p.d) ||
+        !make_packed_map(&mk, &x.uk, p.K, p.kv_heads, p.tokens, p.d) ||
+        !make_packed_map(&mv, &x.uv, p.V, p.kv_heads, p.tokens, p.d) ||
+        !make_packed_map(&mo, &x.uo, p.O, p.heads, p.tokens, p.d))
+        return cudaErrorInvalidValue;
+    x.div_group = fast_div(p.group);
+    x.div_heads = fast_div(p.heads);
+    cudaError_t e = allow_smem<packed_tc_dq>();
+    if (e == cudaSuccess)
+        e = launch_plain(packed_tc_dq, workers(p.lists[kDq], p.heads), kThreads, kDqSmem, s, mq, md, mk, mv, mo, x);
+    if (e == cudaSuccess)
+        e = launch_join(JoinParams{p.lists[kDq], {p.part[0], nullptr}, {p.dQ, p.dQ}, {p.scale, 0.f}, p.heads, p.d}, 1, s);
+    x.div_heads = fast_div(p.kv_heads);
+    if (e == cudaSuccess) e = allow_smem<packed_tc_dkdv>();
+    if (e == cudaSuccess)
+        e = launch_plain(packed_tc_dkdv, workers(p.lists[kDkv], p.kv_heads), kThreads, kDkvSmem, s, mq, md, mk, mv, x);
+    if (e == cudaSuccess)
+        e = launch_join(JoinParams{p.lists[kDkv], {p.part[0], p.part[1]}, {p.dV, p.dK}, {1.f, p.scale}, p.kv_heads, p.d}, 2, s);
+    return e;
+}
+
+}  // namespace packed
+}  // namespace lisa
