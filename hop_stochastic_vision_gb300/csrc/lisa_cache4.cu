@@ -1,9 +1,10 @@
 // lisa_cache4.cu -- the key/value cache in 4 bits: storing tokens and reading them
 // back, and the argument checks of its entry points.
 //
-// Four threads take the 32 elements of a group, eight each: 16 or 32 bytes of a
-// token in, one word of codes out.  Bound by the bytes of the tokens in their own
-// type (a group of bf16 is 64 bytes, held in 18).
+// Four threads take the 32 elements of a group, eight each, of the key and of the
+// value: their loads are on the way together while the token's page is looked up.
+// Bound by the bytes of the tokens in their own type (a group of bf16 is 64 bytes,
+// held in 18).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -31,15 +32,14 @@ struct TokenParams {
     Tensor K, V;                 // read: written
     const int *positions, *sequences;
     long long positions_stride;
-    long long threads;           // 4 G per token, key head and side
+    long long threads;           // 4 G per token and key head
     FastDiv div_n, div_rows;     // by n and by kv_heads
-    int n;
 };
 
-// Which eight elements a thread has: in order of side, quarter, group, head, token (heads side by side in a token) or
-// side, quarter, group, token, head (tokens side by side in a head).
+// Which eight elements a thread has: in order of quarter, group, head, token (heads side by side in a token) or quarter,
+// group, token, head (tokens side by side in a head).
 struct Place {
-    int b, i, head, q, group, value;
+    int b, i, head, q, group;
 };
 template <int D>
 __device__ __forceinline__ Place place_of(const TokenParams &x, long long at, bool heads_first) {
@@ -47,9 +47,7 @@ __device__ __forceinline__ Place place_of(const TokenParams &x, long long at, bo
     Place p;
     p.q = (int)(at & 3);
     p.group = G == 2 ? (int)(at >> 2 & 1) : 0;
-    at >>= G == 2 ? 3 : 2;
-    p.value = (int)(at & 1);
-    int rest = (int)(at >> 1);   // (token, head) pairs: below 2^31
+    int rest = (int)(at >> (G == 2 ? 3 : 2));   // (token, head) pairs: below 2^31
     if (heads_first) {
         int t = split(rest, x.div_rows);
         p.head = rest;
@@ -92,48 +90,78 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
     *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// x / d rounded to nearest, for a y that is 1 / d rounded to nearest, d and the quotient well inside the normal range:
+// one step of Newton's iteration on the quotient is exact then (Markstein, 1990).
+__device__ __forceinline__ float quotient_by(float x, float d, float y) {
+    const float q = x * y;
+    return fmaf(fmaf(-q, d, x), y, q);
+}
+constexpr float kSmall = 0x1p-80f, kLarge = 0x1p80f;
+
+// Codes and scale of a group of 32 elements, eight of them in each of four neighbouring lanes.
+__device__ __forceinline__ uint32_t quantise(const float (&v)[8], __nv_bfloat16 &held) {
+    // the largest magnitude by its bits, which order like the numbers, infinity and then NaN above all
+    unsigned bits = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bits = max(bits, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 1));
+    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 2));
+    const float top = __uint_as_float(bits);
+    uint32_t word = 0;
+    if (top > kSmall && top < kLarge) {
+        held = __float2bfloat16_rn(quotient_by(top, 7.f, 1.f / 7.f));
+        const float scale = __bfloat162float(held), inverse = __frcp_rn(scale);
+#pragma unroll
+        for (int e = 7; e >= 0; --e)   // 1.5 2^23 + 8: the sum's last bits are the code plus 8, rounded to nearest even
+            word = word << 4 | (__float_as_uint(quotient_by(v[e], scale, inverse) + 12582920.f) & 15u);
+    } else {
+        const bool finite = bits < 0x7F800000u;
+        held = __float2bfloat16_rn(finite ? __fdiv_rn(top, 7.f) : __uint_as_float(0x7FFFFFFFu));
+        const float scale = __bfloat162float(held);
+#pragma unroll
+        for (int e = 7; e >= 0; --e) {
+            // beyond 7 only where the scale is a subnormal bf16 number, coarser than its rounding elsewhere
+            const float code = finite && scale > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(v[e], scale)), -7.f), 7.f) : 0.f;
+            word = word << 4 | (uint32_t)((int)code + 8);
+        }
+    }
+    return word;
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) store_tokens(const __grid_constant__ TokenParams x, bool heads_first) {
     chain_begin();
     const long long at = (long long)blockIdx.x * kThreads + threadIdx.x;
     const bool in = at < x.threads;   // every lane stays for the exchange
     const Place p = place_of<D>(x, in ? at : 0, heads_first);
+    const int element = p.group * kGroup + p.q * 8;
+    float k[8], v[8];
+    load8(static_cast<const T *>(x.K.p) + (long long)p.b * x.K.sb + (long long)p.head * x.K.sh + (long long)p.i * x.K.st + element, k);
+    load8(static_cast<const T *>(x.V.p) + (long long)p.b * x.V.sb + (long long)p.head * x.V.sh + (long long)p.i * x.V.st + element, v);
     const long long where = p.b * x.positions_stride + p.i;
     const int position = in ? x.positions[where] : -1;
-    const int page = page_of(x.c, in && x.sequences ? x.sequences[where] : p.b, position);
-    float v[8] = {};
-    const Tensor &t = p.value ? x.V : x.K;
-    if (page >= 0)
-        load8(static_cast<const T *>(t.p) + (long long)p.b * t.sb + (long long)p.head * t.sh + (long long)p.i * t.st +
-                  p.group * kGroup + p.q * 8, v);
-    // the largest magnitude by its bits, which order like the numbers, infinity and then NaN above all
-    unsigned top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const int page = page_of(x.c, x.sequences ? x.sequences[where] : p.b, position);
+    __nv_bfloat16 scale_k, scale_v;
+    const uint32_t word_k = quantise(k, scale_k), word_v = quantise(v, scale_v);
     if (page < 0) return;
-    const bool finite = top < 0x7F800000u;
-    const __nv_bfloat16 held = __float2bfloat16_rn(finite ? __fdiv_rn(__uint_as_float(top), 7.f) : __uint_as_float(0x7FFFFFFFu));
-    const float scale = __bfloat162float(held);
-    uint32_t word = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        // beyond 7 only where the scale is a subnormal bf16 number, coarser than its rounding elsewhere
-        const float code = finite && scale > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(v[e], scale)), -7.f), 7.f) : 0.f;
-        word |= (uint32_t)((int)code + 8) << (4 * e);
-    }
     using B = Block<D>;
     const int token = position % kPage;
     uint8_t *block = x.c.store + ((long long)page * x.c.kv_heads + p.head) * B::kBytes;
-    if (p.value) {
-        *reinterpret_cast<uint16_t *>(block + B::off_v + B::value_half(token, 2 * p.q, p.group)) = (uint16_t)word;
-        *reinterpret_cast<uint16_t *>(block + B::off_v + B::value_half(token, 2 * p.q + 1, p.group)) = (uint16_t)(word >> 16);
-    } else {
-        *reinterpret_cast<uint32_t *>(block + B::key_word(token, p.q, p.group)) = word;
+    *reinterpret_cast<uint32_t *>(block + B::key_word(token, p.q, p.group)) = word_k;
+    uint8_t *values = block + B::off_v;
+    *reinterpret_cast<uint16_t *>(values + B::value_half(token, 2 * p.q, p.group)) = (uint16_t)word_v;
+    *reinterpret_cast<uint16_t *>(values + B::value_half(token, 2 * p.q + 1, p.group)) = (uint16_t)(word_v >> 16);
+    if (p.q == 0) {
+        const int s = (token * B::G + p.group) * 2;
+        *reinterpret_cast<__nv_bfloat16 *>(block + B::off_ks + s) = scale_k;
+        *reinterpret_cast<__nv_bfloat16 *>(block + B::off_vs + s) = scale_v;
     }
-    if (p.q == 0)
-        *reinterpret_cast<__nv_bfloat16 *>(block + (p.value ? B::off_vs : B::off_ks) + (token * B::G + p.group) * 2) = held;
+}
+
+__device__ __forceinline__ void values_of(uint32_t word, float scale, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)   // 2^23 + the code plus 8, less 2^23 + 8
+        v[e] = (__uint_as_float((word >> (4 * e) & 15u) | 0x4B000000u) - 8388616.f) * scale;
 }
 
 template <int D, typename T>
@@ -142,29 +170,25 @@ __global__ void __launch_bounds__(kThreads) read_tokens(const __grid_constant__ 
     const long long at = (long long)blockIdx.x * kThreads + threadIdx.x;
     if (at >= x.threads) return;
     const Place p = place_of<D>(x, at, heads_first);
+    const int element = p.group * kGroup + p.q * 8;
     const long long where = p.b * x.positions_stride + p.i;
     const int position = x.positions[where];
     const int page = page_of(x.c, x.sequences ? x.sequences[where] : p.b, position);
-    float v[8] = {};
+    float k[8] = {}, v[8] = {};
     if (page >= 0) {
         using B = Block<D>;
-        const int token = position % kPage;
-        const uint8_t *block = x.c.store + ((long long)page * x.c.kv_heads + p.head) * B::kBytes;
-        uint32_t word;
-        if (p.value) {
-            word = *reinterpret_cast<const uint16_t *>(block + B::off_v + B::value_half(token, 2 * p.q, p.group));
-            word |= (uint32_t)*reinterpret_cast<const uint16_t *>(block + B::off_v + B::value_half(token, 2 * p.q + 1, p.group)) << 16;
-        } else {
-            word = *reinterpret_cast<const uint32_t *>(block + B::key_word(token, p.q, p.group));
-        }
-        const float scale = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(
-            block + (p.value ? B::off_vs : B::off_ks) + (token * B::G + p.group) * 2));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)((int)(word >> (4 * e) & 15u) - 8) * scale;
+        const int token = position % kPage, s = (token * B::G + p.group) * 2;
+        const uint8_t *block = x.c.store + ((long long)page * x.c.kv_heads + p.head) * B::kBytes, *values = block + B::off_v;
+        const uint32_t word_k = *reinterpret_cast<const uint32_t *>(block + B::key_word(token, p.q, p.group));
+        const uint32_t lo = *reinterpret_cast<const uint16_t *>(values + B::value_half(token, 2 * p.q, p.group));
+        const uint32_t hi = *reinterpret_cast<const uint16_t *>(values + B::value_half(token, 2 * p.q + 1, p.group));
+        const __nv_bfloat16 scale_k = *reinterpret_cast<const __nv_bfloat16 *>(block + B::off_ks + s);
+        const __nv_bfloat16 scale_v = *reinterpret_cast<const __nv_bfloat16 *>(block + B::off_vs + s);
+        values_of(word_k, __bfloat162float(scale_k), k);
+        values_of(lo | hi << 16, __bfloat162float(scale_v), v);
     }
-    const Tensor &t = p.value ? x.V : x.K;
-    store8(static_cast<T *>(const_cast<void *>(t.p)) + (long long)p.b * t.sb + (long long)p.head * t.sh +
-               (long long)p.i * t.st + p.group * kGroup + p.q * 8, v);
+    store8(static_cast<T *>(const_cast<void *>(x.K.p)) + (long long)p.b * x.K.sb + (long long)p.head * x.K.sh + (long long)p.i * x.K.st + element, k);
+    store8(static_cast<T *>(const_cast<void *>(x.V.p)) + (long long)p.b * x.V.sb + (long long)p.head * x.V.sh + (long long)p.i * x.V.st + element, v);
 }
 
 // The struct by itself.
@@ -218,10 +242,9 @@ lisa_status tokens(const lisa_cache4 *cache, const void *K, const lisa_strides *
     x.positions = positions;
     x.sequences = sequences;
     x.positions_stride = positions_stride;
-    x.threads = (long long)B * n * heads * 2 * (d / 8);
+    x.threads = (long long)B * n * heads * (d / 8);
     x.div_n = fast_div(n);
     x.div_rows = fast_div(heads);
-    x.n = n;
     const bool heads_first = ks->head < ks->token;
     const dim3 grid((unsigned)((x.threads + kThreads - 1) / kThreads));
     cudaError_t e;

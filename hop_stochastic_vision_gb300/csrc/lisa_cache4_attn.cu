@@ -82,6 +82,16 @@ __device__ __forceinline__ uint32_t without_offset(uint32_t pair) {
     return r;
 }
 
+// d = A B + (c0, c0, c1, c1): the rows' own first values.
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+constexpr float kFarRef = 0x1p20f;
+
 // kHalves: 1 where at most 8 rows share a key head (the product's upper rows are idle), else 2.
 template <int D, int kHalves>
 __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Params x) {
@@ -188,13 +198,12 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
             float acc[G][4];
 #pragma unroll
             for (int u = 0; u < G; ++u) {
-                acc[u][0] = acc[u][1] = minus[u][0];
-                acc[u][2] = acc[u][3] = kHalves == 2 ? minus[u][kHalves - 1] : 0.f;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    mma_bf16_16816(acc[u], a[u][2 * k][0], kHalves == 2 ? a[u][2 * k][kHalves - 1] : 0u, a[u][2 * k + 1][0],
-                                   kHalves == 2 ? a[u][2 * k + 1][kHalves - 1] : 0u, code_pair(w[u], 2 * k),
-                                   code_pair(w[u], 2 * k + 1));
+                const uint32_t *l = a[u][0], *m = a[u][1], *n = a[u][2], *r = a[u][3];
+                constexpr bool kBoth = kHalves == 2;
+                mma_from(acc[u], l[0], kBoth ? l[kHalves - 1] : 0u, m[0], kBoth ? m[kHalves - 1] : 0u, code_pair(w[u], 0),
+                         code_pair(w[u], 1), minus[u][0], kBoth ? minus[u][kHalves - 1] : 0.f);
+                mma_bf16_16816(acc[u], n[0], kBoth ? n[kHalves - 1] : 0u, r[0], kBoth ? r[kHalves - 1] : 0u,
+                               code_pair(w[u], 2), code_pair(w[u], 3));
             }
 #pragma unroll
             for (int e = 0; e < kHalves; ++e)
@@ -202,30 +211,41 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
                 for (int t = 0; t < 2; ++t) {
                     float v = acc[0][2 * e + t] * sk[t][0];
                     if (G == 2) v = fmaf(acc[G - 1][2 * e + t], sk[t][G - 1], v);
-                    v *= scale2;
                     if (!kWhole) v = j0 + 8 * j + 2 * q4 + t < sees[e] ? v : -INFINITY;
                     s[j][2 * e + t] = v;
                 }
         }
 #pragma unroll
         for (int e = 0; e < kHalves; ++e) {
-            float t = ref[e];
+            float t = s[0][2 * e];
 #pragma unroll
             for (int j = 0; j < 8; ++j) t = fmaxf(t, fmaxf(s[j][2 * e], s[j][2 * e + 1]));
+            t *= scale2;
             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
-            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
+            t = fmaxf(fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2)), ref[e]);
             const float r = t == -INFINITY ? 0.f : t;   // nothing but -inf so far: weights 0, not NaN
             const float f = ex2_approx(ref[e] - r);
             ref[e] = t;
-            float part = 0.f;
+            // The reference's rounding is common to a row's weights of this page and all others and goes out with the sum
+            // while it is small (2^20: an eighth); further out the scores are rounded as the reference was.
+            float mul = scale2;
+            if (__any_sync(0xFFFFFFFFu, fabsf(r) > kFarRef)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    s[j][2 * e] *= mul;
+                    s[j][2 * e + 1] *= mul;
+                }
+                mul = 1.f;
+            }
+            float part[2] = {0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    s[j][2 * e + u] = ex2_approx(s[j][2 * e + u] - r);
-                    part += s[j][2 * e + u];
+                    s[j][2 * e + u] = ex2_approx(fmaf(s[j][2 * e + u], mul, -r));
+                    part[u] += s[j][2 * e + u];
                 }
-            sum[e] = fmaf(sum[e], f, part);
+            sum[e] = fmaf(sum[e], f, part[0] + part[1]);
 #pragma unroll
             for (int u = 0; u < G; ++u)
 #pragma unroll

@@ -4,9 +4,7 @@
 // The angle of a pair is position * frequency modulo one turn.  With the
 // frequency in turns as a 64-bit binary fraction F = 2^64 f / 2 pi, the 64-bit
 // product position * F drops whole turns by itself, so the angle of a far
-// position is as good as that of a near one and costs one integer product.  It
-// is taken to the nearest quarter turn first; what is left, at most an eighth of
-// a turn, becomes an fp32 number, so sin and cos are taken of small arguments only.
+// position is as good as that of a near one and costs three integer instructions.
 //
 // A thread holds the sines and cosines of the pairs in one 16-byte vector of a
 // token and turns that vector of every head in its share of the heads, four
@@ -76,38 +74,75 @@ struct Elements {
         }
     }
 };
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_float(float &o, float x) { o = x; }
-__device__ __forceinline__ void from_float(__nv_bfloat16 &o, float x) { o = __float2bfloat16_rn(x); }
-
-// sin and cos of a 64-bit fraction of a turn.  bf16: the special-function unit's, 2^-20.9 off at most, far below the
-// half step 2^-9 of what is stored; fp32: the library's, of an argument within an eighth of a turn.
-template <typename T>
-__device__ __forceinline__ void sin_cos(unsigned long long phase, float &s, float &c) {
-    const unsigned quarter = (unsigned)((phase + (1ULL << 61)) >> 62);
-    const int rest = (int)((long long)(phase - ((unsigned long long)quarter << 62)) >> 32);   // 2^-32 turns, |.| <= 2^29
-    float sr, cr;
-    if constexpr (sizeof(T) == 2) {
-        const float x = (float)rest * 1.4629180792671596e-9f;   // 2 pi 2^-32
-        sr = __sinf(x);
-        cr = __cosf(x);
-    } else {
-        sincospif((float)rest * 0x1p-31f, &sr, &cr);
-    }
-    const bool swap = quarter & 1u;
-    s = swap ? cr : sr;
-    c = swap ? sr : cr;
-    if (quarter & 2u) s = -s;
-    if ((quarter + 1u) & 2u) c = -c;
+template <int N>
+__device__ __forceinline__ void to_floats(const Elements<float, N> &x, float (&f)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = x.v[e];
 }
+template <int N>
+__device__ __forceinline__ void to_floats(const Elements<__nv_bfloat16, N> &x, float (&f)[N]) {
+    if constexpr (N == 1) {
+        f[0] = __bfloat162float(x.v[0]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {   // a pair is one word
+            const uint32_t w = reinterpret_cast<const uint32_t *>(x.v)[e / 2];
+            f[e] = __uint_as_float(w << 16);
+            f[e + 1] = __uint_as_float(w & 0xFFFF0000u);
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void from_floats(Elements<float, N> &x, const float (&f)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) x.v[e] = f[e];
+}
+template <int N>
+__device__ __forceinline__ void from_floats(Elements<__nv_bfloat16, N> &x, const float (&f)[N]) {
+    if constexpr (N == 1) {
+        x.v[0] = __float2bfloat16_rn(f[0]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) reinterpret_cast<__nv_bfloat162 *>(x.v)[e / 2] = __floats2bfloat162_rn(f[e], f[e + 1]);
+    }
+}
+
+// The upper half of the 64-bit product position * frequency, a signed 32-bit fraction of a turn: what is below 2^-32 turns
+// does not count.  (position as an unsigned number is 2^32 too large where it is negative.)
+__device__ __forceinline__ unsigned phase_of(int position, uint2 turns) {
+    const unsigned place = (unsigned)position;
+    return place * turns.y + __umulhi(place, turns.x) - (position < 0 ? turns.x : 0u);
+}
+// Its sin and cos.  bf16: the special-function unit's, of the whole angle within half a turn, 2^-20.8 off at most with the
+// angle's rounding, far below the half step 2^-9 of what is stored.  fp32: the library's, of the rest of the angle after
+// the nearest quarter turn.
+template <typename T>
+__device__ __forceinline__ void sin_cos(unsigned phase, float &s, float &c) {
+    if constexpr (sizeof(T) == 2) {
+        const float x = (float)(int)phase * 1.4629180792671596e-9f;   // 2 pi 2^-32
+        s = __sinf(x);
+        c = __cosf(x);
+    } else {
+        const unsigned quarter = (phase + (1u << 29)) >> 30;
+        float sr, cr;
+        sincospif((float)(int)(phase - (quarter << 30)) * 0x1p-31f, &sr, &cr);
+        const bool swap = quarter & 1u;
+        s = swap ? cr : sr;
+        c = swap ? sr : cr;
+        if (quarter & 2u) s = -s;
+        if ((quarter + 1u) & 2u) c = -c;
+    }
+}
+
+// Rows of a thread in flight.
+constexpr int kFlight = 4;
 
 template <typename T, int V, bool kNeighbours>
 __global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ RotaryParams x, int inverse) {
-    __shared__ unsigned long long turns[LISA_MAX_PAIRS];
+    __shared__ uint2 turns[LISA_MAX_PAIRS];
     __shared__ int axis[LISA_MAX_PAIRS];
     if (threadIdx.x < LISA_MAX_PAIRS) {
-        turns[threadIdx.x] = x.turns[threadIdx.x];
+        turns[threadIdx.x] = make_uint2((unsigned)x.turns[threadIdx.x], (unsigned)(x.turns[threadIdx.x] >> 32));
         axis[threadIdx.x] = x.axis[threadIdx.x];
     }
     __syncthreads();
@@ -118,6 +153,25 @@ __global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ Rotar
     int i = (int)(at >> x.log_units);
     const int b = split(i, x.div_n);
     const bool turn = p0 < x.pairs;   // a vector is of one kind: V divides the pairs
+    // the vector's two parts: x and y of its pairs, or 2 V elements side by side
+    const int lo = kNeighbours || !turn ? 2 * p0 : p0, hi = kNeighbours || !turn ? 2 * p0 + V : x.pairs + p0;
+    const int r0 = blockIdx.y * x.share, r1 = min(r0 + x.share, x.rows);
+    Elements<T, V> u[kFlight], w[kFlight];
+    auto place = [&](const Tensor &q, const Tensor &k, int r) {
+        const bool key = r >= x.heads;
+        const Tensor &t = key ? k : q;
+        return static_cast<T *>(const_cast<void *>(t.p)) + b * t.sb + (long long)(key ? r - x.heads : r) * t.sh + i * t.st;
+    };
+    auto load = [&](int r) {
+#pragma unroll
+        for (int e = 0; e < kFlight; ++e) {
+            if (r + e >= r1) break;
+            const T *p = place(x.Q, x.K, r + e);
+            u[e].load(p + lo);
+            w[e].load(p + hi);
+        }
+    };
+    load(r0);   // on their way while the angles are found
     float s[V], c[V];
     if (turn) {
         int pos[LISA_MAX_AXES];
@@ -127,48 +181,36 @@ __global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ Rotar
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const int a = axis[p0 + e];
-            const int place = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
-            sin_cos<T>((unsigned long long)(long long)place * turns[p0 + e], s[e], c[e]);
+            sin_cos<T>(phase_of(a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3], turns[p0 + e]), s[e], c[e]);
             if (inverse) s[e] = -s[e];
         }
     }
-    // the vector's two parts: x and y of its pairs, or 2 V elements side by side
-    const int lo = kNeighbours || !turn ? 2 * p0 : p0, hi = kNeighbours || !turn ? 2 * p0 + V : x.pairs + p0;
-    const int r0 = blockIdx.y * x.share, r1 = min(r0 + x.share, x.rows);
-    for (int r = r0; r < r1; r += 4) {
-        Elements<T, V> u[4], w[4];
+    for (int r = r0;;) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (r + e >= r1) break;
-            const bool key = r + e >= x.heads;
-            const Tensor &t = key ? x.K : x.Q;
-            const T *p = static_cast<const T *>(t.p) + b * t.sb + (long long)(key ? r + e - x.heads : r + e) * t.sh + i * t.st;
-            u[e].load(p + lo);
-            w[e].load(p + hi);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kFlight; ++e) {
             if (r + e >= r1) break;
             if (turn) {
+                float f[V], g[V];
+                to_floats(u[e], f);
+                to_floats(w[e], g);
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
-                    // pair k: (a[k], d[k]), or elements 2 k and 2 k + 1 of the two parts together
-                    T &px = !kNeighbours ? u[e].v[k] : (2 * k < V ? u[e].v[2 * k < V ? 2 * k : 0] : w[e].v[2 * k >= V ? 2 * k - V : 0]);
-                    T &py = !kNeighbours ? w[e].v[k]
-                                         : (2 * k + 1 < V ? u[e].v[2 * k + 1 < V ? 2 * k + 1 : 0]
-                                                          : w[e].v[2 * k + 1 >= V ? 2 * k + 1 - V : 0]);
-                    const float vx = to_float(px), vy = to_float(py);
-                    from_float(px, fmaf(vx, c[k], -vy * s[k]));
-                    from_float(py, fmaf(vx, s[k], vy * c[k]));
+                    // pair k: (f[k], g[k]), or elements 2 k and 2 k + 1 of the two parts together
+                    float &px = !kNeighbours ? f[k] : 2 * k < V ? f[2 * k % V] : g[2 * k % V];
+                    float &py = !kNeighbours ? g[k] : 2 * k + 1 < V ? f[(2 * k + 1) % V] : g[(2 * k + 1) % V];
+                    const float vx = px, vy = py;
+                    px = fmaf(vx, c[k], -vy * s[k]);
+                    py = fmaf(vx, s[k], vy * c[k]);
                 }
+                from_floats(u[e], f);
+                from_floats(w[e], g);
             }
-            const bool key = r + e >= x.heads;
-            const Tensor &t = key ? x.Ko : x.Qo;
-            T *p = static_cast<T *>(const_cast<void *>(t.p)) + b * t.sb +
-                   (long long)(key ? r + e - x.heads : r + e) * t.sh + i * t.st;
+            T *p = place(x.Qo, x.Ko, r + e);
             u[e].store(p + lo);
             w[e].store(p + hi);
         }
+        if ((r += kFlight) >= r1) break;
+        load(r);
     }
 }
 
