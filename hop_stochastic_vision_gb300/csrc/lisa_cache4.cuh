@@ -6,16 +6,16 @@
 // the bf16 number 136 + code and a pair of codes 4 bits wide becomes a pair of
 // bf16 operands with one shift and one logic operation.  The codes stand in the
 // order in which the lanes (g = lane / 4, q = lane % 4) of the warp-level product
-// m16n8k16 want them:
-//   keys    B is [elements][tokens]; lane (g, q) supplies elements 8 q .. 8 q + 7 of
-//           every group for token g, one 32-bit word per group.  Within the word
-//           the pairs (i, i + 4) are rows 2 q, 2 q + 1 of a product (the queries'
-//           elements are taken in the same order).  Token t: word (q, group) at
+// m16n8k16 want them as its left side:
+//   keys    rows are tokens; lane (g, q) supplies elements 8 q .. 8 q + 7 of every
+//           group for token g, one 32-bit word per group.  Within the word the pairs
+//           (i, i + 4) are columns 2 q, 2 q + 1 of a product (the queries' elements
+//           are taken in the same order).  Token t: word (q, group) at
 //           t D / 2 + (q G + group) 4.
-//   values  B is [tokens][elements]; lane (g, q) supplies tokens 2 q, 2 q + 1 of
-//           elements 4 g .. 4 g + 3 of every group, one word per group: the even
-//           token's four codes below the odd one's, so the same shift gives the
-//           pair.  Tokens 2 t, 2 t + 1: word (g, group) at t 32 G + (g G + group) 4.
+//   values  rows are elements; lane (g, q) supplies elements 4 g .. 4 g + 3 of every
+//           group for tokens 2 q, 2 q + 1, one word per group: the even token's four
+//           codes below the odd one's, so the same shift gives the pair.  Tokens 2 t,
+//           2 t + 1: word (g, group) at t 32 G + (g G + group) 4.
 // Both are read as consecutive words of a warp, without bank conflicts.  A byte
 // belongs to one token, so tokens are stored without reading their neighbours.
 #pragma once

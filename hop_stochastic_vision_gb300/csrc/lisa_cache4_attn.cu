@@ -1,13 +1,13 @@
 // lisa_cache4_attn.cu -- attention of a few newest tokens over the 4-bit cache
 // (bf16 queries): one pass over the held codes.
 //
-// The rows that share a key head (its query heads times the queries) are the 16
-// rows of a warp-level product, so every code is read and unpacked once for all
-// of them.  A cluster of CTAs shares the pages of one (sequence, key head); a warp
-// walks every fourth page of its CTA's part with its own ring of asynchronous
-// copies (a page of one key head is one block of 4.5 KB), keeps the running
-// maximum, sum and output in registers, and the warps and then the CTAs of the
-// cluster join in a fixed order.
+// The rows that share a key head (its query heads times the queries) are the
+// columns of warp-level products, eight at a time, whose 16 rows are tokens (K Q^T)
+// or elements (V^T P^T), so every code is read and unpacked once for up to 16 rows.
+// A cluster of CTAs shares the pages of one (sequence, key head); a warp walks every
+// fourth page of its CTA's part with its own ring of asynchronous copies (a page of
+// one key head is one block of 4.5 KB), keeps the running maximum, sum and output in
+// registers, and the warps and then the CTAs of the cluster join in a fixed order.
 //
 // Scores and outputs without unpacking to values: with c the codes, sk and sv the
 // scales of token j's group u of 32 elements,
@@ -62,16 +62,17 @@ __device__ __forceinline__ void ld_words(uint32_t addr, uint32_t (&w)[G]) {
     else
         w[0] = ld_shared(addr);
 }
-// Scales of two tokens side by side: s[token][group].
+// A token's scales.
 template <int G>
-__device__ __forceinline__ void ld_scales(uint32_t addr, float (&s)[2][G]) {
-    uint32_t w[G];
-    ld_words<G>(addr, w);
+__device__ __forceinline__ void ld_scales(uint32_t addr, float (&s)[G]) {
     if constexpr (G == 2) {
-        s[0][0] = bf16_lo(w[0]); s[0][1] = bf16_hi(w[0]);
-        s[1][0] = bf16_lo(w[1]); s[1][1] = bf16_hi(w[1]);
+        const uint32_t w = ld_shared(addr);
+        s[0] = bf16_lo(w);
+        s[1] = bf16_hi(w);
     } else {
-        s[0][0] = bf16_lo(w[0]); s[1][0] = bf16_hi(w[0]);
+        uint16_t w;
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(addr) : "memory");
+        s[0] = bf16_lo(w);
     }
 }
 // The pair of codes at bits 4 i of both halves of a word, as the bf16 pair 136 + code.
@@ -82,18 +83,24 @@ __device__ __forceinline__ uint32_t without_offset(uint32_t pair) {
     return r;
 }
 
-// d = A B + (c0, c0, c1, c1): the rows' own first values.
+// d = A B + (c0, c1, c0, c1): the columns' own first values.
 __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1, float c0, float c1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
+// The 8 x 8 matrix of 16-bit elements that a warp holds as (row g, columns 2 q, 2 q + 1), transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 constexpr float kFarRef = 0x1p20f;
 
-// kHalves: 1 where at most 8 rows share a key head (the product's upper rows are idle), else 2.
-template <int D, int kHalves>
+// kTiles: of eight query rows, 1 or 2.
+template <int D, int kTiles>
 __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Params x) {
     using B = Block<D>;
     constexpr int G = B::G;
@@ -145,146 +152,174 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) load(s, s);
 
-    // query rows g and g + 8 of the tile: (head of the group, query), and the keys that each sees
-    int row[kHalves], qi[kHalves], head[kHalves], sees[kHalves];
-    uint32_t a[G][4][kHalves];   // pairs (i, i + 4) of elements 8 q4 .. 8 q4 + 7 of each group
-    float minus[G][kHalves];     // -136 times the sum of the group's elements
+    // Query row 8 e + g as the products' right side: pairs (i, i + 4) of elements 8 q4 .. 8 q4 + 7 of each group; rows
+    // 8 e + 2 q4 + c as their columns: the keys that each sees, and -136 times the sum of the group's elements.
+    uint32_t a[kTiles][G][4];
+    float minus[kTiles][G][2];
+    int sees[kTiles][2];
 #pragma unroll
-    for (int e = 0; e < kHalves; ++e) {
-        row[e] = rt * 16 + g + 8 * e;
-        qi[e] = row[e];
-        head[e] = kvh * p.group + split(qi[e], x.div_n);
-        sees[e] = len - (p.n - 1 - qi[e]);
-        const bool in = row[e] < x.rows;
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.Q.p) + (long long)b * p.Q.sb +
-                                 (long long)head[e] * p.Q.sh + (long long)qi[e] * p.Q.st + 8 * q4;
+    for (int e = 0; e < kTiles; ++e) {
+        const int row = rt * 16 + 8 * e + g;
+        int qi = row;
+        const int head = kvh * p.group + split(qi, x.div_n);
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.Q.p) + (long long)b * p.Q.sb + (long long)head * p.Q.sh +
+                                 (long long)qi * p.Q.st + 8 * q4;
 #pragma unroll
         for (int u = 0; u < G; ++u) {
-            const uint4 v = in ? *reinterpret_cast<const uint4 *>(q + kGroup * u) : make_uint4(0, 0, 0, 0);
-            a[u][0][e] = __byte_perm(v.x, v.z, 0x5410);
-            a[u][1][e] = __byte_perm(v.x, v.z, 0x7632);
-            a[u][2][e] = __byte_perm(v.y, v.w, 0x5410);
-            a[u][3][e] = __byte_perm(v.y, v.w, 0x7632);
+            const uint4 v = row < x.rows ? *reinterpret_cast<const uint4 *>(q + kGroup * u) : make_uint4(0, 0, 0, 0);
+            a[e][u][0] = __byte_perm(v.x, v.z, 0x5410);
+            a[e][u][1] = __byte_perm(v.x, v.z, 0x7632);
+            a[e][u][2] = __byte_perm(v.y, v.w, 0x5410);
+            a[e][u][3] = __byte_perm(v.y, v.w, 0x7632);
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum += bf16_lo(a[u][i][e]) + bf16_hi(a[u][i][e]);
+            for (int i = 0; i < 4; ++i) sum += bf16_lo(a[e][u][i]) + bf16_hi(a[e][u][i]);
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-            minus[u][e] = -136.f * sum;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) minus[e][u][c] = -136.f * __shfl_sync(0xFFFFFFFFu, sum, 4 * (2 * q4 + c));
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            int i = rt * 16 + 8 * e + 2 * q4 + c;
+            split(i, x.div_n);
+            sees[e][c] = len - (p.n - 1 - i);
         }
     }
     const float scale2 = p.scale * kLog2e;
-    float ref[kHalves], sum[kHalves], o[G][4][4];
+    // the running reference and sum (this lane's tokens) of the columns, and their outputs: elements 4 g + 2 m, + 1 of group u
+    float ref[kTiles][2], sum[kTiles][2], o[kTiles][G][2][4];
 #pragma unroll
-    for (int e = 0; e < kHalves; ++e) {
-        ref[e] = -INFINITY;
-        sum[e] = 0.f;
+    for (int e = 0; e < kTiles; ++e) {
+        ref[e][0] = ref[e][1] = -INFINITY;
+        sum[e][0] = sum[e][1] = 0.f;
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) o[e][u][m][0] = o[e][u][m][1] = o[e][u][m][2] = o[e][u][m][3] = 0.f;
     }
-#pragma unroll
-    for (int u = 0; u < G; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[u][j][0] = o[u][j][1] = o[u][j][2] = o[u][j][3] = 0.f;
 
     // one page: its keys from `j0`; not kWhole: some are behind what a row sees
     auto page = [&](uint32_t at, int j0, auto whole) __attribute__((always_inline)) {
         constexpr bool kWhole = decltype(whole)::value;
-        float s[8][2 * kHalves];
+        float s[kTiles][4][4];   // [..][j][2 h + c]: token 16 j + 8 h + g, column c
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t w[G];
-            ld_words<G>(at + B::key_word(8 * j + g, q4, 0), w);
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[2][G];
             float sk[2][G];
-            ld_scales<G>(at + B::off_ks + (8 * j + 2 * q4) * 2 * G, sk);
-            float acc[G][4];
-#pragma unroll
-            for (int u = 0; u < G; ++u) {
-                const uint32_t *l = a[u][0], *m = a[u][1], *n = a[u][2], *r = a[u][3];
-                constexpr bool kBoth = kHalves == 2;
-                mma_from(acc[u], l[0], kBoth ? l[kHalves - 1] : 0u, m[0], kBoth ? m[kHalves - 1] : 0u, code_pair(w[u], 0),
-                         code_pair(w[u], 1), minus[u][0], kBoth ? minus[u][kHalves - 1] : 0.f);
-                mma_bf16_16816(acc[u], n[0], kBoth ? n[kHalves - 1] : 0u, r[0], kBoth ? r[kHalves - 1] : 0u,
-                               code_pair(w[u], 2), code_pair(w[u], 3));
-            }
-#pragma unroll
-            for (int e = 0; e < kHalves; ++e)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    float v = acc[0][2 * e + t] * sk[t][0];
-                    if (G == 2) v = fmaf(acc[G - 1][2 * e + t], sk[t][G - 1], v);
-                    if (!kWhole) v = j0 + 8 * j + 2 * q4 + t < sees[e] ? v : -INFINITY;
-                    s[j][2 * e + t] = v;
-                }
-        }
-#pragma unroll
-        for (int e = 0; e < kHalves; ++e) {
-            float t = s[0][2 * e];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) t = fmaxf(t, fmaxf(s[j][2 * e], s[j][2 * e + 1]));
-            t *= scale2;
-            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
-            t = fmaxf(fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2)), ref[e]);
-            const float r = t == -INFINITY ? 0.f : t;   // nothing but -inf so far: weights 0, not NaN
-            const float f = ex2_approx(ref[e] - r);
-            ref[e] = t;
-            // The reference's rounding is common to a row's weights of this page and all others and goes out with the sum
-            // while it is small (2^20: an eighth); further out the scores are rounded as the reference was.
-            float mul = scale2;
-            if (__any_sync(0xFFFFFFFFu, fabsf(r) > kFarRef)) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s[j][2 * e] *= mul;
-                    s[j][2 * e + 1] *= mul;
-                }
-                mul = 1.f;
-            }
-            float part[2] = {0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    s[j][2 * e + u] = ex2_approx(fmaf(s[j][2 * e + u], mul, -r));
-                    part[u] += s[j][2 * e + u];
-                }
-            sum[e] = fmaf(sum[e], f, part[0] + part[1]);
-#pragma unroll
-            for (int u = 0; u < G; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    o[u][j][2 * e] *= f;
-                    o[u][j][2 * e + 1] *= f;
-                }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t w[G][4] = {};   // p sv of the step's 16 tokens, as the product's left side
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int j = 2 * k + h;
-                float sv[2][G];
-                ld_scales<G>(at + B::off_vs + (8 * j + 2 * q4) * 2 * G, sv);
+                ld_words<G>(at + B::key_word(16 * j + 8 * h + g, q4, 0), w[h]);
+                ld_scales<G>(at + B::off_ks + (16 * j + 8 * h + g) * 2 * G, sk[h]);
+            }
+            float acc[kTiles][G][4];
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                uint32_t c[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[h][i] = code_pair(w[h][u], i);
+#pragma unroll
+                for (int e = 0; e < kTiles; ++e) {
+                    mma_from(acc[e][u], c[0][0], c[1][0], c[0][1], c[1][1], a[e][u][0], a[e][u][1], minus[e][u][0], minus[e][u][1]);
+                    mma_bf16_16816(acc[e][u], c[0][2], c[1][2], c[0][3], c[1][3], a[e][u][2], a[e][u][3]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kTiles; ++e)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float v = acc[e][0][2 * h + c] * sk[h][0];
+                        if (G == 2) v = fmaf(acc[e][G - 1][2 * h + c], sk[h][G - 1], v);
+                        if (!kWhole) v = j0 + 16 * j + 8 * h + g < sees[e][c] ? v : -INFINITY;
+                        s[e][j][2 * h + c] = v;
+                    }
+        }
+#pragma unroll
+        for (int e = 0; e < kTiles; ++e)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float t = s[e][0][c];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) t = fmaxf(t, fmaxf(s[e][j][c], s[e][j][2 + c]));
+                t *= scale2;
+#pragma unroll
+                for (int m = 4; m < 32; m <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, m));
+                t = fmaxf(t, ref[e][c]);
+                const float r = t == -INFINITY ? 0.f : t;   // nothing but -inf so far: weights 0, not NaN
+                const float f = ex2_approx(ref[e][c] - r);
+                ref[e][c] = t;
+                // The reference's rounding is common to a row's weights of this page and all others and goes out with the
+                // sum while it is small (2^20: an eighth); further out the scores are rounded as the reference was.
+                float mul = scale2;
+                if (__any_sync(0xFFFFFFFFu, fabsf(r) > kFarRef)) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[e][j][c] *= mul;
+                        s[e][j][2 + c] *= mul;
+                    }
+                    mul = 1.f;
+                }
+                float part[2] = {0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        s[e][j][2 * h + c] = ex2_approx(fmaf(s[e][j][2 * h + c], mul, -r));
+                        part[h] += s[e][j][2 * h + c];
+                    }
+                sum[e][c] = fmaf(sum[e][c], f, part[0] + part[1]);
 #pragma unroll
                 for (int u = 0; u < G; ++u)
 #pragma unroll
-                    for (int e = 0; e < kHalves; ++e) {
+                    for (int m = 0; m < 2; ++m) {
+                        o[e][u][m][c] *= f;
+                        o[e][u][m][2 + c] *= f;
+                    }
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // p sv of the step's 16 tokens as the product's right side: columns are rows of P, transposed
+            uint32_t w[kTiles][G][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int token = 16 * j + 8 * h + g;
+                float sv[G];
+                ld_scales<G>(at + B::off_vs + token * 2 * G, sv);
+#pragma unroll
+                for (int e = 0; e < kTiles; ++e)
+#pragma unroll
+                    for (int u = 0; u < G; ++u) {
                         float v[2];
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            v[t] = s[j][2 * e + t] * sv[t][u];
+                        for (int c = 0; c < 2; ++c) {
+                            v[c] = s[e][j][2 * h + c] * sv[u];
                             // behind what the row sees a scale may be anything
-                            if (!kWhole && j0 + 8 * j + 2 * q4 + t >= sees[e]) v[t] = 0.f;
+                            if (!kWhole && j0 + token >= sees[e][c]) v[c] = 0.f;
                         }
-                        w[u][2 * h + e] = pack_bf16(v[0], v[1]);
+                        w[e][u][h] = transposed(pack_bf16(v[0], v[1]));
                     }
             }
             uint32_t lo[G], hi[G];
-            ld_words<G>(at + B::off_v + B::value_half(16 * k + 2 * q4, g, 0), lo);
-            ld_words<G>(at + B::off_v + B::value_half(16 * k + 8 + 2 * q4, g, 0), hi);
+            ld_words<G>(at + B::off_v + B::value_half(16 * j + 2 * q4, g, 0), lo);
+            ld_words<G>(at + B::off_v + B::value_half(16 * j + 8 + 2 * q4, g, 0), hi);
 #pragma unroll
-            for (int u = 0; u < G; ++u)
+            for (int u = 0; u < G; ++u) {
+                uint32_t c[2][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mma_bf16_16816(o[u][j], w[u][0], w[u][1], w[u][2], w[u][3], without_offset(code_pair(lo[u], j)),
-                                   without_offset(code_pair(hi[u], j)));
+                for (int i = 0; i < 4; ++i) {
+                    c[0][i] = without_offset(code_pair(lo[u], i));
+                    c[1][i] = without_offset(code_pair(hi[u], i));
+                }
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < kTiles; ++e)
+                        mma_bf16_16816(o[e][u][m], c[0][2 * m], c[0][2 * m + 1], c[1][2 * m], c[1][2 * m + 1], w[e][u][0], w[e][u][1]);
+            }
         }
     };
     const int all_see = len - (p.n - 1);   // keys that every row of the sequence sees
@@ -309,23 +344,23 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
     constexpr int kPitch = D + 4;
     float *part = reinterpret_cast<float *>(sm) + warp * 16 * kPitch;
     float *joined = reinterpret_cast<float *>(sm) + kWarps * 16 * kPitch;
-    constexpr int kRows = 8 * kHalves;
+    constexpr int kRows = 8 * kTiles;
 #pragma unroll
-    for (int e = 0; e < kHalves; ++e) {
-        sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
-        sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
-        if (q4 == 0) {
-            stat_s[warp][0][g + 8 * e] = ref[e];
-            stat_s[warp][1][g + 8 * e] = sum[e];
+    for (int e = 0; e < kTiles; ++e)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int r = 8 * e + 2 * q4 + c;
+#pragma unroll
+            for (int m = 4; m < 32; m <<= 1) sum[e][c] += __shfl_xor_sync(0xFFFFFFFFu, sum[e][c], m);
+            if (g == 0) {
+                stat_s[warp][0][r] = ref[e][c];
+                stat_s[warp][1][r] = sum[e][c];
+            }
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+                *reinterpret_cast<float4 *>(part + r * kPitch + kGroup * u + 4 * g) =
+                    make_float4(o[e][u][0][c], o[e][u][0][2 + c], o[e][u][1][c], o[e][u][1][2 + c]);
         }
-        // column 2 q4 of the products is element 8 q4 + j of the group, column 2 q4 + 1 element 8 q4 + 4 + j
-#pragma unroll
-        for (int u = 0; u < G; ++u)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                *reinterpret_cast<float4 *>(part + (g + 8 * e) * kPitch + kGroup * u + 8 * q4 + 4 * t) =
-                    make_float4(o[u][0][2 * e + t], o[u][1][2 * e + t], o[u][2][2 * e + t], o[u][3][2 * e + t]);
-    }
     __syncthreads();
     const int cl = x.splits;
     for (int e = tid; e < kRows * (D / 4); e += kThreads) {
@@ -402,9 +437,9 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
     if (cl > 1) cluster_sync();   // no CTA leaves while its results are being read
 }
 
-template <int D, int kHalves>
+template <int D, int kTiles>
 cudaError_t go(const Params &x, cudaStream_t s) {
-    cudaError_t e = allow_smem<attention<D, kHalves>>();
+    cudaError_t e = allow_smem<attention<D, kTiles>>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[2];
@@ -419,7 +454,7 @@ cudaError_t go(const Params &x, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = x.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attention<D, kHalves>, x);
+    return cudaLaunchKernelEx(&cfg, attention<D, kTiles>, x);
 }
 
 }  // namespace
