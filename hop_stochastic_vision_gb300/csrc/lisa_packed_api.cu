@@ -5,6 +5,8 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include <cuda_runtime.h>
 
@@ -47,20 +49,85 @@ void each_unit(const Batch &b, int pass, F f) {
     }
 }
 
-// Steps of a part.  Units go to kSms workers, the longest first, each to the one
-// with the least to do.  That evens out while the longest unit is below an even
-// share of the whole; where it is not, units are cut into parts of at most half
-// a share, of four steps at least (a part's sums go through memory).
+// The workers with the least to do first, of equals the lowest.
+struct Workers {
+    struct Worker { long long load; int id; } heap[kSms];
+    Workers() {
+        for (int w = 0; w < kSms; ++w) heap[w] = {0, w};
+    }
+    static bool before(const Worker &a, const Worker &c) { return a.load < c.load || (a.load == c.load && a.id < c.id); }
+    // Gives the next item to the first; returns who that was.
+    int take(long long cost) {
+        const int id = heap[0].id;
+        heap[0].load += cost;
+        for (int at = 0;;) {   // sift down
+            int least = at;
+            for (int c = 2 * at + 1; c <= 2 * at + 2 && c < kSms; ++c)
+                if (before(heap[c], heap[least])) least = c;
+            if (least == at) return id;
+            std::swap(heap[at], heap[least]);
+            at = least;
+        }
+    }
+    long long most() const {
+        long long x = 0;
+        for (const Worker &w : heap) x = std::max(x, w.load);
+        return x;
+    }
+};
+constexpr int kItemCost = 1;   // an item's start and end, in steps
+constexpr int kJoinCost = 5;   // the join's launch and its copies through memory
+
+// Part k of `parts` of a unit's steps.
+inline int part_begin(int steps, int parts, int k) { return (int)((long long)steps * k / parts); }
+
+// The steps of a part at most.  Units go to kSms workers, the longest first, each
+// to the one with the least to do.  Where that leaves some with much more than an
+// even share, units may be cut into parts that leave their sums in memory for a
+// join.  A handful of part sizes around the share is tried out; what takes the
+// busiest worker the least, the join counted, is kept.  (4096 causal tokens of 12
+// heads, forward: parts of half a share throughout 52 us; see the table of cases.)
 int part_steps(const Batch &b, int pass) {
-    long long sum = 0;
+    constexpr int kMinPart = 4, kMaxTried = 8192;
+    long long sum = 0, units = 0;
     int longest = 0;
     each_unit(b, pass, [&](int, int, int, int steps) {
         sum += steps;
+        ++units;
         longest = std::max(longest, steps);
     });
-    const long long share = (sum * b.heads_of(pass) + kSms - 1) / kSms;
-    if (longest <= std::max<long long>(share, 4)) return longest;
-    return (int)std::max<long long>((share + 1) / 2, 4);
+    const int heads = b.heads_of(pass);
+    const long long share = (sum * heads + kSms - 1) / kSms;
+    if (longest <= kMinPart || heads == 0) return longest;
+    // so many items that they even out unless one outdoes the share by itself
+    if (units * heads > kMaxTried) return longest <= share ? longest : (int)std::max<long long>(share, kMinPart);
+    const std::unique_ptr<int[]> cost(new (std::nothrow) int[units * (kMaxTried / heads / units + 1)]);
+    if (!cost) return longest;
+    int best = longest;
+    long long least = -1;
+    for (const double part : {0.0, 1.0, 0.67, 0.5, 0.33}) {
+        const int most = part == 0.0 ? longest : (int)std::max<long long>(std::llround(share * part), kMinPart);
+        if (part != 0.0 && most >= longest) continue;
+        long long n = 0;
+        each_unit(b, pass, [&](int, int, int, int steps) {
+            const int parts = (steps + most - 1) / most;
+            n += parts;
+            if (n * heads <= kMaxTried)
+                for (int k = 0; k < parts; ++k)
+                    cost[n - parts + k] = part_begin(steps, parts, k + 1) - part_begin(steps, parts, k);
+        });
+        if (n * heads > kMaxTried) continue;
+        std::sort(cost.get(), cost.get() + n, [](int x, int y) { return x > y; });
+        Workers workers;
+        for (long long e = 0; e < n; ++e)
+            for (int h = 0; h < heads; ++h) workers.take(cost[e] + kItemCost);
+        const long long time = workers.most() + (n > units ? kJoinCost : 0);
+        if (least < 0 || time < least) {
+            least = time;
+            best = most;
+        }
+    }
+    return best;
 }
 
 struct Counts {
@@ -78,8 +145,8 @@ Counts each_item(const Batch &b, int pass, I item, J join) {
             ++n.joins;
         }
         for (int k = 0; k < parts; ++k) {
-            const int t0 = (int)((long long)steps * k / parts), t1 = (int)((long long)steps * (k + 1) / parts);
-            item(Item{row0, len, first, t0, t1, parts > 1 ? n.parts++ : -1, steps, 0});
+            item(Item{row0, len, first, part_begin(steps, parts, k), part_begin(steps, parts, k + 1),
+                      parts > 1 ? n.parts++ : -1, steps, 0});
             ++n.items;
         }
     });
@@ -129,25 +196,12 @@ bool measure(const Batch &b, lisa_packed &out, size_t &bytes) {
     return true;
 }
 
-// (item, head) pairs to the workers: each to the one with the least to do, of equals the lowest.
+// (item, head) pairs to the workers: each to the one with the least to do.
 template <typename F>
 void deal(const Item *items, int n, int heads, F f) {
-    struct Worker { long long load; int id; } heap[kSms];
-    for (int w = 0; w < kSms; ++w) heap[w] = {0, w};
-    const auto before = [](const Worker &a, const Worker &c) { return a.load < c.load || (a.load == c.load && a.id < c.id); };
+    Workers workers;
     for (int e = 0; e < n; ++e)
-        for (int h = 0; h < heads; ++h) {
-            f(heap[0].id, e * heads + h);
-            heap[0].load += items[e].t1 - items[e].t0 + 1;   // one for an item's start and end
-            for (int at = 0;;) {   // sift down
-                int least = at;
-                for (int c = 2 * at + 1; c <= 2 * at + 2 && c < kSms; ++c)
-                    if (before(heap[c], heap[least])) least = c;
-                if (least == at) break;
-                std::swap(heap[at], heap[least]);
-                at = least;
-            }
-        }
+        for (int h = 0; h < heads; ++h) f(workers.take(items[e].t1 - items[e].t0 + kItemCost), e * heads + h);
 }
 
 // A number that changes with any of the struct's sizes (FNV-1a over them).

@@ -145,28 +145,42 @@ def lisa_cache4_attention(cache, Q, qs, O, os, lse, lens, B, heads, n, scale, dt
 
 
 # -- tensors of a call ------------------------------------------------------------------
+# What a call's shapes and strides come to in the ABI's terms is worked out once for
+# each combination; types, devices and addresses are looked at in every call.
 
-@functools.lru_cache(maxsize=4096)
 def _strides_of(shape, stride) -> lisa_strides:
     """Strides of [.., heads, tokens, d], 3-d or 4-d; one that no step uses may be anything legal."""
     d = shape[-1]
     if stride[-1] != 1 and d > 1:
         raise ValueError("the elements of a token must be contiguous (last stride 1)")
+    if max(shape) >> 31:      # the call itself refuses far less, if it gets to see it
+        raise LisaError(LISA_ERR_UNSUPPORTED)
     used = tuple(t if s > 1 else d for s, t in zip(shape[:-1], stride[:-1]))
     return lisa_strides(*((0,) + used if len(used) == 2 else used))
 
 
-def _strides(t, name, dims, dtype, index) -> lisa_strides:
-    if t.dtype != dtype or dtype not in _DTYPES:
-        raise ValueError("%s must be of the call's type, float32 or bfloat16" % name)
-    if t.dim() not in dims:
-        raise ValueError("%s must have %s dimensions" % (name, " or ".join(map(str, dims))))
-    at = t.get_device()
-    if at != index or at < 0:
-        raise ValueError("these operators run on CUDA tensors only" if at < 0 else "tensors must be on one device")
-    if max(t.shape) >> 31:      # the call itself refuses far less, if it gets to see it
-        raise LisaError(LISA_ERR_UNSUPPORTED)
-    return _strides_of(tuple(t.shape), t.stride())
+_cached_strides = functools.lru_cache(maxsize=4096)(_strides_of)
+
+
+def _fresh_strides(shape) -> lisa_strides:
+    """Strides of a new contiguous tensor."""
+    out, step = [1], 1
+    for s in shape[:0:-1]:
+        step *= max(s, 1)
+        out.append(step)
+    return _strides_of(shape, tuple(reversed(out)))
+
+
+def _check(dtype, index, *tensors) -> None:
+    """The call's tensors are of its type and on its device."""
+    if dtype not in _DTYPES:
+        raise ValueError("the tensors must be float32 or bfloat16")
+    for t in tensors:
+        if t.dtype != dtype:
+            raise ValueError("a tensor is %s, the call %s" % (t.dtype, dtype))
+        at = t.get_device()
+        if at != index or at < 0:
+            raise ValueError("these operators run on CUDA tensors only" if at < 0 else "tensors must be on one device")
 
 
 # -- rotary positions ---------------------------------------------------------------------
@@ -206,51 +220,65 @@ class RotaryAxes:
                                        (ctypes.c_double * LISA_MAX_PAIRS)(*frequencies))
 
 
-def _rotary(stream, q, k, qs, ks, positions, where, rule, out, inverse):
+@functools.lru_cache(maxsize=1024)
+def _rotary_sizes(d, axes, q_shape, q_stride, k_shape, k_stride, p_shape, p_stride):
+    """(strides of q, k, new q', new k'), (axis stride, batch stride, B, heads, kv_heads, n, d)."""
+    if len(q_shape) not in (3, 4):
+        raise ValueError("q must have 3 or 4 dimensions")
+    n, B = q_shape[-2], q_shape[0] if len(q_shape) == 4 else 1
+    if q_shape[-1] != d:
+        raise ValueError("the rule is of width %d, q of %d" % (d, q_shape[-1]))
+    if k_shape is not None and (len(k_shape) != len(q_shape) or k_shape[:-3] != q_shape[:-3] or k_shape[-2:] != q_shape[-2:]):
+        raise ValueError("k must be [B, kv_heads, n, d] for q [B, heads, n, d]")
+    batch = 0
+    if p_shape != (axes, n):
+        if p_shape != (axes, B, n) or len(q_shape) != 4:
+            raise ValueError("positions must be [%d, %d] or [%d, %d, %d]" % (axes, n, axes, B, n))
+        batch = p_stride[1] if B > 1 else 0
+    if n > 1 and p_stride[-1] != 1:
+        raise ValueError("the positions of an axis must be contiguous")
+    k_like = (None, None) if k_shape is None else (_strides_of(k_shape, k_stride), _fresh_strides(k_shape))
+    return ((_strides_of(q_shape, q_stride), k_like[0], _fresh_strides(q_shape), k_like[1]),
+            (p_stride[0] if axes > 1 else 0, batch, B, q_shape[-3], 0 if k_shape is None else k_shape[-3], n, d))
+
+
+def _rotary(stream, q, k, strides, positions, sizes, rule, out, inverse):
+    qs, ks, qos, kos = strides
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
-    qo, ko = out
-    index = q.get_device()
-    qos = _strides(qo, "out", (q.dim(),), q.dtype, index)
-    kos = None if k is None else _strides(ko, "out", (q.dim(),), q.dtype, index)
-    B, heads, n, d = q.shape if q.dim() == 4 else (1,) + tuple(q.shape)
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ko = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    else:
+        qo, ko = out
+        qos = _cached_strides(qo.shape, qo.stride())
+        kos = None if k is None else _cached_strides(ko.shape, ko.stride())
     status = _library().lisa_rotary(q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, qo.data_ptr(), qos,
-                                    None if k is None else ko.data_ptr(), kos, positions.data_ptr(), *where, B, heads,
-                                    0 if k is None else k.shape[-3], n, d, rule.struct, inverse, _DTYPES[q.dtype],
-                                    stream)
+                                    None if k is None else ko.data_ptr(), kos, positions.data_ptr(), *sizes, rule.struct,
+                                    inverse, _DTYPES[q.dtype], stream)
     if status != LISA_OK:
         raise LisaError(status)
     return qo if k is None else (qo, ko)
 
 
 def _turn(q, k, positions, rule, out, stream, inverse):
-    index = q.get_device()
-    qs = _strides(q, "q", (3, 4), q.dtype, index)
-    ks = None if k is None else _strides(k, "k", (q.dim(),), q.dtype, index)
-    d, n = q.shape[-1], q.shape[-2]
-    B = q.shape[0] if q.dim() == 4 else 1
-    if d != rule.d:
-        raise ValueError("the rule is of width %d, q of %d" % (rule.d, d))
-    if k is not None and (k.shape[:-3] != q.shape[:-3] or k.shape[-2:] != q.shape[-2:]):
-        raise ValueError("k must be [B, kv_heads, n, d] for q [B, heads, n, d]")
+    index, dtype = q.get_device(), q.dtype
+    if k is None:
+        _check(dtype, index, q)
+        k_shape = k_stride = None
+    else:
+        _check(dtype, index, q, k)
+        k_shape, k_stride = k.shape, k.stride()
     if positions.get_device() != index or positions.dtype != torch.int32:
         raise ValueError("positions must be an int32 CUDA tensor on q's device")
-    shape, stride = tuple(positions.shape), positions.stride()
-    if shape == (rule.axes, n):
-        where = (stride[0] if rule.axes > 1 else 0, 0)
-    elif shape == (rule.axes, B, n) and q.dim() == 4:
-        where = (stride[0] if rule.axes > 1 else 0, stride[1] if B > 1 else 0)
-    else:
-        raise ValueError("positions must be [%d, %d] or [%d, %d, %d]" % (rule.axes, n, rule.axes, B, n))
-    if n > 1 and stride[-1] != 1:
-        raise ValueError("the positions of an axis must be contiguous")
+    strides, sizes = _rotary_sizes(rule.d, rule.axes, q.shape, q.stride(), k_shape, k_stride, positions.shape,
+                                   positions.stride())
     if out is not None:
-        if k is None:
-            out = (out, None)
+        out = (out, None) if k is None else out
+        _check(dtype, index, out[0])
+        if k is not None:
+            _check(dtype, index, out[1])
         if out[0].shape != q.shape or (k is not None and out[1].shape != k.shape):
             raise ValueError("out must have the shapes of q and k")
-    return _run(index, stream, _rotary, q, k, qs, ks, positions, where, rule, out, inverse)
+    return _run(index, stream, _rotary, q, k, strides, positions, sizes, rule, out, inverse)
 
 
 def rotary(q: torch.Tensor, k, positions: torch.Tensor, rule: RotaryAxes, *, out=None, stream=None):
@@ -307,19 +335,27 @@ class PackedSequences:
         return self._bytes[key]
 
 
+@functools.lru_cache(maxsize=1024)
+def _packed_strides(heads, kv_heads, tokens, q_shape, q_stride, k_shape, k_stride, v_shape, v_stride):
+    """Strides of q, k, v, of a new tensor like q and like k."""
+    if len(q_shape) != 3 or q_shape[0] != heads or k_shape != (kv_heads,) + q_shape[1:] or v_shape != k_shape:
+        raise ValueError("q must be [%d, tokens, d], k and v [%d, tokens, d] for these sequences" % (heads, kv_heads))
+    if q_shape[1] < tokens:
+        raise ValueError("the sequences have %d tokens, the tensors %d" % (tokens, q_shape[1]))
+    return (_strides_of(q_shape, q_stride), _strides_of(k_shape, k_stride), _strides_of(v_shape, v_stride),
+            _fresh_strides(q_shape), _fresh_strides(k_shape))
+
+
 def _packed_args(q, k, v, seqs, scale):
     index, dtype = q.get_device(), q.dtype
-    qs, ks, vs = (_strides(t, name, (3,), dtype, index) for t, name in ((q, "q"), (k, "k"), (v, "v")))
-    heads, tokens, d = q.shape
-    if heads != seqs.heads or k.shape != (seqs.kv_heads, tokens, d) or v.shape != k.shape:
-        raise ValueError("q must be [%d, tokens, d], k and v [%d, tokens, d] for these sequences"
-                         % (seqs.heads, seqs.kv_heads))
-    if tokens < seqs.tokens:
-        raise ValueError("the sequences have %d tokens, the tensors %d" % (seqs.tokens, tokens))
+    _check(dtype, index, q, k, v)
+    qs, ks, vs, *fresh = _packed_strides(seqs.heads, seqs.kv_heads, seqs.tokens, q.shape, q.stride(), k.shape, k.stride(),
+                                         v.shape, v.stride())
     if seqs.index != index:
         raise ValueError("tensors must be on one device")
-    scale = _default_scale(d) if scale is None else float(scale)
-    return index, (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs), (seqs.struct, d, scale, _DTYPES[dtype])
+    d = q.shape[2]
+    return (index, (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs),
+            (seqs.struct, d, _default_scale(d) if scale is None else float(scale), _DTYPES[dtype]), fresh)
 
 
 def _fresh(shape, dtype, device, seqs):
@@ -328,10 +364,11 @@ def _fresh(shape, dtype, device, seqs):
     return make(shape, dtype=dtype, device=device)
 
 
-def _prompt_forward(stream, q, head, tail, seqs, return_lse, out, workspace):
+def _prompt_forward(stream, q, head, tail, fresh, seqs, return_lse, out, workspace):
     if out is None:
-        out = _fresh(q.shape, q.dtype, q.device, seqs)
-    os = _strides(out, "out", (3,), q.dtype, q.get_device())
+        out, os = _fresh(q.shape, q.dtype, q.device, seqs), fresh[0]
+    else:
+        os = _cached_strides(out.shape, out.stride())
     lse = _fresh(q.shape[:2], torch.float32, q.device, seqs) if return_lse else None
     keep, ws, nbytes = _workspace(workspace, seqs.workspace_bytes(tail[1], tail[3]), q.device)
     status = _library().lisa_prompt_attention(*head, out.data_ptr(), os, lse.data_ptr() if return_lse else None,
@@ -351,21 +388,20 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqs: Pa
     tokens, d] (a new contiguous tensor, 0 behind the sequences, unless ``out`` is
     given, which is left as it was there), with ``return_lse`` also the fp32
     log-sum-exp [heads, tokens] that the backward pass reads."""
-    index, head, tail = _packed_args(q, k, v, seqs, scale)
-    if out is not None and out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    return _run(index, stream, _prompt_forward, q, head, tail, seqs, return_lse, out, workspace)
+    index, head, tail, fresh = _packed_args(q, k, v, seqs, scale)
+    if out is not None:
+        _check(q.dtype, index, out)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    return _run(index, stream, _prompt_forward, q, head, tail, fresh, seqs, return_lse, out, workspace)
 
 
-def _prompt_backward(stream, q, k, head, saved, tail, seqs, workspace):
+def _prompt_backward(stream, q, k, head, saved, tail, fresh, seqs, workspace):
     dq = _fresh(q.shape, q.dtype, q.device, seqs)
     dk, dv = (_fresh(k.shape, q.dtype, q.device, seqs) for _ in range(2))
-    index = q.get_device()
-    grads = []
-    for t in (dq, dk, dv):
-        grads += [t.data_ptr(), _strides(t, "gradients", (3,), q.dtype, index)]
     keep, ws, nbytes = _workspace(workspace, seqs.workspace_bytes(tail[1], tail[3], True), q.device)
-    status = _library().lisa_prompt_attention_backward(*head, *saved, *grads, *tail, ws, nbytes, stream)
+    status = _library().lisa_prompt_attention_backward(*head, *saved, dq.data_ptr(), fresh[0], dk.data_ptr(), fresh[1],
+                                                       dv.data_ptr(), fresh[1], *tail, ws, nbytes, stream)
     del keep
     if status != LISA_OK:
         raise LisaError(status)
@@ -376,15 +412,16 @@ def prompt_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                               dout: torch.Tensor, seqs: PackedSequences, *, scale=None, workspace=None, stream=None):
     """Gradients (dq, dk, dv) of ``prompt_attention`` for the upstream gradient
     ``dout``, given the forward's ``out`` and ``lse``; 0 behind the sequences."""
-    index, head, tail = _packed_args(q, k, v, seqs, scale)
+    index, head, tail, fresh = _packed_args(q, k, v, seqs, scale)
+    _check(q.dtype, index, out, dout)
     if out.shape != q.shape or dout.shape != q.shape:
         raise ValueError("out and dout must have q's shape")
     if not (lse.get_device() == index and lse.dtype == torch.float32 and lse.is_contiguous()
             and lse.shape == q.shape[:2]):
         raise ValueError("lse must be the forward's contiguous fp32 tensor [heads, tokens]")
-    saved = (out.data_ptr(), _strides(out, "out", (3,), q.dtype, index), lse.data_ptr(), q.shape[1], dout.data_ptr(),
-             _strides(dout, "dout", (3,), q.dtype, index))
-    return _run(index, stream, _prompt_backward, q, k, head, saved, tail, seqs, workspace)
+    saved = (out.data_ptr(), _cached_strides(out.shape, out.stride()), lse.data_ptr(), q.shape[1], dout.data_ptr(),
+             _cached_strides(dout.shape, dout.stride()))
+    return _run(index, stream, _prompt_backward, q, k, head, saved, tail, fresh, seqs, workspace)
 
 
 # -- the cache in 4 bits -------------------------------------------------------------------
@@ -417,39 +454,44 @@ class Cache4:
                            table.stride(0) if sequences > 1 else 0)
 
 
-def _places(cache, positions, sequences):
-    """(B, n, address, address, stride) of tokens given by positions [B, n], or [tokens] with their sequences."""
-    for t in (positions, sequences):
-        if t is not None and not (t.get_device() == cache.index and t.dtype == torch.int32):
-            raise ValueError("positions and sequences must be int32 CUDA tensors on the cache's device")
-    packed = positions.dim() == 1
-    if positions.dim() not in (1, 2) or packed != (sequences is not None):
+@functools.lru_cache(maxsize=1024)
+def _place_sizes(kv_heads, d, shape, stride, packed):
+    """Shape of k and v, strides of new ones, (stride, B, n) of tokens at positions of this shape."""
+    if len(shape) not in (1, 2) or packed != (len(shape) == 1):
         raise ValueError("positions must be [B, n], or [tokens] with the tokens' sequences")
-    if sequences is not None and (sequences.shape != positions.shape or sequences.stride() != positions.stride()):
-        raise ValueError("sequences must be laid out like the positions")
-    n = positions.shape[-1]
-    if n > 1 and positions.stride(-1) != 1:
+    n = shape[-1]
+    if n > 1 and stride[-1] != 1:
         raise ValueError("the positions of an entry must be contiguous")
-    B = 1 if packed else positions.shape[0]
-    return (B, n, positions.data_ptr(), None if sequences is None else sequences.data_ptr(),
-            positions.stride(0) if B > 1 and not packed else 0)
+    B = 1 if packed else shape[0]
+    like = (kv_heads, n, d) if packed else (B, kv_heads, n, d)
+    return like, _fresh_strides(like), (stride[0] if B > 1 else 0, B, n)
+
+
+def _places(cache, positions, sequences):
+    """(shape of k and v, strides of new ones, the ABI's arguments) of the tokens of a call."""
+    index = cache.index
+    if positions.get_device() != index or positions.dtype != torch.int32:
+        raise ValueError("positions must be an int32 CUDA tensor on the cache's device")
+    if sequences is not None:
+        if sequences.get_device() != index or sequences.dtype != torch.int32:
+            raise ValueError("sequences must be an int32 CUDA tensor on the cache's device")
+        if sequences.shape != positions.shape or sequences.stride() != positions.stride():
+            raise ValueError("sequences must be laid out like the positions")
+    like, fresh, sizes = _place_sizes(cache.kv_heads, cache.d, positions.shape, positions.stride(), sequences is not None)
+    return like, fresh, (positions.data_ptr(), None if sequences is None else sequences.data_ptr()) + sizes
 
 
 def _cache_call(stream, call, struct, k, v, ks, vs, places):
-    B, n, at, sequences, stride = places
-    status = call(struct, k.data_ptr(), ks, v.data_ptr(), vs, at, sequences, stride, B, n, _DTYPES[k.dtype], stream)
+    status = call(struct, k.data_ptr(), ks, v.data_ptr(), vs, *places, _DTYPES[k.dtype], stream)
     if status != LISA_OK:
         raise LisaError(status)
 
 
-def _cache_tensors(cache, k, v, positions):
-    dims = (positions.dim() + 2,)
-    ks, vs = (_strides(t, name, dims, k.dtype, cache.index) for t, name in ((k, "k"), (v, "v")))
-    shape = (cache.kv_heads, positions.shape[-1], cache.d)
-    shape = shape if positions.dim() == 1 else (positions.shape[0],) + shape
-    if k.shape != shape or v.shape != shape:
-        raise ValueError("k and v must be %s for these positions" % (list(shape),))
-    return ks, vs
+def _cache_tensors(cache, k, v, like):
+    _check(k.dtype, cache.index, k, v)
+    if k.shape != like or v.shape != like:
+        raise ValueError("k and v must be %s for these positions" % (list(like),))
+    return _cached_strides(k.shape, k.stride()), _cached_strides(v.shape, v.stride())
 
 
 def cache_store(cache: Cache4, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, positions: torch.Tensor,
@@ -459,18 +501,21 @@ def cache_store(cache: Cache4, k: torch.Tensor, v: torch.Tensor, table: torch.Te
     tokens [kv_heads, tokens, d] at positions [tokens] of ``sequences`` [tokens].  A
     position below 0 or beyond the table, or without a page, stores nothing; those
     that a sequence gets in one call have to differ."""
-    places = _places(cache, positions, sequences)
-    ks, vs = _cache_tensors(cache, k, v, positions)
+    like, _, places = _places(cache, positions, sequences)
+    ks, vs = _cache_tensors(cache, k, v, like)
     _run(cache.index, stream, _cache_call, _library().lisa_cache4_store, cache.struct(table), k, v, ks, vs, places)
 
 
-def _cache_read(stream, cache, struct, shape, dtype, out, positions, places):
+def _cache_read(stream, cache, struct, like, dtype, out, fresh, places):
     if out is None:
         device = cache.store.device
-        out = tuple(torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
-    ks, vs = _cache_tensors(cache, *out, positions)
-    _cache_call(stream, _library().lisa_cache4_read, struct, *out, ks, vs, places)
-    return out
+        k, v = torch.empty(like, dtype=dtype, device=device), torch.empty(like, dtype=dtype, device=device)
+        ks = vs = fresh
+    else:
+        k, v = out
+        ks, vs = _cache_tensors(cache, k, v, like)
+    _cache_call(stream, _library().lisa_cache4_read, struct, k, v, ks, vs, places)
+    return k, v
 
 
 def cache_read(cache: Cache4, table: torch.Tensor, positions: torch.Tensor, sequences: torch.Tensor = None, *,
@@ -480,17 +525,25 @@ def cache_read(cache: Cache4, table: torch.Tensor, positions: torch.Tensor, sequ
     token."""
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32 or bfloat16")
-    places = _places(cache, positions, sequences)
-    shape = (cache.kv_heads, positions.shape[-1], cache.d)
-    shape = shape if positions.dim() == 1 else (positions.shape[0],) + shape
-    return _run(cache.index, stream, _cache_read, cache, cache.struct(table), shape, dtype, out, positions, places)
+    like, fresh, places = _places(cache, positions, sequences)
+    return _run(cache.index, stream, _cache_read, cache, cache.struct(table), like, dtype, out, fresh, places)
 
 
-def _cache_attention(stream, q, qs, cache, struct, lens, scale, return_lse, out):
+@functools.lru_cache(maxsize=1024)
+def _attention_strides(d, q_shape, q_stride):
+    """Strides of q and of a new tensor like it."""
+    if len(q_shape) != 4 or q_shape[3] != d:
+        raise ValueError("q must be [B, heads, n, %d]" % d)
+    return _strides_of(q_shape, q_stride), _fresh_strides(q_shape)
+
+
+def _cache_attention(stream, q, strides, struct, lens, scale, return_lse, out):
     B, heads, n, _ = q.shape
+    qs, os = strides
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    os = _strides(out, "out", (4,), q.dtype, cache.index)
+    else:
+        os = _cached_strides(out.shape, out.stride())
     lse = torch.empty((B, heads, n), dtype=torch.float32, device=q.device) if return_lse else None
     status = _library().lisa_cache4_attention(struct, q.data_ptr(), qs, out.data_ptr(), os,
                                               lse.data_ptr() if return_lse else None, lens.data_ptr(), B, heads, n,
@@ -507,15 +560,17 @@ def cache_attention(q: torch.Tensor, cache: Cache4, table: torch.Tensor, lens: t
     ``lens`` [B] tokens (int32), and query i the tokens up to its own, lens - n + i.
     ``scale`` defaults to 1 / sqrt(d).  Returns O like q, with ``return_lse`` also
     the fp32 log-sum-exp [B, heads, n]."""
-    qs = _strides(q, "q", (4,), torch.bfloat16, cache.index)
-    B, heads, n, d = q.shape
-    if d != cache.d:
-        raise ValueError("the cache is of width %d, q of %d" % (cache.d, d))
+    index = cache.index
+    _check(torch.bfloat16, index, q)
+    strides = _attention_strides(cache.d, q.shape, q.stride())
     struct = cache.struct(table)
-    if table.shape[0] != B or not (lens.get_device() == cache.index and lens.dtype == torch.int32
-                                   and lens.is_contiguous() and lens.shape == (B,)):
+    B, d = q.shape[0], cache.d
+    if table.shape[0] != B or not (lens.get_device() == index and lens.dtype == torch.int32 and lens.is_contiguous()
+                                   and lens.shape == (B,)):
         raise ValueError("lens must be a contiguous int32 CUDA tensor [B], and the table have B rows")
-    if out is not None and out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    return _run(cache.index, stream, _cache_attention, q, qs, cache, struct, lens,
+    if out is not None:
+        _check(torch.bfloat16, index, out)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    return _run(index, stream, _cache_attention, q, strides, struct, lens,
                 _default_scale(d) if scale is None else float(scale), return_lse, out)

@@ -336,3 +336,8 @@ def test_empty_caches_launch_nothing():
         assert _tokens(call, K=0, V=0, positions=0, n=0) == OK
     assert _attend(Q=0, O=0, lens=0, **none) == OK and _attend(Q=0, O=0, lens=0, n=0) == OK
     assert _attend(Q=0, O=0, lens=0, heads=0) == OK
+
+
+def test_a_plan_without_heads():
+    packed = _packed((5000,), heads=0, kv=0)
+    assert list(packed.parts) == [0, 0, 0]

@@ -92,10 +92,10 @@ def test_many_sequences(lisa, dtype, causal):
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("lengths,heads,kv", [([2000], 1, 1), ([1500, 3, 900], 2, 1), ([1030, 40], 6, 2)])
 def test_long_sequences_of_few_heads(lisa, causal, lengths, heads, kv):
-    """Units cut into parts, in every pass."""
+    """Units cut into parts: in the pass over the keys for all of these, in all three for the first two."""
     c = Case(lisa, BF16, lengths, heads, kv, 64, causal=causal, seed=5)
     s = c.seqs.struct
-    assert all(s.parts[p] > 0 for p in range(3))
+    assert s.parts[2] > 0 and (heads > 2 or (s.parts[0] > 0 and s.parts[1] > 0))
     c.check()
     Case(lisa, BF16, lengths, heads, kv, 32, causal=causal, seed=6, layout="tokens").check()
 
