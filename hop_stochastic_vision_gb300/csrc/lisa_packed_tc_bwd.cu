@@ -13,9 +13,12 @@
 // owner: no atomics, no fp32 dQ in memory, the same bits every time.  A unit cut
 // into parts leaves its sums in memory for a join that adds them in order.
 //
-// Four warpgroups share a tile by columns, 32 each, a thread per row.  The threads
-// take S and dP into registers as soon as both are there, so the next tile's
-// products run under this tile's arithmetic.
+// Four warpgroups share a tile by columns, 32 each, a thread per row.  Two of them
+// with their 64 columns are a group that has barriers and products of its own, so
+// the groups drift apart and one is in its exponentials while the other waits or
+// loads; the products are issued in one order whatever the groups do.  The threads
+// take S and dP into registers as soon as both are there, so the group's next
+// products run under this one's arithmetic.
 //
 // Tiles are loaded from wherever the sequence begins, so a tile may hold tokens of
 // the next one.  Their weights and dS are set to 0 whatever the products say, and
@@ -31,6 +34,8 @@ constexpr int kMathWarps = kMath / 32;
 constexpr int kThreads = kMath + 128;   // behind them: products (two warps), loads, a helper
 constexpr int kFront = kMathWarps, kLoads = kMathWarps + 1, kBack = kMathWarps + 2, kHelper = kMathWarps + 3;
 constexpr int kStrip = 32;         // columns of a thread's row
+constexpr int kGroups = 2, kGroupWarps = kMathWarps / kGroups, kGroupCols = kRows / kGroups;
+constexpr uint32_t kGroupRows = kGroupCols * 128 / 16;   // a group's rows of a tile, in descriptor units
 constexpr uint32_t kPair = 2 * kTileBytes / 16;   // a ring stage of two tiles, in descriptor units
 constexpr int kSlots = 2;          // items' own tiles held
 constexpr int kDqStages = 3, kDkvStages = 3;
@@ -56,6 +61,19 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(bar));
 }
+// [128 x 64] (+)= A (tensor memory, 128 x k) * B (k token rows); k a multiple of 16, at most a group's columns.
+__device__ __forceinline__ void mma_group_rows(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, int k, bool accumulate) {
+    constexpr uint32_t idesc = make_idesc_bf16(128, 64, false, true);
+    if (k == kGroupCols) {
+#pragma unroll
+        for (int ks = 0; ks < kGroupCols / 16; ++ks) tc_mma_ta(d_tmem, a_tmem + ks * 8, b + 128 * ks, idesc, ks > 0 || accumulate);
+    } else {
+        for (int ks = 0; ks < k / 16; ++ks) tc_mma_ta(d_tmem, a_tmem + ks * 8, b + 128 * ks, idesc, ks > 0 || accumulate);
+    }
+}
+// Columns of a group among the `cols` of a tile; 0: it has nothing to do there.
+__device__ __forceinline__ int group_cols(int cols, int group) { return min(max(cols - group * kGroupCols, 0), kGroupCols); }
+
 __device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
 
 // The loading thread waits for the last use of every slot, so nothing arrives on the CTA's barriers once it has gone.
@@ -69,7 +87,8 @@ __device__ __forceinline__ int uses_of(int total, int slot, int stages) {
 // ------------------------------------------------------------------------ dQ
 struct DqBars {
     uint64_t q_full[kSlots], q_empty[kSlots], kv_full[kDqStages], kv_empty[kDqStages];
-    uint64_t full, free, ds_full, dq_done;   // S and dP of a tile: there, in registers
+    uint64_t full[kGroups], free[kGroups], ds_full[kGroups], dq_done[kGroups];   // S and dP: there, in registers
+    uint64_t out_full, out_read;   // the item's dQ: there, in registers
 };
 constexpr int kDqSmem = (3 * kSlots + 2 * kDqStages) * kTileBytes + 1024;
 
@@ -98,10 +117,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bar.kv_full[s]), 1);
             mbar_init(smem_u32(&bar.kv_empty[s]), 1);
         }
-        mbar_init(smem_u32(&bar.full), 1);
-        mbar_init(smem_u32(&bar.dq_done), 1);
-        mbar_init(smem_u32(&bar.free), kMathWarps);
-        mbar_init(smem_u32(&bar.ds_full), kMathWarps);
+        for (int g = 0; g < kGroups; ++g) {
+            mbar_init(smem_u32(&bar.full[g]), 1);
+            mbar_init(smem_u32(&bar.dq_done[g]), 1);
+            mbar_init(smem_u32(&bar.free[g]), kGroupWarps);
+            mbar_init(smem_u32(&bar.ds_full[g]), kGroupWarps);
+        }
+        mbar_init(smem_u32(&bar.out_full), 1);
+        mbar_init(smem_u32(&bar.out_read), kMathWarps);
         dead = 0;
         fence_mbar_init();
     }
@@ -145,8 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == kFront) {
-        // S and dP of each tile
-        int kt = 0;
+        // S and dP of each tile, group by group
+        int ns[kGroups] = {0, 0};
         Cursor c, cq;
         const uint64_t q0 = desc_rows(qd), k0 = desc_rows(ring), v0 = desc_rows(ring + kTileBytes);
         for (int k = walk.begin; k < walk.end; ++k) {
@@ -155,43 +178,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_on(smem_u32(&bar.q_full[qs]), cq.phase, guard, kErrTimeoutLoad);
             cq.next(kSlots);
             const uint64_t qa = q0 + (uint32_t)qs * (3 * kTileBytes / 16), da = qa + kTileBytes / 16;
-            for (int j = w.t0; j < w.t1; ++j, ++kt, c.next(kDqStages)) {
+            for (int j = w.t0; j < w.t1; ++j, c.next(kDqStages)) {
                 const int s = c.slot, cols = tile_cols(tile_rows(w.len, j * kRows));
                 wait_on(smem_u32(&bar.kv_full[s]), c.phase, guard, kErrTimeoutLoad);
-                if (kt > 0) wait_on(smem_u32(&bar.free), (kt - 1) & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                if (elect_one()) {
-                    mma_rows_rows(tS, qa, k0 + (uint32_t)s * kPair, cols);
-                    mma_rows_rows(tP, da, v0 + (uint32_t)s * kPair, cols);
-                    tc_commit(smem_u32(&bar.full));
-                    if (j == w.t1 - 1) tc_commit(smem_u32(&bar.q_empty[qs]));
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int mine = group_cols(cols, g);
+                    if (mine == 0) break;
+                    if (ns[g] > 0) wait_on(smem_u32(&bar.free[g]), (ns[g] - 1) & 1, guard, kErrTimeoutMma);
+                    ++ns[g];
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = (uint32_t)s * kPair + g * kGroupRows;
+                        mma_rows_rows(tS + g * kGroupCols, qa, k0 + at, mine);
+                        mma_rows_rows(tP + g * kGroupCols, da, v0 + at, mine);
+                        tc_commit(smem_u32(&bar.full[g]));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (j == w.t1 - 1) {
+                    if (elect_one()) tc_commit(smem_u32(&bar.q_empty[qs]));
+                    __syncwarp();
+                }
             }
         }
     } else if (warp == kBack) {
         // dQ += dS K.  S and dP have read the K and V tiles: dS comes of them.
-        int kt = 0;
+        int ns[kGroups] = {0, 0};
         Cursor c;
         const uint64_t kt0 = desc_tokens(ring);
         for (int k = walk.begin; k < walk.end; ++k) {
             const Work w = walk.at(k);
-            for (int j = w.t0; j < w.t1; ++j, ++kt, c.next(kDqStages)) {
-                wait_on(smem_u32(&bar.ds_full), kt & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
+            if (k > walk.begin) wait_on(smem_u32(&bar.out_read), (k - walk.begin - 1) & 1, guard, kErrTimeoutMma);
+            for (int j = w.t0; j < w.t1; ++j, c.next(kDqStages)) {
+                const int cols = tile_cols(tile_rows(w.len, j * kRows));
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int mine = group_cols(cols, g);
+                    if (mine == 0) break;
+                    wait_on(smem_u32(&bar.ds_full[g]), ns[g]++ & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        mma_group_rows(tDq, tDs + g * (kGroupCols / 2), kt0 + (uint32_t)c.slot * kPair + g * kGroupRows, mine,
+                                       j > w.t0 || g > 0);
+                        tc_commit(smem_u32(&bar.dq_done[g]));
+                    }
+                    __syncwarp();
+                }
                 if (elect_one()) {
-                    mma_weights_rows(tDq, tDs, kt0 + (uint32_t)c.slot * kPair, tile_cols(tile_rows(w.len, j * kRows)), j > w.t0);
-                    tc_commit(smem_u32(&bar.dq_done));
                     tc_commit(smem_u32(&bar.kv_empty[c.slot]));
+                    if (j == w.t1 - 1) tc_commit(smem_u32(&bar.out_full));
                 }
                 __syncwarp();
             }
         }
     } else {
-        const int strip = warp >> 2, c0 = kStrip * strip, wt = tid & 127;
+        const int strip = warp >> 2, group = warp / kGroupWarps, c0 = kStrip * strip, wt = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
-        int kt = 0;
+        int kt = 0, ns = 0;   // tiles so far, and of those the group's
         Cursor cq;
         // the row's lse of a pair of the list, as it is in memory (a use would wait for it)
         auto lse_of = [&](int k) {
@@ -238,12 +283,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int rows = tile_rows(w.len, j * kRows), cols = tile_cols(rows);
                 const bool diagonal = p.causal && j * kRows == w.first;
                 const int keys = (diagonal ? min(rows, wt + 1) : rows) - c0;   // of this strip, that the row sees
+                if (group_cols(cols, group) == 0) {   // the other group has all of the tile
+                    if (single) {
+                        reinterpret_cast<float2 *>(sm + (3 * cq.slot + 2) * kTileBytes)[strip * kRows + wt] = make_float2(0.f, 0.f);
+                        math_barrier();
+                    }
+                    continue;
+                }
                 float s[kStrip], dp[kStrip];
-                wait_on(smem_u32(&bar.full), kt & 1, guard, kErrTimeoutMma);
+                wait_on(smem_u32(&bar.full[group]), ns & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 load_strips(tS + c0 + lanes, s, tP + c0 + lanes, dp);
                 tc_fence_before();
-                arrive_warp(&bar.free, lane);
+                arrive_warp(&bar.free[group], lane);
 #pragma unroll
                 for (int c = 0; c < kStrip; c += 2) fma2(s[c], s[c + 1], s[c], s[c + 1], scale2, scale2, nl, nl);
                 if (diagonal || rows < kRows) {   // dP of keys behind the last one holds whatever their values hold
@@ -289,25 +341,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // the previous dS has been read
-                if (kt > 0) wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
+                if (ns > 0) wait_on(smem_u32(&bar.dq_done[group]), (ns - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 tmem_st16(tDs + c0 / 2 + lanes, ds);
-                if (strip == 0 && rows < cols && w.row0 + w.len < p.tokens) {
-                    // S is done with the tile: what the next sequence holds may not meet dS = 0
+                if (strip == 2 * group && rows < cols && cols <= (group + 1) * kGroupCols && w.row0 + w.len < p.tokens) {
+                    // S is done with the group's keys: what the next sequence holds may not meet dS = 0
                     zero_rows(ring + 2 * (kt % kDqStages) * kTileBytes, rows, cols, wt);
                     fence_proxy_async();
                 }
                 tc_wait_st();
                 tc_fence_before();
-                arrive_warp(&bar.ds_full, lane);
+                arrive_warp(&bar.ds_full[group], lane);
+                ++ns;
             }
             if (strip == 0 && in && w.t0 == 0) p.delta[(size_t)w.h * p.tokens + w.row0 + i] = delta;
-            wait_on(smem_u32(&bar.dq_done), (kt - 1) & 1, guard, kErrTimeoutMma);
+            wait_on(smem_u32(&bar.out_full), (k - walk.begin) & 1, guard, kErrTimeoutMma);
             tc_fence_after();
             float o[16];
             tmem_ld16_nowait(tDq + 16 * strip + lanes, o);
             tc_wait_ld();
             tc_fence_before();
+            arrive_warp(&bar.out_read, lane);
             if (w.part < 0) {
                 // staged where the item's O was: its last reader was delta, before every warp's dS
                 store_rows_bf16<16>(qd + (3 * cq.slot + 2) * kTileBytes + (uint32_t)warp * 1024u, o, p.scale,
@@ -335,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct DkvBars {
     uint64_t kv_full[kSlots], kv_empty[kSlots], q_full[kDkvStages], q_empty[kDkvStages];
     uint64_t aux_full[kDkvStages], aux_empty[kDkvStages];
-    uint64_t full, free, w_full, w_done;   // S and dP: there, in registers; P and dS: there, read
+    uint64_t full[kGroups], free[kGroups], w_full[kGroups], w_done[kGroups];   // S and dP: there, in registers; P and dS: there, read
+    uint64_t out_full, out_read;   // the item's dV and dK: there, in registers
 };
 // What the arithmetic needs of a tile's queries, one entry per column.
 struct QueryAux {
@@ -392,10 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bar.aux_full[s]), 1);
             mbar_init(smem_u32(&bar.aux_empty[s]), kMathWarps);
         }
-        mbar_init(smem_u32(&bar.full), 1);
-        mbar_init(smem_u32(&bar.w_done), 1);
-        mbar_init(smem_u32(&bar.free), kMathWarps);
-        mbar_init(smem_u32(&bar.w_full), kMathWarps);
+        for (int g = 0; g < kGroups; ++g) {
+            mbar_init(smem_u32(&bar.full[g]), 1);
+            mbar_init(smem_u32(&bar.w_done[g]), 1);
+            mbar_init(smem_u32(&bar.free[g]), kGroupWarps);
+            mbar_init(smem_u32(&bar.w_full[g]), kGroupWarps);
+        }
+        mbar_init(smem_u32(&bar.out_full), 1);
+        mbar_init(smem_u32(&bar.out_read), kMathWarps);
         dead = 0;
         fence_mbar_init();
     }
@@ -458,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == kFront) {
-        // S^T and dP^T of each tile
-        int n = 0;
+        // S^T and dP^T of each tile, group by group
+        int ns[kGroups] = {0, 0};
         Cursor c, ck;
         const uint64_t k0 = desc_rows(kv), v0 = desc_rows(kv + kTileBytes), q0 = desc_rows(ring),
                        d0 = desc_rows(ring + kTileBytes);
@@ -470,62 +529,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             ck.next(kSlots);
             const uint64_t ka = k0 + (uint32_t)ks * kPair, va = v0 + (uint32_t)ks * kPair;
             Steps st(w, p.group, p.causal);
-            for (int u = w.t0; u < w.t1; ++u, ++n, c.next(kDkvStages), st.next()) {
+            for (int u = w.t0; u < w.t1; ++u, c.next(kDkvStages), st.next()) {
                 const int s = c.slot, cols = tile_cols(tile_rows(w.len, st.qt * kRows));
                 wait_on(smem_u32(&bar.q_full[s]), c.phase, guard, kErrTimeoutLoad);
-                if (n > 0) wait_on(smem_u32(&bar.free), (n - 1) & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
-                if (elect_one()) {
-                    mma_rows_rows(tS, ka, q0 + (uint32_t)s * kPair, cols);
-                    mma_rows_rows(tD, va, d0 + (uint32_t)s * kPair, cols);
-                    tc_commit(smem_u32(&bar.full));
-                    if (u == w.t1 - 1) tc_commit(smem_u32(&bar.kv_empty[ks]));
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int mine = group_cols(cols, g);
+                    if (mine == 0) break;
+                    if (ns[g] > 0) wait_on(smem_u32(&bar.free[g]), (ns[g] - 1) & 1, guard, kErrTimeoutMma);
+                    ++ns[g];
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = (uint32_t)s * kPair + g * kGroupRows;
+                        mma_rows_rows(tS + g * kGroupCols, ka, q0 + at, mine);
+                        mma_rows_rows(tD + g * kGroupCols, va, d0 + at, mine);
+                        tc_commit(smem_u32(&bar.full[g]));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (u == w.t1 - 1) {
+                    if (elect_one()) tc_commit(smem_u32(&bar.kv_empty[ks]));
+                    __syncwarp();
+                }
             }
         }
     } else if (warp == kBack) {
         // dV += P^T dO, dK += dS^T Q.  S^T and dP^T have read the tiles too: P and dS come of them.
-        int n = 0;
+        int ns[kGroups] = {0, 0};
         Cursor c;
         const uint64_t qt0 = desc_tokens(ring), dt0 = desc_tokens(ring + kTileBytes);
         for (int k = walk.begin; k < walk.end; ++k) {
             const Work w = walk.at(k);
             Steps st(w, p.group, p.causal);
-            for (int u = w.t0; u < w.t1; ++u, ++n, c.next(kDkvStages), st.next()) {
+            if (k > walk.begin) wait_on(smem_u32(&bar.out_read), (k - walk.begin - 1) & 1, guard, kErrTimeoutMma);
+            for (int u = w.t0; u < w.t1; ++u, c.next(kDkvStages), st.next()) {
                 const int s = c.slot, cols = tile_cols(tile_rows(w.len, st.qt * kRows));
-                wait_on(smem_u32(&bar.w_full), n & 1, guard, kErrTimeoutMma);
-                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int mine = group_cols(cols, g);
+                    if (mine == 0) break;
+                    wait_on(smem_u32(&bar.w_full[g]), ns[g]++ & 1, guard, kErrTimeoutMma);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = (uint32_t)s * kPair + g * kGroupRows;
+                        const bool add = u > w.t0 || g > 0;
+                        mma_group_rows(tDv, tPw + g * (kGroupCols / 2), dt0 + at, mine, add);
+                        mma_group_rows(tDk, tDs + g * (kGroupCols / 2), qt0 + at, mine, add);
+                        tc_commit(smem_u32(&bar.w_done[g]));
+                    }
+                    __syncwarp();
+                }
                 if (elect_one()) {
-                    mma_weights_rows(tDv, tPw, dt0 + (uint32_t)s * kPair, cols, u > w.t0);
-                    mma_weights_rows(tDk, tDs, qt0 + (uint32_t)s * kPair, cols, u > w.t0);
-                    tc_commit(smem_u32(&bar.w_done));
                     tc_commit(smem_u32(&bar.q_empty[s]));
+                    if (u == w.t1 - 1) tc_commit(smem_u32(&bar.out_full));
                 }
                 __syncwarp();
             }
         }
     } else {
-        const int strip = warp >> 2, c0 = kStrip * strip, wt = tid & 127;
+        const int strip = warp >> 2, group = warp / kGroupWarps, c0 = kStrip * strip, wt = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float scale2 = p.scale * kLog2e;
-        int n = 0;
+        int ns = 0;   // the group's tiles so far
         Cursor ca;
         for (int k = walk.begin; k < walk.end; ++k) {
             const Work w = walk.at(k);
             const int j = w.first + wt;
             Steps st(w, p.group, p.causal);
-            for (int u = w.t0; u < w.t1; ++u, ++n, ca.next(kDkvStages), st.next()) {
+            for (int u = w.t0; u < w.t1; ++u, ca.next(kDkvStages), st.next()) {
                 const int rows = tile_rows(w.len, st.qt * kRows), cols = tile_cols(rows);
                 const bool diagonal = p.causal && st.qt * kRows == w.first;
                 const QueryAux &a = aux[ca.slot];
-                float s[kStrip], dp[kStrip];
                 wait_on(smem_u32(&bar.aux_full[ca.slot]), ca.phase, guard, kErrTimeoutLoad);
-                wait_on(smem_u32(&bar.full), n & 1, guard, kErrTimeoutMma);
+                if (group_cols(cols, group) == 0) {   // the other group has all of the tile
+                    arrive_warp(&bar.aux_empty[ca.slot], lane);
+                    continue;
+                }
+                float s[kStrip], dp[kStrip];
+                wait_on(smem_u32(&bar.full[group]), ns & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 load_strips(tS + c0 + lanes, s, tD + c0 + lanes, dp);
                 tc_fence_before();
-                arrive_warp(&bar.free, lane);
+                arrive_warp(&bar.free[group], lane);
 #pragma unroll
                 for (int c = 0; c < kStrip; c += 4) {
                     const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
@@ -558,13 +643,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ds[(e >> 1) + 1] = pack_bf16(dp[e + 2], dp[e + 3]);
                 }
                 // the previous P and dS have been read
-                if (n > 0) wait_on(smem_u32(&bar.w_done), (n - 1) & 1, guard, kErrTimeoutMma);
+                if (ns > 0) wait_on(smem_u32(&bar.w_done[group]), (ns - 1) & 1, guard, kErrTimeoutMma);
+                ++ns;
                 tc_fence_after();
                 tmem_st16(tPw + c0 / 2 + lanes, pw);
                 tmem_st16(tDs + c0 / 2 + lanes, ds);
-                if (strip < 2 && rows < cols && w.row0 + w.len < p.tokens) {
-                    // S and dP are done with the tiles: what the next sequence holds may not meet weights of 0
-                    zero_rows(ring + (2 * ca.slot + strip) * kTileBytes, rows, cols, wt);
+                if (rows < cols && cols <= (group + 1) * kGroupCols && w.row0 + w.len < p.tokens) {
+                    // S and dP are done with the group's queries: what the next sequence holds may not meet weights of 0
+                    // (the group's first strip has the tile of Q, the second that of dO)
+                    zero_rows(ring + (2 * ca.slot + (strip & 1)) * kTileBytes, rows, cols, wt);
                     fence_proxy_async();
                 }
                 tc_wait_st();
@@ -572,17 +659,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&bar.aux_empty[ca.slot]));
-                    mbar_arrive(smem_u32(&bar.w_full));
+                    mbar_arrive(smem_u32(&bar.w_full[group]));
                 }
             }
             // ---- strips 0, 1 store dV, 2 and 3 dK, 32 columns each
             float o[kStrip];
             const int dk = strip >> 1, oc = kStrip * (strip & 1);
-            wait_on(smem_u32(&bar.w_done), (n - 1) & 1, guard, kErrTimeoutMma);
+            wait_on(smem_u32(&bar.out_full), (k - walk.begin) & 1, guard, kErrTimeoutMma);
             tc_fence_after();
             tmem_ld32_nowait((dk ? tDk : tDv) + oc + lanes, o);
             tc_wait_ld();
             tc_fence_before();
+            arrive_warp(&bar.out_read, lane);
             if (w.part < 0) {
                 const Tensor &t = dk ? p.dK : p.dV;
                 const int r0 = j - lane;
