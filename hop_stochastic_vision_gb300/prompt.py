@@ -245,8 +245,8 @@ def _rotary_sizes(d, axes, q_shape, q_stride, k_shape, k_stride, p_shape, p_stri
 def _rotary(stream, q, k, strides, positions, sizes, rule, out, inverse):
     qs, ks, qos, kos = strides
     if out is None:
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        ko = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
     else:
         qo, ko = out
         qos = _cached_strides(qo.shape, qo.stride())
@@ -302,7 +302,8 @@ class PackedSequences:
     other along the tokens, and how the work on them is shared out for ``heads``
     query heads on ``kv_heads`` key heads; ``causal``: a query reads the keys up to
     itself, else all of its sequence.  Made once for a batch, for every layer and
-    every captured graph that has it; making it copies a table to ``device``."""
+    every captured graph that has it; making it copies a table to ``device``, which a
+    capture does not allow."""
 
     def __init__(self, lengths, heads: int, kv_heads: int = None, *, causal: bool = True, device="cuda"):
         lengths = [_int32(x) for x in lengths]
@@ -317,11 +318,11 @@ class PackedSequences:
                                       ctypes.byref(self.struct))
         if status != LISA_OK:
             raise LisaError(status)
-        self.table = table.to(device)
-        if not self.table.is_cuda:
+        self._table = table.to(device)
+        if not self._table.is_cuda:
             raise ValueError("a packed batch lives on a CUDA device")
-        self.index = self.table.get_device()
-        self.struct.plan = self.table.data_ptr()
+        self.index = self._table.get_device()
+        self.struct.plan = self._table.data_ptr()
         self.lengths, self.tokens = tuple(lengths), self.struct.tokens
         self.heads, self.kv_heads, self.causal = heads, kv_heads, bool(causal)
         self._bytes = {}
@@ -437,6 +438,7 @@ class Cache4:
         nbytes = lisa_cache4_bytes(self.pages, self.kv_heads, self.d)
         if nbytes == 0 and not (self.pages == 0 or self.kv_heads == 0):
             raise LisaError(LISA_ERR_UNSUPPORTED)
+        self._bytes = nbytes
         self.store = torch.zeros(nbytes, dtype=torch.uint8, device=device)
         if not self.store.is_cuda:
             raise ValueError("a cache lives on a CUDA device")
@@ -444,6 +446,10 @@ class Cache4:
 
     def struct(self, table: torch.Tensor) -> lisa_cache4:
         """The C struct of the cache with this table."""
+        store = self.store
+        if not (store.get_device() == self.index and store.dtype == torch.uint8 and store.is_contiguous()
+                and store.numel() == self._bytes):
+            raise ValueError("the cache's store must stay a contiguous uint8 CUDA tensor of %d bytes" % self._bytes)
         if not (table.get_device() == self.index and table.dtype == torch.int32 and table.dim() == 2
                 and (table.shape[1] <= 1 or table.stride(1) == 1)):
             raise ValueError("the table must be an int32 CUDA tensor [sequences, width] on the cache's device")
@@ -541,7 +547,7 @@ def _cache_attention(stream, q, strides, struct, lens, scale, return_lse, out):
     B, heads, n, _ = q.shape
     qs, os = strides
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         os = _cached_strides(out.shape, out.stride())
     lse = torch.empty((B, heads, n), dtype=torch.float32, device=q.device) if return_lse else None

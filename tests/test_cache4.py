@@ -220,7 +220,7 @@ def test_the_newest_tokens_see_up_to_themselves(lisa, n, heads, kv, d):
     Check(k, v, q, lens).against(out, lse)
 
 
-@pytest.mark.parametrize("B,heads,kv,m", [(1, 2, 1, 9000), (2, 4, 4, 5000), (40, 4, 2, 1000)])
+@pytest.mark.parametrize("B,heads,kv,m", [(1, 2, 1, 9000), (2, 4, 4, 5000), (40, 4, 2, 1000), (1, 3, 1, 70000)])
 def test_long_caches(lisa, B, heads, kv, m):
     """Pages shared out over a cluster, more of them for a warp than it looks up at once."""
     lens = [m - 37 * b % m for b in range(B)]
@@ -291,6 +291,24 @@ def test_empty_calls(lisa):
     assert not out.any() and (lse == -math.inf).all()
 
 
+def test_pages_behind_four_gigabytes(lisa):
+    """A pool of 5 GB: tokens in its first and last pages."""
+    pages, kv, d = 280000, 4, 64
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB of device memory")
+    cache = lisa.Cache4(pages, kv, d)
+    assert cache.store.numel() > 1 << 32
+    k, v, q = rand(1, kv, 150, d, seed=1), rand(1, kv, 150, d, seed=2), rand(1, 8, 1, d, seed=3)
+    table = torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32, device="cuda")
+    at = torch.arange(150, dtype=torch.int32, device="cuda")[None]
+    lisa.cache_store(cache, k.cuda(), v.cuda(), table, at)
+    for x, y in zip((k, v), lisa.cache_read(cache, table, at)):
+        assert torch.equal(stands_for(x)[0].to(BF16), y.cpu())
+    out, lse = lisa.cache_attention(q.cuda(), cache, table, torch.tensor([150], dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    Check(k, v, q, [150]).against(out, lse)
+
+
 def test_streams_and_graphs(lisa):
     """A captured step: the new token into the cache, then attention over it; the length grows between replays."""
     B, kv, m, d = 3, 2, 200, 64
@@ -356,6 +374,9 @@ def test_refusals(lisa):
         lisa.cache_attention(q, cache, table, lens, out=q)
     with pytest.raises(lisa.LisaError):
         lisa.cache_attention(q, cache, table, lens, scale=-1.0)
+    cache.store = cache.store[:-1]
+    with pytest.raises(ValueError):
+        lisa.cache_attention(q, cache, table, lens)                    # another store than the cache's own
     for bad in ((4, 2, 16), (4, 2, 128), (-1, 2, 64), (1 << 25, 1, 32)):
         with pytest.raises(lisa.LisaError):
             lisa.Cache4(*bad)

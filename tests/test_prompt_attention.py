@@ -192,6 +192,24 @@ def test_repeated_keys_of_all_heads(lisa):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_tokens_far_apart(lisa, dtype):
+    """Offsets beyond 32 bits: tokens 2^26 elements apart, so the last ones behind 2^31."""
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB of device memory")
+    lengths, heads, d, apart = [9, 30], 2, 32, 1 << 26
+    c = Case(lisa, dtype, lengths, heads, 1, d, seed=3)
+    wide = torch.empty(39 * apart, dtype=dtype, device="cuda")
+    for name, first, h in (("q", 0, heads), ("k", 4096, 1), ("v", 8192, 1), ("do", 12288, heads)):
+        view = wide.as_strided((h, 39, d), (64, apart, 1), first)
+        view.copy_(getattr(c, name))
+        setattr(c, name, view)
+    given = torch.empty_like(c.q, memory_format=torch.contiguous_format)
+    c.check()
+    assert torch.equal(c.forward(out=given)[0], c.forward()[0])
+    del view
+
+
 def test_other_streams_and_captured_graphs(lisa):
     lengths = [260, 100, 0, 900]
     c = Case(lisa, BF16, lengths, 4, 2, 64)

@@ -1,0 +1,150 @@
+"""The operators around a prompt as they are used together, on the GPU: a packed
+prompt of images and text, trained; then answered token by token from the cache
+in 4 bits; beside the cross attention over the same tokens."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+HEADS, KV, D = 6, 2, 64
+
+
+@pytest.fixture(scope="module")
+def lisa():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from hop_stochastic_vision_gb300 import build, lisa as binding
+    build.build()
+    binding.load()
+    return binding
+
+
+def _rand(*shape, seed):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed))
+
+
+def _places(lengths):
+    """(time, row, column) of every packed token: a sequence begins with an image of 5 columns, text goes on in time."""
+    out = []
+    for L in lengths:
+        i = torch.arange(L)
+        image = min(L, 35)
+        t = torch.where(i < image, 0, i - image + 1)
+        out.append(torch.stack((t, torch.where(i < image, i // 5, t), torch.where(i < image, i % 5, t))))
+    return torch.cat(out, 1).int()
+
+
+def _turned(x, places, rule, sections):
+    """x [heads, tokens, D] in 64 bits, turned by its definition (neighbouring elements)."""
+    axis = [a for a, s in enumerate(sections) for _ in range(s)]
+    angle = torch.stack([places[a].double() * f for a, f in zip(axis, rule.frequencies)], -1)
+    z = torch.view_as_complex(x.unflatten(-1, (-1, 2)).contiguous()) * torch.polar(torch.ones_like(angle), angle)
+    return torch.view_as_real(z).flatten(-2)
+
+
+def _attend(q, k, v, causal_from=0):
+    """Softmax attention of the newest rows of q over k, v [.., m, D], 64 bits."""
+    n, m = q.shape[-2], k.shape[-2]
+    s = q @ k.transpose(-1, -2) / math.sqrt(D)
+    seen = torch.arange(m)[None, :] <= torch.arange(m - n, m)[:, None]
+    return torch.softmax(torch.where(seen, s, -math.inf), -1) @ v
+
+
+def _close(got, want, steps):
+    """Within `steps` roundings of bf16, half a step of 2^-8 each, of the largest value of a token's head."""
+    off = (got.double().cpu() - want).abs().amax(-1)
+    assert bool((off <= steps * 2.0 ** -8 * want.abs().amax(-1).clamp(min=0.05)).all()), float(off.max())
+
+
+def test_a_training_step(lisa):
+    """Rotary positions and prompt attention, forward and backward, against 64-bit autograd of the whole."""
+    lengths, sections = [130, 1, 77, 0, 260], [8, 12, 12]
+    T = sum(lengths)
+    rule = lisa.RotaryAxes(D, sections, pairing="neighbours")
+    seqs = lisa.PackedSequences(lengths, HEADS, KV)
+    places = _places(lengths)
+    q, k, v, do = (_rand(h, T, D, seed=s).to(BF16) for h, s in ((HEADS, 1), (KV, 2), (KV, 3), (HEADS, 4)))
+    pos = places.cuda()
+    qr, kr = lisa.rotary(q.cuda(), k.cuda(), pos, rule)
+    out, lse = lisa.prompt_attention(qr, kr, v.cuda(), seqs, return_lse=True)
+    dqr, dkr, dv = lisa.prompt_attention_backward(qr, kr, v.cuda(), out, lse, do.cuda(), seqs)
+    dq, dk = lisa.rotary_backward(dqr, dkr, pos, rule)
+
+    x = [t.double().requires_grad_() for t in (q, k, v)]
+    tq, tk = _turned(x[0], places, rule, sections), _turned(x[1], places, rule, sections)
+    parts, at = [], 0
+    for L in lengths:
+        rows, at = slice(at, at + L), at + L
+        if L:
+            parts.append(_attend(tq[:, rows].unflatten(0, (KV, -1)), tk[:, None, rows], x[2][:, None, rows]).flatten(0, 1))
+    want = torch.cat(parts, 1)
+    want.backward(do.double())
+    # rounded on the way: q, k turned, p, dS, o in delta, the gradients before and after the turn
+    _close(out, want.detach(), 4)
+    for got, t in zip((dq, dk, dv), x):
+        _close(got, t.grad, 8)
+
+
+def test_a_prompt_and_its_answer(lisa):
+    """Prompts into the cache, then tokens one by one: each step's output against 64-bit attention over what the cache
+    stands for, and against the cross attention over what it reads back."""
+    lengths, sections = [63, 200, 1], [8, 12, 12]
+    B, T, steps = len(lengths), sum(lengths), 5
+    rule = lisa.RotaryAxes(D, sections, pairing="neighbours")
+    seqs = lisa.PackedSequences(lengths, HEADS, KV)
+    q, k, v = (_rand(h, T, D, seed=s).to(BF16).cuda() for h, s in ((HEADS, 5), (KV, 6), (KV, 7)))
+    qr, kr = lisa.rotary(q, k, _places(lengths).cuda(), rule)
+    out = lisa.prompt_attention(qr, kr, v, seqs)
+    assert torch.isfinite(out).all()
+    cache = lisa.Cache4(16, KV, D)
+    table = torch.randperm(16, generator=torch.Generator().manual_seed(1))[:B * 5].reshape(B, 5).int().cuda()
+    sequence = torch.repeat_interleave(torch.arange(B), torch.tensor(lengths)).int().cuda()
+    at = torch.cat([torch.arange(L) for L in lengths]).int().cuda()
+    lisa.cache_store(cache, kr, v, table, at, sequence)
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    where = torch.arange(5 * 64, dtype=torch.int32, device="cuda").repeat(B, 1)
+    for step in range(steps):
+        qn, kn, vn = (_rand(B, h, 1, D, seed=10 * step + s).to(BF16).cuda() for h, s in ((HEADS, 1), (KV, 2), (KV, 3)))
+        qn, kn = lisa.rotary(qn, kn, (lens[None, :, None] + 1).repeat(3, 1, 1), rule)
+        lisa.cache_store(cache, kn, vn, table, lens[:, None].contiguous())
+        lens += 1
+        got = lisa.cache_attention(qn, cache, table, lens)
+        held = lisa.cache_read(cache, table, where, dtype=torch.float32)
+        for b in range(B):
+            L = lengths[b] + step + 1
+            kk, vv = (x[b, :, None, :L].double().cpu() for x in held)
+            _close(got[b], _attend(qn[b].double().cpu().unflatten(0, (KV, -1)), kk, vv).flatten(0, 1), 2)
+        kb, vb = lisa.cache_read(cache, table, where)
+        _close(got, lisa.cross_attention(qn, kb, vb, kv_lens=lens).double().cpu(), 6)
+
+
+def test_captured_steps_follow_the_lengths(lisa):
+    """One captured step (rotary, store, attention), replayed as the sequence grows, against the same calls made anew."""
+    rule = lisa.RotaryAxes(D, [32])
+    caches = [lisa.Cache4(4, KV, D) for _ in range(2)]
+    table = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    q, k, v = (torch.zeros(1, h, 1, D, dtype=BF16, device="cuda") for h in (HEADS, KV, KV))
+    lens = torch.ones(1, dtype=torch.int32, device="cuda")
+    pos = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+
+    def step(cache):
+        qr, kr = lisa.rotary(q, k, pos, rule)
+        lisa.cache_store(cache, kr, v, table, pos)
+        return lisa.cache_attention(qr, cache, table, lens)
+
+    step(caches[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(caches[0])
+    for i in range(70):
+        for x, s in ((q, 1), (k, 2), (v, 3)):
+            x.copy_(_rand(*x.shape, seed=100 * i + s))
+        lens.fill_(i + 1)
+        pos.fill_(i)
+        graph.replay()
+        assert torch.equal(captured, step(caches[1]))
+    assert torch.equal(caches[0].store, caches[1].store)

@@ -160,6 +160,21 @@ def test_repeated_inputs_and_empty_ones(lisa):
         assert lisa.rotary(x, None, torch.zeros(1, shape[2], dtype=torch.int32, device="cuda"), rule).shape == shape
 
 
+def test_tokens_far_apart(lisa):
+    """Offsets beyond 32 bits: heads 2^30 elements apart."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of device memory")
+    rule = lisa.RotaryAxes(64, [16, 16])
+    wide = torch.empty(5 << 30, dtype=BF16, device="cuda")
+    q = wide.as_strided((1, 5, 7, 64), (0, 1 << 30, 64, 1))
+    x = rand((1, 5, 7, 64), BF16, 20)
+    q.copy_(x)
+    pos = torch.randint(0, 90, (2, 7), dtype=torch.int32)
+    ref = want(x, pos, rule, "halves", [16, 16])
+    check(lisa.rotary(q, None, pos.cuda(), rule), ref)
+    check(lisa.rotary(q, None, pos.cuda(), rule, out=q), ref)
+
+
 def test_not_a_number_stays_in_its_pair(lisa):
     rule = lisa.RotaryAxes(16, [8])
     q = rand((1, 1, 3, 16), F32, 13)
