@@ -210,7 +210,7 @@ unsigned seal_of(const lisa_packed &s) {
     const auto add = [&](unsigned v) { x = (x ^ v) * 16777619u; };
     add((unsigned)s.plan_bytes);
     add((unsigned)(s.plan_bytes >> 32));
-    for (const int v : {s.sequences, s.tokens, s.heads, s.kv_heads, s.causal}) add((unsigned)v);
+    for (const int v : {s.sequences, s.tokens, s.heads, s.kv_heads, s.causal, s.one_tile}) add((unsigned)v);
     for (int pass = 0; pass < kPasses; ++pass)
         for (const int v : {s.items[pass], s.joins[pass], s.parts[pass]}) add((unsigned)v);
     return x;
@@ -246,6 +246,7 @@ extern "C" lisa_status lisa_packed_plan(const int *lengths, int sequences, int h
     out.heads = heads;
     out.kv_heads = kv_heads;
     out.causal = causal;
+    for (int s = 0; s < sequences; ++s) out.one_tile |= lengths[s] > 0 && lengths[s] <= kStep;
     out.seal = seal_of(out);
     std::memset(plan, 0, bytes);
     char *base = static_cast<char *>(plan);
@@ -366,6 +367,7 @@ Problem problem_of(const lisa_packed &s, int d, float scale) {
     p.group = s.heads / s.kv_heads;
     p.d = d;
     p.causal = s.causal;
+    p.one_tile = s.one_tile;
     p.scale = scale;
     for (int pass = 0; pass < kPasses; ++pass) p.lists[pass] = lists_of(s, pass);
     return p;

@@ -20,9 +20,17 @@
 // take S and dP into registers as soon as both are there, so the group's next
 // products run under this one's arithmetic.
 //
+// P and dS are rounded to bf16 for their products.  Where a row of dQ, dK or dV has the
+// terms of one tile alone (sequences of up to 128 tokens, the first rows under the
+// causal mask) that rounding, of few terms or a single one, would be as large as the
+// result's own, so what it leaves goes into a second product there.  (A kernel without
+// that branch is 4% faster and takes the batches that have no such sequence.)
+//
 // Tiles are loaded from wherever the sequence begins, so a tile may hold tokens of
 // the next one.  Their weights and dS are set to 0 whatever the products say, and
 // the rows that the second products would multiply with those zeros are set to 0.
+#include <type_traits>
+
 #include "lisa_packed_tc.cuh"
 
 namespace lisa {
@@ -61,15 +69,23 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(bar));
 }
-// [128 x 64] (+)= A (tensor memory, 128 x k) * B (k token rows); k a multiple of 16, at most a group's columns.
+// [128 x 64] (+)= A (tensor memory, 128 x k) * B (k token rows); k a multiple of 16, at most a group's columns.  A's 32 k
+// of a strip are 16 columns of tensor memory, the strips kApart columns apart.
+template <int kApart = kStrip / 2>
 __device__ __forceinline__ void mma_group_rows(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, int k, bool accumulate) {
     constexpr uint32_t idesc = make_idesc_bf16(128, 64, false, true);
     if (k == kGroupCols) {
 #pragma unroll
-        for (int ks = 0; ks < kGroupCols / 16; ++ks) tc_mma_ta(d_tmem, a_tmem + ks * 8, b + 128 * ks, idesc, ks > 0 || accumulate);
+        for (int ks = 0; ks < kGroupCols / 16; ++ks)
+            tc_mma_ta(d_tmem, a_tmem + (ks >> 1) * kApart + (ks & 1) * 8, b + 128 * ks, idesc, ks > 0 || accumulate);
     } else {
-        for (int ks = 0; ks < k / 16; ++ks) tc_mma_ta(d_tmem, a_tmem + ks * 8, b + 128 * ks, idesc, ks > 0 || accumulate);
+        for (int ks = 0; ks < k / 16; ++ks)
+            tc_mma_ta(d_tmem, a_tmem + (ks >> 1) * kApart + (ks & 1) * 8, b + 128 * ks, idesc, ks > 0 || accumulate);
     }
+}
+// What the rounding to a bf16 pair leaves of two numbers, as a bf16 pair.
+__device__ __forceinline__ uint32_t rest_of(float x, float y, uint32_t pair) {
+    return pack_bf16(x - bf16_lo(pair), y - bf16_hi(pair));
 }
 // Columns of a group among the `cols` of a tile; 0: it has nothing to do there.
 __device__ __forceinline__ int group_cols(int cols, int group) { return min(max(cols - group * kGroupCols, 0), kGroupCols); }
@@ -135,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_slot;
     chain_begin();
     if (blockIdx.x == 0 && tid == 0) *p.err = 0;
-    const uint32_t tS = tmem, tP = tmem + 128, tDs = tmem + 256, tDq = tmem + 320;
+    const uint32_t tS = tmem, tP = tmem + 128, tDs = tmem + 256, tDq = tmem + 320, tRest = tmem + 384;
     const Walk walk = walk_of(p.lists[kDq], x.div_heads);
 
     if (warp == kHelper) {
@@ -219,8 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_on(smem_u32(&bar.ds_full[g]), ns[g]++ & 1, guard, kErrTimeoutMma);
                     tc_fence_after();
                     if (elect_one()) {
-                        mma_group_rows(tDq, tDs + g * (kGroupCols / 2), kt0 + (uint32_t)c.slot * kPair + g * kGroupRows, mine,
-                                       j > w.t0 || g > 0);
+                        const uint64_t rows = kt0 + (uint32_t)c.slot * kPair + g * kGroupRows;
+                        mma_group_rows(tDq, tDs + g * (kGroupCols / 2), rows, mine, j > w.t0 || g > 0);
+                        if (w.steps == 1) mma_group_rows(tDq, tRest + g * (kGroupCols / 2), rows, mine, true);
                         tc_commit(smem_u32(&bar.dq_done[g]));
                     }
                     __syncwarp();
@@ -308,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int c = 0; c < kStrip; ++c) s[c] = ex2_approx(s[c]);
-                uint32_t ds[kStrip / 2];
+                uint32_t ds[kStrip / 2], rest[kStrip / 2];
                 if (single) {   // delta from the unrounded weights: few keys, where dP - delta cancels most, do without
                                 // the rounding of O
                     float e0 = 0.f, e1 = 0.f, t0 = 0.f, t1 = 0.f;
@@ -331,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float u, v;
                         fma2(u, v, s[e], s[e + 1], -delta, -delta, dp[e], dp[e + 1]);
                         ds[e >> 1] = pack_bf16(u, v);
+                        rest[e >> 1] = rest_of(u, v, ds[e >> 1]);
                     }
                 } else {
 #pragma unroll
@@ -344,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ns > 0) wait_on(smem_u32(&bar.dq_done[group]), (ns - 1) & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 tmem_st16(tDs + c0 / 2 + lanes, ds);
+                if (single) tmem_st16(tRest + c0 / 2 + lanes, rest);
                 if (strip == 2 * group && rows < cols && cols <= (group + 1) * kGroupCols && w.row0 + w.len < p.tokens) {
                     // S is done with the group's keys: what the next sequence holds may not meet dS = 0
                     zero_rows(ring + 2 * (kt % kDqStages) * kTileBytes, rows, cols, wt);
@@ -419,6 +438,8 @@ struct Steps {
     }
 };
 
+// kOneTile: sequences of up to 128 tokens are among them.
+template <bool kOneTile>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_tc_dkdv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md,
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -574,7 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t at = (uint32_t)s * kPair + g * kGroupRows;
                         const bool add = u > w.t0 || g > 0;
                         mma_group_rows(tDv, tPw + g * (kGroupCols / 2), dt0 + at, mine, add);
+                        if (kOneTile && w.len <= kRows) mma_group_rows<kStrip>(tDv, tS + g * kGroupCols, dt0 + at, mine, true);
                         mma_group_rows(tDk, tDs + g * (kGroupCols / 2), qt0 + at, mine, add);
+                        if (kOneTile && w.len <= kRows) mma_group_rows<kStrip>(tDk, tD + g * kGroupCols, qt0 + at, mine, true);
                         tc_commit(smem_u32(&bar.w_done[g]));
                     }
                     __syncwarp();
@@ -596,21 +619,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Work w = walk.at(k);
             const int j = w.first + wt;
             Steps st(w, p.group, p.causal);
-            for (int u = w.t0; u < w.t1; ++u, ca.next(kDkvStages), st.next()) {
+            auto step = [&](auto one_tile) __attribute__((always_inline)) {
+                constexpr bool kAlone = decltype(one_tile)::value;   // the sequence is one tile
                 const int rows = tile_rows(w.len, st.qt * kRows), cols = tile_cols(rows);
                 const bool diagonal = p.causal && st.qt * kRows == w.first;
                 const QueryAux &a = aux[ca.slot];
                 wait_on(smem_u32(&bar.aux_full[ca.slot]), ca.phase, guard, kErrTimeoutLoad);
                 if (group_cols(cols, group) == 0) {   // the other group has all of the tile
                     arrive_warp(&bar.aux_empty[ca.slot], lane);
-                    continue;
+                    return;
                 }
                 float s[kStrip], dp[kStrip];
                 wait_on(smem_u32(&bar.full[group]), ns & 1, guard, kErrTimeoutMma);
                 tc_fence_after();
                 load_strips(tS + c0 + lanes, s, tD + c0 + lanes, dp);
                 tc_fence_before();
-                arrive_warp(&bar.free[group], lane);
+                if constexpr (!kAlone) arrive_warp(&bar.free[group], lane);   // else the rests go where S and dP were
 #pragma unroll
                 for (int c = 0; c < kStrip; c += 4) {
                     const float4 l = *reinterpret_cast<const float4 *>(a.nl + c0 + c);
@@ -648,6 +672,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 tmem_st16(tPw + c0 / 2 + lanes, pw);
                 tmem_st16(tDs + c0 / 2 + lanes, ds);
+                if constexpr (kAlone) {
+#pragma unroll
+                    for (int e = 0; e < kStrip; e += 2) {
+                        pw[e >> 1] = rest_of(s[e], s[e + 1], pw[e >> 1]);
+                        ds[e >> 1] = rest_of(dp[e], dp[e + 1], ds[e >> 1]);
+                    }
+                    tmem_st16(tS + c0 + lanes, pw);   // where the thread's own strips were: the other's may not be read yet
+                    tmem_st16(tD + c0 + lanes, ds);
+                }
                 if (rows < cols && cols <= (group + 1) * kGroupCols && w.row0 + w.len < p.tokens) {
                     // S and dP are done with the group's queries: what the next sequence holds may not meet weights of 0
                     // (the group's first strip has the tile of Q, the second that of dO)
@@ -661,6 +694,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(smem_u32(&bar.aux_empty[ca.slot]));
                     mbar_arrive(smem_u32(&bar.w_full[group]));
                 }
+                if constexpr (kAlone) {   // the next S and dP have to wait for the products with the rests
+                    wait_on(smem_u32(&bar.w_done[group]), (ns - 1) & 1, guard, kErrTimeoutMma);
+                    arrive_warp(&bar.free[group], lane);
+                }
+            };
+            if (kOneTile && w.len <= kRows) {
+                for (int u = w.t0; u < w.t1; ++u, ca.next(kDkvStages), st.next()) step(std::bool_constant<kOneTile>{});
+            } else {
+                for (int u = w.t0; u < w.t1; ++u, ca.next(kDkvStages), st.next()) step(std::false_type{});
             }
             // ---- strips 0, 1 store dV, 2 and 3 dK, 32 columns each
             float o[kStrip];
@@ -753,9 +795,10 @@ cudaError_t launch_tc_backward(const Problem &p, cudaStream_t s) {
     if (e == cudaSuccess)
         e = launch_join(JoinParams{p.lists[kDq], {p.part[0], nullptr}, {p.dQ, p.dQ}, {p.scale, 0.f}, p.heads, p.d}, 1, s);
     x.div_heads = fast_div(p.kv_heads);
-    if (e == cudaSuccess) e = allow_smem<packed_tc_dkdv>();
+    if (e == cudaSuccess) e = p.one_tile ? allow_smem<packed_tc_dkdv<true>>() : allow_smem<packed_tc_dkdv<false>>();
     if (e == cudaSuccess)
-        e = launch_plain(packed_tc_dkdv, workers(p.lists[kDkv], p.kv_heads), kThreads, kDkvSmem, s, mq, md, mk, mv, x);
+        e = launch_plain(p.one_tile ? packed_tc_dkdv<true> : packed_tc_dkdv<false>, workers(p.lists[kDkv], p.kv_heads),
+                         kThreads, kDkvSmem, s, mq, md, mk, mv, x);
     if (e == cudaSuccess)
         e = launch_join(JoinParams{p.lists[kDkv], {p.part[0], p.part[1]}, {p.dV, p.dK}, {1.f, p.scale}, p.kv_heads, p.d}, 2, s);
     return e;

@@ -34,7 +34,7 @@ class lisa_rotary_rule(ctypes.Structure):
 class lisa_packed(ctypes.Structure):
     _fields_ = [("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t), ("sequences", ctypes.c_int),
                 ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
-                ("causal", ctypes.c_int), ("items", ctypes.c_int * 3), ("joins", ctypes.c_int * 3),
+                ("causal", ctypes.c_int), ("one_tile", ctypes.c_int), ("items", ctypes.c_int * 3), ("joins", ctypes.c_int * 3),
                 ("parts", ctypes.c_int * 3), ("seal", ctypes.c_uint)]
 
 

@@ -211,7 +211,7 @@ BAD = [
     (dict(packed=_packed), INV), (dict(ws=0), WSP), (dict(wbytes=16), WSP), (dict(ws=FAKE + 32 * MB + 8), INV),
 ]
 BAD_PACKED = [dict(plan=0), dict(plan=FAKE + 8), dict(tokens=306), dict(tokens=-1), dict(heads=5), dict(kv_heads=4),
-              dict(kv_heads=0), dict(causal=0), dict(plan_bytes=16), dict(heads=1 << 20), dict(sequences=3), dict(seal=0),
+              dict(kv_heads=0), dict(causal=0), dict(plan_bytes=16), dict(heads=1 << 20), dict(sequences=3), dict(seal=0), dict(one_tile=0),
               dict(items=(ctypes.c_int * 3)(9, 9, 9)), dict(parts=(ctypes.c_int * 3)(9, 9, 9))]
 
 

@@ -242,6 +242,37 @@ def test_other_streams_and_captured_graphs(lisa):
 
 
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths,heads,kv", [([2, 2, 1, 2, 1, 2], 1, 1), ([12, 4, 6, 1, 7], 2, 1), ([128, 100, 65, 64], 3, 1)])
+def test_few_tokens_keep_their_gradients(lisa, causal, lengths, heads, kv):
+    """Sequences of one tile: dQ = scale sum dS k and dK = scale sum dS q are good to their own rounding, since what the
+    rounding of dS leaves is added.  Half a step of the result, 2^-8 of it, twice that step's 2^-8 of what is left of dS,
+    and fp32 behind them: s of magnitude up to 20 with a few 2^-22 of it in the exponent (2^-15 of p), dP - delta with
+    (64 + 8) 2^-22 of |dO| |v| (2^-15 of it)."""
+    c = Case(lisa, BF16, lengths, heads, kv, 64, causal=causal, seed=sum(lengths))
+    out, lse = c.forward()
+    dq, dk, _ = (x.double().cpu() for x in c.backward(out, lse))
+    q, k, v, do = (x.double() for x in c.ref)
+    k, v = (x.repeat_interleave(heads // kv, 0) for x in (k, v))
+    at = 0
+    for L in lengths:
+        rows, at = slice(at, at + L), at + L
+        s = q[:, rows] @ k[:, rows].transpose(1, 2) * c.scale
+        if causal:
+            s = s.masked_fill(torch.ones(L, L).triu(1).bool(), -math.inf)
+        p = torch.softmax(s, -1)
+        dp = do[:, rows] @ v[:, rows].transpose(1, 2)
+        ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+        size = do[:, rows].abs() @ v[:, rows].abs().transpose(1, 2)
+        off = 2.0 ** -15 * ds.abs() + p * (2.0 ** -15 * (dp.abs() + (p * dp).abs().sum(-1, keepdim=True)) + 2.0 ** -15 * (
+            size + (p * size).sum(-1, keepdim=True)))
+        for got, want, noise in ((dq[:, rows], ds @ k[:, rows], off @ k[:, rows].abs()),
+                                 (dk[:, rows], (ds.transpose(1, 2) @ q[:, rows]).unflatten(0, (kv, -1)).sum(1),
+                                  (off.transpose(1, 2) @ q[:, rows].abs()).unflatten(0, (kv, -1)).sum(1))):
+            bound = 1.01 * 2.0 ** -8 * c.scale * want.abs() + c.scale * noise + 2.0 ** -126
+            assert bool(((got - c.scale * want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("causal", [True, False])
 def test_gradient_against_differences(lisa, causal):
     """fp32 directional derivatives by central differences, as for the cross attention: off by h^2 / 6 of the third
     derivative and by the rounding of the two sums, 2^-23 sum |o dO| (L + d) / h at most."""
