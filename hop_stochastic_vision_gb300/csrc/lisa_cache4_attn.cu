@@ -283,7 +283,9 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             // p sv of the step's 16 tokens as the product's right side: columns are rows of P, transposed
-            uint32_t w[kTiles][G][2];
+            // (and what its rounding leaves, in a sequence's last page: of few tokens that would be as much as the
+            // rounding of the result)
+            uint32_t w[kTiles][G][2], rest[kTiles][G][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int token = 16 * j + 8 * h + g;
@@ -300,7 +302,9 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
                             // behind what the row sees a scale may be anything
                             if (!kWhole && j0 + token >= sees[e][c]) v[c] = 0.f;
                         }
-                        w[e][u][h] = transposed(pack_bf16(v[0], v[1]));
+                        const uint32_t pair = pack_bf16(v[0], v[1]);
+                        w[e][u][h] = transposed(pair);
+                        if (!kWhole) rest[e][u][h] = transposed(pack_bf16(v[0] - bf16_lo(pair), v[1] - bf16_hi(pair)));
                     }
             }
             uint32_t lo[G], hi[G];
@@ -317,8 +321,12 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int e = 0; e < kTiles; ++e)
+                    for (int e = 0; e < kTiles; ++e) {
                         mma_bf16_16816(o[e][u][m], c[0][2 * m], c[0][2 * m + 1], c[1][2 * m], c[1][2 * m + 1], w[e][u][0], w[e][u][1]);
+                        if (!kWhole)
+                            mma_bf16_16816(o[e][u][m], c[0][2 * m], c[0][2 * m + 1], c[1][2 * m], c[1][2 * m + 1],
+                                           rest[e][u][0], rest[e][u][1]);
+                    }
             }
         }
     };
