@@ -382,43 +382,60 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// o = sum_s w_s o_s / sum_s w_s with w_s = 2^(ref_s - ref) sum_s: the parts of a row, in order.  Reference and sum come
-// apart: far from 0 their lse would have lost the sum (at 2^24 the last place is 2), and parts of unequal lengths would
-// weigh the same.  A CTA takes 32 rows of one cut unit and head, a thread four elements at a time.
-constexpr int kJoinRows = 32;
-__global__ void __launch_bounds__(256) join_forward(const __grid_constant__ Problem p) {
+// o = sum_s w_s o_s / sum_s w_s with w_s = 2^(ref_s - ref) sum_s: the parts of a row, in order, four on their way at a
+// time.  Reference and sum come apart: far from 0 their lse would have lost the sum (at 2^24 the last place is 2), and parts
+// of unequal lengths would weigh the same.  A thread takes four elements of a row.
+constexpr int kJoinThreads = 256, kFlight = 4;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_forward(const __grid_constant__ Problem p) {
+    constexpr int kVec = D / 4, kJoinRows = kJoinThreads / kVec, kBlocks = unit_rows(kForward) / kJoinRows;
     chain_begin();
-    const Lists &l = p.lists[kForward];
-    const Join j = l.joins[blockIdx.x / (unit_rows(kForward) / kJoinRows)];
-    const int r0 = (int)(blockIdx.x % (unit_rows(kForward) / kJoinRows)) * kJoinRows, h = blockIdx.y, vec = p.d / 4;
-    for (int e = threadIdx.x; e < kJoinRows * vec; e += 256) {
-        const int r = r0 + e / vec, c = e % vec * 4;
-        if (r >= j.rows) continue;
-        const size_t at0 = ((size_t)j.part * p.heads + h) * unit_rows(kForward) + r;
-        const size_t step = (size_t)p.heads * unit_rows(kForward);
-        float top = -INFINITY;
-        for (int s = 0; s < j.parts; ++s) top = fmaxf(top, p.stat_part[at0 + s * step].x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < j.parts; ++s) {
-            const float2 st = p.stat_part[at0 + s * step];
-            const float w = ex2_approx(st.x - ref) * st.y;
-            const float4 v = *reinterpret_cast<const float4 *>(p.part[0] + (at0 + s * step) * p.d + c);
-            sum += w;
-            o[0] = fmaf(w, v.x, o[0]);
-            o[1] = fmaf(w, v.y, o[1]);
-            o[2] = fmaf(w, v.z, o[2]);
-            o[3] = fmaf(w, v.w, o[3]);
+    const Join j = p.lists[kForward].joins[blockIdx.x / kBlocks];
+    const int r = (int)(blockIdx.x % kBlocks) * kJoinRows + threadIdx.x / kVec, c = threadIdx.x % kVec * 4, h = blockIdx.y;
+    if (r >= j.rows) return;
+    const size_t at0 = ((size_t)j.part * p.heads + h) * unit_rows(kForward) + r;
+    const size_t step = (size_t)p.heads * unit_rows(kForward);
+    float top = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < j.parts; s0 += kFlight) {
+        float2 st[kFlight];
+        float4 v[kFlight];
+#pragma unroll
+        for (int s = 0; s < kFlight; ++s) {
+            const bool in = s0 + s < j.parts;
+            st[s] = in ? p.stat_part[at0 + (s0 + s) * step] : make_float2(-INFINITY, 0.f);
+            v[s] = in ? *reinterpret_cast<const float4 *>(p.part[0] + (at0 + (s0 + s) * step) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;
-        uint2 out;
-        out.x = pack_bf16(o[0] * inv, o[1] * inv);
-        out.y = pack_bf16(o[2] * inv, o[3] * inv);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + (long long)h * p.O.sh +
-                                   (long long)(j.row + r) * p.O.st + c) = out;
-        if (c == 0 && p.lse)
-            p.lse[(long long)h * p.lse_stride + j.row + r] = top == -INFINITY ? -INFINITY : kLn2 * (top + log2f(sum));
+        float now = top;
+#pragma unroll
+        for (int s = 0; s < kFlight; ++s) now = fmaxf(now, st[s].x);
+        const float ref = now == -INFINITY ? 0.f : now, f = ex2_approx(top - ref);
+        top = now;
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= f;
+#pragma unroll
+        for (int s = 0; s < kFlight; ++s) {
+            const float w = ex2_approx(st[s].x - ref) * st[s].y;
+            sum += w;
+            o[0] = fmaf(w, v[s].x, o[0]);
+            o[1] = fmaf(w, v[s].y, o[1]);
+            o[2] = fmaf(w, v[s].z, o[2]);
+            o[3] = fmaf(w, v[s].w, o[3]);
+        }
     }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    uint2 out;
+    out.x = pack_bf16(o[0] * inv, o[1] * inv);
+    out.y = pack_bf16(o[2] * inv, o[3] * inv);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + (long long)h * p.O.sh +
+                               (long long)(j.row + r) * p.O.st + c) = out;
+    if (c == 0 && p.lse)
+        p.lse[(long long)h * p.lse_stride + j.row + r] = top == -INFINITY ? -INFINITY : kLn2 * (top + log2f(sum));
+}
+template <int D>
+cudaError_t launch_join(const Problem &p, cudaStream_t s) {
+    const unsigned blocks = (unsigned)p.lists[kForward].n_joins * (unit_rows(kForward) / (kJoinThreads / (D / 4)));
+    return launch_chained(join_forward<D>, dim3(blocks, (unsigned)p.heads), kJoinThreads, 0, s, p);
 }
 
 }  // namespace
@@ -437,9 +454,7 @@ cudaError_t launch_tc_forward(const Problem &p, cudaStream_t s) {
     if (e == cudaSuccess)
         e = launch_chained(packed_tc_forward, workers(p.lists[kForward], p.heads), kFwdThreads, kFwdSmem, s, mq, mk, mv, x);
     if (e == cudaSuccess && p.lists[kForward].n_joins > 0)
-        e = launch_chained(join_forward,
-                           dim3((unsigned)p.lists[kForward].n_joins * (unit_rows(kForward) / kJoinRows), (unsigned)p.heads),
-                           256, 0, s, p);
+        e = p.d == 16 ? launch_join<16>(p, s) : p.d == 32 ? launch_join<32>(p, s) : launch_join<64>(p, s);
     return e;
 }
 

@@ -757,6 +757,7 @@ __global__ void __launch_bounds__(256) join_gradients(const __grid_constant__ Jo
         if (r >= j.rows) continue;
         const float *at = x.part[which] + (((size_t)j.part * x.heads + h) * unit_rows(kDq) + r) * x.d + c;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (int s = 0; s < j.parts; ++s, at += step) {
             const float4 a = *reinterpret_cast<const float4 *>(at);
             v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
