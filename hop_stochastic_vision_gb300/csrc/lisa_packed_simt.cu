@@ -8,8 +8,7 @@
 //
 // Bound by a tile's latency where there are few (sequences of 196, 1, 49, 0 and 130, 2
 // heads of 16: 11, 12.5 and 15.9 us for up to four tiles one behind the other), by fp32
-// arithmetic and shared-memory loads where there are many (4096 tokens of 12 heads, d =
-// 64, forward 946 us with bf16 inputs, 27 TFLOP/s).
+// arithmetic and shared-memory loads where there are many.
 #include <cuda_runtime.h>
 
 #include "lisa_attn_simt.cuh"
