@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + (long long)b * p.O.sb +
                                    (long long)h * p.O.sh + (long long)i * p.O.st + d) = out;
         if (d == 0 && p.lse)
-            p.lse[((size_t)b * p.heads + h) * p.n + i] = t == -INFINITY ? -INFINITY : kLn2 * (t + log2f(l));
+            p.lse[((size_t)b * p.heads + h) * p.n + i] = l == 0.f ? -INFINITY : kLn2 * (t + log2f(l));   // NaN scores: NaN
     }
     if (cl > 1) cluster_sync();   // no CTA leaves while its results are being read
 }

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) packed_forward(const __grid_constant
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) out[(long long)i * p.O.st + tx + 16 * c] = acc[r][c] * inv;
         if (p.lse && tx == 0)
-            p.lse[h * p.lse_stride + w.row0 + i] = top[r] == -INFINITY ? -INFINITY : top[r] + logf(sum[r]);
+            p.lse[h * p.lse_stride + w.row0 + i] = sum[r] == 0.f ? -INFINITY : top[r] + logf(sum[r]);
     }
 }
 

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                         (long long)(w.row0 + i0) * p.O.st,
                                     p.O.st, w.len - i0, p.d, lane);
                 if (p.lse && i < w.len)
-                    p.lse[(long long)w.h * p.lse_stride + w.row0 + i] = ref == -INFINITY ? -INFINITY : kLn2 * (ref + log2f(sum));
+                    p.lse[(long long)w.h * p.lse_stride + w.row0 + i] = sum == 0.f ? -INFINITY : kLn2 * (ref + log2f(sum));
             } else if (i < w.len) {
                 const size_t at = ((size_t)w.part * p.heads + w.h) * unit_rows(kForward) + t * kRows + wt;
                 p.stat_part[at] = make_float2(ref, sum);
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_forward(const __grid_consta
     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(const_cast<void *>(p.O.p)) + (long long)h * p.O.sh +
                                (long long)(j.row + r) * p.O.st + c) = out;
     if (c == 0 && p.lse)
-        p.lse[(long long)h * p.lse_stride + j.row + r] = top == -INFINITY ? -INFINITY : kLn2 * (top + log2f(sum));
+        p.lse[(long long)h * p.lse_stride + j.row + r] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
 }
 template <int D>
 cudaError_t launch_join(const Problem &p, cudaStream_t s) {

@@ -260,6 +260,17 @@ def test_not_a_number_in_tokens_that_a_row_does_not_see(lisa):
     assert torch.equal(got[:, :, :2], want[:, :, :2]) and torch.isnan(got[:, :, 2]).all()
 
 
+def test_only_keys_that_are_not_numbers(lisa):
+    """A row all of whose keys are NaN has no value and no lse; -inf would say that it saw nothing."""
+    k, v, q = torch.full((2, 1, 300, 32), math.nan, dtype=BF16), rand(2, 1, 300, 32, seed=2), rand(2, 3, 1, 32, seed=3)
+    k[1] = rand(1, 300, 32, seed=1)
+    cache, table = filled(lisa, k, v, [300, 70])
+    out, lse = lisa.cache_attention(q.cuda(), cache, table, torch.tensor([300, 70], dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    Check(k[1:], v[1:], q[1:], [70]).against(out[1:], lse[1:])
+
+
 def test_layouts_and_given_outputs(lisa):
     k, v, q = rand(2, 2, 90, 32, seed=1), rand(2, 2, 90, 32, seed=2), rand(2, 4, 3, 32, seed=3)
     cache, table = filled(lisa, k, v, [90, 50])

@@ -167,6 +167,25 @@ def test_keys_of_minus_infinity(lisa, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lengths", [[300, 20], [2000, 20]])
+def test_rows_without_a_number_have_no_lse(lisa, dtype, lengths):
+    """Scores of -inf and, in a later tile, NaN; and a row of NaN alone: NaN, not the -inf of a row that saw nothing.
+    (Whole sequences, and ones cut into parts.)"""
+    c = Case(lisa, dtype, lengths, 1, 1, 64, causal=False)
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    c.k.zero_()
+    c.k[:, :lengths[0], 0] = -math.inf
+    c.k[:, lengths[0] - 3, 0] = math.nan
+    c.q[:, lengths[0] + 7] = math.nan
+    out, lse = c.forward()
+    rows = torch.arange(sum(lengths))
+    bad = (rows < lengths[0]) | (rows == lengths[0] + 7)
+    assert torch.isnan(lse[:, bad]).all() and torch.isnan(out[:, bad]).all()
+    assert torch.isfinite(lse[:, ~bad]).all() and torch.isfinite(out[:, ~bad]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("causal", [True, False])
 def test_same_bits_every_time_whatever_the_workspace_holds(lisa, dtype, causal):
     c = Case(lisa, dtype, [1300, 60], 2, 1, 64, causal=causal)
@@ -239,6 +258,23 @@ def test_other_streams_and_captured_graphs(lisa):
         oe, le = other.forward()
         for a, b in zip((og, lg) + gg, (oe, le) + other.backward(oe, le)):
             assert torch.equal(a, b)
+
+
+def test_a_batch_that_is_dropped_while_another_stream_reads_it(lisa):
+    c = Case(lisa, BF16, [260, 100], 4, 2, 64)
+    want, _ = c.forward()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        got, _ = c.forward()
+    c.seqs.record_stream(side)
+    at, nbytes = c.seqs.struct.plan, c.seqs.struct.plan_bytes
+    c.seqs = None
+    new = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert at not in [x.data_ptr() for x in new]
+    side.synchronize()
+    assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("causal", [True, False])
