@@ -303,7 +303,9 @@ class PackedSequences:
     query heads on ``kv_heads`` key heads; ``causal``: a query reads the keys up to
     itself, else all of its sequence.  Made once for a batch, for every layer and
     every captured graph that has it; making it copies a table to ``device``, which a
-    capture does not allow."""
+    capture does not allow.  The table goes with the object: keep it as long as graphs
+    that read it are replayed, and ``record_stream`` other streams than the one it was
+    made on, as for a tensor."""
 
     def __init__(self, lengths, heads: int, kv_heads: int = None, *, causal: bool = True, device="cuda"):
         lengths = [_int32(x) for x in lengths]
@@ -326,6 +328,10 @@ class PackedSequences:
         self.lengths, self.tokens = tuple(lengths), self.struct.tokens
         self.heads, self.kv_heads, self.causal = heads, kv_heads, bool(causal)
         self._bytes = {}
+
+    def record_stream(self, stream: torch.cuda.Stream) -> None:
+        """The table's memory is not handed on before what ``stream`` has been given has run."""
+        self._table.record_stream(stream)
 
     def workspace_bytes(self, d: int, dtype: int, backward: bool = False) -> int:
         """Workspace of a call, by its width and the ABI's type."""

@@ -83,9 +83,10 @@ typedef struct lisa_packed {
 } lisa_packed;
 
 /*
- * lengths: host, `sequences` of them (0 .. 2^20), each from 0, 2^22 in all;
- * causal 0 or 1.  The bytes of the plan (0 for arguments that lisa_packed_plan
- * would reject), and the plan with its struct (`plan` left NULL).
+ * lengths: host, `sequences` of them (0 .. 2^20), each from 0, 2^22 in all, and
+ * at most 2^24 pairs of a head and a unit of 128 tokens; causal 0 or 1.  The bytes
+ * of the plan (0 for arguments that lisa_packed_plan would reject), and the plan
+ * with its struct (`plan` left NULL).
  */
 size_t lisa_packed_plan_bytes(const int *lengths, int sequences, int heads, int kv_heads, int causal);
 lisa_status lisa_packed_plan(const int *lengths, int sequences, int heads, int kv_heads, int causal, void *plan,
@@ -173,7 +174,9 @@ lisa_status lisa_cache4_read(const lisa_cache4 *cache, void *K, const lisa_strid
  * them too: Q [B][heads][n][d] (LISA_BF16), entry b on sequence b of lens[b]
  * tokens (device int32 [B], taken to 0 .. width * LISA_CACHE4_PAGE).  Query i
  * stands at lens[b] - n + i and sees the tokens up to there; one that stands
- * before the first sees none: o = 0, lse = -inf.  O and lse (fp32 [B][heads][n],
+ * before the first sees none: o = 0, lse = -inf.  A score is good to 2^-13 of the
+ * sum over the groups of 32 elements of sum |q| times the largest |k|; sum |q| of a
+ * group is at most 2^118.  O and lse (fp32 [B][heads][n],
  * may be NULL) are written.  scale is finite and > 0.  Made for few queries: every
  * 16 rows (queries times the heads that share a key head) read the cache anew;
  * n heads / kv_heads is at most 1024.

@@ -341,3 +341,11 @@ def test_empty_caches_launch_nothing():
 def test_a_plan_without_heads():
     packed = _packed((5000,), heads=0, kv=0)
     assert list(packed.parts) == [0, 0, 0]
+
+
+def test_plans_of_too_many_pairs():
+    """2^20 sequences of one token: 16 heads are 2^24 pairs, 17 are more."""
+    lengths = [1] * (1 << 20)
+    assert prompt.lisa_packed_plan_bytes(lengths, 1 << 20, 16, 16, 1) > 0
+    assert prompt.lisa_packed_plan_bytes(lengths, 1 << 20, 17, 17, 1) == 0
+    assert prompt.lisa_packed_plan(lengths, 1 << 20, 17, 17, 1, None, 0, prompt.lisa_packed()) == UNS
