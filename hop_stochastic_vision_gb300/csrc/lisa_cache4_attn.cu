@@ -16,7 +16,7 @@
 // Bound by the instructions of unpacking: shifts, logic, maxima and conversions share a
 // pipe that takes two cycles for each, and a page costs a scheduler with four warps
 // some 1200 cycles, alone 2000 (keys 580, softmax 380, values 630, the next copies
-// 250).  64 sequences of up to 4096 tokens, 12 heads on 4: 39 MB in 20.5 us with the
+// 250).  64 sequences of up to 4096 tokens, 12 heads on 4: 39 MB in 18.6 us with the
 // launch; all of 4096 76 MB in 28.8, 2.6 TB/s.  Before the first page are 2.3 us of
 // dependent reads, behind the last 2 us of joining.
 //
@@ -45,6 +45,7 @@ struct Params {
     AttnProblem p;
     int rows, rtiles;            // query rows per key head, tiles of 16 of them
     int splits;                  // CTAs of a cluster
+    int round;                   // sequences that fill the SMs once; 0: taken as they come
     FastDiv div_rtiles, div_n;
 };
 
@@ -116,13 +117,35 @@ __global__ void __launch_bounds__(kThreads) attention(const __grid_constant__ Pa
     __shared__ float stat_s[kWarps + 1][2][16];   // reference (in log2 units) and sum, per warp and joined
     const AttnProblem &p = x.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
-    const int split_id = blockIdx.x, b = blockIdx.z;
+    const int split_id = blockIdx.x;
     int rt = blockIdx.y;
     const int kvh = split(rt, x.div_rtiles);
     const uint32_t ring = smem_u32(sm) + (uint32_t)warp * (kStages * B::kBytes);
     static_assert(kRing >= (kWarps + 1) * 16 * (D + 4) * 4, "the rings hold the warps' results at the end");
     chain_begin();
 
+    int b = blockIdx.z;
+    if (x.round > 0) {
+        // b of the sequences in order of length, the longest first and every other round of them backwards: an SM gets
+        // long and short ones if CTAs are dealt out in turn
+        __shared__ __align__(16) int lens_s[kThreads];
+        __shared__ int b_s;
+        const int mine = tid < p.B ? max(p.lens[tid], 0) : -1, round = b / x.round, begin = round * x.round;
+        if (round & 1) b = begin + min(begin + x.round, p.B) - 1 - b;
+        lens_s[tid] = mine;
+        __syncthreads();
+        if (tid < p.B) {
+            int rank = 0;
+            for (int t = 0; t < p.B; t += 4) {
+                const int4 l = *reinterpret_cast<const int4 *>(lens_s + t);
+                rank += (l.x > mine || (l.x == mine && t < tid)) + (l.y > mine || (l.y == mine && t + 1 < tid)) +
+                        (l.z > mine || (l.z == mine && t + 2 < tid)) + (l.w > mine || (l.w == mine && t + 3 < tid));
+            }
+            if (rank == b) b_s = tid;
+        }
+        __syncthreads();
+        b = b_s;
+    }
     const int len = min(max(p.lens[b], 0), p.c.width * kPage);
     const int pages = (len + kPage - 1) / kPage, per = (pages + x.splits - 1) / x.splits;
     const int c0 = min(split_id * per, pages), c1 = min(c0 + per, pages);
@@ -486,6 +509,11 @@ cudaError_t launch_attention(const AttnProblem &p, int d, cudaStream_t s) {
     // of 4096 28.7, 28.8, 28.8, 26.8; 64 of 4096 20.6, then 12.4 throughout; 4 of 16384 67.6, then 14.4.
     const long long ctas = (long long)p.B * p.c.kv_heads * x.rtiles;
     x.splits = (int)std::max<long long>(1, std::min<long long>(8, std::min<long long>(4 * kSms / ctas, p.c.width / kWarps)));
+    // Sequences in order of their lengths where a warp may have four pages or more to take (and a CTA has a thread for each
+    // sequence): 128, 64 and 32 of up to 4096 tokens, 4 key heads, as they come 37.0, 20.6 and 14.4 us, in order 32.9, 18.6
+    // and 12.4; of shorter walks the ordering costs more than it gives (100 of up to 1000 tokens, 3 key heads, 10.4 and 12.4).
+    const long long fill = (long long)x.splits * p.c.kv_heads * x.rtiles;
+    x.round = p.B > 1 && p.B <= kThreads && p.c.width >= 4 * kWarps * x.splits ? (int)std::max<long long>(1, kSms / fill) : 0;
     // With the tiles of 16 rows the same calls take 28.8, 41, 18.5 and 16.5 us.
     if (x.rows <= 8) return d == 64 ? go<64, 1>(x, s) : go<32, 1>(x, s);
     return d == 64 ? go<64, 2>(x, s) : go<32, 2>(x, s);

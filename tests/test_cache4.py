@@ -391,3 +391,16 @@ def test_refusals(lisa):
     for bad in ((4, 2, 16), (4, 2, 128), (-1, 2, 64), (1 << 25, 1, 32)):
         with pytest.raises(lisa.LisaError):
             lisa.Cache4(*bad)
+
+
+@pytest.mark.parametrize("B,heads,kv,lens", [
+    (128, 2, 1, lambda b: 2000 - 13 * b), (70, 12, 4, lambda b: (b * 577) % 2049), (5, 3, 3, lambda b: (2048, 0, 2048, 7, -3)[b]),
+    (129, 2, 1, lambda b: (b * 91) % 2000), (40, 1, 1, lambda b: 1025)])
+def test_many_sequences_of_unequal_lengths(lisa, B, heads, kv, lens):
+    """Sequences taken in the order of their lengths (equal ones, empty ones, more than are ordered): each gets its own."""
+    lens = [lens(b) for b in range(B)]
+    k, v, q = rand(B, kv, 2048, 32, seed=1), rand(B, kv, 2048, 32, seed=2), rand(B, heads, 1, 32, seed=3)
+    cache, table = filled(lisa, k, v, [max(x, 0) for x in lens], width=64)
+    out, lse = lisa.cache_attention(q.cuda(), cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    Check(k, v, q, lens).against(out, lse)
