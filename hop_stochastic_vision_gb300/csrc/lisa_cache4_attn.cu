@@ -482,7 +482,9 @@ cudaError_t go(const Params &x, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    // in order of length: begun on empty SMs, since early CTAs, the longest, would crowd together where the kernel before
+    // leaves room (64 of up to 4096 tokens, one call behind the other, 25.6 us, so 18.9)
+    at[0].val.programmaticStreamSerializationAllowed = x.round > 0 ? 0 : 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = (unsigned)x.splits;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
@@ -510,8 +512,9 @@ cudaError_t launch_attention(const AttnProblem &p, int d, cudaStream_t s) {
     const long long ctas = (long long)p.B * p.c.kv_heads * x.rtiles;
     x.splits = (int)std::max<long long>(1, std::min<long long>(8, std::min<long long>(4 * kSms / ctas, p.c.width / kWarps)));
     // Sequences in order of their lengths where a warp may have four pages or more to take (and a CTA has a thread for each
-    // sequence): 128, 64 and 32 of up to 4096 tokens, 4 key heads, as they come 37.0, 20.6 and 14.4 us, in order 32.9, 18.6
-    // and 12.4; of shorter walks the ordering costs more than it gives (100 of up to 1000 tokens, 3 key heads, 10.4 and 12.4).
+    // sequence).  128, 64 and 32 of up to 4096 tokens in any order, 4 key heads, one call behind the other: as they come
+    // 41.6, 24.0 and 13.7 us, in order 34.9, 18.9 and 12.3; 64 of 4096 each 28.1 and 30.8.  Of shorter walks the ordering
+    // costs more than it gives (100 of up to 1000 tokens, 3 key heads, 10.4 and 12.4).
     const long long fill = (long long)x.splits * p.c.kv_heads * x.rtiles;
     x.round = p.B > 1 && p.B <= kThreads && p.c.width >= 4 * kWarps * x.splits ? (int)std::max<long long>(1, kSms / fill) : 0;
     // With the tiles of 16 rows the same calls take 28.8, 41, 18.5 and 16.5 us.
